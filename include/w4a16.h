@@ -383,6 +383,31 @@ int w4a16_kv_attention_decode_batch(const void* q, int dtype, int64_t B, int64_t
                                     float* work, void* out, void* stream);
 
 /*
+ * w4a16_attention_prompt -- causal attention over whole prompts: the attention that produces a
+ * prompt's outputs from the 16-bit queries, keys and values of its projections, before the keys
+ * and values are quantized into the cache (w4a16_kv_quantize) that the decode entry points read.
+ * B sequences of different lengths are packed along one token axis:
+ *   out[i][h] = sum_{j <= i, j in the sequence of i} p_j v_j,
+ *   p = softmax_j(q[i][h] . k[j][h / (Hq / Hkv)] / sqrt(D)).
+ *   q     [T, Hq, D] fp16/bf16 (dtype); row i starts at element i * q_stride.  k, v [T, Hkv, D]
+ *         likewise: the three may be column blocks of one fused projection's output.  Heads are
+ *         adjacent (head h at element h * D of its row).  16-byte aligned; the strides are
+ *         multiples of 8, at least Hq * D (k, v: Hkv * D) and at most 2^24.  D is 64 or 128.
+ *   cu_seqlens  device int32 [B + 1], not decreasing: sequence b is the tokens cu_seqlens[b] ..
+ *         cu_seqlens[b + 1] - 1 (possibly none).  Values are clamped into [0, T] on the device;
+ *         decreasing values leave rows of out unspecified, never an access outside the tensors.
+ *   out   [T, Hq, D] dense, same dtype, 16-byte aligned; must not overlap the inputs.  Rows before
+ *         the first and behind the last sequence are not written, and q, k and v are not read
+ *         there: a padded batch may hold anything in them.
+ * Scores, softmax statistics and outputs are held in fp32; the softmax weights are rounded once to
+ * dtype for the product with the values, and the output is rounded once.
+ * Limits: 1 <= B <= 2^20, 1 <= T <= 2^30, (T / 32 + B) * Hq < 2^31, Hq <= 65535.
+ */
+int w4a16_attention_prompt(const void* q, const void* k, const void* v, int dtype, int64_t T, int64_t B,
+                           const int32_t* cu_seqlens, int64_t Hq, int64_t Hkv, int64_t D, int64_t q_stride,
+                           int64_t k_stride, int64_t v_stride, void* out, void* stream);
+
+/*
  * w4a16_linear_workspace -- bytes of fp32 workspace that w4a16_linear_ws can use for this
  * problem (0: it would not split K and behaves as w4a16_linear); a negative status for invalid
  * arguments.  Host only.

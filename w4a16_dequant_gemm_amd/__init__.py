@@ -21,6 +21,8 @@ the library's HIP kernels; there is no CPU or PyTorch fallback.
     W8A8 with SmoothQuant on the INT8 matrix cores.
 ``kv_quantize(x, bits)`` / ``kv_attention_decode(q, cache, T)``
     per-token KV8 / KV4 cache quantization and the decode attention over the quantized cache.
+``attention_prompt(q, k, v, cu_seqlens)``
+    causal attention over packed prompts, on the 16-bit keys and values before they are cached.
 """
 
 from __future__ import annotations
@@ -37,12 +39,29 @@ __all__ = [
     "w8a16_quantize_pack", "w8a16_linear", "w8a16_select_path", "linear_workspace", "linear_ws",
     "abi_version", "lib", "gptq_hessian", "gptq_factor", "gptq_quantize", "awq_stats",
     "awq_search", "awq_scale", "w8a8_smooth", "w8a8_quantize_weight", "w8a8_quantize_act",
-    "w8a8_linear", "kv_quantize", "kv_attention_decode",
+    "w8a8_linear", "kv_quantize", "kv_attention_decode", "attention_prompt",
 ]
 
 
 def _stream() -> int:
     return torch.cuda.current_stream().cuda_stream
+
+
+def _call(fn, what: str, device: torch.device, *args) -> None:
+    """``fn(*args, stream)`` on ``device``, on the stream current there, whichever device is
+    current; raises on a negative status."""
+    if device.index == torch.cuda.current_device():
+        check(fn(*args, torch.cuda.current_stream().cuda_stream), what)
+        return
+    with torch.cuda.device(device):
+        check(fn(*args, torch.cuda.current_stream().cuda_stream), what)
+
+
+def _same_device(x: torch.Tensor, name: str, **others) -> None:
+    """Every given tensor (None: absent) is a GPU tensor on the device of ``x``."""
+    for other, t in others.items():
+        if t is not None and t.device != x.device:
+            raise ValueError(f"{other} must be on the device of {name}")
 
 
 def _need(t: torch.Tensor, name: str, dtype, ndim: int) -> None:
@@ -533,4 +552,54 @@ def kv_attention_decode(q: torch.Tensor, kcache, vcache, T: int, bits: int = 8,
     check(L.w4a16_kv_attention_decode(q.data_ptr(), dt, Hq, Hkv, T, Tmax, D, bits, kc.data_ptr(), ks.data_ptr(),
                                       ptr(kz), vc.data_ptr(), vs.data_ptr(), ptr(vz), work.data_ptr(),
                                       out.data_ptr(), _stream()), "w4a16_kv_attention_decode")
+    return out
+
+
+def _need_heads(t: torch.Tensor, name: str, dtype) -> None:
+    """``t [T, H, D]``: a GPU tensor of adjacent heads (a row is ``H * D`` consecutive values);
+    rows may be further apart, as in a column block of a wider tensor."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be 3-D")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if (t.shape[2] > 1 and t.stride(2) != 1) or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+        raise ValueError(f"the heads of {name} must be adjacent (strides [*, D, 1])")
+
+
+def attention_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
+                     out: torch.Tensor | None = None) -> torch.Tensor:
+    """Causal attention over packed prompts: ``out[i, h] = softmax_j(q[i, h] . k[j, h // G] /
+    sqrt(D)) . v`` over the tokens ``j <= i`` of the sequence of ``i``, ``G = Hq / Hkv``.
+
+    ``q [T, Hq, D]``, ``k`` and ``v [T, Hkv, D]`` are fp16 or bf16; their heads are adjacent, their
+    rows may be strided (column blocks of a fused projection).  Sequence ``b`` is the tokens
+    ``cu_seqlens[b] .. cu_seqlens[b + 1] - 1`` (int32 ``[B + 1]`` on the device, not decreasing).
+    Rows outside every sequence are neither read nor written: in an ``out`` of the caller's they
+    keep what they held, in the returned tensor of a call without ``out`` they are undefined."""
+    dt = _dtype_code(q)
+    _need_heads(q, "q", q.dtype)
+    _need_heads(k, "k", q.dtype)
+    _need_heads(v, "v", q.dtype)
+    _need(cu_seqlens, "cu_seqlens", torch.int32, 1)
+    T, Hq, D = q.shape
+    Hkv = k.shape[1]
+    if k.shape != v.shape or k.shape[0] != T or k.shape[2] != D:
+        raise ValueError("k and v must be [T, Hkv, D]")
+    if cu_seqlens.shape[0] < 2:
+        raise ValueError("cu_seqlens must be [B + 1] with B >= 1")
+    _same_device(q, "q", k=k, v=v, cu_seqlens=cu_seqlens, out=out)
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
+    else:
+        _need(out, "out", q.dtype, 3)
+        if out.shape != q.shape:
+            raise ValueError("out must be [T, Hq, D]")
+    # the stride of a single row is arbitrary in torch: the dense one then
+    sq, sk, sv = (t.stride(0) if T > 1 else t.shape[1] * D for t in (q, k, v))
+    _call(lib().w4a16_attention_prompt, "w4a16_attention_prompt", q.device, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+          dt, T, cu_seqlens.shape[0] - 1, cu_seqlens.data_ptr(), Hq, Hkv, D, sq, sk, sv, out.data_ptr())
     return out

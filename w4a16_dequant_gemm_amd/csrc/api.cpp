@@ -404,6 +404,26 @@ int w4a16_kv_attention_decode_batch(const void* q, int dtype, int64_t B, int64_t
                                                  vscales, vzeros, work, out, static_cast<hipStream_t>(stream)));
 }
 
+int w4a16_attention_prompt(const void* q, const void* k, const void* v, int dtype, int64_t T, int64_t B,
+                           const int32_t* cu_seqlens, int64_t Hq, int64_t Hkv, int64_t D, int64_t q_stride,
+                           int64_t k_stride, int64_t v_stride, void* out, void* stream) {
+    if (!q || !k || !v || !cu_seqlens || !out) return W4A16_ERR_NULL;
+    if (dtype != W4A16_F16 && dtype != W4A16_BF16) return W4A16_ERR_DTYPE;
+    if (T < 1 || T > (int64_t(1) << 30) || B < 1 || B > (int64_t(1) << 20) || Hq < 1 || Hkv < 1 || Hq > 65535 ||
+        Hq % Hkv != 0 || (D != 64 && D != 128) || (T / 32 + B) * Hq > kMaxDim)
+        return W4A16_ERR_SHAPE;
+    constexpr int64_t kMaxStride = int64_t(1) << 24;
+    if (q_stride < Hq * D || k_stride < Hkv * D || v_stride < Hkv * D || q_stride > kMaxStride ||
+        k_stride > kMaxStride || v_stride > kMaxStride)
+        return W4A16_ERR_SHAPE;
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || q_stride % 8 || k_stride % 8 || v_stride % 8 ||
+        !aligned(cu_seqlens, 4) || !aligned(out, 16))
+        return W4A16_ERR_ALIGN;
+    const w4a16::PromptArgs a = {q, k, v, cu_seqlens, out, dtype, (int)B, (int)T,
+                                 (int)Hq, (int)Hkv, (int)D, (int)q_stride, (int)k_stride, (int)v_stride};
+    return hip_status(w4a16::launch_attention_prompt(a, static_cast<hipStream_t>(stream)));
+}
+
 int w4a16_select_path(int64_t M, int64_t N, int64_t K, int64_t group_size, int dtype) {
     // Fake, aligned, non-null pointers: only shapes are examined.
     alignas(16) static const unsigned char dummy[16] = {0};

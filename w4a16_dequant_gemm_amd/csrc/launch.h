@@ -85,6 +85,17 @@ hipError_t launch_kv_attention(const void* q, int dtype, int B, int Hq, int Hkv,
                                const uint16_t* kz, const void* vc, const uint16_t* vs, const uint16_t* vz,
                                float* work, void* out, hipStream_t st);
 
+// Prompt attention (attention.hip): B sequences packed along T tokens, their bounds cu [B + 1] on
+// the device (clamped into [0, T]); rows of q / k / v are qs / ks / vs elements apart, those of
+// out Hq * D.
+struct PromptArgs {
+    const void *q, *k, *v;
+    const int* cu;
+    void* out;
+    int dtype, B, T, Hq, Hkv, D, qs, ks, vs;
+};
+hipError_t launch_attention_prompt(const PromptArgs& a, hipStream_t st);
+
 // AWQ (awq.hip)
 long long awq_workspace_doubles(long long N, long long K, long long n);
 hipError_t launch_awq_stats(const void* X, int dtype, int n, int K, float* xmean, hipStream_t s);
