@@ -58,7 +58,8 @@ typedef enum {
     W4A16_ERR_SCHEME = -6,  /* unknown quantization scheme                          */
     W4A16_ERR_HIP = -7,     /* the HIP runtime reported an error at launch          */
     W4A16_ERR_PATH = -8,    /* a forced kernel path cannot run this problem         */
-    W4A16_ERR_SCRATCH = -9  /* the static scratch buffer is too small (see below)    */
+    W4A16_ERR_SCRATCH = -9, /* the static scratch buffer is too small (see below)    */
+    W4A16_ERR_OVERLAP = -10 /* an output overlaps an input that is still being read */
 } w4a16_status;
 
 typedef enum { W4A16_F16 = 0, W4A16_BF16 = 1 } w4a16_dtype;
@@ -406,6 +407,95 @@ int w4a16_kv_attention_decode_batch(const void* q, int dtype, int64_t B, int64_t
 int w4a16_attention_prompt(const void* q, const void* k, const void* v, int dtype, int64_t T, int64_t B,
                            const int32_t* cu_seqlens, int64_t Hq, int64_t Hkv, int64_t D, int64_t q_stride,
                            int64_t k_stride, int64_t v_stride, void* out, void* stream);
+
+/*
+ * The K and V caches of one call, as pointers (the layout of w4a16_kv_quantize): codes 16-byte
+ * aligned, scales and zeros 2-byte aligned, zeros only for bits == 4 (NULL otherwise).
+ */
+typedef struct {
+    const void* kcodes;
+    const uint16_t *kscales, *kzeros;
+    const void* vcodes;
+    const uint16_t *vscales, *vzeros;
+} w4a16_kv_cache;
+
+/* The same for an output. */
+typedef struct {
+    void* kcodes;
+    uint16_t *kscales, *kzeros;
+    void* vcodes;
+    uint16_t *vscales, *vzeros;
+} w4a16_kv_cache_out;
+
+/* fp32 elements of the w4a16_kv_attention_decode_shared workspace (host only), or a negative
+ * status. */
+int64_t w4a16_kv_attention_shared_workspace(int64_t B, int64_t Hq, int64_t Hkv, int64_t P, int64_t Tmax,
+                                            int64_t D);
+
+/*
+ * w4a16_kv_attention_decode_shared -- decode attention for a batch of B sequences that begin with
+ * the same P tokens (a system prompt, a document): out[b][h] = softmax(q[b][h] . K / sqrt(D)) V over
+ * the shared tokens and then the first lengths[b] tokens of the sequence's own cache, kv head
+ * h / (Hq / Hkv).  The prefix is held once and read once per 128 query rows (B * Hq / Hkv rows per
+ * kv head), not once per sequence.
+ *   q        [B, Hq, D] fp16/bf16, 16-byte aligned; out [B, Hq, D] same dtype.
+ *   prefix   w4a16_kv_quantize output with H = Hkv and T = Pmax ([Hkv, Pmax, ...]); its first P
+ *            tokens are read, 0 <= P <= Pmax <= 2^24.  P == 0: its pointers are not looked at.
+ *   own      [B, Hkv, Tmax, ...], 1 <= Tmax <= 2^24.
+ *   lengths  device int32 [B]; each value is clamped into [0, Tmax] on the device.  A sequence with
+ *            P + lengths[b] == 0 gets zeros.
+ *   work     w4a16_kv_attention_shared_workspace(...) fp32 elements, 16-byte aligned (scratch,
+ *            contents undefined after the call; calls that overlap on one buffer race).
+ * Scores, softmax statistics and sums are fp32; the softmax weights times V's scales are rounded
+ * once to fp16 (relative 2^-11) for the product with the codes, and the output is rounded once.
+ * Limits: B <= 65535, B * Hq <= 2^24, Hkv * (Pmax + B * Tmax) <= 2^33.
+ */
+int w4a16_kv_attention_decode_shared(const void* q, int dtype, int64_t B, int64_t Hq, int64_t Hkv, int64_t D,
+                                     int bits, const w4a16_kv_cache* prefix, int64_t P, int64_t Pmax,
+                                     const w4a16_kv_cache* own, const int32_t* lengths, int64_t Tmax, float* work,
+                                     void* out, void* stream);
+
+/* fp32 elements of the w4a16_kv_attention_decode_weights workspace (host only), or a negative
+ * status. */
+int64_t w4a16_kv_attention_weights_workspace(int64_t B, int64_t Hq, int64_t Hkv, int64_t Tmax, int64_t D);
+
+/*
+ * w4a16_kv_attention_decode_weights -- the batched decode attention over caches [B, Hkv, Tmax, ...]
+ * that also adds up the attention every cached token receives, the statistic w4a16_kv_evict keeps
+ * tokens by:
+ *   sums[b][hk][t] = weights[b][hk][t] + sum over the heads h of kv head hk of p[b][h][t],
+ * p the softmax weights, for t < lengths[b]; entries behind are not written.
+ *   lengths  device int32 [B]; each value is clamped into [0, Tmax] on the device.  A sequence of
+ *            length 0 gets zeros.
+ *   weights  [B, Hkv, Tmax] fp32, or NULL: the sums start from 0.
+ *   sums     [B, Hkv, Tmax] fp32; may be `weights` (accumulation in place).
+ *   work     w4a16_kv_attention_weights_workspace(...) fp32 elements, 16-byte aligned (scratch).
+ * q, out, caches, arithmetic and limits as for w4a16_kv_attention_decode_shared without a prefix
+ * (B * Hq * Tmax <= 2^36 besides).
+ */
+int w4a16_kv_attention_decode_weights(const void* q, int dtype, int64_t B, int64_t Hq, int64_t Hkv, int64_t D,
+                                      int bits, const w4a16_kv_cache* own, const int32_t* lengths, int64_t Tmax,
+                                      const float* weights, float* sums, float* work, void* out, void* stream);
+
+/*
+ * w4a16_kv_evict -- shrink caches [B, Hkv, Tmax, ...] to at most `budget` tokens per sequence.  Of a
+ * sequence of n = lengths[b] tokens (clamped into [0, Tmax]) every kv head keeps all if n <= budget,
+ * else its last `recent` tokens and, of the earlier ones, the budget - recent with the largest
+ * weights[b][hk][t]; among equal weights the earlier token is kept (-0 equals +0, NaN counts as
+ * larger than any number).  The kept tokens stay in order and move to the front of `out`, codes
+ * and parameters unchanged; rows of out behind them are not written.
+ *   weights      [B, Hkv, Tmax] fp32 (w4a16_kv_attention_decode_weights).
+ *   out          [B, Hkv, Tout, ...], min(budget, Tmax) <= Tout <= 2^24.
+ *   weights_out  [B, Hkv, Tout] fp32: the kept tokens' weights, 0 behind them (a token appended
+ *                there starts with none).
+ *   lengths_out  int32 [B]: min(n, budget).
+ *   kept         int32 [B, Hkv, budget]: the kept tokens' indices, -1 behind them.
+ * 0 <= recent <= budget, 1 <= budget <= 2^24; the other limits as above (B * Hkv <= 65535).
+ * No output may overlap an input (W4A16_ERR_OVERLAP): shrink into a second cache.
+ */
+int w4a16_kv_evict(const w4a16_kv_cache* in, const float* weights, const int32_t* lengths, int64_t B, int64_t Hkv,
+                   int64_t Tmax, int64_t D, int bits, int64_t budget, int64_t recent, const w4a16_kv_cache_out* out,
+                   int64_t Tout, float* weights_out, int32_t* lengths_out, int32_t* kept, void* stream);
 
 /*
  * w4a16_linear_workspace -- bytes of fp32 workspace that w4a16_linear_ws can use for this

@@ -23,6 +23,11 @@ the library's HIP kernels; there is no CPU or PyTorch fallback.
     per-token KV8 / KV4 cache quantization and the decode attention over the quantized cache.
 ``attention_prompt(q, k, v, cu_seqlens)``
     causal attention over packed prompts, on the 16-bit keys and values before they are cached.
+``kv_attention_decode_shared(q, kprefix, vprefix, P, kcache, vcache, lengths)``
+    decode attention of a batch whose sequences share a cached prefix, read once for all.
+``kv_attention_decode_weights(q, kcache, vcache, lengths, weights)`` / ``kv_evict(kcache, vcache, weights, ...)``
+    decode attention that adds up the attention weight of every cached token, and the compaction
+    of a cache to the recent and the most attended tokens.
 """
 
 from __future__ import annotations
@@ -30,7 +35,7 @@ from __future__ import annotations
 import torch
 
 from . import _lib as _lib_mod
-from ._lib import (ASYM, BF16, F16, OK, PATH_AUTO, PATH_GEMV, PATH_NAMES, PATH_PREFILL,
+from ._lib import (ASYM, BF16, F16, KvCache, OK, PATH_AUTO, PATH_GEMV, PATH_NAMES, PATH_PREFILL,
                    PATH_SKINNY, SYM, W4A16Error, check, lib)
 
 __all__ = [
@@ -40,6 +45,7 @@ __all__ = [
     "abi_version", "lib", "gptq_hessian", "gptq_factor", "gptq_quantize", "awq_stats",
     "awq_search", "awq_scale", "w8a8_smooth", "w8a8_quantize_weight", "w8a8_quantize_act",
     "w8a8_linear", "kv_quantize", "kv_attention_decode", "attention_prompt",
+    "kv_attention_decode_shared", "kv_attention_decode_weights", "kv_evict",
 ]
 
 
@@ -603,3 +609,196 @@ def attention_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
     _call(lib().w4a16_attention_prompt, "w4a16_attention_prompt", q.device, q.data_ptr(), k.data_ptr(), v.data_ptr(),
           dt, T, cu_seqlens.shape[0] - 1, cu_seqlens.data_ptr(), Hq, Hkv, D, sq, sk, sv, out.data_ptr())
     return out
+
+
+def _need_cache(cache, name: str, bits: int, lead: int, D: int):
+    """Checks ``(codes, scales, zeros)`` of a quantized cache with ``lead`` leading axes besides the
+    tokens'; returns the shape of its scales."""
+    if bits not in (8, 4):
+        raise ValueError("bits must be 8 or 4")
+    codes, scales, zeros = cache
+    _need(codes, f"{name} codes", torch.int8 if bits == 8 else torch.int32, lead + 2)
+    _need(scales, f"{name} scales", torch.float16, lead + 1)
+    if tuple(codes.shape) != (*scales.shape, D if bits == 8 else D // 8):
+        raise ValueError(f"{name} codes must be [..., {'D' if bits == 8 else 'D/8'}] over its scales' shape")
+    if bits == 4:
+        if zeros is None:
+            raise ValueError(f"{name} needs zeros for 4-bit codes")
+        _need(zeros, f"{name} zeros", torch.float16, lead + 1)
+        if zeros.shape != scales.shape:
+            raise ValueError(f"{name} zeros must match its scales")
+    return scales.shape
+
+
+def _need_caches(k, v, names, bits: int, lead: int, D: int, like: torch.Tensor):
+    """A K and a V cache of one shape on the device of ``like``."""
+    shape = _need_cache(k, names[0], bits, lead, D)
+    if _need_cache(v, names[1], bits, lead, D) != shape:
+        raise ValueError(f"{names[0]} and {names[1]} must have the same shape")
+    for c, name in zip((k, v), names):
+        for t in c[:2 if bits == 8 else 3]:
+            if t.device != like.device:
+                raise ValueError(f"{name} must be on the device of the other arguments")
+    return shape
+
+
+def _cache_struct(k, v, bits: int) -> KvCache:
+    z = (k[2].data_ptr(), v[2].data_ptr()) if bits == 4 else (None, None)
+    return KvCache(k[0].data_ptr(), k[1].data_ptr(), z[0], v[0].data_ptr(), v[1].data_ptr(), z[1])
+
+
+def _work(work, need: int, what: str, like: torch.Tensor) -> torch.Tensor:
+    """The scratch buffer of a call: allocated, or the caller's checked."""
+    if need < 0:
+        raise W4A16Error(int(need), what)
+    if work is None:
+        return torch.empty(need, dtype=torch.float32, device=like.device)
+    if work.dtype != torch.float32 or work.device != like.device or not work.is_contiguous() or work.numel() < need:
+        raise ValueError(f"work must be a contiguous float32 tensor on {like.device} of at least {need} elements")
+    return work
+
+
+def _decode_out(out, q: torch.Tensor) -> torch.Tensor:
+    if out is None:
+        return torch.empty_like(q)
+    _need(out, "out", q.dtype, 3)
+    if out.shape != q.shape or out.device != q.device:
+        raise ValueError("out must be [B, Hq, D] on the device of q")
+    return out
+
+
+def kv_attention_shared_workspace(B: int, Hq: int, Hkv: int, P: int, Tmax: int, D: int) -> int:
+    """fp32 elements of the scratch buffer that :func:`kv_attention_decode_shared` needs."""
+    need = lib().w4a16_kv_attention_shared_workspace(B, Hq, Hkv, P, Tmax, D)
+    if need < 0:
+        raise W4A16Error(int(need), "w4a16_kv_attention_shared_workspace")
+    return int(need)
+
+
+def kv_attention_weights_workspace(B: int, Hq: int, Hkv: int, Tmax: int, D: int) -> int:
+    """fp32 elements of the scratch buffer that :func:`kv_attention_decode_weights` needs."""
+    need = lib().w4a16_kv_attention_weights_workspace(B, Hq, Hkv, Tmax, D)
+    if need < 0:
+        raise W4A16Error(int(need), "w4a16_kv_attention_weights_workspace")
+    return int(need)
+
+
+def kv_attention_decode_shared(q: torch.Tensor, kprefix, vprefix, P: int, kcache, vcache, lengths: torch.Tensor,
+                               bits: int = 8, out: torch.Tensor | None = None,
+                               work: torch.Tensor | None = None) -> torch.Tensor:
+    """Decode attention of ``B`` sequences that begin with the same tokens: ``q [B, Hq, D]`` over the
+    first ``P`` tokens of the shared caches ``(codes, scales, zeros)`` of shape ``[Hkv, Pmax, ...]``,
+    then the first ``lengths[b]`` (int32, on the device, possibly 0) of the sequence's own
+    ``[B, Hkv, Tmax, ...]``.  The prefix is held and read once for the batch.  A sequence without any
+    token gets zeros.  ``work`` is an optional fp32 buffer of at least
+    :func:`kv_attention_shared_workspace` elements; calls that may overlap need one each."""
+    dt = _dtype_code(q)
+    _need(q, "q", q.dtype, 3)
+    _need(lengths, "lengths", torch.int32, 1)
+    B, Hq, D = q.shape
+    Bc, Hkv, Tmax = _need_caches(kcache, vcache, ("kcache", "vcache"), bits, 2, D, q)
+    Hp, Pmax = _need_caches(kprefix, vprefix, ("kprefix", "vprefix"), bits, 1, D, q)
+    if Bc != B or lengths.shape[0] != B or Hp != Hkv:
+        raise ValueError("caches must be [B, Hkv, Tmax, ...], prefixes [Hkv, Pmax, ...] and lengths [B]")
+    _same_device(q, "q", lengths=lengths)
+    if not 0 <= P <= Pmax:
+        raise ValueError("P must be in [0, Pmax]")
+    L = lib()
+    out = _decode_out(out, q)
+    work = _work(work, L.w4a16_kv_attention_shared_workspace(B, Hq, Hkv, P, Tmax, D),
+                 "w4a16_kv_attention_shared_workspace", q)
+    _call(L.w4a16_kv_attention_decode_shared, "w4a16_kv_attention_decode_shared", q.device, q.data_ptr(), dt, B, Hq,
+          Hkv, D, bits, _cache_struct(kprefix, vprefix, bits), P, Pmax, _cache_struct(kcache, vcache, bits),
+          lengths.data_ptr(), Tmax, work.data_ptr(), out.data_ptr())
+    return out
+
+
+def kv_attention_decode_weights(q: torch.Tensor, kcache, vcache, lengths: torch.Tensor, weights: torch.Tensor | None,
+                                bits: int = 8, sums: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                                work: torch.Tensor | None = None):
+    """Decode attention over caches ``[B, Hkv, Tmax, ...]`` that adds up the attention every cached
+    token receives; returns ``(out, sums)``.
+
+    ``sums[b, hk, t] = weights[b, hk, t] + sum of the softmax weights of the heads of kv head hk`` for
+    ``t < lengths[b]`` (entries behind are not written), fp32 ``[B, Hkv, Tmax]``.  ``sums`` defaults to
+    ``weights``, which is then updated in place; ``weights=None`` starts from 0 (``sums`` defaults to
+    a zero tensor then).  A sequence of length 0 gets zeros.  ``work`` is an optional fp32 buffer of at
+    least :func:`kv_attention_weights_workspace` elements."""
+    dt = _dtype_code(q)
+    _need(q, "q", q.dtype, 3)
+    _need(lengths, "lengths", torch.int32, 1)
+    B, Hq, D = q.shape
+    Bc, Hkv, Tmax = shape = _need_caches(kcache, vcache, ("kcache", "vcache"), bits, 2, D, q)
+    if Bc != B or lengths.shape[0] != B:
+        raise ValueError("caches must be [B, Hkv, Tmax, ...] and lengths [B]")
+    if sums is None:
+        sums = torch.zeros(shape, dtype=torch.float32, device=q.device) if weights is None else weights
+    for t, name in ((weights, "weights"), (sums, "sums")):
+        if t is not None:
+            _need(t, name, torch.float32, 3)
+            if t.shape != shape:
+                raise ValueError(f"{name} must be [B, Hkv, Tmax]")
+    _same_device(q, "q", lengths=lengths, weights=weights, sums=sums)
+    L = lib()
+    out = _decode_out(out, q)
+    work = _work(work, L.w4a16_kv_attention_weights_workspace(B, Hq, Hkv, Tmax, D),
+                 "w4a16_kv_attention_weights_workspace", q)
+    _call(L.w4a16_kv_attention_decode_weights, "w4a16_kv_attention_decode_weights", q.device, q.data_ptr(), dt, B, Hq,
+          Hkv, D, bits, _cache_struct(kcache, vcache, bits), lengths.data_ptr(), Tmax,
+          None if weights is None else weights.data_ptr(), sums.data_ptr(), work.data_ptr(), out.data_ptr())
+    return out, sums
+
+
+def kv_evict(kcache, vcache, weights: torch.Tensor, lengths: torch.Tensor, budget: int, recent: int, bits: int = 8,
+             capacity: int | None = None, out=None):
+    """Shrink caches ``[B, Hkv, Tmax, ...]`` to at most ``budget`` tokens per sequence: every kv head
+    keeps its last ``recent`` tokens and, of the earlier ones, those with the largest ``weights``
+    (fp32 ``[B, Hkv, Tmax]``, see :func:`kv_attention_decode_weights`; the earlier token among
+    equals), in their order.  A sequence of at most ``budget`` tokens keeps all of them.
+
+    Returns ``(kcache, vcache, weights, lengths, kept)`` in memory of their own, never in place: caches
+    and weights with room for ``capacity`` tokens (default ``Tmax``), the weights 0 behind the kept
+    tokens, ``lengths = min(lengths, budget)`` and the kept tokens' old indices, int32
+    ``[B, Hkv, budget]``, -1 behind them.  ``out`` takes such a tuple to write into (its shapes then
+    give the capacity); cache rows behind the kept tokens are not written, in a call without
+    ``out`` they are undefined."""
+    _need(weights, "weights", torch.float32, 3)
+    _need(lengths, "lengths", torch.int32, 1)
+    if bits not in (8, 4):
+        raise ValueError("bits must be 8 or 4")
+    if not isinstance(kcache[0], torch.Tensor) or kcache[0].dim() != 4:
+        raise ValueError("kcache codes must be 4-D")
+    D = kcache[0].shape[3] * (1 if bits == 8 else 8)
+    B, Hkv, Tmax = shape = _need_caches(kcache, vcache, ("kcache", "vcache"), bits, 2, D, weights)
+    if weights.shape != shape or lengths.shape[0] != B:
+        raise ValueError("weights must be [B, Hkv, Tmax] and lengths [B]")
+    _same_device(weights, "weights", lengths=lengths)
+    if not 0 <= recent <= budget or budget < 1:
+        raise ValueError("0 <= recent <= budget and budget >= 1 must hold")
+    if out is None:
+        room = (B, Hkv, Tmax if capacity is None else capacity)
+        if room[2] < min(budget, Tmax):
+            raise ValueError("capacity must be at least min(budget, Tmax)")
+
+        def new(c):
+            return tuple(torch.empty(room + tuple(t.shape[3:]), dtype=t.dtype, device=t.device) if t is not None else None
+                         for t in (c if bits == 4 else (c[0], c[1], None)))
+        out = (new(kcache), new(vcache), torch.empty(room, dtype=torch.float32, device=weights.device),
+               torch.empty_like(lengths), torch.empty((B, Hkv, budget), dtype=torch.int32, device=weights.device))
+    ko, vo, wo, lo, kept = out
+    Bo, Ho, Tout = _need_caches(ko, vo, ("out kcache", "out vcache"), bits, 2, D, weights)
+    _need(wo, "out weights", torch.float32, 3)
+    _need(lo, "out lengths", torch.int32, 1)
+    _need(kept, "out kept", torch.int32, 3)
+    if (Bo, Ho) != (B, Hkv) or wo.shape != (B, Hkv, Tout) or lo.shape[0] != B or kept.shape != (B, Hkv, budget):
+        raise ValueError("out must be caches [B, Hkv, capacity, ...], weights [B, Hkv, capacity], lengths [B] and "
+                         "kept [B, Hkv, budget]")
+    if capacity is not None and Tout != capacity:
+        raise ValueError("out and capacity disagree")
+    if Tout < min(budget, Tmax):
+        raise ValueError("out must have room for min(budget, Tmax) tokens")
+    _same_device(weights, "weights", **{"out weights": wo, "out lengths": lo, "out kept": kept})
+    _call(lib().w4a16_kv_evict, "w4a16_kv_evict", weights.device, _cache_struct(kcache, vcache, bits),
+          weights.data_ptr(), lengths.data_ptr(), B, Hkv, Tmax, D, bits, budget, recent, _cache_struct(ko, vo, bits),
+          Tout, wo.data_ptr(), lo.data_ptr(), kept.data_ptr())
+    return (ko, vo, wo, lo, kept)

@@ -13,8 +13,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libw4a16.so")
 
 OK = 0
-ERR_NULL, ERR_SHAPE, ERR_GROUP, ERR_ALIGN, ERR_DTYPE, ERR_SCHEME, ERR_HIP, ERR_PATH, ERR_SCRATCH = \
-    -1, -2, -3, -4, -5, -6, -7, -8, -9
+ERR_NULL, ERR_SHAPE, ERR_GROUP, ERR_ALIGN, ERR_DTYPE, ERR_SCHEME, ERR_HIP, ERR_PATH, ERR_SCRATCH, \
+    ERR_OVERLAP = -1, -2, -3, -4, -5, -6, -7, -8, -9, -10
 F16, BF16 = 0, 1
 ASYM, SYM = 0, 1
 PATH_AUTO, PATH_GEMV, PATH_SKINNY, PATH_PREFILL = 0, 1, 2, 3
@@ -25,6 +25,12 @@ class LinearItem(ctypes.Structure):
     _fields_ = [("X", ctypes.c_void_p), ("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
                 ("group_size", ctypes.c_int64), ("qweight", ctypes.c_void_p), ("scales", ctypes.c_void_p),
                 ("zeros", ctypes.c_void_p), ("Y", ctypes.c_void_p)]
+
+
+class KvCache(ctypes.Structure):
+    """``w4a16_kv_cache`` / ``w4a16_kv_cache_out`` of the C ABI."""
+    _fields_ = [("kcodes", ctypes.c_void_p), ("kscales", ctypes.c_void_p), ("kzeros", ctypes.c_void_p),
+                ("vcodes", ctypes.c_void_p), ("vscales", ctypes.c_void_p), ("vzeros", ctypes.c_void_p)]
 
 
 _lib = None
@@ -113,6 +119,19 @@ def lib() -> ctypes.CDLL:
                                                   vp, vp, vp, vp, vp]
     L.w4a16_attention_prompt.restype = i32
     L.w4a16_attention_prompt.argtypes = [vp, vp, vp, i32, i64, i64, vp, i64, i64, i64, i64, i64, i64, vp, vp]
+    cache = ctypes.POINTER(KvCache)
+    L.w4a16_kv_attention_shared_workspace.restype = i64
+    L.w4a16_kv_attention_shared_workspace.argtypes = [i64, i64, i64, i64, i64, i64]
+    L.w4a16_kv_attention_decode_shared.restype = i32
+    L.w4a16_kv_attention_decode_shared.argtypes = [vp, i32, i64, i64, i64, i64, i32, cache, i64, i64, cache, vp, i64,
+                                                   vp, vp, vp]
+    L.w4a16_kv_attention_weights_workspace.restype = i64
+    L.w4a16_kv_attention_weights_workspace.argtypes = [i64, i64, i64, i64, i64]
+    L.w4a16_kv_attention_decode_weights.restype = i32
+    L.w4a16_kv_attention_decode_weights.argtypes = [vp, i32, i64, i64, i64, i64, i32, cache, vp, i64, vp, vp, vp, vp,
+                                                    vp]
+    L.w4a16_kv_evict.restype = i32
+    L.w4a16_kv_evict.argtypes = [cache, vp, vp, i64, i64, i64, i64, i32, i64, i64, cache, i64, vp, vp, vp, vp]
     L.w4a16_gptq_quantize.restype = i32
     L.w4a16_gptq_quantize.argtypes = [vp, i64, i64, i64, i32, vp, vp, vp, vp, vp, vp]
     _lib = L

@@ -51,6 +51,38 @@ int check_shape_group(int64_t N, int64_t K, int64_t g, int* G, int* gshift) {
     return W4A16_OK;
 }
 
+// Pointer and alignment checks of a quantized cache (const and output form).
+template <class Cache>
+int check_cache(const Cache* c, int bits) {
+    if (!c || !c->kcodes || !c->kscales || !c->vcodes || !c->vscales) return W4A16_ERR_NULL;
+    if (bits == 4 && (!c->kzeros || !c->vzeros)) return W4A16_ERR_NULL;
+    if (!aligned(c->kcodes, 16) || !aligned(c->vcodes, 16) || !aligned(c->kscales, 2) || !aligned(c->vscales, 2) ||
+        (bits == 4 && (!aligned(c->kzeros, 2) || !aligned(c->vzeros, 2))))
+        return W4A16_ERR_ALIGN;
+    return W4A16_OK;
+}
+
+w4a16::KvCache as_cache(const w4a16_kv_cache& c) {
+    return {c.kcodes, c.kscales, c.kzeros, c.vcodes, c.vscales, c.vzeros};
+}
+
+constexpr int64_t kMaxTokens = int64_t(1) << 24;          // tokens of a cached sequence
+constexpr int64_t kMaxCacheRows = int64_t(1) << 33;       // (sequence, head, token) rows of a cache
+
+// Sizes of the batched decode attention over quantized caches (the shared prefix: P of Pmax tokens).
+int check_kv_batch(int64_t B, int64_t Hq, int64_t Hkv, int64_t P, int64_t Pmax, int64_t Tmax, int64_t D) {
+    if (B < 1 || B > 65535 || Hq < 1 || Hkv < 1 || Hq > 65535 || Hq % Hkv != 0 || B * Hq > (int64_t(1) << 24) ||
+        Tmax < 1 || Tmax > kMaxTokens || P < 0 || P > Pmax || Pmax > kMaxTokens || (D != 64 && D != 128) ||
+        Hkv * Pmax + B * Hkv * Tmax > kMaxCacheRows)
+        return W4A16_ERR_SHAPE;
+    return W4A16_OK;
+}
+
+bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a && b && x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
+}
+
 int hip_status(hipError_t e) { return e == hipSuccess ? W4A16_OK : W4A16_ERR_HIP; }
 
 int validate_linear(const void* X, int dtype, int64_t M, int64_t N, int64_t K, int64_t g,
@@ -162,6 +194,7 @@ const char* w4a16_strerror(int status) {
         case W4A16_ERR_SCHEME: return "unknown quantization scheme";
         case W4A16_ERR_HIP: return "HIP runtime error at launch";
         case W4A16_ERR_PATH: return "the requested kernel path does not support this problem";
+        case W4A16_ERR_OVERLAP: return "an output overlaps an input that is still being read";
         case W4A16_ERR_SCRATCH:
             return "the problem needs more workspace than the library's static scratch buffer (64 MiB)";
         default: return "unknown status";
@@ -422,6 +455,136 @@ int w4a16_attention_prompt(const void* q, const void* k, const void* v, int dtyp
     const w4a16::PromptArgs a = {q, k, v, cu_seqlens, out, dtype, (int)B, (int)T,
                                  (int)Hq, (int)Hkv, (int)D, (int)q_stride, (int)k_stride, (int)v_stride};
     return hip_status(w4a16::launch_attention_prompt(a, static_cast<hipStream_t>(stream)));
+}
+
+int64_t w4a16_kv_attention_shared_workspace(int64_t B, int64_t Hq, int64_t Hkv, int64_t P, int64_t Tmax,
+                                            int64_t D) {
+    const int st = check_kv_batch(B, Hq, Hkv, P, P, Tmax, D);
+    if (st != W4A16_OK) return st;
+    return w4a16::kv_shared_workspace_floats(B, Hq, Hkv, P, Tmax, D);
+}
+
+int w4a16_kv_attention_decode_shared(const void* q, int dtype, int64_t B, int64_t Hq, int64_t Hkv, int64_t D,
+                                     int bits, const w4a16_kv_cache* prefix, int64_t P, int64_t Pmax,
+                                     const w4a16_kv_cache* own, const int32_t* lengths, int64_t Tmax, float* work,
+                                     void* out, void* stream) {
+    if (!q || !own || !lengths || !work || !out) return W4A16_ERR_NULL;
+    if (dtype != W4A16_F16 && dtype != W4A16_BF16) return W4A16_ERR_DTYPE;
+    if (bits != 8 && bits != 4) return W4A16_ERR_SCHEME;
+    int st = check_kv_batch(B, Hq, Hkv, P, Pmax, Tmax, D);
+    if (st == W4A16_OK) st = check_cache(own, bits);
+    if (st == W4A16_OK && P > 0) st = check_cache(prefix, bits);
+    if (st != W4A16_OK) return st;
+    if (!aligned(q, 16) || !aligned(lengths, 4) || !aligned(work, 16) || !aligned(out, 2)) return W4A16_ERR_ALIGN;
+    w4a16::KvSharedArgs a = {};
+    a.q = q;
+    a.out = out;
+    if (P > 0) a.prefix = as_cache(*prefix);
+    a.own = as_cache(*own);
+    a.lens = lengths;
+    a.dtype = dtype;
+    a.bits = bits;
+    a.B = (int)B;
+    a.Hq = (int)Hq;
+    a.Hkv = (int)Hkv;
+    a.D = (int)D;
+    a.P = (int)P;
+    a.Pmax = (int)Pmax;
+    a.Tmax = (int)Tmax;
+    return hip_status(w4a16::launch_kv_shared(a, work, static_cast<hipStream_t>(stream)));
+}
+
+int64_t w4a16_kv_attention_weights_workspace(int64_t B, int64_t Hq, int64_t Hkv, int64_t Tmax, int64_t D) {
+    const int st = check_kv_batch(B, Hq, Hkv, 0, 0, Tmax, D);
+    if (st != W4A16_OK) return st;
+    if (B * Hq * Tmax > (int64_t(1) << 36)) return W4A16_ERR_SHAPE;
+    return w4a16::kv_weights_workspace_floats(B, Hq, Hkv, Tmax, D);
+}
+
+int w4a16_kv_attention_decode_weights(const void* q, int dtype, int64_t B, int64_t Hq, int64_t Hkv, int64_t D,
+                                      int bits, const w4a16_kv_cache* own, const int32_t* lengths, int64_t Tmax,
+                                      const float* weights, float* sums, float* work, void* out, void* stream) {
+    if (!q || !own || !lengths || !sums || !work || !out) return W4A16_ERR_NULL;
+    if (dtype != W4A16_F16 && dtype != W4A16_BF16) return W4A16_ERR_DTYPE;
+    if (bits != 8 && bits != 4) return W4A16_ERR_SCHEME;
+    int st = check_kv_batch(B, Hq, Hkv, 0, 0, Tmax, D);
+    if (st == W4A16_OK && B * Hq * Tmax > (int64_t(1) << 36)) st = W4A16_ERR_SHAPE;
+    if (st == W4A16_OK) st = check_cache(own, bits);
+    if (st != W4A16_OK) return st;
+    if (!aligned(q, 16) || !aligned(lengths, 4) || (weights && !aligned(weights, 4)) || !aligned(sums, 4) ||
+        !aligned(work, 16) || !aligned(out, 2))
+        return W4A16_ERR_ALIGN;
+    const int64_t n = B * Hkv * Tmax * 4;
+    if (weights != sums && overlap(weights, n, sums, n)) return W4A16_ERR_OVERLAP;
+    w4a16::KvWeightsArgs a = {};
+    a.q = q;
+    a.out = out;
+    a.own = as_cache(*own);
+    a.lens = lengths;
+    a.weights = weights;
+    a.sums = sums;
+    a.dtype = dtype;
+    a.bits = bits;
+    a.B = (int)B;
+    a.Hq = (int)Hq;
+    a.Hkv = (int)Hkv;
+    a.D = (int)D;
+    a.Tmax = (int)Tmax;
+    return hip_status(w4a16::launch_kv_weights(a, work, static_cast<hipStream_t>(stream)));
+}
+
+int w4a16_kv_evict(const w4a16_kv_cache* in, const float* weights, const int32_t* lengths, int64_t B, int64_t Hkv,
+                   int64_t Tmax, int64_t D, int bits, int64_t budget, int64_t recent, const w4a16_kv_cache_out* out,
+                   int64_t Tout, float* weights_out, int32_t* lengths_out, int32_t* kept, void* stream) {
+    if (!in || !weights || !lengths || !out || !weights_out || !lengths_out || !kept) return W4A16_ERR_NULL;
+    if (bits != 8 && bits != 4) return W4A16_ERR_SCHEME;
+    int st = check_kv_batch(B, Hkv, Hkv, 0, 0, Tmax, D);
+    if (st == W4A16_OK && (budget < 1 || budget > kMaxTokens || recent < 0 || recent > budget || Tout > kMaxTokens ||
+                           Tout < std::min(budget, Tmax) || B * Hkv * std::max(Tout, budget) > kMaxCacheRows))
+        st = W4A16_ERR_SHAPE;
+    if (st == W4A16_OK) st = check_cache(in, bits);
+    if (st == W4A16_OK) st = check_cache(out, bits);
+    if (st != W4A16_OK) return st;
+    if (!aligned(weights, 4) || !aligned(lengths, 4) || !aligned(weights_out, 4) || !aligned(lengths_out, 4) ||
+        !aligned(kept, 4))
+        return W4A16_ERR_ALIGN;
+    // blocks read their inputs at times of their own: no output may share memory with an input,
+    // nor with another output
+    struct Span {
+        const void* p;
+        int64_t n;
+    };
+    const int64_t R = B * Hkv * Tmax, Ro = B * Hkv * Tout, cb = D * bits / 8;
+    const Span ins[] = {{in->kcodes, R * cb}, {in->vcodes, R * cb}, {in->kscales, 2 * R}, {in->vscales, 2 * R},
+                        {bits == 4 ? in->kzeros : nullptr, 2 * R}, {bits == 4 ? in->vzeros : nullptr, 2 * R},
+                        {weights, 4 * R}, {lengths, 4 * B}};
+    const Span outs[] = {{out->kcodes, Ro * cb}, {out->vcodes, Ro * cb}, {out->kscales, 2 * Ro},
+                         {out->vscales, 2 * Ro}, {bits == 4 ? out->kzeros : nullptr, 2 * Ro},
+                         {bits == 4 ? out->vzeros : nullptr, 2 * Ro}, {weights_out, 4 * Ro}, {lengths_out, 4 * B},
+                         {kept, 4 * B * Hkv * budget}};
+    for (const Span& o : outs) {
+        for (const Span& i : ins)
+            if (overlap(o.p, o.n, i.p, i.n)) return W4A16_ERR_OVERLAP;
+        for (const Span& o2 : outs)
+            if (&o != &o2 && overlap(o.p, o.n, o2.p, o2.n)) return W4A16_ERR_OVERLAP;
+    }
+    w4a16::KvEvictArgs a = {};
+    a.in = as_cache(*in);
+    a.out = {out->kcodes, out->kscales, out->kzeros, out->vcodes, out->vscales, out->vzeros};
+    a.weights = weights;
+    a.lens = lengths;
+    a.weights_out = weights_out;
+    a.lens_out = lengths_out;
+    a.kept = kept;
+    a.bits = bits;
+    a.B = (int)B;
+    a.Hkv = (int)Hkv;
+    a.D = (int)D;
+    a.Tmax = (int)Tmax;
+    a.Tout = (int)Tout;
+    a.budget = (int)budget;
+    a.recent = (int)recent;
+    return hip_status(w4a16::launch_kv_evict(a, static_cast<hipStream_t>(stream)));
 }
 
 int w4a16_select_path(int64_t M, int64_t N, int64_t K, int64_t group_size, int dtype) {

@@ -85,6 +85,56 @@ hipError_t launch_kv_attention(const void* q, int dtype, int B, int Hq, int Hkv,
                                const uint16_t* kz, const void* vc, const uint16_t* vs, const uint16_t* vz,
                                float* work, void* out, hipStream_t st);
 
+// Decode attention on the matrix cores (kv_attend.hip).  K and V caches with their parameters;
+// own: [B, Hkv, Tmax, ...] with lens (device, B entries, clamped into [0, Tmax]); prefix:
+// [Hkv, Pmax, ...], the first P tokens, shared by every sequence.
+struct KvCache {
+    const void* kc;
+    const uint16_t *ks, *kz;
+    const void* vc;
+    const uint16_t *vs, *vz;
+};
+struct KvSharedArgs {
+    const void* q;
+    void* out;
+    KvCache prefix, own;
+    const int* lens;
+    int dtype, bits, B, Hq, Hkv, D, P, Pmax, Tmax;
+};
+struct KvWeightsArgs {
+    const void* q;
+    void* out;
+    KvCache own;
+    const int* lens;
+    const float* weights;   // NULL: start from 0
+    float* sums;
+    int dtype, bits, B, Hq, Hkv, D, Tmax;
+};
+long long kv_shared_workspace_floats(long long B, long long Hq, long long Hkv, long long P, long long Tmax,
+                                     long long D);
+long long kv_weights_workspace_floats(long long B, long long Hq, long long Hkv, long long Tmax, long long D);
+hipError_t launch_kv_shared(const KvSharedArgs& a, float* work, hipStream_t st);
+hipError_t launch_kv_weights(const KvWeightsArgs& a, float* work, hipStream_t st);
+
+// Eviction (kv_evict.hip): caches [B, Hkv, Tmax, ...] to out [B, Hkv, Tout, ...], Tout >=
+// min(budget, Tmax); kept [B, Hkv, budget].
+struct KvCacheOut {
+    void* kc;
+    uint16_t *ks, *kz;
+    void* vc;
+    uint16_t *vs, *vz;
+};
+struct KvEvictArgs {
+    KvCache in;
+    const float* weights;
+    const int* lens;
+    KvCacheOut out;
+    float* weights_out;
+    int *lens_out, *kept;
+    int bits, B, Hkv, D, Tmax, Tout, budget, recent;
+};
+hipError_t launch_kv_evict(const KvEvictArgs& a, hipStream_t st);
+
 // Prompt attention (attention.hip): B sequences packed along T tokens, their bounds cu [B + 1] on
 // the device (clamped into [0, T]); rows of q / k / v are qs / ks / vs elements apart, those of
 // out Hq * D.
