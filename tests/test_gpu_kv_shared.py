@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import w4a16_dequant_gemm_amd as W4
-from tests.kv_util import attend, check_out, cmax, f64, make_cache, rows, spoil, weight_error
+from tests.kv_util import attend, check_out, cmax, f64, make_cache, offsets, rows, spoil, weight_error
 
 pytestmark = pytest.mark.gpu
 H, BF = torch.float16, torch.bfloat16
@@ -36,6 +36,7 @@ def check(out, q, kp, vp, P, k, v, lens, bits):
     Hkv = kp[1].shape[0]
     G = Hq // Hkv
     KP, VP, K, V = (rows(c, bits) for c in (kp, vp, k, v))
+    KPZ, VPZ, KZ, VZ = (offsets(c, bits) for c in (kp, vp, k, v))
     got, qd = f64(out), f64(q)
     smax = max([float(vp[1][:, :P].float().max()) if P else 0.0] +
                [float(v[1][b, :, :n].float().max()) for b, n in enumerate(lens) if n])
@@ -47,7 +48,8 @@ def check(out, q, kp, vp, P, k, v, lens, bits):
             kk = np.concatenate([KP[hk, :P], K[b, hk, :n]])
             vv = np.concatenate([VP[hk, :P], V[b, hk, :n]])
             hs = slice(hk * G, (hk + 1) * G)
-            ref, _, mag, qk = attend(qd[b, hs], kk, vv)
+            ref, _, mag, qk = attend(qd[b, hs], kk, vv, np.concatenate([KPZ[hk, :P], KZ[b, hk, :n]]),
+                                     np.concatenate([VPZ[hk, :P], VZ[b, hk, :n]]))
             check_out(got[b, hs], ref, mag, q.dtype, weight_error(D, qk), P + n, smax, c)
 
 

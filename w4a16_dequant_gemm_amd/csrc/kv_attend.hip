@@ -46,6 +46,15 @@ __device__ __forceinline__ void codes_int4(uint32_t w, f16x2 z, uint32_t out[4])
     for (int i = 0; i < 4; ++i) out[i] = as_u(as_h2(((w >> (4 * i)) & 0x000F000Fu) | 0x64006400u) - off - z);
 }
 
+// the lanes 32 .. 63 of a and the lanes 0 .. 31 of b trade places
+__device__ __forceinline__ void swap_halves(float& a, float& b) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(int, a), __builtin_bit_cast(int, b), false,
+                                                    false);
+    const int x = r[0], y = r[1];
+    a = __builtin_bit_cast(float, x);
+    b = __builtin_bit_cast(float, y);
+}
+
 // One set of caches as a block sees it: the rows of one (sequence and) kv head.
 struct CacheRows {
     const unsigned char *kc, *vc;
@@ -75,9 +84,8 @@ __device__ __forceinline__ float wave_max(float v) {
 
 // Tokens [t0, t1) of a cache for the rows row0 .. (R in all): row r is query head
 // hq0 + (r / G) * Hq + r % G of the batch.  Writes each row's (max, sum) to ml and its unnormalized
-// output (elements in storage order, see codes_int4) to po at index head * nsplit + split.
-// SCORES: also the base-2 scores, score[head * spad + token].
-template <int BITS, int D, int WQ, int WK, bool SCORES>
+// output to po at index head * nsplit + split.
+template <int BITS, int D, int WQ, int WK>
 struct Attend {
     static constexpr int NBUF = WK == 1 ? 2 : 1;
     static constexpr int KT = WK == 1 ? 64 : 128;          // tokens of a tile
@@ -91,8 +99,7 @@ struct Attend {
 
     static __device__ __forceinline__ void run(Lds& lds, const uint16_t* __restrict__ q, bool bf16, int Hq, int G,
                                                long long hq0, int row0, int R, CacheRows c, int t0, int t1, int nsplit,
-                                               int split, float2* __restrict__ ml, float* __restrict__ po,
-                                               float* __restrict__ score, int spad) {
+                                               int split, float2* __restrict__ ml, float* __restrict__ po) {
         const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
         const int n = lane & 31, h = lane >> 5;
         const int wq = wave % WQ, wk = wave / WQ;
@@ -251,19 +258,6 @@ struct Attend {
                         mt = fmaxf(mt, v);
                     }
                 }
-            if constexpr (SCORES) {
-                if (row < R) {
-#pragma unroll
-                    for (int b = 0; b < KB; ++b)
-#pragma unroll
-                        for (int g = 0; g < 4; ++g) {
-                            const int tok = tok0 + 32 * b + 8 * g + 4 * h;
-                            if (tok < t1)
-                                *reinterpret_cast<f32x4*>(score + head * spad + tok) =
-                                    f32x4{S[b][4 * g], S[b][4 * g + 1], S[b][4 * g + 2], S[b][4 * g + 3]};
-                        }
-                }
-            }
             mt = max_halves(mt);
             const float vm = __builtin_bit_cast(
                 float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, lds.vmax[buf][wk * KW / 64])));
@@ -312,6 +306,21 @@ struct Attend {
 
         l = sum_halves(l);
         const float vout = vcap * 0.0078125f;              // O in its own units
+        if constexpr (BITS == 4) {
+            // lane halves hold elements 0 4 1 5 and 2 6 3 7 of every eight: to 0 .. 3 and 4 .. 7
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    float e0 = o[i][4 * g], e1 = o[i][4 * g + 1], e2 = o[i][4 * g + 2], e3 = o[i][4 * g + 3];
+                    swap_halves(e0, e1);
+                    swap_halves(e2, e3);
+                    o[i][4 * g] = e0;
+                    o[i][4 * g + 1] = e2;
+                    o[i][4 * g + 2] = e1;
+                    o[i][4 * g + 3] = e3;
+                }
+        }
         const long long at = head * nsplit + split;
         if constexpr (WK == 1) {
             if (row < R) {
@@ -368,6 +377,377 @@ struct Attend {
     }
 };
 
+// 16 rows x 16 keys (S) or 16 elements (O) per tile: lane l holds column l % 16 (a query row), rows
+// 4 (l / 16) + i.
+__device__ __forceinline__ f32x4 mfma16(const u32x4& a, const u32x4& b, const f32x4& c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0,
+                                                  0);
+}
+
+// Transposing LDS reads of the four groups of 16 lanes: 8-bit (8 rows of 16 bytes, lanes 2 r and
+// 2 r + 1 at row r) and 4-bit (16 rows of 16 nibbles, lane r at row r); lane i of a group receives
+// column i, the rows in order.
+typedef int i32x2 __attribute__((ext_vector_type(2)));
+template <int BITS>
+__device__ __forceinline__ u32x2 lds_read_tr_codes(const unsigned char* p) {
+    const auto q = (__attribute__((address_space(3))) i32x2*)p;
+    if constexpr (BITS == 8) return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr8_b64_v2i32(q));
+    else return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr4_b64_v2i32(q));
+}
+
+// The same value of the four lanes l % 16 + 16 k: their maximum / sum, in all of them.
+template <class Op>
+__device__ __forceinline__ float across_quarters(float x, Op op) {
+    int i = __builtin_bit_cast(int, x);
+    const auto r = __builtin_amdgcn_permlane16_swap(i, i, false, false);
+    int a = r[0], b = r[1];
+    float lo, hi;
+    halves(op(__builtin_bit_cast(float, a), __builtin_bit_cast(float, b)), lo, hi);
+    return op(lo, hi);
+}
+
+// Orders what one wave writes to LDS before what its other lanes read of it (the LDS pipe keeps a
+// wave's accesses in order; this keeps the compiler from moving them).
+__device__ __forceinline__ void wave_lds_fence() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// Few rows: tokens [t0, t1) of a cache for the rows row0 .. row0 + 15 (R in all; numbered as in
+// Attend).  Nothing here is bound by arithmetic, so the aim is loads in flight and few
+// instructions: each wave of the block streams tiles of its own (wave, wave + 4, ...), with no
+// barrier until the four are joined at the end.
+//   K's codes go from memory to the matrix cores: lane l loads the quarter l / 16 of key l % 16's
+//     row, consecutive bytes, and the query's fragment is loaded in the same order.
+//   V's codes are stored to LDS as they are and read back transposed (8- or 4-bit).
+//   A code u (int8: c + 128) becomes the fp16 subnormal u 2^-24 by masks or byte permutes alone; the
+//     matrix cores multiply subnormals exactly.  The zero point (int8: 128) is taken out of the fp32
+//     sums: S starts at -z sum(q) 2^-24, and sum(p z) comes out of one more product, with the same
+//     rounded p, and is subtracted from O at the end.
+//   4-bit: two of the four masks leave 16 u; the query entries (K) and the weights (V, through the
+//     token's scale) that meet them are divided by 16.
+// Weights p s_t enter the second product times VNORM / vcap, vcap the largest V scale so far, and the
+// running maximum may lag by LAG, so that they stay below 2^15; an fp16 subnormal among them is
+// below 2^-14 of that, so its rounding adds at most 2^-32 vcap.
+template <int BITS, int D, bool SCORES>
+struct Stream {
+    static constexpr int KT = BITS == 8 && D == 128 ? 32 : 64;   // tokens of a tile
+    static constexpr int NS = KT / 16;                           // S tiles
+    static constexpr int RB = BITS == 8 ? D : D / 2;             // bytes of a cached row
+    static constexpr int KW = RB / 16;                           // K: dwords per lane and S tile
+    static constexpr int VL = KT * RB / 1024 > 0 ? KT * RB / 1024 : 1;   // V: 16-byte loads per lane
+    static constexpr int VP = RB / 16;                           // 16-byte pieces of a row
+    static constexpr int QS = D / 32;                            // k-steps of the first product
+    static constexpr float LAG = BITS == 8 ? 8.0f : 4.0f;
+    static constexpr float VNORM = BITS == 8 ? 128.0f : 2048.0f;
+    static_assert(KT * RB % 1024 == 0, "whole loads");
+
+    struct alignas(16) WaveLds {
+        unsigned char v[KT * RB];
+        float ks[KT], vs[KT], kz[BITS == 4 ? KT : 1];
+        _Float16 vz[BITS == 4 ? KT : 4];
+    };
+    union Lds {
+        WaveLds w[4];
+        float join[4][D / 4][16][4];
+    };
+
+    // Where 16-byte piece c of token r's V row sits: spread over the banks for the transposing reads,
+    // whose 32 lanes of a pass take one piece of the tokens 4 q + {0 .. 3} (+ 16 k), q of two values.
+    static __device__ __forceinline__ int vpiece(int r, int c) {
+        if constexpr (VP == 8) return c ^ (((r >> 1) & 1) | ((r >> 1) & 2) | ((r >> 2) & 4));
+        else if constexpr (VP == 4 && BITS == 8) return c ^ (((r >> 2) & 1) | ((r >> 3) & 2));
+        else if constexpr (VP == 4) return c ^ ((r >> 4) & 3);
+        else return c ^ ((r >> 5) & 1);
+    }
+
+    static __device__ __forceinline__ void run(Lds& lds, float (*sm)[16], float (*sl)[16],
+                                               const uint16_t* __restrict__ q, bool bf16, int Hq, int G, long long hq0,
+                                               int row0, int R, const CacheRows& c, int t0, int t1, int nsplit,
+                                               int split, float2* __restrict__ ml, float* __restrict__ po,
+                                               float* __restrict__ score, int spad) {
+        const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+        const int n = lane & 15, qd = lane >> 4;
+        const int row = row0 + n;
+        const int rr = min(row, R - 1);
+        const long long head = hq0 + (long long)(rr / G) * Hq + rr % G;
+        WaveLds& L = lds.w[wave];
+
+        u32x4 kr[NS * KW / 4 > 0 ? NS * KW / 4 : 1], vr[VL];
+        uint16_t pk = 0, pv = 0, pkz = 0, pvz = 0;
+        auto load = [&](int t) {
+            const int base = t0 + t * KT;
+            // tokens behind the span: its last one, masked out of the scores
+#pragma unroll
+            for (int s = 0; s < NS; ++s) {
+                const uint32_t off = (uint32_t)min(base + 16 * s + n, t1 - 1) * RB + RB / 4 * qd;
+                if constexpr (KW == 2) {
+                    const u32x2 x = *reinterpret_cast<const u32x2*>(c.kc + off);
+                    kr[s / 2][2 * (s % 2)] = x.x;
+                    kr[s / 2][2 * (s % 2) + 1] = x.y;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < KW / 4; ++i)
+                        kr[s * (KW / 4) + i] = *reinterpret_cast<const u32x4*>(c.kc + off + 16 * i);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < VL; ++i) {
+                const int p = lane + 64 * i;
+                vr[i] = *reinterpret_cast<const u32x4*>(c.vc + (uint32_t)min(base + p / VP, t1 - 1) * RB + 16 * (p % VP));
+            }
+            const uint32_t tok = (uint32_t)min(base + lane % KT, t1 - 1);
+            if constexpr (KT == 64) {
+                pk = c.ks[tok];
+                pv = c.vs[tok];
+            } else {
+                pk = (lane < 32 ? c.ks : c.vs)[tok];             // lower half K's, upper half V's scales
+            }
+            if constexpr (BITS == 4) {
+                pkz = c.kz[tok];
+                pvz = c.vz[tok];
+            }
+        };
+        const int tiles = (t1 - t0 + KT - 1) / KT;
+        if (wave < tiles) load(wave);
+        __builtin_amdgcn_sched_barrier(0);
+
+        // the row's query as fp16 times 2^e, in the order of the codes, and its sum
+        u32x4 qf[QS];
+        float cl, qsum = 0.0f;                             // score scale; -2^-24 sum of the fp16 query
+        {
+            const uint16_t* qp = q + head * D + qd * (D / 4);
+#pragma unroll
+            for (int s = 0; s < QS; ++s) qf[s] = *reinterpret_cast<const u32x4*>(qp + 8 * s);
+            cl = 1.4426950408889634f * 16777216.0f / sqrtf((float)D);
+            if (bf16) {
+                float mx = 0.0f;
+#pragma unroll
+                for (int s = 0; s < QS; ++s)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        mx = fmaxf(mx, fmaxf(fabsf(bf2f(qf[s][i] & 0xFFFFu)), fabsf(bf2f(qf[s][i] >> 16))));
+                mx = across_quarters(mx, [](float a, float b) { return fmaxf(a, b); });
+                const int e = mx > 0.0f ? 15 - __builtin_amdgcn_frexp_expf(mx) : 0;
+                cl = ldexpf(cl, -e);
+#pragma unroll
+                for (int s = 0; s < QS; ++s)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        qf[s][i] = pack2<DT_F16>(ldexpf(bf2f(qf[s][i] & 0xFFFFu), e), ldexpf(bf2f(qf[s][i] >> 16), e));
+            }
+#pragma unroll
+            for (int s = 0; s < QS; ++s) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) qsum += pair_sum<DT_F16>(qf[s][i]);
+                if constexpr (BITS == 4) {
+                    uint32_t o[4];
+                    permute_x8(qf[s].x, qf[s].y, qf[s].z, qf[s].w, o);
+                    const f16x2 sixteenth = {(_Float16)0.0625f, (_Float16)0.0625f};
+                    qf[s] = u32x4{o[0], as_u(as_h2(o[1]) * sixteenth), o[2], as_u(as_h2(o[3]) * sixteenth)};
+                }
+            }
+            qsum = across_quarters(qsum, [](float a, float b) { return a + b; }) * -5.9604644775390625e-8f;
+        }
+
+        constexpr int OT = D / 16;
+        f32x4 o[OT], oz = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < OT; ++i) o[i] = oz;
+        const float NEG = -__builtin_inff();
+        float m = NEG, l = 0.0f;                           // base-2 domain
+        float vcap = 5.9604644775390625e-8f;               // fp16's smallest
+
+        for (int t = wave; t < tiles; t += 4) {
+            // this tile's V codes and parameters to LDS
+#pragma unroll
+            for (int i = 0; i < VL; ++i) {
+                const int p = lane + 64 * i;
+                *reinterpret_cast<u32x4*>(L.v + (p / VP) * RB + 16 * vpiece(p / VP, p % VP)) = vr[i];
+            }
+            const float vsc = KT == 64 ? h2f(pv) : lane < 32 ? 0.0f : h2f(pk);
+            if (__builtin_amdgcn_ballot_w64(fabsf(vsc) > vcap)) {
+                const float vn = wave_max(fmaxf(fabsf(vsc), vcap));
+                const float f = vcap / vn;
+                vcap = vn;
+#pragma unroll
+                for (int i = 0; i < OT; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[i][e] *= f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) oz[e] *= f;
+            }
+            const float vinv = VNORM / vcap;
+            if constexpr (KT == 64) {
+                L.ks[lane] = h2f(pk);
+                L.vs[lane] = BITS == 4 && (lane & 2) ? vsc * (vinv * 0.0625f) : vsc * vinv;
+            } else {
+                (lane < 32 ? L.ks : L.vs)[lane & 31] = lane < 32 ? h2f(pk) : vsc * vinv;
+            }
+            if constexpr (BITS == 4) {
+                L.kz[lane] = h2f(pkz);
+                const _Float16 z = __builtin_bit_cast(_Float16, pvz);
+                L.vz[lane] = lane & 2 ? z * (_Float16)16.0f : z;
+            }
+            wave_lds_fence();
+
+            // S = q . u - z sum(q), in units of 2^-24
+            f32x4 S[NS];
+#pragma unroll
+            for (int s = 0; s < NS; ++s) {
+                if constexpr (BITS == 8) {
+                    const float b = 128.0f * qsum;
+                    S[s] = f32x4{b, b, b, b};
+                } else {
+                    S[s] = *reinterpret_cast<const f32x4*>(&L.kz[16 * s + 4 * qd]) * qsum;
+                }
+#pragma unroll
+                for (int k = 0; k < QS; ++k) {
+                    u32x4 a;
+                    if constexpr (BITS == 8) {
+                        const int at = s * KW + 2 * k;
+                        const uint32_t x = kr[at / 4][at % 4] ^ 0x80808080u, y = kr[at / 4][at % 4 + 1] ^ 0x80808080u;
+                        a = u32x4{perm(0u, x, 0x0C010C00u), perm(0u, x, 0x0C030C02u), perm(0u, y, 0x0C010C00u),
+                                  perm(0u, y, 0x0C030C02u)};
+                    } else {
+                        const int at = s * KW + k;
+                        uint32_t d[4];
+                        unpack_mask_f16(kr[at / 4][at % 4], d);
+                        a = u32x4{d[0], d[1], d[2], d[3]};
+                    }
+                    S[s] = mfma16(a, qf[k], S[s]);
+                }
+            }
+            if (t + 4 < tiles) load(t + 4);
+
+            const int tok0 = t0 + t * KT;
+            float mt = NEG;
+#pragma unroll
+            for (int s = 0; s < NS; ++s) S[s] = S[s] * (*reinterpret_cast<const f32x4*>(&L.ks[16 * s + 4 * qd]) * cl);
+            if (tok0 + KT > t1) {
+#pragma unroll
+                for (int s = 0; s < NS; ++s)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (tok0 + 16 * s + 4 * qd + i >= t1) S[s][i] = NEG;
+            }
+#pragma unroll
+            for (int s = 0; s < NS; ++s)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) mt = fmaxf(mt, S[s][i]);
+            if constexpr (SCORES) {
+                if (row < R) {
+#pragma unroll
+                    for (int s = 0; s < NS; ++s) {
+                        const int tok = tok0 + 16 * s + 4 * qd;
+                        if (tok < t1) *reinterpret_cast<f32x4*>(score + head * spad + tok) = S[s];
+                    }
+                }
+            }
+            mt = across_quarters(mt, [](float a, float b) { return fmaxf(a, b); });
+            if (__builtin_amdgcn_ballot_w64(mt > m + LAG)) {
+                const float mn = fmaxf(m, mt);
+                const float f = mn == NEG ? 1.0f : exp2_raw(m - mn);
+                m = mn;
+                l *= f;
+#pragma unroll
+                for (int i = 0; i < OT; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[i][e] *= f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) oz[e] *= f;
+            }
+            const float ms = m == NEG ? 0.0f : m;          // a row with nothing yet: every weight is 0
+            u32x4 P[NS / 2];
+#pragma unroll
+            for (int s = 0; s < NS; ++s) {
+                const f32x4 v4 = *reinterpret_cast<const f32x4*>(&L.vs[16 * s + 4 * qd]);
+                float p[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    p[i] = exp2_raw(S[s][i] - ms);
+                    l += p[i];
+                    p[i] *= v4[i];
+                }
+                P[s / 2][2 * (s % 2)] = pack2<DT_F16>(p[0], p[1]);
+                P[s / 2][2 * (s % 2) + 1] = pack2<DT_F16>(p[2], p[3]);
+            }
+            // O += V^T P^T with raw codes, oz += z P
+#pragma unroll
+            for (int k = 0; k < NS / 2; ++k) {
+                u32x4 z;
+                if constexpr (BITS == 8) {
+                    z = u32x4{0x58005800u, 0x58005800u, 0x58005800u, 0x58005800u};       // 128
+                } else {
+                    const u32x2 z0 = *reinterpret_cast<const u32x2*>(&L.vz[32 * k + 4 * qd]);
+                    const u32x2 z1 = *reinterpret_cast<const u32x2*>(&L.vz[32 * k + 16 + 4 * qd]);
+                    z = u32x4{z0.x, z0.y, z1.x, z1.y};
+                }
+                oz = mfma16(z, P[k], oz);
+            }
+#pragma unroll
+            for (int i = 0; i < OT; ++i) {
+                if constexpr (BITS == 8) {
+#pragma unroll
+                    for (int k = 0; k < NS / 2; ++k) {
+                        const int r = n >> 1;                                      // row of the lane pair
+                        const int tok = 32 * k + 4 * qd + (r & 3) + 16 * (r >> 2);
+                        u32x2 w = lds_read_tr_codes<8>(L.v + tok * RB + 16 * vpiece(tok, i) + 8 * (n & 1));
+                        w.x ^= 0x80808080u;
+                        w.y ^= 0x80808080u;
+                        o[i] = mfma16(u32x4{perm(0u, w.x, 0x0C010C00u), perm(0u, w.x, 0x0C030C02u),
+                                            perm(0u, w.y, 0x0C010C00u), perm(0u, w.y, 0x0C030C02u)},
+                                      P[k], o[i]);
+                    }
+                } else {
+                    // row r of the group is the token whose nibble the masks put at its place: nibbles
+                    // a and a + 4 of a dword are elements 2 a and 2 a + 1 of the fragment
+                    const int j = 2 * (n & 3) + ((n >> 2) & 1);
+                    const int tok = 32 * (n >> 3) + 4 * qd + (j & 3) + 16 * (j >> 2);
+                    const u32x2 w = lds_read_tr_codes<4>(L.v + tok * RB + 16 * vpiece(tok, i >> 1) + 8 * (i & 1));
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        uint32_t d[4];
+                        unpack_mask_f16(k ? w.y : w.x, d);
+                        o[i] = mfma16(u32x4{d[0], d[1], d[2], d[3]}, P[k], o[i]);
+                    }
+                }
+            }
+            wave_lds_fence();                              // before the next tile overwrites this one
+        }
+
+        // join the four waves: each leaves its output, rescaled to the common maximum, in LDS and
+        // adds up its quarter of the elements over all of them
+        l = across_quarters(l, [](float a, float b) { return a + b; });
+        if (qd == 0) {
+            sm[wave][n] = m;
+            sl[wave][n] = l;
+        }
+        __syncthreads();
+        const float M = fmaxf(fmaxf(sm[0][n], sm[1][n]), fmaxf(sm[2][n], sm[3][n]));
+        float Lt = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) Lt += M == NEG ? 0.0f : sl[w][n] * exp2_raw(sm[w][n] - M);
+        const float f = M == NEG ? 0.0f : exp2_raw(m - M) * (vcap / VNORM);
+#pragma unroll
+        for (int i = 0; i < OT; ++i)
+            *reinterpret_cast<f32x4*>(lds.join[wave][4 * i + qd][n]) = (o[i] * 16777216.0f - oz) * f;
+        __syncthreads();
+        if (row < R) {
+            const long long at = head * nsplit + split;
+            if (wave == 0 && qd == 0) ml[at] = make_float2(M, Lt);
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) {
+                const int dq = wave * (D / 16) + 4 * i + qd;
+                f32x4 a = *reinterpret_cast<const f32x4*>(lds.join[0][dq][n]);
+#pragma unroll
+                for (int w = 1; w < 4; ++w) a += *reinterpret_cast<const f32x4*>(lds.join[w][dq][n]);
+                *reinterpret_cast<f32x4*>(po + at * D + 4 * dq) = a;
+            }
+        }
+    }
+};
+
 template <int BITS, int D>
 __device__ __forceinline__ CacheRows cache_rows(const KvCache& c, long long rowbase) {
     constexpr int RB = BITS == 8 ? D : D / 2;
@@ -390,14 +770,14 @@ __device__ __forceinline__ void empty_split(long long hq0, int G, int Hq, int ro
     }
 }
 
-// The shared prefix: block = (kv head and split, tile of 32 WQ rows).  The row tiles of one span run
-// on one XCD, one after the other, so that the span's codes are read from HBM once.
+// The shared prefix, many rows: block = (kv head and split, tile of 32 WQ rows).  The row tiles of
+// one span run on one XCD, one after the other, so that the span's codes are read from HBM once.
 template <int BITS, int D, int WQ>
 __global__ __launch_bounds__(kThreads, 2) void kv_prefix_kernel(const uint16_t* __restrict__ q, int bf16, int B, int Hq,
                                                                 int Hkv, KvCache c, int P, int Pmax, int chunk,
                                                                 int psplit, int nsplit, float2* __restrict__ ml,
                                                                 float* __restrict__ po) {
-    using A = Attend<BITS, D, WQ, 4 / WQ, false>;
+    using A = Attend<BITS, D, WQ, 4 / WQ>;
     __shared__ __attribute__((aligned(16))) typename A::Lds lds;
     const int G = Hq / Hkv, R = B * G;
     const int rtiles = (R + 32 * WQ - 1) / (32 * WQ);
@@ -407,30 +787,62 @@ __global__ __launch_bounds__(kThreads, 2) void kv_prefix_kernel(const uint16_t* 
     const int kvh = span / psplit, split = span % psplit;
     const int t0 = split * chunk, t1 = min(P, t0 + chunk);
     A::run(lds, q, bf16 != 0, Hq, G, (long long)kvh * G, rt * 32 * WQ, R,
-           cache_rows<BITS, D>(c, (long long)kvh * Pmax), t0, t1, nsplit, split, ml, po, nullptr, 0);
+           cache_rows<BITS, D>(c, (long long)kvh * Pmax), t0, t1, nsplit, split, ml, po);
 }
 
-// The sequences' own caches: block = (split, kv head and tile of 32 of its heads, sequence).
+// Streaming: the first `pblocks` blocks take the shared prefix where it has few rows (block = kv head,
+// tile of 16 of its B G rows, split), the others the sequences' own caches (block = sequence, kv
+// head, tile of 16 of its G heads, split; splits vary fastest).
+struct StreamGrid {
+    int pblocks, psplit, pchunk, P, Pmax;    // prefix splits come first among a row's nsplit
+    int osplit, ochunk, Tmax, nsplit;
+};
 template <int BITS, int D, bool SCORES>
-__global__ __launch_bounds__(kThreads, 2) void kv_own_kernel(const uint16_t* __restrict__ q, int bf16, int Hq, int Hkv,
-                                                             KvCache c, const int* __restrict__ lens, int Tmax,
-                                                             int chunk, int first, int nsplit, float2* __restrict__ ml,
-                                                             float* __restrict__ po, float* __restrict__ score,
-                                                             int spad) {
-    using A = Attend<BITS, D, 1, 4, SCORES>;
+__global__ __launch_bounds__(kThreads, 3) void kv_stream_kernel(const uint16_t* __restrict__ q, int bf16, int B, int Hq,
+                                                                int Hkv, KvCache prefix, KvCache own,
+                                                                const int* __restrict__ lens, StreamGrid g,
+                                                                float2* __restrict__ ml, float* __restrict__ po,
+                                                                float* __restrict__ score, int spad) {
+    using A = Stream<BITS, D, SCORES>;
     __shared__ __attribute__((aligned(16))) typename A::Lds lds;
-    const int G = Hq / Hkv, htiles = (G + 31) / 32;
-    const int kvh = blockIdx.y / htiles, row0 = 32 * (blockIdx.y % htiles);
-    const int b = blockIdx.z, split = first + blockIdx.x;
-    const int T = min(max(lens[b], 0), Tmax);
-    const int t0 = blockIdx.x * chunk, t1 = min(T, t0 + chunk);
-    const long long hq0 = (long long)b * Hq + (long long)kvh * G;
-    if (t0 >= t1) {
-        empty_split(hq0, G, Hq, row0, min(32, G - row0), nsplit, split, ml);
-        return;
+    __shared__ float sm[4][16], sl[4][16];
+    const int G = Hq / Hkv;
+    int id = blockIdx.x;
+    CacheRows c;
+    long long hq0;
+    int row0, R, t0, t1, split;
+    if (id < g.pblocks) {
+        R = B * G;
+        const int rtiles = (R + 15) / 16;
+        row0 = 16 * (id % rtiles);
+        id /= rtiles;
+        split = id % g.psplit;
+        const int kvh = id / g.psplit;
+        hq0 = (long long)kvh * G;
+        t0 = split * g.pchunk;
+        t1 = min(g.P, t0 + g.pchunk);
+        c = cache_rows<BITS, D>(prefix, (long long)kvh * g.Pmax);
+    } else {
+        id -= g.pblocks;
+        R = G;
+        const int htiles = (G + 15) / 16;
+        split = id % g.osplit;
+        id /= g.osplit;
+        row0 = 16 * (id % htiles);
+        id /= htiles;
+        const int kvh = id % Hkv, b = id / Hkv;
+        hq0 = (long long)b * Hq + (long long)kvh * G;
+        const int T = min(max(lens[b], 0), g.Tmax);
+        t0 = split * g.ochunk;
+        t1 = min(T, t0 + g.ochunk);
+        split += g.psplit;
+        if (t0 >= t1) {
+            empty_split(hq0, G, Hq, row0, min(16, G - row0), g.nsplit, split, ml);
+            return;
+        }
+        c = cache_rows<BITS, D>(own, ((long long)b * Hkv + kvh) * g.Tmax);
     }
-    A::run(lds, q, bf16 != 0, Hq, G, hq0, row0, G, cache_rows<BITS, D>(c, ((long long)b * Hkv + kvh) * Tmax), t0, t1,
-           nsplit, split, ml, po, score, spad);
+    A::run(lds, sm, sl, q, bf16 != 0, Hq, G, hq0, row0, R, c, t0, t1, g.nsplit, split, ml, po, score, spad);
 }
 
 // (max, sum) over all splits of a row; every lane of the wave gets it.
@@ -451,7 +863,7 @@ __device__ __forceinline__ void row_stats(const float2* __restrict__ ml, int nsp
 
 // One block per query head of the batch: wave w adds up splits w, w + 4, ...; a row that saw no
 // token gets zeros.
-template <int BITS, int D>
+template <int D>
 __device__ __forceinline__ void merge_row(float (*part)[D], long long head, const float2* __restrict__ ml,
                                           const float* __restrict__ po, int nsplit, int bf16,
                                           uint16_t* __restrict__ out) {
@@ -479,24 +891,22 @@ __device__ __forceinline__ void merge_row(float (*part)[D], long long head, cons
     __syncthreads();
     if (tid < D) {
         const float s = (part[0][tid] + part[1][tid]) + (part[2][tid] + part[3][tid]);
-        // 4-bit rows are stored in the order 0 4 1 5 2 6 3 7 of every eight elements
-        const int e = BITS == 8 ? tid : (tid & ~7) + ((tid & 1) << 2) + ((tid & 7) >> 1);
         const float v = L > 0.0f ? s / L : 0.0f;
-        out[head * D + e] = bf16 ? f2bf_bits(v) : f2h_bits(v);
+        out[head * D + tid] = bf16 ? f2bf_bits(v) : f2h_bits(v);
     }
 }
 
-template <int BITS, int D>
+template <int D>
 __global__ __launch_bounds__(kThreads) void kv_merge_kernel(const float2* __restrict__ ml, const float* __restrict__ po,
                                                             int nsplit, int bf16, uint16_t* __restrict__ out) {
     __shared__ float part[4][D];
-    merge_row<BITS, D>(part, blockIdx.x, ml, po, nsplit, bf16, out);
+    merge_row<D>(part, blockIdx.x, ml, po, nsplit, bf16, out);
 }
 
 // Output and accumulated weights in one launch: the first `heads` blocks merge a query head each,
 // the others turn kSpan scores of a (sequence, kv head) into weights.
 constexpr int kSpan = 4 * kThreads;
-template <int BITS, int D>
+template <int D>
 __global__ __launch_bounds__(kThreads) void kv_weights_kernel(const float2* __restrict__ ml,
                                                               const float* __restrict__ po, int nsplit, int bf16,
                                                               uint16_t* __restrict__ out, int heads, int Hq, int Hkv,
@@ -506,7 +916,7 @@ __global__ __launch_bounds__(kThreads) void kv_weights_kernel(const float2* __re
                                                               float* __restrict__ sums) {
     __shared__ float part[4][D];
     if (blockIdx.x < (unsigned)heads) {
-        merge_row<BITS, D>(part, blockIdx.x, ml, po, nsplit, bf16, out);
+        merge_row<D>(part, blockIdx.x, ml, po, nsplit, bf16, out);
         return;
     }
     const int i = blockIdx.x - heads;
@@ -535,57 +945,64 @@ __global__ __launch_bounds__(kThreads) void kv_weights_kernel(const float2* __re
 
 // ------------------------------------------------------------------------------- host side
 
-constexpr long long kBlocks = 2048;      // blocks of the own caches' kernel to aim for
+constexpr long long kBlocks = 2048;      // blocks of the streaming kernel to aim for
 constexpr long long kPrefixBlocks = 1024;
 constexpr int kMinChunk = 256;           // tokens of a split, at least
+constexpr int kStreamRows = 16;          // prefix rows per kv head up to which it is streamed
 
 int divup(long long a, long long b) { return (int)((a + b - 1) / b); }
 
-// tokens per split of a sequence's own cache (a multiple of the tile)
-int own_chunk(long long B, long long Hq, long long Hkv, long long T) {
-    const long long pairs = B * Hkv * ((Hq / Hkv + 31) / 32);
-    const long long ns = kBlocks / pairs > 1 ? kBlocks / pairs : 1;
-    const long long c = divup(divup(T, ns), 128) * 128;
-    return (int)(c < kMinChunk ? kMinChunk : c);
+int chunk_of(long long T, long long tiles, long long blocks) {
+    const long long ns = blocks / tiles > 1 ? blocks / tiles : 1;
+    const long long c = divup(divup(T, ns), kMinChunk) * (long long)kMinChunk;
+    return (int)c;
 }
-int prefix_wq(long long R) { return R <= 32 ? 1 : R <= 64 ? 2 : 4; }
+// tokens per split of a sequence's own cache, and of the prefix
+int own_chunk(long long B, long long Hq, long long Hkv, long long T) {
+    return chunk_of(T, B * Hkv * divup(Hq / Hkv, 16), kBlocks);
+}
+int prefix_wq(long long R) { return R <= kStreamRows ? 0 : R <= 64 ? 2 : 4; }   // 0: streaming
 int prefix_chunk(long long B, long long Hq, long long Hkv, long long P) {
+    if (P == 0) return kMinChunk;
     const long long R = B * (Hq / Hkv);
-    const long long tiles = Hkv * divup(R, 32 * prefix_wq(R));
-    const long long ns = kPrefixBlocks / tiles > 1 ? kPrefixBlocks / tiles : 1;
-    const long long c = divup(divup(P, ns), 128) * 128;
-    return (int)(c < kMinChunk ? kMinChunk : c);
+    const int wq = prefix_wq(R);
+    return wq == 0 ? chunk_of(P, Hkv * divup(R, 16), kBlocks) : chunk_of(P, Hkv * divup(R, 32 * wq), kPrefixBlocks);
 }
 
 long long parts_floats(long long heads, long long ns, long long D) { return heads * ns * (D + 2); }
 
 template <int BITS, int D>
 hipError_t shared(const KvSharedArgs& a, float* work, hipStream_t st) {
-    const int pc = prefix_chunk(a.B, a.Hq, a.Hkv, a.P), ps = divup(a.P, pc);
-    const int oc = own_chunk(a.B, a.Hq, a.Hkv, a.Tmax), os = divup(a.Tmax, oc);
-    const int ns = ps + os, G = a.Hq / a.Hkv;
-    const long long heads = (long long)a.B * a.Hq;
+    const int G = a.Hq / a.Hkv;
+    StreamGrid g = {};
+    g.P = a.P;
+    g.Pmax = a.Pmax;
+    g.Tmax = a.Tmax;
+    g.pchunk = prefix_chunk(a.B, a.Hq, a.Hkv, a.P);
+    g.psplit = divup(a.P, g.pchunk);
+    g.ochunk = own_chunk(a.B, a.Hq, a.Hkv, a.Tmax);
+    g.osplit = divup(a.Tmax, g.ochunk);
+    g.nsplit = g.psplit + g.osplit;
+    const long long heads = (long long)a.B * a.Hq, R = (long long)a.B * G;
     float* po = work;                                       // 16-byte aligned rows first
-    float2* ml = reinterpret_cast<float2*>(work + heads * ns * D);
+    float2* ml = reinterpret_cast<float2*>(work + heads * g.nsplit * D);
     const auto q = static_cast<const uint16_t*>(a.q);
-    const int bf16 = a.dtype == DT_BF16;
-    if (ps > 0) {
-        const long long R = (long long)a.B * G;
-        const int wq = prefix_wq(R), rtiles = divup(R, 32 * wq);
-        const dim3 grid((unsigned)(8 * divup((long long)a.Hkv * ps, 8) * (long long)rtiles));
-        if (wq == 1)
-            hipLaunchKernelGGL((kv_prefix_kernel<BITS, D, 1>), grid, dim3(kThreads), 0, st, q, bf16, a.B, a.Hq, a.Hkv,
-                               a.prefix, a.P, a.Pmax, pc, ps, ns, ml, po);
-        else if (wq == 2)
+    const int bf16 = a.dtype == DT_BF16, wq = prefix_wq(R);
+    if (wq == 0) {
+        g.pblocks = a.Hkv * g.psplit * divup(R, 16);
+    } else if (g.psplit > 0) {
+        const dim3 grid((unsigned)(8 * divup((long long)a.Hkv * g.psplit, 8) * (long long)divup(R, 32 * wq)));
+        if (wq == 2)
             hipLaunchKernelGGL((kv_prefix_kernel<BITS, D, 2>), grid, dim3(kThreads), 0, st, q, bf16, a.B, a.Hq, a.Hkv,
-                               a.prefix, a.P, a.Pmax, pc, ps, ns, ml, po);
+                               a.prefix, a.P, a.Pmax, g.pchunk, g.psplit, g.nsplit, ml, po);
         else
             hipLaunchKernelGGL((kv_prefix_kernel<BITS, D, 4>), grid, dim3(kThreads), 0, st, q, bf16, a.B, a.Hq, a.Hkv,
-                               a.prefix, a.P, a.Pmax, pc, ps, ns, ml, po);
+                               a.prefix, a.P, a.Pmax, g.pchunk, g.psplit, g.nsplit, ml, po);
     }
-    hipLaunchKernelGGL((kv_own_kernel<BITS, D, false>), dim3(os, a.Hkv * divup(G, 32), a.B), dim3(kThreads), 0, st, q,
-                       bf16, a.Hq, a.Hkv, a.own, a.lens, a.Tmax, oc, ps, ns, ml, po, nullptr, 0);
-    hipLaunchKernelGGL((kv_merge_kernel<BITS, D>), dim3((unsigned)heads), dim3(kThreads), 0, st, ml, po, ns, bf16,
+    const unsigned blocks = (unsigned)(g.pblocks + (long long)a.B * a.Hkv * divup(G, 16) * g.osplit);
+    hipLaunchKernelGGL((kv_stream_kernel<BITS, D, false>), dim3(blocks), dim3(kThreads), 0, st, q, bf16, a.B, a.Hq,
+                       a.Hkv, a.prefix, a.own, a.lens, g, ml, po, nullptr, 0);
+    hipLaunchKernelGGL((kv_merge_kernel<D>), dim3((unsigned)heads), dim3(kThreads), 0, st, ml, po, g.nsplit, bf16,
                        static_cast<uint16_t*>(a.out));
     return hipGetLastError();
 }
@@ -594,18 +1011,24 @@ int score_pad(long long Tmax) { return (int)((Tmax + 3) / 4 * 4); }
 
 template <int BITS, int D>
 hipError_t weights(const KvWeightsArgs& a, float* work, hipStream_t st) {
-    const int oc = own_chunk(a.B, a.Hq, a.Hkv, a.Tmax), ns = divup(a.Tmax, oc), G = a.Hq / a.Hkv;
+    const int G = a.Hq / a.Hkv;
+    StreamGrid g = {};
+    g.Tmax = a.Tmax;
+    g.ochunk = own_chunk(a.B, a.Hq, a.Hkv, a.Tmax);
+    g.osplit = g.nsplit = divup(a.Tmax, g.ochunk);
+    const int ns = g.nsplit;
     const long long heads = (long long)a.B * a.Hq;
     const int spad = score_pad(a.Tmax);
     float* score = work;
     float* po = work + heads * spad;
     float2* ml = reinterpret_cast<float2*>(po + heads * ns * D);
     const int bf16 = a.dtype == DT_BF16;
-    hipLaunchKernelGGL((kv_own_kernel<BITS, D, true>), dim3(ns, a.Hkv * divup(G, 32), a.B), dim3(kThreads), 0, st,
-                       static_cast<const uint16_t*>(a.q), bf16, a.Hq, a.Hkv, a.own, a.lens, a.Tmax, oc, 0, ns, ml, po,
+    const unsigned blocks = (unsigned)((long long)a.B * a.Hkv * divup(G, 16) * g.osplit);
+    hipLaunchKernelGGL((kv_stream_kernel<BITS, D, true>), dim3(blocks), dim3(kThreads), 0, st,
+                       static_cast<const uint16_t*>(a.q), bf16, a.B, a.Hq, a.Hkv, KvCache{}, a.own, a.lens, g, ml, po,
                        score, spad);
     const int spans = divup(a.Tmax, kSpan);
-    hipLaunchKernelGGL((kv_weights_kernel<BITS, D>), dim3((unsigned)(heads + (long long)a.B * a.Hkv * spans)),
+    hipLaunchKernelGGL((kv_weights_kernel<D>), dim3((unsigned)(heads + (long long)a.B * a.Hkv * spans)),
                        dim3(kThreads), 0, st, ml, po, ns, bf16, static_cast<uint16_t*>(a.out), (int)heads, a.Hq, a.Hkv,
                        a.lens, a.Tmax, spans, score, spad, a.weights, a.sums);
     return hipGetLastError();
