@@ -477,6 +477,10 @@ int w4a16_kv_attention_decode_weights(const void* q, int dtype, int64_t B, int64
                                       int bits, const w4a16_kv_cache* own, const int32_t* lengths, int64_t Tmax,
                                       const float* weights, float* sums, float* work, void* out, void* stream);
 
+/* fp32 elements of the w4a16_kv_evict workspace (host only; 0: none, for up to 8192 tokens), or a
+ * negative status. */
+int64_t w4a16_kv_evict_workspace(int64_t B, int64_t Hkv, int64_t Tmax);
+
 /*
  * w4a16_kv_evict -- shrink caches [B, Hkv, Tmax, ...] to at most `budget` tokens per sequence.  Of a
  * sequence of n = lengths[b] tokens (clamped into [0, Tmax]) every kv head keeps all if n <= budget,
@@ -490,12 +494,14 @@ int w4a16_kv_attention_decode_weights(const void* q, int dtype, int64_t B, int64
  *                there starts with none).
  *   lengths_out  int32 [B]: min(n, budget).
  *   kept         int32 [B, Hkv, budget]: the kept tokens' indices, -1 behind them.
- * 0 <= recent <= budget, 1 <= budget <= 2^24; the other limits as above (B * Hkv <= 65535).
+ *   work         w4a16_kv_evict_workspace(B, Hkv, Tmax) fp32 elements, 16-byte aligned (scratch), or
+ *                NULL when that is 0.
+ * 0 <= recent <= budget, 1 <= budget <= 2^24; the other limits as above.
  * No output may overlap an input (W4A16_ERR_OVERLAP): shrink into a second cache.
  */
 int w4a16_kv_evict(const w4a16_kv_cache* in, const float* weights, const int32_t* lengths, int64_t B, int64_t Hkv,
                    int64_t Tmax, int64_t D, int bits, int64_t budget, int64_t recent, const w4a16_kv_cache_out* out,
-                   int64_t Tout, float* weights_out, int32_t* lengths_out, int32_t* kept, void* stream);
+                   int64_t Tout, float* weights_out, int32_t* lengths_out, int32_t* kept, float* work, void* stream);
 
 /*
  * w4a16_linear_workspace -- bytes of fp32 workspace that w4a16_linear_ws can use for this

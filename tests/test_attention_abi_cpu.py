@@ -106,14 +106,14 @@ def test_weights_refusals(lib):
 
 def evict(lib, **kw):
     a = dict(bits=8, w=B, lens=C, B=2, Hkv=4, Tmax=100, D=64, budget=50, recent=10, Tout=60, wo=D, lo=D + 0x10000,
-             kept=D + 0x20000)
+             kept=D + 0x20000, work=None)
     a.update(kw)
     shift = E - A
     src = a["src"] if "src" in a else cache(a["bits"])
     dst = a["dst"] if "dst" in a else L.KvCache(*(None if p is None else p + shift for p in (
         getattr(cache(a["bits"]), f) for f, _ in L.KvCache._fields_)))
     return lib.w4a16_kv_evict(src, a["w"], a["lens"], a["B"], a["Hkv"], a["Tmax"], a["D"], a["bits"], a["budget"],
-                              a["recent"], dst, a["Tout"], a["wo"], a["lo"], a["kept"], None)
+                              a["recent"], dst, a["Tout"], a["wo"], a["lo"], a["kept"], a["work"], None)
 
 
 @pytest.mark.parametrize("kw,status", [
@@ -123,6 +123,7 @@ def evict(lib, **kw):
     (dict(recent=51), L.ERR_SHAPE), (dict(Tout=49), L.ERR_SHAPE), (dict(Tout=(1 << 24) + 1), L.ERR_SHAPE),
     (dict(Tmax=0), L.ERR_SHAPE), (dict(w=B + 2), L.ERR_ALIGN), (dict(wo=D + 1), L.ERR_ALIGN), (dict(lens=C + 1), L.ERR_ALIGN),
     (dict(lo=D + 0x10002), L.ERR_ALIGN), (dict(kept=D + 0x20001), L.ERR_ALIGN),
+    (dict(Tmax=8193), L.ERR_NULL), (dict(Tmax=8193, work=D + 0x30008), L.ERR_ALIGN),
     (dict(dst="src"), L.ERR_OVERLAP), (dict(wo=B + 4), L.ERR_OVERLAP), (dict(lo=C), L.ERR_OVERLAP),
     (dict(lo=D), L.ERR_OVERLAP), (dict(kept=A), L.ERR_OVERLAP)])
 def test_evict_refusals(lib, kw, status):
@@ -147,6 +148,9 @@ def test_workspaces(lib):
     assert need(2, 8, 4, 9, 64) >= 2 * 8 * (9 + 64 + 2)
     assert need(2, 8, 3, 9, 64) == L.ERR_SHAPE and need(0, 8, 4, 9, 64) == L.ERR_SHAPE
     assert need(65535, 256, 4, 1 << 13, 64) == L.ERR_SHAPE
+    need = lib.w4a16_kv_evict_workspace
+    assert need(4, 8, 8192) == 0 and need(4, 8, 8193) > 4 * 8 * 2 * 5120 and need(1, 1, 1 << 24) > 64 * 5120
+    assert need(0, 8, 8193) == L.ERR_SHAPE and need(1, 1, (1 << 24) + 1) == L.ERR_SHAPE
 
 
 def test_overlap_status_has_a_text(lib):

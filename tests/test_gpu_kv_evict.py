@@ -89,7 +89,9 @@ CASES = [(1, 1, 1, [1], 1, 0, 64, 8), (1, 1, 2, [2], 1, 0, 64, 4), (1, 1, 2, [2]
          (3, 2, 65, [65, 64, 0], 64, 10, 64, 8), (2, 3, 130, [129, 3], 128, 128, 128, 4),
          (4, 1, 1000, [1000, 999, 500, -4], 500, 0, 128, 8), (2, 2, 1025, [1025, 5000], 17, 5, 64, 4),
          (1, 2, 5001, [5001], 2048, 100, 128, 4), (2, 1, 300, [300, 40], 400, 50, 64, 8),
-         (1, 1, 20011, [20011], 20010, 1, 64, 8)]
+         (1, 1, 20011, [20011], 20010, 1, 64, 8), (1, 2, 8192, [8192], 4000, 8, 64, 4), (2, 1, 8193, [8193, 100], 5000, 4500, 64, 8),
+         (3, 2, 30000, [30000, 9000, 0], 9000, 20, 64, 8), (2, 1, 25000, [25000, 16385], 16384, 16384, 64, 4),
+         (1, 1, 600001, [600001], 70000, 66000, 64, 4), (2, 1, 40000, [40000, 39999], 12000, 11990, 64, 8)]
 
 
 @pytest.mark.parametrize("B,Hkv,T,lens,budget,recent,D,bits", CASES)

@@ -683,6 +683,14 @@ def kv_attention_weights_workspace(B: int, Hq: int, Hkv: int, Tmax: int, D: int)
     return int(need)
 
 
+def kv_evict_workspace(B: int, Hkv: int, Tmax: int) -> int:
+    """fp32 elements of the scratch buffer that :func:`kv_evict` needs (0: none)."""
+    need = lib().w4a16_kv_evict_workspace(B, Hkv, Tmax)
+    if need < 0:
+        raise W4A16Error(int(need), "w4a16_kv_evict_workspace")
+    return int(need)
+
+
 def kv_attention_decode_shared(q: torch.Tensor, kprefix, vprefix, P: int, kcache, vcache, lengths: torch.Tensor,
                                bits: int = 8, out: torch.Tensor | None = None,
                                work: torch.Tensor | None = None) -> torch.Tensor:
@@ -750,7 +758,7 @@ def kv_attention_decode_weights(q: torch.Tensor, kcache, vcache, lengths: torch.
 
 
 def kv_evict(kcache, vcache, weights: torch.Tensor, lengths: torch.Tensor, budget: int, recent: int, bits: int = 8,
-             capacity: int | None = None, out=None):
+             capacity: int | None = None, out=None, work: torch.Tensor | None = None):
     """Shrink caches ``[B, Hkv, Tmax, ...]`` to at most ``budget`` tokens per sequence: every kv head
     keeps its last ``recent`` tokens and, of the earlier ones, those with the largest ``weights``
     (fp32 ``[B, Hkv, Tmax]``, see :func:`kv_attention_decode_weights`; the earlier token among
@@ -761,7 +769,8 @@ def kv_evict(kcache, vcache, weights: torch.Tensor, lengths: torch.Tensor, budge
     tokens, ``lengths = min(lengths, budget)`` and the kept tokens' old indices, int32
     ``[B, Hkv, budget]``, -1 behind them.  ``out`` takes such a tuple to write into (its shapes then
     give the capacity); cache rows behind the kept tokens are not written, in a call without
-    ``out`` they are undefined."""
+    ``out`` they are undefined.  ``work`` is an optional fp32 buffer of at least
+    :func:`kv_evict_workspace` elements (0 for up to 8192 tokens)."""
     _need(weights, "weights", torch.float32, 3)
     _need(lengths, "lengths", torch.int32, 1)
     if bits not in (8, 4):
@@ -798,7 +807,11 @@ def kv_evict(kcache, vcache, weights: torch.Tensor, lengths: torch.Tensor, budge
     if Tout < min(budget, Tmax):
         raise ValueError("out must have room for min(budget, Tmax) tokens")
     _same_device(weights, "weights", **{"out weights": wo, "out lengths": lo, "out kept": kept})
-    _call(lib().w4a16_kv_evict, "w4a16_kv_evict", weights.device, _cache_struct(kcache, vcache, bits),
+    L = lib()
+    need = L.w4a16_kv_evict_workspace(B, Hkv, Tmax)
+    if need or work is not None:
+        work = _work(work, need, "w4a16_kv_evict_workspace", weights)
+    _call(L.w4a16_kv_evict, "w4a16_kv_evict", weights.device, _cache_struct(kcache, vcache, bits),
           weights.data_ptr(), lengths.data_ptr(), B, Hkv, Tmax, D, bits, budget, recent, _cache_struct(ko, vo, bits),
-          Tout, wo.data_ptr(), lo.data_ptr(), kept.data_ptr())
+          Tout, wo.data_ptr(), lo.data_ptr(), kept.data_ptr(), None if work is None else work.data_ptr())
     return (ko, vo, wo, lo, kept)

@@ -131,7 +131,9 @@ def lib() -> ctypes.CDLL:
     L.w4a16_kv_attention_decode_weights.argtypes = [vp, i32, i64, i64, i64, i64, i32, cache, vp, i64, vp, vp, vp, vp,
                                                     vp]
     L.w4a16_kv_evict.restype = i32
-    L.w4a16_kv_evict.argtypes = [cache, vp, vp, i64, i64, i64, i64, i32, i64, i64, cache, i64, vp, vp, vp, vp]
+    L.w4a16_kv_evict.argtypes = [cache, vp, vp, i64, i64, i64, i64, i32, i64, i64, cache, i64, vp, vp, vp, vp, vp]
+    L.w4a16_kv_evict_workspace.restype = i64
+    L.w4a16_kv_evict_workspace.argtypes = [i64, i64, i64]
     L.w4a16_gptq_quantize.restype = i32
     L.w4a16_gptq_quantize.argtypes = [vp, i64, i64, i64, i32, vp, vp, vp, vp, vp, vp]
     _lib = L

@@ -533,9 +533,14 @@ int w4a16_kv_attention_decode_weights(const void* q, int dtype, int64_t B, int64
     return hip_status(w4a16::launch_kv_weights(a, work, static_cast<hipStream_t>(stream)));
 }
 
+int64_t w4a16_kv_evict_workspace(int64_t B, int64_t Hkv, int64_t Tmax) {
+    const int st = check_kv_batch(B, Hkv, Hkv, 0, 0, Tmax, 64);
+    return st != W4A16_OK ? st : w4a16::kv_evict_workspace_words(B, Hkv, Tmax);
+}
+
 int w4a16_kv_evict(const w4a16_kv_cache* in, const float* weights, const int32_t* lengths, int64_t B, int64_t Hkv,
                    int64_t Tmax, int64_t D, int bits, int64_t budget, int64_t recent, const w4a16_kv_cache_out* out,
-                   int64_t Tout, float* weights_out, int32_t* lengths_out, int32_t* kept, void* stream) {
+                   int64_t Tout, float* weights_out, int32_t* lengths_out, int32_t* kept, float* work, void* stream) {
     if (!in || !weights || !lengths || !out || !weights_out || !lengths_out || !kept) return W4A16_ERR_NULL;
     if (bits != 8 && bits != 4) return W4A16_ERR_SCHEME;
     int st = check_kv_batch(B, Hkv, Hkv, 0, 0, Tmax, D);
@@ -545,6 +550,9 @@ int w4a16_kv_evict(const w4a16_kv_cache* in, const float* weights, const int32_t
     if (st == W4A16_OK) st = check_cache(in, bits);
     if (st == W4A16_OK) st = check_cache(out, bits);
     if (st != W4A16_OK) return st;
+    const int64_t words = w4a16::kv_evict_workspace_words(B, Hkv, Tmax);
+    if (words > 0 && !work) return W4A16_ERR_NULL;
+    if (words > 0 && !aligned(work, 16)) return W4A16_ERR_ALIGN;
     if (!aligned(weights, 4) || !aligned(lengths, 4) || !aligned(weights_out, 4) || !aligned(lengths_out, 4) ||
         !aligned(kept, 4))
         return W4A16_ERR_ALIGN;
@@ -584,7 +592,7 @@ int w4a16_kv_evict(const w4a16_kv_cache* in, const float* weights, const int32_t
     a.Tout = (int)Tout;
     a.budget = (int)budget;
     a.recent = (int)recent;
-    return hip_status(w4a16::launch_kv_evict(a, static_cast<hipStream_t>(stream)));
+    return hip_status(w4a16::launch_kv_evict(a, reinterpret_cast<uint32_t*>(work), static_cast<hipStream_t>(stream)));
 }
 
 int w4a16_select_path(int64_t M, int64_t N, int64_t K, int64_t group_size, int dtype) {

@@ -16,8 +16,9 @@
 // along the tokens (WK = 4, few rows: each wave then has its own softmax state and the four are
 // joined at the end).  A token's scales stay out of the 16-bit operands: K's multiplies the fp32
 // score, V's the softmax weight before it is rounded to fp16.  bf16 queries are scaled by a power
-// of two per row so that their largest entry is in [2^14, 2^15) and become fp16 exactly (8-bit
-// significands; an entry below 2^-28 of the row's largest may lose bits, 2^-39 of that entry).
+// of two per row (streaming: per 16 rows) so that their largest entry is in [2^14, 2^15) and become
+// fp16 exactly (8-bit significands; an entry below 2^-21 of the largest may lose bits, 2^-39 of that
+// largest one).
 // Rounded to 16 bits are only the weights p s_t (fp16, relative 2^-11, scaled so that the largest
 // s_t seen so far becomes 2^7 and small ones keep their bits) and the output.  Scores, maxima,
 // sums and outputs are fp32; splits are joined by a second launch.
@@ -417,8 +418,9 @@ __device__ __forceinline__ void wave_lds_fence() {
 // Attend).  Nothing here is bound by arithmetic, so the aim is loads in flight and few
 // instructions: each wave of the block streams tiles of its own (wave, wave + 4, ...), with no
 // barrier until the four are joined at the end.
-//   K's codes go from memory to the matrix cores: lane l loads the quarter l / 16 of key l % 16's
-//     row, consecutive bytes, and the query's fragment is loaded in the same order.
+//   K's codes go from memory to the matrix cores: lane l loads the quarter l / 16 of every 64 bytes
+//     (32 for the shortest rows) of key l % 16's row, so a load covers whole cache lines, and the
+//     query's fragment is loaded in the same order.
 //   V's codes are stored to LDS as they are and read back transposed (8- or 4-bit).
 //   A code u (int8: c + 128) becomes the fp16 subnormal u 2^-24 by masks or byte permutes alone; the
 //     matrix cores multiply subnormals exactly.  The zero point (int8: 128) is taken out of the fp32
@@ -435,6 +437,8 @@ struct Stream {
     static constexpr int NS = KT / 16;                           // S tiles
     static constexpr int RB = BITS == 8 ? D : D / 2;             // bytes of a cached row
     static constexpr int KW = RB / 16;                           // K: dwords per lane and S tile
+    static constexpr int KB = RB / 4 < 16 ? RB / 4 : 16;         // K: bytes per load
+    static constexpr int KQ = KB * 8 / BITS;                     // codes per load
     static constexpr int VL = KT * RB / 1024 > 0 ? KT * RB / 1024 : 1;   // V: 16-byte loads per lane
     static constexpr int VP = RB / 16;                           // 16-byte pieces of a row
     static constexpr int QS = D / 32;                            // k-steps of the first product
@@ -480,7 +484,7 @@ struct Stream {
             // tokens behind the span: its last one, masked out of the scores
 #pragma unroll
             for (int s = 0; s < NS; ++s) {
-                const uint32_t off = (uint32_t)min(base + 16 * s + n, t1 - 1) * RB + RB / 4 * qd;
+                const uint32_t off = (uint32_t)min(base + 16 * s + n, t1 - 1) * RB + KB * qd;
                 if constexpr (KW == 2) {
                     const u32x2 x = *reinterpret_cast<const u32x2*>(c.kc + off);
                     kr[s / 2][2 * (s % 2)] = x.x;
@@ -488,7 +492,7 @@ struct Stream {
                 } else {
 #pragma unroll
                     for (int i = 0; i < KW / 4; ++i)
-                        kr[s * (KW / 4) + i] = *reinterpret_cast<const u32x4*>(c.kc + off + 16 * i);
+                        kr[s * (KW / 4) + i] = *reinterpret_cast<const u32x4*>(c.kc + off + 64 * i);
                 }
             }
 #pragma unroll
@@ -516,9 +520,10 @@ struct Stream {
         u32x4 qf[QS];
         float cl, qsum = 0.0f;                             // score scale; -2^-24 sum of the fp16 query
         {
-            const uint16_t* qp = q + head * D + qd * (D / 4);
+            const uint16_t* qp = q + head * D + KQ * qd;
 #pragma unroll
-            for (int s = 0; s < QS; ++s) qf[s] = *reinterpret_cast<const u32x4*>(qp + 8 * s);
+            for (int s = 0; s < QS; ++s)
+                qf[s] = *reinterpret_cast<const u32x4*>(qp + 8 * s % KQ + 4 * KQ * (8 * s / KQ));
             cl = 1.4426950408889634f * 16777216.0f / sqrtf((float)D);
             if (bf16) {
                 float mx = 0.0f;
@@ -527,7 +532,7 @@ struct Stream {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         mx = fmaxf(mx, fmaxf(fabsf(bf2f(qf[s][i] & 0xFFFFu)), fabsf(bf2f(qf[s][i] >> 16))));
-                mx = across_quarters(mx, [](float a, float b) { return fmaxf(a, b); });
+                mx = wave_max(mx);                         // one factor for all rows: it goes into K's scales
                 const int e = mx > 0.0f ? 15 - __builtin_amdgcn_frexp_expf(mx) : 0;
                 cl = ldexpf(cl, -e);
 #pragma unroll
@@ -579,10 +584,10 @@ struct Stream {
             }
             const float vinv = VNORM / vcap;
             if constexpr (KT == 64) {
-                L.ks[lane] = h2f(pk);
+                L.ks[lane] = h2f(pk) * cl;
                 L.vs[lane] = BITS == 4 && (lane & 2) ? vsc * (vinv * 0.0625f) : vsc * vinv;
             } else {
-                (lane < 32 ? L.ks : L.vs)[lane & 31] = lane < 32 ? h2f(pk) : vsc * vinv;
+                (lane < 32 ? L.ks : L.vs)[lane & 31] = lane < 32 ? h2f(pk) * cl : vsc * vinv;
             }
             if constexpr (BITS == 4) {
                 L.kz[lane] = h2f(pkz);
@@ -623,7 +628,7 @@ struct Stream {
             const int tok0 = t0 + t * KT;
             float mt = NEG;
 #pragma unroll
-            for (int s = 0; s < NS; ++s) S[s] = S[s] * (*reinterpret_cast<const f32x4*>(&L.ks[16 * s + 4 * qd]) * cl);
+            for (int s = 0; s < NS; ++s) S[s] = S[s] * *reinterpret_cast<const f32x4*>(&L.ks[16 * s + 4 * qd]);
             if (tok0 + KT > t1) {
 #pragma unroll
                 for (int s = 0; s < NS; ++s)
@@ -791,8 +796,11 @@ __global__ __launch_bounds__(kThreads, 2) void kv_prefix_kernel(const uint16_t* 
 }
 
 // Streaming: the first `pblocks` blocks take the shared prefix where it has few rows (block = kv head,
-// tile of 16 of its B G rows, split), the others the sequences' own caches (block = sequence, kv
-// head, tile of 16 of its G heads, split; splits vary fastest).
+// tile of 16 of its B G rows, split), the others the sequences' own caches (block = split, sequence, kv
+// head, tile of 16 of its G heads).  Splits vary slowest and each turns the rest by one: consecutive
+// blocks run on the 8 XCDs in turn, and the late splits of short sequences, which are empty, have to
+// fall on all of them (with the splits fastest, 16 sequences of 1024 .. 4096 tokens and 4 splits
+// took 70 us instead of 53, two XCDs having no empty split at all).
 struct StreamGrid {
     int pblocks, psplit, pchunk, P, Pmax;    // prefix splits come first among a row's nsplit
     int osplit, ochunk, Tmax, nsplit;
@@ -826,8 +834,9 @@ __global__ __launch_bounds__(kThreads, 3) void kv_stream_kernel(const uint16_t* 
         id -= g.pblocks;
         R = G;
         const int htiles = (G + 15) / 16;
-        split = id % g.osplit;
-        id /= g.osplit;
+        const int pairs = B * Hkv * htiles;
+        split = id / pairs;
+        id = (id % pairs + split) % pairs;
         row0 = 16 * (id % htiles);
         id /= htiles;
         const int kvh = id % Hkv, b = id / Hkv;

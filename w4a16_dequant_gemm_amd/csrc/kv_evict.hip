@@ -2,11 +2,15 @@
 // its most recent tokens and, of the older ones, those with the largest accumulated weight
 // (kv_attend.hip adds it up), in their order, in a cache of their own.
 //
-// Two launches.  Select (one block per sequence and kv head): the budget-th largest weight by radix
-// selection on order-preserving integer keys, eight bits a pass, then one ordered pass that writes
-// the kept tokens' indices and weights; ties go to the earlier token.  Gather: the kept rows' codes
-// and parameters, 16 bytes per thread.  Nothing is dequantized, so the kept rows are the same bits.
-// Both are bound by memory: the weights once, the kept rows in and out once.
+// Select finds the budget-th largest weight by radix selection on order-preserving integer keys,
+// digits of 11, 11 and 10 bits, and writes the kept tokens' indices and weights in order; ties go to
+// the earlier token.  Up to kBatch tokens are one block per (sequence, kv head), the weights in
+// registers from the first digit to the end.  Longer ones are cut into chunks, one block each, and
+// take four launches: one per digit, in which a block adds up the chunks' histograms of the previous
+// digit for itself, and the ordered write, where the same histograms tell how much the chunks before
+// this one keep.  (One block walking 100001 weights of each of 8 heads took 142 us.)
+// Gather copies the kept rows' codes and parameters, 16 bytes per thread; nothing is dequantized, so
+// the kept rows are the same bits.  All of it is bound by memory: the weights, the kept rows in and out.
 #include "common.h"
 #include "launch.h"
 
@@ -16,7 +20,12 @@ namespace {
 
 constexpr int kSelThreads = 1024;
 constexpr int kSelWaves = kSelThreads / 64;
-constexpr int kCopies = 32;       // histogram copies: lanes of a wave that share a bin do not collide
+constexpr int kPer = 8;                          // tokens of a thread and batch
+constexpr int kBatch = kSelThreads * kPer;
+constexpr int kChunks = 64;                      // chunks of a sequence, at most
+constexpr int kBins = 2048;
+constexpr int kCopies = 4;                       // of the histogram: lanes that share a digit collide less
+constexpr int kShift[3] = {21, 10, 0};
 
 // Order of floats as unsigned integers; -0 = +0, NaN above everything.
 __device__ __forceinline__ uint32_t order_key(float w) {
@@ -29,123 +38,257 @@ __device__ __forceinline__ int lanes_below(unsigned long long mask) {
     return __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
 }
 
+struct SelectLds {
+    uint32_t hist[kBins * kCopies];
+    int sum[kSelWaves], before[kSelWaves];
+    int digit, rem;
+    int gt[kSelWaves], eq[kSelWaves];
+};
+
+// What is known of the threshold key: its leading digits, and how many of the tokens that agree with
+// them are kept (the largest).
+struct Threshold {
+    uint32_t prefix, mask;
+    int rem;
+};
+
+// A batch's weights: token base + 512 wave + 64 j + lane in x[j]; a wave's tokens are consecutive.
+__device__ __forceinline__ int token(int base, int j) {
+    return base + (int)(threadIdx.x >> 6) * 64 * kPer + 64 * j + (int)(threadIdx.x & 63);
+}
+__device__ __forceinline__ void load_batch(const float* __restrict__ w, int base, int n, float x[kPer]) {
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        const int t = token(base, j);
+        x[j] = t < n ? w[t] : 0.0f;
+    }
+}
+
+__device__ __forceinline__ void clear_hist(SelectLds& s) {
+    for (int i = threadIdx.x; i < kBins * kCopies; i += kSelThreads) s.hist[i] = 0;
+}
+__device__ __forceinline__ void count_batch(SelectLds& s, const float x[kPer], int base, int old, const Threshold& th,
+                                            int level) {
+    const uint32_t bins = level == 2 ? 1023u : 2047u;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        const uint32_t k = order_key(x[j]);
+        if (token(base, j) < old && (k & th.mask) == th.prefix)
+            atomicAdd(&s.hist[((k >> kShift[level]) & bins) * kCopies + (threadIdx.x & (kCopies - 1))], 1u);
+    }
+}
+// This thread's two digits, 2047 - 2 tid and 2046 - 2 tid.
+__device__ __forceinline__ int count_of(const SelectLds& s, int which) {
+    const uint32_t* h = s.hist + (kBins - 1 - 2 * (int)threadIdx.x - which) * kCopies;
+    return (int)(h[0] + h[1] + h[2] + h[3]);
+}
+
+// The next digit of the threshold from the counts c0, c1 of this thread's two digits: the highest with
+// th.rem or more tokens at or above it.  p0, p1: the same counts in the chunks before this one; adds
+// how many of those are above the digit to `above` and returns how many are at it.
+__device__ __forceinline__ int next_digit(SelectLds& s, int c0, int c1, int p0, int p1, int level, Threshold& th,
+                                          int& above) {
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+    int inc = c0 + c1;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+        const int o = __shfl_up(inc, off, 64);
+        if (lane >= off) inc += o;
+    }
+    if (lane == 63) s.sum[wave] = inc;
+    __syncthreads();
+    for (int i = 0; i < wave; ++i) inc += s.sum[i];
+    const int higher = inc - c0 - c1;                // tokens at this thread's higher digits' tail
+    if (higher < th.rem && inc >= th.rem) {
+        const bool first = higher + c0 >= th.rem;
+        s.digit = kBins - 1 - 2 * tid - (first ? 0 : 1);
+        s.rem = th.rem - higher - (first ? 0 : c0);
+    }
+    __syncthreads();
+    const int d = s.digit, mine = kBins - 1 - 2 * tid;
+    int gt = (mine > d ? p0 : 0) + (mine - 1 > d ? p1 : 0);
+    const int eq = mine == d ? p0 : mine - 1 == d ? p1 : 0;
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) gt += __shfl_xor(gt, off, 64);
+    if (lane == 0) s.before[wave] = gt;
+    if (mine == d || mine - 1 == d) s.sum[0] = eq;   // (everyone is past reading the sums)
+    th.rem = s.rem;
+    th.prefix |= (uint32_t)d << kShift[level];
+    th.mask |= (level == 2 ? 1023u : 2047u) << kShift[level];
+    __syncthreads();
+    for (int i = 0; i < kSelWaves; ++i) above += s.before[i];
+    const int at = s.sum[0];
+    __syncthreads();
+    return at;
+}
+
+// Writes the kept tokens of one batch in order, from position `pos` on with `ties` tokens at the
+// threshold seen before; both move on.  kt.prefix is the whole key (nothing is above it and no tie
+// is taken when no old token is kept).
+__device__ __forceinline__ void write_batch(SelectLds& s, const float x[kPer], int base, int old, int n,
+                                            const Threshold& kt, int& pos, int& ties, int* __restrict__ ko,
+                                            float* __restrict__ wo) {
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    unsigned long long gtm[kPer], eqm[kPer];
+    int gt = 0, eq = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        const int t = token(base, j);
+        const uint32_t k = order_key(x[j]);
+        const unsigned long long lm = __builtin_amdgcn_ballot_w64(t >= old && t < n);
+        gtm[j] = __builtin_amdgcn_ballot_w64(t < old && k > kt.prefix) | lm;
+        eqm[j] = __builtin_amdgcn_ballot_w64(t < old && k == kt.prefix);
+        gt += __builtin_popcountll(gtm[j]);
+        eq += __builtin_popcountll(eqm[j]);
+    }
+    if (lane == 0) {
+        s.gt[wave] = gt;
+        s.eq[wave] = eq;
+    }
+    __syncthreads();
+    int p = pos, q = ties;                           // of this wave
+    for (int i = 0; i < kSelWaves; ++i) {
+        const int e = s.eq[i], g = s.gt[i] + min(max(kt.rem - ties, 0), e);
+        if (i < wave) {
+            p += g;
+            q += e;
+        }
+        pos += g;
+        ties += e;
+    }
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        const bool keep = (gtm[j] >> lane & 1) || ((eqm[j] >> lane & 1) && q + lanes_below(eqm[j]) < kt.rem);
+        const unsigned long long km = __builtin_amdgcn_ballot_w64(keep);
+        if (keep) {
+            const int at = p + lanes_below(km);
+            ko[at] = token(base, j);
+            wo[at] = x[j];
+        }
+        p += __builtin_popcountll(km);
+        q += __builtin_popcountll(eqm[j]);
+    }
+    __syncthreads();                                 // before the next batch's counts
+}
+
+// Behind the kept tokens: index -1, weight 0 (threads first, first + step, ... of the sequence).
+__device__ __forceinline__ void fill_rest(int count, int budget, int Tout, int first, int step, int* ko, float* wo) {
+    for (int i = count + first; i < budget; i += step) ko[i] = -1;
+    for (int i = count + first; i < Tout; i += step) wo[i] = 0.0f;
+}
+
+// One block per (sequence, kv head) of up to kBatch tokens.
 __global__ __launch_bounds__(kSelThreads) void kv_select_kernel(const float* __restrict__ weights,
                                                                 const int* __restrict__ lens, int Hkv, int Tmax,
                                                                 int budget, int recent, int Tout,
                                                                 float* __restrict__ weights_out,
                                                                 int* __restrict__ lens_out, int* __restrict__ kept) {
-    __shared__ uint32_t hist[256][kCopies];
-    __shared__ uint32_t total[256];
-    __shared__ uint32_t s_prefix, s_need;
-    __shared__ int s_gt[kSelWaves], s_eq[kSelWaves];
-    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+    __shared__ SelectLds s;
     const long long bh = blockIdx.x;
     const int b = blockIdx.x / Hkv;
-    const int n = min(max(lens[b], 0), Tmax);
-    const int count = min(n, budget);
+    const int n = min(max(lens[b], 0), Tmax), count = min(n, budget);
     const float* w = weights + bh * Tmax;
     float* wo = weights_out + bh * Tout;
     int* ko = kept + bh * budget;
-    if (tid == 0 && blockIdx.x % Hkv == 0) lens_out[b] = count;
-    for (int i = count + tid; i < budget; i += kSelThreads) ko[i] = -1;
-    for (int i = count + tid; i < Tout; i += kSelThreads) wo[i] = 0.0f;
-    if (n <= budget) {
-        for (int i = tid; i < n; i += kSelThreads) {
-            ko[i] = i;
-            wo[i] = w[i];
-        }
-        return;
-    }
-    // of the `old` earlier tokens keep the `need` largest (0 <= need < old)
-    const int old = n - recent, need = budget - recent;
-    uint32_t prefix = 0, mask = 0;
-    int rem = need;
-    if (need > 0) {
-        for (int shift = 24; shift >= 0; shift -= 8) {
-            for (int i = tid; i < 256 * kCopies; i += kSelThreads) hist[0][i] = 0;
+    float x[kPer];
+    load_batch(w, 0, n, x);
+    if (threadIdx.x == 0 && blockIdx.x % Hkv == 0) lens_out[b] = count;
+    fill_rest(count, budget, Tout, threadIdx.x, kSelThreads, ko, wo);
+    // n <= budget: every token is "recent"
+    const int old = n <= budget ? 0 : n - recent;
+    Threshold th = {0, 0, n <= budget ? 0 : budget - recent};
+    if (th.rem > 0) {
+        int above = 0;
+        for (int level = 0; level < 3; ++level) {
+            clear_hist(s);
             __syncthreads();
-            for (int t = tid; t < old; t += kSelThreads) {
-                const uint32_t k = order_key(w[t]);
-                if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & 255][lane % kCopies], 1u);
-            }
+            count_batch(s, x, 0, old, th, level);
             __syncthreads();
-            if (tid < 256) {
-                uint32_t s = 0;
-                for (int c = 0; c < kCopies; ++c) s += hist[tid][(c + tid) % kCopies];
-                total[tid] = s;
-            }
-            __syncthreads();
-            // the highest digit with `rem` or more keys at or above it: lane l of wave 0 adds up the
-            // digits 4 l .. 4 l + 3, a suffix sum over the lanes finds the lane
-            if (wave == 0) {
-                const int c0 = total[4 * lane], c1 = total[4 * lane + 1], c2 = total[4 * lane + 2],
-                          c3 = total[4 * lane + 3];
-                int suf = c0 + c1 + c2 + c3;
-                const int mine = suf;
-#pragma unroll
-                for (int off = 1; off < 64; off <<= 1) {
-                    const int o = __shfl_down(suf, off, 64);
-                    suf += lane + off < 64 ? o : 0;
-                }
-                int above = suf - mine;
-                if (above < rem && suf >= rem) {
-                    int d = 3;
-                    if (above + c3 < rem) { above += c3; d = 2; }
-                    if (d == 2 && above + c2 < rem) { above += c2; d = 1; }
-                    if (d == 1 && above + c1 < rem) { above += c1; d = 0; }
-                    s_prefix = prefix | ((uint32_t)(4 * lane + d) << shift);
-                    s_need = rem - above;
-                }
-            }
-            __syncthreads();
-            prefix = s_prefix;
-            rem = s_need;
-            mask |= 255u << shift;
+            next_digit(s, count_of(s, 0), count_of(s, 1), 0, 0, level, th, above);
         }
     } else {
-        prefix = 0xFFFFFFFFu;            // nothing old is kept: no key is above, and no tie is taken
+        th.prefix = 0xFFFFFFFFu;
     }
-    // wave w owns the tokens [lo, hi); how many of them are above the threshold, and at it
-    const int per = ((n + kSelWaves - 1) / kSelWaves + 63) / 64 * 64;
-    const int lo = min(wave * per, n), hi = min(lo + per, n);
-    int gt = 0, eq = 0;
-    for (int t = lo + lane; t < min(hi, old); t += 64) {
-        const uint32_t k = order_key(w[t]);
-        gt += k > prefix;
-        eq += k == prefix;
-    }
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) {
-        gt += __shfl_xor(gt, off, 64);
-        eq += __shfl_xor(eq, off, 64);
-    }
-    if (lane == 0) {
-        s_gt[wave] = gt;
-        s_eq[wave] = eq;
-    }
-    __syncthreads();
-    int ties = 0, pos = 0;               // ties seen and tokens kept before this wave's
-    for (int i = 0; i < wave; ++i) {
-        const int take = min(max(rem - ties, 0), s_eq[i]);
-        const int ihi = min(min(i * per, n) + per, n);
-        pos += s_gt[i] + take + max(0, ihi - max(min(i * per, n), old));
-        ties += s_eq[i];
-    }
-    for (int t0 = lo; t0 < hi; t0 += 64) {
-        const int t = t0 + lane;
-        const float x = t < hi ? w[t] : 0.0f;
-        const uint32_t k = order_key(x);
-        const bool is_eq = t < hi && t < old && k == prefix;
-        const unsigned long long eqm = __builtin_amdgcn_ballot_w64(is_eq);
-        const bool keep = t < hi && (t >= old || k > prefix || (is_eq && ties + lanes_below(eqm) < rem));
-        const unsigned long long km = __builtin_amdgcn_ballot_w64(keep);
-        if (keep) {
-            const int p = pos + lanes_below(km);
-            ko[p] = t;
-            wo[p] = x;
+    int pos = 0, ties = 0;
+    write_batch(s, x, 0, old, n, th, pos, ties, ko, wo);
+}
+
+// Longer sequences, one launch per digit (LEVEL 0 .. 2) and the ordered write (LEVEL 3).  Workspace of a
+// (sequence, kv head): per chunk its three histograms and its state after the previous launch (the
+// threshold so far, and how many tokens above it the chunks before this one hold).
+struct ChunkState {
+    uint32_t prefix, mask;
+    int rem, above;
+};
+constexpr int kChunkWords = 3 * kBins + 4;
+template <int LEVEL>
+__global__ __launch_bounds__(kSelThreads) void kv_select_chunk_kernel(
+    const float* __restrict__ weights, const int* __restrict__ lens, int Hkv, int Tmax, int budget, int recent,
+    int Tout, int chunks, int chunk, uint32_t* __restrict__ work, float* __restrict__ weights_out,
+    int* __restrict__ lens_out, int* __restrict__ kept) {
+    __shared__ SelectLds s;
+    const int tid = threadIdx.x;
+    const long long bh = blockIdx.x / chunks;
+    const int me = blockIdx.x % chunks, b = (int)(bh / Hkv);
+    const int n = min(max(lens[b], 0), Tmax), count = min(n, budget);
+    const float* w = weights + bh * Tmax;
+    const int old = n <= budget ? 0 : n - recent;
+    const int need = n <= budget ? 0 : budget - recent;
+    const int lo = me * chunk, hi = min(n, lo + chunk);
+    uint32_t* all = work + bh * chunks * kChunkWords;
+    uint32_t* own = all + me * kChunkWords;
+    ChunkState* state = reinterpret_cast<ChunkState*>(own + 3 * kBins);
+    const int live = (old + chunk - 1) / chunk;      // chunks with old tokens: the ones with histograms
+    if (LEVEL < 3 && (need == 0 || me >= live)) return;
+    Threshold th = {0, 0, need};
+    int above = 0, at = 0;
+    if constexpr (LEVEL > 0) {
+        if (need > 0) {
+            if (LEVEL > 1 && me < live) {
+                th = {state->prefix, state->mask, state->rem};
+                above = state->above;
+            } else if (LEVEL > 1) {                  // (LEVEL 3, a chunk of recent tokens only)
+                const ChunkState* last = reinterpret_cast<const ChunkState*>(all + (live - 1) * kChunkWords + 3 * kBins);
+                th = {last->prefix, last->mask, last->rem};
+            }
+            int c0 = 0, c1 = 0, p0 = 0, p1 = 0;
+            for (int c = 0; c < live; ++c) {
+                const uint2 v = *reinterpret_cast<const uint2*>(all + c * kChunkWords + (LEVEL - 1) * kBins + 2 * tid);
+                c0 += (int)v.x;
+                c1 += (int)v.y;
+                p0 += c < me ? (int)v.x : 0;
+                p1 += c < me ? (int)v.y : 0;
+            }
+            at = next_digit(s, c0, c1, p0, p1, LEVEL - 1, th, above);
+            if (LEVEL < 3 && tid == 0) *state = {th.prefix, th.mask, th.rem, above};
+        } else {
+            th.prefix = 0xFFFFFFFFu;
         }
-        ties += __builtin_popcountll(eqm);
-        pos += __builtin_popcountll(km);
+    }
+    float x[kPer];
+    if constexpr (LEVEL < 3) {
+        clear_hist(s);
+        __syncthreads();
+        for (int base = lo; base < min(hi, old); base += kBatch) {
+            load_batch(w, base, min(hi, old), x);
+            count_batch(s, x, base, min(hi, old), th, LEVEL);
+        }
+        __syncthreads();
+        *reinterpret_cast<uint2*>(own + LEVEL * kBins + 2 * tid) =
+            make_uint2((uint32_t)count_of(s, 0), (uint32_t)count_of(s, 1));
+    } else {
+        float* wo = weights_out + bh * Tout;
+        int* ko = kept + bh * budget;
+        if (tid == 0 && me == 0 && bh % Hkv == 0) lens_out[b] = count;
+        fill_rest(count, budget, Tout, me * kSelThreads + tid, chunks * kSelThreads, ko, wo);
+        // before this chunk: what is above the threshold, the ties that are taken, and recent tokens
+        int ties = at, pos;
+        if (me >= live) pos = need + max(0, lo - old);          // (all old tokens come before)
+        else pos = above + min(ties, th.rem) + max(0, lo - old);
+        for (int base = lo; base < hi; base += kBatch) {
+            load_batch(w, base, hi, x);
+            write_batch(s, x, base, old, hi, th, pos, ties, ko, wo);
+        }
     }
 }
 
@@ -195,9 +338,31 @@ void gather(const KvEvictArgs& a, hipStream_t st) {
 
 }  // namespace
 
-hipError_t launch_kv_evict(const KvEvictArgs& a, hipStream_t st) {
-    hipLaunchKernelGGL(kv_select_kernel, dim3(a.B * a.Hkv), dim3(kSelThreads), 0, st, a.weights, a.lens, a.Hkv, a.Tmax,
-                       a.budget, a.recent, a.Tout, a.weights_out, a.lens_out, a.kept);
+// Tokens of a chunk: whole batches, at most kChunks chunks.
+static int chunk_tokens(long long Tmax) { return (int)((Tmax + (long long)kBatch * kChunks - 1) / (kBatch * kChunks)) * kBatch; }
+
+long long kv_evict_workspace_words(long long B, long long Hkv, long long Tmax) {
+    if (Tmax <= kBatch) return 0;
+    const int chunk = chunk_tokens(Tmax);
+    return B * Hkv * ((Tmax + chunk - 1) / chunk) * kChunkWords;
+}
+
+hipError_t launch_kv_evict(const KvEvictArgs& a, uint32_t* work, hipStream_t st) {
+    if (a.Tmax <= kBatch) {
+        hipLaunchKernelGGL(kv_select_kernel, dim3(a.B * a.Hkv), dim3(kSelThreads), 0, st, a.weights, a.lens, a.Hkv,
+                           a.Tmax, a.budget, a.recent, a.Tout, a.weights_out, a.lens_out, a.kept);
+    } else {
+        const int chunk = chunk_tokens(a.Tmax), chunks = (a.Tmax + chunk - 1) / chunk;
+        const dim3 grid((unsigned)chunks * a.B * a.Hkv);
+#define W4A16_SELECT(L)                                                                                               \
+    hipLaunchKernelGGL(kv_select_chunk_kernel<L>, grid, dim3(kSelThreads), 0, st, a.weights, a.lens, a.Hkv, a.Tmax,    \
+                       a.budget, a.recent, a.Tout, chunks, chunk, work, a.weights_out, a.lens_out, a.kept)
+        W4A16_SELECT(0);
+        W4A16_SELECT(1);
+        W4A16_SELECT(2);
+        W4A16_SELECT(3);
+#undef W4A16_SELECT
+    }
     if (a.bits == 8) a.D == 64 ? gather<4, false>(a, st) : gather<8, false>(a, st);
     else a.D == 64 ? gather<2, true>(a, st) : gather<4, true>(a, st);
     return hipGetLastError();

@@ -133,7 +133,8 @@ struct KvEvictArgs {
     int *lens_out, *kept;
     int bits, B, Hkv, D, Tmax, Tout, budget, recent;
 };
-hipError_t launch_kv_evict(const KvEvictArgs& a, hipStream_t st);
+long long kv_evict_workspace_words(long long B, long long Hkv, long long Tmax);   // 0: none needed
+hipError_t launch_kv_evict(const KvEvictArgs& a, uint32_t* work, hipStream_t st);
 
 // Prompt attention (attention.hip): B sequences packed along T tokens, their bounds cu [B + 1] on
 // the device (clamped into [0, T]); rows of q / k / v are qs / ks / vs elements apart, those of
