@@ -60,15 +60,15 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 }
 
 // Where 16-byte piece c of row r of a [keys, D] tile sits in its row: the pieces are permuted so
-// that the 32 rows of a fragment read (K) and the 4 rows x 64 bytes of a transposing read (V)
-// fall in different banks.
+// that the 32 rows of a fragment read (K), the 4 rows x 64 bytes of a transposing read (V) and the
+// pieces of a store that skips 2 or 4 of them fall in different banks.
 template <int D>
 __device__ __forceinline__ int swz_k(int r, int c) {
     return D == 128 ? c ^ (r & 15) : c ^ ((r >> 1) & 7);
 }
 template <int D>
 __device__ __forceinline__ int swz_v(int r, int c) {
-    return D == 128 ? c ^ ((r & 3) << 2) : c ^ (((r >> 1) & 1) << 2);
+    return D == 128 ? c ^ ((r & 3) * 5) : c ^ (((r << 1) & 4) | ((r >> 1) & 3));
 }
 
 }  // namespace w4a16

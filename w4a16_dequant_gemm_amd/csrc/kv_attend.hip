@@ -31,20 +31,24 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// The codes of one 32-bit word as exact fp16 integers: int8 c (4 codes, in order) or nibbles
-// u - z (8 codes, order 0 4 1 5 2 6 3 7).  The code is OR-ed / permuted into the mantissa of 1024.
+// The codes of one 32-bit word as exact fp16 values: int8 c 2^-9 (4 codes, in order) or nibbles
+// (u - z) 2^-9 (8 codes, order 0 4 1 5 2 6 3 7; exact for |u - z| <= 2048).  Masks or byte permutes
+// leave the unsigned code as the subnormal u 2^-24 (two of the four masks: 16 u 2^-24), one packed
+// fused multiply-add scales it and takes the zero point out.
 __device__ __forceinline__ f16x2 as_h2(uint32_t w) { return __builtin_bit_cast(f16x2, w); }
 __device__ __forceinline__ uint32_t as_u(f16x2 h) { return __builtin_bit_cast(uint32_t, h); }
+__device__ __forceinline__ f16x2 both(float v) { return f16x2{(_Float16)v, (_Float16)v}; }
+constexpr float kCodeUnit = 512.0f;                        // 2^9
 __device__ __forceinline__ void codes_int8(uint32_t w, uint32_t out[2]) {
     const uint32_t b = w ^ 0x80808080u;                    // c + 128 per byte
-    const f16x2 off = {(_Float16)1152.0f, (_Float16)1152.0f};
-    out[0] = as_u(as_h2(perm(0x64646464u, b, 0x04010400u)) - off);
-    out[1] = as_u(as_h2(perm(0x64646464u, b, 0x04030402u)) - off);
+    out[0] = as_u(__builtin_elementwise_fma(as_h2(perm(0u, b, 0x0C010C00u)), both(32768.0f), both(-0.25f)));
+    out[1] = as_u(__builtin_elementwise_fma(as_h2(perm(0u, b, 0x0C030C02u)), both(32768.0f), both(-0.25f)));
 }
-__device__ __forceinline__ void codes_int4(uint32_t w, f16x2 z, uint32_t out[4]) {
-    const f16x2 off = {(_Float16)1024.0f, (_Float16)1024.0f};
+__device__ __forceinline__ void codes_int4(uint32_t w, f16x2 z9, uint32_t out[4]) {      // z9 = -z 2^-9
+    unpack_mask_f16(w, out);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) out[i] = as_u(as_h2(((w >> (4 * i)) & 0x000F000Fu) | 0x64006400u) - off - z);
+    for (int i = 0; i < 4; ++i)
+        out[i] = as_u(__builtin_elementwise_fma(as_h2(out[i]), both(i & 1 ? 2048.0f : 32768.0f), z9));
 }
 
 // the lanes 32 .. 63 of a and the lanes 0 .. 31 of b trade places
@@ -110,13 +114,13 @@ struct Attend {
 
         // the row's query as fp16, in the codes' order, times 2^e
         u32x4 qf[D / 16];
-        float cl;                                          // score scale: log2(e) / sqrt(D) / 2^e
+        float cl;                                          // score scale: 2^9 log2(e) / sqrt(D) / 2^e
         {
             u32x4 raw[D / 16];
             const uint16_t* qp = q + head * D + 8 * h;
 #pragma unroll
             for (int s = 0; s < D / 16; ++s) raw[s] = *reinterpret_cast<const u32x4*>(qp + 16 * s);
-            cl = 1.4426950408889634f / sqrtf((float)D);
+            cl = 1.4426950408889634f * kCodeUnit / sqrtf((float)D);
             if (bf16) {
                 float mx = 0.0f;
 #pragma unroll
@@ -124,7 +128,11 @@ struct Attend {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         mx = fmaxf(mx, fmaxf(fabsf(bf2f(raw[s][i] & 0xFFFFu)), fabsf(bf2f(raw[s][i] >> 16))));
-                mx = max_halves(mx);
+                // one factor for all rows of the block: it goes into K's scales
+                mx = wave_max(mx);
+                if (lane == 0) lds.m[wave][0] = mx;
+                __syncthreads();
+                mx = fmaxf(fmaxf(lds.m[0][0], lds.m[1][0]), fmaxf(lds.m[2][0], lds.m[3][0]));
                 const int e = mx > 0.0f ? 15 - __builtin_amdgcn_frexp_expf(mx) : 0;
                 cl = ldexpf(cl, -e);
 #pragma unroll
@@ -151,9 +159,12 @@ struct Attend {
 #pragma unroll
             for (int e = 0; e < 16; ++e) o[i][e] = 0.0f;
         const float NEG = -__builtin_inff();
-        float m = NEG, l = 0.0f;                           // base-2 domain
-        // weights enter the second product times 128 / vcap, vcap the largest V scale so far
+        // A weight is kept as 2^(s - sub), sub = m - lv with 2^lv = 128 / vcap, vcap the largest V scale so
+        // far: that is what the second product takes (times the token's V scale, so at most 2^15),
+        // and the common factor goes through l and O alike.  m may lag the maximum by 8.
+        float sub = 0.0f, l = 0.0f;                        // base-2 domain
         float vcap = 5.9604644775390625e-8f;               // fp16's smallest
+        float lv = 31.0f;                                  // log2(128 / vcap)
 
         u32x4 kr[PT], vr[PT];
         uint16_t pks = 0, pvs = 0, pkz[PT], pvz[PT];
@@ -199,7 +210,7 @@ struct Attend {
                                 codes_int8(w[2 * j + 1], d + 2);
                             } else {
                                 const _Float16 z = __builtin_bit_cast(_Float16, kv ? pvz[i] : pkz[i]);
-                                codes_int4(w[j], f16x2{z, z}, d);
+                                codes_int4(w[j], f16x2{z, z} * both(-0.001953125f), d);
                             }
                             const int ch = OUT * pc + j;
                             *reinterpret_cast<u32x4*>(dst + 8 * (kv ? swz_v<D>(r, ch) : swz_k<D>(r, ch))) =
@@ -210,7 +221,7 @@ struct Attend {
             }
             if (tid < KT) {                                // whole waves
                 const float s = h2f(pvs);
-                lds.ks[buf][tid] = h2f(pks);
+                lds.ks[buf][tid] = h2f(pks) * cl;
                 lds.vs[buf][tid] = s;
                 const float mx = wave_max(fabsf(s));
                 if (lane == 0) lds.vmax[buf][tid >> 6] = mx;
@@ -243,40 +254,51 @@ struct Attend {
                     S[b] = mfma<DT_F16>(a, qf[s], S[b]);
                 }
             }
-            // scores in the base-2 domain: times K's scale and the row's factor
-            const bool tail = tok0 + KW > t1;
-            float mt = NEG;
+            // exponents: the score times K's scale and the row's factor, minus the reference
+            float mx = NEG;
 #pragma unroll
             for (int b = 0; b < KB; ++b)
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
                     const f32x4 s4 = *reinterpret_cast<const f32x4*>(ksp + 32 * b + 8 * g + 4 * h);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        float v = S[b][4 * g + j] * (s4[j] * cl);
-                        if (tail && tok0 + 32 * b + 8 * g + 4 * h + j >= t1) v = NEG;
-                        S[b][4 * g + j] = v;
-                        mt = fmaxf(mt, v);
-                    }
+                    for (int j = 0; j < 4; ++j) S[b][4 * g + j] = fmaf(S[b][4 * g + j], s4[j], -sub);
                 }
-            mt = max_halves(mt);
+            if (tok0 + KW > t1) {
+#pragma unroll
+                for (int b = 0; b < KB; ++b)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        if (tok0 + 32 * b + 8 * (e >> 2) + 4 * h + (e & 3) >= t1) S[b][e] = NEG;
+            }
+#pragma unroll
+            for (int b = 0; b < KB; ++b)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) mx = fmaxf(mx, S[b][e]);
+            mx = max_halves(mx);
             const float vm = __builtin_bit_cast(
                 float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, lds.vmax[buf][wk * KW / 64])));
-            // the maximum may lag by 8 (weights up to 2^8), so O is rarely rescaled
-            if (vm > vcap || __builtin_amdgcn_ballot_w64(mt > m + 8.0f)) {
-                const float mn = fmaxf(m, mt), vn = fmaxf(vcap, vm);
-                const float f = mn == NEG ? 1.0f : exp2_raw(m - mn);
-                const float fo = f * (vcap / vn);
-                m = mn;
-                vcap = vn;
-                l *= f;
+            if (t == 0 || vm > vcap || __builtin_amdgcn_ballot_w64(mx > 8.0f + lv)) {
+                vcap = fmaxf(vcap, vm);
+                const float ln = 7.0f - __builtin_amdgcn_logf(vcap);
+                // the largest exponent becomes lv (the first tile's too, however low); a share of the
+                // first tile without any token stays as it is, and all its weights are 0
+                const float up = t > 0 ? fmaxf(mx, lv) : mx == NEG ? ln : mx;
+                const float d = up - ln, f = exp2_raw(-d);
+                lv = ln;
+                sub += d;
+                if (t > 0) {
+                    l *= f;
 #pragma unroll
-                for (int i = 0; i < D / 32; ++i)
+                    for (int i = 0; i < D / 32; ++i)
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) o[i][e] *= fo;
+                        for (int e = 0; e < 16; ++e) o[i][e] *= f;
+                }
+#pragma unroll
+                for (int b = 0; b < KB; ++b)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) S[b][e] -= d;
             }
-            const float vinv = 128.0f / vcap;
-            const float ms = m == NEG ? 0.0f : m;          // a row with nothing yet: every weight is 0
             u32x4 P[2 * KB];
 #pragma unroll
             for (int b = 0; b < KB; ++b)
@@ -286,9 +308,9 @@ struct Attend {
                     float p[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        p[j] = exp2_raw(S[b][4 * g + j] - ms);
+                        p[j] = exp2_raw(S[b][4 * g + j]);
                         l += p[j];
-                        p[j] *= s4[j] * vinv;
+                        p[j] *= s4[j];
                     }
                     P[2 * b + (g >> 1)][2 * (g & 1)] = pack2<DT_F16>(p[0], p[1]);
                     P[2 * b + (g >> 1)][2 * (g & 1) + 1] = pack2<DT_F16>(p[2], p[3]);
@@ -306,7 +328,7 @@ struct Attend {
         }
 
         l = sum_halves(l);
-        const float vout = vcap * 0.0078125f;              // O in its own units
+        const float m = l > 0.0f ? sub : NEG;              // the reference of l and O
         if constexpr (BITS == 4) {
             // lane halves hold elements 0 4 1 5 and 2 6 3 7 of every eight: to 0 .. 3 and 4 .. 7
 #pragma unroll
@@ -332,8 +354,7 @@ struct Attend {
 #pragma unroll
                     for (int g = 0; g < 4; ++g)
                         *reinterpret_cast<f32x4*>(op + 32 * i + 8 * g) =
-                            f32x4{o[i][4 * g] * vout, o[i][4 * g + 1] * vout, o[i][4 * g + 2] * vout,
-                                  o[i][4 * g + 3] * vout};
+                            f32x4{o[i][4 * g], o[i][4 * g + 1], o[i][4 * g + 2], o[i][4 * g + 3]} * kCodeUnit;
             }
         } else {
             // join the WK waves of each row set: every wave leaves its output, rescaled to the
@@ -350,7 +371,7 @@ struct Attend {
 #pragma unroll
             for (int w = 0; w < WK; ++w)
                 L += M == NEG ? 0.0f : lds.l[w * WQ + wq][n] * exp2_raw(lds.m[w * WQ + wq][n] - M);
-            const float f = M == NEG ? 0.0f : exp2_raw(m - M) * vout;
+            const float f = M == NEG ? 0.0f : exp2_raw(m - M) * kCodeUnit;
             float* ow = reinterpret_cast<float*>(lds.k);   // [wave][D / 4][32 rows][4] floats
             static_assert(sizeof(lds.k) + sizeof(lds.v) >= 4 * 32 * D * sizeof(float), "join buffer");
             static_assert(offsetof(Lds, v) == sizeof(lds.k), "join buffer spans k and v");
@@ -955,7 +976,7 @@ __global__ __launch_bounds__(kThreads) void kv_weights_kernel(const float2* __re
 // ------------------------------------------------------------------------------- host side
 
 constexpr long long kBlocks = 2048;      // blocks of the streaming kernel to aim for
-constexpr long long kPrefixBlocks = 1024;
+constexpr long long kPrefixBlocks = 512;
 constexpr int kMinChunk = 256;           // tokens of a split, at least
 constexpr int kStreamRows = 16;          // prefix rows per kv head up to which it is streamed
 
