@@ -44,26 +44,87 @@ __device__ __forceinline__ int find_sequence(const int* __restrict__ cu, int B, 
     return lo;
 }
 
+// A tile's rows straight to LDS: instruction i of the wave fills 1 KB, lane l 16 bytes at 16 l, which
+// hold the piece that the tile's permutation puts there.
+template <int D>
+struct TileLoad {
+    static constexpr int CH = D / 8;                    // 16-byte pieces of a row
+    static constexpr int RI = 64 / CH;                  // rows per instruction
+    static constexpr int NI = kKeys / RI / 4;           // instructions per wave
+    __device__ static __forceinline__ int row(int wave, int lane, int i) { return (wave * NI + i) * RI + lane / CH; }
+    __device__ static __forceinline__ void issue(const uint16_t* tile, const int (&off)[NI], uint16_t* lds, int wave) {
+        const __amdgpu_buffer_rsrc_t r =
+            __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(tile), 0, -1, 0x00020000);
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                r, (__attribute__((address_space(3))) void*)(lds + (wave * NI + i) * RI * D), 16, off[i], 0, 0, 0);
+    }
+};
+
+__device__ __forceinline__ bool any_lane(bool p) { return __builtin_amdgcn_ballot_w64(p) != 0; }
+// this wave's loads into LDS have landed, and its reads of LDS are in registers
+__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory"); }
+
+// Pipeline: in iteration t a wave turns the scores of tile t into weights while the matrix cores work
+// on the scores of tile t + 1 (independent instructions, interleaved), then multiplies the weights
+// with V(t).  One barrier an iteration: at its top every wave has waited for its own loads of the
+// previous one, so K(t + 1) and V(t) are complete, and K(t) and V(t - 1) have been read; K(t + 2) and
+// V(t + 1) are loaded over them.  The two buffers of K and of V are four LDS objects, so that the
+// compiler does not make a read of one wait for loads into another.
 template <int DT, int D>
 __global__ __launch_bounds__(256, 2) void attention_prompt_kernel(
     const uint16_t* __restrict__ q, const uint16_t* __restrict__ k, const uint16_t* __restrict__ v,
     const int* __restrict__ cu, int B, int T, int Hq, int Hkv, int qs, int ks, int vs, int tiles,
     uint16_t* __restrict__ out) {
-    constexpr int CH = D / 8;                       // 16-byte pieces of a row
-    constexpr int PT = kKeys * CH / 256;            // pieces a thread stages per tile
-    __shared__ __attribute__((aligned(16))) uint16_t Ks[2][kKeys * D], Vs[2][kKeys * D];
+    using L = TileLoad<D>;
+    __shared__ __attribute__((aligned(16))) uint16_t K0[kKeys * D], K1[kKeys * D], V0[kKeys * D], V1[kKeys * D];
 
-    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
     const int n = lane & 31, h = lane >> 5;
     // late row tiles (the ones with most keys) first; heads vary fastest
     const int head = blockIdx.x % Hq;
     const int slot = tiles - 1 - blockIdx.x / Hq;
     const int b = find_sequence(cu, B, T, slot, lane);
-    const int s0 = min(max(cu[b], 0), T);
-    const int len = min(max(cu[b + 1], s0), T) - s0;
+    const int s0 = __builtin_amdgcn_readfirstlane(min(max(cu[b], 0), T));
+    const int len = __builtin_amdgcn_readfirstlane(min(max(cu[b + 1], s0), T)) - s0;
     const int row0 = (slot - (s0 / kRows + b)) * kRows;
     if (row0 < 0 || row0 >= len) return;            // a slot between two sequences
     const int kvh = head / (Hq / Hkv);
+
+    const int ntiles = (min(row0 + kRows, len) + kKeys - 1) / kKeys;
+    const uint16_t* kb = k + (long long)s0 * ks + kvh * D;
+    const uint16_t* vb = v + (long long)s0 * vs + kvh * D;
+    int koff[L::NI], voff[L::NI];                   // byte offsets in a tile
+    // rows behind the sequence are replaced by its last one: they may hold anything
+    auto k_offsets = [&](int last) {
+#pragma unroll
+        for (int i = 0; i < L::NI; ++i) {
+            const int r = L::row(wave, lane, i);
+            koff[i] = (min(r, last) * ks + 8 * swz_k<D>(r, lane % L::CH)) * 2;
+        }
+    };
+    auto v_offsets = [&](int last) {
+#pragma unroll
+        for (int i = 0; i < L::NI; ++i) {
+            const int r = L::row(wave, lane, i);
+            voff[i] = (min(r, last) * vs + 8 * swz_v<D>(r, lane % L::CH)) * 2;
+        }
+    };
+    k_offsets(len - 1);
+    v_offsets(len - 1);
+    auto load_k = [&](int t, uint16_t* lds) {
+        if (t >= ntiles) return;
+        if (t > 0 && (t + 1) * kKeys > len) k_offsets(len - 1 - t * kKeys);       // the last tile
+        L::issue(kb + (long long)t * kKeys * ks, koff, lds, wave);
+    };
+    auto load_v = [&](int t, uint16_t* lds) {
+        if (t >= ntiles) return;
+        if (t > 0 && (t + 1) * kKeys > len) v_offsets(len - 1 - t * kKeys);
+        L::issue(vb + (long long)t * kKeys * vs, voff, lds, wave);
+    };
+    load_k(0, K0);
+    load_v(0, V0);
 
     const int wrow = row0 + 32 * wave;              // first row of the wave
     const int row = wrow + n;                       // the lane's row (behind the sequence: not stored)
@@ -73,6 +134,8 @@ __global__ __launch_bounds__(256, 2) void attention_prompt_kernel(
 #pragma unroll
         for (int s = 0; s < D / 16; ++s) qf[s] = *reinterpret_cast<const u32x4*>(qp + 16 * s);
     }
+    // tiles with a key that some row of the wave sees; only the last of them needs a mask
+    const int own = wrow < len ? min(wrow + 31, len - 1) / kKeys + 1 : 0;
 
     f32x16 o[D / 32];
 #pragma unroll
@@ -84,115 +147,167 @@ __global__ __launch_bounds__(256, 2) void attention_prompt_kernel(
     bool big = false;                               // wave-uniform: some |c M| is above 2^20
     const float c = 1.4426950408889634f / sqrtf((float)D);
 
-    const int ntiles = (min(row0 + kRows, len) + kKeys - 1) / kKeys;
-    const uint16_t* kb = k + (long long)s0 * ks + kvh * D;
-    const uint16_t* vb = v + (long long)s0 * vs + kvh * D;
-    u32x4 kr[PT], vr[PT];
-    // rows behind the sequence are replaced by its last one: they may hold anything
-    auto load = [&](int t) {
-        const uint16_t* kt = kb + (long long)t * kKeys * ks;
-        const uint16_t* vt = vb + (long long)t * kKeys * vs;
-        const int last = len - 1 - t * kKeys;
+    // running maximum of tile t; where it rises O and l are rescaled
+    auto maximum = [&](f32x16 (&S)[2], float& sub) {
+        float mt = S[0][0];
 #pragma unroll
-        for (int i = 0; i < PT; ++i) {
-            const int p = tid + 256 * i, r = min(p / CH, last), ch = p % CH;
-            kr[i] = *reinterpret_cast<const u32x4*>(kt + r * ks + 8 * ch);
-            vr[i] = *reinterpret_cast<const u32x4*>(vt + r * vs + 8 * ch);
-        }
-    };
-    auto store = [&](int buf) {
+        for (int kb2 = 0; kb2 < 2; ++kb2)
 #pragma unroll
-        for (int i = 0; i < PT; ++i) {
-            const int p = tid + 256 * i, r = p / CH, ch = p % CH;
-            *reinterpret_cast<u32x4*>(&Ks[buf][r * D + 8 * swz_k<D>(r, ch)]) = kr[i];
-            *reinterpret_cast<u32x4*>(&Vs[buf][r * D + 8 * swz_v<D>(r, ch)]) = vr[i];
-        }
-    };
-
-    load(0);
-    store(0);
-    __syncthreads();
-    for (int t = 0; t < ntiles; ++t) {
-        if (t + 1 < ntiles) load(t + 1);
-        const uint16_t* K = Ks[t & 1];
-        const uint16_t* V = Vs[t & 1];
-        const int key0 = t * kKeys;
-        if (key0 <= wrow + 31) {                    // wave-uniform: some key is visible to some row
-            f32x16 S[2];
-#pragma unroll
-            for (int kb2 = 0; kb2 < 2; ++kb2) {
-#pragma unroll
-                for (int e = 0; e < 16; ++e) S[kb2][e] = 0.0f;
-                const int r = 32 * kb2 + n;
-#pragma unroll
-                for (int s = 0; s < D / 16; ++s) {
-                    const u32x4 a = *reinterpret_cast<const u32x4*>(K + r * D + 8 * swz_k<D>(r, 2 * s + h));
-                    S[kb2] = mfma<DT>(a, qf[s], S[kb2]);
-                }
-            }
-            if (key0 + kKeys - 1 > wrow) {
-#pragma unroll
-                for (int kb2 = 0; kb2 < 2; ++kb2)
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        if (key0 + 32 * kb2 + 8 * (e >> 2) + 4 * h + (e & 3) > row) S[kb2][e] = -__builtin_inff();
-            }
-            float mt = S[0][0];
-#pragma unroll
-            for (int kb2 = 0; kb2 < 2; ++kb2)
-#pragma unroll
-                for (int e = 0; e < 16; ++e) mt = fmaxf(mt, S[kb2][e]);
-            mt = max_halves(mt);
-            // O and l follow a maximum that may lag the true one by 8 / c (weights up to 2^8): the
-            // rescaling of O is then rare, and exact either way
-            if (__builtin_amdgcn_ballot_w64(mt > M + 8.0f / c)) {
-                const float Mn = fmaxf(M, mt);
-                const float f = exp2_raw((M - Mn) * c);
-                M = Mn;
-                m = M * c;
-                l *= f;
-#pragma unroll
-                for (int i = 0; i < D / 32; ++i)
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) o[i][e] *= f;
-                big = __builtin_amdgcn_ballot_w64(fabsf(m) > 1048576.0f) != 0;
-            }
-            // c S - m in one fused operation, exact up to the rounding of m, which all weights of a
-            // row share and which cancels; where it could pass the exponent range, S - M first
-            float sub = m;
-            if (big) {
-                sub = 0.0f;
-#pragma unroll
-                for (int kb2 = 0; kb2 < 2; ++kb2)
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) S[kb2][e] -= M;
-            }
-            u32x4 P[4];
-#pragma unroll
-            for (int kb2 = 0; kb2 < 2; ++kb2)
-#pragma unroll
-                for (int s = 0; s < 2; ++s)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float p0 = exp2_raw(fmaf(S[kb2][8 * s + 2 * j], c, -sub));
-                        const float p1 = exp2_raw(fmaf(S[kb2][8 * s + 2 * j + 1], c, -sub));
-                        l += p0 + p1;
-                        P[2 * kb2 + s][j] = pack2<DT>(p0, p1);
-                    }
+            for (int e = 0; e < 16; ++e) mt = fmaxf(mt, S[kb2][e]);
+        mt = max_halves(mt);
+        // O and l follow a maximum that may lag the true one by 8 / c (weights up to 2^8): the
+        // rescaling of O is then rare, and exact either way
+        if (any_lane(mt > M + 8.0f / c)) {
+            const float Mn = fmaxf(M, mt);
+            const float f = exp2_raw((M - Mn) * c);
+            M = Mn;
+            m = M * c;
+            l *= f;
 #pragma unroll
             for (int i = 0; i < D / 32; ++i)
 #pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    const int r = 16 * s + 4 * h + ((lane & 15) >> 2);
-                    const int ch = 4 * i + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
-                    const u32x2 a0 = lds_read_tr(V + r * D + 8 * swz_v<D>(r, ch) + 4 * (lane & 1));
-                    const u32x2 a1 = lds_read_tr(V + (r + 8) * D + 8 * swz_v<D>(r + 8, ch) + 4 * (lane & 1));
-                    o[i] = mfma<DT>(u32x4{a0.x, a0.y, a1.x, a1.y}, P[s], o[i]);
-                }
+                for (int e = 0; e < 16; ++e) o[i][e] *= f;
+            big = any_lane(fabsf(m) > 1048576.0f);
         }
-        if (t + 1 < ntiles) store((t + 1) & 1);
+        // c S - m in one fused operation, exact up to the rounding of m, which all weights of a
+        // row share and which cancels; where it could pass the exponent range, S - M first
+        sub = m;
+        if (big) {
+            sub = 0.0f;
+#pragma unroll
+            for (int kb2 = 0; kb2 < 2; ++kb2)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) S[kb2][e] -= M;
+        }
+    };
+    auto weights = [&](const f32x16 (&S)[2], float sub, u32x4 (&P)[4]) {
+#pragma unroll
+        for (int kb2 = 0; kb2 < 2; ++kb2)
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float p0 = exp2_raw(fmaf(S[kb2][8 * s + 2 * j], c, -sub));
+                    const float p1 = exp2_raw(fmaf(S[kb2][8 * s + 2 * j + 1], c, -sub));
+                    l += p0 + p1;
+                    P[2 * kb2 + s][j] = pack2<DT>(p0, p1);
+                }
+    };
+    auto values = [&](const uint16_t* V, const u32x4 (&P)[4]) {
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                const int r = 16 * s + 4 * h + ((lane & 15) >> 2);
+                const int ch = 4 * i + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+                const u32x2 a0 = lds_read_tr(V + r * D + 8 * swz_v<D>(r, ch) + 4 * (lane & 1));
+                const u32x2 a1 = lds_read_tr(V + (r + 8) * D + 8 * swz_v<D>(r + 8, ch) + 4 * (lane & 1));
+                o[i] = mfma<DT>(u32x4{a0.x, a0.y, a1.x, a1.y}, P[s], o[i]);
+            }
+    };
+    // piece 2 s + h of key 32 kb2 + n: the permutation is an exclusive or, so one register and one
+    // operation a read do (kept opaque, or the compiler holds an address per piece)
+    auto key_piece = [&](const uint16_t* K, int kb2, int s) {
+        int at = n * D + 8 * swz_k<D>(n, h);
+        asm("" : "+v"(at));
+        return *reinterpret_cast<const u32x4*>(K + 32 * kb2 * D + (at ^ (16 * s)));
+    };
+    auto scores = [&](const uint16_t* K, f32x16 (&S)[2]) {
+#pragma unroll
+        for (int kb2 = 0; kb2 < 2; ++kb2) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) S[kb2][e] = 0.0f;
+#pragma unroll
+            for (int s = 0; s < D / 16; ++s) S[kb2] = mfma<DT>(key_piece(K, kb2, s), qf[s], S[kb2]);
+        }
+    };
+    // weights of S and scores of the next tile, a k-step's products and its share of the weights at a
+    // time, the fragments one k-step ahead
+    auto weights_and_scores = [&](const f32x16 (&S)[2], float sub, u32x4 (&P)[4], const uint16_t* K, f32x16 (&Sn)[2]) {
+        constexpr int KS = D / 16, PW = 16 / KS;    // k-steps; pairs of weights per k-step
+        u32x4 a0 = key_piece(K, 0, 0), a1 = key_piece(K, 1, 0);
+#pragma unroll
+        for (int kb2 = 0; kb2 < 2; ++kb2)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) Sn[kb2][e] = 0.0f;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            u32x4 n0, n1;
+            if (s + 1 < KS) {
+                n0 = key_piece(K, 0, s + 1);
+                n1 = key_piece(K, 1, s + 1);
+            }
+            Sn[0] = mfma<DT>(a0, qf[s], Sn[0]);
+            Sn[1] = mfma<DT>(a1, qf[s], Sn[1]);
+#pragma unroll
+            for (int i = 0; i < PW; ++i) {
+                const int pr = PW * s + i, kb2 = pr >> 3, e = 2 * (pr & 7);
+                const float p0 = exp2_raw(fmaf(S[kb2][e], c, -sub));
+                const float p1 = exp2_raw(fmaf(S[kb2][e + 1], c, -sub));
+                l += p0 + p1;
+                P[pr >> 2][pr & 3] = pack2<DT>(p0, p1);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            a0 = n0;
+            a1 = n1;
+        }
+    };
+    // top of iteration t: Kl takes K(t + 2), Vl takes V(t + 1)
+    auto turn = [&](int t, uint16_t* Kl, uint16_t* Vl) {
+        wait_loads();
         __syncthreads();
+        load_k(t + 2, Kl);
+        load_v(t + 1, Vl);
+    };
+    // iteration t where the wave sees tile t + 1 too: Kn = K(t + 1), Vc = V(t)
+    auto full_step = [&](int t, const uint16_t* Kn, uint16_t* Kl, const uint16_t* Vc, uint16_t* Vl, f32x16 (&S)[2],
+                         f32x16 (&Sn)[2]) {
+        turn(t, Kl, Vl);
+        u32x4 P[4];
+        float sub;
+        maximum(S, sub);
+        weights_and_scores(S, sub, P, Kn, Sn);
+        values(Vc, P);
+    };
+    // the wave's last tile, the only one with a key behind one of its rows
+    auto last_step = [&](int t, uint16_t* Kl, const uint16_t* Vc, uint16_t* Vl, f32x16 (&S)[2]) {
+        turn(t, Kl, Vl);
+        const int seen = row - 4 * h - t * kKeys;       // (one register to compare constants with)
+#pragma unroll
+        for (int kb2 = 0; kb2 < 2; ++kb2)
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                if (32 * kb2 + 8 * (e >> 2) + (e & 3) > seen) S[kb2][e] = -__builtin_inff();
+        u32x4 P[4];
+        float sub;
+        maximum(S, sub);
+        weights(S, sub, P);
+        values(Vc, P);
+    };
+
+    f32x16 Sa[2], Sb[2];
+    wait_loads();
+    __syncthreads();
+    load_k(1, K1);
+    // A block's rows begin at a multiple of two tiles, so its waves 0 and 1 end in an even tile and
+    // waves 2 and 3 in the odd one after it; a wave without rows only keeps the barriers.
+    int t = 0;
+    if (own > 0) {
+        scores(K0, Sa);
+        for (; t + 2 < own; t += 2) {
+            full_step(t, K1, K0, V0, V1, Sa, Sb);
+            full_step(t + 1, K0, K1, V1, V0, Sb, Sa);
+        }
+        if (t + 1 < own) {
+            full_step(t, K1, K0, V0, V1, Sa, Sb);
+            last_step(t + 1, K1, V1, V0, Sb);
+            t += 2;
+        } else {
+            last_step(t, K0, V0, V1, Sa);
+            t += 1;
+        }
     }
+    for (; t < ntiles; ++t) turn(t, t & 1 ? K1 : K0, t & 1 ? V0 : V1);
 
     l = sum_halves(l);
     if (row < len) {

@@ -265,11 +265,12 @@ struct Attend {
                     for (int j = 0; j < 4; ++j) S[b][4 * g + j] = fmaf(S[b][4 * g + j], s4[j], -sub);
                 }
             if (tok0 + KW > t1) {
+                const int left = t1 - tok0 - 4 * h;        // (one register to compare constants with)
 #pragma unroll
                 for (int b = 0; b < KB; ++b)
 #pragma unroll
                     for (int e = 0; e < 16; ++e)
-                        if (tok0 + 32 * b + 8 * (e >> 2) + 4 * h + (e & 3) >= t1) S[b][e] = NEG;
+                        if (32 * b + 8 * (e >> 2) + (e & 3) >= left) S[b][e] = NEG;
             }
 #pragma unroll
             for (int b = 0; b < KB; ++b)
@@ -651,11 +652,12 @@ struct Stream {
 #pragma unroll
             for (int s = 0; s < NS; ++s) S[s] = S[s] * *reinterpret_cast<const f32x4*>(&L.ks[16 * s + 4 * qd]);
             if (tok0 + KT > t1) {
+                const int left = t1 - tok0 - 4 * qd;
 #pragma unroll
                 for (int s = 0; s < NS; ++s)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        if (tok0 + 16 * s + 4 * qd + i >= t1) S[s][i] = NEG;
+                        if (16 * s + i >= left) S[s][i] = NEG;
             }
 #pragma unroll
             for (int s = 0; s < NS; ++s)
