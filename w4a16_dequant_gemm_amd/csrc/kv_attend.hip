@@ -74,7 +74,14 @@ struct TileLds {
     float m[4][32], l[4][32];
 };
 
-// The largest of the 64 lanes' non-negative values, in every lane.
+// Orders what one wave writes to LDS before what its other lanes read of it (the LDS pipe keeps a
+// wave's accesses in order; this keeps the compiler from moving them).
+__device__ __forceinline__ void wave_lds_fence() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// The largest of the 64 lanes' values, in every lane.
 __device__ __forceinline__ float wave_max(float v) {
     v = fmaxf(v, dpp_mov<0xB1>(v));
     v = fmaxf(v, dpp_mov<0x4E>(v));
@@ -347,15 +354,29 @@ struct Attend {
         }
         const long long at = head * nsplit + split;
         if constexpr (WK == 1) {
-            if (row < R) {
-                if (h == 0) ml[at] = make_float2(m, l);
-                float* op = po + at * D + 4 * h;
+            // through LDS, so that a row is stored as whole lines: lanes store 16 bytes 4 rows of a
+            // column apart otherwise (32 sequences behind 4096 tokens: 4 us of 23)
+            if (h == 0 && row < R) ml[at] = make_float2(m, l);
+            static_assert(sizeof(lds.k) + sizeof(lds.v) >= 4 * 32 * D * sizeof(float), "output buffer");
+            static_assert(offsetof(Lds, v) == sizeof(lds.k), "output buffer spans k and v");
+            constexpr int CQ = D / 4;                      // 16-byte pieces of a row
+            f32x4* ow = reinterpret_cast<f32x4*>(lds.k) + wave * 32 * CQ;
+            __syncthreads();                               // everyone is done with K and V
 #pragma unroll
-                for (int i = 0; i < D / 32; ++i)
+            for (int i = 0; i < D / 32; ++i)
 #pragma unroll
-                    for (int g = 0; g < 4; ++g)
-                        *reinterpret_cast<f32x4*>(op + 32 * i + 8 * g) =
-                            f32x4{o[i][4 * g], o[i][4 * g + 1], o[i][4 * g + 2], o[i][4 * g + 3]} * kCodeUnit;
+                for (int g = 0; g < 4; ++g)
+                    ow[n * CQ + ((8 * i + 2 * g + h) ^ (n % CQ))] =
+                        f32x4{o[i][4 * g], o[i][4 * g + 1], o[i][4 * g + 2], o[i][4 * g + 3]} * kCodeUnit;
+            wave_lds_fence();
+            const int c = lane % CQ;
+#pragma unroll 4
+            for (int r = lane / CQ; r < 32; r += 64 / CQ) {
+                const int gr = row0 + 32 * wq + r;
+                if (gr < R) {
+                    const long long to = (hq0 + (long long)(gr / G) * Hq + gr % G) * nsplit + split;
+                    *reinterpret_cast<f32x4*>(po + to * D + 4 * c) = ow[r * CQ + (c ^ (r % CQ))];
+                }
             }
         } else {
             // join the WK waves of each row set: every wave leaves its output, rescaled to the
@@ -427,13 +448,6 @@ __device__ __forceinline__ float across_quarters(float x, Op op) {
     float lo, hi;
     halves(op(__builtin_bit_cast(float, a), __builtin_bit_cast(float, b)), lo, hi);
     return op(lo, hi);
-}
-
-// Orders what one wave writes to LDS before what its other lanes read of it (the LDS pipe keeps a
-// wave's accesses in order; this keeps the compiler from moving them).
-__device__ __forceinline__ void wave_lds_fence() {
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_wave_barrier();
 }
 
 // Few rows: tokens [t0, t1) of a cache for the rows row0 .. row0 + 15 (R in all; numbered as in
@@ -798,83 +812,76 @@ __device__ __forceinline__ void empty_split(long long hq0, int G, int Hq, int ro
     }
 }
 
-// The shared prefix, many rows: block = (kv head and split, tile of 32 WQ rows).  The row tiles of
-// one span run on one XCD, one after the other, so that the span's codes are read from HBM once.
-template <int BITS, int D, int WQ>
-__global__ __launch_bounds__(kThreads, 2) void kv_prefix_kernel(const uint16_t* __restrict__ q, int bf16, int B, int Hq,
-                                                                int Hkv, KvCache c, int P, int Pmax, int chunk,
-                                                                int psplit, int nsplit, float2* __restrict__ ml,
-                                                                float* __restrict__ po) {
-    using A = Attend<BITS, D, WQ, 4 / WQ>;
-    __shared__ __attribute__((aligned(16))) typename A::Lds lds;
-    const int G = Hq / Hkv, R = B * G;
-    const int rtiles = (R + 32 * WQ - 1) / (32 * WQ);
-    const int j = blockIdx.x / 8;
-    const int span = blockIdx.x % 8 + 8 * (j / rtiles), rt = j % rtiles;
-    if (span >= Hkv * psplit) return;
-    const int kvh = span / psplit, split = span % psplit;
-    const int t0 = split * chunk, t1 = min(P, t0 + chunk);
-    A::run(lds, q, bf16 != 0, Hq, G, (long long)kvh * G, rt * 32 * WQ, R,
-           cache_rows<BITS, D>(c, (long long)kvh * Pmax), t0, t1, nsplit, split, ml, po);
-}
-
-// Streaming: the first `pblocks` blocks take the shared prefix where it has few rows (block = kv head,
-// tile of 16 of its B G rows, split), the others the sequences' own caches (block = split, sequence, kv
-// head, tile of 16 of its G heads).  Splits vary slowest and each turns the rest by one: consecutive
-// blocks run on the 8 XCDs in turn, and the late splits of short sequences, which are empty, have to
-// fall on all of them (with the splits fastest, 16 sequences of 1024 .. 4096 tokens and 4 splits
-// took 70 us instead of 53, two XCDs having no empty split at all).
-struct StreamGrid {
+// The shared prefix in the first `pblocks` blocks, the sequences' own caches in the others, so that the
+// arithmetic of the one and the loads of the other share the GPU.
+//   Prefix, WQ > 0 (many rows): block = (kv head and split, tile of 32 WQ rows).  The row tiles of one
+//     span run on one XCD, one after the other, so that the span's codes are read from HBM once.
+//   Prefix, WQ == 0 (few rows, streamed): block = kv head, split, tile of 16 of its B G rows.
+//   Own caches: block = split, sequence, kv head, tile of 16 of its G heads.  Splits vary slowest and
+//     each turns the rest by one: consecutive blocks run on the 8 XCDs in turn, and the late splits
+//     of short sequences, which are empty, have to fall on all of them (with the splits fastest, 16
+//     sequences of 1024 .. 4096 tokens and 4 splits took 70 us instead of 58, two XCDs having no
+//     empty split at all).
+struct DecodeGrid {
     int pblocks, psplit, pchunk, P, Pmax;    // prefix splits come first among a row's nsplit
     int osplit, ochunk, Tmax, nsplit;
 };
-template <int BITS, int D, bool SCORES>
-__global__ __launch_bounds__(kThreads, 3) void kv_stream_kernel(const uint16_t* __restrict__ q, int bf16, int B, int Hq,
+template <int BITS, int D, int WQ>
+struct PrefixKind {
+    using type = Attend<BITS, D, WQ, 4 / WQ>;
+};
+template <int BITS, int D>
+struct PrefixKind<BITS, D, 0> {
+    using type = Stream<BITS, D, false>;
+};
+template <int BITS, int D, int WQ, bool SCORES>
+__global__ __launch_bounds__(kThreads, 2) void kv_decode_kernel(const uint16_t* __restrict__ q, int bf16, int B, int Hq,
                                                                 int Hkv, KvCache prefix, KvCache own,
-                                                                const int* __restrict__ lens, StreamGrid g,
+                                                                const int* __restrict__ lens, DecodeGrid g,
                                                                 float2* __restrict__ ml, float* __restrict__ po,
                                                                 float* __restrict__ score, int spad) {
-    using A = Stream<BITS, D, SCORES>;
-    __shared__ __attribute__((aligned(16))) typename A::Lds lds;
+    using A = typename PrefixKind<BITS, D, WQ>::type;
+    using S = Stream<BITS, D, SCORES>;
+    __shared__ union alignas(16) {
+        typename A::Lds a;
+        typename S::Lds s;
+    } lds;
     __shared__ float sm[4][16], sl[4][16];
     const int G = Hq / Hkv;
     int id = blockIdx.x;
-    CacheRows c;
-    long long hq0;
-    int row0, R, t0, t1, split;
     if (id < g.pblocks) {
-        R = B * G;
-        const int rtiles = (R + 15) / 16;
-        row0 = 16 * (id % rtiles);
-        id /= rtiles;
-        split = id % g.psplit;
-        const int kvh = id / g.psplit;
-        hq0 = (long long)kvh * G;
-        t0 = split * g.pchunk;
-        t1 = min(g.P, t0 + g.pchunk);
-        c = cache_rows<BITS, D>(prefix, (long long)kvh * g.Pmax);
-    } else {
-        id -= g.pblocks;
-        R = G;
-        const int htiles = (G + 15) / 16;
-        const int pairs = B * Hkv * htiles;
-        split = id / pairs;
-        id = (id % pairs + split) % pairs;
-        row0 = 16 * (id % htiles);
-        id /= htiles;
-        const int kvh = id % Hkv, b = id / Hkv;
-        hq0 = (long long)b * Hq + (long long)kvh * G;
-        const int T = min(max(lens[b], 0), g.Tmax);
-        t0 = split * g.ochunk;
-        t1 = min(T, t0 + g.ochunk);
-        split += g.psplit;
-        if (t0 >= t1) {
-            empty_split(hq0, G, Hq, row0, min(16, G - row0), g.nsplit, split, ml);
-            return;
-        }
-        c = cache_rows<BITS, D>(own, ((long long)b * Hkv + kvh) * g.Tmax);
+        const int R = B * G;
+        constexpr int RT = WQ > 0 ? 32 * WQ : 16;
+        const int rtiles = (R + RT - 1) / RT;
+        const int j = id / 8;
+        const int span = id % 8 + 8 * (j / rtiles), rt = j % rtiles;
+        if (span >= Hkv * g.psplit) return;
+        const int kvh = span / g.psplit, split = span % g.psplit;
+        const int t0 = split * g.pchunk, t1 = min(g.P, t0 + g.pchunk);
+        const CacheRows c = cache_rows<BITS, D>(prefix, (long long)kvh * g.Pmax);
+        if constexpr (WQ > 0)
+            A::run(lds.a, q, bf16 != 0, Hq, G, (long long)kvh * G, rt * RT, R, c, t0, t1, g.nsplit, split, ml, po);
+        else
+            A::run(lds.a, sm, sl, q, bf16 != 0, Hq, G, (long long)kvh * G, rt * RT, R, c, t0, t1, g.nsplit, split, ml,
+                   po, nullptr, 0);
+        return;
     }
-    A::run(lds, sm, sl, q, bf16 != 0, Hq, G, hq0, row0, R, c, t0, t1, g.nsplit, split, ml, po, score, spad);
+    id -= g.pblocks;
+    const int htiles = (G + 15) / 16, pairs = B * Hkv * htiles;
+    const int os = id / pairs;
+    id = (id % pairs + os) % pairs;
+    const int row0 = 16 * (id % htiles);
+    id /= htiles;
+    const int kvh = id % Hkv, b = id / Hkv;
+    const long long hq0 = (long long)b * Hq + (long long)kvh * G;
+    const int T = min(max(lens[b], 0), g.Tmax);
+    const int t0 = os * g.ochunk, t1 = min(T, t0 + g.ochunk), split = g.psplit + os;
+    if (t0 >= t1) {
+        empty_split(hq0, G, Hq, row0, min(16, G - row0), g.nsplit, split, ml);
+        return;
+    }
+    S::run(lds.s, sm, sl, q, bf16 != 0, Hq, G, hq0, row0, G,
+           cache_rows<BITS, D>(own, ((long long)b * Hkv + kvh) * g.Tmax), t0, t1, g.nsplit, split, ml, po, score, spad);
 }
 
 // (max, sum) over all splits of a row; every lane of the wave gets it.
@@ -887,42 +894,37 @@ __device__ __forceinline__ void row_stats(const float2* __restrict__ ml, int nsp
         if (mn != NEG) l = l * exp2_raw(m - mn) + v.y * exp2_raw(v.x - mn);
         m = mn;
     }
-    M = m;
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor(M, off, 64));
+    M = wave_max(m);
     L = wave_sum(m == NEG ? 0.0f : l * exp2_raw(m - M));
 }
 
-// One block per query head of the batch: wave w adds up splits w, w + 4, ...; a row that saw no
+// One block per query head of the batch: each group of D / 4 threads adds up splits grp, grp + NG, ...
+// (16 bytes a thread, several loads in flight), the groups are added through LDS; a row that saw no
 // token gets zeros.
 template <int D>
 __device__ __forceinline__ void merge_row(float (*part)[D], long long head, const float2* __restrict__ ml,
                                           const float* __restrict__ po, int nsplit, int bf16,
                                           uint16_t* __restrict__ out) {
-    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-    constexpr int V = D / 64;                              // elements per lane
+    constexpr int CQ = D / 4, NG = kThreads / CQ;
+    const int tid = threadIdx.x, c = tid % CQ, grp = tid / CQ;
     const float2* mlr = ml + head * nsplit;
+    const float* pr = po + head * nsplit * D + 4 * c;
     float M, L;
-    row_stats(mlr, nsplit, lane, M, L);
-    float acc[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) acc[i] = 0.0f;
+    row_stats(mlr, nsplit, tid & 63, M, L);
+    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 4
-    for (int j = wave; j < nsplit; j += 4) {
-        const float mj = mlr[j].x;
-        const float w = mj == -__builtin_inff() ? 0.0f : exp2_raw(mj - M);
-        const float* p = po + (head * nsplit + j) * D + lane * V;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const float x = p[i];
-            acc[i] = w > 0.0f ? fmaf(w, x, acc[i]) : acc[i];   // an empty split's output is not defined
-        }
+    for (int j = grp; j < nsplit; j += NG) {
+        const float2 v = mlr[j];
+        const f32x4 x = *reinterpret_cast<const f32x4*>(pr + (long long)j * D);
+        // an empty split's output is not defined
+        if (v.y > 0.0f) acc += x * exp2_raw(v.x - M);
     }
-#pragma unroll
-    for (int i = 0; i < V; ++i) part[wave][lane * V + i] = acc[i];
+    *reinterpret_cast<f32x4*>(&part[grp][4 * c]) = acc;
     __syncthreads();
     if (tid < D) {
-        const float s = (part[0][tid] + part[1][tid]) + (part[2][tid] + part[3][tid]);
+        float s = part[0][tid];
+#pragma unroll
+        for (int i = 1; i < NG; ++i) s += part[i][tid];
         const float v = L > 0.0f ? s / L : 0.0f;
         out[head * D + tid] = bf16 ? f2bf_bits(v) : f2h_bits(v);
     }
@@ -931,13 +933,14 @@ __device__ __forceinline__ void merge_row(float (*part)[D], long long head, cons
 template <int D>
 __global__ __launch_bounds__(kThreads) void kv_merge_kernel(const float2* __restrict__ ml, const float* __restrict__ po,
                                                             int nsplit, int bf16, uint16_t* __restrict__ out) {
-    __shared__ float part[4][D];
+    __shared__ __attribute__((aligned(16))) float part[kThreads / (D / 4)][D];
     merge_row<D>(part, blockIdx.x, ml, po, nsplit, bf16, out);
 }
 
 // Output and accumulated weights in one launch: the first `heads` blocks merge a query head each,
 // the others turn kSpan scores of a (sequence, kv head) into weights.
 constexpr int kSpan = 4 * kThreads;
+constexpr int kStatHeads = 64;           // heads whose statistics are at hand at a time
 template <int D>
 __global__ __launch_bounds__(kThreads) void kv_weights_kernel(const float2* __restrict__ ml,
                                                               const float* __restrict__ po, int nsplit, int bf16,
@@ -946,7 +949,8 @@ __global__ __launch_bounds__(kThreads) void kv_weights_kernel(const float2* __re
                                                               const float* __restrict__ score, int spad,
                                                               const float* __restrict__ weights,
                                                               float* __restrict__ sums) {
-    __shared__ float part[4][D];
+    __shared__ __attribute__((aligned(16))) float part[kThreads / (D / 4)][D];
+    __shared__ float2 stat[kStatHeads];                    // a head's maximum and 1 / sum
     if (blockIdx.x < (unsigned)heads) {
         merge_row<D>(part, blockIdx.x, ml, po, nsplit, bf16, out);
         return;
@@ -957,22 +961,35 @@ __global__ __launch_bounds__(kThreads) void kv_weights_kernel(const float2* __re
     const int T = min(max(lens[b], 0), Tmax);
     if (t0 >= T) return;
     const long long hq0 = (long long)b * Hq + (long long)(bh % Hkv) * G;
-    const int t = t0 + 4 * threadIdx.x;
-    float w[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int g = 0; g < G; ++g) {
-        float M, L;
-        row_stats(ml + (hq0 + g) * nsplit, nsplit, threadIdx.x & 63, M, L);
-        const float inv = 1.0f / L;
-        if (t < T) {
-            const f32x4 s = *reinterpret_cast<const f32x4*>(score + (hq0 + g) * spad + t);
+    const int t = t0 + 4 * threadIdx.x, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const long long at = (long long)bh * Tmax + t;
+    float before[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) w[j] = fmaf(exp2_raw(s[j] - M), inv, w[j]);
+    for (int j = 0; j < 4; ++j) before[j] = weights && t + j < T ? weights[at + j] : 0.0f;
+    f32x4 w = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int g0 = 0; g0 < G; g0 += kStatHeads) {
+        const int gn = min(G - g0, kStatHeads);
+        if (g0 > 0) __syncthreads();
+        for (int g = wave; g < gn; g += kThreads / 64) {
+            float M, L;
+            row_stats(ml + (hq0 + g0 + g) * nsplit, nsplit, lane, M, L);
+            if (lane == 0) stat[g] = make_float2(M, 1.0f / L);
+        }
+        __syncthreads();
+        if (t < T) {
+            const float* sp = score + (hq0 + g0) * spad + t;
+#pragma unroll 4
+            for (int g = 0; g < gn; ++g) {
+                const f32x4 s = *reinterpret_cast<const f32x4*>(sp + (long long)g * spad);
+                const float2 st = stat[g];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) w[j] = fmaf(exp2_raw(s[j] - st.x), st.y, w[j]);
+            }
         }
     }
-    const long long at = (long long)bh * Tmax + t;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-        if (t + j < T) sums[at + j] = (weights ? weights[at + j] : 0.0f) + w[j];
+        if (t + j < T) sums[at + j] = before[j] + w[j];
 }
 
 // ------------------------------------------------------------------------------- host side
@@ -984,21 +1001,21 @@ constexpr int kStreamRows = 16;          // prefix rows per kv head up to which 
 
 int divup(long long a, long long b) { return (int)((a + b - 1) / b); }
 
-int chunk_of(long long T, long long tiles, long long blocks) {
+int chunk_of(long long T, long long tiles, long long blocks, long long least) {
     const long long ns = blocks / tiles > 1 ? blocks / tiles : 1;
-    const long long c = divup(divup(T, ns), kMinChunk) * (long long)kMinChunk;
-    return (int)c;
+    return (int)(divup(divup(T, ns), least) * least);
 }
 // tokens per split of a sequence's own cache, and of the prefix
 int own_chunk(long long B, long long Hq, long long Hkv, long long T) {
-    return chunk_of(T, B * Hkv * divup(Hq / Hkv, 16), kBlocks);
+    return chunk_of(T, B * Hkv * divup(Hq / Hkv, 16), kBlocks, kMinChunk);
 }
 int prefix_wq(long long R) { return R <= kStreamRows ? 0 : R <= 64 ? 2 : 4; }   // 0: streaming
 int prefix_chunk(long long B, long long Hq, long long Hkv, long long P) {
     if (P == 0) return kMinChunk;
     const long long R = B * (Hq / Hkv);
     const int wq = prefix_wq(R);
-    return wq == 0 ? chunk_of(P, Hkv * divup(R, 16), kBlocks) : chunk_of(P, Hkv * divup(R, 32 * wq), kPrefixBlocks);
+    return wq == 0 ? chunk_of(P, Hkv * divup(R, 16), kBlocks, kMinChunk)
+                   : chunk_of(P, Hkv * divup(R, 32 * wq), kPrefixBlocks, kMinChunk);
 }
 
 long long parts_floats(long long heads, long long ns, long long D) { return heads * ns * (D + 2); }
@@ -1006,34 +1023,30 @@ long long parts_floats(long long heads, long long ns, long long D) { return head
 template <int BITS, int D>
 hipError_t shared(const KvSharedArgs& a, float* work, hipStream_t st) {
     const int G = a.Hq / a.Hkv;
-    StreamGrid g = {};
+    const long long heads = (long long)a.B * a.Hq, R = (long long)a.B * G;
+    const int wq = prefix_wq(R);
+    DecodeGrid g = {};
     g.P = a.P;
     g.Pmax = a.Pmax;
     g.Tmax = a.Tmax;
     g.pchunk = prefix_chunk(a.B, a.Hq, a.Hkv, a.P);
     g.psplit = divup(a.P, g.pchunk);
+    g.pblocks = (int)(8 * divup((long long)a.Hkv * g.psplit, 8) * (long long)divup(R, wq ? 32 * wq : 16));
     g.ochunk = own_chunk(a.B, a.Hq, a.Hkv, a.Tmax);
     g.osplit = divup(a.Tmax, g.ochunk);
     g.nsplit = g.psplit + g.osplit;
-    const long long heads = (long long)a.B * a.Hq, R = (long long)a.B * G;
     float* po = work;                                       // 16-byte aligned rows first
     float2* ml = reinterpret_cast<float2*>(work + heads * g.nsplit * D);
     const auto q = static_cast<const uint16_t*>(a.q);
-    const int bf16 = a.dtype == DT_BF16, wq = prefix_wq(R);
-    if (wq == 0) {
-        g.pblocks = a.Hkv * g.psplit * divup(R, 16);
-    } else if (g.psplit > 0) {
-        const dim3 grid((unsigned)(8 * divup((long long)a.Hkv * g.psplit, 8) * (long long)divup(R, 32 * wq)));
-        if (wq == 2)
-            hipLaunchKernelGGL((kv_prefix_kernel<BITS, D, 2>), grid, dim3(kThreads), 0, st, q, bf16, a.B, a.Hq, a.Hkv,
-                               a.prefix, a.P, a.Pmax, g.pchunk, g.psplit, g.nsplit, ml, po);
-        else
-            hipLaunchKernelGGL((kv_prefix_kernel<BITS, D, 4>), grid, dim3(kThreads), 0, st, q, bf16, a.B, a.Hq, a.Hkv,
-                               a.prefix, a.P, a.Pmax, g.pchunk, g.psplit, g.nsplit, ml, po);
-    }
-    const unsigned blocks = (unsigned)(g.pblocks + (long long)a.B * a.Hkv * divup(G, 16) * g.osplit);
-    hipLaunchKernelGGL((kv_stream_kernel<BITS, D, false>), dim3(blocks), dim3(kThreads), 0, st, q, bf16, a.B, a.Hq,
-                       a.Hkv, a.prefix, a.own, a.lens, g, ml, po, nullptr, 0);
+    const int bf16 = a.dtype == DT_BF16;
+    const dim3 grid((unsigned)(g.pblocks + (long long)a.B * a.Hkv * divup(G, 16) * g.osplit));
+#define W4A16_DECODE(WQ)                                                                                              \
+    hipLaunchKernelGGL((kv_decode_kernel<BITS, D, WQ, false>), grid, dim3(kThreads), 0, st, q, bf16, a.B, a.Hq, a.Hkv, \
+                       a.prefix, a.own, a.lens, g, ml, po, nullptr, 0)
+    if (wq == 0) W4A16_DECODE(0);
+    else if (wq == 2) W4A16_DECODE(2);
+    else W4A16_DECODE(4);
+#undef W4A16_DECODE
     hipLaunchKernelGGL((kv_merge_kernel<D>), dim3((unsigned)heads), dim3(kThreads), 0, st, ml, po, g.nsplit, bf16,
                        static_cast<uint16_t*>(a.out));
     return hipGetLastError();
@@ -1044,7 +1057,7 @@ int score_pad(long long Tmax) { return (int)((Tmax + 3) / 4 * 4); }
 template <int BITS, int D>
 hipError_t weights(const KvWeightsArgs& a, float* work, hipStream_t st) {
     const int G = a.Hq / a.Hkv;
-    StreamGrid g = {};
+    DecodeGrid g = {};
     g.Tmax = a.Tmax;
     g.ochunk = own_chunk(a.B, a.Hq, a.Hkv, a.Tmax);
     g.osplit = g.nsplit = divup(a.Tmax, g.ochunk);
@@ -1056,7 +1069,7 @@ hipError_t weights(const KvWeightsArgs& a, float* work, hipStream_t st) {
     float2* ml = reinterpret_cast<float2*>(po + heads * ns * D);
     const int bf16 = a.dtype == DT_BF16;
     const unsigned blocks = (unsigned)((long long)a.B * a.Hkv * divup(G, 16) * g.osplit);
-    hipLaunchKernelGGL((kv_stream_kernel<BITS, D, true>), dim3(blocks), dim3(kThreads), 0, st,
+    hipLaunchKernelGGL((kv_decode_kernel<BITS, D, 0, true>), dim3(blocks), dim3(kThreads), 0, st,
                        static_cast<const uint16_t*>(a.q), bf16, a.B, a.Hq, a.Hkv, KvCache{}, a.own, a.lens, g, ml, po,
                        score, spad);
     const int spans = divup(a.Tmax, kSpan);
