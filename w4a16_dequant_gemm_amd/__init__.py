@@ -56,21 +56,28 @@ def _stream() -> int:
 def _call(fn, what: str, device: torch.device, *args) -> None:
     """``fn(*args, stream)`` on ``device``, on the stream current there, whichever device is
     current; raises on a negative status."""
-    if device.index == torch.cuda.current_device():
-        check(fn(*args, torch.cuda.current_stream().cuda_stream), what)
-        return
-    with torch.cuda.device(device):
-        check(fn(*args, torch.cuda.current_stream().cuda_stream), what)
+    i = device.index
+    stream = torch._C._cuda_getCurrentRawStream(i)      # the handle alone, without a Stream object
+    if i == torch._C._cuda_getDevice():
+        status = fn(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, stream)
+    if status != OK:
+        raise W4A16Error(status, what)
 
 
 def _same_device(x: torch.Tensor, name: str, **others) -> None:
     """Every given tensor (None: absent) is a GPU tensor on the device of ``x``."""
+    dev = x.get_device()
     for other, t in others.items():
-        if t is not None and t.device != x.device:
+        if t is not None and t.get_device() != dev:
             raise ValueError(f"{other} must be on the device of {name}")
 
 
 def _need(t: torch.Tensor, name: str, dtype, ndim: int) -> None:
+    if isinstance(t, torch.Tensor) and t.dtype == dtype and t.dim() == ndim and t.is_cuda and t.is_contiguous():
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
@@ -561,9 +568,9 @@ def kv_attention_decode(q: torch.Tensor, kcache, vcache, T: int, bits: int = 8,
     return out
 
 
-def _need_heads(t: torch.Tensor, name: str, dtype) -> None:
-    """``t [T, H, D]``: a GPU tensor of adjacent heads (a row is ``H * D`` consecutive values);
-    rows may be further apart, as in a column block of a wider tensor."""
+def _need_heads(t: torch.Tensor, name: str, dtype) -> int:
+    """``t [T, H, D]``: a GPU tensor of adjacent heads (a row is ``H * D`` consecutive values); rows
+    may be further apart, as in a column block of a wider tensor.  Returns the rows' distance."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
@@ -572,8 +579,11 @@ def _need_heads(t: torch.Tensor, name: str, dtype) -> None:
         raise ValueError(f"{name} must be 3-D")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
-    if (t.shape[2] > 1 and t.stride(2) != 1) or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+    T, H, D = t.shape
+    st, sh, sd = t.stride()
+    if (D > 1 and sd != 1) or (H > 1 and sh != D):
         raise ValueError(f"the heads of {name} must be adjacent (strides [*, D, 1])")
+    return st if T > 1 else H * D          # (a single row's stride is arbitrary in torch)
 
 
 def attention_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
@@ -587,9 +597,7 @@ def attention_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
     Rows outside every sequence are neither read nor written: in an ``out`` of the caller's they
     keep what they held, in the returned tensor of a call without ``out`` they are undefined."""
     dt = _dtype_code(q)
-    _need_heads(q, "q", q.dtype)
-    _need_heads(k, "k", q.dtype)
-    _need_heads(v, "v", q.dtype)
+    sq, sk, sv = _need_heads(q, "q", q.dtype), _need_heads(k, "k", q.dtype), _need_heads(v, "v", q.dtype)
     _need(cu_seqlens, "cu_seqlens", torch.int32, 1)
     T, Hq, D = q.shape
     Hkv = k.shape[1]
@@ -604,41 +612,41 @@ def attention_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
         _need(out, "out", q.dtype, 3)
         if out.shape != q.shape:
             raise ValueError("out must be [T, Hq, D]")
-    # the stride of a single row is arbitrary in torch: the dense one then
-    sq, sk, sv = (t.stride(0) if T > 1 else t.shape[1] * D for t in (q, k, v))
     _call(lib().w4a16_attention_prompt, "w4a16_attention_prompt", q.device, q.data_ptr(), k.data_ptr(), v.data_ptr(),
           dt, T, cu_seqlens.shape[0] - 1, cu_seqlens.data_ptr(), Hq, Hkv, D, sq, sk, sv, out.data_ptr())
     return out
 
 
-def _need_cache(cache, name: str, bits: int, lead: int, D: int):
+def _need_cache(cache, name: str, bits: int, lead: int, D: int, like: torch.Tensor):
     """Checks ``(codes, scales, zeros)`` of a quantized cache with ``lead`` leading axes besides the
-    tokens'; returns the shape of its scales."""
-    if bits not in (8, 4):
-        raise ValueError("bits must be 8 or 4")
+    tokens', on the device of ``like``; returns the shape of its scales."""
     codes, scales, zeros = cache
     _need(codes, f"{name} codes", torch.int8 if bits == 8 else torch.int32, lead + 2)
     _need(scales, f"{name} scales", torch.float16, lead + 1)
-    if tuple(codes.shape) != (*scales.shape, D if bits == 8 else D // 8):
+    shape, cs = scales.shape, codes.shape
+    if cs[:-1] != shape or cs[-1] * (1 if bits == 8 else 8) != D:
         raise ValueError(f"{name} codes must be [..., {'D' if bits == 8 else 'D/8'}] over its scales' shape")
+    dev = like.get_device()
+    if codes.get_device() != dev or scales.get_device() != dev:
+        raise ValueError(f"{name} must be on the device of the other arguments")
     if bits == 4:
         if zeros is None:
             raise ValueError(f"{name} needs zeros for 4-bit codes")
         _need(zeros, f"{name} zeros", torch.float16, lead + 1)
-        if zeros.shape != scales.shape:
+        if zeros.shape != shape:
             raise ValueError(f"{name} zeros must match its scales")
-    return scales.shape
+        if zeros.get_device() != dev:
+            raise ValueError(f"{name} must be on the device of the other arguments")
+    return shape
 
 
-def _need_caches(k, v, names, bits: int, lead: int, D: int, like: torch.Tensor):
+def _need_caches(k, v, kname: str, vname: str, bits: int, lead: int, D: int, like: torch.Tensor):
     """A K and a V cache of one shape on the device of ``like``."""
-    shape = _need_cache(k, names[0], bits, lead, D)
-    if _need_cache(v, names[1], bits, lead, D) != shape:
-        raise ValueError(f"{names[0]} and {names[1]} must have the same shape")
-    for c, name in zip((k, v), names):
-        for t in c[:2 if bits == 8 else 3]:
-            if t.device != like.device:
-                raise ValueError(f"{name} must be on the device of the other arguments")
+    if bits != 8 and bits != 4:
+        raise ValueError("bits must be 8 or 4")
+    shape = _need_cache(k, kname, bits, lead, D, like)
+    if _need_cache(v, vname, bits, lead, D, like) != shape:
+        raise ValueError(f"{kname} and {vname} must have the same shape")
     return shape
 
 
@@ -704,8 +712,8 @@ def kv_attention_decode_shared(q: torch.Tensor, kprefix, vprefix, P: int, kcache
     _need(q, "q", q.dtype, 3)
     _need(lengths, "lengths", torch.int32, 1)
     B, Hq, D = q.shape
-    Bc, Hkv, Tmax = _need_caches(kcache, vcache, ("kcache", "vcache"), bits, 2, D, q)
-    Hp, Pmax = _need_caches(kprefix, vprefix, ("kprefix", "vprefix"), bits, 1, D, q)
+    Bc, Hkv, Tmax = _need_caches(kcache, vcache, "kcache", "vcache", bits, 2, D, q)
+    Hp, Pmax = _need_caches(kprefix, vprefix, "kprefix", "vprefix", bits, 1, D, q)
     if Bc != B or lengths.shape[0] != B or Hp != Hkv:
         raise ValueError("caches must be [B, Hkv, Tmax, ...], prefixes [Hkv, Pmax, ...] and lengths [B]")
     _same_device(q, "q", lengths=lengths)
@@ -736,7 +744,7 @@ def kv_attention_decode_weights(q: torch.Tensor, kcache, vcache, lengths: torch.
     _need(q, "q", q.dtype, 3)
     _need(lengths, "lengths", torch.int32, 1)
     B, Hq, D = q.shape
-    Bc, Hkv, Tmax = shape = _need_caches(kcache, vcache, ("kcache", "vcache"), bits, 2, D, q)
+    Bc, Hkv, Tmax = shape = _need_caches(kcache, vcache, "kcache", "vcache", bits, 2, D, q)
     if Bc != B or lengths.shape[0] != B:
         raise ValueError("caches must be [B, Hkv, Tmax, ...] and lengths [B]")
     if sums is None:
@@ -773,12 +781,12 @@ def kv_evict(kcache, vcache, weights: torch.Tensor, lengths: torch.Tensor, budge
     :func:`kv_evict_workspace` elements (0 for up to 8192 tokens)."""
     _need(weights, "weights", torch.float32, 3)
     _need(lengths, "lengths", torch.int32, 1)
-    if bits not in (8, 4):
+    if bits != 8 and bits != 4:
         raise ValueError("bits must be 8 or 4")
     if not isinstance(kcache[0], torch.Tensor) or kcache[0].dim() != 4:
         raise ValueError("kcache codes must be 4-D")
     D = kcache[0].shape[3] * (1 if bits == 8 else 8)
-    B, Hkv, Tmax = shape = _need_caches(kcache, vcache, ("kcache", "vcache"), bits, 2, D, weights)
+    B, Hkv, Tmax = shape = _need_caches(kcache, vcache, "kcache", "vcache", bits, 2, D, weights)
     if weights.shape != shape or lengths.shape[0] != B:
         raise ValueError("weights must be [B, Hkv, Tmax] and lengths [B]")
     _same_device(weights, "weights", lengths=lengths)
@@ -795,7 +803,7 @@ def kv_evict(kcache, vcache, weights: torch.Tensor, lengths: torch.Tensor, budge
         out = (new(kcache), new(vcache), torch.empty(room, dtype=torch.float32, device=weights.device),
                torch.empty_like(lengths), torch.empty((B, Hkv, budget), dtype=torch.int32, device=weights.device))
     ko, vo, wo, lo, kept = out
-    Bo, Ho, Tout = _need_caches(ko, vo, ("out kcache", "out vcache"), bits, 2, D, weights)
+    Bo, Ho, Tout = _need_caches(ko, vo, "out kcache", "out vcache", bits, 2, D, weights)
     _need(wo, "out weights", torch.float32, 3)
     _need(lo, "out lengths", torch.int32, 1)
     _need(kept, "out kept", torch.int32, 3)

@@ -38,10 +38,32 @@ __device__ __forceinline__ int lanes_below(unsigned long long mask) {
     return __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
 }
 
+// Inclusive sum over the lanes 0 .. l of a wave (row shifts, then the rows' totals onto the next ones).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int dpp_add(int v) {
+    return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
+}
+__device__ __forceinline__ int wave_scan(int v) {
+    v = dpp_add<0x111, 0xF>(v);                  // row_shr 1, 2, 4, 8
+    v = dpp_add<0x112, 0xF>(v);
+    v = dpp_add<0x114, 0xF>(v);
+    v = dpp_add<0x118, 0xF>(v);
+    v = dpp_add<0x142, 0xA>(v);                  // row_bcast 15 into rows 1 and 3
+    return dpp_add<0x143, 0xC>(v);               // row_bcast 31 into rows 2 and 3
+}
+__device__ __forceinline__ int last_lane(int v) { return __builtin_amdgcn_readlane(v, 63); }
+// The sum of sixteen values v[0 .. 15], and of those before index `upto`.
+__device__ __forceinline__ int sum16(const int* v, int upto, int& before) {
+    const int lane = threadIdx.x & 63;
+    const int s = wave_scan(lane < 16 ? v[lane] : 0);
+    before = upto > 0 ? __builtin_amdgcn_readlane(s, upto - 1) : 0;
+    return __builtin_amdgcn_readlane(s, 15);
+}
+
 struct SelectLds {
-    uint32_t hist[kBins * kCopies];
+    __attribute__((aligned(16))) uint32_t hist[2][kBins * kCopies];    // of this digit, and cleared for the next
     int sum[kSelWaves], before[kSelWaves];
-    int digit, rem;
+    int digit, rem, whole, at;
     int gt[kSelWaves], eq[kSelWaves];
 };
 
@@ -50,6 +72,11 @@ struct SelectLds {
 struct Threshold {
     uint32_t prefix, mask;
     int rem;
+    // every token that agrees so far is kept: no further digit is needed
+    __device__ __forceinline__ void close() {
+        prefix -= 1;                             // (rem > 0 tokens have that key or a larger one: not 0)
+        rem = 0;
+    }
 };
 
 // A batch's weights: token base + 512 wave + 64 j + lane in x[j]; a wave's tokens are consecutive.
@@ -64,62 +91,62 @@ __device__ __forceinline__ void load_batch(const float* __restrict__ w, int base
     }
 }
 
-__device__ __forceinline__ void clear_hist(SelectLds& s) {
-    for (int i = threadIdx.x; i < kBins * kCopies; i += kSelThreads) s.hist[i] = 0;
+__device__ __forceinline__ void clear_hist(SelectLds& s, int buf) {
+    u32x4* h = reinterpret_cast<u32x4*>(s.hist[buf]);
+    for (int i = threadIdx.x; i < kBins * kCopies / 4; i += kSelThreads) h[i] = u32x4{0, 0, 0, 0};
 }
-__device__ __forceinline__ void count_batch(SelectLds& s, const float x[kPer], int base, int old, const Threshold& th,
-                                            int level) {
+__device__ __forceinline__ void count_batch(SelectLds& s, int buf, const float x[kPer], int base, int old,
+                                            const Threshold& th, int level) {
     const uint32_t bins = level == 2 ? 1023u : 2047u;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
         const uint32_t k = order_key(x[j]);
         if (token(base, j) < old && (k & th.mask) == th.prefix)
-            atomicAdd(&s.hist[((k >> kShift[level]) & bins) * kCopies + (threadIdx.x & (kCopies - 1))], 1u);
+            atomicAdd(&s.hist[buf][((k >> kShift[level]) & bins) * kCopies + (threadIdx.x & (kCopies - 1))], 1u);
     }
 }
 // This thread's two digits, 2047 - 2 tid and 2046 - 2 tid.
-__device__ __forceinline__ int count_of(const SelectLds& s, int which) {
-    const uint32_t* h = s.hist + (kBins - 1 - 2 * (int)threadIdx.x - which) * kCopies;
-    return (int)(h[0] + h[1] + h[2] + h[3]);
+__device__ __forceinline__ void counts(const SelectLds& s, int buf, int& c0, int& c1) {
+    const u32x4* h = reinterpret_cast<const u32x4*>(s.hist[buf]) + (kBins - 2 - 2 * (int)threadIdx.x);
+    const u32x4 lo = h[0], hi = h[1];
+    c0 = (int)(hi.x + hi.y + hi.z + hi.w);
+    c1 = (int)(lo.x + lo.y + lo.z + lo.w);
 }
+static_assert(kCopies == 4, "a digit's copies are one 16-byte load");
 
 // The next digit of the threshold from the counts c0, c1 of this thread's two digits: the highest with
-// th.rem or more tokens at or above it.  p0, p1: the same counts in the chunks before this one; adds
-// how many of those are above the digit to `above` and returns how many are at it.
-__device__ __forceinline__ int next_digit(SelectLds& s, int c0, int c1, int p0, int p1, int level, Threshold& th,
-                                          int& above) {
-    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-    int inc = c0 + c1;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-        const int o = __shfl_up(inc, off, 64);
-        if (lane >= off) inc += o;
-    }
-    if (lane == 63) s.sum[wave] = inc;
+// th.rem or more tokens at or above it.  Returns whether all tokens at it are kept.
+__device__ __forceinline__ bool next_digit(SelectLds& s, int c0, int c1, int level, Threshold& th) {
+    const int tid = threadIdx.x, wave = tid >> 6;
+    int inc = wave_scan(c0 + c1), before;
+    if ((tid & 63) == 63) s.sum[wave] = inc;
     __syncthreads();
-    for (int i = 0; i < wave; ++i) inc += s.sum[i];
-    const int higher = inc - c0 - c1;                // tokens at this thread's higher digits' tail
+    sum16(s.sum, wave, before);
+    inc += before;
+    const int higher = inc - c0 - c1;                // tokens at the digits above this thread's
     if (higher < th.rem && inc >= th.rem) {
         const bool first = higher + c0 >= th.rem;
         s.digit = kBins - 1 - 2 * tid - (first ? 0 : 1);
         s.rem = th.rem - higher - (first ? 0 : c0);
+        s.whole = s.rem == (first ? c0 : c1);
     }
     __syncthreads();
-    const int d = s.digit, mine = kBins - 1 - 2 * tid;
-    int gt = (mine > d ? p0 : 0) + (mine - 1 > d ? p1 : 0);
-    const int eq = mine == d ? p0 : mine - 1 == d ? p1 : 0;
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) gt += __shfl_xor(gt, off, 64);
-    if (lane == 0) s.before[wave] = gt;
-    if (mine == d || mine - 1 == d) s.sum[0] = eq;   // (everyone is past reading the sums)
     th.rem = s.rem;
-    th.prefix |= (uint32_t)d << kShift[level];
+    th.prefix |= (uint32_t)s.digit << kShift[level];
     th.mask |= (level == 2 ? 1023u : 2047u) << kShift[level];
+    return s.whole != 0;
+}
+// Of the counts p0, p1 of this thread's two digits: the sum over the digits above the threshold's, and
+// the count at it.
+__device__ __forceinline__ int above_digit(SelectLds& s, int p0, int p1, int& at) {
+    const int tid = threadIdx.x, d = s.digit, mine = kBins - 1 - 2 * tid;
+    const int gt = last_lane(wave_scan((mine > d ? p0 : 0) + (mine - 1 > d ? p1 : 0)));
+    if ((tid & 63) == 0) s.before[tid >> 6] = gt;
+    if (mine == d || mine - 1 == d) s.at = mine == d ? p0 : p1;
     __syncthreads();
-    for (int i = 0; i < kSelWaves; ++i) above += s.before[i];
-    const int at = s.sum[0];
-    __syncthreads();
-    return at;
+    at = s.at;
+    int unused;
+    return sum16(s.before, 0, unused);
 }
 
 // Writes the kept tokens of one batch in order, from position `pos` on with `ties` tokens at the
@@ -146,16 +173,13 @@ __device__ __forceinline__ void write_batch(SelectLds& s, const float x[kPer], i
         s.eq[wave] = eq;
     }
     __syncthreads();
-    int p = pos, q = ties;                           // of this wave
-    for (int i = 0; i < kSelWaves; ++i) {
-        const int e = s.eq[i], g = s.gt[i] + min(max(kt.rem - ties, 0), e);
-        if (i < wave) {
-            p += g;
-            q += e;
-        }
-        pos += g;
-        ties += e;
-    }
+    // kept and tied tokens of the waves before this one, and of all
+    int eq_before, gt_before;
+    const int eq_all = sum16(s.eq, wave, eq_before), gt_all = sum16(s.gt, wave, gt_before);
+    const auto taken = [&](int e) { return min(max(kt.rem - ties, 0), e); };     // of the first e ties
+    int p = pos + gt_before + taken(eq_before), q = ties + eq_before;
+    pos += gt_all + taken(eq_all);
+    ties += eq_all;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
         const bool keep = (gtm[j] >> lane & 1) || ((eqm[j] >> lane & 1) && q + lanes_below(eqm[j]) < kt.rem);
@@ -198,13 +222,18 @@ __global__ __launch_bounds__(kSelThreads) void kv_select_kernel(const float* __r
     const int old = n <= budget ? 0 : n - recent;
     Threshold th = {0, 0, n <= budget ? 0 : budget - recent};
     if (th.rem > 0) {
-        int above = 0;
+        clear_hist(s, 0);
+        __syncthreads();
         for (int level = 0; level < 3; ++level) {
-            clear_hist(s);
+            count_batch(s, level & 1, x, 0, old, th, level);
+            if (level < 2) clear_hist(s, (level + 1) & 1);
             __syncthreads();
-            count_batch(s, x, 0, old, th, level);
-            __syncthreads();
-            next_digit(s, count_of(s, 0), count_of(s, 1), 0, 0, level, th, above);
+            int c0, c1;
+            counts(s, level & 1, c0, c1);
+            if (next_digit(s, c0, c1, level, th)) {
+                th.close();
+                break;
+            }
         }
     } else {
         th.prefix = 0xFFFFFFFFu;
@@ -242,6 +271,7 @@ __global__ __launch_bounds__(kSelThreads) void kv_select_chunk_kernel(
     if (LEVEL < 3 && (need == 0 || me >= live)) return;
     Threshold th = {0, 0, need};
     int above = 0, at = 0;
+    if constexpr (LEVEL < 3) clear_hist(s, 0);
     if constexpr (LEVEL > 0) {
         if (need > 0) {
             if (LEVEL > 1 && me < live) {
@@ -252,6 +282,7 @@ __global__ __launch_bounds__(kSelThreads) void kv_select_chunk_kernel(
                 th = {last->prefix, last->mask, last->rem};
             }
             int c0 = 0, c1 = 0, p0 = 0, p1 = 0;
+#pragma unroll 8
             for (int c = 0; c < live; ++c) {
                 const uint2 v = *reinterpret_cast<const uint2*>(all + c * kChunkWords + (LEVEL - 1) * kBins + 2 * tid);
                 c0 += (int)v.x;
@@ -259,7 +290,8 @@ __global__ __launch_bounds__(kSelThreads) void kv_select_chunk_kernel(
                 p0 += c < me ? (int)v.x : 0;
                 p1 += c < me ? (int)v.y : 0;
             }
-            at = next_digit(s, c0, c1, p0, p1, LEVEL - 1, th, above);
+            next_digit(s, c0, c1, LEVEL - 1, th);
+            above += above_digit(s, p0, p1, at);
             if (LEVEL < 3 && tid == 0) *state = {th.prefix, th.mask, th.rem, above};
         } else {
             th.prefix = 0xFFFFFFFFu;
@@ -267,15 +299,15 @@ __global__ __launch_bounds__(kSelThreads) void kv_select_chunk_kernel(
     }
     float x[kPer];
     if constexpr (LEVEL < 3) {
-        clear_hist(s);
-        __syncthreads();
         for (int base = lo; base < min(hi, old); base += kBatch) {
             load_batch(w, base, min(hi, old), x);
-            count_batch(s, x, base, min(hi, old), th, LEVEL);
+            if (base == lo) __syncthreads();             // (the cleared histogram)
+            count_batch(s, 0, x, base, min(hi, old), th, LEVEL);
         }
         __syncthreads();
-        *reinterpret_cast<uint2*>(own + LEVEL * kBins + 2 * tid) =
-            make_uint2((uint32_t)count_of(s, 0), (uint32_t)count_of(s, 1));
+        int c0, c1;
+        counts(s, 0, c0, c1);
+        *reinterpret_cast<uint2*>(own + LEVEL * kBins + 2 * tid) = make_uint2((uint32_t)c0, (uint32_t)c1);
     } else {
         float* wo = weights_out + bh * Tout;
         int* ko = kept + bh * budget;
