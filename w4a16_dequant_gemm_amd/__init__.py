@@ -617,35 +617,45 @@ def attention_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
     return out
 
 
-def _need_cache(cache, name: str, bits: int, lead: int, D: int, like: torch.Tensor):
+def _cache_shape(cache, name: str, bits: int, lead: int, D: int, dev: int):
     """Checks ``(codes, scales, zeros)`` of a quantized cache with ``lead`` leading axes besides the
-    tokens', on the device of ``like``; returns the shape of its scales."""
+    tokens', on device ``dev``; returns the shape of its scales."""
     codes, scales, zeros = cache
     _need(codes, f"{name} codes", torch.int8 if bits == 8 else torch.int32, lead + 2)
     _need(scales, f"{name} scales", torch.float16, lead + 1)
-    shape, cs = scales.shape, codes.shape
-    if cs[:-1] != shape or cs[-1] * (1 if bits == 8 else 8) != D:
+    shape = scales.shape
+    if codes.shape != (*shape, D if bits == 8 else D // 8):
         raise ValueError(f"{name} codes must be [..., {'D' if bits == 8 else 'D/8'}] over its scales' shape")
-    dev = like.get_device()
-    if codes.get_device() != dev or scales.get_device() != dev:
-        raise ValueError(f"{name} must be on the device of the other arguments")
     if bits == 4:
         if zeros is None:
             raise ValueError(f"{name} needs zeros for 4-bit codes")
         _need(zeros, f"{name} zeros", torch.float16, lead + 1)
         if zeros.shape != shape:
             raise ValueError(f"{name} zeros must match its scales")
-        if zeros.get_device() != dev:
+    for t in cache[:2 if bits == 8 else 3]:
+        if t.get_device() != dev:
             raise ValueError(f"{name} must be on the device of the other arguments")
     return shape
 
 
 def _need_caches(k, v, kname: str, vname: str, bits: int, lead: int, D: int, like: torch.Tensor):
-    """A K and a V cache of one shape on the device of ``like``."""
+    """A K and a V cache of one shape on the device of ``like``; returns the shape of their scales."""
     if bits != 8 and bits != 4:
         raise ValueError("bits must be 8 or 4")
-    shape = _need_cache(k, kname, bits, lead, D, like)
-    if _need_cache(v, vname, bits, lead, D, like) != shape:
+    dev = like.get_device()
+    (kc, ks, kz), (vc, vs, vz) = k, v
+    if bits == 8 and isinstance(kc, torch.Tensor) and isinstance(ks, torch.Tensor) and isinstance(
+            vc, torch.Tensor) and isinstance(vs, torch.Tensor):
+        # the usual case in one expression; anything else is looked at piece by piece below
+        shape = ks.shape
+        want = (*shape, D)
+        if (len(shape) == lead + 1 and kc.dtype == vc.dtype == torch.int8 and ks.dtype == vs.dtype == torch.float16
+                and vs.shape == shape and kc.shape == want and vc.shape == want
+                and dev == kc.get_device() == ks.get_device() == vc.get_device() == vs.get_device()
+                and kc.is_contiguous() and ks.is_contiguous() and vc.is_contiguous() and vs.is_contiguous()):
+            return shape
+    shape = _cache_shape(k, kname, bits, lead, D, dev)
+    if _cache_shape(v, vname, bits, lead, D, dev) != shape:
         raise ValueError(f"{kname} and {vname} must have the same shape")
     return shape
 
