@@ -27,10 +27,50 @@ namespace {
 constexpr int kRows = 128;      // query rows of a block
 constexpr int kKeys = 64;       // keys of a tile
 
-// The sequence of row tile `slot`.  Sequence b owns the slots first(b) = cu[b] / kRows + b and the
-// following ceil(length / kRows) - 1; first() grows by at least that many per sequence, so the
-// last b with first(b) <= slot is the only candidate.  64-way search, one load per level.
-__device__ __forceinline__ int find_sequence(const int* __restrict__ cu, int B, int T, int slot, int lane) {
+// The row tile that comes `rank`-th in order of work (tile j of a sequence has j + 1 times kRows keys,
+// less the last one's shortfall): late tiles of all sequences first, so that the long blocks do not
+// start last.  Lane b holds sequence b's tile count (B <= 64), F(j) = sum_b max(0, tiles_b - j) tiles
+// are numbered j or later; j is the largest with F(j) > rank, found by bisection over the counts, and
+// the sequences with more than j tiles follow in their order.  Returns false behind the last tile.
+__device__ __forceinline__ int lanes_sum(int v) {
+    v += __builtin_amdgcn_mov_dpp(v, 0xB1, 0xF, 0xF, true);      // quad_perm [1,0,3,2]
+    v += __builtin_amdgcn_mov_dpp(v, 0x4E, 0xF, 0xF, true);      // quad_perm [2,3,0,1]
+    v += __builtin_amdgcn_mov_dpp(v, 0x141, 0xF, 0xF, true);     // row_half_mirror
+    v += __builtin_amdgcn_mov_dpp(v, 0x140, 0xF, 0xF, true);     // row_mirror
+    return (__builtin_amdgcn_readlane(v, 0) + __builtin_amdgcn_readlane(v, 16)) +
+           (__builtin_amdgcn_readlane(v, 32) + __builtin_amdgcn_readlane(v, 48));
+}
+__device__ __forceinline__ bool ranked_tile(const int* __restrict__ cu, int B, int T, int rank, int lane, int& s0,
+                                            int& len, int& row0) {
+    int first = 0, n = 0;
+    if (lane < B) {
+        first = min(max(cu[lane], 0), T);
+        n = min(max(cu[lane + 1], first), T) - first;
+    }
+    const int tiles = (n + kRows - 1) / kRows;
+    if (lanes_sum(tiles) <= rank) return false;
+    int lo = 0, hi = T / kRows + 1;                 // F(lo) > rank >= F(hi)
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (lanes_sum(max(0, tiles - mid)) > rank) lo = mid;
+        else hi = mid;
+    }
+    int r = rank - lanes_sum(max(0, tiles - hi));   // among the sequences that have a tile lo
+    unsigned long long m = __builtin_amdgcn_ballot_w64(tiles > lo);
+    for (; r > 0; --r) m &= m - 1;
+    const int b = __builtin_ctzll(m);
+    s0 = __builtin_amdgcn_readlane(first, b);
+    len = __builtin_amdgcn_readlane(n, b);
+    row0 = lo * kRows;
+    return true;
+}
+
+// With more sequences, the sequence of row tile `slot`.  Sequence b owns the slots first(b) = cu[b] /
+// kRows + b and the following ceil(length / kRows) - 1; first() grows by at least that many per
+// sequence, so the last b with first(b) <= slot is the only candidate.  64-way search, one load per
+// level.  Returns false for a slot between two sequences.
+__device__ __forceinline__ bool slot_tile(const int* __restrict__ cu, int B, int T, int slot, int lane, int& s0,
+                                          int& len, int& row0) {
     int lo = 0, hi = B;
     while (hi - lo > 1) {
         const int step = (hi - lo + 63) >> 6;
@@ -41,7 +81,10 @@ __device__ __forceinline__ int find_sequence(const int* __restrict__ cu, int B, 
         lo += (n - 1) * step;
         hi = min(hi, lo + step);
     }
-    return lo;
+    s0 = __builtin_amdgcn_readfirstlane(min(max(cu[lo], 0), T));
+    len = __builtin_amdgcn_readfirstlane(min(max(cu[lo + 1], s0), T)) - s0;
+    row0 = (slot - (s0 / kRows + lo)) * kRows;
+    return row0 >= 0 && row0 < len;
 }
 
 // A tile's rows straight to LDS: instruction i of the wave fills 1 KB, lane l 16 bytes at 16 l, which
@@ -82,14 +125,12 @@ __global__ __launch_bounds__(256, 2) void attention_prompt_kernel(
 
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
     const int n = lane & 31, h = lane >> 5;
-    // late row tiles (the ones with most keys) first; heads vary fastest
-    const int head = blockIdx.x % Hq;
-    const int slot = tiles - 1 - blockIdx.x / Hq;
-    const int b = find_sequence(cu, B, T, slot, lane);
-    const int s0 = __builtin_amdgcn_readfirstlane(min(max(cu[b], 0), T));
-    const int len = __builtin_amdgcn_readfirstlane(min(max(cu[b + 1], s0), T)) - s0;
-    const int row0 = (slot - (s0 / kRows + b)) * kRows;
-    if (row0 < 0 || row0 >= len) return;            // a slot between two sequences
+    // the tiles with most keys first; heads vary fastest
+    const int head = blockIdx.x % Hq, tile = blockIdx.x / Hq;
+    int s0, len, row0;
+    if (!(B <= 64 ? ranked_tile(cu, B, T, tile, lane, s0, len, row0)
+                  : slot_tile(cu, B, T, tiles - 1 - tile, lane, s0, len, row0)))
+        return;
     const int kvh = head / (Hq / Hkv);
 
     const int ntiles = (min(row0 + kRows, len) + kKeys - 1) / kKeys;
