@@ -120,6 +120,50 @@ def test_bf16_queries_far_from_one(bits, qscale):
                     np.testing.assert_allclose(f64(out)[b, h], vv[s.argmax()], rtol=2.0 ** -7, atol=1e-6)
 
 
+@pytest.mark.parametrize("B,Hq,Hkv", [(4, 8, 2), (12, 8, 2), (40, 8, 2)])
+@pytest.mark.parametrize("bits", [8, 4])
+def test_bf16_queries_of_very_different_size(bits, B, Hq, Hkv):
+    """Rows that share a block, from 1e-30 to 1e6 in size: each keeps its bits (16, 48 and 160 rows
+    per kv head, one for each arrangement of the waves)."""
+    q, kp, vp, k, v = problem(B, Hq, Hkv, 128, 150, 9, bits, BF, seed=60)
+    size = torch.tensor([1e-30, 1.0, 1e-9, 1e6, 0.0, 1e-3, 3e4])[torch.arange(B * Hq) % 7].view(B, Hq, 1)
+    q = (q.cpu().float() * size).to(BF).cuda()
+    lens = [i % 10 for i in range(B)]
+    out = W4.kv_attention_decode_shared(q, kp, vp, 150, k, v, torch.tensor(lens, dtype=torch.int32, device="cuda"), bits)
+    torch.cuda.synchronize()
+    keep = (size.flatten() <= 1.0).view(B, Hq)                 # the large rows' scores differ by more than fp32 holds
+    assert torch.isfinite(out).all()
+    small = torch.where(keep[..., None].cuda(), q, torch.zeros_like(q))
+    same = W4.kv_attention_decode_shared(small, kp, vp, 150, k, v, torch.tensor(lens, dtype=torch.int32, device="cuda"), bits)
+    torch.cuda.synchronize()
+    check(same, small, kp, vp, 150, k, v, lens, bits)
+    # beside large rows a row's weights may differ by their fp16 roundings alone
+    a, b = f64(out)[keep.numpy()], f64(same)[keep.numpy()]
+    assert np.abs(a - b).max() <= 2.0 ** -7 * np.abs(b).max()
+
+
+@pytest.mark.parametrize("B,Hq,Hkv", [(4, 8, 2), (12, 8, 2), (40, 8, 2)])
+@pytest.mark.parametrize("dtype", [H, BF])
+def test_rows_without_numbers_leave_the_others_alone(B, Hq, Hkv, dtype):
+    """Unused places of a padded batch: NaN and infinities in some queries, the other rows as before."""
+    q, kp, vp, k, v = problem(B, Hq, Hkv, 64, 140, 9, 8, dtype, seed=61)
+    lt = torch.tensor([i % 10 for i in range(B)], dtype=torch.int32, device="cuda")
+    clean = W4.kv_attention_decode_shared(q, kp, vp, 140, k, v, lt, 8)
+    bad = q.clone()
+    bad[1] = float("nan")
+    bad[2, 3, 5] = float("inf")
+    bad[B - 1, 1] = -float("inf")
+    out = W4.kv_attention_decode_shared(bad, kp, vp, 140, k, v, lt, 8)
+    torch.cuda.synchronize()
+    ok = torch.ones((B, Hq), dtype=torch.bool)
+    ok[1] = False
+    ok[2, 3] = ok[B - 1, 1] = False
+    a, b = f64(out)[ok.numpy()], f64(clean)[ok.numpy()]
+    assert np.isfinite(a).all()
+    # the common factor of the bf16 rows may be another one: the same values, up to a rounding
+    assert np.abs(a - b).max() <= (0.0 if dtype == H else 2.0 ** -7 * np.abs(b).max())
+
+
 def test_zero_value_rows_beside_small_ones():
     """A row of zeros is stored with scale 1 beside values of 1e-3: the small rows keep their bits."""
     q, kp, vp, k, v = problem(2, 4, 2, 64, 200, 10, 8, BF, seed=53, vscale=1e-3)

@@ -16,9 +16,8 @@
 // along the tokens (WK = 4, few rows: each wave then has its own softmax state and the four are
 // joined at the end).  A token's scales stay out of the 16-bit operands: K's multiplies the fp32
 // score, V's the softmax weight before it is rounded to fp16.  bf16 queries are scaled by a power
-// of two per row (streaming: per 16 rows) so that their largest entry is in [2^14, 2^15) and become
-// fp16 exactly (8-bit significands; an entry below 2^-21 of the largest may lose bits, 2^-39 of that
-// largest one).
+// of two (query_exponent) and become fp16 exactly (8-bit significands; an entry far below its row's
+// largest may lose bits that are below 2^-21 of that one).
 // Rounded to 16 bits are only the weights p s_t (fp16, relative 2^-11, scaled so that the largest
 // s_t seen so far becomes 2^7 and small ones keep their bits) and the output.  Scores, maxima,
 // sums and outputs are fp32; splits are joined by a second launch.
@@ -58,6 +57,20 @@ __device__ __forceinline__ void swap_halves(float& a, float& b) {
     const int x = r[0], y = r[1];
     a = __builtin_bit_cast(float, x);
     b = __builtin_bit_cast(float, y);
+}
+
+// The power of two 2^e that a row of a bf16 query takes on its way to fp16, its largest entry being
+// mx, the largest of all rows top (0: nothing finite).  The common factor brings top into [2^14,
+// 2^15) and goes out of the scores with K's scales (cl); rows far below top, whose bits it would push
+// out of fp16, take a factor of their own, and their scores rowf.  Returns whether there are any.
+__device__ __forceinline__ float finite_or_zero(float x) { return x < __builtin_inff() ? x : 0.0f; }
+__device__ __forceinline__ bool query_exponent(float mx, float top, int& e, float& cl, float& rowf) {
+    const int e0 = top > 0.0f ? 15 - __builtin_amdgcn_frexp_expf(top) : 0;
+    const bool mixed = __builtin_amdgcn_ballot_w64(mx > 0.0f && mx < top * 3.814697265625e-6f) != 0;   // 2^-18
+    e = mixed && mx > 0.0f ? 15 - __builtin_amdgcn_frexp_expf(mx) : e0;
+    cl = ldexpf(cl, -e0);
+    rowf = ldexpf(1.0f, e0 - e);
+    return mixed;
 }
 
 // One set of caches as a block sees it: the rows of one (sequence and) kv head.
@@ -121,7 +134,8 @@ struct Attend {
 
         // the row's query as fp16, in the codes' order, times 2^e
         u32x4 qf[D / 16];
-        float cl;                                          // score scale: 2^9 log2(e) / sqrt(D) / 2^e
+        float cl, rowf = 1.0f;                             // score scale: 2^9 log2(e) / sqrt(D) / 2^e
+        bool mixed = false;                                // wave-uniform: the rows' factors differ
         {
             u32x4 raw[D / 16];
             const uint16_t* qp = q + head * D + 8 * h;
@@ -135,13 +149,14 @@ struct Attend {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         mx = fmaxf(mx, fmaxf(fabsf(bf2f(raw[s][i] & 0xFFFFu)), fabsf(bf2f(raw[s][i] >> 16))));
-                // one factor for all rows of the block: it goes into K's scales
-                mx = wave_max(mx);
-                if (lane == 0) lds.m[wave][0] = mx;
+                // one factor for all rows of the block, which goes into K's scales
+                mx = finite_or_zero(max_halves(mx));
+                const float wave_mx = wave_max(mx);
+                if (lane == 0) lds.m[wave][0] = wave_mx;
                 __syncthreads();
-                mx = fmaxf(fmaxf(lds.m[0][0], lds.m[1][0]), fmaxf(lds.m[2][0], lds.m[3][0]));
-                const int e = mx > 0.0f ? 15 - __builtin_amdgcn_frexp_expf(mx) : 0;
-                cl = ldexpf(cl, -e);
+                const float top = fmaxf(fmaxf(lds.m[0][0], lds.m[1][0]), fmaxf(lds.m[2][0], lds.m[3][0]));
+                int e;
+                mixed = query_exponent(mx, top, e, cl, rowf);
 #pragma unroll
                 for (int s = 0; s < D / 16; ++s)
 #pragma unroll
@@ -260,6 +275,12 @@ struct Attend {
                     const u32x4 a = *reinterpret_cast<const u32x4*>(K + r * D + 8 * swz_k<D>(r, 2 * s + h));
                     S[b] = mfma<DT_F16>(a, qf[s], S[b]);
                 }
+            }
+            if (mixed) {
+#pragma unroll
+                for (int b = 0; b < KB; ++b)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) S[b][e] *= rowf;
             }
             // exponents: the score times K's scale and the row's factor, minus the reference
             float mx = NEG;
@@ -554,7 +575,7 @@ struct Stream {
 
         // the row's query as fp16 times 2^e, in the order of the codes, and its sum
         u32x4 qf[QS];
-        float cl, qsum = 0.0f;                             // score scale; -2^-24 sum of the fp16 query
+        float cl, qsum = 0.0f, rowf = 1.0f;                // score scale; -2^-24 sum of the fp16 query
         {
             const uint16_t* qp = q + head * D + KQ * qd;
 #pragma unroll
@@ -568,9 +589,10 @@ struct Stream {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         mx = fmaxf(mx, fmaxf(fabsf(bf2f(qf[s][i] & 0xFFFFu)), fabsf(bf2f(qf[s][i] >> 16))));
-                mx = wave_max(mx);                         // one factor for all rows: it goes into K's scales
-                const int e = mx > 0.0f ? 15 - __builtin_amdgcn_frexp_expf(mx) : 0;
-                cl = ldexpf(cl, -e);
+                // one factor for all rows of the tile, which goes into K's scales
+                mx = finite_or_zero(across_quarters(mx, [](float a, float b) { return fmaxf(a, b); }));
+                int e;
+                query_exponent(mx, wave_max(mx), e, cl, rowf);
 #pragma unroll
                 for (int s = 0; s < QS; ++s)
 #pragma unroll
@@ -664,7 +686,7 @@ struct Stream {
             const int tok0 = t0 + t * KT;
             float mt = NEG;
 #pragma unroll
-            for (int s = 0; s < NS; ++s) S[s] = S[s] * *reinterpret_cast<const f32x4*>(&L.ks[16 * s + 4 * qd]);
+            for (int s = 0; s < NS; ++s) S[s] = S[s] * (*reinterpret_cast<const f32x4*>(&L.ks[16 * s + 4 * qd]) * rowf);
             if (tok0 + KT > t1) {
                 const int left = t1 - tok0 - 4 * qd;
 #pragma unroll
@@ -834,8 +856,8 @@ template <int BITS, int D>
 struct PrefixKind<BITS, D, 0> {
     using type = Stream<BITS, D, false>;
 };
-template <int BITS, int D, int WQ, bool SCORES>
-__global__ __launch_bounds__(kThreads, 2) void kv_decode_kernel(const uint16_t* __restrict__ q, int bf16, int B, int Hq,
+template <int BITS, int D, int WQ, bool SCORES>    // (streaming alone: three blocks a CU)
+__global__ __launch_bounds__(kThreads, WQ == 0 ? 3 : 2) void kv_decode_kernel(const uint16_t* __restrict__ q, int bf16, int B, int Hq,
                                                                 int Hkv, KvCache prefix, KvCache own,
                                                                 const int* __restrict__ lens, DecodeGrid g,
                                                                 float2* __restrict__ ml, float* __restrict__ po,
