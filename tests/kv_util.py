@@ -6,16 +6,14 @@ Bound on an output element.  With u the rounding of the output type (fp16 2^-11,
 * a softmax weight times V's scale is rounded once to fp16: relative 2^-11 of it, or, where it is
   below fp16's normal range, an absolute 2^-25 in units in which the largest scale is 2^7, that is
   2^-32 smax per token, times the largest code cmax;
-* the weight itself carries the fp32 error of its score, which may be summed as q . u - z sum(q) on
-  unsigned codes u: (D + 8) 2^-24 sum_d |q_d| (|k_d| + |z| s) / sqrt(D) (z = 128 for 8-bit codes), and
+* the weight itself carries the fp32 error of its score, (D + 8) 2^-24 sum_d |q_d k_d| / sqrt(D), and
   32 * 2^-24 of exponential, sums and joining the splits, twice (the row's normalization has the
-  error of its weights): e = 2 ((D + 8) max_t sum |q| (|k| + |z| s) / sqrt(D) + 32) 2^-24;
-* the output's sum runs in fp32 over products of 16 tokens or more, on unsigned codes likewise:
-  (n / 16 + 40) 2^-24 sum_t p_t (|v_t| + |z_t| s_t);
+  error of its weights): e = 2 ((D + 8) max_t sum |q k| / sqrt(D) + 32) 2^-24;
+* the output's sum runs in fp32 over products of 16 tokens or more: (n / 16 + 40) 2^-24 sum p |v|;
 * the output is rounded once (below fp16's normal range by 2^-25 at most):
 
-    |out - ref| <= u |ref| + (1 + u) ((2^-11 + e) sum p |v| + (n / 16 + 40) 2^-24 sum p (|v| + |z| s))
-                   + n 2^-32 smax cmax + 2^-25 [fp16].
+    |out - ref| <= u |ref| + (1 + u) (2^-11 + e + (n / 16 + 40) 2^-24) sum p |v| + n 2^-32 smax cmax
+                   + 2^-25 [fp16].
 
 An accumulated weight has no 16-bit rounding: |sum - ref| <= e sum_h p + 4 * 2^-24 |ref|.
 """
@@ -59,22 +57,15 @@ def cmax(cache, bits):
     return 127.0 if bits == 8 else 15.0 + float(cache[2].float().abs().max())
 
 
-def offsets(cache, bits):
-    """``|z| s`` of every row, fp64 ``[..., T]``: what unsigned codes carry besides the value."""
-    return f64(cache[1]) * (128.0 if bits == 8 else np.abs(f64(cache[2])))
-
-
-def attend(q, k, v, kz=0.0, vz=0.0):
-    """``(out, weights, (sum p |v|, sum p (|v| + vz)), max sum |q| (|k| + kz) / sqrt(D))`` of queries
-    ``[R, D]`` over ``k, v [n, D]`` with row offsets ``kz, vz [n]``."""
-    D, n = q.shape[1], k.shape[0]
-    if n == 0:
-        return np.zeros_like(q), np.zeros((q.shape[0], 0)), (np.zeros_like(q), np.zeros_like(q)), 0.0
-    kz, vz = (np.broadcast_to(z, (n,))[:, None] for z in (kz, vz))
+def attend(q, k, v):
+    """``(out, weights, sum p |v|, max sum |q k| / sqrt(D))`` of queries ``[R, D]`` over ``k, v [n, D]``."""
+    D = q.shape[1]
+    if k.shape[0] == 0:
+        return np.zeros_like(q), np.zeros((q.shape[0], 0)), np.zeros_like(q), 0.0
     s = q @ k.T / np.sqrt(D)
     p = np.exp(s - s.max(1, keepdims=True))
     p /= p.sum(1, keepdims=True)
-    return p @ v, p, (p @ np.abs(v), p @ (np.abs(v) + vz)), float((np.abs(q) @ (np.abs(k) + kz).T).max() / np.sqrt(D))
+    return p @ v, p, p @ np.abs(v), float((np.abs(q) @ np.abs(k).T).max() / np.sqrt(D))
 
 
 def weight_error(D, qk):
@@ -83,8 +74,7 @@ def weight_error(D, qk):
 
 def check_out(got, ref, mag, dtype, e, n, smax, c):
     u = U[dtype]
-    tol = u * np.abs(ref) + (1 + u) * ((2.0 ** -11 + e) * mag[0] + (n / 16 + 40) * 2.0 ** -24 * mag[1])
-    tol = tol + n * 2.0 ** -32 * smax * c
+    tol = u * np.abs(ref) + (1 + u) * (2.0 ** -11 + e + (n / 16 + 40) * 2.0 ** -24) * mag + n * 2.0 ** -32 * smax * c
     if dtype == torch.float16:
         tol = tol + 2.0 ** -25
     assert np.all(np.isfinite(got))

@@ -9,7 +9,7 @@ import pytest
 import torch
 
 import w4a16_dequant_gemm_amd as W4
-from tests.kv_util import attend, check_out, cmax, f64, make_cache, offsets, rows, weight_error
+from tests.kv_util import attend, check_out, cmax, f64, make_cache, rows, weight_error
 
 pytestmark = pytest.mark.gpu
 H, BF = torch.float16, torch.bfloat16
@@ -195,13 +195,12 @@ def test_prompt_decode_evict_decode(bits):
         qd = torch.randn((B, Hq, D), generator=g).to(dtype).cuda()
         o, w = W4.kv_attention_decode_weights(qd, kc, vc, lt, weights, bits)
         K, V = rows(kc, bits), rows(vc, bits)
-        KZ, VZ = offsets(kc, bits), offsets(vc, bits)
         ps = []
         for b in range(B):
             n = int(lt[b])
             for hk in range(Hkv):
                 hs = slice(hk * G, hk * G + G)
-                ref, p, mag, qk = attend(f64(qd)[b, hs], K[b, hk, :n], V[b, hk, :n], KZ[b, hk, :n], VZ[b, hk, :n])
+                ref, p, mag, qk = attend(f64(qd)[b, hs], K[b, hk, :n], V[b, hk, :n])
                 check_out(f64(o)[b, hs], ref, mag, dtype, weight_error(D, qk), n, f64(vc[1])[b, :, :n].max(),
                           cmax((None, None, vc[2][b, :, :n] if vc[2] is not None else None), bits))
                 ps.append((b, hk, n, p.sum(0)))

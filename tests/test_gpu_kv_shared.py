@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import w4a16_dequant_gemm_amd as W4
-from tests.kv_util import attend, check_out, cmax, f64, make_cache, offsets, rows, spoil, weight_error
+from tests.kv_util import attend, check_out, cmax, f64, make_cache, rows, spoil, weight_error
 
 pytestmark = pytest.mark.gpu
 H, BF = torch.float16, torch.bfloat16
@@ -36,7 +36,6 @@ def check(out, q, kp, vp, P, k, v, lens, bits):
     Hkv = kp[1].shape[0]
     G = Hq // Hkv
     KP, VP, K, V = (rows(c, bits) for c in (kp, vp, k, v))
-    KPZ, VPZ, KZ, VZ = (offsets(c, bits) for c in (kp, vp, k, v))
     got, qd = f64(out), f64(q)
     smax = max([float(vp[1][:, :P].float().max()) if P else 0.0] +
                [float(v[1][b, :, :n].float().max()) for b, n in enumerate(lens) if n])
@@ -48,8 +47,7 @@ def check(out, q, kp, vp, P, k, v, lens, bits):
             kk = np.concatenate([KP[hk, :P], K[b, hk, :n]])
             vv = np.concatenate([VP[hk, :P], V[b, hk, :n]])
             hs = slice(hk * G, (hk + 1) * G)
-            ref, _, mag, qk = attend(qd[b, hs], kk, vv, np.concatenate([KPZ[hk, :P], KZ[b, hk, :n]]),
-                                     np.concatenate([VPZ[hk, :P], VZ[b, hk, :n]]))
+            ref, _, mag, qk = attend(qd[b, hs], kk, vv)
             check_out(got[b, hs], ref, mag, q.dtype, weight_error(D, qk), P + n, smax, c)
 
 
@@ -61,7 +59,9 @@ CASES = [
     (9, 8, 1, 64, 1000, [7 * i for i in range(9)], 64, 8, BF), (33, 2, 2, 128, 129, [i % 5 for i in range(33)], 4, 4, H),
     (20, 8, 1, 128, 700, [i for i in range(20)], 32, 8, H), (2, 40, 1, 64, 90, [100, 3], 100, 8, H),
     (3, 40, 1, 128, 20, [0, 260, 40], 300, 4, BF), (65, 1, 1, 64, 2100, [1] * 65, 1, 4, H),
-    (2, 2, 1, 128, 5000, [4000, 1], 4100, 8, H), (1, 3, 3, 128, 513, [600], 640, 4, H)]
+    (2, 2, 1, 128, 5000, [4000, 1], 4100, 8, H), (1, 3, 3, 128, 513, [600], 640, 4, H),
+    (5, 8, 2, 64, 127, [3, 0, 65, 64, 1], 70, 4, BF), (12, 4, 1, 64, 191, [i for i in range(12)], 16, 8, H),
+    (64, 1, 1, 64, 320, [0] * 64, 1, 4, H), (16, 1, 1, 128, 64, [5] * 16, 5, 8, BF), (17, 1, 1, 128, 192, [5] * 17, 5, 4, BF)]
 
 
 @pytest.mark.parametrize("B,Hq,Hkv,D,P,lens,Tmax,bits,dtype", CASES)

@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import w4a16_dequant_gemm_amd as W4
-from tests.kv_util import attend, check_out, cmax, f64, make_cache, offsets, rows, spoil, weight_error
+from tests.kv_util import attend, check_out, cmax, f64, make_cache, rows, spoil, weight_error
 
 pytestmark = pytest.mark.gpu
 H, BF = torch.float16, torch.bfloat16
@@ -33,12 +33,11 @@ def check(out, sums, q, k, v, before, lens, bits):
     B, Hq, D = q.shape
     Hkv = k[1].shape[1]
     G = Hq // Hkv
-    KZ, VZ = offsets(k, bits), offsets(v, bits)
     K, V, got, qd, s, w0 = rows(k, bits), rows(v, bits), f64(out), f64(q), f64(sums), f64(before)
     for b, n in enumerate(lens):
         for hk in range(Hkv):
             hs = slice(hk * G, (hk + 1) * G)
-            ref, p, mag, qk = attend(qd[b, hs], K[b, hk, :n], V[b, hk, :n], KZ[b, hk, :n], VZ[b, hk, :n])
+            ref, p, mag, qk = attend(qd[b, hs], K[b, hk, :n], V[b, hk, :n])
             e = weight_error(D, qk)
             if n:
                 check_out(got[b, hs], ref, mag, q.dtype, e, n, f64(v[1])[b, :, :n].max(),

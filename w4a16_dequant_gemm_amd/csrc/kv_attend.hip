@@ -43,12 +43,13 @@ __device__ __forceinline__ void codes_int8(uint32_t w, uint32_t out[2]) {
     out[0] = as_u(__builtin_elementwise_fma(as_h2(perm(0u, b, 0x0C010C00u)), both(32768.0f), both(-0.25f)));
     out[1] = as_u(__builtin_elementwise_fma(as_h2(perm(0u, b, 0x0C030C02u)), both(32768.0f), both(-0.25f)));
 }
-__device__ __forceinline__ void codes_int4(uint32_t w, f16x2 z9, uint32_t out[4]) {      // z9 = -z 2^-9
+__device__ __forceinline__ void codes_int4(uint32_t w, const u32x4& z9, uint32_t out[4]) {    // z9: -z 2^-9 of each
     unpack_mask_f16(w, out);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        out[i] = as_u(__builtin_elementwise_fma(as_h2(out[i]), both(i & 1 ? 2048.0f : 32768.0f), z9));
+        out[i] = as_u(__builtin_elementwise_fma(as_h2(out[i]), both(i & 1 ? 2048.0f : 32768.0f), as_h2(z9[i])));
 }
+__device__ __forceinline__ u32x4 same_zero(uint32_t pair) { return u32x4{pair, pair, pair, pair}; }
 
 // the lanes 32 .. 63 of a and the lanes 0 .. 31 of b trade places
 __device__ __forceinline__ void swap_halves(float& a, float& b) {
@@ -232,7 +233,7 @@ struct Attend {
                                 codes_int8(w[2 * j + 1], d + 2);
                             } else {
                                 const _Float16 z = __builtin_bit_cast(_Float16, kv ? pvz[i] : pkz[i]);
-                                codes_int4(w[j], f16x2{z, z} * both(-0.001953125f), d);
+                                codes_int4(w[j], same_zero(as_u(f16x2{z, z} * both(-0.001953125f))), d);
                             }
                             const int ch = OUT * pc + j;
                             *reinterpret_cast<u32x4*>(dst + 8 * (kv ? swz_v<D>(r, ch) : swz_k<D>(r, ch))) =
@@ -479,15 +480,13 @@ __device__ __forceinline__ float across_quarters(float x, Op op) {
 //     (32 for the shortest rows) of key l % 16's row, so a load covers whole cache lines, and the
 //     query's fragment is loaded in the same order.
 //   V's codes are stored to LDS as they are and read back transposed (8- or 4-bit).
-//   A code u (int8: c + 128) becomes the fp16 subnormal u 2^-24 by masks or byte permutes alone; the
-//     matrix cores multiply subnormals exactly.  The zero point (int8: 128) is taken out of the fp32
-//     sums: S starts at -z sum(q) 2^-24, and sum(p z) comes out of one more product, with the same
-//     rounded p, and is subtracted from O at the end.
-//   4-bit: two of the four masks leave 16 u; the query entries (K) and the weights (V, through the
-//     token's scale) that meet them are divided by 16.
-// Weights p s_t enter the second product times VNORM / vcap, vcap the largest V scale so far, and the
-// running maximum may lag by LAG, so that they stay below 2^15; an fp16 subnormal among them is
-// below 2^-14 of that, so its rounding adds at most 2^-32 vcap.
+//   Codes become exact normal fp16 values with their zero point taken out (codes_int8 / codes_int4):
+//     subnormals u 2^-24 would do without the multiply-add, but the matrix cores align a product by its
+//     operands' exponents, a subnormal's being 2^-14, and drop what falls below: with 4-bit codes that
+//     left sums off by 2^-15 of sum(p z), more than the output's rounding.
+// Weights p s_t enter the second product times 128 / vcap, vcap the largest V scale so far, and the
+// running maximum may lag by 8, so that they stay below 2^15; an fp16 subnormal among them is below
+// 2^-14 of that, so its rounding adds at most 2^-32 vcap.
 template <int BITS, int D, bool SCORES>
 struct Stream {
     static constexpr int KT = BITS == 8 && D == 128 ? 32 : 64;   // tokens of a tile
@@ -499,14 +498,13 @@ struct Stream {
     static constexpr int VL = KT * RB / 1024 > 0 ? KT * RB / 1024 : 1;   // V: 16-byte loads per lane
     static constexpr int VP = RB / 16;                           // 16-byte pieces of a row
     static constexpr int QS = D / 32;                            // k-steps of the first product
-    static constexpr float LAG = BITS == 8 ? 8.0f : 4.0f;
-    static constexpr float VNORM = BITS == 8 ? 128.0f : 2048.0f;
+    static constexpr float LAG = 8.0f, VNORM = 128.0f;
     static_assert(KT * RB % 1024 == 0, "whole loads");
 
     struct alignas(16) WaveLds {
         unsigned char v[KT * RB];
-        float ks[KT], vs[KT], kz[BITS == 4 ? KT : 1];
-        _Float16 vz[BITS == 4 ? KT : 4];
+        float ks[KT], vs[KT];
+        _Float16 kz[BITS == 4 ? KT : 4], vz[BITS == 4 ? KT : 4];     // -z 2^-9
     };
     union Lds {
         WaveLds w[4];
@@ -573,15 +571,15 @@ struct Stream {
         if (wave < tiles) load(wave);
         __builtin_amdgcn_sched_barrier(0);
 
-        // the row's query as fp16 times 2^e, in the order of the codes, and its sum
+        // the row's query as fp16 times 2^e, in the order of the codes
         u32x4 qf[QS];
-        float cl, qsum = 0.0f, rowf = 1.0f;                // score scale; -2^-24 sum of the fp16 query
+        float cl, rowf = 1.0f;                             // score scale: 2^9 log2(e) / sqrt(D) / 2^e
         {
             const uint16_t* qp = q + head * D + KQ * qd;
 #pragma unroll
             for (int s = 0; s < QS; ++s)
                 qf[s] = *reinterpret_cast<const u32x4*>(qp + 8 * s % KQ + 4 * KQ * (8 * s / KQ));
-            cl = 1.4426950408889634f * 16777216.0f / sqrtf((float)D);
+            cl = 1.4426950408889634f * kCodeUnit / sqrtf((float)D);
             if (bf16) {
                 float mx = 0.0f;
 #pragma unroll
@@ -601,22 +599,18 @@ struct Stream {
             }
 #pragma unroll
             for (int s = 0; s < QS; ++s) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) qsum += pair_sum<DT_F16>(qf[s][i]);
                 if constexpr (BITS == 4) {
                     uint32_t o[4];
                     permute_x8(qf[s].x, qf[s].y, qf[s].z, qf[s].w, o);
-                    const f16x2 sixteenth = {(_Float16)0.0625f, (_Float16)0.0625f};
-                    qf[s] = u32x4{o[0], as_u(as_h2(o[1]) * sixteenth), o[2], as_u(as_h2(o[3]) * sixteenth)};
+                    qf[s] = u32x4{o[0], o[1], o[2], o[3]};
                 }
             }
-            qsum = across_quarters(qsum, [](float a, float b) { return a + b; }) * -5.9604644775390625e-8f;
         }
 
         constexpr int OT = D / 16;
-        f32x4 o[OT], oz = {0.0f, 0.0f, 0.0f, 0.0f};
+        f32x4 o[OT];
 #pragma unroll
-        for (int i = 0; i < OT; ++i) o[i] = oz;
+        for (int i = 0; i < OT; ++i) o[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         const float NEG = -__builtin_inff();
         float m = NEG, l = 0.0f;                           // base-2 domain
         float vcap = 5.9604644775390625e-8f;               // fp16's smallest
@@ -637,48 +631,41 @@ struct Stream {
                 for (int i = 0; i < OT; ++i)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) o[i][e] *= f;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) oz[e] *= f;
             }
             const float vinv = VNORM / vcap;
             if constexpr (KT == 64) {
                 L.ks[lane] = h2f(pk) * cl;
-                L.vs[lane] = BITS == 4 && (lane & 2) ? vsc * (vinv * 0.0625f) : vsc * vinv;
+                L.vs[lane] = vsc * vinv;
             } else {
                 (lane < 32 ? L.ks : L.vs)[lane & 31] = lane < 32 ? h2f(pk) * cl : vsc * vinv;
             }
             if constexpr (BITS == 4) {
-                L.kz[lane] = h2f(pkz);
-                const _Float16 z = __builtin_bit_cast(_Float16, pvz);
-                L.vz[lane] = lane & 2 ? z * (_Float16)16.0f : z;
+                L.kz[lane] = __builtin_bit_cast(_Float16, pkz) * (_Float16)-0.001953125f;
+                L.vz[lane] = __builtin_bit_cast(_Float16, pvz) * (_Float16)-0.001953125f;
             }
             wave_lds_fence();
 
-            // S = q . u - z sum(q), in units of 2^-24
             f32x4 S[NS];
 #pragma unroll
             for (int s = 0; s < NS; ++s) {
-                if constexpr (BITS == 8) {
-                    const float b = 128.0f * qsum;
-                    S[s] = f32x4{b, b, b, b};
-                } else {
-                    S[s] = *reinterpret_cast<const f32x4*>(&L.kz[16 * s + 4 * qd]) * qsum;
+                S[s] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                u32x4 z = {0, 0, 0, 0};
+                if constexpr (BITS == 4) {
+                    const _Float16 zk = L.kz[16 * s + n];
+                    z = same_zero(as_u(f16x2{zk, zk}));
                 }
 #pragma unroll
                 for (int k = 0; k < QS; ++k) {
-                    u32x4 a;
+                    uint32_t d[4];
                     if constexpr (BITS == 8) {
                         const int at = s * KW + 2 * k;
-                        const uint32_t x = kr[at / 4][at % 4] ^ 0x80808080u, y = kr[at / 4][at % 4 + 1] ^ 0x80808080u;
-                        a = u32x4{perm(0u, x, 0x0C010C00u), perm(0u, x, 0x0C030C02u), perm(0u, y, 0x0C010C00u),
-                                  perm(0u, y, 0x0C030C02u)};
+                        codes_int8(kr[at / 4][at % 4], d);
+                        codes_int8(kr[at / 4][at % 4 + 1], d + 2);
                     } else {
                         const int at = s * KW + k;
-                        uint32_t d[4];
-                        unpack_mask_f16(kr[at / 4][at % 4], d);
-                        a = u32x4{d[0], d[1], d[2], d[3]};
+                        codes_int4(kr[at / 4][at % 4], z, d);
                     }
-                    S[s] = mfma16(a, qf[k], S[s]);
+                    S[s] = mfma16(u32x4{d[0], d[1], d[2], d[3]}, qf[k], S[s]);
                 }
             }
             if (t + 4 < tiles) load(t + 4);
@@ -718,8 +705,6 @@ struct Stream {
                 for (int i = 0; i < OT; ++i)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) o[i][e] *= f;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) oz[e] *= f;
             }
             const float ms = m == NEG ? 0.0f : m;          // a row with nothing yet: every weight is 0
             u32x4 P[NS / 2];
@@ -736,19 +721,15 @@ struct Stream {
                 P[s / 2][2 * (s % 2)] = pack2<DT_F16>(p[0], p[1]);
                 P[s / 2][2 * (s % 2) + 1] = pack2<DT_F16>(p[2], p[3]);
             }
-            // O += V^T P^T with raw codes, oz += z P
+            // O += V^T P^T; 4-bit: the tokens' zero points in the order of the fragment
+            u32x4 z[NS / 2];
 #pragma unroll
-            for (int k = 0; k < NS / 2; ++k) {
-                u32x4 z;
-                if constexpr (BITS == 8) {
-                    z = u32x4{0x58005800u, 0x58005800u, 0x58005800u, 0x58005800u};       // 128
-                } else {
+            for (int k = 0; k < NS / 2; ++k)
+                if constexpr (BITS == 4) {
                     const u32x2 z0 = *reinterpret_cast<const u32x2*>(&L.vz[32 * k + 4 * qd]);
                     const u32x2 z1 = *reinterpret_cast<const u32x2*>(&L.vz[32 * k + 16 + 4 * qd]);
-                    z = u32x4{z0.x, z0.y, z1.x, z1.y};
+                    z[k] = u32x4{z0.x, z0.y, z1.x, z1.y};
                 }
-                oz = mfma16(z, P[k], oz);
-            }
 #pragma unroll
             for (int i = 0; i < OT; ++i) {
                 if constexpr (BITS == 8) {
@@ -756,12 +737,11 @@ struct Stream {
                     for (int k = 0; k < NS / 2; ++k) {
                         const int r = n >> 1;                                      // row of the lane pair
                         const int tok = 32 * k + 4 * qd + (r & 3) + 16 * (r >> 2);
-                        u32x2 w = lds_read_tr_codes<8>(L.v + tok * RB + 16 * vpiece(tok, i) + 8 * (n & 1));
-                        w.x ^= 0x80808080u;
-                        w.y ^= 0x80808080u;
-                        o[i] = mfma16(u32x4{perm(0u, w.x, 0x0C010C00u), perm(0u, w.x, 0x0C030C02u),
-                                            perm(0u, w.y, 0x0C010C00u), perm(0u, w.y, 0x0C030C02u)},
-                                      P[k], o[i]);
+                        const u32x2 w = lds_read_tr_codes<8>(L.v + tok * RB + 16 * vpiece(tok, i) + 8 * (n & 1));
+                        uint32_t d[4];
+                        codes_int8(w.x, d);
+                        codes_int8(w.y, d + 2);
+                        o[i] = mfma16(u32x4{d[0], d[1], d[2], d[3]}, P[k], o[i]);
                     }
                 } else {
                     // row r of the group is the token whose nibble the masks put at its place: nibbles
@@ -772,7 +752,7 @@ struct Stream {
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         uint32_t d[4];
-                        unpack_mask_f16(k ? w.y : w.x, d);
+                        codes_int4(k ? w.y : w.x, z[k], d);
                         o[i] = mfma16(u32x4{d[0], d[1], d[2], d[3]}, P[k], o[i]);
                     }
                 }
@@ -792,10 +772,10 @@ struct Stream {
         float Lt = 0.0f;
 #pragma unroll
         for (int w = 0; w < 4; ++w) Lt += M == NEG ? 0.0f : sl[w][n] * exp2_raw(sm[w][n] - M);
-        const float f = M == NEG ? 0.0f : exp2_raw(m - M) * (vcap / VNORM);
+        const float f = M == NEG ? 0.0f : exp2_raw(m - M) * (vcap / VNORM * kCodeUnit);
 #pragma unroll
         for (int i = 0; i < OT; ++i)
-            *reinterpret_cast<f32x4*>(lds.join[wave][4 * i + qd][n]) = (o[i] * 16777216.0f - oz) * f;
+            *reinterpret_cast<f32x4*>(lds.join[wave][4 * i + qd][n]) = o[i] * f;
         __syncthreads();
         if (row < R) {
             const long long at = head * nsplit + split;
