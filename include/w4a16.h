@@ -397,12 +397,13 @@ int w4a16_kv_attention_decode_batch(const void* q, int dtype, int64_t B, int64_t
  *   cu_seqlens  device int32 [B + 1], not decreasing: sequence b is the tokens cu_seqlens[b] ..
  *         cu_seqlens[b + 1] - 1 (possibly none).  Values are clamped into [0, T] on the device;
  *         decreasing values leave rows of out unspecified, never an access outside the tensors.
- *   out   [T, Hq, D] dense, same dtype, 16-byte aligned; must not overlap the inputs.  Rows before
- *         the first and behind the last sequence are not written, and q, k and v are not read
- *         there: a padded batch may hold anything in them.
+ *   out   [T, Hq, D] dense, same dtype, 16-byte aligned; must not overlap the inputs, each taken
+ *         from its first element to its last (W4A16_ERR_OVERLAP).  Rows before the first and behind
+ *         the last sequence are not written, and q, k and v are not read there: a padded batch may
+ *         hold anything in them.
  * Scores, softmax statistics and outputs are held in fp32; the softmax weights are rounded once to
  * dtype for the product with the values, and the output is rounded once.
- * Limits: 1 <= B <= 2^20, 1 <= T <= 2^30, (T / 32 + B) * Hq < 2^31, Hq <= 65535.
+ * Limits: 1 <= B <= 2^20, 1 <= T <= 2^30, (T / 128 + B) * Hq < 2^24, Hq <= 65535.
  */
 int w4a16_attention_prompt(const void* q, const void* k, const void* v, int dtype, int64_t T, int64_t B,
                            const int32_t* cu_seqlens, int64_t Hq, int64_t Hkv, int64_t D, int64_t q_stride,
@@ -436,8 +437,8 @@ int64_t w4a16_kv_attention_shared_workspace(int64_t B, int64_t Hq, int64_t Hkv, 
  * w4a16_kv_attention_decode_shared -- decode attention for a batch of B sequences that begin with
  * the same P tokens (a system prompt, a document): out[b][h] = softmax(q[b][h] . K / sqrt(D)) V over
  * the shared tokens and then the first lengths[b] tokens of the sequence's own cache, kv head
- * h / (Hq / Hkv).  The prefix is held once and read once per 128 query rows (B * Hq / Hkv rows per
- * kv head), not once per sequence.
+ * h / (Hq / Hkv).  The prefix is held once and read once per 128 of the B * Hq / Hkv
+ * query rows of a kv head, not once per sequence.
  *   q        [B, Hq, D] fp16/bf16, 16-byte aligned; out [B, Hq, D] same dtype.
  *   prefix   w4a16_kv_quantize output with H = Hkv and T = Pmax ([Hkv, Pmax, ...]); its first P
  *            tokens are read, 0 <= P <= Pmax <= 2^24.  P == 0: its pointers are not looked at.
@@ -446,9 +447,11 @@ int64_t w4a16_kv_attention_shared_workspace(int64_t B, int64_t Hq, int64_t Hkv, 
  *            P + lengths[b] == 0 gets zeros.
  *   work     w4a16_kv_attention_shared_workspace(...) fp32 elements, 16-byte aligned (scratch,
  *            contents undefined after the call; calls that overlap on one buffer race).
- * Scores, softmax statistics and sums are fp32; the softmax weights times V's scales are rounded
- * once to fp16 (relative 2^-11) for the product with the codes, and the output is rounded once.
- * Limits: B <= 65535, B * Hq <= 2^24, Hkv * (Pmax + B * Tmax) <= 2^33.
+ * Scores, softmax statistics and sums are fp32; the codes less their zero points (|z| <= 2048) are
+ * exact, the softmax weights times V's scales are rounded once to fp16 (relative 2^-11) for the
+ * product with them, and the output is rounded once.  bf16 queries are scaled by a power of two
+ * into fp16, exact but for entries below 2^-21 of the largest of their row.
+ * Limits: B <= 65535, B * Hq < 2^22, Hkv * (Pmax + B * Tmax) <= 2^33.
  */
 int w4a16_kv_attention_decode_shared(const void* q, int dtype, int64_t B, int64_t Hq, int64_t Hkv, int64_t D,
                                      int bits, const w4a16_kv_cache* prefix, int64_t P, int64_t Pmax,

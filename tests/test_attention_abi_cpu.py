@@ -33,9 +33,11 @@ def prompt(lib, **kw):
     (dict(Hkv=3), L.ERR_SHAPE), (dict(Hq=0), L.ERR_SHAPE), (dict(D=96), L.ERR_SHAPE), (dict(qs=504), L.ERR_SHAPE),
     (dict(ks=248), L.ERR_SHAPE), (dict(vs=248), L.ERR_SHAPE), (dict(qs=(1 << 24) + 8), L.ERR_SHAPE),
     (dict(T=(1 << 30) + 1), L.ERR_SHAPE), (dict(T=1 << 30, Hq=64), L.ERR_SHAPE), (dict(B=(1 << 20) + 1), L.ERR_SHAPE),
+    (dict(B=1 << 18, Hq=64, qs=4096), L.ERR_SHAPE), (dict(T=1 << 29, Hq=4, qs=1024), L.ERR_SHAPE),
     (dict(qs=1028), L.ERR_ALIGN), (dict(ks=1026), L.ERR_ALIGN), (dict(q=A + 8), L.ERR_ALIGN),
     (dict(k=B + 2), L.ERR_ALIGN), (dict(v=C + 4), L.ERR_ALIGN), (dict(cu=D + 2), L.ERR_ALIGN),
-    (dict(out=E + 8), L.ERR_ALIGN)])
+    (dict(out=E + 8), L.ERR_ALIGN), (dict(out=A), L.ERR_OVERLAP), (dict(out=C + 2 * 1024), L.ERR_OVERLAP),
+    (dict(out=B + 2 * (99 * 1024 + 4 * 64) - 16), L.ERR_OVERLAP), (dict(out=D - 16), L.ERR_OVERLAP)])
 def test_prompt_refusals(lib, kw, status):
     assert prompt(lib, **kw) == status
 
@@ -53,7 +55,7 @@ BAD_CACHES = [(8, dict(kcodes=None), L.ERR_NULL), (8, dict(kscales=None), L.ERR_
               (4, dict(vzeros=A + 1), L.ERR_ALIGN)]
 SIZES = [(dict(Hkv=3), L.ERR_SHAPE), (dict(B=0), L.ERR_SHAPE), (dict(B=65536), L.ERR_SHAPE), (dict(D=32), L.ERR_SHAPE),
          (dict(Tmax=0), L.ERR_SHAPE), (dict(Tmax=(1 << 24) + 1), L.ERR_SHAPE), (dict(B=4096, Hq=65532), L.ERR_SHAPE),
-         (dict(bits=6), L.ERR_SCHEME), (dict(dt=3), L.ERR_DTYPE), (dict(q=None), L.ERR_NULL), (dict(own=None), L.ERR_NULL),
+         (dict(B=1 << 15, Hq=128), L.ERR_SHAPE), (dict(bits=6), L.ERR_SCHEME), (dict(dt=3), L.ERR_DTYPE), (dict(q=None), L.ERR_NULL), (dict(own=None), L.ERR_NULL),
          (dict(lens=None), L.ERR_NULL), (dict(work=None), L.ERR_NULL), (dict(out=None), L.ERR_NULL),
          (dict(q=B + 8), L.ERR_ALIGN), (dict(lens=C + 2), L.ERR_ALIGN), (dict(work=D + 8), L.ERR_ALIGN),
          (dict(out=E + 1), L.ERR_ALIGN)]
@@ -121,7 +123,7 @@ def evict(lib, **kw):
     (dict(wo=None), L.ERR_NULL), (dict(lo=None), L.ERR_NULL), (dict(kept=None), L.ERR_NULL), (dict(bits=3), L.ERR_SCHEME),
     (dict(B=0), L.ERR_SHAPE), (dict(D=100), L.ERR_SHAPE), (dict(budget=0), L.ERR_SHAPE), (dict(recent=-1), L.ERR_SHAPE),
     (dict(recent=51), L.ERR_SHAPE), (dict(Tout=49), L.ERR_SHAPE), (dict(Tout=(1 << 24) + 1), L.ERR_SHAPE),
-    (dict(Tmax=0), L.ERR_SHAPE), (dict(w=B + 2), L.ERR_ALIGN), (dict(wo=D + 1), L.ERR_ALIGN), (dict(lens=C + 1), L.ERR_ALIGN),
+    (dict(Tmax=0), L.ERR_SHAPE), (dict(B=1 << 14, Hkv=256, Tmax=1, Tout=1), L.ERR_SHAPE), (dict(w=B + 2), L.ERR_ALIGN), (dict(wo=D + 1), L.ERR_ALIGN), (dict(lens=C + 1), L.ERR_ALIGN),
     (dict(lo=D + 0x10002), L.ERR_ALIGN), (dict(kept=D + 0x20001), L.ERR_ALIGN),
     (dict(Tmax=8193), L.ERR_NULL), (dict(Tmax=8193, work=D + 0x30008), L.ERR_ALIGN),
     (dict(dst="src"), L.ERR_OVERLAP), (dict(wo=B + 4), L.ERR_OVERLAP), (dict(lo=C), L.ERR_OVERLAP),

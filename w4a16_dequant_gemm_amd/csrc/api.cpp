@@ -68,10 +68,14 @@ w4a16::KvCache as_cache(const w4a16_kv_cache& c) {
 
 constexpr int64_t kMaxTokens = int64_t(1) << 24;          // tokens of a cached sequence
 constexpr int64_t kMaxCacheRows = int64_t(1) << 33;       // (sequence, head, token) rows of a cache
+// A launch has fewer than 2^32 threads: query heads of a batch, of which eviction gives each a block of
+// 1024 (the attention kernels: a block of 256 each, or per 1024 cache rows of each kv head).
+constexpr int64_t kMaxHeads = (int64_t(1) << 22) - 1;
+constexpr int64_t kMaxPromptBlocks = (int64_t(1) << 24) - 1;    // of 256 threads
 
 // Sizes of the batched decode attention over quantized caches (the shared prefix: P of Pmax tokens).
 int check_kv_batch(int64_t B, int64_t Hq, int64_t Hkv, int64_t P, int64_t Pmax, int64_t Tmax, int64_t D) {
-    if (B < 1 || B > 65535 || Hq < 1 || Hkv < 1 || Hq > 65535 || Hq % Hkv != 0 || B * Hq > (int64_t(1) << 24) ||
+    if (B < 1 || B > 65535 || Hq < 1 || Hkv < 1 || Hq > 65535 || Hq % Hkv != 0 || B * Hq > kMaxHeads ||
         Tmax < 1 || Tmax > kMaxTokens || P < 0 || P > Pmax || Pmax > kMaxTokens || (D != 64 && D != 128) ||
         Hkv * Pmax + B * Hkv * Tmax > kMaxCacheRows)
         return W4A16_ERR_SHAPE;
@@ -443,7 +447,7 @@ int w4a16_attention_prompt(const void* q, const void* k, const void* v, int dtyp
     if (!q || !k || !v || !cu_seqlens || !out) return W4A16_ERR_NULL;
     if (dtype != W4A16_F16 && dtype != W4A16_BF16) return W4A16_ERR_DTYPE;
     if (T < 1 || T > (int64_t(1) << 30) || B < 1 || B > (int64_t(1) << 20) || Hq < 1 || Hkv < 1 || Hq > 65535 ||
-        Hq % Hkv != 0 || (D != 64 && D != 128) || (T / 32 + B) * Hq > kMaxDim)
+        Hq % Hkv != 0 || (D != 64 && D != 128) || (T / 128 + B) * Hq > kMaxPromptBlocks)
         return W4A16_ERR_SHAPE;
     constexpr int64_t kMaxStride = int64_t(1) << 24;
     if (q_stride < Hq * D || k_stride < Hkv * D || v_stride < Hkv * D || q_stride > kMaxStride ||
@@ -452,6 +456,11 @@ int w4a16_attention_prompt(const void* q, const void* k, const void* v, int dtyp
     if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || q_stride % 8 || k_stride % 8 || v_stride % 8 ||
         !aligned(cu_seqlens, 4) || !aligned(out, 16))
         return W4A16_ERR_ALIGN;
+    // blocks read keys, values and queries at times of their own
+    const int64_t no = 2 * T * Hq * D, nkv = Hkv * D;
+    if (overlap(out, no, q, 2 * ((T - 1) * q_stride + Hq * D)) || overlap(out, no, k, 2 * ((T - 1) * k_stride + nkv)) ||
+        overlap(out, no, v, 2 * ((T - 1) * v_stride + nkv)) || overlap(out, no, cu_seqlens, 4 * (B + 1)))
+        return W4A16_ERR_OVERLAP;
     const w4a16::PromptArgs a = {q, k, v, cu_seqlens, out, dtype, (int)B, (int)T,
                                  (int)Hq, (int)Hkv, (int)D, (int)q_stride, (int)k_stride, (int)v_stride};
     return hip_status(w4a16::launch_attention_prompt(a, static_cast<hipStream_t>(stream)));

@@ -11,6 +11,8 @@
 // this one keep.  (One block walking 100001 weights of each of 8 heads took 142 us.)
 // Gather copies the kept rows' codes and parameters, 16 bytes per thread; nothing is dequantized, so
 // the kept rows are the same bits.  All of it is bound by memory: the weights, the kept rows in and out.
+#include <algorithm>
+
 #include "common.h"
 #include "launch.h"
 
@@ -325,16 +327,19 @@ __global__ __launch_bounds__(kSelThreads) void kv_select_chunk_kernel(
 }
 
 // Rows of 16 PR bytes: block = 64 kept rows of one (sequence, kv head), K and V with their
-// parameters.  Z: with zero points (4-bit codes).
+// parameters.  Z: with zero points (4-bit codes).  `first`: the launch's
+// first block (a launch has fewer than 2^32 threads, so 2^30 rows take a second one).
 constexpr int kGatherRows = 64;
+constexpr long long kGatherBlocks = (1 << 24) - 1;
 template <int PR, bool Z>
 __global__ __launch_bounds__(256) void kv_gather_kernel(const int* __restrict__ lens, int Hkv, int Tmax, int budget,
-                                                        int Tout, int groups, const int* __restrict__ kept, KvCache in,
-                                                        KvCacheOut out) {
-    const long long bh = blockIdx.x / groups;
+                                                        int Tout, int groups, int first,
+                                                        const int* __restrict__ kept, KvCache in, KvCacheOut out) {
+    const int id = first + (int)blockIdx.x;
+    const long long bh = id / groups;
     const int n = min(max(lens[(int)bh / Hkv], 0), Tmax);
     const int count = min(n, budget);
-    const int r0 = blockIdx.x % groups * kGatherRows;
+    const int r0 = id % groups * kGatherRows;
     if (r0 >= count) return;
     const int rows = min(kGatherRows, count - r0);
     const int* ko = kept + bh * budget + r0;
@@ -364,8 +369,10 @@ template <int PR, bool Z>
 void gather(const KvEvictArgs& a, hipStream_t st) {
     const int rows = a.budget < a.Tmax ? a.budget : a.Tmax;
     const int groups = (rows + kGatherRows - 1) / kGatherRows;
-    hipLaunchKernelGGL((kv_gather_kernel<PR, Z>), dim3((unsigned)groups * a.B * a.Hkv), dim3(256), 0, st, a.lens, a.Hkv,
-                       a.Tmax, a.budget, a.Tout, groups, a.kept, a.in, a.out);
+    const long long blocks = (long long)groups * a.B * a.Hkv;
+    for (long long first = 0; first < blocks; first += kGatherBlocks)
+        hipLaunchKernelGGL((kv_gather_kernel<PR, Z>), dim3((unsigned)std::min(blocks - first, kGatherBlocks)), dim3(256),
+                           0, st, a.lens, a.Hkv, a.Tmax, a.budget, a.Tout, groups, (int)first, a.kept, a.in, a.out);
 }
 
 }  // namespace
