@@ -61,7 +61,10 @@ CASES = [
     (3, 40, 1, 128, 20, [0, 260, 40], 300, 4, BF), (65, 1, 1, 64, 2100, [1] * 65, 1, 4, H),
     (2, 2, 1, 128, 5000, [4000, 1], 4100, 8, H), (1, 3, 3, 128, 513, [600], 640, 4, H),
     (5, 8, 2, 64, 127, [3, 0, 65, 64, 1], 70, 4, BF), (12, 4, 1, 64, 191, [i for i in range(12)], 16, 8, H),
-    (64, 1, 1, 64, 320, [0] * 64, 1, 4, H), (16, 1, 1, 128, 64, [5] * 16, 5, 8, BF), (17, 1, 1, 128, 192, [5] * 17, 5, 4, BF)]
+    (64, 1, 1, 64, 320, [0] * 64, 1, 4, H), (16, 1, 1, 128, 64, [5] * 16, 5, 8, BF), (17, 1, 1, 128, 192, [5] * 17, 5, 4, BF),
+    # many rows and a prefix that is short beside the own caches (streamed), the next longer one (not)
+    (40, 8, 2, 128, 75, [7 * i for i in range(40)], 300, 8, BF), (40, 8, 2, 128, 76, [7 * i for i in range(40)], 300, 8, BF),
+    (33, 3, 1, 64, 33, [4 * i for i in range(33)], 132, 4, H), (33, 3, 1, 64, 34, [4 * i for i in range(33)], 132, 4, H)]
 
 
 @pytest.mark.parametrize("B,Hq,Hkv,D,P,lens,Tmax,bits,dtype", CASES)

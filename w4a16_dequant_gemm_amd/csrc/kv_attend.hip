@@ -7,20 +7,21 @@
 // over the P shared tokens and the lengths[b] own ones (kv head h / (Hq / Hkv)), and
 //   sums[b, kv head, t] = weights[b, kv head, t] + sum over the group's heads of p_t.
 //
-// A block takes up to 32 WQ query rows that read the same cached rows and one span of tokens (a
-// split).  Rows of the shared prefix are all B * G queries of a kv head (the prefix is read once per
-// 128 of them, not once per sequence); rows of a sequence's own cache are the G heads of a kv head.
-// The tokens go through in tiles: the codes are loaded coalesced one tile ahead into registers,
-// turned into exact fp16 integers (c - z) and stored to LDS, and the four waves of the block
-// multiply them on the matrix cores (attn.h), side by side along the rows (WQ = 4, many rows) or
-// along the tokens (WK = 4, few rows: each wave then has its own softmax state and the four are
-// joined at the end).  A token's scales stay out of the 16-bit operands: K's multiplies the fp32
-// score, V's the softmax weight before it is rounded to fp16.  bf16 queries are scaled by a power
-// of two (query_exponent) and become fp16 exactly (8-bit significands; an entry far below its row's
-// largest may lose bits that are below 2^-21 of that one).
+// A block takes query rows that read the same cached rows and one span of their tokens (a split);
+// a second launch joins the splits.  Two kernels share the first launch:
+//   Attend, for the many rows of a prefix (all B * G queries of a kv head, 32 a wave): the codes are
+//     turned into fp16 once per block, in LDS, and the prefix is read once per 128 rows.
+//   Stream, for tiles of 16 rows (a sequence's own cache: the G heads of a kv head; a prefix of few
+//     queries, or short beside the own caches): every wave streams tokens of its own, with no barrier between the first and the join.
+// Both multiply on the matrix cores, transposed (attn.h): S^T = K Q^T leaves a query row to a lane,
+// which turns its scores into weights, and O^T = V^T P^T takes them from the lane's registers.
+// A code goes in as the exact fp16 value (c - z) 2^-9, and a token's scales stay out of the 16-bit
+// operands: K's multiplies the fp32 score, V's the softmax weight before it is rounded to fp16.
+// bf16 queries are scaled by a power of two (query_exponent) and become fp16 exactly (8-bit
+// significands; an entry far below its row's largest may lose bits that are below 2^-21 of that one).
 // Rounded to 16 bits are only the weights p s_t (fp16, relative 2^-11, scaled so that the largest
 // s_t seen so far becomes 2^7 and small ones keep their bits) and the output.  Scores, maxima,
-// sums and outputs are fp32; splits are joined by a second launch.
+// sums and outputs are fp32.
 #include "attn.h"
 #include "launch.h"
 
@@ -108,9 +109,21 @@ __device__ __forceinline__ float wave_max(float v) {
     return fmaxf(fmaxf(r[0], r[1]), fmaxf(r[2], r[3]));
 }
 
-// Tokens [t0, t1) of a cache for the rows row0 .. (R in all): row r is query head
+// Tokens [t0, t1) of a cache for the 32 WQ rows from row0 on (R in all): row r is query head
 // hq0 + (r / G) * Hq + r % G of the batch.  Writes each row's (max, sum) to ml and its unnormalized
 // output to po at index head * nsplit + split.
+// The waves stand along the rows, or (WQ = 2, WK = 2: up to 64 rows) in pairs along the rows and the
+// tokens, each pair's two softmax states joined at the end.  Codes are loaded one tile ahead into
+// registers, 16 bytes a lane, and stored as fp16 into LDS whose 16-byte pieces are permuted so
+// that neither product's reads meet in a bank; with two buffers (WK = 1) a tile costs one barrier.
+// Bound by instructions rather than by its bytes: per code three or four operations to make it fp16
+// (per block, so 128 rows share them), per score a scale, an exponential, a sum, another scale and a
+// rounding.  128 sequences behind 32768 KV4 tokens, 32 heads on 8, D = 128 (70 GFLOP; with own caches of up
+// to 1024 tokens 117 MB of cache): 105 us for the launch, 0.67 PFLOP/s; the vector units are busy 42 %
+// of the cycles, the matrix cores 27 %, and waves wait 33 % of theirs.  Tried and slower or equal: tiles
+// of 32 tokens (three waves a SIMD instead of two: 165 us against 126 then), the scores of the next
+// tile interleaved with the weights of this one as in attention.hip (118 us; with a second set of
+// code registers 143), one wave a SIMD with twice the registers (166).
 template <int BITS, int D, int WQ, int WK>
 struct Attend {
     static constexpr int NBUF = WK == 1 ? 2 : 1;
@@ -472,10 +485,14 @@ __device__ __forceinline__ float across_quarters(float x, Op op) {
     return op(lo, hi);
 }
 
-// Few rows: tokens [t0, t1) of a cache for the rows row0 .. row0 + 15 (R in all; numbered as in
-// Attend).  Nothing here is bound by arithmetic, so the aim is loads in flight and few
+// Tokens [t0, t1) of a cache for the rows row0 .. row0 + 15 (R in all; numbered as in
+// Attend), 16 x 16 x 32 products.  The cache is read once, so the aim is loads in flight and few
 // instructions: each wave of the block streams tiles of its own (wave, wave + 4, ...), with no
-// barrier until the four are joined at the end.
+// barrier until the four are joined at the end, and loads the next tile while it works on one.
+// Measured: 16 sequences of up to 4096 KV8 tokens, 32 heads, D = 128 (318 MB with the scores): 62 us,
+// 5.1 TB/s; 8 of up to 65536 KV4 tokens, 32 heads on 8 (365 MB): 97 us, 3.8 TB/s, the vector units busy
+// 60 % of the cycles (twice the codes a byte).  Three blocks a CU: four spilled (254 us against 97).
+// The staged form before it, with barriers between tiles, took 112 and 220 us for the same.
 //   K's codes go from memory to the matrix cores: lane l loads the quarter l / 16 of every 64 bytes
 //     (32 for the shortest rows) of key l % 16's row, so a load covers whole cache lines, and the
 //     query's fragment is loaded in the same order.
@@ -818,12 +835,12 @@ __device__ __forceinline__ void empty_split(long long hq0, int G, int Hq, int ro
 // arithmetic of the one and the loads of the other share the GPU.
 //   Prefix, WQ > 0 (many rows): block = (kv head and split, tile of 32 WQ rows).  The row tiles of one
 //     span run on one XCD, one after the other, so that the span's codes are read from HBM once.
-//   Prefix, WQ == 0 (few rows, streamed): block = kv head, split, tile of 16 of its B G rows.
+//   Prefix, WQ == 0 (streamed): block = kv head, split, tile of 16 of its B G rows.
 //   Own caches: block = split, sequence, kv head, tile of 16 of its G heads.  Splits vary slowest and
 //     each turns the rest by one: consecutive blocks run on the 8 XCDs in turn, and the late splits
 //     of short sequences, which are empty, have to fall on all of them (with the splits fastest, 16
-//     sequences of 1024 .. 4096 tokens and 4 splits took 70 us instead of 58, two XCDs having no
-//     empty split at all).
+//     sequences of 1024 .. 4096 tokens and 4 splits took 12 us longer, two XCDs having no empty
+//     split at all).
 struct DecodeGrid {
     int pblocks, psplit, pchunk, P, Pmax;    // prefix splits come first among a row's nsplit
     int osplit, ochunk, Tmax, nsplit;
@@ -900,9 +917,11 @@ __device__ __forceinline__ void row_stats(const float2* __restrict__ ml, int nsp
     L = wave_sum(m == NEG ? 0.0f : l * exp2_raw(m - M));
 }
 
-// One block per query head of the batch: each group of D / 4 threads adds up splits grp, grp + NG, ...
-// (16 bytes a thread, several loads in flight), the groups are added through LDS; a row that saw no
-// token gets zeros.
+// out = sum_j O_j 2^(m_j - M) / sum_j l_j 2^(m_j - M) over the splits j.  One block per query head of
+// the batch: each group of D / 4 threads adds up splits grp, grp + NG, ... (16 bytes a thread, several
+// loads in flight), the groups are added through LDS; a row that saw no token gets zeros.  Bound by the
+// latency of two dependent loads, then by the partial outputs' bytes: 2.7 us for 32 heads, 4.2 us
+// for 1024 of 17 splits, 9.3 us (39 MB) for 4096 of up to 18.
 template <int D>
 __device__ __forceinline__ void merge_row(float (*part)[D], long long head, const float2* __restrict__ ml,
                                           const float* __restrict__ po, int nsplit, int bf16,
@@ -940,7 +959,10 @@ __global__ __launch_bounds__(kThreads) void kv_merge_kernel(const float2* __rest
 }
 
 // Output and accumulated weights in one launch: the first `heads` blocks merge a query head each,
-// the others turn kSpan scores of a (sequence, kv head) into weights.
+// the others turn kSpan scores of a (sequence, kv head) into weights: a token's p of each head is
+// 2^(score - M) / L, so the streaming kernel leaves the scores (base 2, fp32) instead of reading the
+// cache twice.  Bound by the scores' bytes, G x 4 a token and kv head: 8.4 us (15 MB) for 16 x 32 heads
+// of up to 4096 tokens, 16 us (70 MB, G = 4) for 8 x 32 of up to 65536.
 constexpr int kSpan = 4 * kThreads;
 constexpr int kStatHeads = 64;           // heads whose statistics are at hand at a time
 template <int D>
@@ -996,10 +1018,13 @@ __global__ __launch_bounds__(kThreads) void kv_weights_kernel(const float2* __re
 
 // ------------------------------------------------------------------------------- host side
 
-constexpr long long kBlocks = 2048;      // blocks of the streaming kernel to aim for
+// Blocks to aim for: streaming, 8 a CU against ragged lengths (1024, 4096 and 8192 within 3 % or slower);
+// Attend, the 2 a CU that run at once.  A split has at least 256 tokens: a row of its partial output is as
+// large as four rows of KV8 cache, and 128 rows write one each (32 sequences behind 4096 tokens: 128 and
+// 64 tokens, 28 and 37 us against 23).
+constexpr long long kBlocks = 2048;
 constexpr long long kPrefixBlocks = 512;
-constexpr int kMinChunk = 256;           // tokens of a split, at least
-constexpr int kStreamRows = 16;          // prefix rows per kv head up to which it is streamed
+constexpr int kMinChunk = 256;
 
 int divup(long long a, long long b) { return (int)((a + b - 1) / b); }
 
@@ -1011,11 +1036,20 @@ int chunk_of(long long T, long long tiles, long long blocks, long long least) {
 int own_chunk(long long B, long long Hq, long long Hkv, long long T) {
     return chunk_of(T, B * Hkv * divup(Hq / Hkv, 16), kBlocks, kMinChunk);
 }
-int prefix_wq(long long R) { return R <= kStreamRows ? 0 : R <= 64 ? 2 : 4; }   // 0: streaming
-int prefix_chunk(long long B, long long Hq, long long Hkv, long long P) {
+// How the R = B G rows of a kv head meet the prefix: streamed (0) where they are one tile of Stream's, or
+// where the own caches are most of the work (the kernel then runs three blocks a CU instead of two), else
+// Attend with WQ = 2 or 4.  Whole calls, streamed / 2 / 4, KV8, 32 heads on 8, D = 128:
+//   16 sequences of up to 4096 own tokens, no prefix / 512 tokens   23.3 / 25.7 / 25.8, 24.7 / 27.3 / 27.3 us
+//   64 of up to 2048, 512 / 4096 tokens                 39.4 / 41.1 / 40.8, 54.5 / 52.7 / 48.2
+//   8 rows, 4096 / 32768 tokens, 100 own ones           16.8 / 16.9 / 17.2, 25.9 / 26.5 / 32.2
+//   20, 64 rows, 32768 tokens                           33.8 / 26.6 / 33.3, 40.0 / 31.2 / 37.2
+//   128, 256 rows, 32768 tokens                         61.0 / 40.4 / 41.2, 98.1 / 65.1 / 61.1
+// (128 rows of bf16, 4096 tokens and up to 512 own ones: 24.4 / 23.0 / 21.0, so those take 4).
+int prefix_wq(long long R, long long P, long long Tmax) { return R <= 16 || 4 * P <= Tmax ? 0 : R <= 64 ? 2 : 4; }
+int prefix_chunk(long long B, long long Hq, long long Hkv, long long P, long long Tmax) {
     if (P == 0) return kMinChunk;
     const long long R = B * (Hq / Hkv);
-    const int wq = prefix_wq(R);
+    const int wq = prefix_wq(R, P, Tmax);
     return wq == 0 ? chunk_of(P, Hkv * divup(R, 16), kBlocks, kMinChunk)
                    : chunk_of(P, Hkv * divup(R, 32 * wq), kPrefixBlocks, kMinChunk);
 }
@@ -1026,12 +1060,12 @@ template <int BITS, int D>
 hipError_t shared(const KvSharedArgs& a, float* work, hipStream_t st) {
     const int G = a.Hq / a.Hkv;
     const long long heads = (long long)a.B * a.Hq, R = (long long)a.B * G;
-    const int wq = prefix_wq(R);
+    const int wq = prefix_wq(R, a.P, a.Tmax);
     DecodeGrid g = {};
     g.P = a.P;
     g.Pmax = a.Pmax;
     g.Tmax = a.Tmax;
-    g.pchunk = prefix_chunk(a.B, a.Hq, a.Hkv, a.P);
+    g.pchunk = prefix_chunk(a.B, a.Hq, a.Hkv, a.P, a.Tmax);
     g.psplit = divup(a.P, g.pchunk);
     g.pblocks = (int)(8 * divup((long long)a.Hkv * g.psplit, 8) * (long long)divup(R, wq ? 32 * wq : 16));
     g.ochunk = own_chunk(a.B, a.Hq, a.Hkv, a.Tmax);
@@ -1085,7 +1119,7 @@ hipError_t weights(const KvWeightsArgs& a, float* work, hipStream_t st) {
 
 long long kv_shared_workspace_floats(long long B, long long Hq, long long Hkv, long long P, long long Tmax,
                                      long long D) {
-    return parts_floats(B * Hq, divup(P, prefix_chunk(B, Hq, Hkv, P)) + divup(Tmax, own_chunk(B, Hq, Hkv, Tmax)), D);
+    return parts_floats(B * Hq, divup(P, prefix_chunk(B, Hq, Hkv, P, Tmax)) + divup(Tmax, own_chunk(B, Hq, Hkv, Tmax)), D);
 }
 
 long long kv_weights_workspace_floats(long long B, long long Hq, long long Hkv, long long Tmax, long long D) {
