@@ -119,7 +119,7 @@ __device__ __forceinline__ float wave_max(float v) {
 // Bound by instructions rather than by its bytes: per code three or four operations to make it fp16
 // (per block, so 128 rows share them), per score a scale, an exponential, a sum, another scale and a
 // rounding.  128 sequences behind 32768 KV4 tokens, 32 heads on 8, D = 128 (70 GFLOP; with own caches of up
-// to 1024 tokens 117 MB of cache): 105 us for the launch, 0.67 PFLOP/s; the vector units are busy 42 %
+// to 1024 tokens 117 MB of cache): 105 us for the launch (117 traced), 0.67 PFLOP/s; the vector units are busy 42 %
 // of the cycles, the matrix cores 27 %, and waves wait 33 % of theirs.  Tried and slower or equal: tiles
 // of 32 tokens (three waves a SIMD instead of two: 165 us against 126 then), the scores of the next
 // tile interleaved with the weights of this one as in attention.hip (118 us; with a second set of
