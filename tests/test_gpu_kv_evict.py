@@ -91,7 +91,11 @@ CASES = [(1, 1, 1, [1], 1, 0, 64, 8), (1, 1, 2, [2], 1, 0, 64, 4), (1, 1, 2, [2]
          (1, 2, 5001, [5001], 2048, 100, 128, 4), (2, 1, 300, [300, 40], 400, 50, 64, 8),
          (1, 1, 20011, [20011], 20010, 1, 64, 8), (1, 2, 8192, [8192], 4000, 8, 64, 4), (2, 1, 8193, [8193, 100], 5000, 4500, 64, 8),
          (3, 2, 30000, [30000, 9000, 0], 9000, 20, 64, 8), (2, 1, 25000, [25000, 16385], 16384, 16384, 64, 4),
-         (1, 1, 600001, [600001], 70000, 66000, 64, 4), (2, 1, 40000, [40000, 39999], 12000, 11990, 64, 8)]
+         (1, 1, 600001, [600001], 70000, 66000, 64, 4), (2, 1, 40000, [40000, 39999], 12000, 11990, 64, 8),
+         # kept rows of 64 KB, the most that the selecting block copies, and one row more
+         (3, 2, 3001, [3001, 512, 700], 512, 30, 128, 8), (3, 2, 3001, [3001, 513, 700], 513, 30, 128, 8),
+         (1, 3, 4000, [4000], 2048, 0, 64, 4), (1, 3, 4000, [4000], 2049, 2049, 64, 4),
+         (2, 1, 8192, [8192, 1], 1024, 1, 128, 4), (2, 1, 8192, [8192, 1025], 1025, 1, 64, 8)]
 
 
 @pytest.mark.parametrize("B,Hkv,T,lens,budget,recent,D,bits", CASES)

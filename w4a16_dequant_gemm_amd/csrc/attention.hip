@@ -38,9 +38,10 @@ constexpr int kKeys = 64;       // keys of a tile
 
 // The row tile that comes `rank`-th in order of work (tile j of a sequence has j + 1 times kRows keys,
 // less the last one's shortfall): late tiles of all sequences first, so that the long blocks do not
-// start last (12 prompts of up to 1024 tokens: 43.7 -> 41.0 us).  Lane b holds sequence b's tile count (B <= 64), F(j) = sum_b max(0, tiles_b - j) tiles
-// are numbered j or later; j is the largest with F(j) > rank, found by bisection over the counts, and
-// the sequences with more than j tiles follow in their order.  Returns false behind the last tile.
+// start last (12 prompts of up to 1024 tokens: 43.7 -> 41.0 us).  Lane b holds sequence b's tile count
+// (B <= 64), F(j) = sum_b max(0, tiles_b - j) tiles are numbered j or later; j is the largest with
+// F(j) > rank, found by bisection over the counts, and the sequences with more than j tiles follow in
+// their order.  Returns false behind the last tile.
 __device__ __forceinline__ int lanes_sum(int v) {
     v += __builtin_amdgcn_mov_dpp(v, 0xB1, 0xF, 0xF, true);      // quad_perm [1,0,3,2]
     v += __builtin_amdgcn_mov_dpp(v, 0x4E, 0xF, 0xF, true);      // quad_perm [2,3,0,1]

@@ -12,7 +12,8 @@
 //   Attend, for the many rows of a prefix (all B * G queries of a kv head, 32 a wave): the codes are
 //     turned into fp16 once per block, in LDS, and the prefix is read once per 128 rows.
 //   Stream, for tiles of 16 rows (a sequence's own cache: the G heads of a kv head; a prefix of few
-//     queries, or short beside the own caches): every wave streams tokens of its own, with no barrier between the first and the join.
+//     queries, or short beside the own caches): every wave streams tokens of its own, with no barrier
+//     between the first and the join.
 // Both multiply on the matrix cores, transposed (attn.h): S^T = K Q^T leaves a query row to a lane,
 // which turns its scores into weights, and O^T = V^T P^T takes them from the lane's registers.
 // A code goes in as the exact fp16 value (c - z) 2^-9, and a token's scales stay out of the 16-bit

@@ -10,11 +10,12 @@
 // digit for itself, and the ordered write, where the same histograms tell how much the chunks before
 // this one keep.  (One block walking 100001 weights of each of 8 heads took 142 us; these launches 31.)
 // Gather copies the kept rows' codes and parameters, 16 bytes per thread; nothing is dequantized, so
-// the kept rows are the same bits.  All of it is bound by memory: the weights, the kept rows in and out.
+// the kept rows are the same bits.  Where a head keeps few rows the selecting block copies them.
+// All of it is bound by memory: the weights, the kept rows in and out.
 // Measured: 16 x 32 heads of up to 4096 KV8 tokens, D = 128, halved: select 15.9 us, gather 100 us (533
 // MB, 5.3 TB/s); 8 heads of 100001 KV4 tokens to 16384: select 4.5 + 7.6 + 7.8 + 11 us, each launch the
 // latency of its chain (length, earlier histograms, scan, weights; fetching the weights first did not
-// shorten it), gather 9.8 us; 2 x 2 heads of 300: 7.0 + 3.2 us.
+// shorten it), gather 9.8 us; 2 x 2 heads of 300 to 128: 8 us, one launch.
 #include <algorithm>
 
 #include "common.h"
@@ -207,12 +208,40 @@ __device__ __forceinline__ void fill_rest(int count, int budget, int Tout, int f
     for (int i = count + first; i < Tout; i += step) wo[i] = 0.0f;
 }
 
-// One block per (sequence, kv head) of up to kBatch tokens.
+// The rows src + ko[0 .. rows) of the caches to dst, dst + 1, ...: 16 PR bytes of codes each of K and V,
+// with their parameters.  Z: with zero points (4-bit codes).
+template <int PR, bool Z, int THREADS>
+__device__ __forceinline__ void copy_rows(const KvCache& in, const KvCacheOut& out, const int* ko, long long src,
+                                          long long dst, int rows) {
+    const u32x4* kc = static_cast<const u32x4*>(in.kc);
+    const u32x4* vc = static_cast<const u32x4*>(in.vc);
+    u32x4* kd = static_cast<u32x4*>(out.kc);
+    u32x4* vd = static_cast<u32x4*>(out.vc);
+    for (int p = threadIdx.x; p < rows * PR; p += THREADS) {
+        const int r = p / PR, c = p % PR;
+        const long long s = (src + ko[r]) * PR + c, d = (dst + r) * PR + c;
+        kd[d] = kc[s];
+        vd[d] = vc[s];
+    }
+    for (int r = threadIdx.x; r < rows; r += THREADS) {
+        const long long s = src + ko[r], d = dst + r;
+        out.ks[d] = in.ks[s];
+        out.vs[d] = in.vs[s];
+        if constexpr (Z) {
+            out.kz[d] = in.kz[s];
+            out.vz[d] = in.vz[s];
+        }
+    }
+}
+
+// One block per (sequence, kv head) of up to kBatch tokens; PR > 0: it copies the kept rows too.
+template <int PR, bool Z>
 __global__ __launch_bounds__(kSelThreads) void kv_select_kernel(const float* __restrict__ weights,
                                                                 const int* __restrict__ lens, int Hkv, int Tmax,
                                                                 int budget, int recent, int Tout,
                                                                 float* __restrict__ weights_out,
-                                                                int* __restrict__ lens_out, int* __restrict__ kept) {
+                                                                int* __restrict__ lens_out, int* kept, KvCache in,
+                                                                KvCacheOut out) {
     __shared__ SelectLds s;
     const long long bh = blockIdx.x;
     const int b = blockIdx.x / Hkv;
@@ -245,7 +274,8 @@ __global__ __launch_bounds__(kSelThreads) void kv_select_kernel(const float* __r
         th.prefix = 0xFFFFFFFFu;
     }
     int pos = 0, ties = 0;
-    write_batch(s, x, 0, old, n, th, pos, ties, ko, wo);
+    write_batch(s, x, 0, old, n, th, pos, ties, ko, wo);       // (ends with a barrier)
+    if constexpr (PR > 0) copy_rows<PR, Z, kSelThreads>(in, out, ko, bh * Tmax, bh * Tout, count);
 }
 
 // Longer sequences, one launch per digit (LEVEL 0 .. 2) and the ordered write (LEVEL 3).  Workspace of a
@@ -330,9 +360,8 @@ __global__ __launch_bounds__(kSelThreads) void kv_select_chunk_kernel(
     }
 }
 
-// Rows of 16 PR bytes: block = 64 kept rows of one (sequence, kv head), K and V with their
-// parameters.  Z: with zero points (4-bit codes).  `first`: the launch's
-// first block (a launch has fewer than 2^32 threads, so 2^30 rows take a second one).
+// Rows of 16 PR bytes: block = 64 kept rows of one (sequence, kv head).  `first`: the launch's first
+// block (a launch has fewer than 2^32 threads, so 2^30 rows take a second one).
 constexpr int kGatherRows = 64;
 constexpr long long kGatherBlocks = (1 << 24) - 1;
 template <int PR, bool Z>
@@ -345,28 +374,7 @@ __global__ __launch_bounds__(256) void kv_gather_kernel(const int* __restrict__ 
     const int count = min(n, budget);
     const int r0 = id % groups * kGatherRows;
     if (r0 >= count) return;
-    const int rows = min(kGatherRows, count - r0);
-    const int* ko = kept + bh * budget + r0;
-    const long long src = bh * Tmax, dst = bh * Tout + r0;
-    const u32x4* kc = static_cast<const u32x4*>(in.kc);
-    const u32x4* vc = static_cast<const u32x4*>(in.vc);
-    u32x4* kd = static_cast<u32x4*>(out.kc);
-    u32x4* vd = static_cast<u32x4*>(out.vc);
-    for (int p = threadIdx.x; p < rows * PR; p += 256) {
-        const int r = p / PR, c = p % PR;
-        const long long s = (src + ko[r]) * PR + c, d = (dst + r) * PR + c;
-        kd[d] = kc[s];
-        vd[d] = vc[s];
-    }
-    if ((int)threadIdx.x < rows) {
-        const long long s = src + ko[threadIdx.x], d = dst + threadIdx.x;
-        out.ks[d] = in.ks[s];
-        out.vs[d] = in.vs[s];
-        if constexpr (Z) {
-            out.kz[d] = in.kz[s];
-            out.vz[d] = in.vz[s];
-        }
-    }
+    copy_rows<PR, Z, 256>(in, out, kept + bh * budget + r0, bh * Tmax, bh * Tout + r0, min(kGatherRows, count - r0));
 }
 
 template <int PR, bool Z>
@@ -390,10 +398,25 @@ long long kv_evict_workspace_words(long long B, long long Hkv, long long Tmax) {
     return B * Hkv * ((Tmax + chunk - 1) / chunk) * kChunkWords;
 }
 
-hipError_t launch_kv_evict(const KvEvictArgs& a, uint32_t* work, hipStream_t st) {
+// Kept rows that the selecting block copies itself: up to 64 KB of K's codes.  Against a launch of its own,
+// us in a graph (a call by itself saves 3 us of submission besides): 8 heads of 1000 KV4 tokens to 125 / 500
+// (D = 128) 8.7 / 9.5 against 9.9 / 10.0, 512 heads 17.7 / 26.5 against 20.2 / 31.3; of 4096 to 512 / 2048
+// 10.2 / 14.6 against 10.9 / 11.1 and 30.1 / 88.1 against 35.9 / 81.7.
+constexpr long long kWholeBytes = 65536;
+
+template <int PR, bool Z>
+static void evict(const KvEvictArgs& a, uint32_t* work, hipStream_t st) {
     if (a.Tmax <= kBatch) {
-        hipLaunchKernelGGL(kv_select_kernel, dim3(a.B * a.Hkv), dim3(kSelThreads), 0, st, a.weights, a.lens, a.Hkv,
-                           a.Tmax, a.budget, a.recent, a.Tout, a.weights_out, a.lens_out, a.kept);
+        const bool whole = (long long)a.budget * 16 * PR <= kWholeBytes;
+#define W4A16_SELECT(ROWS)                                                                                            \
+    hipLaunchKernelGGL((kv_select_kernel<ROWS, Z>), dim3(a.B * a.Hkv), dim3(kSelThreads), 0, st, a.weights, a.lens,    \
+                       a.Hkv, a.Tmax, a.budget, a.recent, a.Tout, a.weights_out, a.lens_out, a.kept, a.in, a.out)
+        if (whole) {
+            W4A16_SELECT(PR);
+            return;
+        }
+        W4A16_SELECT(0);
+#undef W4A16_SELECT
     } else {
         const int chunk = chunk_tokens(a.Tmax), chunks = (a.Tmax + chunk - 1) / chunk;
         const dim3 grid((unsigned)chunks * a.B * a.Hkv);
@@ -406,8 +429,12 @@ hipError_t launch_kv_evict(const KvEvictArgs& a, uint32_t* work, hipStream_t st)
         W4A16_SELECT(3);
 #undef W4A16_SELECT
     }
-    if (a.bits == 8) a.D == 64 ? gather<4, false>(a, st) : gather<8, false>(a, st);
-    else a.D == 64 ? gather<2, true>(a, st) : gather<4, true>(a, st);
+    gather<PR, Z>(a, st);
+}
+
+hipError_t launch_kv_evict(const KvEvictArgs& a, uint32_t* work, hipStream_t st) {
+    if (a.bits == 8) a.D == 64 ? evict<4, false>(a, work, st) : evict<8, false>(a, work, st);
+    else a.D == 64 ? evict<2, true>(a, work, st) : evict<4, true>(a, work, st);
     return hipGetLastError();
 }
 
