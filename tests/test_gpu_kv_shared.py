@@ -64,7 +64,15 @@ CASES = [
     (64, 1, 1, 64, 320, [0] * 64, 1, 4, H), (16, 1, 1, 128, 64, [5] * 16, 5, 8, BF), (17, 1, 1, 128, 192, [5] * 17, 5, 4, BF),
     # many rows and a prefix that is short beside the own caches (streamed), the next longer one (not)
     (40, 8, 2, 128, 75, [7 * i for i in range(40)], 300, 8, BF), (40, 8, 2, 128, 76, [7 * i for i in range(40)], 300, 8, BF),
-    (33, 3, 1, 64, 33, [4 * i for i in range(33)], 132, 4, H), (33, 3, 1, 64, 34, [4 * i for i in range(33)], 132, 4, H)]
+    (33, 3, 1, 64, 33, [4 * i for i in range(33)], 132, 4, H), (33, 3, 1, 64, 34, [4 * i for i in range(33)], 132, 4, H),
+    # the same sizes with more room for own tokens, so that a sequence is not one block's work
+    (40, 8, 2, 128, 150, [7 * i for i in range(40)], 600, 8, BF), (40, 8, 2, 128, 151, [7 * i for i in range(40)], 600, 8, BF),
+    (1, 1, 1, 64, 1, [0], 512, 8, H), (3, 4, 4, 128, 63, [1, 0, 5], 450, 8, BF), (2, 6, 2, 64, 64, [64, 65], 449, 4, H),
+    (33, 2, 2, 128, 129, [i % 5 for i in range(33)], 400, 4, H), (12, 4, 1, 64, 191, [i for i in range(12)], 400, 8, H),
+    (64, 1, 1, 64, 320, [0] * 64, 300, 4, H), (17, 1, 1, 128, 192, [5] * 17, 400, 4, BF), (3, 40, 1, 128, 130, [0, 260, 40], 500, 4, BF),
+    (5, 8, 2, 64, 127, [3, 0, 65, 64, 1], 500, 4, BF), (2, 40, 1, 64, 256, [100, 256], 256, 8, H), (2, 40, 1, 64, 256, [100, 257], 257, 8, H),
+    # many sequences behind a prefix that is too much to read for each
+    (1100, 4, 4, 64, 240, [i % 12 for i in range(1100)], 12, 8, H)]
 
 
 @pytest.mark.parametrize("B,Hq,Hkv,D,P,lens,Tmax,bits,dtype", CASES)
@@ -81,10 +89,11 @@ def test_shared_prefix(B, Hq, Hkv, D, P, lens, Tmax, bits, dtype):
 
 
 @pytest.mark.parametrize("bits", [8, 4])
-def test_no_prefix_and_no_tokens(bits):
+@pytest.mark.parametrize("room", [150, 700])
+def test_no_prefix_and_no_tokens(bits, room):
     """P = 0 leaves the own tokens; a sequence with neither gets zeros."""
     lens = [0, 130, 1]
-    q, kp, vp, k, v = problem(3, 4, 2, 128, 0, 150, bits, H, seed=50)
+    q, kp, vp, k, v = problem(3, 4, 2, 128, 0, room, bits, H, seed=50)
     lt = torch.tensor(lens, dtype=torch.int32, device="cuda")
     out = torch.full_like(q, float("nan"))
     W4.kv_attention_decode_shared(q, kp, vp, 0, k, v, lt, bits, out=out)
@@ -103,9 +112,10 @@ def test_lengths_outside_are_clamped():
 
 @pytest.mark.parametrize("bits", [8, 4])
 @pytest.mark.parametrize("qscale", [1e-30, 1e4])
-def test_bf16_queries_far_from_one(bits, qscale):
+@pytest.mark.parametrize("room", [30, 500])
+def test_bf16_queries_far_from_one(bits, qscale, room):
     """bf16 queries outside fp16's range: scaled by a power of two inside the kernel."""
-    q, kp, vp, k, v = problem(4, 8, 2, 128, 150, 30, bits, BF, seed=52, qscale=qscale)
+    q, kp, vp, k, v = problem(4, 8, 2, 128, 150, room, bits, BF, seed=52, qscale=qscale)
     lens = [0, 30, 7, 1]
     out = W4.kv_attention_decode_shared(q, kp, vp, 150, k, v, torch.tensor(lens, dtype=torch.int32, device="cuda"), bits)
     torch.cuda.synchronize()
@@ -125,10 +135,11 @@ def test_bf16_queries_far_from_one(bits, qscale):
 
 @pytest.mark.parametrize("B,Hq,Hkv", [(4, 8, 2), (12, 8, 2), (40, 8, 2)])
 @pytest.mark.parametrize("bits", [8, 4])
-def test_bf16_queries_of_very_different_size(bits, B, Hq, Hkv):
+@pytest.mark.parametrize("room", [9, 400])
+def test_bf16_queries_of_very_different_size(bits, B, Hq, Hkv, room):
     """Rows that share a block, from 1e-30 to 1e6 in size: each keeps its bits (16, 48 and 160 rows
-    per kv head, one for each arrangement of the waves)."""
-    q, kp, vp, k, v = problem(B, Hq, Hkv, 128, 150, 9, bits, BF, seed=60)
+    per kv head, one for each arrangement of the waves; a sequence as one block's work)."""
+    q, kp, vp, k, v = problem(B, Hq, Hkv, 128, 150, room, bits, BF, seed=60)
     size = torch.tensor([1e-30, 1.0, 1e-9, 1e6, 0.0, 1e-3, 3e4])[torch.arange(B * Hq) % 7].view(B, Hq, 1)
     q = (q.cpu().float() * size).to(BF).cuda()
     lens = [i % 10 for i in range(B)]
@@ -147,9 +158,10 @@ def test_bf16_queries_of_very_different_size(bits, B, Hq, Hkv):
 
 @pytest.mark.parametrize("B,Hq,Hkv", [(4, 8, 2), (12, 8, 2), (40, 8, 2)])
 @pytest.mark.parametrize("dtype", [H, BF])
-def test_rows_without_numbers_leave_the_others_alone(B, Hq, Hkv, dtype):
+@pytest.mark.parametrize("room", [9, 400])
+def test_rows_without_numbers_leave_the_others_alone(B, Hq, Hkv, dtype, room):
     """Unused places of a padded batch: NaN and infinities in some queries, the other rows as before."""
-    q, kp, vp, k, v = problem(B, Hq, Hkv, 64, 140, 9, 8, dtype, seed=61)
+    q, kp, vp, k, v = problem(B, Hq, Hkv, 64, 140, room, 8, dtype, seed=61)
     lt = torch.tensor([i % 10 for i in range(B)], dtype=torch.int32, device="cuda")
     clean = W4.kv_attention_decode_shared(q, kp, vp, 140, k, v, lt, 8)
     bad = q.clone()
@@ -167,9 +179,10 @@ def test_rows_without_numbers_leave_the_others_alone(B, Hq, Hkv, dtype):
     assert np.abs(a - b).max() <= (0.0 if dtype == H else 2.0 ** -7 * np.abs(b).max())
 
 
-def test_zero_value_rows_beside_small_ones():
+@pytest.mark.parametrize("room", [10, 500])
+def test_zero_value_rows_beside_small_ones(room):
     """A row of zeros is stored with scale 1 beside values of 1e-3: the small rows keep their bits."""
-    q, kp, vp, k, v = problem(2, 4, 2, 64, 200, 10, 8, BF, seed=53, vscale=1e-3)
+    q, kp, vp, k, v = problem(2, 4, 2, 64, 200, room, 8, BF, seed=53, vscale=1e-3)
     c, s, _ = vp
     c[:, 17] = 0
     s[:, 17] = 1.0

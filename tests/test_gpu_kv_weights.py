@@ -54,7 +54,12 @@ def check(out, sums, q, k, v, before, lens, bits):
 CASES = [(1, 1, 1, 64, [1], 1, 8, H), (2, 4, 2, 128, [5, 0], 7, 4, BF), (3, 6, 2, 64, [127, 128, 129], 131, 8, BF),
          (2, 8, 1, 128, [255, 257], 261, 4, H), (1, 3, 1, 128, [1025], 1030, 8, H), (2, 40, 1, 64, [300, 33], 301, 8, H),
          (4, 4, 4, 128, [2049, 1, 700, 2050], 2051, 8, H), (1, 8, 2, 64, [5003], 5003, 4, BF),
-         (1, 33, 1, 128, [70], 70, 4, H)]
+         (1, 33, 1, 128, [70], 70, 4, H),
+         # room for more tokens than one block's work, and the most and the least that is not
+         (2, 4, 2, 128, [5, 0], 600, 4, BF), (3, 6, 2, 64, [127, 128, 129], 512, 8, BF), (3, 6, 2, 64, [127, 128, 513], 513, 8, BF),
+         (1, 33, 1, 128, [70], 530, 4, H), (2, 8, 1, 128, [255, 257], 600, 4, H), (1, 16, 1, 128, [511], 512, 4, H),
+         (2, 17, 1, 64, [300, 512], 512, 8, BF), (64, 4, 4, 64, [16 * i + 15 for i in range(64)], 1024, 8, H),
+         (64, 4, 4, 64, [16 * i + 1 for i in range(64)], 1025, 4, H)]
 
 
 @pytest.mark.parametrize("B,Hq,Hkv,D,lens,Tmax,bits,dtype", CASES)

@@ -8,7 +8,7 @@
 //   sums[b, kv head, t] = weights[b, kv head, t] + sum over the group's heads of p_t.
 //
 // A block takes query rows that read the same cached rows and one span of their tokens (a split);
-// a second launch joins the splits.  Two kernels share the first launch:
+// a second launch joins the splits (short sequences: one launch, kv_whole_kernel).  Two ways to take them:
 //   Attend, for the many rows of a prefix (all B * G queries of a kv head, 32 a wave): the codes are
 //     turned into fp16 once per block, in LDS, and the prefix is read once per 128 rows.
 //   Stream, for tiles of 16 rows (a sequence's own cache: the G heads of a kv head; a prefix of few
@@ -505,7 +505,9 @@ __device__ __forceinline__ float across_quarters(float x, Op op) {
 // Weights p s_t enter the second product times 128 / vcap, vcap the largest V scale so far, and the
 // running maximum may lag by 8, so that they stay below 2^15; an fp16 subnormal among them is below
 // 2^-14 of that, so its rounding adds at most 2^-32 vcap.
-template <int BITS, int D, bool SCORES>
+// WHOLE: the tokens [0, n2) of a second cache follow, and the block sees everything its rows do: it
+// normalizes and rounds them to out instead of leaving them to a merge.
+template <int BITS, int D, bool SCORES, bool WHOLE = false>
 struct Stream {
     static constexpr int KT = BITS == 8 && D == 128 ? 32 : 64;   // tokens of a tile
     static constexpr int NS = KT / 16;                           // S tiles
@@ -540,10 +542,11 @@ struct Stream {
 
     static __device__ __forceinline__ void run(Lds& lds, float (*sm)[16], float (*sl)[16],
                                                const uint16_t* __restrict__ q, bool bf16, int Hq, int G, long long hq0,
-                                               int row0, int R, const CacheRows& c, int t0, int t1, int nsplit,
+                                               int row0, int R, const CacheRows& c1, int t0, int t1, int nsplit,
                                                int split, float2* __restrict__ ml, float* __restrict__ po,
-                                               float* __restrict__ score, int spad) {
-        const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+                                               float* __restrict__ score, int spad, const CacheRows& c2 = {}, int n2 = 0,
+                                               uint16_t* __restrict__ out = nullptr) {
+        const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
         const int n = lane & 15, qd = lane >> 4;
         const int row = row0 + n;
         const int rr = min(row, R - 1);
@@ -552,12 +555,25 @@ struct Stream {
 
         u32x4 kr[NS * KW / 4 > 0 ? NS * KW / 4 : 1], vr[VL];
         uint16_t pk = 0, pv = 0, pkz = 0, pvz = 0;
+        const int tiles1 = (t1 - t0 + KT - 1) / KT;
+        // tile t: its cache, first token and the end of the span that it is in
+        auto place = [&](int t, int& tok, int& end) -> const CacheRows& {
+            if (WHOLE && t >= tiles1) {
+                tok = (t - tiles1) * KT;
+                end = n2;
+                return c2;
+            }
+            tok = t0 + t * KT;
+            end = t1;
+            return c1;
+        };
         auto load = [&](int t) {
-            const int base = t0 + t * KT;
+            int base, end;
+            const CacheRows c = place(t, base, end);
             // tokens behind the span: its last one, masked out of the scores
 #pragma unroll
             for (int s = 0; s < NS; ++s) {
-                const uint32_t off = (uint32_t)min(base + 16 * s + n, t1 - 1) * RB + KB * qd;
+                const uint32_t off = (uint32_t)min(base + 16 * s + n, end - 1) * RB + KB * qd;
                 if constexpr (KW == 2) {
                     const u32x2 x = *reinterpret_cast<const u32x2*>(c.kc + off);
                     kr[s / 2][2 * (s % 2)] = x.x;
@@ -571,9 +587,9 @@ struct Stream {
 #pragma unroll
             for (int i = 0; i < VL; ++i) {
                 const int p = lane + 64 * i;
-                vr[i] = *reinterpret_cast<const u32x4*>(c.vc + (uint32_t)min(base + p / VP, t1 - 1) * RB + 16 * (p % VP));
+                vr[i] = *reinterpret_cast<const u32x4*>(c.vc + (uint32_t)min(base + p / VP, end - 1) * RB + 16 * (p % VP));
             }
-            const uint32_t tok = (uint32_t)min(base + lane % KT, t1 - 1);
+            const uint32_t tok = (uint32_t)min(base + lane % KT, end - 1);
             if constexpr (KT == 64) {
                 pk = c.ks[tok];
                 pv = c.vs[tok];
@@ -585,7 +601,7 @@ struct Stream {
                 pvz = c.vz[tok];
             }
         };
-        const int tiles = (t1 - t0 + KT - 1) / KT;
+        const int tiles = tiles1 + (WHOLE ? (n2 + KT - 1) / KT : 0);
         if (wave < tiles) load(wave);
         __builtin_amdgcn_sched_barrier(0);
 
@@ -688,12 +704,13 @@ struct Stream {
             }
             if (t + 4 < tiles) load(t + 4);
 
-            const int tok0 = t0 + t * KT;
+            int tok0, end;
+            place(t, tok0, end);
             float mt = NEG;
 #pragma unroll
             for (int s = 0; s < NS; ++s) S[s] = S[s] * (*reinterpret_cast<const f32x4*>(&L.ks[16 * s + 4 * qd]) * rowf);
-            if (tok0 + KT > t1) {
-                const int left = t1 - tok0 - 4 * qd;
+            if (tok0 + KT > end) {
+                const int left = end - tok0 - 4 * qd;
 #pragma unroll
                 for (int s = 0; s < NS; ++s)
 #pragma unroll
@@ -709,7 +726,7 @@ struct Stream {
 #pragma unroll
                     for (int s = 0; s < NS; ++s) {
                         const int tok = tok0 + 16 * s + 4 * qd;
-                        if (tok < t1) *reinterpret_cast<f32x4*>(score + head * spad + tok) = S[s];
+                        if (tok < end) *reinterpret_cast<f32x4*>(score + head * spad + tok) = S[s];
                     }
                 }
             }
@@ -796,15 +813,27 @@ struct Stream {
             *reinterpret_cast<f32x4*>(lds.join[wave][4 * i + qd][n]) = o[i] * f;
         __syncthreads();
         if (row < R) {
-            const long long at = head * nsplit + split;
-            if (wave == 0 && qd == 0) ml[at] = make_float2(M, Lt);
+            const long long at = WHOLE ? head : head * nsplit + split;
+            if (!WHOLE && wave == 0 && qd == 0) ml[at] = make_float2(M, Lt);
 #pragma unroll
             for (int i = 0; i < D / 64; ++i) {
                 const int dq = wave * (D / 16) + 4 * i + qd;
                 f32x4 a = *reinterpret_cast<const f32x4*>(lds.join[0][dq][n]);
 #pragma unroll
                 for (int w = 1; w < 4; ++w) a += *reinterpret_cast<const f32x4*>(lds.join[w][dq][n]);
-                *reinterpret_cast<f32x4*>(po + at * D + 4 * dq) = a;
+                if constexpr (WHOLE) {
+                    uint16_t r[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float v = Lt > 0.0f ? a[j] / Lt : 0.0f;        // (no token at all: zeros)
+                        r[j] = bf16 ? f2bf_bits(v) : f2h_bits(v);
+                    }
+                    // out is aligned to its elements only
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) out[at * D + 4 * dq + j] = r[j];
+                } else {
+                    *reinterpret_cast<f32x4*>(po + at * D + 4 * dq) = a;
+                }
             }
         }
     }
@@ -902,6 +931,51 @@ __global__ __launch_bounds__(kThreads, WQ == 0 ? 3 : 2) void kv_decode_kernel(co
     }
     S::run(lds.s, sm, sl, q, bf16 != 0, Hq, G, hq0, row0, G,
            cache_rows<BITS, D>(own, ((long long)b * Hkv + kvh) * g.Tmax), t0, t1, g.nsplit, split, ml, po, score, spad);
+}
+
+// Short sequences in one launch: block = sequence, kv head, tile of 16 of its G heads, over the prefix
+// and the sequence's own tokens.  SCORES (G <= 16, no prefix): then the accumulated weights, from the scores
+// that the block's waves have just written.  Bound by the latency of a few dependent tiles a wave: 4
+// sequences behind 333 KV8 tokens, D = 64: 6 us; one of 500, with weights: 8.
+template <int BITS, int D, bool SCORES>
+__global__ __launch_bounds__(kThreads, 2) void kv_whole_kernel(const uint16_t* __restrict__ q, int bf16, int Hq, int Hkv,
+                                                               KvCache prefix, int P, int Pmax, KvCache own,
+                                                               const int* __restrict__ lens, int Tmax,
+                                                               uint16_t* __restrict__ out, float* score, int spad,
+                                                               const float* weights, float* sums) {
+    using S = Stream<BITS, D, SCORES, true>;
+    __shared__ typename S::Lds lds;
+    __shared__ float sm[4][16], sl[4][16];
+    const int G = Hq / Hkv, htiles = (G + 15) / 16;
+    const int row0 = 16 * (blockIdx.x % htiles);
+    const int bh = blockIdx.x / htiles, kvh = bh % Hkv, b = bh / Hkv;
+    const long long hq0 = (long long)b * Hq + (long long)kvh * G;
+    const int T = min(max(lens[b], 0), Tmax);
+    const CacheRows mine = cache_rows<BITS, D>(own, (long long)bh * Tmax);
+    if constexpr (SCORES) {
+        S::run(lds, sm, sl, q, bf16 != 0, Hq, G, hq0, row0, G, mine, 0, T, 0, 0, nullptr, nullptr, score, spad, mine, 0,
+               out);
+        // sm, sl: written before the barrier that the scores were written before
+        for (int t = 4 * threadIdx.x; t < T; t += 4 * kThreads) {
+            f32x4 w = {0.0f, 0.0f, 0.0f, 0.0f};
+            for (int g = 0; g < G; ++g) {
+                const float M = fmaxf(fmaxf(sm[0][g], sm[1][g]), fmaxf(sm[2][g], sm[3][g]));
+                float L = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) L += sl[i][g] * exp2_raw(sm[i][g] - M);
+                const f32x4 s = *reinterpret_cast<const f32x4*>(score + (hq0 + g) * spad + t);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) w[j] = fmaf(exp2_raw(s[j] - M), 1.0f / L, w[j]);
+            }
+            const long long at = (long long)bh * Tmax + t;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (t + j < T) sums[at + j] = (weights ? weights[at + j] : 0.0f) + w[j];
+        }
+    } else {
+        S::run(lds, sm, sl, q, bf16 != 0, Hq, G, hq0, row0, G, cache_rows<BITS, D>(prefix, (long long)kvh * Pmax), 0, P, 0,
+               0, nullptr, nullptr, nullptr, 0, mine, T, out);
+    }
 }
 
 // (max, sum) over all splits of a row; every lane of the wave gets it.
@@ -1055,12 +1129,33 @@ int prefix_chunk(long long B, long long Hq, long long Hkv, long long P, long lon
                    : chunk_of(P, Hkv * divup(R, 32 * wq), kPrefixBlocks, kMinChunk);
 }
 
+// Whether a block takes a sequence and kv head whole (kv_whole_kernel) instead of splits that a second
+// launch joins.  Whole / split, us in a graph (a call by itself saves 3 us of submission besides), KV8, D = 128:
+//   prefix and own caches of half each, 512 tokens: 4 x 8 kv heads 8.4 / 8.7, 16 x 8 8.4 / 12.4, 256 x 8
+//     32.9 / 38.7, 64 x 32 33.3 / 32.4, 256 x 32 138.8 / 124.8 (the prefix is read again for every
+//     sequence); 1024 tokens: 4 x 8 12.0 / 8.7, 64 x 8 19.1 / 22.4, 64 x 32 59.4 / 52.0
+//   with weights: 4 x 8 kv heads of 256 / 512 / 1024 tokens 7.7 / 10, 9.7 / 9.9, 13.4 / 10.2; calls with ragged
+//     lengths: 256 heads of up to 1024 / 2048 17.2 / 19.6, 28.9 / 28.2; 1024 of 2048 / 4096 (4-bit) 52.7 / 53.2,
+//     113.0 / 112.9
+bool whole_shared(long long B, long long Hkv, long long P, long long Tmax) {
+    return P + Tmax <= 512 && B * Hkv * P <= (1 << 20);
+}
+bool whole_weights(long long B, long long Hkv, int G, long long Tmax) {
+    return G <= 16 && (Tmax <= 512 || (Tmax <= 2048 && Tmax * Tmax <= 4096 * B * Hkv));
+}
+
 long long parts_floats(long long heads, long long ns, long long D) { return heads * ns * (D + 2); }
 
 template <int BITS, int D>
 hipError_t shared(const KvSharedArgs& a, float* work, hipStream_t st) {
     const int G = a.Hq / a.Hkv;
     const long long heads = (long long)a.B * a.Hq, R = (long long)a.B * G;
+    if (whole_shared(a.B, a.Hkv, a.P, a.Tmax)) {
+        hipLaunchKernelGGL((kv_whole_kernel<BITS, D, false>), dim3((unsigned)(a.B * a.Hkv * divup(G, 16))), dim3(kThreads),
+                           0, st, static_cast<const uint16_t*>(a.q), a.dtype == DT_BF16, a.Hq, a.Hkv, a.prefix, a.P, a.Pmax,
+                           a.own, a.lens, a.Tmax, static_cast<uint16_t*>(a.out), nullptr, 0, nullptr, nullptr);
+        return hipGetLastError();
+    }
     const int wq = prefix_wq(R, a.P, a.Tmax);
     DecodeGrid g = {};
     g.P = a.P;
@@ -1105,6 +1200,12 @@ hipError_t weights(const KvWeightsArgs& a, float* work, hipStream_t st) {
     float* po = work + heads * spad;
     float2* ml = reinterpret_cast<float2*>(po + heads * ns * D);
     const int bf16 = a.dtype == DT_BF16;
+    if (whole_weights(a.B, a.Hkv, G, a.Tmax)) {
+        hipLaunchKernelGGL((kv_whole_kernel<BITS, D, true>), dim3((unsigned)(a.B * a.Hkv)), dim3(kThreads), 0, st,
+                           static_cast<const uint16_t*>(a.q), bf16, a.Hq, a.Hkv, KvCache{}, 0, 0, a.own, a.lens, a.Tmax,
+                           static_cast<uint16_t*>(a.out), score, spad, a.weights, a.sums);
+        return hipGetLastError();
+    }
     const unsigned blocks = (unsigned)((long long)a.B * a.Hkv * divup(G, 16) * g.osplit);
     hipLaunchKernelGGL((kv_decode_kernel<BITS, D, 0, true>), dim3(blocks), dim3(kThreads), 0, st,
                        static_cast<const uint16_t*>(a.q), bf16, a.B, a.Hq, a.Hkv, KvCache{}, a.own, a.lens, g, ml, po,
