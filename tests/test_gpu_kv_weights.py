@@ -85,6 +85,24 @@ def test_weights(B, Hq, Hkv, D, lens, Tmax, bits, dtype):
     check(out3, got3, q, k, v, torch.zeros_like(w), lens, bits)
 
 
+@pytest.mark.parametrize("room", [300, 700])
+def test_a_query_that_is_no_number_gives_none(room):
+    """NaN in one sequence's queries, an infinity in one head of another: NaN there, the rest as before."""
+    q, k, v, w = problem(3, 8, 2, 64, room, 8, H, seed=13)
+    lens = torch.tensor([300, 0, 77], dtype=torch.int32, device="cuda")
+    clean, sums = W4.kv_attention_decode_weights(q, k, v, lens, w, 8, sums=torch.zeros_like(w))
+    bad = q.clone()
+    bad[:2] = float("nan")
+    bad[2, 5, 9] = float("inf")
+    out, got = W4.kv_attention_decode_weights(bad, k, v, lens, w, 8, sums=torch.zeros_like(w))
+    torch.cuda.synchronize()
+    assert torch.isnan(out[0]).all() and torch.isnan(out[2, 5]).all() and (out[1] == 0).all()
+    keep = [i for i in range(8) if i != 5]
+    assert torch.equal(out[2, keep], clean[2, keep])
+    assert torch.isnan(got[0, :, :300]).all() and torch.isnan(got[2, 1, :77]).all()
+    assert torch.equal(got[2, 0], sums[2, 0]) and (got[1] == 0).all() and (got[2, :, 77:] == 0).all()
+
+
 def test_each_head_hands_out_one():
     """The weights of a kv head's G queries add up to G."""
     q, k, v, _ = problem(3, 12, 4, 128, 900, 8, H, seed=9)

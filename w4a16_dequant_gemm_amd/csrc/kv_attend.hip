@@ -372,7 +372,7 @@ struct Attend {
         }
 
         l = sum_halves(l);
-        const float m = l > 0.0f ? sub : NEG;              // the reference of l and O
+        const float m = l == 0.0f ? NEG : sub;             // the reference of l and O (NaN: of no number)
         if constexpr (BITS == 4) {
             // lane halves hold elements 0 4 1 5 and 2 6 3 7 of every eight: to 0 .. 3 and 4 .. 7
 #pragma unroll
@@ -806,7 +806,7 @@ struct Stream {
         const float M = fmaxf(fmaxf(sm[0][n], sm[1][n]), fmaxf(sm[2][n], sm[3][n]));
         float Lt = 0.0f;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) Lt += M == NEG ? 0.0f : sl[w][n] * exp2_raw(sm[w][n] - M);
+        for (int w = 0; w < 4; ++w) Lt += M == NEG ? sl[w][n] : sl[w][n] * exp2_raw(sm[w][n] - M);   // (0 or NaN)
         const float f = M == NEG ? 0.0f : exp2_raw(m - M) * (vcap / VNORM * kCodeUnit);
 #pragma unroll
         for (int i = 0; i < OT; ++i)
@@ -825,7 +825,7 @@ struct Stream {
                     uint16_t r[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const float v = Lt > 0.0f ? a[j] / Lt : 0.0f;        // (no token at all: zeros)
+                        const float v = tiles > 0 ? a[j] / Lt : 0.0f;        // (no token at all: zeros)
                         r[j] = bf16 ? f2bf_bits(v) : f2h_bits(v);
                     }
                     // out is aligned to its elements only
@@ -985,21 +985,22 @@ __device__ __forceinline__ void row_stats(const float2* __restrict__ ml, int nsp
     for (int j = lane; j < nsplit; j += 64) {
         const float2 v = ml[j];
         const float mn = fmaxf(m, v.x);
-        if (mn != NEG) l = l * exp2_raw(m - mn) + v.y * exp2_raw(v.x - mn);
+        l = mn == NEG ? l + v.y : l * exp2_raw(m - mn) + v.y * exp2_raw(v.x - mn);     // (at -inf: 0 or NaN)
         m = mn;
     }
     M = wave_max(m);
-    L = wave_sum(m == NEG ? 0.0f : l * exp2_raw(m - M));
+    L = wave_sum(m == NEG ? l : l * exp2_raw(m - M));
 }
 
 // out = sum_j O_j 2^(m_j - M) / sum_j l_j 2^(m_j - M) over the splits j.  One block per query head of
 // the batch: each group of D / 4 threads adds up splits grp, grp + NG, ... (16 bytes a thread, several
-// loads in flight), the groups are added through LDS; a row that saw no token gets zeros.  Bound by the
+// loads in flight), the groups are added through LDS; a row without any token gets zeros, one of scores
+// that are no numbers NaN.  Bound by the
 // latency of two dependent loads, then by the partial outputs' bytes: 2.7 us for 32 heads, 4.2 us
 // for 1024 of 17 splits, 9.3 us (39 MB) for 4096 of up to 18.
 template <int D>
 __device__ __forceinline__ void merge_row(float (*part)[D], long long head, const float2* __restrict__ ml,
-                                          const float* __restrict__ po, int nsplit, int bf16,
+                                          const float* __restrict__ po, int nsplit, int bf16, bool tokens,
                                           uint16_t* __restrict__ out) {
     constexpr int CQ = D / 4, NG = kThreads / CQ;
     const int tid = threadIdx.x, c = tid % CQ, grp = tid / CQ;
@@ -1013,7 +1014,7 @@ __device__ __forceinline__ void merge_row(float (*part)[D], long long head, cons
         const float2 v = mlr[j];
         const f32x4 x = *reinterpret_cast<const f32x4*>(pr + (long long)j * D);
         // an empty split's output is not defined
-        if (v.y > 0.0f) acc += x * exp2_raw(v.x - M);
+        if (v.y != 0.0f) acc += x * exp2_raw(v.x - M);
     }
     *reinterpret_cast<f32x4*>(&part[grp][4 * c]) = acc;
     __syncthreads();
@@ -1021,16 +1022,17 @@ __device__ __forceinline__ void merge_row(float (*part)[D], long long head, cons
         float s = part[0][tid];
 #pragma unroll
         for (int i = 1; i < NG; ++i) s += part[i][tid];
-        const float v = L > 0.0f ? s / L : 0.0f;
+        const float v = tokens ? s / L : 0.0f;
         out[head * D + tid] = bf16 ? f2bf_bits(v) : f2h_bits(v);
     }
 }
 
 template <int D>
 __global__ __launch_bounds__(kThreads) void kv_merge_kernel(const float2* __restrict__ ml, const float* __restrict__ po,
-                                                            int nsplit, int bf16, uint16_t* __restrict__ out) {
+                                                            int nsplit, int bf16, int Hq, int P,
+                                                            const int* __restrict__ lens, uint16_t* __restrict__ out) {
     __shared__ __attribute__((aligned(16))) float part[kThreads / (D / 4)][D];
-    merge_row<D>(part, blockIdx.x, ml, po, nsplit, bf16, out);
+    merge_row<D>(part, blockIdx.x, ml, po, nsplit, bf16, P > 0 || lens[blockIdx.x / Hq] > 0, out);
 }
 
 // Output and accumulated weights in one launch: the first `heads` blocks merge a query head each,
@@ -1051,7 +1053,7 @@ __global__ __launch_bounds__(kThreads) void kv_weights_kernel(const float2* __re
     __shared__ __attribute__((aligned(16))) float part[kThreads / (D / 4)][D];
     __shared__ float2 stat[kStatHeads];                    // a head's maximum and 1 / sum
     if (blockIdx.x < (unsigned)heads) {
-        merge_row<D>(part, blockIdx.x, ml, po, nsplit, bf16, out);
+        merge_row<D>(part, blockIdx.x, ml, po, nsplit, bf16, lens[blockIdx.x / Hq] > 0, out);
         return;
     }
     const int i = blockIdx.x - heads;
@@ -1180,7 +1182,7 @@ hipError_t shared(const KvSharedArgs& a, float* work, hipStream_t st) {
     else W4A16_DECODE(4);
 #undef W4A16_DECODE
     hipLaunchKernelGGL((kv_merge_kernel<D>), dim3((unsigned)heads), dim3(kThreads), 0, st, ml, po, g.nsplit, bf16,
-                       static_cast<uint16_t*>(a.out));
+                       a.Hq, a.P, a.lens, static_cast<uint16_t*>(a.out));
     return hipGetLastError();
 }
 

@@ -407,7 +407,7 @@ constexpr long long kWholeBytes = 65536;
 template <int PR, bool Z>
 static void evict(const KvEvictArgs& a, uint32_t* work, hipStream_t st) {
     if (a.Tmax <= kBatch) {
-        const bool whole = (long long)a.budget * 16 * PR <= kWholeBytes;
+        const bool whole = std::min(a.budget, a.Tmax) * 16LL * PR <= kWholeBytes;
 #define W4A16_SELECT(ROWS)                                                                                            \
     hipLaunchKernelGGL((kv_select_kernel<ROWS, Z>), dim3(a.B * a.Hkv), dim3(kSelThreads), 0, st, a.weights, a.lens,    \
                        a.Hkv, a.Tmax, a.budget, a.recent, a.Tout, a.weights_out, a.lens_out, a.kept, a.in, a.out)
