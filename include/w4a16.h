@@ -403,6 +403,7 @@ int w4a16_kv_attention_decode_batch(const void* q, int dtype, int64_t B, int64_t
  *         hold anything in them.
  * Scores, softmax statistics and outputs are held in fp32; the softmax weights are rounded once to
  * dtype for the product with the values, and the output is rounded once.
+ * A row depends on the tokens up to its own alone, whatever later ones hold (infinities, NaN).
  * Limits: 1 <= B <= 2^20, 1 <= T <= 2^30, (T / 128 + B) * Hq < 2^24, Hq <= 65535.
  */
 int w4a16_attention_prompt(const void* q, const void* k, const void* v, int dtype, int64_t T, int64_t B,

@@ -148,6 +148,35 @@ def test_nan_in_one_sequence_stays_there(dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n,at", [(200, 100), (200, 40), (129, 128), (64, 63), (33, 1), (700, 650)])
+def test_later_tokens_without_numbers_are_not_seen(n, at, D, dtype):
+    """Infinities and NaN in the key and the value of one token: the rows before it as if it were not there,
+    those from it on without numbers where they should be."""
+    q, k, v, cu = packed([n], 2, 1, D, dtype, seed=n + at, fused=False)
+    for what in ("value", "key", "both"):
+        k2, v2 = k.clone(), v.clone()
+        if what != "value":
+            k2[at] = float("nan")
+        if what != "key":
+            v2[at, :, 3] = float("inf")
+            v2[at, :, 9] = float("nan")
+        out = W4.attention_prompt(q, k2, v2, cu)
+        torch.cuda.synchronize()
+        check(out[:at], q[:at], k[:at], v[:at], [at])
+        if what == "value":
+            assert torch.isinf(out[at:, :, 3]).all() and torch.isnan(out[at:, :, 9]).all()
+            some = torch.ones(D, dtype=torch.bool)
+            some[[3, 9]] = False
+            ref, mag = (x[at:, :, some.numpy()] for x in reference(f64(q), f64(k), f64(v), [n]))
+            u = U[dtype]                                   # the bound of check()
+            tol = u * np.abs(ref) + (1 + u) * (u + E) * mag + n * 2.0 ** -25 * np.abs(f64(v)).max()
+            assert (np.abs(f64(out)[at:, :, some.numpy()] - ref) <= tol).all()
+        else:
+            assert torch.isnan(out[at:]).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
 def test_peaked_scores_rising_along_the_row(dtype):
     """Scores that rise by far more than the kernel's rescaling threshold, tile after tile, and
     then fall: the running maximum moves often, and late tiles weigh nothing."""

@@ -119,6 +119,38 @@ __device__ __forceinline__ bool any_lane(bool p) { return __builtin_amdgcn_ballo
 // this wave's loads into LDS have landed, and its reads of LDS are in registers
 __device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory"); }
 
+template <int DT>
+__device__ __forceinline__ float value_of(uint16_t bits) {
+    if constexpr (DT == DT_F16) return h2f(bits);
+    else return bf2f(bits);
+}
+// One row token by token over its first `keys` keys, by a wave: lane l holds elements l and l + 64.
+template <int DT, int D>
+__device__ __forceinline__ void row_by_token(const uint16_t* q, const uint16_t* kb, int ks, const uint16_t* vb, int vs,
+                                             int keys, int lane, uint16_t* out) {
+    constexpr int N = D / 64;
+    const float c = 1.4426950408889634f / sqrtf((float)D);
+    float qv[N], o[N], M = -__builtin_inff(), l = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        qv[i] = value_of<DT>(q[lane + 64 * i]);
+        o[i] = 0.0f;
+    }
+    for (int j = 0; j < keys; ++j) {
+        float s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) s = fmaf(qv[i], value_of<DT>(kb[(long long)j * ks + lane + 64 * i]), s);
+        s = wave_sum(s);
+        const float Mn = fmaxf(M, s), f = M == Mn ? 1.0f : exp2_raw((M - Mn) * c), p = exp2_raw((s - Mn) * c);
+        M = Mn;
+        l = fmaf(l, f, p);
+#pragma unroll
+        for (int i = 0; i < N; ++i) o[i] = fmaf(o[i], f, p * value_of<DT>(vb[(long long)j * vs + lane + 64 * i]));
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) out[lane + 64 * i] = (uint16_t)pack2<DT>(o[i] / l, 0.0f);
+}
+
 // Pipeline: in iteration t a wave turns the scores of tile t into weights while the matrix cores work
 // on the scores of tile t + 1 (independent instructions, interleaved), then multiplies the weights
 // with V(t).  One barrier an iteration: at its top every wave has waited for its own loads of the
@@ -361,7 +393,16 @@ __global__ __launch_bounds__(256, 2) void attention_prompt_kernel(
     for (; t < ntiles; ++t) turn(t, t & 1 ? K1 : K0, t & 1 ? V0 : V1);
 
     l = sum_halves(l);
-    if (row < len) {
+    // A key behind a row has weight 0, but the matrix cores multiply that with the key's value: a row
+    // without numbers whose sum is one may owe that to an infinity or NaN that it does not see.
+    bool odd = false;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; e += 2) odd |= __builtin_isunordered(o[i][e], o[i][e + 1]);
+    const unsigned long long om = __builtin_amdgcn_ballot_w64(odd && l == l && row < len);
+    const uint32_t redo = (uint32_t)om | (uint32_t)(om >> 32);
+    if (row < len && !(redo >> n & 1)) {
         const float inv = 1.0f / l;
         uint16_t* op = out + (long long)(s0 + row) * Hq * D + head * D + 4 * h;
 #pragma unroll
@@ -371,6 +412,11 @@ __global__ __launch_bounds__(256, 2) void attention_prompt_kernel(
                 *reinterpret_cast<u32x2*>(op + 32 * i + 8 * g) =
                     u32x2{pack2<DT>(o[i][4 * g] * inv, o[i][4 * g + 1] * inv),
                           pack2<DT>(o[i][4 * g + 2] * inv, o[i][4 * g + 3] * inv)};
+    }
+    for (uint32_t left = redo; left != 0; left &= left - 1) {
+        const int r = __builtin_ctz(left);
+        const long long at = (long long)(s0 + wrow + r);
+        row_by_token<DT, D>(q + at * qs + head * D, kb, ks, vb, vs, wrow + r + 1, lane, out + at * Hq * D + head * D);
     }
 }
 
