@@ -429,8 +429,8 @@ typedef struct {
     uint16_t *vscales, *vzeros;
 } w4a16_kv_cache_out;
 
-/* fp32 elements of the w4a16_kv_attention_decode_shared workspace (host only), or a negative
- * status. */
+/* fp32 elements of the w4a16_kv_attention_decode_shared workspace (host only; 0: none, for short
+ * sequences), or a negative status. */
 int64_t w4a16_kv_attention_shared_workspace(int64_t B, int64_t Hq, int64_t Hkv, int64_t P, int64_t Tmax,
                                             int64_t D);
 
@@ -447,7 +447,8 @@ int64_t w4a16_kv_attention_shared_workspace(int64_t B, int64_t Hq, int64_t Hkv, 
  *   lengths  device int32 [B]; each value is clamped into [0, Tmax] on the device.  A sequence with
  *            P + lengths[b] == 0 gets zeros; a query that is no number gets NaN and leaves the others alone.
  *   work     w4a16_kv_attention_shared_workspace(...) fp32 elements, 16-byte aligned (scratch,
- *            contents undefined after the call; calls that overlap on one buffer race).
+ *            contents undefined after the call; calls that overlap on one buffer race), or NULL when
+ *            that is 0.
  * Scores, softmax statistics and sums are fp32; the codes less their zero points (|z| <= 2048) are
  * exact, the softmax weights times V's scales are rounded once to fp16 (relative 2^-11) for the
  * product with them, and the output is rounded once.  bf16 queries are scaled by a power of two

@@ -245,7 +245,9 @@ def test_refusals():
     with pytest.raises(ValueError):
         run(q, kp, vp, 10, k, v, lt.cpu(), 8)
     with pytest.raises(ValueError):
-        run(q, kp, vp, 10, k, v, lt, 8, work=torch.empty(3, device="cuda"))
+        run(q, kp, vp, 10, k, v, lt, 8, work=torch.empty(3, device="cuda", dtype=H))
+    with pytest.raises(ValueError):                         # (room for 600 own tokens needs some)
+        run(q, kp, vp, 10, *problem(2, 4, 2, 64, 10, 600, 8, H, seed=57)[3:], lt, 8, work=torch.empty(3, device="cuda"))
     with pytest.raises(ValueError):
         run(q, kp, vp, 10, k, v, lt, 8, out=torch.empty((2, 4, 32), dtype=H, device="cuda"))
     with pytest.raises(W4.W4A16Error):

@@ -638,21 +638,29 @@ def _cache_shape(cache, name: str, bits: int, lead: int, D: int, dev: int):
     return shape
 
 
+_INT8, _INT32, _HALF = torch.int8, torch.int32, torch.float16
+
+
 def _need_caches(k, v, kname: str, vname: str, bits: int, lead: int, D: int, like: torch.Tensor):
     """A K and a V cache of one shape on the device of ``like``; returns the shape of their scales."""
     if bits != 8 and bits != 4:
         raise ValueError("bits must be 8 or 4")
     dev = like.get_device()
     (kc, ks, kz), (vc, vs, vz) = k, v
-    if bits == 8 and isinstance(kc, torch.Tensor) and isinstance(ks, torch.Tensor) and isinstance(
-            vc, torch.Tensor) and isinstance(vs, torch.Tensor):
+    if isinstance(kc, torch.Tensor) and isinstance(ks, torch.Tensor) and isinstance(vc, torch.Tensor) and isinstance(
+            vs, torch.Tensor):
         # the usual case in one expression; anything else is looked at piece by piece below
         shape = ks.shape
-        want = (*shape, D)
-        if (len(shape) == lead + 1 and kc.dtype == vc.dtype == torch.int8 and ks.dtype == vs.dtype == torch.float16
+        want = (*shape, D if bits == 8 else D // 8)
+        code = _INT8 if bits == 8 else _INT32
+        if (len(shape) == lead + 1 and kc.dtype is code and vc.dtype is code and ks.dtype is _HALF and vs.dtype is _HALF
                 and vs.shape == shape and kc.shape == want and vc.shape == want
                 and dev == kc.get_device() == ks.get_device() == vc.get_device() == vs.get_device()
-                and kc.is_contiguous() and ks.is_contiguous() and vc.is_contiguous() and vs.is_contiguous()):
+                and kc.is_contiguous() and ks.is_contiguous() and vc.is_contiguous() and vs.is_contiguous()
+                and (bits == 8 or (isinstance(kz, torch.Tensor) and isinstance(vz, torch.Tensor) and kz.dtype is _HALF
+                                   and vz.dtype is _HALF and kz.shape == shape and vz.shape == shape
+                                   and dev == kz.get_device() == vz.get_device() and kz.is_contiguous()
+                                   and vz.is_contiguous()))):
             return shape
     shape = _cache_shape(k, kname, bits, lead, D, dev)
     if _cache_shape(v, vname, bits, lead, D, dev) != shape:
@@ -686,7 +694,7 @@ def _decode_out(out, q: torch.Tensor) -> torch.Tensor:
 
 
 def kv_attention_shared_workspace(B: int, Hq: int, Hkv: int, P: int, Tmax: int, D: int) -> int:
-    """fp32 elements of the scratch buffer that :func:`kv_attention_decode_shared` needs."""
+    """fp32 elements of the scratch buffer that :func:`kv_attention_decode_shared` needs (0: none)."""
     need = lib().w4a16_kv_attention_shared_workspace(B, Hq, Hkv, P, Tmax, D)
     if need < 0:
         raise W4A16Error(int(need), "w4a16_kv_attention_shared_workspace")
@@ -717,7 +725,8 @@ def kv_attention_decode_shared(q: torch.Tensor, kprefix, vprefix, P: int, kcache
     then the first ``lengths[b]`` (int32, on the device, possibly 0) of the sequence's own
     ``[B, Hkv, Tmax, ...]``.  The prefix is held and read once for the batch.  A sequence without any
     token gets zeros.  ``work`` is an optional fp32 buffer of at least
-    :func:`kv_attention_shared_workspace` elements; calls that may overlap need one each."""
+    :func:`kv_attention_shared_workspace` elements (0 for short sequences); calls that may overlap
+    need one each."""
     dt = _dtype_code(q)
     _need(q, "q", q.dtype, 3)
     _need(lengths, "lengths", torch.int32, 1)
@@ -731,11 +740,12 @@ def kv_attention_decode_shared(q: torch.Tensor, kprefix, vprefix, P: int, kcache
         raise ValueError("P must be in [0, Pmax]")
     L = lib()
     out = _decode_out(out, q)
-    work = _work(work, L.w4a16_kv_attention_shared_workspace(B, Hq, Hkv, P, Tmax, D),
-                 "w4a16_kv_attention_shared_workspace", q)
+    need = L.w4a16_kv_attention_shared_workspace(B, Hq, Hkv, P, Tmax, D)
+    if need or work is not None:
+        work = _work(work, need, "w4a16_kv_attention_shared_workspace", q)
     _call(L.w4a16_kv_attention_decode_shared, "w4a16_kv_attention_decode_shared", q.device, q.data_ptr(), dt, B, Hq,
           Hkv, D, bits, _cache_struct(kprefix, vprefix, bits), P, Pmax, _cache_struct(kcache, vcache, bits),
-          lengths.data_ptr(), Tmax, work.data_ptr(), out.data_ptr())
+          lengths.data_ptr(), Tmax, None if work is None else work.data_ptr(), out.data_ptr())
     return out
 
 

@@ -477,10 +477,11 @@ int w4a16_kv_attention_decode_shared(const void* q, int dtype, int64_t B, int64_
                                      int bits, const w4a16_kv_cache* prefix, int64_t P, int64_t Pmax,
                                      const w4a16_kv_cache* own, const int32_t* lengths, int64_t Tmax, float* work,
                                      void* out, void* stream) {
-    if (!q || !own || !lengths || !work || !out) return W4A16_ERR_NULL;
+    if (!q || !own || !lengths || !out) return W4A16_ERR_NULL;
     if (dtype != W4A16_F16 && dtype != W4A16_BF16) return W4A16_ERR_DTYPE;
     if (bits != 8 && bits != 4) return W4A16_ERR_SCHEME;
     int st = check_kv_batch(B, Hq, Hkv, P, Pmax, Tmax, D);
+    if (st == W4A16_OK && !work && w4a16::kv_shared_workspace_floats(B, Hq, Hkv, P, Tmax, D) > 0) st = W4A16_ERR_NULL;
     if (st == W4A16_OK) st = check_cache(own, bits);
     if (st == W4A16_OK && P > 0) st = check_cache(prefix, bits);
     if (st != W4A16_OK) return st;

@@ -1223,6 +1223,7 @@ hipError_t weights(const KvWeightsArgs& a, float* work, hipStream_t st) {
 
 long long kv_shared_workspace_floats(long long B, long long Hq, long long Hkv, long long P, long long Tmax,
                                      long long D) {
+    if (whole_shared(B, Hkv, P, Tmax)) return 0;
     return parts_floats(B * Hq, divup(P, prefix_chunk(B, Hq, Hkv, P, Tmax)) + divup(Tmax, own_chunk(B, Hq, Hkv, Tmax)), D);
 }
 
