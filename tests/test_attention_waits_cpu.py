@@ -23,8 +23,8 @@ def test_barriers_wait_for_the_tiles(tmp_path):
            os.path.join(build.CSRC, "attention.hip"), "-o", str(out)]
     res = subprocess.run(cmd, capture_output=True, text=True)
     assert res.returncode == 0, res.stderr[-2000:]
-    kernels = re.findall(r"^(_ZN\S*attention_prompt_kernel\S*):\s*; @.*?$(.*?)s_endpgm", out.read_text(), re.M | re.S)
-    assert len(kernels) == 4
+    kernels = re.findall(r"^(_ZN\S*attention_prompt_kernel\S*):\s*; @.*?$(.*?)^\.Lfunc_end", out.read_text(), re.M | re.S)
+    assert len(kernels) == 8
     for name, body in kernels:
         loads = barriers = 0
         pending = False

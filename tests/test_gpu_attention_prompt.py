@@ -92,7 +92,11 @@ CASES = [([1], 1, 1, 64, torch.float16), ([1, 1, 1], 8, 2, 128, torch.bfloat16),
          ([63, 64, 65], 3, 1, 128, torch.float16), ([127, 128, 129], 2, 2, 128, torch.bfloat16),
          ([0, 5, 0, 0, 70, 0], 6, 2, 64, torch.float16), ([255, 256, 257, 1], 8, 1, 128, torch.float16),
          ([513], 4, 2, 64, torch.float16), ([1000, 3, 200], 2, 1, 128, torch.bfloat16),
-         ([0], 2, 1, 64, torch.float16), ([1537], 2, 2, 128, torch.float16)]
+         ([0], 2, 1, 64, torch.float16), ([1537], 2, 2, 128, torch.float16),
+         # few blocks of many tiles: two groups of waves, the second with and without tiles of its own
+         ([1024], 2, 1, 64, torch.bfloat16), ([1025], 4, 2, 128, torch.bfloat16), ([2047, 1], 2, 2, 64, torch.float16),
+         ([1, 2047], 1, 1, 128, torch.float16), ([0, 2111, 33, 960], 3, 1, 128, torch.bfloat16), ([1900, 64, 0], 2, 1, 64, torch.float16),
+         ([1023], 4, 2, 128, torch.bfloat16)]
 
 
 @pytest.mark.parametrize("lens,Hq,Hkv,D,dtype", CASES)
@@ -149,7 +153,7 @@ def test_nan_in_one_sequence_stays_there(dtype):
 
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
 @pytest.mark.parametrize("D", [64, 128])
-@pytest.mark.parametrize("n,at", [(200, 100), (200, 40), (129, 128), (64, 63), (33, 1), (700, 650)])
+@pytest.mark.parametrize("n,at", [(200, 100), (200, 40), (129, 128), (64, 63), (33, 1), (700, 650), (1300, 1290), (1200, 1)])
 def test_later_tokens_without_numbers_are_not_seen(n, at, D, dtype):
     """Infinities and NaN in the key and the value of one token: the rows before it as if it were not there,
     those from it on without numbers where they should be."""
@@ -177,10 +181,11 @@ def test_later_tokens_without_numbers_are_not_seen(n, at, D, dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
-def test_peaked_scores_rising_along_the_row(dtype):
+@pytest.mark.parametrize("n", [700, 1400])
+def test_peaked_scores_rising_along_the_row(dtype, n):
     """Scores that rise by far more than the kernel's rescaling threshold, tile after tile, and
     then fall: the running maximum moves often, and late tiles weigh nothing."""
-    n, D = 700, 64
+    D = 64
     g = torch.Generator().manual_seed(3)
     q = torch.randn((n, 1, D), generator=g)
     k = torch.randn((n, 1, D), generator=g)
@@ -195,9 +200,10 @@ def test_peaked_scores_rising_along_the_row(dtype):
     check(out, q, k, v, [n], e=4.8e-4)
 
 
-def test_large_finite_scores_give_the_largest_key():
+@pytest.mark.parametrize("n", [130, 1400])
+def test_large_finite_scores_give_the_largest_key(n):
     """fp16 inputs near the type's largest value: scores of 1e10 and more, one key wins outright."""
-    n, D = 130, 64
+    D = 64
     q = torch.full((n, 1, D), 60000.0, dtype=torch.float16, device="cuda")
     k = torch.full((n, 1, D), -60000.0, dtype=torch.float16, device="cuda")
     k[0] = 60000.0

@@ -24,7 +24,7 @@
 // instructions, not what hides them, would shorten it: raised issue priorities, the maximum interleaved
 // with the second product and stores of the output through LDS changed nothing.  12 packed prompts of
 // up to 1024 tokens, fp16: 40 us, the longest block's 16 tiles of keys; 6 of up to 96: 6 us, latency.
-// One prompt of 128 / 512 / 1024 / 2048 / 4096 tokens: 8.5 / 15 / 26 / 54 / 173 us.  Before the loads went
+// One prompt of 128 / 512 / 1024 / 2048 / 4096 tokens: 8.8 / 16 / 24 / 51 / 154 us.  Before the loads went
 // straight to LDS and the scores of the next tile under the weights of this one: 2313 and 49 us.
 #include "attn.h"
 #include "launch.h"
@@ -157,15 +157,22 @@ __device__ __forceinline__ void row_by_token(const uint16_t* q, const uint16_t* 
 // previous one, so K(t + 1) and V(t) are complete, and K(t) and V(t - 1) have been read; K(t + 2) and
 // V(t + 1) are loaded over them.  The two buffers of K and of V are four LDS objects, so that the
 // compiler does not make a read of one wait for loads into another.
-template <int DT, int D>
-__global__ __launch_bounds__(256, 2) void attention_prompt_kernel(
+//
+// GROUPS == 2: eight waves, the first four take the first half of the keys and the others the rest, each
+// with buffers of its own; the second four leave their outputs in LDS and the first add them to theirs.
+template <int DT, int D, int GROUPS>
+__global__ __launch_bounds__(256 * GROUPS, 2) void attention_prompt_kernel(
     const uint16_t* __restrict__ q, const uint16_t* __restrict__ k, const uint16_t* __restrict__ v,
     const int* __restrict__ cu, int B, int T, int Hq, int Hkv, int qs, int ks, int vs, int tiles,
     uint16_t* __restrict__ out) {
     using L = TileLoad<D>;
-    __shared__ __attribute__((aligned(16))) uint16_t K0[kKeys * D], K1[kKeys * D], V0[kKeys * D], V1[kKeys * D];
+    constexpr int TILE = kKeys * D;
+    __shared__ __attribute__((aligned(16))) uint16_t lK0[GROUPS * TILE], lK1[GROUPS * TILE], lV0[GROUPS * TILE],
+        lV1[GROUPS * TILE];
 
-    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6) & 3, grp = __builtin_amdgcn_readfirstlane(tid >> 8);
+    uint16_t *K0 = lK0 + grp * TILE, *K1 = lK1 + grp * TILE, *V0 = lV0 + grp * TILE, *V1 = lV1 + grp * TILE;
     const int n = lane & 31, h = lane >> 5;
     // the tiles with most keys first; heads vary fastest
     const int head = blockIdx.x % Hq, tile = blockIdx.x / Hq;
@@ -175,9 +182,16 @@ __global__ __launch_bounds__(256, 2) void attention_prompt_kernel(
         return;
     const int kvh = head / (Hq / Hkv);
 
-    const int ntiles = (min(row0 + kRows, len) + kKeys - 1) / kKeys;
-    const uint16_t* kb = k + (long long)s0 * ks + kvh * D;
-    const uint16_t* vb = v + (long long)s0 * vs + kvh * D;
+    const int alltiles = (min(row0 + kRows, len) + kKeys - 1) / kKeys;
+    // the group's tiles are tile0, tile0 + 1, ...; tiles, keys and rows count from there on below
+    const int half = GROUPS == 2 ? (alltiles + 1) / 2 : alltiles;
+    const int tile0 = grp * half, ntiles = grp ? alltiles - half : half, turns = half;
+    const int key0 = tile0 * kKeys;
+    const uint16_t* kall = k + (long long)s0 * ks + kvh * D;
+    const uint16_t* vall = v + (long long)s0 * vs + kvh * D;
+    const uint16_t* kb = kall + (long long)key0 * ks;
+    const uint16_t* vb = vall + (long long)key0 * vs;
+    const int keys = len - key0;
     int koff[L::NI], voff[L::NI];                   // byte offsets in a tile
     // rows behind the sequence are replaced by its last one: they may hold anything
     auto k_offsets = [&](int last) {
@@ -194,16 +208,16 @@ __global__ __launch_bounds__(256, 2) void attention_prompt_kernel(
             voff[i] = (min(r, last) * vs + 8 * swz_v<D>(r, lane % L::CH)) * 2;
         }
     };
-    k_offsets(len - 1);
-    v_offsets(len - 1);
+    k_offsets(keys - 1);
+    v_offsets(keys - 1);
     auto load_k = [&](int t, uint16_t* lds) {
         if (t >= ntiles) return;
-        if (t > 0 && (t + 1) * kKeys > len) k_offsets(len - 1 - t * kKeys);       // the last tile
+        if (t > 0 && (t + 1) * kKeys > keys) k_offsets(keys - 1 - t * kKeys);     // the last tile
         L::issue(kb + (long long)t * kKeys * ks, koff, lds, wave);
     };
     auto load_v = [&](int t, uint16_t* lds) {
         if (t >= ntiles) return;
-        if (t > 0 && (t + 1) * kKeys > len) v_offsets(len - 1 - t * kKeys);
+        if (t > 0 && (t + 1) * kKeys > keys) v_offsets(keys - 1 - t * kKeys);
         L::issue(vb + (long long)t * kKeys * vs, voff, lds, wave);
     };
     load_k(0, K0);
@@ -218,7 +232,7 @@ __global__ __launch_bounds__(256, 2) void attention_prompt_kernel(
         for (int s = 0; s < D / 16; ++s) qf[s] = *reinterpret_cast<const u32x4*>(qp + 16 * s);
     }
     // tiles with a key that some row of the wave sees; only the last of them needs a mask
-    const int own = wrow < len ? min(wrow + 31, len - 1) / kKeys + 1 : 0;
+    const int own = wrow < len ? min(max(min(wrow + 31, len - 1) / kKeys + 1 - tile0, 0), ntiles) : 0;
 
     f32x16 o[D / 32];
 #pragma unroll
@@ -355,7 +369,7 @@ __global__ __launch_bounds__(256, 2) void attention_prompt_kernel(
     // the wave's last tile, the only one with a key behind one of its rows
     auto last_step = [&](int t, uint16_t* Kl, const uint16_t* Vc, uint16_t* Vl, f32x16 (&S)[2]) {
         turn(t, Kl, Vl);
-        const int seen = row - 4 * h - t * kKeys;       // (one register to compare constants with)
+        const int seen = row - key0 - 4 * h - t * kKeys;       // (one register to compare constants with)
 #pragma unroll
         for (int kb2 = 0; kb2 < 2; ++kb2)
 #pragma unroll
@@ -390,9 +404,37 @@ __global__ __launch_bounds__(256, 2) void attention_prompt_kernel(
             t += 1;
         }
     }
-    for (; t < ntiles; ++t) turn(t, t & 1 ? K1 : K0, t & 1 ? V0 : V1);
+    for (; t < turns; ++t) turn(t, t & 1 ? K1 : K0, t & 1 ? V0 : V1);
 
     l = sum_halves(l);
+    if constexpr (GROUPS == 2) {
+        __shared__ float2 stat[4][64];
+        float* joint = reinterpret_cast<float*>(wave == 0 ? lK0 : wave == 1 ? lK1 : wave == 2 ? lV0 : lV1) + 4 * lane;
+        static_assert(GROUPS * TILE * 2 >= 32 * D * 4, "a wave's output");
+        __syncthreads();                            // everyone is done with K and V
+        if (grp == 1) {
+            stat[wave][lane] = make_float2(M, l);
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+                for (int g = 0; g < 4; ++g)
+                    *reinterpret_cast<f32x4*>(joint + 256 * (4 * i + g)) =
+                        f32x4{o[i][4 * g], o[i][4 * g + 1], o[i][4 * g + 2], o[i][4 * g + 3]};
+        }
+        __syncthreads();
+        if (grp == 1) return;
+        const float2 other = stat[wave][lane];
+        const float Mn = fmaxf(M, other.x), f0 = exp2_raw((M - Mn) * c), f1 = exp2_raw((other.x - Mn) * c);
+        l = l * f0 + other.y * f1;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const f32x4 x = *reinterpret_cast<const f32x4*>(joint + 256 * (4 * i + g));
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[i][4 * g + j] = fmaf(o[i][4 * g + j], f0, x[j] * f1);
+            }
+    }
     // A key behind a row has weight 0, but the matrix cores multiply that with the key's value: a row
     // without numbers whose sum is one may owe that to an infinity or NaN that it does not see.
     bool odd = false;
@@ -416,17 +458,29 @@ __global__ __launch_bounds__(256, 2) void attention_prompt_kernel(
     for (uint32_t left = redo; left != 0; left &= left - 1) {
         const int r = __builtin_ctz(left);
         const long long at = (long long)(s0 + wrow + r);
-        row_by_token<DT, D>(q + at * qs + head * D, kb, ks, vb, vs, wrow + r + 1, lane, out + at * Hq * D + head * D);
+        row_by_token<DT, D>(q + at * qs + head * D, kall, ks, vall, vs, wrow + r + 1, lane, out + at * Hq * D + head * D);
     }
+}
+
+// Two groups of waves a block where the blocks leave the GPU half empty and most have many tiles.  One /
+// two groups, us: 8 heads, D = 64, one prompt of 512 / 1024 / 4096 tokens 11.3 / 11.1, 17.5 / 15.7, 53.1 / 41.6;
+// 32 heads, D = 128, of 512 / 1024 / 1536 / 2048 / 3000 16.2 / 16.7, 26.0 / 24.4, 37.1 / 35.6, 51.4 / 51.3,
+// 89.6 / 102.6; 12 of up to 1024, 8 heads 17.0 / 20.3.
+bool split_keys(const PromptArgs& a) {
+    return (a.T / kRows + a.B) * (long long)a.Hq <= 448 && a.T >= 1024LL * a.B;
 }
 
 template <int DT, int D>
 hipError_t prompt(const PromptArgs& a, hipStream_t st) {
     const int tiles = a.T / kRows + a.B;
-    hipLaunchKernelGGL((attention_prompt_kernel<DT, D>), dim3((unsigned)tiles * a.Hq), dim3(256), 0, st,
-                       static_cast<const uint16_t*>(a.q), static_cast<const uint16_t*>(a.k),
-                       static_cast<const uint16_t*>(a.v), a.cu, a.B, a.T, a.Hq, a.Hkv, a.qs, a.ks, a.vs, tiles,
-                       static_cast<uint16_t*>(a.out));
+#define W4A16_PROMPT(GROUPS)                                                                                          \
+    hipLaunchKernelGGL((attention_prompt_kernel<DT, D, GROUPS>), dim3((unsigned)tiles * a.Hq), dim3(256 * GROUPS), 0,  \
+                       st, static_cast<const uint16_t*>(a.q), static_cast<const uint16_t*>(a.k),                       \
+                       static_cast<const uint16_t*>(a.v), a.cu, a.B, a.T, a.Hq, a.Hkv, a.qs, a.ks, a.vs, tiles,        \
+                       static_cast<uint16_t*>(a.out))
+    if (split_keys(a)) W4A16_PROMPT(2);
+    else W4A16_PROMPT(1);
+#undef W4A16_PROMPT
     return hipGetLastError();
 }
 
