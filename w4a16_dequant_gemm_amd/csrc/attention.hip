@@ -155,8 +155,9 @@ __device__ __forceinline__ void row_by_token(const uint16_t* q, const uint16_t* 
 // on the scores of tile t + 1 (independent instructions, interleaved), then multiplies the weights
 // with V(t).  One barrier an iteration: at its top every wave has waited for its own loads of the
 // previous one, so K(t + 1) and V(t) are complete, and K(t) and V(t - 1) have been read; K(t + 2) and
-// V(t + 1) are loaded over them.  The two buffers of K and of V are four LDS objects, so that the
-// compiler does not make a read of one wait for loads into another.
+// V(t + 1) are loaded over them.  The first two tiles are asked for at once (1 - 6 % for short prompts).
+// The two buffers of K and of V are four LDS objects, so that the compiler does not make a read of one
+// wait for loads into another.
 //
 // GROUPS == 2: eight waves, the first four take the first half of the keys and the others the rest, each
 // with buffers of its own; the second four leave their outputs in LDS and the first add them to theirs.
@@ -222,6 +223,8 @@ __global__ __launch_bounds__(256 * GROUPS, 2) void attention_prompt_kernel(
     };
     load_k(0, K0);
     load_v(0, V0);
+    load_k(1, K1);
+    load_v(1, V1);
 
     const int wrow = row0 + 32 * wave;              // first row of the wave
     const int row = wrow + n;                       // the lane's row (behind the sequence: not stored)
@@ -349,12 +352,12 @@ __global__ __launch_bounds__(256 * GROUPS, 2) void attention_prompt_kernel(
             a1 = n1;
         }
     };
-    // top of iteration t: Kl takes K(t + 2), Vl takes V(t + 1)
+    // top of iteration t: Kl takes K(t + 2), Vl takes V(t + 1) (V(1) is there from the start)
     auto turn = [&](int t, uint16_t* Kl, uint16_t* Vl) {
         wait_loads();
         __syncthreads();
         load_k(t + 2, Kl);
-        load_v(t + 1, Vl);
+        if (t > 0) load_v(t + 1, Vl);
     };
     // iteration t where the wave sees tile t + 1 too: Kn = K(t + 1), Vc = V(t)
     auto full_step = [&](int t, const uint16_t* Kn, uint16_t* Kl, const uint16_t* Vc, uint16_t* Vl, f32x16 (&S)[2],
@@ -385,7 +388,6 @@ __global__ __launch_bounds__(256 * GROUPS, 2) void attention_prompt_kernel(
     f32x16 Sa[2], Sb[2];
     wait_loads();
     __syncthreads();
-    load_k(1, K1);
     // A block's rows begin at a multiple of two tiles, so its waves 0 and 1 end in an even tile and
     // waves 2 and 3 in the odd one after it; a wave without rows only keeps the barriers.
     int t = 0;
