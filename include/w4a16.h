@@ -460,8 +460,8 @@ int w4a16_kv_attention_decode_shared(const void* q, int dtype, int64_t B, int64_
                                      const w4a16_kv_cache* own, const int32_t* lengths, int64_t Tmax, float* work,
                                      void* out, void* stream);
 
-/* fp32 elements of the w4a16_kv_attention_decode_weights workspace (host only), or a negative
- * status. */
+/* fp32 elements of the w4a16_kv_attention_decode_weights workspace (host only; 0: none, for short
+ * sequences), or a negative status. */
 int64_t w4a16_kv_attention_weights_workspace(int64_t B, int64_t Hq, int64_t Hkv, int64_t Tmax, int64_t D);
 
 /*
@@ -474,7 +474,8 @@ int64_t w4a16_kv_attention_weights_workspace(int64_t B, int64_t Hq, int64_t Hkv,
  *            length 0 gets zeros.
  *   weights  [B, Hkv, Tmax] fp32, or NULL: the sums start from 0.
  *   sums     [B, Hkv, Tmax] fp32; may be `weights` (accumulation in place).
- *   work     w4a16_kv_attention_weights_workspace(...) fp32 elements, 16-byte aligned (scratch).
+ *   work     w4a16_kv_attention_weights_workspace(...) fp32 elements, 16-byte aligned (scratch), or NULL
+ *            when that is 0.
  * q, out, caches, arithmetic and limits as for w4a16_kv_attention_decode_shared without a prefix
  * (B * Hq * Tmax <= 2^36 besides).
  */

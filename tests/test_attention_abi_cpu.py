@@ -149,7 +149,8 @@ def test_workspaces(lib):
     assert need(2, 8, 3, 10, 8, 64) == L.ERR_SHAPE and need(2, 8, 4, -1, 8, 64) == L.ERR_SHAPE
     assert need(2, 8, 4, 10, 0, 64) == L.ERR_SHAPE and need(2, 8, 4, 10, 8, 65) == L.ERR_SHAPE
     need = lib.w4a16_kv_attention_weights_workspace
-    assert need(2, 8, 4, 9, 64) >= 2 * 8 * (9 + 64 + 2)
+    assert need(2, 8, 4, 1000, 64) >= 2 * 8 * (1000 + 64 + 2) and need(2, 34, 2, 9, 64) >= 2 * 34 * (9 + 64 + 2)
+    assert need(2, 8, 4, 512, 64) == 0 and need(200, 8, 4, 1000, 64) >= 200 * 8 * 1000
     assert need(2, 8, 3, 9, 64) == L.ERR_SHAPE and need(0, 8, 4, 9, 64) == L.ERR_SHAPE
     assert need(65535, 256, 4, 1 << 13, 64) == L.ERR_SHAPE
     need = lib.w4a16_kv_evict_workspace

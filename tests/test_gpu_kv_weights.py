@@ -120,10 +120,12 @@ def test_agrees_with_the_batched_decode():
     assert (out.float() - ref.float()).abs().max() <= 4 * 2.0 ** -11 * max(1.0, ref.float().abs().max().item())
 
 
-def test_work_buffer_and_repeat():
-    q, k, v, w = problem(2, 8, 2, 64, 333, 8, BF, seed=11)
-    lens = torch.tensor([333, 100], dtype=torch.int32, device="cuda")
-    need = W4.kv_attention_weights_workspace(2, 8, 2, 333, 64)
+@pytest.mark.parametrize("B,T", [(2, 333), (2, 900), (140, 900)])
+def test_work_buffer_and_repeat(B, T):
+    """None, one for splits and one for the scores alone: nothing behind its end is written."""
+    q, k, v, w = problem(B, 8, 2, 64, T, 8, BF, seed=11)
+    lens = torch.tensor([T, 100] + [T - 3 * i for i in range(B - 2)], dtype=torch.int32, device="cuda")
+    need = W4.kv_attention_weights_workspace(B, 8, 2, T, 64)
     work = torch.full((need + 4,), float("nan"), device="cuda")
     s1, s2 = torch.zeros_like(w), torch.zeros_like(w)
     a, _ = W4.kv_attention_decode_weights(q, k, v, lens, w, 8, sums=s1, work=work)
@@ -147,7 +149,9 @@ def test_refusals():
     with pytest.raises(ValueError):
         run(q, k, tuple(t[:, :, :5].contiguous() if t is not None else None for t in v), lt, w, 8)
     with pytest.raises(ValueError):
-        run(q, k, v, lt, w, 8, work=torch.empty(1, device="cuda"))
+        run(q, k, v, lt, w, 8, work=torch.empty(1, device="cuda", dtype=H))
+    with pytest.raises(ValueError):                          # (room for 600 tokens needs some)
+        run(*problem(2, 4, 2, 64, 600, 8, H, seed=14)[:3], lt, None, 8, work=torch.empty(1, device="cuda"))
     big = torch.zeros(w.numel() + 3, device="cuda")
     with pytest.raises(W4.W4A16Error):                       # sums overlap weights, but are not they
         run(q, k, v, lt, big[:w.numel()].view_as(w), 8, sums=big[3:].view_as(w))

@@ -702,7 +702,7 @@ def kv_attention_shared_workspace(B: int, Hq: int, Hkv: int, P: int, Tmax: int, 
 
 
 def kv_attention_weights_workspace(B: int, Hq: int, Hkv: int, Tmax: int, D: int) -> int:
-    """fp32 elements of the scratch buffer that :func:`kv_attention_decode_weights` needs."""
+    """fp32 elements of the scratch buffer that :func:`kv_attention_decode_weights` needs (0: none)."""
     need = lib().w4a16_kv_attention_weights_workspace(B, Hq, Hkv, Tmax, D)
     if need < 0:
         raise W4A16Error(int(need), "w4a16_kv_attention_weights_workspace")
@@ -759,7 +759,7 @@ def kv_attention_decode_weights(q: torch.Tensor, kcache, vcache, lengths: torch.
     ``t < lengths[b]`` (entries behind are not written), fp32 ``[B, Hkv, Tmax]``.  ``sums`` defaults to
     ``weights``, which is then updated in place; ``weights=None`` starts from 0 (``sums`` defaults to
     a zero tensor then).  A sequence of length 0 gets zeros.  ``work`` is an optional fp32 buffer of at
-    least :func:`kv_attention_weights_workspace` elements."""
+    least :func:`kv_attention_weights_workspace` elements (0 for short sequences)."""
     dt = _dtype_code(q)
     _need(q, "q", q.dtype, 3)
     _need(lengths, "lengths", torch.int32, 1)
@@ -777,11 +777,13 @@ def kv_attention_decode_weights(q: torch.Tensor, kcache, vcache, lengths: torch.
     _same_device(q, "q", lengths=lengths, weights=weights, sums=sums)
     L = lib()
     out = _decode_out(out, q)
-    work = _work(work, L.w4a16_kv_attention_weights_workspace(B, Hq, Hkv, Tmax, D),
-                 "w4a16_kv_attention_weights_workspace", q)
+    need = L.w4a16_kv_attention_weights_workspace(B, Hq, Hkv, Tmax, D)
+    if need or work is not None:
+        work = _work(work, need, "w4a16_kv_attention_weights_workspace", q)
     _call(L.w4a16_kv_attention_decode_weights, "w4a16_kv_attention_decode_weights", q.device, q.data_ptr(), dt, B, Hq,
           Hkv, D, bits, _cache_struct(kcache, vcache, bits), lengths.data_ptr(), Tmax,
-          None if weights is None else weights.data_ptr(), sums.data_ptr(), work.data_ptr(), out.data_ptr())
+          None if weights is None else weights.data_ptr(), sums.data_ptr(),
+          None if work is None else work.data_ptr(), out.data_ptr())
     return out, sums
 
 

@@ -514,11 +514,12 @@ int64_t w4a16_kv_attention_weights_workspace(int64_t B, int64_t Hq, int64_t Hkv,
 int w4a16_kv_attention_decode_weights(const void* q, int dtype, int64_t B, int64_t Hq, int64_t Hkv, int64_t D,
                                       int bits, const w4a16_kv_cache* own, const int32_t* lengths, int64_t Tmax,
                                       const float* weights, float* sums, float* work, void* out, void* stream) {
-    if (!q || !own || !lengths || !sums || !work || !out) return W4A16_ERR_NULL;
+    if (!q || !own || !lengths || !sums || !out) return W4A16_ERR_NULL;
     if (dtype != W4A16_F16 && dtype != W4A16_BF16) return W4A16_ERR_DTYPE;
     if (bits != 8 && bits != 4) return W4A16_ERR_SCHEME;
     int st = check_kv_batch(B, Hq, Hkv, 0, 0, Tmax, D);
     if (st == W4A16_OK && B * Hq * Tmax > (int64_t(1) << 36)) st = W4A16_ERR_SHAPE;
+    if (st == W4A16_OK && !work && w4a16::kv_weights_workspace_floats(B, Hq, Hkv, Tmax, D) > 0) st = W4A16_ERR_NULL;
     if (st == W4A16_OK) st = check_cache(own, bits);
     if (st != W4A16_OK) return st;
     if (!aligned(q, 16) || !aligned(lengths, 4) || (weights && !aligned(weights, 4)) || !aligned(sums, 4) ||

@@ -507,7 +507,10 @@ __device__ __forceinline__ float across_quarters(float x, Op op) {
 // 2^-14 of that, so its rounding adds at most 2^-32 vcap.
 // WHOLE: the tokens [0, n2) of a second cache follow, and the block sees everything its rows do: it
 // normalizes and rounds them to out instead of leaving them to a merge.
-template <int BITS, int D, bool SCORES, bool WHOLE = false>
+// SCORES: every score (base 2) is left in `score`, for row r and token t at index r spad + t, r the row's head
+// in the batch, or (kInLds) its lane.
+constexpr int kNone = 0, kInMemory = 1, kInLds = 2;
+template <int BITS, int D, int SCORES, bool WHOLE = false>
 struct Stream {
     static constexpr int KT = BITS == 8 && D == 128 ? 32 : 64;   // tokens of a tile
     static constexpr int NS = KT / 16;                           // S tiles
@@ -721,12 +724,12 @@ struct Stream {
             for (int s = 0; s < NS; ++s)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) mt = fmaxf(mt, S[s][i]);
-            if constexpr (SCORES) {
+            if constexpr (SCORES != kNone) {
                 if (row < R) {
 #pragma unroll
                     for (int s = 0; s < NS; ++s) {
                         const int tok = tok0 + 16 * s + 4 * qd;
-                        if (tok < end) *reinterpret_cast<f32x4*>(score + head * spad + tok) = S[s];
+                        if (tok < end) *reinterpret_cast<f32x4*>(score + (SCORES == kInLds ? n : head) * spad + tok) = S[s];
                     }
                 }
             }
@@ -881,7 +884,7 @@ struct PrefixKind {
 };
 template <int BITS, int D>
 struct PrefixKind<BITS, D, 0> {
-    using type = Stream<BITS, D, false>;
+    using type = Stream<BITS, D, kNone>;
 };
 template <int BITS, int D, int WQ, bool SCORES>    // (streaming alone: three blocks a CU)
 __global__ __launch_bounds__(kThreads, WQ == 0 ? 3 : 2) void kv_decode_kernel(const uint16_t* __restrict__ q, int bf16, int B, int Hq,
@@ -890,7 +893,7 @@ __global__ __launch_bounds__(kThreads, WQ == 0 ? 3 : 2) void kv_decode_kernel(co
                                                                 float2* __restrict__ ml, float* __restrict__ po,
                                                                 float* __restrict__ score, int spad) {
     using A = typename PrefixKind<BITS, D, WQ>::type;
-    using S = Stream<BITS, D, SCORES>;
+    using S = Stream<BITS, D, SCORES ? kInMemory : kNone>;
     __shared__ union alignas(16) {
         typename A::Lds a;
         typename S::Lds s;
@@ -935,9 +938,10 @@ __global__ __launch_bounds__(kThreads, WQ == 0 ? 3 : 2) void kv_decode_kernel(co
 
 // Short sequences in one launch: block = sequence, kv head, tile of 16 of its G heads, over the prefix
 // and the sequence's own tokens.  SCORES (G <= 16, no prefix): then the accumulated weights, from the scores
-// that the block's waves have just written.  Bound by the latency of a few dependent tiles a wave: 4
+// that the block's waves have just written (up to kLdsTokens tokens to LDS).  Bound by the latency of a few dependent tiles a wave: 4
 // sequences behind 333 KV8 tokens, D = 64: 6 us; one of 500, with weights: 8.
-template <int BITS, int D, bool SCORES>
+constexpr int kLdsTokens = 512, kLdsStride = kLdsTokens + 4;     // (+ 4: the 16 rows start in different banks)
+template <int BITS, int D, int SCORES>
 __global__ __launch_bounds__(kThreads, 2) void kv_whole_kernel(const uint16_t* __restrict__ q, int bf16, int Hq, int Hkv,
                                                                KvCache prefix, int P, int Pmax, KvCache own,
                                                                const int* __restrict__ lens, int Tmax,
@@ -946,14 +950,17 @@ __global__ __launch_bounds__(kThreads, 2) void kv_whole_kernel(const uint16_t* _
     using S = Stream<BITS, D, SCORES, true>;
     __shared__ typename S::Lds lds;
     __shared__ float sm[4][16], sl[4][16];
+    __shared__ __attribute__((aligned(16))) float near[SCORES == kInLds ? 16 * kLdsStride : 4];
     const int G = Hq / Hkv, htiles = (G + 15) / 16;
     const int row0 = 16 * (blockIdx.x % htiles);
     const int bh = blockIdx.x / htiles, kvh = bh % Hkv, b = bh / Hkv;
     const long long hq0 = (long long)b * Hq + (long long)kvh * G;
     const int T = min(max(lens[b], 0), Tmax);
     const CacheRows mine = cache_rows<BITS, D>(own, (long long)bh * Tmax);
-    if constexpr (SCORES) {
-        S::run(lds, sm, sl, q, bf16 != 0, Hq, G, hq0, row0, G, mine, 0, T, 0, 0, nullptr, nullptr, score, spad, mine, 0,
+    if constexpr (SCORES != kNone) {
+        const int stride = SCORES == kInLds ? kLdsStride : spad;
+        float* at0 = SCORES == kInLds ? near : score;
+        S::run(lds, sm, sl, q, bf16 != 0, Hq, G, hq0, row0, G, mine, 0, T, 0, 0, nullptr, nullptr, at0, stride, mine, 0,
                out);
         // sm, sl: written before the barrier that the scores were written before
         for (int t = 4 * threadIdx.x; t < T; t += 4 * kThreads) {
@@ -963,7 +970,8 @@ __global__ __launch_bounds__(kThreads, 2) void kv_whole_kernel(const uint16_t* _
                 float L = 0.0f;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) L += sl[i][g] * exp2_raw(sm[i][g] - M);
-                const f32x4 s = *reinterpret_cast<const f32x4*>(score + (hq0 + g) * spad + t);
+                const f32x4 s =
+                    *reinterpret_cast<const f32x4*>(at0 + (SCORES == kInLds ? g : hq0 + g) * stride + t);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) w[j] = fmaf(exp2_raw(s[j] - M), 1.0f / L, w[j]);
             }
@@ -1153,7 +1161,7 @@ hipError_t shared(const KvSharedArgs& a, float* work, hipStream_t st) {
     const int G = a.Hq / a.Hkv;
     const long long heads = (long long)a.B * a.Hq, R = (long long)a.B * G;
     if (whole_shared(a.B, a.Hkv, a.P, a.Tmax)) {
-        hipLaunchKernelGGL((kv_whole_kernel<BITS, D, false>), dim3((unsigned)(a.B * a.Hkv * divup(G, 16))), dim3(kThreads),
+        hipLaunchKernelGGL((kv_whole_kernel<BITS, D, kNone>), dim3((unsigned)(a.B * a.Hkv * divup(G, 16))), dim3(kThreads),
                            0, st, static_cast<const uint16_t*>(a.q), a.dtype == DT_BF16, a.Hq, a.Hkv, a.prefix, a.P, a.Pmax,
                            a.own, a.lens, a.Tmax, static_cast<uint16_t*>(a.out), nullptr, 0, nullptr, nullptr);
         return hipGetLastError();
@@ -1203,9 +1211,13 @@ hipError_t weights(const KvWeightsArgs& a, float* work, hipStream_t st) {
     float2* ml = reinterpret_cast<float2*>(po + heads * ns * D);
     const int bf16 = a.dtype == DT_BF16;
     if (whole_weights(a.B, a.Hkv, G, a.Tmax)) {
-        hipLaunchKernelGGL((kv_whole_kernel<BITS, D, true>), dim3((unsigned)(a.B * a.Hkv)), dim3(kThreads), 0, st,
-                           static_cast<const uint16_t*>(a.q), bf16, a.Hq, a.Hkv, KvCache{}, 0, 0, a.own, a.lens, a.Tmax,
-                           static_cast<uint16_t*>(a.out), score, spad, a.weights, a.sums);
+#define W4A16_WHOLE(SCORES)                                                                                            \
+    hipLaunchKernelGGL((kv_whole_kernel<BITS, D, SCORES>), dim3((unsigned)(a.B * a.Hkv)), dim3(kThreads), 0, st,       \
+                       static_cast<const uint16_t*>(a.q), bf16, a.Hq, a.Hkv, KvCache{}, 0, 0, a.own, a.lens, a.Tmax,   \
+                       static_cast<uint16_t*>(a.out), score, spad, a.weights, a.sums)
+        if (a.Tmax <= kLdsTokens) W4A16_WHOLE(kInLds);
+        else W4A16_WHOLE(kInMemory);
+#undef W4A16_WHOLE
         return hipGetLastError();
     }
     const unsigned blocks = (unsigned)((long long)a.B * a.Hkv * divup(G, 16) * g.osplit);
@@ -1228,6 +1240,7 @@ long long kv_shared_workspace_floats(long long B, long long Hq, long long Hkv, l
 }
 
 long long kv_weights_workspace_floats(long long B, long long Hq, long long Hkv, long long Tmax, long long D) {
+    if (whole_weights(B, Hkv, (int)(Hq / Hkv), Tmax)) return Tmax <= kLdsTokens ? 0 : B * Hq * score_pad(Tmax);
     return B * Hq * score_pad(Tmax) + parts_floats(B * Hq, divup(Tmax, own_chunk(B, Hq, Hkv, Tmax)), D);
 }
 
