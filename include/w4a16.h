@@ -445,7 +445,8 @@ int64_t w4a16_kv_attention_shared_workspace(int64_t B, int64_t Hq, int64_t Hkv, 
  *            tokens are read, 0 <= P <= Pmax <= 2^24.  P == 0: its pointers are not looked at.
  *   own      [B, Hkv, Tmax, ...], 1 <= Tmax <= 2^24.
  *   lengths  device int32 [B]; each value is clamped into [0, Tmax] on the device.  A sequence with
- *            P + lengths[b] == 0 gets zeros; a query that is no number gets NaN and leaves the others alone.
+ *            P + lengths[b] == 0 gets zeros; a query that is no number gets NaN and leaves the others
+ *            alone (up to the rounding of their weights).
  *   work     w4a16_kv_attention_shared_workspace(...) fp32 elements, 16-byte aligned (scratch,
  *            contents undefined after the call; calls that overlap on one buffer race), or NULL when
  *            that is 0.

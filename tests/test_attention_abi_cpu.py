@@ -56,7 +56,7 @@ BAD_CACHES = [(8, dict(kcodes=None), L.ERR_NULL), (8, dict(kscales=None), L.ERR_
 SIZES = [(dict(Hkv=3), L.ERR_SHAPE), (dict(B=0), L.ERR_SHAPE), (dict(B=65536), L.ERR_SHAPE), (dict(D=32), L.ERR_SHAPE),
          (dict(Tmax=0), L.ERR_SHAPE), (dict(Tmax=(1 << 24) + 1), L.ERR_SHAPE), (dict(B=4096, Hq=65532), L.ERR_SHAPE),
          (dict(B=1 << 15, Hq=128), L.ERR_SHAPE), (dict(bits=6), L.ERR_SCHEME), (dict(dt=3), L.ERR_DTYPE), (dict(q=None), L.ERR_NULL), (dict(own=None), L.ERR_NULL),
-         (dict(lens=None), L.ERR_NULL), (dict(work=None, Tmax=600), L.ERR_NULL), (dict(out=None), L.ERR_NULL),
+         (dict(lens=None), L.ERR_NULL), (dict(work=None, Tmax=1100), L.ERR_NULL), (dict(out=None), L.ERR_NULL),
          (dict(q=B + 8), L.ERR_ALIGN), (dict(lens=C + 2), L.ERR_ALIGN), (dict(work=D + 8), L.ERR_ALIGN),
          (dict(out=E + 1), L.ERR_ALIGN)]
 
@@ -92,7 +92,7 @@ def test_decode_cache_refusals(lib, call, bits, kw, status):
 
 def test_shared_prefix_refusals(lib):
     assert shared(lib, P=11) == L.ERR_SHAPE
-    assert shared(lib, P=600, Pmax=600, work=None) == L.ERR_NULL
+    assert shared(lib, P=1100, Pmax=1100, work=None) == L.ERR_NULL
     assert shared(lib, P=-1) == L.ERR_SHAPE
     assert shared(lib, Pmax=(1 << 24) + 1) == L.ERR_SHAPE
     assert shared(lib, prefix=None) == L.ERR_NULL
@@ -143,13 +143,13 @@ def test_evict_cache_refusals(lib, bits, kw, status):
 
 def test_workspaces(lib):
     need = lib.w4a16_kv_attention_shared_workspace
-    assert need(2, 8, 4, 600, 8, 64) >= 2 * 8 * (64 + 2) * 2
-    assert need(2, 8, 4, 0, 600, 64) >= 2 * 8 * (64 + 2)
+    assert need(2, 8, 4, 1100, 8, 64) >= 2 * 8 * (64 + 2) * 2
+    assert need(2, 8, 4, 0, 1100, 64) >= 2 * 8 * (64 + 2)
     assert need(2, 8, 4, 10, 8, 64) == 0 and need(2, 8, 4, 0, 512, 64) == 0
     assert need(2, 8, 3, 10, 8, 64) == L.ERR_SHAPE and need(2, 8, 4, -1, 8, 64) == L.ERR_SHAPE
     assert need(2, 8, 4, 10, 0, 64) == L.ERR_SHAPE and need(2, 8, 4, 10, 8, 65) == L.ERR_SHAPE
     need = lib.w4a16_kv_attention_weights_workspace
-    assert need(2, 8, 4, 1000, 64) >= 2 * 8 * (1000 + 64 + 2) and need(2, 34, 2, 9, 64) >= 2 * 34 * (9 + 64 + 2)
+    assert need(2, 8, 4, 1100, 64) >= 2 * 8 * (1100 + 64 + 2) and need(2, 34, 2, 9, 64) >= 2 * 34 * (9 + 64 + 2)
     assert need(2, 8, 4, 512, 64) == 0 and need(200, 8, 4, 1000, 64) >= 200 * 8 * 1000
     assert need(2, 8, 3, 9, 64) == L.ERR_SHAPE and need(0, 8, 4, 9, 64) == L.ERR_SHAPE
     assert need(65535, 256, 4, 1 << 13, 64) == L.ERR_SHAPE

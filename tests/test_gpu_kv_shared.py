@@ -65,12 +65,17 @@ CASES = [
     # many rows and a prefix that is short beside the own caches (streamed), the next longer one (not)
     (40, 8, 2, 128, 75, [7 * i for i in range(40)], 300, 8, BF), (40, 8, 2, 128, 76, [7 * i for i in range(40)], 300, 8, BF),
     (33, 3, 1, 64, 33, [4 * i for i in range(33)], 132, 4, H), (33, 3, 1, 64, 34, [4 * i for i in range(33)], 132, 4, H),
-    # the same sizes with more room for own tokens, so that a sequence is not one block's work
-    (40, 8, 2, 128, 150, [7 * i for i in range(40)], 600, 8, BF), (40, 8, 2, 128, 151, [7 * i for i in range(40)], 600, 8, BF),
-    (1, 1, 1, 64, 1, [0], 512, 8, H), (3, 4, 4, 128, 63, [1, 0, 5], 450, 8, BF), (2, 6, 2, 64, 64, [64, 65], 449, 4, H),
+    # the same sizes with more room for own tokens: one block of eight waves, or of four, a sequence ...
+    (40, 8, 2, 128, 150, [7 * i for i in range(40)], 600, 8, BF), (40, 8, 2, 128, 151, [7 * i for i in range(40)], 873, 8, BF),
+    (130, 8, 2, 64, 400, [i for i in range(130)], 200, 4, BF), (1, 1, 1, 64, 1, [0], 512, 8, H), (3, 4, 4, 128, 63, [1, 0, 5], 450, 8, BF), (2, 6, 2, 64, 64, [64, 65], 449, 4, H),
     (33, 2, 2, 128, 129, [i % 5 for i in range(33)], 400, 4, H), (12, 4, 1, 64, 191, [i for i in range(12)], 400, 8, H),
     (64, 1, 1, 64, 320, [0] * 64, 300, 4, H), (17, 1, 1, 128, 192, [5] * 17, 400, 4, BF), (3, 40, 1, 128, 130, [0, 260, 40], 500, 4, BF),
     (5, 8, 2, 64, 127, [3, 0, 65, 64, 1], 500, 4, BF), (2, 40, 1, 64, 256, [100, 256], 256, 8, H), (2, 40, 1, 64, 256, [100, 257], 257, 8, H),
+    # ... or splits
+    (40, 8, 2, 128, 250, [7 * i for i in range(40)], 1000, 8, BF), (40, 8, 2, 128, 251, [7 * i for i in range(40)], 1000, 8, BF),
+    (1, 1, 1, 64, 1, [0], 1100, 8, H), (3, 4, 4, 128, 63, [1, 0, 5], 1100, 8, BF), (33, 2, 2, 128, 300, [i % 5 for i in range(33)], 1000, 4, H),
+    (12, 4, 1, 64, 291, [i for i in range(12)], 900, 8, H), (64, 1, 1, 64, 320, [0] * 64, 900, 4, H), (17, 1, 1, 128, 292, [5] * 17, 900, 4, BF),
+    (3, 40, 1, 128, 330, [0, 260, 40], 900, 4, BF), (5, 8, 2, 64, 127, [3, 0, 65, 64, 1], 1000, 4, BF), (2, 6, 2, 64, 64, [64, 65], 1000, 4, H),
     # many sequences behind a prefix that is too much to read for each
     (1100, 4, 4, 64, 240, [i % 12 for i in range(1100)], 12, 8, H)]
 
@@ -89,7 +94,7 @@ def test_shared_prefix(B, Hq, Hkv, D, P, lens, Tmax, bits, dtype):
 
 
 @pytest.mark.parametrize("bits", [8, 4])
-@pytest.mark.parametrize("room", [150, 700])
+@pytest.mark.parametrize("room", [150, 700, 1100])
 def test_no_prefix_and_no_tokens(bits, room):
     """P = 0 leaves the own tokens; a sequence with neither gets zeros."""
     lens = [0, 130, 1]
@@ -112,7 +117,7 @@ def test_lengths_outside_are_clamped():
 
 @pytest.mark.parametrize("bits", [8, 4])
 @pytest.mark.parametrize("qscale", [1e-30, 1e4])
-@pytest.mark.parametrize("room", [30, 500])
+@pytest.mark.parametrize("room", [30, 500, 1000])
 def test_bf16_queries_far_from_one(bits, qscale, room):
     """bf16 queries outside fp16's range: scaled by a power of two inside the kernel."""
     q, kp, vp, k, v = problem(4, 8, 2, 128, 150, room, bits, BF, seed=52, qscale=qscale)
@@ -135,22 +140,22 @@ def test_bf16_queries_far_from_one(bits, qscale, room):
 
 @pytest.mark.parametrize("B,Hq,Hkv", [(4, 8, 2), (12, 8, 2), (40, 8, 2)])
 @pytest.mark.parametrize("bits", [8, 4])
-@pytest.mark.parametrize("room", [9, 400])
-def test_bf16_queries_of_very_different_size(bits, B, Hq, Hkv, room):
+@pytest.mark.parametrize("P,room", [(150, 9), (150, 600), (300, 900)])
+def test_bf16_queries_of_very_different_size(bits, B, Hq, Hkv, P, room):
     """Rows that share a block, from 1e-30 to 1e6 in size: each keeps its bits (16, 48 and 160 rows
     per kv head, one for each arrangement of the waves; a sequence as one block's work)."""
-    q, kp, vp, k, v = problem(B, Hq, Hkv, 128, 150, room, bits, BF, seed=60)
+    q, kp, vp, k, v = problem(B, Hq, Hkv, 128, P, room, bits, BF, seed=60)
     size = torch.tensor([1e-30, 1.0, 1e-9, 1e6, 0.0, 1e-3, 3e4])[torch.arange(B * Hq) % 7].view(B, Hq, 1)
     q = (q.cpu().float() * size).to(BF).cuda()
     lens = [i % 10 for i in range(B)]
-    out = W4.kv_attention_decode_shared(q, kp, vp, 150, k, v, torch.tensor(lens, dtype=torch.int32, device="cuda"), bits)
+    out = W4.kv_attention_decode_shared(q, kp, vp, P, k, v, torch.tensor(lens, dtype=torch.int32, device="cuda"), bits)
     torch.cuda.synchronize()
     keep = (size.flatten() <= 1.0).view(B, Hq)                 # the large rows' scores differ by more than fp32 holds
     assert torch.isfinite(out).all()
     small = torch.where(keep[..., None].cuda(), q, torch.zeros_like(q))
-    same = W4.kv_attention_decode_shared(small, kp, vp, 150, k, v, torch.tensor(lens, dtype=torch.int32, device="cuda"), bits)
+    same = W4.kv_attention_decode_shared(small, kp, vp, P, k, v, torch.tensor(lens, dtype=torch.int32, device="cuda"), bits)
     torch.cuda.synchronize()
-    check(same, small, kp, vp, 150, k, v, lens, bits)
+    check(same, small, kp, vp, P, k, v, lens, bits)
     # beside large rows a row's weights may differ by their fp16 roundings alone
     a, b = f64(out)[keep.numpy()], f64(same)[keep.numpy()]
     assert np.abs(a - b).max() <= 2.0 ** -7 * np.abs(b).max()
@@ -158,28 +163,31 @@ def test_bf16_queries_of_very_different_size(bits, B, Hq, Hkv, room):
 
 @pytest.mark.parametrize("B,Hq,Hkv", [(4, 8, 2), (12, 8, 2), (40, 8, 2)])
 @pytest.mark.parametrize("dtype", [H, BF])
-@pytest.mark.parametrize("room", [9, 400])
-def test_rows_without_numbers_leave_the_others_alone(B, Hq, Hkv, dtype, room):
+@pytest.mark.parametrize("P,room", [(140, 9), (140, 600), (290, 900)])
+def test_rows_without_numbers_leave_the_others_alone(B, Hq, Hkv, dtype, P, room):
     """Unused places of a padded batch: NaN and infinities in some queries, the other rows as before."""
-    q, kp, vp, k, v = problem(B, Hq, Hkv, 64, 140, room, 8, dtype, seed=61)
+    q, kp, vp, k, v = problem(B, Hq, Hkv, 64, P, room, 8, dtype, seed=61)
     lt = torch.tensor([i % 10 for i in range(B)], dtype=torch.int32, device="cuda")
-    clean = W4.kv_attention_decode_shared(q, kp, vp, 140, k, v, lt, 8)
+    clean = W4.kv_attention_decode_shared(q, kp, vp, P, k, v, lt, 8)
     bad = q.clone()
     bad[1] = float("nan")
     bad[2, 3, 5] = float("inf")
     bad[B - 1, 1] = -float("inf")
-    out = W4.kv_attention_decode_shared(bad, kp, vp, 140, k, v, lt, 8)
+    out = W4.kv_attention_decode_shared(bad, kp, vp, P, k, v, lt, 8)
     torch.cuda.synchronize()
     ok = torch.ones((B, Hq), dtype=torch.bool)
     ok[1] = False
     ok[2, 3] = ok[B - 1, 1] = False
     a, b = f64(out)[ok.numpy()], f64(clean)[ok.numpy()]
     assert np.isfinite(a).all() and np.isnan(f64(out)[~ok.numpy()]).all()
+    check(torch.where(ok[..., None].cuda(), out, clean), q, kp, vp, P, k, v, [i % 10 for i in range(B)], 8)
+    if P > 256:         # rows of a wave move their references together: other roundings of the weights
+        return
     # the common factor of the bf16 rows may be another one: the same values, up to a rounding
     assert np.abs(a - b).max() <= (0.0 if dtype == H else 2.0 ** -7 * np.abs(b).max())
 
 
-@pytest.mark.parametrize("room", [10, 500])
+@pytest.mark.parametrize("room", [10, 500, 1000])
 def test_zero_value_rows_beside_small_ones(room):
     """A row of zeros is stored with scale 1 beside values of 1e-3: the small rows keep their bits."""
     q, kp, vp, k, v = problem(2, 4, 2, 64, 200, room, 8, BF, seed=53, vscale=1e-3)
@@ -246,8 +254,8 @@ def test_refusals():
         run(q, kp, vp, 10, k, v, lt.cpu(), 8)
     with pytest.raises(ValueError):
         run(q, kp, vp, 10, k, v, lt, 8, work=torch.empty(3, device="cuda", dtype=H))
-    with pytest.raises(ValueError):                         # (room for 600 own tokens needs some)
-        run(q, kp, vp, 10, *problem(2, 4, 2, 64, 10, 600, 8, H, seed=57)[3:], lt, 8, work=torch.empty(3, device="cuda"))
+    with pytest.raises(ValueError):                         # (room for 1100 own tokens needs some)
+        run(q, kp, vp, 10, *problem(2, 4, 2, 64, 10, 1100, 8, H, seed=57)[3:], lt, 8, work=torch.empty(3, device="cuda"))
     with pytest.raises(ValueError):
         run(q, kp, vp, 10, k, v, lt, 8, out=torch.empty((2, 4, 32), dtype=H, device="cuda"))
     with pytest.raises(W4.W4A16Error):

@@ -59,7 +59,9 @@ CASES = [(1, 1, 1, 64, [1], 1, 8, H), (2, 4, 2, 128, [5, 0], 7, 4, BF), (3, 6, 2
          (2, 4, 2, 128, [5, 0], 600, 4, BF), (3, 6, 2, 64, [127, 128, 129], 512, 8, BF), (3, 6, 2, 64, [127, 128, 513], 513, 8, BF),
          (1, 33, 1, 128, [70], 530, 4, H), (2, 8, 1, 128, [255, 257], 600, 4, H), (1, 16, 1, 128, [511], 512, 4, H),
          (2, 17, 1, 64, [300, 512], 512, 8, BF), (64, 4, 4, 64, [16 * i + 15 for i in range(64)], 1024, 8, H),
-         (64, 4, 4, 64, [16 * i + 1 for i in range(64)], 1025, 4, H)]
+         (64, 4, 4, 64, [16 * i + 1 for i in range(64)], 1025, 4, H), (65, 4, 4, 64, [15 * i for i in range(65)], 1000, 4, BF),
+         (2, 4, 2, 128, [5, 0], 1100, 4, BF), (3, 6, 2, 64, [127, 128, 769], 769, 8, BF), (1, 33, 1, 128, [70], 1100, 4, H),
+         (2, 8, 1, 128, [255, 768], 768, 4, H), (2, 8, 1, 128, [255, 257], 1100, 4, H), (43, 3, 3, 128, [23 * i + 1 for i in range(43)], 1024, 8, BF)]
 
 
 @pytest.mark.parametrize("B,Hq,Hkv,D,lens,Tmax,bits,dtype", CASES)
@@ -85,7 +87,7 @@ def test_weights(B, Hq, Hkv, D, lens, Tmax, bits, dtype):
     check(out3, got3, q, k, v, torch.zeros_like(w), lens, bits)
 
 
-@pytest.mark.parametrize("room", [300, 700])
+@pytest.mark.parametrize("room", [300, 700, 1100])
 def test_a_query_that_is_no_number_gives_none(room):
     """NaN in one sequence's queries, an infinity in one head of another: NaN there, the rest as before."""
     q, k, v, w = problem(3, 8, 2, 64, room, 8, H, seed=13)
@@ -120,7 +122,7 @@ def test_agrees_with_the_batched_decode():
     assert (out.float() - ref.float()).abs().max() <= 4 * 2.0 ** -11 * max(1.0, ref.float().abs().max().item())
 
 
-@pytest.mark.parametrize("B,T", [(2, 333), (2, 900), (140, 900)])
+@pytest.mark.parametrize("B,T", [(2, 333), (2, 700), (2, 1100), (140, 900)])
 def test_work_buffer_and_repeat(B, T):
     """None, one for splits and one for the scores alone: nothing behind its end is written."""
     q, k, v, w = problem(B, 8, 2, 64, T, 8, BF, seed=11)

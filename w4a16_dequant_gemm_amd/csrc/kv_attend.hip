@@ -488,8 +488,8 @@ __device__ __forceinline__ float across_quarters(float x, Op op) {
 
 // Tokens [t0, t1) of a cache for the rows row0 .. row0 + 15 (R in all; numbered as in
 // Attend), 16 x 16 x 32 products.  The cache is read once, so the aim is loads in flight and few
-// instructions: each wave of the block streams tiles of its own (wave, wave + 4, ...), with no
-// barrier until the four are joined at the end, and loads the next tile while it works on one.
+// instructions: each of the block's NW waves streams tiles of its own (wave, wave + NW, ...), with no
+// barrier until they are joined at the end, and loads the next tile while it works on one.
 // Measured: 16 sequences of up to 4096 KV8 tokens, 32 heads, D = 128 (318 MB with the scores): 62 us,
 // 5.1 TB/s; 8 of up to 65536 KV4 tokens, 32 heads on 8 (365 MB): 97 us, 3.8 TB/s, the vector units busy
 // 60 % of the cycles (twice the codes a byte).  Three blocks a CU: four spilled (254 us against 97).
@@ -510,7 +510,7 @@ __device__ __forceinline__ float across_quarters(float x, Op op) {
 // SCORES: every score (base 2) is left in `score`, for row r and token t at index r spad + t, r the row's head
 // in the batch, or (kInLds) its lane.
 constexpr int kNone = 0, kInMemory = 1, kInLds = 2;
-template <int BITS, int D, int SCORES, bool WHOLE = false>
+template <int BITS, int D, int SCORES, bool WHOLE = false, int NW = 4>
 struct Stream {
     static constexpr int KT = BITS == 8 && D == 128 ? 32 : 64;   // tokens of a tile
     static constexpr int NS = KT / 16;                           // S tiles
@@ -530,8 +530,8 @@ struct Stream {
         _Float16 kz[BITS == 4 ? KT : 4], vz[BITS == 4 ? KT : 4];     // -z 2^-9
     };
     union Lds {
-        WaveLds w[4];
-        float join[4][D / 4][16][4];
+        WaveLds w[NW];
+        float join[NW][D / 4][16][4];
     };
 
     // Where 16-byte piece c of token r's V row sits: spread over the banks for the transposing reads,
@@ -652,7 +652,7 @@ struct Stream {
         float m = NEG, l = 0.0f;                           // base-2 domain
         float vcap = 5.9604644775390625e-8f;               // fp16's smallest
 
-        for (int t = wave; t < tiles; t += 4) {
+        for (int t = wave; t < tiles; t += NW) {
             // this tile's V codes and parameters to LDS
 #pragma unroll
             for (int i = 0; i < VL; ++i) {
@@ -705,7 +705,7 @@ struct Stream {
                     S[s] = mfma16(u32x4{d[0], d[1], d[2], d[3]}, qf[k], S[s]);
                 }
             }
-            if (t + 4 < tiles) load(t + 4);
+            if (t + NW < tiles) load(t + NW);
 
             int tok0, end;
             place(t, tok0, end);
@@ -798,18 +798,19 @@ struct Stream {
             wave_lds_fence();                              // before the next tile overwrites this one
         }
 
-        // join the four waves: each leaves its output, rescaled to the common maximum, in LDS and
-        // adds up its quarter of the elements over all of them
+        // join the waves: each leaves its output, rescaled to the common maximum, in LDS and adds up its
+        // share of the elements over all of them
         l = across_quarters(l, [](float a, float b) { return a + b; });
         if (qd == 0) {
             sm[wave][n] = m;
             sl[wave][n] = l;
         }
         __syncthreads();
-        const float M = fmaxf(fmaxf(sm[0][n], sm[1][n]), fmaxf(sm[2][n], sm[3][n]));
-        float Lt = 0.0f;
+        float M = sm[0][n], Lt = 0.0f;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) Lt += M == NEG ? sl[w][n] : sl[w][n] * exp2_raw(sm[w][n] - M);   // (0 or NaN)
+        for (int w = 1; w < NW; ++w) M = fmaxf(M, sm[w][n]);
+#pragma unroll
+        for (int w = 0; w < NW; ++w) Lt += M == NEG ? sl[w][n] : sl[w][n] * exp2_raw(sm[w][n] - M);   // (0 or NaN)
         const float f = M == NEG ? 0.0f : exp2_raw(m - M) * (vcap / VNORM * kCodeUnit);
 #pragma unroll
         for (int i = 0; i < OT; ++i)
@@ -819,11 +820,12 @@ struct Stream {
             const long long at = WHOLE ? head : head * nsplit + split;
             if (!WHOLE && wave == 0 && qd == 0) ml[at] = make_float2(M, Lt);
 #pragma unroll
-            for (int i = 0; i < D / 64; ++i) {
-                const int dq = wave * (D / 16) + 4 * i + qd;
+            for (int i = 0; i < (D / 16 + NW - 1) / NW; ++i) {
+                const int dq = 4 * (wave + NW * i) + qd;
+                if (D / 16 < NW && dq >= D / 4) break;
                 f32x4 a = *reinterpret_cast<const f32x4*>(lds.join[0][dq][n]);
 #pragma unroll
-                for (int w = 1; w < 4; ++w) a += *reinterpret_cast<const f32x4*>(lds.join[w][dq][n]);
+                for (int w = 1; w < NW; ++w) a += *reinterpret_cast<const f32x4*>(lds.join[w][dq][n]);
                 if constexpr (WHOLE) {
                     uint16_t r[4];
 #pragma unroll
@@ -941,15 +943,15 @@ __global__ __launch_bounds__(kThreads, WQ == 0 ? 3 : 2) void kv_decode_kernel(co
 // that the block's waves have just written (up to kLdsTokens tokens to LDS).  Bound by the latency of a few dependent tiles a wave: 4
 // sequences behind 333 KV8 tokens, D = 64: 6 us; one of 500, with weights: 8.
 constexpr int kLdsTokens = 512, kLdsStride = kLdsTokens + 4;     // (+ 4: the 16 rows start in different banks)
-template <int BITS, int D, int SCORES>
-__global__ __launch_bounds__(kThreads, 2) void kv_whole_kernel(const uint16_t* __restrict__ q, int bf16, int Hq, int Hkv,
+template <int BITS, int D, int SCORES, int NW>
+__global__ __launch_bounds__(64 * NW, 2) void kv_whole_kernel(const uint16_t* __restrict__ q, int bf16, int Hq, int Hkv,
                                                                KvCache prefix, int P, int Pmax, KvCache own,
                                                                const int* __restrict__ lens, int Tmax,
                                                                uint16_t* __restrict__ out, float* score, int spad,
                                                                const float* weights, float* sums) {
-    using S = Stream<BITS, D, SCORES, true>;
+    using S = Stream<BITS, D, SCORES, true, NW>;
     __shared__ typename S::Lds lds;
-    __shared__ float sm[4][16], sl[4][16];
+    __shared__ float sm[NW][16], sl[NW][16];
     __shared__ __attribute__((aligned(16))) float near[SCORES == kInLds ? 16 * kLdsStride : 4];
     const int G = Hq / Hkv, htiles = (G + 15) / 16;
     const int row0 = 16 * (blockIdx.x % htiles);
@@ -963,13 +965,14 @@ __global__ __launch_bounds__(kThreads, 2) void kv_whole_kernel(const uint16_t* _
         S::run(lds, sm, sl, q, bf16 != 0, Hq, G, hq0, row0, G, mine, 0, T, 0, 0, nullptr, nullptr, at0, stride, mine, 0,
                out);
         // sm, sl: written before the barrier that the scores were written before
-        for (int t = 4 * threadIdx.x; t < T; t += 4 * kThreads) {
+        for (int t = 4 * threadIdx.x; t < T; t += 256 * NW) {
             f32x4 w = {0.0f, 0.0f, 0.0f, 0.0f};
             for (int g = 0; g < G; ++g) {
-                const float M = fmaxf(fmaxf(sm[0][g], sm[1][g]), fmaxf(sm[2][g], sm[3][g]));
-                float L = 0.0f;
+                float M = sm[0][g], L = 0.0f;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) L += sl[i][g] * exp2_raw(sm[i][g] - M);
+                for (int i = 1; i < NW; ++i) M = fmaxf(M, sm[i][g]);
+#pragma unroll
+                for (int i = 0; i < NW; ++i) L += sl[i][g] * exp2_raw(sm[i][g] - M);
                 const f32x4 s =
                     *reinterpret_cast<const f32x4*>(at0 + (SCORES == kInLds ? g : hq0 + g) * stride + t);
 #pragma unroll
@@ -1139,19 +1142,30 @@ int prefix_chunk(long long B, long long Hq, long long Hkv, long long P, long lon
                    : chunk_of(P, Hkv * divup(R, 32 * wq), kPrefixBlocks, kMinChunk);
 }
 
-// Whether a block takes a sequence and kv head whole (kv_whole_kernel) instead of splits that a second
-// launch joins.  Whole / split, us in a graph (a call by itself saves 3 us of submission besides), KV8, D = 128:
-//   prefix and own caches of half each, 512 tokens: 4 x 8 kv heads 8.4 / 8.7, 16 x 8 8.4 / 12.4, 256 x 8
-//     32.9 / 38.7, 64 x 32 33.3 / 32.4, 256 x 32 138.8 / 124.8 (the prefix is read again for every
-//     sequence); 1024 tokens: 4 x 8 12.0 / 8.7, 64 x 8 19.1 / 22.4, 64 x 32 59.4 / 52.0
-//   with weights: 4 x 8 kv heads of 256 / 512 / 1024 tokens 7.7 / 10, 9.7 / 9.9, 13.4 / 10.2; calls with ragged
-//     lengths: 256 heads of up to 1024 / 2048 17.2 / 19.6, 28.9 / 28.2; 1024 of 2048 / 4096 (4-bit) 52.7 / 53.2,
-//     113.0 / 112.9
-bool whole_shared(long long B, long long Hkv, long long P, long long Tmax) {
-    return P + Tmax <= 512 && B * Hkv * P <= (1 << 20);
+// Waves of a block that takes a sequence and kv head whole (kv_whole_kernel), or 0: splits that a second
+// launch joins.  Us in a graph, whole / split; a call by itself saves 3 - 4 us of submission besides, so that
+// a little more is taken where few blocks leave the GPU empty.  KV8, D = 128:
+//   prefix (3 / 4 of the tokens) and own caches, 4 waves: 1 x 8, 16 x 8, 64 x 8 kv heads of 512 tokens 8.0 / 8.5,
+//     8.2 / 12.4, 11.6 / 17.1; 64 x 32 33 / 32, 256 x 32 139 / 125 (the prefix is read again for every sequence);
+//     64 x 8 of 768, 1024, 1536 14.9 / 18.2, 18.1 / 18.8, 24.2 / 21.5; 16 x 32, one row each, of 768 15.8 / 12.6
+//   8 waves: 1 x 8 of 768, 1024 9.5 / 8.3, 10.8 / 8.3; 16 x 8 9.9 / 12.6, 11.2 / 12.7; 32 x 8 10.3 / 16.4,
+//     11.4 / 16.5
+//   with weights, 4 waves: 1 x 8 of 512 9.3 / 9.7; 64 x 8 of 1024, 2048 27.4 / 34.0, 50.1 / 55.1; of ragged lengths
+//     1024 kv heads of 2048, 4096 (4-bit) 52.7 / 53.2, 113.0 / 112.9
+//   8 waves: 1 x 8 of 768, 1024 11.1 / 9.7, 12.6 / 9.7 (4-bit 9.3 / 9.1, 11.0 / 9.2); 16 x 8 11.7 / 12.8, 14.0 /
+//     14.1, 1536 17.6 / 17.5; of 512 tokens 10.3 against 10.0 with 4 waves
+int whole_shared(long long B, long long Hkv, long long G, long long P, long long Tmax) {
+    const long long N = P + Tmax, blocks = B * Hkv * divup(G, 16);
+    if (N <= 512 && B * Hkv * P <= (1 << 20)) return 4;
+    if (N <= 768 && blocks <= 256) return 8;
+    return N <= 1024 && B * G > 16 && blocks <= 512 ? (blocks <= 256 ? 8 : 4) : 0;
 }
-bool whole_weights(long long B, long long Hkv, int G, long long Tmax) {
-    return G <= 16 && (Tmax <= 512 || (Tmax <= 2048 && Tmax * Tmax <= 4096 * B * Hkv));
+int whole_weights(long long B, long long Hkv, long long G, long long Tmax) {
+    const long long blocks = B * Hkv;
+    if (G > 16) return 0;
+    if (Tmax <= 512) return 4;
+    if (blocks <= 256) return Tmax <= 768 || (Tmax <= 1024 && blocks >= 128) ? 8 : 0;
+    return Tmax <= 2048 && Tmax * Tmax <= 4096 * blocks ? 4 : 0;
 }
 
 long long parts_floats(long long heads, long long ns, long long D) { return heads * ns * (D + 2); }
@@ -1160,12 +1174,17 @@ template <int BITS, int D>
 hipError_t shared(const KvSharedArgs& a, float* work, hipStream_t st) {
     const int G = a.Hq / a.Hkv;
     const long long heads = (long long)a.B * a.Hq, R = (long long)a.B * G;
-    if (whole_shared(a.B, a.Hkv, a.P, a.Tmax)) {
-        hipLaunchKernelGGL((kv_whole_kernel<BITS, D, kNone>), dim3((unsigned)(a.B * a.Hkv * divup(G, 16))), dim3(kThreads),
-                           0, st, static_cast<const uint16_t*>(a.q), a.dtype == DT_BF16, a.Hq, a.Hkv, a.prefix, a.P, a.Pmax,
-                           a.own, a.lens, a.Tmax, static_cast<uint16_t*>(a.out), nullptr, 0, nullptr, nullptr);
+#define W4A16_WHOLE(NW)                                                                                                \
+    hipLaunchKernelGGL((kv_whole_kernel<BITS, D, kNone, NW>), dim3((unsigned)(a.B * a.Hkv * divup(G, 16))),            \
+                       dim3(64 * NW), 0, st, static_cast<const uint16_t*>(a.q), a.dtype == DT_BF16, a.Hq, a.Hkv,       \
+                       a.prefix, a.P, a.Pmax, a.own, a.lens, a.Tmax, static_cast<uint16_t*>(a.out), nullptr, 0,        \
+                       nullptr, nullptr)
+    if (const int nw = whole_shared(a.B, a.Hkv, G, a.P, a.Tmax)) {
+        if (nw == 4) W4A16_WHOLE(4);
+        else W4A16_WHOLE(8);
         return hipGetLastError();
     }
+#undef W4A16_WHOLE
     const int wq = prefix_wq(R, a.P, a.Tmax);
     DecodeGrid g = {};
     g.P = a.P;
@@ -1210,16 +1229,17 @@ hipError_t weights(const KvWeightsArgs& a, float* work, hipStream_t st) {
     float* po = work + heads * spad;
     float2* ml = reinterpret_cast<float2*>(po + heads * ns * D);
     const int bf16 = a.dtype == DT_BF16;
-    if (whole_weights(a.B, a.Hkv, G, a.Tmax)) {
-#define W4A16_WHOLE(SCORES)                                                                                            \
-    hipLaunchKernelGGL((kv_whole_kernel<BITS, D, SCORES>), dim3((unsigned)(a.B * a.Hkv)), dim3(kThreads), 0, st,       \
+#define W4A16_WHOLE(SCORES, NW)                                                                                        \
+    hipLaunchKernelGGL((kv_whole_kernel<BITS, D, SCORES, NW>), dim3((unsigned)(a.B * a.Hkv)), dim3(64 * NW), 0, st,    \
                        static_cast<const uint16_t*>(a.q), bf16, a.Hq, a.Hkv, KvCache{}, 0, 0, a.own, a.lens, a.Tmax,   \
                        static_cast<uint16_t*>(a.out), score, spad, a.weights, a.sums)
-        if (a.Tmax <= kLdsTokens) W4A16_WHOLE(kInLds);
-        else W4A16_WHOLE(kInMemory);
-#undef W4A16_WHOLE
+    if (const int nw = whole_weights(a.B, a.Hkv, G, a.Tmax)) {
+        if (a.Tmax <= kLdsTokens) W4A16_WHOLE(kInLds, 4);
+        else if (nw == 4) W4A16_WHOLE(kInMemory, 4);
+        else W4A16_WHOLE(kInMemory, 8);
         return hipGetLastError();
     }
+#undef W4A16_WHOLE
     const unsigned blocks = (unsigned)((long long)a.B * a.Hkv * divup(G, 16) * g.osplit);
     hipLaunchKernelGGL((kv_decode_kernel<BITS, D, 0, true>), dim3(blocks), dim3(kThreads), 0, st,
                        static_cast<const uint16_t*>(a.q), bf16, a.B, a.Hq, a.Hkv, KvCache{}, a.own, a.lens, g, ml, po,
@@ -1235,12 +1255,12 @@ hipError_t weights(const KvWeightsArgs& a, float* work, hipStream_t st) {
 
 long long kv_shared_workspace_floats(long long B, long long Hq, long long Hkv, long long P, long long Tmax,
                                      long long D) {
-    if (whole_shared(B, Hkv, P, Tmax)) return 0;
+    if (whole_shared(B, Hkv, Hq / Hkv, P, Tmax)) return 0;
     return parts_floats(B * Hq, divup(P, prefix_chunk(B, Hq, Hkv, P, Tmax)) + divup(Tmax, own_chunk(B, Hq, Hkv, Tmax)), D);
 }
 
 long long kv_weights_workspace_floats(long long B, long long Hq, long long Hkv, long long Tmax, long long D) {
-    if (whole_weights(B, Hkv, (int)(Hq / Hkv), Tmax)) return Tmax <= kLdsTokens ? 0 : B * Hq * score_pad(Tmax);
+    if (whole_weights(B, Hkv, Hq / Hkv, Tmax)) return Tmax <= kLdsTokens ? 0 : B * Hq * score_pad(Tmax);
     return B * Hq * score_pad(Tmax) + parts_floats(B * Hq, divup(Tmax, own_chunk(B, Hq, Hkv, Tmax)), D);
 }
 
