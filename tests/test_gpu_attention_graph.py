@@ -53,6 +53,7 @@ def test_replays_equal_eager_calls():
         (lambda o: W4.attention_prompt(pq, pk, pv, cu, out=o), lambda: torch.zeros((700, 8, D), dtype=dt, device="cuda")),
         (lambda o: W4.kv_attention_decode_shared(q, kp, vp, 500, k, v, lengths, 8, out=o, work=ws),
          lambda: torch.zeros_like(q)),
+        (lambda o: W4.kv_attention_decode_shared(q, kp, vp, 100, k, v, lengths, 8, out=o), lambda: torch.zeros_like(q)),
         (lambda o: W4.kv_attention_decode_weights(q, k4, v4, lengths, w, 4, sums=o[1], out=o[0], work=ww),
          lambda: (torch.zeros_like(q), torch.zeros_like(w))),
         (lambda o: W4.kv_evict(k4, v4, w, lengths, 200, 20, 4, out=o), evict_out),

@@ -594,8 +594,8 @@ def attention_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
     ``q [T, Hq, D]``, ``k`` and ``v [T, Hkv, D]`` are fp16 or bf16; their heads are adjacent, their
     rows may be strided (column blocks of a fused projection).  Sequence ``b`` is the tokens
     ``cu_seqlens[b] .. cu_seqlens[b + 1] - 1`` (int32 ``[B + 1]`` on the device, not decreasing).
-    Rows outside every sequence are neither read nor written: in an ``out`` of the caller's they
-    keep what they held, in the returned tensor of a call without ``out`` they are undefined."""
+    Rows outside every sequence are neither read nor written: in an ``out`` of the caller's (which
+    must not overlap the inputs) they keep what they held, in the returned tensor of a call without ``out`` they are undefined."""
     dt = _dtype_code(q)
     sq, sk, sv = _need_heads(q, "q", q.dtype), _need_heads(k, "k", q.dtype), _need_heads(v, "v", q.dtype)
     _need(cu_seqlens, "cu_seqlens", torch.int32, 1)
