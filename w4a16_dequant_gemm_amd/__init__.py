@@ -49,6 +49,9 @@ __all__ = [
 ]
 
 
+_INT8, _INT32, _HALF = torch.int8, torch.int32, torch.float16
+
+
 def _stream() -> int:
     return torch.cuda.current_stream().cuda_stream
 
@@ -76,7 +79,7 @@ def _same_device(x: torch.Tensor, name: str, **others) -> None:
 
 
 def _need(t: torch.Tensor, name: str, dtype, ndim: int) -> None:
-    if isinstance(t, torch.Tensor) and t.dtype == dtype and t.dim() == ndim and t.is_cuda and t.is_contiguous():
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.dim() == ndim and t.is_cuda and t.is_contiguous():
         return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -597,23 +600,38 @@ def attention_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
     Rows outside every sequence are neither read nor written: in an ``out`` of the caller's (which
     must not overlap the inputs) they keep what they held, in the returned tensor of a call without ``out`` they are undefined."""
     dt = _dtype_code(q)
-    sq, sk, sv = _need_heads(q, "q", q.dtype), _need_heads(k, "k", q.dtype), _need_heads(v, "v", q.dtype)
-    _need(cu_seqlens, "cu_seqlens", torch.int32, 1)
-    T, Hq, D = q.shape
-    Hkv = k.shape[1]
-    if k.shape != v.shape or k.shape[0] != T or k.shape[2] != D:
-        raise ValueError("k and v must be [T, Hkv, D]")
-    if cu_seqlens.shape[0] < 2:
+    dtype, dev = q.dtype, q.get_device()
+    strides = None
+    if (q.dim() == 3 and isinstance(k, torch.Tensor) and isinstance(v, torch.Tensor) and dev >= 0 and k.dtype is dtype
+            and v.dtype is dtype and dev == k.get_device() == v.get_device()):
+        # the usual case in few steps; anything else is looked at piece by piece below
+        T, Hq, D = q.shape
+        kshape = k.shape
+        if len(kshape) == 3 and T > 1 and D > 1 and kshape[0] == T and kshape[2] == D and v.shape == kshape:
+            (sq, hq, dq), (sk, hk, dk), (sv, hv, dv) = q.stride(), k.stride(), v.stride()
+            if dq == dk == dv == 1 and hq == hk == hv == D:
+                strides, Hkv = (sq, sk, sv), kshape[1]
+    if strides is None:
+        strides = _need_heads(q, "q", dtype), _need_heads(k, "k", dtype), _need_heads(v, "v", dtype)
+        T, Hq, D = q.shape
+        Hkv = k.shape[1]
+        if k.shape != v.shape or k.shape[0] != T or k.shape[2] != D:
+            raise ValueError("k and v must be [T, Hkv, D]")
+        _same_device(q, "q", k=k, v=v)
+    _need(cu_seqlens, "cu_seqlens", _INT32, 1)
+    B = cu_seqlens.shape[0] - 1
+    if B < 1:
         raise ValueError("cu_seqlens must be [B + 1] with B >= 1")
-    _same_device(q, "q", k=k, v=v, cu_seqlens=cu_seqlens, out=out)
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
+        out = torch.empty((T, Hq, D), dtype=dtype, device=q.device)
     else:
-        _need(out, "out", q.dtype, 3)
+        _need(out, "out", dtype, 3)
         if out.shape != q.shape:
             raise ValueError("out must be [T, Hq, D]")
+    if dev != cu_seqlens.get_device() or dev != out.get_device():
+        raise ValueError("cu_seqlens and out must be on the device of q")
     _call(lib().w4a16_attention_prompt, "w4a16_attention_prompt", q.device, q.data_ptr(), k.data_ptr(), v.data_ptr(),
-          dt, T, cu_seqlens.shape[0] - 1, cu_seqlens.data_ptr(), Hq, Hkv, D, sq, sk, sv, out.data_ptr())
+          dt, T, B, cu_seqlens.data_ptr(), Hq, Hkv, D, *strides, out.data_ptr())
     return out
 
 
@@ -636,9 +654,6 @@ def _cache_shape(cache, name: str, bits: int, lead: int, D: int, dev: int):
         if t.get_device() != dev:
             raise ValueError(f"{name} must be on the device of the other arguments")
     return shape
-
-
-_INT8, _INT32, _HALF = torch.int8, torch.int32, torch.float16
 
 
 def _need_caches(k, v, kname: str, vname: str, bits: int, lead: int, D: int, like: torch.Tensor):
@@ -735,7 +750,8 @@ def kv_attention_decode_shared(q: torch.Tensor, kprefix, vprefix, P: int, kcache
     Hp, Pmax = _need_caches(kprefix, vprefix, "kprefix", "vprefix", bits, 1, D, q)
     if Bc != B or lengths.shape[0] != B or Hp != Hkv:
         raise ValueError("caches must be [B, Hkv, Tmax, ...], prefixes [Hkv, Pmax, ...] and lengths [B]")
-    _same_device(q, "q", lengths=lengths)
+    if lengths.get_device() != q.get_device():
+        raise ValueError("lengths must be on the device of q")
     if not 0 <= P <= Pmax:
         raise ValueError("P must be in [0, Pmax]")
     L = lib()
@@ -811,7 +827,8 @@ def kv_evict(kcache, vcache, weights: torch.Tensor, lengths: torch.Tensor, budge
     B, Hkv, Tmax = shape = _need_caches(kcache, vcache, "kcache", "vcache", bits, 2, D, weights)
     if weights.shape != shape or lengths.shape[0] != B:
         raise ValueError("weights must be [B, Hkv, Tmax] and lengths [B]")
-    _same_device(weights, "weights", lengths=lengths)
+    if lengths.get_device() != weights.get_device():
+        raise ValueError("lengths must be on the device of weights")
     if not 0 <= recent <= budget or budget < 1:
         raise ValueError("0 <= recent <= budget and budget >= 1 must hold")
     if out is None:
@@ -836,7 +853,8 @@ def kv_evict(kcache, vcache, weights: torch.Tensor, lengths: torch.Tensor, budge
         raise ValueError("out and capacity disagree")
     if Tout < min(budget, Tmax):
         raise ValueError("out must have room for min(budget, Tmax) tokens")
-    _same_device(weights, "weights", **{"out weights": wo, "out lengths": lo, "out kept": kept})
+    if not weights.get_device() == wo.get_device() == lo.get_device() == kept.get_device():
+        raise ValueError("out must be on the device of weights")
     L = lib()
     need = L.w4a16_kv_evict_workspace(B, Hkv, Tmax)
     if need or work is not None:
