@@ -510,7 +510,13 @@ __device__ __forceinline__ float across_quarters(float x, Op op) {
 // SCORES: every score (base 2) is left in `score`, for row r and token t at index r spad + t, r the row's head
 // in the batch, or (kInLds) its lane.
 constexpr int kNone = 0, kInMemory = 1, kInLds = 2;
-template <int BITS, int D, int SCORES, bool WHOLE = false, int NW = 4>
+// ONCE: the codes are read once and loaded so that the caches do not keep them.
+template <bool ONCE, class V>
+__device__ __forceinline__ V load_codes(const unsigned char* p) {
+    if constexpr (ONCE) return __builtin_nontemporal_load(reinterpret_cast<const V*>(p));
+    else return *reinterpret_cast<const V*>(p);
+}
+template <int BITS, int D, int SCORES, bool WHOLE = false, int NW = 4, bool ONCE = false>
 struct Stream {
     static constexpr int KT = BITS == 8 && D == 128 ? 32 : 64;   // tokens of a tile
     static constexpr int NS = KT / 16;                           // S tiles
@@ -578,19 +584,19 @@ struct Stream {
             for (int s = 0; s < NS; ++s) {
                 const uint32_t off = (uint32_t)min(base + 16 * s + n, end - 1) * RB + KB * qd;
                 if constexpr (KW == 2) {
-                    const u32x2 x = *reinterpret_cast<const u32x2*>(c.kc + off);
+                    const u32x2 x = load_codes<ONCE, u32x2>(c.kc + off);
                     kr[s / 2][2 * (s % 2)] = x.x;
                     kr[s / 2][2 * (s % 2) + 1] = x.y;
                 } else {
 #pragma unroll
                     for (int i = 0; i < KW / 4; ++i)
-                        kr[s * (KW / 4) + i] = *reinterpret_cast<const u32x4*>(c.kc + off + 64 * i);
+                        kr[s * (KW / 4) + i] = load_codes<ONCE, u32x4>(c.kc + off + 64 * i);
                 }
             }
 #pragma unroll
             for (int i = 0; i < VL; ++i) {
                 const int p = lane + 64 * i;
-                vr[i] = *reinterpret_cast<const u32x4*>(c.vc + (uint32_t)min(base + p / VP, end - 1) * RB + 16 * (p % VP));
+                vr[i] = load_codes<ONCE, u32x4>(c.vc + (uint32_t)min(base + p / VP, end - 1) * RB + 16 * (p % VP));
             }
             const uint32_t tok = (uint32_t)min(base + lane % KT, end - 1);
             if constexpr (KT == 64) {
@@ -888,14 +894,13 @@ template <int BITS, int D>
 struct PrefixKind<BITS, D, 0> {
     using type = Stream<BITS, D, kNone>;
 };
-template <int BITS, int D, int WQ, bool SCORES>    // (streaming alone: three blocks a CU)
-__global__ __launch_bounds__(kThreads, WQ == 0 ? 3 : 2) void kv_decode_kernel(const uint16_t* __restrict__ q, int bf16, int B, int Hq,
-                                                                int Hkv, KvCache prefix, KvCache own,
-                                                                const int* __restrict__ lens, DecodeGrid g,
-                                                                float2* __restrict__ ml, float* __restrict__ po,
-                                                                float* __restrict__ score, int spad) {
+template <int BITS, int D, int WQ, bool SCORES, bool ONCE>
+__global__ __launch_bounds__(kThreads, WQ == 0 ? 3 : 2)    // (streaming alone: three blocks a CU)
+void kv_decode_kernel(const uint16_t* __restrict__ q, int bf16, int B, int Hq, int Hkv, KvCache prefix, KvCache own,
+                      const int* __restrict__ lens, DecodeGrid g, float2* __restrict__ ml, float* __restrict__ po,
+                      float* __restrict__ score, int spad) {
     using A = typename PrefixKind<BITS, D, WQ>::type;
-    using S = Stream<BITS, D, SCORES ? kInMemory : kNone>;
+    using S = Stream<BITS, D, SCORES ? kInMemory : kNone, false, 4, ONCE>;
     __shared__ union alignas(16) {
         typename A::Lds a;
         typename S::Lds s;
@@ -1113,6 +1118,13 @@ __global__ __launch_bounds__(kThreads) void kv_weights_kernel(const float2* __re
 constexpr long long kBlocks = 2048;
 constexpr long long kPrefixBlocks = 512;
 constexpr int kMinChunk = 256;
+// Own caches that are read once (one tile of heads) and are most of the work pass the GPU's caches by: with
+// weights, caches that are not in the last-level cache (as between the layers of a model) of 17 MB 13.0 -> 12.0 us,
+// 134 MB 42.8 -> 40.1, 268 MB 62.3 -> 55.6, 537 MB 119 -> 106; one and the same cache again and again 10.9 -> 10.8,
+// 34.0 -> 39.6, 49.3 -> 55.4, 117 -> 106.  Not behind a longer prefix: 128 sequences of up to 1024 behind 32768
+// tokens 118.8 -> 120.2, 32 of up to 512 behind 4096 21.8 -> 23.0; nor where two tiles of heads read them: G = 32,
+// 34 MB, 33.5 -> 38.1.
+constexpr int kOnceHeads = 16;
 
 int divup(long long a, long long b) { return (int)((a + b - 1) / b); }
 
@@ -1201,12 +1213,13 @@ hipError_t shared(const KvSharedArgs& a, float* work, hipStream_t st) {
     const auto q = static_cast<const uint16_t*>(a.q);
     const int bf16 = a.dtype == DT_BF16;
     const dim3 grid((unsigned)(g.pblocks + (long long)a.B * a.Hkv * divup(G, 16) * g.osplit));
-#define W4A16_DECODE(WQ)                                                                                              \
-    hipLaunchKernelGGL((kv_decode_kernel<BITS, D, WQ, false>), grid, dim3(kThreads), 0, st, q, bf16, a.B, a.Hq, a.Hkv, \
-                       a.prefix, a.own, a.lens, g, ml, po, nullptr, 0)
-    if (wq == 0) W4A16_DECODE(0);
-    else if (wq == 2) W4A16_DECODE(2);
-    else W4A16_DECODE(4);
+#define W4A16_DECODE(WQ, ONCE)                                                                                         \
+    hipLaunchKernelGGL((kv_decode_kernel<BITS, D, WQ, false, ONCE>), grid, dim3(kThreads), 0, st, q, bf16, a.B, a.Hq,  \
+                       a.Hkv, a.prefix, a.own, a.lens, g, ml, po, nullptr, 0)
+    if (wq == 2) W4A16_DECODE(2, false);
+    else if (wq == 4) W4A16_DECODE(4, false);
+    else if (G <= kOnceHeads) W4A16_DECODE(0, true);
+    else W4A16_DECODE(0, false);
 #undef W4A16_DECODE
     hipLaunchKernelGGL((kv_merge_kernel<D>), dim3((unsigned)heads), dim3(kThreads), 0, st, ml, po, g.nsplit, bf16,
                        a.Hq, a.P, a.lens, static_cast<uint16_t*>(a.out));
@@ -1241,9 +1254,13 @@ hipError_t weights(const KvWeightsArgs& a, float* work, hipStream_t st) {
     }
 #undef W4A16_WHOLE
     const unsigned blocks = (unsigned)((long long)a.B * a.Hkv * divup(G, 16) * g.osplit);
-    hipLaunchKernelGGL((kv_decode_kernel<BITS, D, 0, true>), dim3(blocks), dim3(kThreads), 0, st,
-                       static_cast<const uint16_t*>(a.q), bf16, a.B, a.Hq, a.Hkv, KvCache{}, a.own, a.lens, g, ml, po,
-                       score, spad);
+#define W4A16_DECODE(ONCE)                                                                                             \
+    hipLaunchKernelGGL((kv_decode_kernel<BITS, D, 0, true, ONCE>), dim3(blocks), dim3(kThreads), 0, st,                \
+                       static_cast<const uint16_t*>(a.q), bf16, a.B, a.Hq, a.Hkv, KvCache{}, a.own, a.lens, g, ml, po, \
+                       score, spad)
+    if (G <= kOnceHeads) W4A16_DECODE(true);
+    else W4A16_DECODE(false);
+#undef W4A16_DECODE
     const int spans = divup(a.Tmax, kSpan);
     hipLaunchKernelGGL((kv_weights_kernel<D>), dim3((unsigned)(heads + (long long)a.B * a.Hkv * spans)),
                        dim3(kThreads), 0, st, ml, po, ns, bf16, static_cast<uint16_t*>(a.out), (int)heads, a.Hq, a.Hkv,
