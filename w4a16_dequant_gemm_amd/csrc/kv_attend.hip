@@ -491,8 +491,8 @@ __device__ __forceinline__ float across_quarters(float x, Op op) {
 // instructions: each of the block's NW waves streams tiles of its own (wave, wave + NW, ...), with no
 // barrier until they are joined at the end, and loads the next tile while it works on one.
 // Measured: 16 sequences of up to 4096 KV8 tokens, 32 heads, D = 128 (318 MB with the scores): 62 us,
-// 5.1 TB/s; 8 of up to 65536 KV4 tokens, 32 heads on 8 (365 MB): 97 us, 3.8 TB/s, the vector units busy
-// 60 % of the cycles (twice the codes a byte).  Three blocks a CU: four spilled (254 us against 97).
+// 5.1 TB/s; 8 of up to 65536 KV4 tokens, 32 heads on 8 (365 MB): 94 us, 3.9 TB/s, the vector units busy
+// 60 % of the cycles (twice the codes a byte).  Three blocks a CU: four spilled (254 us against 97 then).
 // The staged form before it, with barriers between tiles, took 112 and 220 us for the same.
 //   K's codes go from memory to the matrix cores: lane l loads the quarter l / 16 of every 64 bytes
 //     (32 for the shortest rows) of key l % 16's row, so a load covers whole cache lines, and the
@@ -1054,8 +1054,8 @@ __global__ __launch_bounds__(kThreads) void kv_merge_kernel(const float2* __rest
 // Output and accumulated weights in one launch: the first `heads` blocks merge a query head each,
 // the others turn kSpan scores of a (sequence, kv head) into weights: a token's p of each head is
 // 2^(score - M) / L, so the streaming kernel leaves the scores (base 2, fp32) instead of reading the
-// cache twice.  Bound by the scores' bytes, G x 4 a token and kv head: 8.4 us (15 MB) for 16 x 32 heads
-// of up to 4096 tokens, 16 us (70 MB, G = 4) for 8 x 32 of up to 65536.
+// cache twice.  Bound by the scores' bytes, G x 4 a token and kv head: 7.8 us (15 MB) for 16 x 32 heads
+// of up to 4096 tokens, 15 us (70 MB, G = 4) for 8 x 32 of up to 65536.
 constexpr int kSpan = 4 * kThreads;
 constexpr int kStatHeads = 64;           // heads whose statistics are at hand at a time
 template <int D>

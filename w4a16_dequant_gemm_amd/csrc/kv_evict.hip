@@ -12,8 +12,8 @@
 // Gather copies the kept rows' codes and parameters, 16 bytes per thread; nothing is dequantized, so
 // the kept rows are the same bits.  Where a head keeps few rows the selecting block copies them.
 // All of it is bound by memory: the weights, the kept rows in and out.
-// Measured: 16 x 32 heads of up to 4096 KV8 tokens, D = 128, halved: select 15.9 us, gather 100 us (533
-// MB, 5.3 TB/s); 8 heads of 100001 KV4 tokens to 16384: select 4.5 + 7.6 + 7.8 + 11 us, each launch the
+// Measured: 16 x 32 heads of up to 4096 KV8 tokens, D = 128, halved: select 15.7 us, gather 93 us (533
+// MB, 5.7 TB/s); 8 heads of 100001 KV4 tokens to 16384: select 4.5 + 7.6 + 7.8 + 11 us, each launch the
 // latency of its chain (length, earlier histograms, scan, weights; fetching the weights first did not
 // shorten it), gather 9.8 us; 2 x 2 heads of 300 to 128: 8 us, one launch.
 #include <algorithm>
