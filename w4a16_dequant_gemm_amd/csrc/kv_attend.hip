@@ -124,7 +124,8 @@ __device__ __forceinline__ float wave_max(float v) {
 // of the cycles, the matrix cores 27 %, and waves wait 33 % of theirs.  Tried and slower or equal: tiles
 // of 32 tokens (three waves a SIMD instead of two: 165 us against 126 then), the scores of the next
 // tile interleaved with the weights of this one as in attention.hip (118 us; with a second set of
-// code registers 143), one wave a SIMD with twice the registers (166).
+// code registers 143), one wave a SIMD with twice the registers (166), blocks of eight waves and 256 rows,
+// which halve the work on codes (131 against 115).
 template <int BITS, int D, int WQ, int WK>
 struct Attend {
     static constexpr int NBUF = WK == 1 ? 2 : 1;
@@ -945,8 +946,9 @@ void kv_decode_kernel(const uint16_t* __restrict__ q, int bf16, int B, int Hq, i
 
 // Short sequences in one launch: block = sequence, kv head, tile of 16 of its G heads, over the prefix
 // and the sequence's own tokens.  SCORES (G <= 16, no prefix): then the accumulated weights, from the scores
-// that the block's waves have just written (up to kLdsTokens tokens to LDS).  Bound by the latency of a few dependent tiles a wave: 4
-// sequences behind 333 KV8 tokens, D = 64: 6 us; one of 500, with weights: 8.
+// that the block's waves have just written (up to kLdsTokens tokens to LDS).  Bound by the latency of a
+// few dependent tiles a wave: 4 sequences behind 333 KV8 tokens, D = 64: 6.4 us; one of 500, with
+// weights: 7.2.
 constexpr int kLdsTokens = 512, kLdsStride = kLdsTokens + 4;     // (+ 4: the 16 rows start in different banks)
 template <int BITS, int D, int SCORES, int NW>
 __global__ __launch_bounds__(64 * NW, 2) void kv_whole_kernel(const uint16_t* __restrict__ q, int bf16, int Hq, int Hkv,
