@@ -439,8 +439,8 @@ int64_t w4a16_kv_attention_shared_workspace(int64_t B, int64_t Hq, int64_t Hkv, 
  * the same P tokens (a system prompt, a document): out[b][h] = softmax(q[b][h] . K / sqrt(D)) V over
  * the shared tokens and then the first lengths[b] tokens of the sequence's own cache, kv head
  * h / (Hq / Hkv).  The prefix is held once and read once per 128 of the B * Hq / Hkv
- * query rows of a kv head, not once per sequence.
- *   q        [B, Hq, D] fp16/bf16, 16-byte aligned; out [B, Hq, D] same dtype.
+ * query rows of a kv head, not once per sequence (short ones out of the GPU's caches).
+ *   q        [B, Hq, D] fp16/bf16, 16-byte aligned; out [B, Hq, D] same dtype, apart from the inputs and work.
  *   prefix   w4a16_kv_quantize output with H = Hkv and T = Pmax ([Hkv, Pmax, ...]); its first P
  *            tokens are read, 0 <= P <= Pmax <= 2^24.  P == 0: its pointers are not looked at.
  *   own      [B, Hkv, Tmax, ...], 1 <= Tmax <= 2^24.

@@ -738,7 +738,7 @@ def kv_attention_decode_shared(q: torch.Tensor, kprefix, vprefix, P: int, kcache
     """Decode attention of ``B`` sequences that begin with the same tokens: ``q [B, Hq, D]`` over the
     first ``P`` tokens of the shared caches ``(codes, scales, zeros)`` of shape ``[Hkv, Pmax, ...]``,
     then the first ``lengths[b]`` (int32, on the device, possibly 0) of the sequence's own
-    ``[B, Hkv, Tmax, ...]``.  The prefix is held and read once for the batch.  A sequence without any
+    ``[B, Hkv, Tmax, ...]``.  The prefix is held once for the batch, and a long one read once.  A sequence without any
     token gets zeros.  ``work`` is an optional fp32 buffer of at least
     :func:`kv_attention_shared_workspace` elements (0 for short sequences); calls that may overlap
     need one each."""
