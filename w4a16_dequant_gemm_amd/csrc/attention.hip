@@ -23,7 +23,7 @@
 // cores are busy 60 % of the cycles at the clock that the power limit leaves (1.75 GHz), so what saves
 // instructions, not what hides them, would shorten it: raised issue priorities, the maximum interleaved
 // with the second product and stores of the output through LDS changed nothing.  12 packed prompts of
-// up to 1024 tokens, fp16: 40 us, the longest block's 16 tiles of keys; 6 of up to 96: 6 us, latency.
+// up to 1024 tokens, fp16: 40 us (a block costs 5 us besides 1.9 a tile of keys); 6 of up to 96: 6.6 us, latency.
 // One prompt of 128 / 512 / 1024 / 2048 / 4096 tokens: 8.8 / 16 / 24 / 51 / 154 us.  Before the loads went
 // straight to LDS and the scores of the next tile under the weights of this one: 2313 and 49 us.
 #include "attn.h"
