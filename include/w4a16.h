@@ -429,8 +429,10 @@ typedef struct {
     uint16_t *vscales, *vzeros;
 } w4a16_kv_cache_out;
 
-/* fp32 elements of the w4a16_kv_attention_decode_shared workspace (host only; 0: none, for short
- * sequences), or a negative status. */
+/* fp32 elements of workspace that hold every w4a16_kv_attention_decode_shared call of these heads with
+ * at most B sequences, P shared and Tmax own tokens (host only; 0: none, for short sequences), or a
+ * negative status.  The size never grows where B, P or Tmax shrinks: one buffer for a program's largest
+ * call does for the others. */
 int64_t w4a16_kv_attention_shared_workspace(int64_t B, int64_t Hq, int64_t Hkv, int64_t P, int64_t Tmax,
                                             int64_t D);
 
@@ -461,8 +463,8 @@ int w4a16_kv_attention_decode_shared(const void* q, int dtype, int64_t B, int64_
                                      const w4a16_kv_cache* own, const int32_t* lengths, int64_t Tmax, float* work,
                                      void* out, void* stream);
 
-/* fp32 elements of the w4a16_kv_attention_decode_weights workspace (host only; 0: none, for short
- * sequences), or a negative status. */
+/* fp32 elements of workspace that hold every w4a16_kv_attention_decode_weights call of these heads with
+ * at most B sequences and Tmax tokens (host only; 0: none, for short sequences), or a negative status. */
 int64_t w4a16_kv_attention_weights_workspace(int64_t B, int64_t Hq, int64_t Hkv, int64_t Tmax, int64_t D);
 
 /*
@@ -484,8 +486,8 @@ int w4a16_kv_attention_decode_weights(const void* q, int dtype, int64_t B, int64
                                       int bits, const w4a16_kv_cache* own, const int32_t* lengths, int64_t Tmax,
                                       const float* weights, float* sums, float* work, void* out, void* stream);
 
-/* fp32 elements of the w4a16_kv_evict workspace (host only; 0: none, for up to 8192 tokens), or a
- * negative status. */
+/* fp32 elements of workspace that hold every w4a16_kv_evict call of at most B sequences and Tmax tokens
+ * (host only; 0: none, for up to 8192 tokens), or a negative status. */
 int64_t w4a16_kv_evict_workspace(int64_t B, int64_t Hkv, int64_t Tmax);
 
 /*

@@ -709,7 +709,8 @@ def _decode_out(out, q: torch.Tensor) -> torch.Tensor:
 
 
 def kv_attention_shared_workspace(B: int, Hq: int, Hkv: int, P: int, Tmax: int, D: int) -> int:
-    """fp32 elements of the scratch buffer that :func:`kv_attention_decode_shared` needs (0: none)."""
+    """fp32 elements of a scratch buffer that holds every :func:`kv_attention_decode_shared` call of these
+    heads with at most ``B`` sequences, ``P`` shared and ``Tmax`` own tokens (0: none)."""
     need = lib().w4a16_kv_attention_shared_workspace(B, Hq, Hkv, P, Tmax, D)
     if need < 0:
         raise W4A16Error(int(need), "w4a16_kv_attention_shared_workspace")
@@ -717,7 +718,8 @@ def kv_attention_shared_workspace(B: int, Hq: int, Hkv: int, P: int, Tmax: int, 
 
 
 def kv_attention_weights_workspace(B: int, Hq: int, Hkv: int, Tmax: int, D: int) -> int:
-    """fp32 elements of the scratch buffer that :func:`kv_attention_decode_weights` needs (0: none)."""
+    """fp32 elements of a scratch buffer that holds every :func:`kv_attention_decode_weights` call of these
+    heads with at most ``B`` sequences and ``Tmax`` tokens (0: none)."""
     need = lib().w4a16_kv_attention_weights_workspace(B, Hq, Hkv, Tmax, D)
     if need < 0:
         raise W4A16Error(int(need), "w4a16_kv_attention_weights_workspace")
@@ -725,7 +727,8 @@ def kv_attention_weights_workspace(B: int, Hq: int, Hkv: int, Tmax: int, D: int)
 
 
 def kv_evict_workspace(B: int, Hkv: int, Tmax: int) -> int:
-    """fp32 elements of the scratch buffer that :func:`kv_evict` needs (0: none)."""
+    """fp32 elements of a scratch buffer that holds every :func:`kv_evict` call of at most ``B`` sequences
+    and ``Tmax`` tokens (0: none)."""
     need = lib().w4a16_kv_evict_workspace(B, Hkv, Tmax)
     if need < 0:
         raise W4A16Error(int(need), "w4a16_kv_evict_workspace")

@@ -481,7 +481,7 @@ int w4a16_kv_attention_decode_shared(const void* q, int dtype, int64_t B, int64_
     if (dtype != W4A16_F16 && dtype != W4A16_BF16) return W4A16_ERR_DTYPE;
     if (bits != 8 && bits != 4) return W4A16_ERR_SCHEME;
     int st = check_kv_batch(B, Hq, Hkv, P, Pmax, Tmax, D);
-    if (st == W4A16_OK && !work && w4a16::kv_shared_workspace_floats(B, Hq, Hkv, P, Tmax, D) > 0) st = W4A16_ERR_NULL;
+    if (st == W4A16_OK && !work && w4a16::kv_shared_call_floats(B, Hq, Hkv, P, Tmax, D) > 0) st = W4A16_ERR_NULL;
     if (st == W4A16_OK) st = check_cache(own, bits);
     if (st == W4A16_OK && P > 0) st = check_cache(prefix, bits);
     if (st != W4A16_OK) return st;
@@ -519,7 +519,7 @@ int w4a16_kv_attention_decode_weights(const void* q, int dtype, int64_t B, int64
     if (bits != 8 && bits != 4) return W4A16_ERR_SCHEME;
     int st = check_kv_batch(B, Hq, Hkv, 0, 0, Tmax, D);
     if (st == W4A16_OK && B * Hq * Tmax > (int64_t(1) << 36)) st = W4A16_ERR_SHAPE;
-    if (st == W4A16_OK && !work && w4a16::kv_weights_workspace_floats(B, Hq, Hkv, Tmax, D) > 0) st = W4A16_ERR_NULL;
+    if (st == W4A16_OK && !work && w4a16::kv_weights_call_floats(B, Hq, Hkv, Tmax, D) > 0) st = W4A16_ERR_NULL;
     if (st == W4A16_OK) st = check_cache(own, bits);
     if (st != W4A16_OK) return st;
     if (!aligned(q, 16) || !aligned(lengths, 4) || (weights && !aligned(weights, 4)) || !aligned(sums, 4) ||

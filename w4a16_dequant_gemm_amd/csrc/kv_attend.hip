@@ -23,6 +23,8 @@
 // Rounded to 16 bits are only the weights p s_t (fp16, relative 2^-11, scaled so that the largest
 // s_t seen so far becomes 2^7 and small ones keep their bits) and the output.  Scores, maxima,
 // sums and outputs are fp32.
+#include <algorithm>
+
 #include "attn.h"
 #include "launch.h"
 
@@ -1272,15 +1274,49 @@ hipError_t weights(const KvWeightsArgs& a, float* work, hipStream_t st) {
 
 }  // namespace
 
-long long kv_shared_workspace_floats(long long B, long long Hq, long long Hkv, long long P, long long Tmax,
-                                     long long D) {
+long long kv_shared_call_floats(long long B, long long Hq, long long Hkv, long long P, long long Tmax, long long D) {
     if (whole_shared(B, Hkv, Hq / Hkv, P, Tmax)) return 0;
     return parts_floats(B * Hq, divup(P, prefix_chunk(B, Hq, Hkv, P, Tmax)) + divup(Tmax, own_chunk(B, Hq, Hkv, Tmax)), D);
 }
 
-long long kv_weights_workspace_floats(long long B, long long Hq, long long Hkv, long long Tmax, long long D) {
+long long kv_weights_call_floats(long long B, long long Hq, long long Hkv, long long Tmax, long long D) {
     if (whole_weights(B, Hkv, Hq / Hkv, Tmax)) return Tmax <= kLdsTokens ? 0 : B * Hq * score_pad(Tmax);
     return B * Hq * score_pad(Tmax) + parts_floats(B * Hq, divup(Tmax, own_chunk(B, Hq, Hkv, Tmax)), D);
+}
+
+// The sizes that callers are told: what any call of at most B sequences, P and Tmax tokens uses.  (What a
+// call uses itself falls here and there as these grow: chunks are rounded up, and the rules above
+// change the kernel.)  A row has at most max(1, blocks / tiles) splits and one per kMinChunk tokens, so
+// over all b <= B:
+//   own caches, b Hkv tiles(G) tiles: Hq b max(1, min(c / b, s)) <= Hq max(B, min(c, B s)), with
+//     c = kBlocks / (Hkv tiles(G)) and s the splits of kMinChunk tokens;
+//   prefix, Hkv divup(b G, rt) tiles of rt rows for b Hq rows: blocks / tiles splits are at most blocks rt
+//     rows' outputs, kBlocks of 16 or kPrefixBlocks of 64 or, for more than 64 rows, of 128.
+static long long own_rows(long long B, long long Hq, long long Hkv, long long Tmax) {
+    const long long c = kBlocks / (Hkv * divup(Hq / Hkv, 16));
+    return Hq * std::max(B, std::min(c, B * divup(Tmax, kMinChunk)));
+}
+static long long prefix_rows(long long B, long long Hq, long long Hkv, long long P) {
+    if (P == 0) return 0;
+    const long long most = std::max(16 * kBlocks, (B * (Hq / Hkv) > 64 ? 128 : 64) * kPrefixBlocks);
+    return std::max(B * Hq, std::min(most, B * Hq * divup(P, kMinChunk)));
+}
+
+long long kv_shared_workspace_floats(long long B, long long Hq, long long Hkv, long long P, long long Tmax,
+                                     long long D) {
+    // whole_shared, where every smaller call is one of its too (the last rule asks for more than 16 rows)
+    const long long G = Hq / Hkv, N = P + Tmax, blocks = B * Hkv * divup(G, 16);
+    if (whole_shared(B, Hkv, G, P, Tmax) && (N <= 512 || (N <= 768 && blocks <= 256) || G > 16)) return 0;
+    return (prefix_rows(B, Hq, Hkv, P) + own_rows(B, Hq, Hkv, Tmax)) * (D + 2);
+}
+
+long long kv_weights_workspace_floats(long long B, long long Hq, long long Hkv, long long Tmax, long long D) {
+    const bool few = Hq / Hkv <= 16;
+    if (few && Tmax <= kLdsTokens) return 0;
+    const long long scores = B * Hq * score_pad(Tmax);
+    // whole_weights at every smaller size too
+    if (few && Tmax <= 768 && B * Hkv <= 256) return scores;
+    return scores + own_rows(B, Hq, Hkv, Tmax) * (D + 2);
 }
 
 hipError_t launch_kv_shared(const KvSharedArgs& a, float* work, hipStream_t st) {

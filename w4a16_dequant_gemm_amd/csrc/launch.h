@@ -110,6 +110,9 @@ struct KvWeightsArgs {
     float* sums;
     int dtype, bits, B, Hq, Hkv, D, Tmax;
 };
+// fp32 elements of workspace: what a call uses, and what any call of at most these B, P and Tmax does.
+long long kv_shared_call_floats(long long B, long long Hq, long long Hkv, long long P, long long Tmax, long long D);
+long long kv_weights_call_floats(long long B, long long Hq, long long Hkv, long long Tmax, long long D);
 long long kv_shared_workspace_floats(long long B, long long Hq, long long Hkv, long long P, long long Tmax,
                                      long long D);
 long long kv_weights_workspace_floats(long long B, long long Hq, long long Hkv, long long Tmax, long long D);
