@@ -15,8 +15,11 @@
 // that lane if V's rows are taken in the same order, so P goes from registers to the matrix
 // cores without a trip through LDS.
 // P is rounded to the inputs' type (fp16 / bf16) for the second product, the only rounding
-// besides the output's: relative 2^-11 / 2^-8 per weight, like the values themselves; scores,
-// maxima, sums and outputs stay in fp32, and l sums the unrounded weights.
+// besides the output's: relative 2^-11 / 2^-8 per weight, like the values themselves.  fp16 weights
+// are held times 2^7 (kRaise), so that this holds down to 2^-21 of the largest and smaller ones are off by
+// 2^-32 of it at most: taken as they are, weights below 2^-14 would lose bits and those below 2^-25
+// vanish, which long prompts add up (one token of most of the weight and 16384 of 2^-25: 0.35 %).
+// Scores, maxima, sums and outputs stay in fp32, and l sums the unrounded weights.
 //
 // Measured (32 heads, D = 128): one sequence of 16384 tokens, bf16, grouped heads: 1.96 ms, 1.12 PFLOP/s
 // of the causal products' 2.2 TFLOP; a large library product of this card reaches 1.14.  The matrix
@@ -35,6 +38,9 @@ namespace {
 
 constexpr int kRows = 128;      // query rows of a block
 constexpr int kKeys = 64;       // keys of a tile
+// exponent that a row's largest weight gets (2^15 with a maximum that lags by 8); l and O share the factor
+template <int DT>
+constexpr float kRaise = DT == DT_F16 ? 7.0f : 0.0f;
 
 // The row tile that comes `rank`-th in order of work (tile j of a sequence has j + 1 times kRows keys,
 // less the last one's shortfall): late tiles of all sequences first, so that the long blocks do not
@@ -199,8 +205,8 @@ __device__ __forceinline__ void rows_again(const uint16_t* q, int qs, const uint
         for (int s = 0; s < 2; ++s)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float p0 = exp2_raw((S[8 * s + 2 * j] - base) * c);
-                const float p1 = exp2_raw((S[8 * s + 2 * j + 1] - base) * c);
+                const float p0 = exp2_raw(fmaf(S[8 * s + 2 * j] - base, c, kRaise<DT>));
+                const float p1 = exp2_raw(fmaf(S[8 * s + 2 * j + 1] - base, c, kRaise<DT>));
                 l += p0 + p1;
                 P[s][j] = pack2<DT>(p0, p1);
             }
@@ -334,9 +340,9 @@ __global__ __launch_bounds__(256 * GROUPS, 2) void attention_prompt_kernel(
     for (int i = 0; i < D / 32; ++i)
 #pragma unroll
         for (int e = 0; e < 16; ++e) o[i][e] = 0.0f;
-    // softmax in base 2: weight = 2^(c (S - M)), M the row's running maximum (of raw scores)
-    float M = -__builtin_inff(), m = M, l = 0.0f;
-    bool big = false;                               // wave-uniform: some |c M| is above 2^20
+    // softmax in base 2: weight = 2^(c (S - M) + kRaise), M the row's running maximum (of raw scores)
+    float M = -__builtin_inff(), m = M, l = 0.0f;   // m = c M - kRaise
+    bool big = false;                               // wave-uniform: some |m| is above 2^20
     const float c = 1.4426950408889634f / sqrtf((float)D);
 
     // running maximum of tile t; where it rises O and l are rescaled
@@ -347,13 +353,13 @@ __global__ __launch_bounds__(256 * GROUPS, 2) void attention_prompt_kernel(
 #pragma unroll
             for (int e = 0; e < 16; ++e) mt = fmaxf(mt, S[kb2][e]);
         mt = max_halves(mt);
-        // O and l follow a maximum that may lag the true one by 8 / c (weights up to 2^8): the
+        // O and l follow a maximum that may lag the true one by 8 / c (weights up to 2^8 more): the
         // rescaling of O is then rare, and exact either way
         if (any_lane(mt > M + 8.0f / c)) {
             const float Mn = fmaxf(M, mt);
             const float f = exp2_raw((M - Mn) * c);
             M = Mn;
-            m = M * c;
+            m = fmaf(M, c, -kRaise<DT>);
             l *= f;
 #pragma unroll
             for (int i = 0; i < D / 32; ++i)
@@ -365,7 +371,7 @@ __global__ __launch_bounds__(256 * GROUPS, 2) void attention_prompt_kernel(
         // row share and which cancels; where it could pass the exponent range, S - M first
         sub = m;
         if (big) {
-            sub = 0.0f;
+            sub = -kRaise<DT>;
 #pragma unroll
             for (int kb2 = 0; kb2 < 2; ++kb2)
 #pragma unroll
