@@ -121,6 +121,8 @@ struct TileLoad {
     }
 };
 
+// A maximum as a reference: a row whose scores are -inf so far has none.
+__device__ __forceinline__ float number_or_zero(float M) { return M == -__builtin_inff() ? 0.0f : M; }
 __device__ __forceinline__ bool any_lane(bool p) { return __builtin_amdgcn_ballot_w64(p) != 0; }
 // this wave's loads into LDS have landed, and its reads of LDS are in registers
 __device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory"); }
@@ -193,7 +195,7 @@ __device__ __forceinline__ void rows_again(const uint16_t* q, int qs, const uint
             mt = fmaxf(mt, S[e]);
         }
         const float Mn = fmaxf(M, max_halves(mt));
-        const float f = M == Mn ? 1.0f : exp2_raw((M - Mn) * c), base = Mn == -__builtin_inff() ? 0.0f : Mn;
+        const float f = M == Mn ? 1.0f : exp2_raw((M - Mn) * c), base = number_or_zero(Mn);
         M = Mn;
         l *= f;
 #pragma unroll
@@ -341,7 +343,8 @@ __global__ __launch_bounds__(256 * GROUPS, 2) void attention_prompt_kernel(
 #pragma unroll
         for (int e = 0; e < 16; ++e) o[i][e] = 0.0f;
     // softmax in base 2: weight = 2^(c (S - M) + kRaise), M the row's running maximum (of raw scores)
-    float M = -__builtin_inff(), m = M, l = 0.0f;   // m = c M - kRaise
+    float M = -__builtin_inff(), l = 0.0f;
+    float m = -kRaise<DT>;                          // c M - kRaise, with 0 for an M of -inf: all weights are 0
     bool big = false;                               // wave-uniform: some |m| is above 2^20
     const float c = 1.4426950408889634f / sqrtf((float)D);
 
@@ -357,9 +360,9 @@ __global__ __launch_bounds__(256 * GROUPS, 2) void attention_prompt_kernel(
         // rescaling of O is then rare, and exact either way
         if (any_lane(mt > M + 8.0f / c)) {
             const float Mn = fmaxf(M, mt);
-            const float f = exp2_raw((M - Mn) * c);
+            const float f = M == Mn ? 1.0f : exp2_raw((M - Mn) * c);
             M = Mn;
-            m = fmaf(M, c, -kRaise<DT>);
+            m = fmaf(number_or_zero(M), c, -kRaise<DT>);
             l *= f;
 #pragma unroll
             for (int i = 0; i < D / 32; ++i)
@@ -372,10 +375,11 @@ __global__ __launch_bounds__(256 * GROUPS, 2) void attention_prompt_kernel(
         sub = m;
         if (big) {
             sub = -kRaise<DT>;
+            const float ref = number_or_zero(M);
 #pragma unroll
             for (int kb2 = 0; kb2 < 2; ++kb2)
 #pragma unroll
-                for (int e = 0; e < 16; ++e) S[kb2][e] -= M;
+                for (int e = 0; e < 16; ++e) S[kb2][e] -= ref;
         }
     };
     auto weights = [&](const f32x16 (&S)[2], float sub, u32x4 (&P)[4]) {
