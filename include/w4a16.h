@@ -442,7 +442,8 @@ int64_t w4a16_kv_attention_shared_workspace(int64_t B, int64_t Hq, int64_t Hkv, 
  * the shared tokens and then the first lengths[b] tokens of the sequence's own cache, kv head
  * h / (Hq / Hkv).  The prefix is held once and read once per 128 of the B * Hq / Hkv
  * query rows of a kv head, not once per sequence (short ones out of the GPU's caches).
- *   q        [B, Hq, D] fp16/bf16, 16-byte aligned; out [B, Hq, D] same dtype, apart from the inputs and work.
+ *   q        [B, Hq, D] fp16/bf16, 16-byte aligned; out [B, Hq, D] same dtype.  out and work must not
+ *            overlap an input, nor each other (W4A16_ERR_OVERLAP; caches taken whole).
  *   prefix   w4a16_kv_quantize output with H = Hkv and T = Pmax ([Hkv, Pmax, ...]); its first P
  *            tokens are read, 0 <= P <= Pmax <= 2^24.  P == 0: its pointers are not looked at.
  *   own      [B, Hkv, Tmax, ...], 1 <= Tmax <= 2^24.
@@ -476,7 +477,8 @@ int64_t w4a16_kv_attention_weights_workspace(int64_t B, int64_t Hq, int64_t Hkv,
  *   lengths  device int32 [B]; each value is clamped into [0, Tmax] on the device.  A sequence of
  *            length 0 gets zeros.
  *   weights  [B, Hkv, Tmax] fp32, or NULL: the sums start from 0.
- *   sums     [B, Hkv, Tmax] fp32; may be `weights` (accumulation in place).
+ *   sums     [B, Hkv, Tmax] fp32; may be `weights` (accumulation in place), else apart from the inputs,
+ *            out and work.
  *   work     w4a16_kv_attention_weights_workspace(...) fp32 elements, 16-byte aligned (scratch), or NULL
  *            when that is 0.
  * q, out, caches, arithmetic and limits as for w4a16_kv_attention_decode_shared without a prefix
@@ -506,7 +508,8 @@ int64_t w4a16_kv_evict_workspace(int64_t B, int64_t Hkv, int64_t Tmax);
  *   work         w4a16_kv_evict_workspace(B, Hkv, Tmax) fp32 elements, 16-byte aligned (scratch), or
  *                NULL when that is 0.
  * 0 <= recent <= budget, 1 <= budget <= 2^24; the other limits as above.
- * No output may overlap an input (W4A16_ERR_OVERLAP): shrink into a second cache.
+ * No output and no workspace may overlap an input or another of them (W4A16_ERR_OVERLAP): shrink into a
+ * second cache.
  */
 int w4a16_kv_evict(const w4a16_kv_cache* in, const float* weights, const int32_t* lengths, int64_t B, int64_t Hkv,
                    int64_t Tmax, int64_t D, int bits, int64_t budget, int64_t recent, const w4a16_kv_cache_out* out,

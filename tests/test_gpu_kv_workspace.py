@@ -76,3 +76,23 @@ def test_evict():
     want = torch.cat([torch.sort(w[0, 0, :T - 10], descending=True, stable=True)[1][:990].sort()[0],
                       torch.arange(T - 10, T, device="cuda")])
     assert torch.equal(got[4][0, 0].long(), want)
+
+
+def test_overlapping_outputs_are_refused():
+    B, Hq, Hkv, D, T = 2, 8, 2, 64, 700
+    q = torch.randn((B, Hq, D), device="cuda").to(H)
+    k, v = make_cache((B, Hkv, T, D), 8, H, 3), make_cache((B, Hkv, T, D), 8, H, 4)
+    kp, vp = make_cache((Hkv, 9, D), 8, H, 5), make_cache((Hkv, 9, D), 8, H, 6)
+    n = torch.tensor([T, 3], dtype=torch.int32, device="cuda")
+    w = torch.zeros((B, Hkv, T), device="cuda")
+    with pytest.raises(W4.W4A16Error):
+        W4.kv_attention_decode_shared(q, kp, vp, 9, k, v, n, 8, out=q)
+    with pytest.raises(W4.W4A16Error):
+        W4.kv_attention_decode_weights(q, k, v, n, w, 8, out=q)
+    with pytest.raises(W4.W4A16Error):
+        W4.kv_attention_decode_weights(q, k, v, n, w, 8, out=w.view(H).view(-1)[:q.numel()].view(q.shape))
+    with pytest.raises(W4.W4A16Error):
+        W4.kv_attention_decode_weights(q, k, v, n, w, 8, work=v[0].view(torch.float32).view(-1))
+    out, sums = W4.kv_attention_decode_weights(q, k, v, n, w, 8)       # in place
+    torch.cuda.synchronize()
+    assert sums.data_ptr() == w.data_ptr() and abs(float(w.sum()) - B * Hq) < 1e-2

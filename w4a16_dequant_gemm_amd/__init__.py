@@ -742,7 +742,7 @@ def kv_attention_decode_shared(q: torch.Tensor, kprefix, vprefix, P: int, kcache
     first ``P`` tokens of the shared caches ``(codes, scales, zeros)`` of shape ``[Hkv, Pmax, ...]``,
     then the first ``lengths[b]`` (int32, on the device, possibly 0) of the sequence's own
     ``[B, Hkv, Tmax, ...]``.  The prefix is held once for the batch, and a long one read once.  A sequence without any
-    token gets zeros.  ``work`` is an optional fp32 buffer of at least
+    token gets zeros.  ``out`` must not overlap the inputs.  ``work`` is an optional fp32 buffer of at least
     :func:`kv_attention_shared_workspace` elements (0 for short sequences); calls that may overlap
     need one each."""
     dt = _dtype_code(q)
@@ -777,7 +777,8 @@ def kv_attention_decode_weights(q: torch.Tensor, kcache, vcache, lengths: torch.
     ``sums[b, hk, t] = weights[b, hk, t] + sum of the softmax weights of the heads of kv head hk`` for
     ``t < lengths[b]`` (entries behind are not written), fp32 ``[B, Hkv, Tmax]``.  ``sums`` defaults to
     ``weights``, which is then updated in place; ``weights=None`` starts from 0 (``sums`` defaults to
-    a zero tensor then).  A sequence of length 0 gets zeros.  ``work`` is an optional fp32 buffer of at
+    a zero tensor then).  A sequence of length 0 gets zeros.  ``out`` and ``sums`` must not overlap the
+    other inputs or each other.  ``work`` is an optional fp32 buffer of at
     least :func:`kv_attention_weights_workspace` elements (0 for short sequences)."""
     dt = _dtype_code(q)
     _need(q, "q", q.dtype, 3)

@@ -84,7 +84,28 @@ int check_kv_batch(int64_t B, int64_t Hq, int64_t Hkv, int64_t P, int64_t Pmax, 
 
 bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return a && b && x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
+    return a && b && na > 0 && nb > 0 && x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
+}
+
+// Memory that a call reads or writes, from its first byte to its last.
+struct Span {
+    const void* p;
+    int64_t n;
+};
+template <class Cache>
+struct CacheSpans {
+    Span s[6];
+    CacheSpans(const Cache& c, int64_t rows, int64_t D, int bits)
+        : s{{c.kcodes, rows * (D * bits / 8)}, {c.vcodes, rows * (D * bits / 8)}, {c.kscales, 2 * rows}, {c.vscales, 2 * rows},
+            {bits == 4 ? c.kzeros : nullptr, 2 * rows}, {bits == 4 ? c.vzeros : nullptr, 2 * rows}} {}
+};
+// Blocks read their inputs at times of their own: nothing that is written may share memory with an
+// input, nor with anything else that is written.
+template <size_t N>
+bool overlaps(const Span& o, const Span (&others)[N]) {
+    for (const Span& x : others)
+        if (&x != &o && overlap(o.p, o.n, x.p, x.n)) return true;
+    return false;
 }
 
 int hip_status(hipError_t e) { return e == hipSuccess ? W4A16_OK : W4A16_ERR_HIP; }
@@ -486,6 +507,14 @@ int w4a16_kv_attention_decode_shared(const void* q, int dtype, int64_t B, int64_
     if (st == W4A16_OK && P > 0) st = check_cache(prefix, bits);
     if (st != W4A16_OK) return st;
     if (!aligned(q, 16) || !aligned(lengths, 4) || !aligned(work, 16) || !aligned(out, 2)) return W4A16_ERR_ALIGN;
+    const CacheSpans<w4a16_kv_cache> mine(*own, B * Hkv * Tmax, D, bits);
+    const Span ins[] = {{q, 2 * B * Hq * D}, {lengths, 4 * B}};
+    const Span outs[] = {{out, 2 * B * Hq * D}, {work, 4 * w4a16::kv_shared_call_floats(B, Hq, Hkv, P, Tmax, D)}};
+    for (const Span& o : outs) {
+        if (overlaps(o, ins) || overlaps(o, mine.s) || overlaps(o, outs)) return W4A16_ERR_OVERLAP;
+        if (P > 0 && overlaps(o, CacheSpans<w4a16_kv_cache>(*prefix, (Hkv - 1) * Pmax + P, D, bits).s))
+            return W4A16_ERR_OVERLAP;
+    }
     w4a16::KvSharedArgs a = {};
     a.q = q;
     a.out = out;
@@ -525,8 +554,12 @@ int w4a16_kv_attention_decode_weights(const void* q, int dtype, int64_t B, int64
     if (!aligned(q, 16) || !aligned(lengths, 4) || (weights && !aligned(weights, 4)) || !aligned(sums, 4) ||
         !aligned(work, 16) || !aligned(out, 2))
         return W4A16_ERR_ALIGN;
-    const int64_t n = B * Hkv * Tmax * 4;
-    if (weights != sums && overlap(weights, n, sums, n)) return W4A16_ERR_OVERLAP;
+    const CacheSpans<w4a16_kv_cache> mine(*own, B * Hkv * Tmax, D, bits);
+    const Span ins[] = {{q, 2 * B * Hq * D}, {lengths, 4 * B}, {weights == sums ? nullptr : weights, 4 * B * Hkv * Tmax}};
+    const Span outs[] = {{out, 2 * B * Hq * D}, {sums, 4 * B * Hkv * Tmax},
+                         {work, 4 * w4a16::kv_weights_call_floats(B, Hq, Hkv, Tmax, D)}};
+    for (const Span& o : outs)
+        if (overlaps(o, ins) || overlaps(o, mine.s) || overlaps(o, outs)) return W4A16_ERR_OVERLAP;
     w4a16::KvWeightsArgs a = {};
     a.q = q;
     a.out = out;
@@ -561,32 +594,22 @@ int w4a16_kv_evict(const w4a16_kv_cache* in, const float* weights, const int32_t
     if (st == W4A16_OK) st = check_cache(in, bits);
     if (st == W4A16_OK) st = check_cache(out, bits);
     if (st != W4A16_OK) return st;
-    const int64_t words = w4a16::kv_evict_workspace_words(B, Hkv, Tmax);
+    const int64_t words = w4a16::kv_evict_call_words(B, Hkv, Tmax);
     if (words > 0 && !work) return W4A16_ERR_NULL;
     if (words > 0 && !aligned(work, 16)) return W4A16_ERR_ALIGN;
     if (!aligned(weights, 4) || !aligned(lengths, 4) || !aligned(weights_out, 4) || !aligned(lengths_out, 4) ||
         !aligned(kept, 4))
         return W4A16_ERR_ALIGN;
-    // blocks read their inputs at times of their own: no output may share memory with an input,
-    // nor with another output
-    struct Span {
-        const void* p;
-        int64_t n;
-    };
-    const int64_t R = B * Hkv * Tmax, Ro = B * Hkv * Tout, cb = D * bits / 8;
-    const Span ins[] = {{in->kcodes, R * cb}, {in->vcodes, R * cb}, {in->kscales, 2 * R}, {in->vscales, 2 * R},
-                        {bits == 4 ? in->kzeros : nullptr, 2 * R}, {bits == 4 ? in->vzeros : nullptr, 2 * R},
-                        {weights, 4 * R}, {lengths, 4 * B}};
-    const Span outs[] = {{out->kcodes, Ro * cb}, {out->vcodes, Ro * cb}, {out->kscales, 2 * Ro},
-                         {out->vscales, 2 * Ro}, {bits == 4 ? out->kzeros : nullptr, 2 * Ro},
-                         {bits == 4 ? out->vzeros : nullptr, 2 * Ro}, {weights_out, 4 * Ro}, {lengths_out, 4 * B},
-                         {kept, 4 * B * Hkv * budget}};
-    for (const Span& o : outs) {
-        for (const Span& i : ins)
-            if (overlap(o.p, o.n, i.p, i.n)) return W4A16_ERR_OVERLAP;
-        for (const Span& o2 : outs)
-            if (&o != &o2 && overlap(o.p, o.n, o2.p, o2.n)) return W4A16_ERR_OVERLAP;
-    }
+    const int64_t R = B * Hkv * Tmax, Ro = B * Hkv * Tout;
+    const CacheSpans<w4a16_kv_cache> from(*in, R, D, bits);
+    const CacheSpans<w4a16_kv_cache_out> to(*out, Ro, D, bits);
+    const Span ins[] = {{weights, 4 * R}, {lengths, 4 * B}};
+    const Span outs[] = {{weights_out, 4 * Ro}, {lengths_out, 4 * B}, {kept, 4 * B * Hkv * budget},
+                         {work, 4 * words}};
+    for (const Span& o : outs)
+        if (overlaps(o, ins) || overlaps(o, from.s) || overlaps(o, to.s) || overlaps(o, outs)) return W4A16_ERR_OVERLAP;
+    for (const Span& o : to.s)
+        if (overlaps(o, ins) || overlaps(o, from.s) || overlaps(o, to.s)) return W4A16_ERR_OVERLAP;
     w4a16::KvEvictArgs a = {};
     a.in = as_cache(*in);
     a.out = {out->kcodes, out->kscales, out->kzeros, out->vcodes, out->vscales, out->vzeros};

@@ -406,6 +406,12 @@ void gather(const KvEvictArgs& a, hipStream_t st) {
 // Tokens of a chunk: whole batches, at most kChunks chunks.
 static int chunk_tokens(long long Tmax) { return (int)((Tmax + (long long)kBatch * kChunks - 1) / (kBatch * kChunks)) * kBatch; }
 
+long long kv_evict_call_words(long long B, long long Hkv, long long Tmax) {
+    if (Tmax <= kBatch) return 0;
+    const int chunk = chunk_tokens(Tmax);
+    return B * Hkv * ((Tmax + chunk - 1) / chunk) * kChunkWords;
+}
+
 // What any call of at most B sequences and Tmax tokens uses: past kBatch kChunks tokens the chunks become
 // longer, and fewer than kChunks again.
 long long kv_evict_workspace_words(long long B, long long Hkv, long long Tmax) {

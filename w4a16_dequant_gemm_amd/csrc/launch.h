@@ -136,7 +136,8 @@ struct KvEvictArgs {
     int *lens_out, *kept;
     int bits, B, Hkv, D, Tmax, Tout, budget, recent;
 };
-long long kv_evict_workspace_words(long long B, long long Hkv, long long Tmax);   // 0: none needed
+long long kv_evict_call_words(long long B, long long Hkv, long long Tmax);        // what a call uses (0: none)
+long long kv_evict_workspace_words(long long B, long long Hkv, long long Tmax);   // ... any call of at most these
 hipError_t launch_kv_evict(const KvEvictArgs& a, uint32_t* work, hipStream_t st);
 
 // Prompt attention (attention.hip): B sequences packed along T tokens, their bounds cu [B + 1] on
