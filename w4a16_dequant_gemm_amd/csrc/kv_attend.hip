@@ -1068,8 +1068,7 @@ __global__ __launch_bounds__(kThreads) void kv_weights_kernel(const float2* __re
                                                               uint16_t* __restrict__ out, int heads, int Hq, int Hkv,
                                                               const int* __restrict__ lens, int Tmax, int spans,
                                                               const float* __restrict__ score, int spad,
-                                                              const float* __restrict__ weights,
-                                                              float* __restrict__ sums) {
+                                                              const float* weights, float* sums) {   // (may be one)
     __shared__ __attribute__((aligned(16))) float part[kThreads / (D / 4)][D];
     __shared__ float2 stat[kStatHeads];                    // a head's maximum and 1 / sum
     if (blockIdx.x < (unsigned)heads) {
