@@ -19,7 +19,7 @@
 // A code goes in as the exact fp16 value (c - z) 2^-9, and a token's scales stay out of the 16-bit
 // operands: K's multiplies the fp32 score, V's the softmax weight before it is rounded to fp16.
 // bf16 queries are scaled by a power of two (query_exponent) and become fp16 exactly (8-bit
-// significands; an entry far below its row's largest may lose bits that are below 2^-21 of that one).
+// significands; entries below 2^-21 of their row's largest may be off by 2^-29 of that one).
 // Rounded to 16 bits are only the weights p s_t (fp16, relative 2^-11, scaled so that the largest
 // s_t seen so far becomes 2^7 and small ones keep their bits) and the output.  Scores, maxima,
 // sums and outputs are fp32.
@@ -66,12 +66,13 @@ __device__ __forceinline__ void swap_halves(float& a, float& b) {
 
 // The power of two 2^e that a row of a bf16 query takes on its way to fp16, its largest entry being
 // mx, the largest of all rows top (0: nothing finite).  The common factor brings top into [2^14,
-// 2^15) and goes out of the scores with K's scales (cl); rows far below top, whose bits it would push
-// out of fp16, take a factor of their own, and their scores rowf.  Returns whether there are any.
+// 2^15) and goes out of the scores with K's scales (cl); rows below 2^-10 of top, whose bits it would
+// push out of fp16 (2^-21 of 2^4 has its last of 8 bits at fp16's last, 2^-24), take a factor of their own, and
+// their scores rowf.  Returns whether there are any.
 __device__ __forceinline__ float finite_or_zero(float x) { return x < __builtin_inff() ? x : 0.0f; }
 __device__ __forceinline__ bool query_exponent(float mx, float top, int& e, float& cl, float& rowf) {
     const int e0 = top > 0.0f ? 15 - __builtin_amdgcn_frexp_expf(top) : 0;
-    const bool mixed = __builtin_amdgcn_ballot_w64(mx > 0.0f && mx < top * 3.814697265625e-6f) != 0;   // 2^-18
+    const bool mixed = __builtin_amdgcn_ballot_w64(mx > 0.0f && mx < top * 9.765625e-4f) != 0;   // 2^-10
     e = mixed && mx > 0.0f ? 15 - __builtin_amdgcn_frexp_expf(mx) : e0;
     cl = ldexpf(cl, -e0);
     rowf = ldexpf(1.0f, e0 - e);
