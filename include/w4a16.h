@@ -402,8 +402,10 @@ int w4a16_kv_attention_decode_batch(const void* q, int dtype, int64_t B, int64_t
  *         the last sequence are not written, and q, k and v are not read there: a padded batch may
  *         hold anything in them.
  * Scores, softmax statistics and outputs are held in fp32; the softmax weights are rounded once to
- * dtype for the product with the values, and the output is rounded once.
- * A row depends on the tokens up to its own alone, whatever later ones hold (infinities, NaN).
+ * dtype for the product with the values (fp16: relative 2^-11 down to 2^-21 of a row's largest, below by
+ * 2^-32 of it), and the output is rounded once.
+ * A row depends on the tokens up to its own alone, whatever later ones hold (infinities, NaN).  An infinity
+ * or NaN among the values that it sees makes that element of it one or NaN; keys of score -inf weigh 0.
  * Limits: 1 <= B <= 2^20, 1 <= T <= 2^30, (T / 128 + B) * Hq < 2^24, Hq <= 65535.
  */
 int w4a16_attention_prompt(const void* q, const void* k, const void* v, int dtype, int64_t T, int64_t B,
@@ -453,8 +455,9 @@ int64_t w4a16_kv_attention_shared_workspace(int64_t B, int64_t Hq, int64_t Hkv, 
  *   work     w4a16_kv_attention_shared_workspace(...) fp32 elements, 16-byte aligned (scratch,
  *            contents undefined after the call; calls that overlap on one buffer race), or NULL when
  *            that is 0.
- * Scores, softmax statistics and sums are fp32; the codes less their zero points (|z| <= 2048) are
- * exact, the softmax weights times V's scales are rounded once to fp16 (relative 2^-11) for the
+ * Scores, softmax statistics and sums are fp32; the codes less their zero points are exact up to
+ * |z| = 2048 and rounded to fp16 beyond (relative 2^-11; w4a16_kv_attention_decode_batch holds them in
+ * fp32), the softmax weights times V's scales are rounded once to fp16 (relative 2^-11) for the
  * product with them, and the output is rounded once.  bf16 queries are scaled by a power of two
  * into fp16, exact but for entries below 2^-21 of the largest of their row.
  * Limits: B <= 65535, B * Hq < 2^22, Hkv * (Pmax + B * Tmax) <= 2^33.

@@ -598,7 +598,10 @@ def attention_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
     rows may be strided (column blocks of a fused projection).  Sequence ``b`` is the tokens
     ``cu_seqlens[b] .. cu_seqlens[b + 1] - 1`` (int32 ``[B + 1]`` on the device, not decreasing).
     Rows outside every sequence are neither read nor written: in an ``out`` of the caller's (which
-    must not overlap the inputs) they keep what they held, in the returned tensor of a call without ``out`` they are undefined."""
+    must not overlap the inputs) they keep what they held, in the returned tensor of a call without
+    ``out`` they are undefined.  Scores, softmax statistics and sums are fp32; the softmax weights are
+    rounded once to the inputs' type.  A row depends on the tokens up to its own alone, whatever later
+    ones hold; an infinity or NaN among the values that it sees makes that element of it one or NaN."""
     dt = _dtype_code(q)
     dtype, dev = q.dtype, q.get_device()
     strides = None
@@ -744,7 +747,11 @@ def kv_attention_decode_shared(q: torch.Tensor, kprefix, vprefix, P: int, kcache
     ``[B, Hkv, Tmax, ...]``.  The prefix is held once for the batch, and a long one read once.  A sequence without any
     token gets zeros.  ``out`` must not overlap the inputs.  ``work`` is an optional fp32 buffer of at least
     :func:`kv_attention_shared_workspace` elements (0 for short sequences); calls that may overlap
-    need one each."""
+    need one each.
+
+    Scores and sums are fp32.  The softmax weights, with V's scales, are rounded once to fp16 (relative
+    2^-11), and so is ``c - z`` of 4-bit codes whose zero point is beyond 2048 (rows of nearly equal
+    values far from 0); :func:`kv_attention_decode_batch` rounds neither."""
     dt = _dtype_code(q)
     _need(q, "q", q.dtype, 3)
     _need(lengths, "lengths", torch.int32, 1)
@@ -779,7 +786,8 @@ def kv_attention_decode_weights(q: torch.Tensor, kcache, vcache, lengths: torch.
     ``weights``, which is then updated in place; ``weights=None`` starts from 0 (``sums`` defaults to
     a zero tensor then).  A sequence of length 0 gets zeros.  ``out`` and ``sums`` must not overlap the
     other inputs or each other.  ``work`` is an optional fp32 buffer of at
-    least :func:`kv_attention_weights_workspace` elements (0 for short sequences)."""
+    least :func:`kv_attention_weights_workspace` elements (0 for short sequences).  Rounding as in
+    :func:`kv_attention_decode_shared`; the weights that are added up are fp32 throughout."""
     dt = _dtype_code(q)
     _need(q, "q", q.dtype, 3)
     _need(lengths, "lengths", torch.int32, 1)
