@@ -438,6 +438,11 @@ typedef struct {
 int64_t w4a16_kv_attention_shared_workspace(int64_t B, int64_t Hq, int64_t Hkv, int64_t P, int64_t Tmax,
                                             int64_t D);
 
+/* What a call of exactly these sizes uses, at most the above (0 for some more calls, whose smaller ones
+ * use some): for a buffer that is made for one call. */
+int64_t w4a16_kv_attention_shared_call_workspace(int64_t B, int64_t Hq, int64_t Hkv, int64_t P, int64_t Tmax,
+                                                 int64_t D);
+
 /*
  * w4a16_kv_attention_decode_shared -- decode attention for a batch of B sequences that begin with
  * the same P tokens (a system prompt, a document): out[b][h] = softmax(q[b][h] . K / sqrt(D)) V over
@@ -454,7 +459,7 @@ int64_t w4a16_kv_attention_shared_workspace(int64_t B, int64_t Hq, int64_t Hkv, 
  *            alone (up to the rounding of their weights).
  *   work     w4a16_kv_attention_shared_workspace(...) fp32 elements, 16-byte aligned (scratch,
  *            contents undefined after the call; calls that overlap on one buffer race), or NULL when
- *            that is 0.
+ *            the call uses none.
  * Scores, softmax statistics and sums are fp32; the codes less their zero points are exact up to
  * |z| = 2048 and rounded to fp16 beyond (relative 2^-11; w4a16_kv_attention_decode_batch holds them in
  * fp32), the softmax weights times V's scales are rounded once to fp16 (relative 2^-11) for the

@@ -64,6 +64,23 @@ def test_sizes_grow_with_every_dimension(lib, Hq, Hkv, D):
         assert big >= small >= 0, f"evict {(B, T2)}: {big}, {(b, t2)}: {small}"
 
 
+def test_a_call_uses_at_most_what_its_size_says(lib):
+    """Also within the sizes that need none: the call's own use, over all smaller calls."""
+    rng = random.Random(2)
+    zero = 0
+    for Hq, Hkv, D in HEADS:
+        for _ in range(10000):
+            B, P, T = _log(rng, 1, 512), rng.choice([0, _log(rng, 1, 1 << 15)]), _log(rng, 1, 1 << 12)
+            b, p, t = rng.randint(1, B), rng.randint(0, P), rng.randint(1, T)
+            size = lib.w4a16_kv_attention_shared_workspace(B, Hq, Hkv, P, T, D)
+            for s in ((B, P, T), (b, p, t)):
+                use = lib.w4a16_kv_attention_shared_call_workspace(s[0], Hq, Hkv, s[1], s[2], D)
+                assert 0 <= use <= size, f"{(B, P, T)}: {size}, {s} uses {use}"
+                zero += use == 0 and size > 0
+    assert zero > 0
+    assert lib.w4a16_kv_attention_shared_call_workspace(2, 8, 3, 10, 8, 64) == L.ERR_SHAPE
+
+
 def test_short_sequences_need_none_at_any_smaller_size(lib):
     """Where the size is 0 no buffer is passed at all: no smaller call may want one."""
     rng = random.Random(1)

@@ -766,9 +766,9 @@ def kv_attention_decode_shared(q: torch.Tensor, kprefix, vprefix, P: int, kcache
         raise ValueError("P must be in [0, Pmax]")
     L = lib()
     out = _decode_out(out, q)
-    need = L.w4a16_kv_attention_shared_workspace(B, Hq, Hkv, P, Tmax, D)
+    need = L.w4a16_kv_attention_shared_call_workspace(B, Hq, Hkv, P, Tmax, D)
     if need or work is not None:
-        work = _work(work, need, "w4a16_kv_attention_shared_workspace", q)
+        work = _work(work, need, "w4a16_kv_attention_shared_call_workspace", q)
     _call(L.w4a16_kv_attention_decode_shared, "w4a16_kv_attention_decode_shared", q.device, q.data_ptr(), dt, B, Hq,
           Hkv, D, bits, _cache_struct(kprefix, vprefix, bits), P, Pmax, _cache_struct(kcache, vcache, bits),
           lengths.data_ptr(), Tmax, None if work is None else work.data_ptr(), out.data_ptr())

@@ -120,8 +120,9 @@ def lib() -> ctypes.CDLL:
     L.w4a16_attention_prompt.restype = i32
     L.w4a16_attention_prompt.argtypes = [vp, vp, vp, i32, i64, i64, vp, i64, i64, i64, i64, i64, i64, vp, vp]
     cache = ctypes.POINTER(KvCache)
-    L.w4a16_kv_attention_shared_workspace.restype = i64
-    L.w4a16_kv_attention_shared_workspace.argtypes = [i64, i64, i64, i64, i64, i64]
+    for f in (L.w4a16_kv_attention_shared_workspace, L.w4a16_kv_attention_shared_call_workspace):
+        f.restype = i64
+        f.argtypes = [i64, i64, i64, i64, i64, i64]
     L.w4a16_kv_attention_decode_shared.restype = i32
     L.w4a16_kv_attention_decode_shared.argtypes = [vp, i32, i64, i64, i64, i64, i32, cache, i64, i64, cache, vp, i64,
                                                    vp, vp, vp]

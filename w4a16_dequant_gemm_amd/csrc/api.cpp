@@ -494,6 +494,12 @@ int64_t w4a16_kv_attention_shared_workspace(int64_t B, int64_t Hq, int64_t Hkv, 
     return w4a16::kv_shared_workspace_floats(B, Hq, Hkv, P, Tmax, D);
 }
 
+int64_t w4a16_kv_attention_shared_call_workspace(int64_t B, int64_t Hq, int64_t Hkv, int64_t P, int64_t Tmax,
+                                                 int64_t D) {
+    const int st = check_kv_batch(B, Hq, Hkv, P, P, Tmax, D);
+    return st != W4A16_OK ? st : w4a16::kv_shared_call_floats(B, Hq, Hkv, P, Tmax, D);
+}
+
 int w4a16_kv_attention_decode_shared(const void* q, int dtype, int64_t B, int64_t Hq, int64_t Hkv, int64_t D,
                                      int bits, const w4a16_kv_cache* prefix, int64_t P, int64_t Pmax,
                                      const w4a16_kv_cache* own, const int32_t* lengths, int64_t Tmax, float* work,
