@@ -18,7 +18,8 @@
 // besides the output's: relative 2^-11 / 2^-8 per weight, like the values themselves.  fp16 weights
 // are held times 2^7 (kRaise), so that this holds down to 2^-21 of the largest and smaller ones are off by
 // 2^-32 of it at most: taken as they are, weights below 2^-14 would lose bits and those below 2^-25
-// vanish, which long prompts add up (one token of most of the weight and 16384 of 2^-25: 0.35 %).
+// vanish, which rows add up (one token of most of the weight beside 300 or 16384 of 2^-22 .. 2^-28: 2.3 and 1.6
+// times what the rounding may cost).
 // Scores, maxima, sums and outputs stay in fp32, and l sums the unrounded weights.
 //
 // Measured (32 heads, D = 128): one sequence of 16384 tokens, bf16, grouped heads: 1.96 ms, 1.12 PFLOP/s
@@ -28,7 +29,13 @@
 // with the second product and stores of the output through LDS changed nothing.  12 packed prompts of
 // up to 1024 tokens, fp16: 40 us (a block costs 5 us besides 1.9 a tile of keys); 6 of up to 96: 6.6 us, latency.
 // One prompt of 128 / 512 / 1024 / 2048 / 4096 tokens: 8.8 / 16 / 24 / 51 / 154 us.  Before the loads went
-// straight to LDS and the scores of the next tile under the weights of this one: 2313 and 49 us.
+// straight to LDS and the scores of the next tile under the weights of this one: 2313 and 49 us.  At D = 128 the
+// kernel fills the registers and spills 14 vector ones, outside the loop over the tiles.
+//
+// Values that are no numbers: the matrix cores multiply a hidden key's value with its weight of 0, so an
+// infinity or NaN among a row's later tokens of its last tile makes NaN of it.  Such rows are told by their
+// outputs and computed again (rows_again).  Looking through the last tile first and keeping such values out
+// of its product cost every call (12 packed prompts 39 -> 46 us, one of 1024 tokens 24 -> 31).
 #include "attn.h"
 #include "launch.h"
 

@@ -118,8 +118,10 @@ __device__ __forceinline__ float wave_max(float v) {
 // output to po at index head * nsplit + split.
 // The waves stand along the rows, or (WQ = 2, WK = 2: up to 64 rows) in pairs along the rows and the
 // tokens, each pair's two softmax states joined at the end.  Codes are loaded one tile ahead into
-// registers, 16 bytes a lane, and stored as fp16 into LDS whose 16-byte pieces are permuted so
-// that neither product's reads meet in a bank; with two buffers (WK = 1) a tile costs one barrier.
+// registers, 16 bytes a lane, and stored as fp16 into LDS whose 16-byte pieces are permuted to spread
+// both products' reads over the banks (the counters still show 0.8 conflict cycles an LDS instruction with
+// 4-bit codes and 0.6 with 8-bit ones, not traced to an access); with two buffers (WK = 1) a tile costs one
+// barrier.
 // Bound by instructions rather than by its bytes: per code three or four operations to make it fp16
 // (per block, so 128 rows share them), per score a scale, an exponential, a sum, another scale and a
 // rounding.  128 sequences behind 32768 KV4 tokens, 32 heads on 8, D = 128 (70 GFLOP; with own caches of up
@@ -1148,7 +1150,8 @@ int own_chunk(long long B, long long Hq, long long Hkv, long long T) {
 //   8 rows, 4096 / 32768 tokens, 100 own ones           16.8 / 16.9 / 17.2, 25.9 / 26.5 / 32.2
 //   20, 64 rows, 32768 tokens                           33.8 / 26.6 / 33.3, 40.0 / 31.2 / 37.2
 //   128, 256 rows, 32768 tokens                         61.0 / 40.4 / 41.2, 98.1 / 65.1 / 61.1
-// (128 rows of bf16, 4096 tokens and up to 512 own ones: 24.4 / 23.0 / 21.0, so those take 4).
+// (128 rows of bf16, 4096 tokens and up to 512 own ones: 24.4 / 23.0 / 21.0, so those take 4; of fp16 with
+// hardly any own ones 64-row blocks were 19.6 against 22.2: type and own length were not varied apart).
 int prefix_wq(long long R, long long P, long long Tmax) { return R <= 16 || 4 * P <= Tmax ? 0 : R <= 64 ? 2 : 4; }
 int prefix_chunk(long long B, long long Hq, long long Hkv, long long P, long long Tmax) {
     if (P == 0) return kMinChunk;
