@@ -523,6 +523,110 @@ int w4a16_kv_evict(const w4a16_kv_cache* in, const float* weights, const int32_t
                    int64_t Tmax, int64_t D, int bits, int64_t budget, int64_t recent, const w4a16_kv_cache_out* out,
                    int64_t Tout, float* weights_out, int32_t* lengths_out, int32_t* kept, float* work, void* stream);
 
+/* ------------------------------------------------------------------------------------
+ * Paged 8-bit KV cache: caches whose tokens lie in pages of a pool that all sequences share, so that a
+ * sequence takes memory as it grows and equal beginnings are held once.  One scale for each page and kv
+ * head (KV8 above: one for each token).  Rotary positions are applied on the way into it.
+ *
+ * A pool holds `pages` pages of `page` tokens (16, 32, 64 or 128).  Of page i and kv head h
+ *   kcodes  [pages, Hkv, page, D]  8-bit codes, a token's row after the other;
+ *   vcodes  [pages, Hkv, D, page]  across: a dimension's tokens after one another;
+ *   kscales, vscales  [pages, Hkv] fp32; a code c stands for scale * c.
+ * format: W4A16_KV_INT8 (whole numbers -127 .. 127) or W4A16_KV_E4M3 (8-bit floats with 4 exponent and 3
+ * mantissa bits, largest 448).  D is 64 or 128.  Codes 16-byte aligned, everything else 4-byte.
+ *
+ * The sequences of a call, on the device:
+ *   table    int32 [B, table_pages]: entry j of a sequence is the page that holds its tokens j * page and on.
+ *            An entry that is not one of 0 .. pages - 1 is no page: tokens there are not written, read as zeros
+ *            and are not attended to.  Entries may repeat (a shared beginning), but a page that a call appends
+ *            to belongs to one sequence, else its codes are unspecified.
+ *   lengths  int32 [B]: each sequence's tokens, the call's own among them; clamped into
+ *            [0, table_pages * page] (appending and reading: tokens behind the table have no page).
+ *   cu_seqlens  int32 [B + 1], not decreasing: the call is about the last cu_seqlens[b + 1] - cu_seqlens[b]
+ *            tokens of sequence b (possibly none), which are the rows cu_seqlens[b] and on of its T packed ones.
+ *            Values are clamped into [0, T] on the device; decreasing ones leave outputs unspecified, never an
+ *            access outside the tensors.  NULL: one token each, T == B.  Rows of no sequence are
+ *            neither read nor written.  Where a sequence has more rows than tokens, its first rows have no
+ *            place: they are not written, read as zeros and see nothing.
+ * Limits: 1 <= B <= 65535, 1 <= T <= 2^24, 1 <= Hkv <= 65535, 1 <= pages < 2^31,
+ * table_pages * page <= 2^24, (T / page + 2 B) * Hkv + T < 2^23.
+ */
+#define W4A16_KV_INT8 0
+#define W4A16_KV_E4M3 1
+
+typedef struct {
+    void* kcodes;
+    float* kscales;
+    void* vcodes;
+    float* vscales;
+    const int32_t *table, *lengths, *cu_seqlens;
+    int64_t pages, page, table_pages, B, T, Hkv, D;
+    int format;
+} w4a16_kv_paged;
+
+/*
+ * w4a16_rope -- rotation of heads by their tokens' positions: of each head x the pairs
+ *   (x[i], x[i + R / 2]) or, interleaved, (x[2 i], x[2 i + 1]),   i < R / 2,
+ * become mscale * (x0 cos a - x1 sin a, x1 cos a + x0 sin a), a = 2 pi positions[t] freqs[i] / 2^64; the values
+ * behind the first R pass through.  The gradient of x is the same call on that of out with -positions.
+ *   x     [T, H, D] fp16/bf16, heads adjacent, rows x_stride elements apart (>= H * D, <= 2^24).
+ *   out   likewise with out_stride; x itself (and its stride) for a rotation in place, else apart from the inputs.
+ *   positions  int32 [T], any values; freqs int64 [R / 2]: the turns per position in units of 2^-64 (as unsigned
+ *         numbers: turns modulo 1), so that angles are exact however far the position.
+ * Rotated in fp32 and rounded once.  D and R even, 2 <= R <= D <= 512; 1 <= T <= 2^24, 1 <= H <= 65535.
+ * Pointers of 2-byte alignment do (4 and 8 for positions and freqs); rotations are widest with x, out and strides multiples of
+ * 16 bytes, D of 8 and R of 16.
+ */
+int w4a16_rope(const void* x, int dtype, int64_t T, int64_t H, int64_t D, int64_t x_stride, const int32_t* positions,
+               const int64_t* freqs, int64_t R, int interleaved, float mscale, void* out, int64_t out_stride, void* stream);
+
+/*
+ * w4a16_kv_append_paged -- the call's tokens into the pages, keys rotated on the way (R > 0) as w4a16_rope does
+ * (in fp32 and not rounded between).  A page's scale is the largest of max|x| / top (127 or 448) over the tokens written
+ * to it since its first slot was: a call that writes the first slot starts it anew; where later tokens
+ * need a larger one the earlier codes c become the nearest to c * old / new.  Codes are the nearest to x / scale, ties to even.
+ * (A code is off by half a step when written and by half a step of the new scale each time that it is
+ * rounded again.)  Infinities take the largest code and NaN 0; neither counts for the scale.
+ *   k, v  [T, Hkv, D] fp16/bf16 (dtype), heads adjacent, rows k_stride / v_stride elements apart.
+ *   positions  int32 [T], or NULL: every token's place in its sequence.
+ *   q, q_out  [T, Hq, D] (rows q_stride apart; q_out dense), the queries of the same tokens, rotated likewise and
+ *         rounded once, in the same launch; NULL: none.
+ * 16-byte aligned, strides multiples of 8, at least a row and at most 2^24.  R = 0 (freqs NULL): no rotation.
+ * Outputs (the pool, q_out) must be apart from the inputs and one another.
+ */
+int w4a16_kv_append_paged(const w4a16_kv_paged* cache, const void* k, const void* v, int dtype, int64_t k_stride,
+                          int64_t v_stride, const int32_t* positions, const int64_t* freqs, int64_t R, int interleaved,
+                          float mscale, const void* q, int64_t Hq, int64_t q_stride, void* q_out, void* stream);
+
+/*
+ * w4a16_kv_read_paged -- the call's tokens as 16-bit rows: k_out, v_out [T, Hkv, D] dense, 16-byte aligned,
+ * scale * code rounded once to dtype.  Both must be apart from the pool and the other inputs.
+ */
+int w4a16_kv_read_paged(const w4a16_kv_paged* cache, int dtype, void* k_out, void* v_out, void* stream);
+
+/* fp32 elements of workspace that hold every w4a16_kv_attention_paged call of these heads whose table has at most
+ * table_pages * page == tokens of room (host only; 0: none, for short tables), or a negative status.  It does not
+ * depend on the number of sequences or rows. */
+int64_t w4a16_kv_attention_paged_workspace(int64_t Hq, int64_t Hkv, int64_t D, int64_t tokens);
+
+/*
+ * w4a16_kv_attention_paged -- causal attention of the call's tokens (whose own keys and values are in the
+ * pages already) over their sequences: a decode step (cu_seqlens NULL) or chunks of prompts.
+ *   out[i][h] = sum_{j <= place of i} p_j v_j,  p = softmax_j(q[i][h] . k[j][h / (Hq / Hkv)] / sqrt(D)).
+ *   q     [T, Hq, D] fp16/bf16, 16-byte aligned, heads adjacent, rows q_stride elements apart (a multiple of 8).
+ *   out   [T, Hq, D] dense, 16-byte aligned.  A row that sees no token (no place, no page) is zeros; one whose query is no
+ *         number is NaN and leaves the others alone.
+ *   work  w4a16_kv_attention_paged_workspace(...) fp32 elements, 16-byte aligned (scratch, contents undefined after
+ *         the call; calls that overlap on one buffer race), or NULL when that is 0.
+ * Codes enter the products exactly; the softmax weights times V's scales are rounded once to fp16 (relative
+ * 2^-11 down to 2^-29 of the row's largest, below by 2^-40 of it); scores, softmax statistics and sums are fp32, the output is rounded once.
+ * The codes of a sequence's tokens have to be numbers (what w4a16_kv_append_paged writes is); behind them anything may lie.
+ * out and work must be apart from the inputs and each other (W4A16_ERR_OVERLAP).
+ * Limits besides the above: Hq <= 65535, (T * Hq / Hkv / 16 + B + 1024) * Hkv < 2^23.
+ */
+int w4a16_kv_attention_paged(const w4a16_kv_paged* cache, const void* q, int dtype, int64_t Hq, int64_t q_stride,
+                             float* work, void* out, void* stream);
+
 /*
  * w4a16_linear_workspace -- bytes of fp32 workspace that w4a16_linear_ws can use for this
  * problem (0: it would not split K and behaves as w4a16_linear); a negative status for invalid

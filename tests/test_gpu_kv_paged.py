@@ -1,0 +1,464 @@
+"""The paged 8-bit cache: appending (bit for bit against the same fp32 steps on the host), rotation on the way,
+reading back, attention of decode steps and chunks against fp64; pages that are none, empty sequences,
+stale codes that are no numbers, strides, and the loop that a server runs."""
+
+import numpy as np
+import pytest
+import torch
+
+import w4a16_dequant_gemm_amd as W4
+from tests.paged_util import CODES, HostCache, Pool, TOP, check_attention, check_rotated, f64, rotate
+
+pytestmark = pytest.mark.gpu
+NAMES = {torch.int8: "int8", torch.float8_e4m3fn: "e4m3"}
+ids = lambda v: NAMES.get(v, None)
+
+
+def starts(counts):
+    return torch.tensor(np.concatenate([[0], np.cumsum(counts)]), dtype=torch.int32).cuda()
+
+
+def fused(T, heads, D, dtype, seed, scale=1.0):
+    """Column blocks of one wide tensor, as a fused projection leaves them."""
+    x = (torch.randn((T, sum(heads) * D), generator=torch.Generator().manual_seed(seed)) * scale).to(dtype).cuda()
+    return [t.unflatten(1, (h, D)) for t, h in zip(x.split([h * D for h in heads], 1), heads)]
+
+
+# --------------------------------------------------------------------------- append and read
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("codes", CODES, ids=ids)
+@pytest.mark.parametrize("page,D", [(16, 64), (32, 128), (64, 128), (128, 64)])
+def test_append_steps_and_chunks(page, D, codes, dtype):
+    """Several calls in a row on ragged sequences: codes and scales of K (not rotated) and V bit for bit."""
+    Hkv, B, room = 3, 4, 5 * page
+    P = room // page
+    kp, vp = W4.kv_pages(B * P + 2, Hkv, page, D, codes)
+    kp[0].view(torch.uint8).fill_(0x7F)                    # (a pool of torch.empty may hold anything)
+    vp[0].view(torch.uint8).fill_(0x7F)
+    kp[1].fill_(float("nan"))
+    vp[1].fill_(float("nan"))
+    table = torch.randperm(B * P + 2, generator=torch.Generator().manual_seed(1))[:B * P].view(B, P).to(torch.int32)
+    host = [[[HostCache(page, codes) for _ in range(Hkv)] for _ in range(B)] for _ in range(2)]
+    length = [0] * B
+    plan = [[5, 0, page + 3, 1], "step", "step", [1, 2 * page, 0, 2], "step", [page, 1, page - 1, 2 * page + 1], "step"]
+    for i, counts in enumerate(plan):
+        n = [1] * B if counts == "step" else counts
+        k, v = fused(sum(n), [Hkv, Hkv], D, dtype, 10 * i + page, 1.0 + i)
+        length = [a + b for a, b in zip(length, n)]
+        W4.kv_append_paged(k, v, kp, vp, table.cuda(), torch.tensor(length, dtype=torch.int32).cuda(),
+                           None if counts == "step" else starts(n))
+        at = 0
+        for b in range(B):
+            for h in range(Hkv):
+                for x, c in ((k, host[0]), (v, host[1])):
+                    c[b][h].write(x[at:at + n[b], h].float().cpu().numpy(), length[b] - n[b])
+            at += n[b]
+    for (c, s), cache, axis in ((kp, host[0], 0), (vp, host[1], 1)):
+        c, s = f64(c.cpu().float()), s.cpu().numpy()
+        for b in range(B):
+            for h in range(Hkv):
+                for i, (want, scale) in enumerate(cache[b][h].pages):
+                    if len(want):
+                        got = c[table[b, i], h] if axis == 0 else c[table[b, i], h].T
+                        assert s[table[b, i], h] == scale
+                        assert np.array_equal(got[:len(want)], want), (b, h, i)
+    # pages of no sequence are as they were
+    spare = sorted(set(range(B * P + 2)) - set(table.flatten().tolist()))
+    assert (kp[0].view(torch.uint8)[spare] == 0x7F).all() and torch.isnan(vp[1][spare]).all()
+    # and what reading gives is those codes times scales, rounded once
+    lens = torch.tensor(length, dtype=torch.int32).cuda()
+    for back in (length, [min(n, page + 5) for n in length], [1] * B):
+        ko, vo = W4.kv_read_paged(kp, vp, table.cuda(), lens, starts(back), T=sum(back), dtype=dtype)
+        at = 0
+        for b in range(B):
+            for out, cache in ((ko, host[0]), (vo, host[1])):
+                for h in range(Hkv):
+                    rows = np.concatenate([c.astype(np.float32) * s for c, s in cache[b][h].pages if len(c)])
+                    want = torch.from_numpy(rows[length[b] - back[b]:length[b]]).to(dtype)
+                    assert torch.equal(out[at:at + back[b], h].cpu(), want)
+            at += back[b]
+
+
+def grid_check(got, ref, size, scale, codes):
+    """Values off a rotated row by half a step of the code at most (fp32 errors besides)."""
+    half = 0.5 * scale if codes == torch.int8 else np.maximum(np.abs(ref) * 2.0 ** -4, scale * 2.0 ** -10)
+    assert (np.abs(got - ref) <= half * (1 + 2.0 ** -20) + 16 * 2.0 ** -24 * (size + np.abs(ref)) + 2.0 ** -22 * scale * TOP[codes]).all()
+
+
+@pytest.mark.parametrize("codes", CODES, ids=ids)
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("D,R,page", [(64, 64, 16), (128, 128, 64), (128, 64, 32), (128, 34, 128), (64, 2, 16), (128, 126, 32)])
+@pytest.mark.parametrize("explicit", [False, True])
+def test_append_rotates(D, R, page, interleaved, codes, explicit):
+    dtype, Hq, Hkv, n = torch.bfloat16, 6, 2, [page + 7, 1, 0, 3]
+    before = [page // 2 + 1, 40, 7, 0]
+    B, T = 4, sum(n)
+    length = [a + b for a, b in zip(before, n)]
+    P = max(-(-t // page) for t in length)
+    kp, vp = W4.kv_pages(B * P, Hkv, page, D, codes)
+    table = torch.arange(B * P, dtype=torch.int32).view(B, P).cuda()
+    q, k, v = fused(T, [Hq, Hkv, Hkv], D, dtype, D + R)
+    freqs, _ = W4.rope_frequencies(R, 10000.0)
+    words = [int(w) % 2 ** 64 for w in freqs.cpu().tolist()]
+    seq = np.repeat(np.arange(B), n)
+    place = np.concatenate([np.arange(b, a) for a, b in zip(length, before)]).astype(np.int64)
+    pos = np.arange(T) * 1000 - 7000 if explicit else place
+    lens = torch.tensor(length, dtype=torch.int32).cuda()
+    qo = W4.kv_append_paged(k, v, kp, vp, table, lens, starts(n), freqs=freqs, interleaved=interleaved, mscale=0.75, q=q,
+                            positions=torch.from_numpy(pos).to(torch.int32).cuda() if explicit else None)
+    ref, size = rotate(f64(q), pos, words, R, interleaved, 0.75)
+    check_rotated(f64(qo), ref, size, dtype)
+    ref, size = rotate(f64(k), pos, words, R, interleaved, 0.75)
+    c, s = f64(kp[0].cpu().float()), f64(kp[1])
+    for b in range(B):
+        for i in range(P):
+            mine = (seq == b) & (place // page == i)
+            if not mine.any():
+                continue
+            page_id = int(table[b, i])
+            got = c[page_id][:, place[mine] % page].swapaxes(0, 1)
+            # (earlier slots of these pages hold nothing: the scale is the new rows' own, but for the old one's 0)
+            want = np.abs(ref[mine]).max((0, 2)) / TOP[codes]
+            assert np.allclose(s[page_id], want, rtol=2.0 ** -19, atol=0)
+            sc = s[page_id][None, :, None]
+            grid_check(got * sc, ref[mine], size[mine], sc, codes)
+
+
+def test_append_without_positions_is_a_step():
+    """cu_seqlens of one token each, and None, are the same call."""
+    D, Hq, Hkv, page, B = 128, 8, 2, 16, 5
+    q, k, v = fused(B, [Hq, Hkv, Hkv], D, torch.float16, 3)
+    table = torch.arange(2 * B, dtype=torch.int32).view(B, 2).cuda()
+    lens = torch.tensor([1, 16, 17, 32, 0], dtype=torch.int32).cuda()
+    freqs, m = W4.rope_frequencies(D)
+    got = []
+    for cu in (None, starts([1] * B)):
+        kp, vp = W4.kv_pages(2 * B, Hkv, page, D)
+        qo = W4.kv_append_paged(k, v, kp, vp, table, lens, cu, freqs=freqs, q=q)
+        got.append((*kp, *vp, qo))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    assert (got[0][1][-2:] == 0).all()              # (the sequence of length 0 takes none)
+
+
+def test_append_outside_the_table():
+    """Tokens behind the table, at entries that are no pages and without a place are not written; rows of no
+    sequence leave q_out as it was."""
+    D, Hkv, page = 64, 2, 16
+    n = [20, 20, 20, 6]
+    T = sum(n) + 7
+    q, k, v = fused(T, [4, Hkv, Hkv], D, torch.float16, 4)
+    kp, vp = W4.kv_pages(8, Hkv, page, D)
+    kp[0].fill_(-128), vp[0].fill_(-128), kp[1].fill_(5.0), vp[1].fill_(5.0)
+    table = torch.tensor([[0, -1], [1, 8], [2 ** 31 - 1, 3], [4, 5]], dtype=torch.int32)
+    lens = [36, 20, 20, 4]                          # the first overruns its table, the last has two rows too many
+    cu = torch.tensor([3, 23, 43, 63, 69], dtype=torch.int32).cuda()
+    qo = torch.full((T, 4, D), 9.0, dtype=torch.float16, device="cuda")
+    freqs, _ = W4.rope_frequencies(D)
+    W4.kv_append_paged(k, v, kp, vp, table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(), cu, freqs=freqs, q=q, q_out=qo)
+    written = torch.zeros((8, page), dtype=torch.bool)
+    written[1, :] = True                            # tokens 0 .. 15 of the second sequence; its entry 8 is none
+    written[3, :4] = True
+    written[4, :4] = True
+    assert torch.equal((kp[0].cpu() != -128).any(-1).all(1), written)
+    assert torch.equal((vp[0].cpu() != -128).any(2).all(1), written)
+    assert torch.equal((kp[1].cpu() != 5.0).all(1), written.any(1)) and torch.equal((vp[1].cpu() != 5.0).all(1), written.any(1))
+    assert (qo[:3] == 9).all() and (qo[69:] == 9).all() and (qo[3:69] != 9).any(-1).all()
+    # reading: zeros where there is no page, rows of no sequence untouched
+    ko, vo = (torch.full((T, Hkv, D), 9.0, dtype=torch.float16, device="cuda") for _ in range(2))
+    W4.kv_read_paged(kp, vp, table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(), cu, out=(ko, vo))
+    for out in (ko, vo):
+        zero = (out == 0).all(-1).all(-1).cpu()
+        assert (out[:3] == 9).all() and (out[69:] == 9).all()
+        assert zero[3:23].all() and not zero[23:39].any() and zero[39:43].all()
+        assert zero[43:59].all() and not zero[59:63].any() and zero[63:65].all() and not zero[65:69].any()
+
+
+@pytest.mark.parametrize("codes", CODES, ids=ids)
+def test_append_values_that_are_no_numbers(codes):
+    D, page, nan, inf = 64, 16, float("nan"), float("inf")
+    k, v = fused(5, [1, 1], D, torch.float16, 5)
+    k, v = k.clone(), v.clone()
+    k[2, 0, :4] = v[2, 0, :4] = torch.tensor([nan, inf, -inf, 0.5])
+    kp, vp = W4.kv_pages(2, 1, page, D, codes)
+    table = torch.tensor([[1]], dtype=torch.int32).cuda()
+    W4.kv_append_paged(k, v, kp, vp, table, torch.tensor([5], dtype=torch.int32).cuda(), starts([5]))
+    for x, (c, s), axis in ((k, kp, 0), (v, vp, 1)):
+        host = HostCache(page, codes)
+        host.write(x[:, 0].float().cpu().numpy(), 0)
+        got = f64(c.cpu().float())[1, 0]
+        got = got if axis == 0 else got.T
+        assert float(s[1, 0]) == host.pages[0][1] and np.array_equal(got[:5], host.pages[0][0])
+        assert got[2, 0] == 0 and got[2, 1] == TOP[codes] and got[2, 2] == -TOP[codes]
+
+
+def test_append_zeros_and_subnormals():
+    D, page = 64, 16
+    kp, vp = W4.kv_pages(1, 1, page, D)
+    table = torch.zeros((1, 1), dtype=torch.int32).cuda()
+    z = torch.zeros((2, 1, D), dtype=torch.bfloat16, device="cuda")
+    W4.kv_append_paged(z, z, kp, vp, table, torch.tensor([2], dtype=torch.int32).cuda(), starts([2]))
+    assert (kp[1] == 0).all() and (kp[0][0, 0, :2] == 0).all() and (vp[0][0, 0, :, :2] == 0).all()
+    z[:] = 2.0 ** -130
+    W4.kv_append_paged(z[:1], z[:1], kp, vp, table, torch.tensor([3], dtype=torch.int32).cuda())
+    host = HostCache(page, torch.int8)
+    host.write(np.full((1, D), 2.0 ** -130, np.float32), 0)
+    assert float(kp[1]) == host.pages[0][1] and (kp[0][0, 0, 2].cpu().numpy() == host.pages[0][0][0]).all()
+    z[:] = 1.0
+    W4.kv_append_paged(z[:1], z[:1], kp, vp, table, torch.tensor([4], dtype=torch.int32).cuda())
+    assert (kp[0][0, 0, 3] == 127).all() and (kp[0][0, 0, :3] == 0).all() and (vp[0][0, 0, :, 3] == 127).all()
+
+
+# --------------------------------------------------------------------------- attention
+
+def attend(lengths, n, Hq, Hkv, D, page, codes, dtype, seed, decode=False, scale=1.0, qscale=1.0, change=None, room=0):
+    pool = Pool(lengths, Hkv, D, page, codes, seed, scale, room)
+    if change:
+        change(pool)
+    T = sum(n)
+    q, _ = fused(T, [Hq, 1], D, dtype, seed + 1, qscale)
+    out = torch.full((T, Hq, D), 9.0, dtype=dtype, device="cuda")
+    kp, vp, table, lens = pool.cuda()
+    got = W4.kv_attention_paged(q, kp, vp, table, lens, None if decode else starts(n), out=out)
+    assert got is out
+    at = 0
+    for b in range(len(lengths)):
+        check_attention(f64(out[at:at + n[b]]), f64(q[at:at + n[b]]), pool, b, n[b], Hq, dtype)
+        at += n[b]
+    return out
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("codes", CODES, ids=ids)
+@pytest.mark.parametrize("Hq,Hkv,D,page", [(8, 2, 64, 16), (4, 4, 128, 32), (6, 1, 128, 64), (32, 1, 64, 128),
+                                           (17, 1, 128, 16), (3, 3, 64, 64)])
+def test_decode(Hq, Hkv, D, page, codes, dtype):
+    lengths = [1, 0, 63, 64, 65, 2, 130, 700, 16, 17]
+    attend(lengths, [1] * len(lengths), Hq, Hkv, D, page, codes, dtype, D + page, decode=True)
+
+
+@pytest.mark.parametrize("codes", CODES, ids=ids)
+@pytest.mark.parametrize("Hq,Hkv,D,page", [(8, 2, 128, 64), (2, 2, 64, 16)])
+def test_decode_long(Hq, Hkv, D, page, codes):
+    """Sequences that are split over blocks, next to short and empty ones."""
+    attend([5000, 3, 0, 1025, 20000], [1] * 5, Hq, Hkv, D, page, codes, torch.float16, 7, decode=True, qscale=1.5)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("codes", CODES, ids=ids)
+@pytest.mark.parametrize("Hq,Hkv,D,page", [(4, 1, 128, 64), (2, 2, 64, 16), (3, 1, 128, 32), (5, 1, 64, 128)])
+def test_chunks(Hq, Hkv, D, page, codes, dtype):
+    """Chunks behind cached tokens, whole prompts, empty ones, single tokens and more rows than tokens."""
+    lengths, n = [150, 77, 5, 40, 300, 3, 129], [33, 77, 0, 1, 130, 5, 64]
+    attend(lengths, n, Hq, Hkv, D, page, codes, dtype, D + page)
+
+
+@pytest.mark.parametrize("codes", CODES, ids=ids)
+def test_chunks_long(codes):
+    attend([2500, 40, 1200], [20, 40, 3], 4, 2, 128, 64, codes, torch.bfloat16, 11)
+
+
+@pytest.mark.parametrize("codes", CODES, ids=ids)
+@pytest.mark.parametrize("decode", [True, False])
+def test_entries_that_are_no_pages(codes, decode):
+    """Tokens there are not attended to: in the middle, the last page, a whole sequence."""
+    def change(pool):
+        pool.table[0, 1] = -1
+        pool.table[1, 2] = pool.kc.shape[0]
+        pool.table[2, :] = -5
+        pool.table[3, 0] = 2 ** 31 - 1
+    n = [1] * 4 if decode else [20, 3, 5, 40]
+    attend([100, 70, 50, 1300], n, 4, 2, 64, 32, codes, torch.float16, 21, decode=decode, change=change)
+
+
+@pytest.mark.parametrize("codes", CODES, ids=ids)
+@pytest.mark.parametrize("spread", [1e-3, 1e4, 1e8])
+def test_scales_far_apart(codes, spread):
+    """V's scales grow and fall along a sequence by large factors."""
+    def change(pool):
+        for b, row in enumerate(pool.table.tolist()):
+            for i, p in enumerate(row):
+                if p >= 0:
+                    pool.vs[p] *= spread ** (((i + b) % 3) / 2) * (1e-4 if spread > 1e6 else 1.0)
+    attend([400, 131, 1500], [1, 1, 1], 4, 1, 128, 16, codes, torch.bfloat16, 31, decode=True, change=change)
+    attend([400, 131], [17, 90], 2, 1, 64, 16, codes, torch.bfloat16, 32, change=change)
+
+
+def test_one_page_outweighs_all():
+    """A key that takes nearly all the weight, late and early, in a long sequence."""
+    def change(pool):
+        pool.ks[pool.table[0, 3]] *= 60
+        pool.ks[pool.table[1, 200]] *= 60
+    attend([5000, 5000], [1, 1], 4, 2, 64, 16, torch.int8, torch.float16, 41, decode=True, qscale=3.0, change=change)
+
+
+@pytest.mark.parametrize("decode", [True, False])
+def test_queries_that_are_no_numbers(decode):
+    D, Hq, Hkv, page = 128, 8, 2, 32
+    pool = Pool([900, 80, 2000], Hkv, D, page, torch.int8, 51)
+    n = [1, 1, 1] if decode else [9, 80, 5]
+    T = sum(n)
+    q, = fused(T, [Hq], D, torch.float16, 52)
+    kp, vp, table, lens = pool.cuda()
+    cu = None if decode else starts(n)
+    want = W4.kv_attention_paged(q, kp, vp, table, lens, cu)
+    bad = q.clone()
+    bad[0, 1, 5], bad[1, 6, 0], bad[T - 1, 7] = float("nan"), float("inf"), float("-inf")
+    got = W4.kv_attention_paged(bad, kp, vp, table, lens, cu)
+    odd = torch.zeros((T, Hq), dtype=torch.bool, device="cuda")
+    odd[0, 1] = odd[1, 6] = odd[T - 1, 7] = True
+    assert torch.isnan(got[odd]).any(-1).all()
+    assert torch.equal(got[~odd], want[~odd])
+
+
+def test_shared_pages():
+    """Two sequences that begin with the same pages."""
+    def change(pool):
+        pool.table[1, :4] = pool.table[0, :4]
+    attend([100, 90, 200], [1, 1, 1], 4, 2, 128, 16, torch.int8, torch.float16, 61, decode=True, change=change)
+    attend([100, 90, 200], [30, 20, 5], 4, 2, 128, 16, torch.int8, torch.float16, 62, change=change)
+
+
+def test_rows_of_no_sequence_are_left():
+    D, Hq, Hkv, page, T = 64, 4, 2, 16, 60
+    pool = Pool([30, 50], Hkv, D, page, torch.float8_e4m3fn, 71)
+    q, = fused(T, [Hq], D, torch.bfloat16, 72)
+    q[:4] = float("nan")
+    kp, vp, table, lens = pool.cuda()
+    out = torch.full((T, Hq, D), 9.0, dtype=q.dtype, device="cuda")
+    cu = torch.tensor([4, 24, 50], dtype=torch.int32).cuda()
+    W4.kv_attention_paged(q, kp, vp, table, lens, cu, out=out)
+    assert (out[:4] == 9).all() and (out[50:] == 9).all()
+    check_attention(f64(out[4:24]), f64(q[4:24]), pool, 0, 20, Hq, q.dtype)
+    check_attention(f64(out[24:50]), f64(q[24:50]), pool, 1, 26, Hq, q.dtype)
+
+
+@pytest.mark.parametrize("B", [63, 64, 65, 200])
+def test_many_sequences(B):
+    """More sequences than a wave has lanes, some far longer than others."""
+    rng = np.random.default_rng(B)
+    lengths = [int(x) for x in rng.integers(0, 60, B)]
+    lengths[B // 3], lengths[B - 1] = 3000, 1500
+    attend(lengths, [1] * B, 2, 1, 64, 16, torch.int8, torch.float16, B, decode=True)
+    n = [min(x, int(y)) for x, y in zip(lengths, rng.integers(0, 12, B))]
+    attend(lengths, n, 2, 1, 64, 16, torch.int8, torch.float16, B + 1)
+
+
+def test_tables_wider_than_the_sequences():
+    attend([40, 1, 300], [1, 1, 1], 8, 2, 128, 64, torch.int8, torch.float16, 81, decode=True, room=500)
+    attend([40, 1, 300], [7, 1, 200], 8, 2, 128, 64, torch.int8, torch.float16, 82, room=500)
+
+
+# --------------------------------------------------------------------------- together
+
+@pytest.mark.parametrize("codes", CODES, ids=ids)
+def test_serving_loop(codes):
+    """Prompts, then steps, with page allocation as a server does it: every output against attention in fp64 over
+    what reading back gives, and the rows that were read within the codes' steps of the rotated ones."""
+    D, Hq, Hkv, page, dtype, B = 128, 8, 2, 16, torch.bfloat16, 3
+    kp, vp = W4.kv_pages(64, Hkv, page, D, codes)
+    free = torch.randperm(64, generator=torch.Generator().manual_seed(1)).tolist()
+    table = torch.full((B, 20), -1, dtype=torch.int32)
+    freqs, m = W4.rope_frequencies(D, 10000.0, "ramp", factor=4.0, original=128, low=1.0, high=32.0)
+    length = [0] * B
+    for step, n in enumerate([[40, 7, 65], [1, 1, 1], [1, 1, 1], [20, 1, 3], [1, 1, 1]]):
+        length = [a + b for a, b in zip(length, n)]
+        for b in range(B):
+            for i in range(-(-length[b] // page)):
+                if table[b, i] < 0:
+                    table[b, i] = free.pop()
+        q, k, v = fused(sum(n), [Hq, Hkv, Hkv], D, dtype, step)
+        cu = None if n == [1] * B else starts(n)
+        args = (kp, vp, table.cuda(), torch.tensor(length, dtype=torch.int32).cuda())
+        qr = W4.kv_append_paged(k, v, *args, cu, freqs=freqs, mscale=m, q=q)
+        out = f64(W4.kv_attention_paged(qr, *args, cu))
+        kk, vv = W4.kv_read_paged(*args, starts(length), T=sum(length), dtype=dtype)
+        at = first = 0
+        for b in range(B):
+            K, V = f64(kk[first:first + length[b]]), f64(vv[first:first + length[b]])
+            for i in range(n[b]):
+                see = length[b] - n[b] + i + 1
+                for h in range(Hq):
+                    s = K[:see, h // 4] @ f64(qr[at + i, h]) / np.sqrt(D)
+                    p = np.exp(s - s.max())
+                    p /= p.sum()
+                    # the rows were rounded to bf16 on reading: K's moves a weight by up to 2^-8 of sum |q k| / sqrt(D)
+                    # twice, V's an output by 2^-8
+                    move = 2.0 ** -8 * (np.abs(K[:see, h // 4]) @ np.abs(f64(qr[at + i, h]))).max() / np.sqrt(D)
+                    tol = (2.0 ** -7 + 2.0 ** -10 + np.expm1(2 * move)) * (p @ np.abs(V[:see, h // 4])) + 1e-6
+                    assert (np.abs(out[at + i, h] - p @ V[:see, h // 4]) <= tol).all()
+            at += n[b]
+            first += length[b]
+
+
+def graph_of(fn):
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        fn()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph, stream=side):
+            fn()
+    torch.cuda.synchronize()
+    return graph
+
+
+def test_captured_steps():
+    """A decode step in a captured graph, replayed on lengths and inputs that change in place, against eager
+    calls on a copy of the cache."""
+    D, Hq, Hkv, page, B, dtype = 128, 8, 2, 16, 3, torch.float16
+    lengths = [1500, 5, 200]
+    pool = Pool(lengths, Hkv, D, page, torch.int8, 91, room=2)
+    used = set(pool.table[pool.table >= 0].tolist())
+    free = [i for i in range(pool.kc.shape[0]) if i not in used]
+    for b in range(B):
+        pool.table[b, -(-lengths[b] // page)] = free[b]         # the next page of each
+    kp, vp, table, lens = pool.cuda()
+    copy = tuple(tuple(t.clone() for t in c) for c in (kp, vp))
+    q, k, v = fused(B, [Hq, Hkv, Hkv], D, dtype, 92)
+    freqs, _ = W4.rope_frequencies(D)
+    qo, out = torch.empty((B, Hq, D), dtype=dtype, device="cuda"), torch.empty((B, Hq, D), dtype=dtype, device="cuda")
+    work = torch.empty(W4.kv_attention_paged_workspace(Hq, Hkv, D, table.shape[1] * page), device="cuda")
+    start = lens.clone()
+
+    def step():
+        W4.kv_append_paged(k, v, kp, vp, table, lens, freqs=freqs, q=q, q_out=qo)
+        W4.kv_attention_paged(qo, kp, vp, table, lens, out=out, work=work)
+    graph = graph_of(step)
+    for a, c in ((kp, copy[0]), (vp, copy[1])):
+        for x, y in zip(a, c):
+            x.copy_(y)
+    for rep in range(6):
+        lens.copy_(start + rep)
+        for t in (q, k, v):
+            t.copy_(torch.randn(t.shape, generator=torch.Generator().manual_seed(rep)))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        q2 = W4.kv_append_paged(k, v, *copy, table, lens, freqs=freqs, q=q)
+        want = W4.kv_attention_paged(q2, *copy, table, lens)
+        assert torch.equal(out, want) and torch.equal(qo, q2)
+        for a, c in ((kp, copy[0]), (vp, copy[1])):
+            for x, y in zip(a, c):
+                assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
+def test_two_streams():
+    """Calls on two streams with workspaces of their own."""
+    D, Hq, Hkv, page = 128, 8, 2, 16
+    a, b = (Pool([4000, 900], Hkv, D, page, torch.int8, 100 + i) for i in range(2))
+    qs = [fused(2, [Hq], D, torch.float16, 110 + i)[0] for i in range(2)]
+    data = [p.cuda() for p in (a, b)]
+    want = [W4.kv_attention_paged(q, *d) for q, d in zip(qs, data)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [[torch.empty_like(q) for _ in range(20)] for q in qs]
+    works = [torch.empty(W4.kv_attention_paged_workspace(Hq, Hkv, D, 4096), device="cuda") for _ in range(2)]
+    for i in range(20):
+        for s, q, d, o, w in zip(streams, qs, data, outs, works):
+            with torch.cuda.stream(s):
+                W4.kv_attention_paged(q, *d, out=o[i], work=w)
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        for x in o:
+            assert torch.equal(x, w)

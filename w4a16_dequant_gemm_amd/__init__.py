@@ -28,14 +28,23 @@ the library's HIP kernels; there is no CPU or PyTorch fallback.
 ``kv_attention_decode_weights(q, kcache, vcache, lengths, weights)`` / ``kv_evict(kcache, vcache, weights, ...)``
     decode attention that adds up the attention weight of every cached token, and the compaction
     of a cache to the recent and the most attended tokens.
+``rope_frequencies(R, base, scaling)`` / ``rope(x, positions, freqs)``
+    rotary positions: half or interleaved pairs, part of a head, scaled for long contexts.
+``kv_pages(...)`` / ``kv_append_paged(k, v, kpages, vpages, table, lengths, ...)`` / ``kv_read_paged(...)``
+    a paged 8-bit cache with one scale a page and head: pools, appending with the keys (and queries)
+    rotated on the way, reading tokens back as 16-bit rows.
+``kv_attention_paged(q, kpages, vpages, table, lengths, cu_seqlens)``
+    causal attention over the pages, of a decode step's tokens or of chunks of prompts.
 """
 
 from __future__ import annotations
 
+import math
+
 import torch
 
 from . import _lib as _lib_mod
-from ._lib import (ASYM, BF16, F16, KvCache, OK, PATH_AUTO, PATH_GEMV, PATH_NAMES, PATH_PREFILL,
+from ._lib import (ASYM, BF16, F16, KV_E4M3, KV_INT8, KvCache, KvPaged, OK, PATH_AUTO, PATH_GEMV, PATH_NAMES, PATH_PREFILL,
                    PATH_SKINNY, SYM, W4A16Error, check, lib)
 
 __all__ = [
@@ -46,6 +55,8 @@ __all__ = [
     "awq_search", "awq_scale", "w8a8_smooth", "w8a8_quantize_weight", "w8a8_quantize_act",
     "w8a8_linear", "kv_quantize", "kv_attention_decode", "attention_prompt",
     "kv_attention_decode_shared", "kv_attention_decode_weights", "kv_evict",
+    "rope_frequencies", "rope", "kv_pages", "kv_append_paged", "kv_read_paged", "kv_attention_paged",
+    "kv_attention_paged_workspace",
 ]
 
 
@@ -875,3 +886,276 @@ def kv_evict(kcache, vcache, weights: torch.Tensor, lengths: torch.Tensor, budge
           weights.data_ptr(), lengths.data_ptr(), B, Hkv, Tmax, D, bits, budget, recent, _cache_struct(ko, vo, bits),
           Tout, wo.data_ptr(), lo.data_ptr(), kept.data_ptr(), None if work is None else work.data_ptr())
     return (ko, vo, wo, lo, kept)
+
+
+# --------------------------------------------------------------------------- rotary positions, paged cache
+
+def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                     original: int = 0, low: float = 1.0, high: float = 4.0, device="cuda"):
+    """The frequencies of rotary positions, ``base ** (-2 i / rotary_dim)`` radians a position for pair
+    ``i``, and the factor of the rotated values: ``(freqs, mscale)``, what :func:`rope` takes.
+
+    ``freqs`` is int64 ``[rotary_dim / 2]``: turns per position in units of 2^-64 (as unsigned numbers),
+    with which angles stay exact at any position.  ``scaling`` stretches them over longer contexts than
+    the ``original`` positions a model was trained on:
+
+    ``"linear"``  every frequency divided by ``factor``;
+    ``"base"``    the base raised by ``factor ** (R / (R - 2))``, so that the slowest pair is divided by
+                  ``factor`` and the fastest is left alone;
+    ``"bands"``   pairs that turn more than ``high`` times in ``original`` positions are left alone, those
+                  that turn less than ``low`` times divided by ``factor``, those between blended linearly in
+                  their turns;
+    ``"ramp"``    the same blended linearly in the pairs' index between the (whole) indices of ``high`` and
+                  ``low`` turns (usual: 32 and 1), with ``mscale = 0.1 ln(factor) + 1``.
+    """
+    R = rotary_dim
+    if R < 2 or R % 2:
+        raise ValueError("rotary_dim must be even and at least 2")
+    if not base > 0 or not factor > 0:
+        raise ValueError("base and factor must be positive")
+    if scaling not in ("none", "linear", "base", "bands", "ramp"):
+        raise ValueError("scaling must be 'none', 'linear', 'base', 'bands' or 'ramp'")
+    if scaling in ("bands", "ramp") and (original < 1 or not 0 < low < high):
+        raise ValueError(f"scaling '{scaling}' needs original >= 1 and 0 < low < high")
+    mscale = 1.0
+    if scaling == "base" and R > 2:
+        base = base * factor ** (R / (R - 2))
+    f = [base ** (-2.0 * i / R) for i in range(R // 2)]
+    if scaling == "linear":
+        f = [x / factor for x in f]
+    elif scaling == "bands":
+        for i, x in enumerate(f):
+            keep = min(max((original * x / (2 * math.pi) - low) / (high - low), 0.0), 1.0)
+            f[i] = x * (keep + (1.0 - keep) / factor)
+    elif scaling == "ramp":
+        def index(turns):
+            return R * math.log(original / (turns * 2 * math.pi)) / (2 * math.log(base))
+        first, last = max(math.floor(index(high)), 0), min(math.ceil(index(low)), R - 1)
+        for i, x in enumerate(f):
+            keep = 1.0 - min(max((i - first) / max(last - first, 1e-3), 0.0), 1.0)
+            f[i] = x * (keep + (1.0 - keep) / factor)
+        mscale = 0.1 * math.log(factor) + 1.0 if factor > 1.0 else 1.0
+    words = [round(x / (2 * math.pi) * 2.0 ** 64) % 2 ** 64 for x in f]
+    return torch.tensor([w - 2 ** 64 if w >= 2 ** 63 else w for w in words], dtype=torch.int64, device=device), mscale
+
+
+def _rows16(t, name: str, dtype) -> int:
+    """``t [T, H, D]`` with adjacent heads, in the usual case in few steps; returns the rows' distance."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.dim() == 3 and t.is_cuda:
+        T, H, D = t.shape
+        st, sh, sd = t.stride()
+        if sd == 1 and sh == D and T > 1:
+            return st
+    return _need_heads(t, name, dtype)
+
+
+def rope(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, interleaved: bool = False, mscale: float = 1.0,
+         out: torch.Tensor | None = None) -> torch.Tensor:
+    """Rotates the heads of ``x [T, H, D]`` (fp16 / bf16, adjacent heads, rows possibly strided) by their tokens'
+    positions (int32 ``[T]``): the first ``R = 2 * len(freqs)`` values of a head in pairs ``(i, i + R / 2)``, or
+    ``(2 i, 2 i + 1)`` if ``interleaved``, by the angle position times frequency, times ``mscale``; the rest
+    passes through.  ``freqs`` and ``mscale``: :func:`rope_frequencies`.  ``out`` may be ``x`` (in place), else
+    it must not overlap the inputs.  The gradient of ``x`` is ``rope(grad, -positions, ...)``."""
+    dt = _dtype_code(x)
+    dtype, dev = x.dtype, x.get_device()
+    xs = _rows16(x, "x", dtype)
+    T, H, D = x.shape
+    _need(positions, "positions", _INT32, 1)
+    _need(freqs, "freqs", torch.int64, 1)
+    if positions.shape[0] != T:
+        raise ValueError("positions must be [T]")
+    if out is None:
+        out = torch.empty((T, H, D), dtype=dtype, device=x.device)
+        os = H * D
+    else:
+        os = _rows16(out, "out", dtype)
+        if out.shape != x.shape:
+            raise ValueError("out must be [T, H, D]")
+    if not dev == positions.get_device() == freqs.get_device() == out.get_device():
+        raise ValueError("positions, freqs and out must be on the device of x")
+    _call(lib().w4a16_rope, "w4a16_rope", x.device, x.data_ptr(), dt, T, H, D, xs, positions.data_ptr(), freqs.data_ptr(),
+          2 * freqs.shape[0], 1 if interleaved else 0, mscale, out.data_ptr(), os)
+    return out
+
+
+_E4M3 = torch.float8_e4m3fn
+
+
+def kv_pages(pages: int, Hkv: int, page: int, D: int, codes=torch.int8, device="cuda"):
+    """An empty pool of a paged cache, ``(kpages, vpages)``, each ``(codes, scales)``: codes int8 or
+    float8_e4m3fn, K ``[pages, Hkv, page, D]`` and V ``[pages, Hkv, D, page]``, scales fp32 ``[pages, Hkv]``."""
+    if codes not in (_INT8, _E4M3):
+        raise TypeError("codes must be torch.int8 or torch.float8_e4m3fn")
+    if page not in (16, 32, 64, 128) or D not in (64, 128):
+        raise ValueError("page must be 16, 32, 64 or 128 and D 64 or 128")
+
+    def pool(shape):
+        return (torch.zeros(shape, dtype=torch.uint8, device=device).view(codes),
+                torch.zeros((pages, Hkv), dtype=torch.float32, device=device))
+    return pool((pages, Hkv, page, D)), pool((pages, Hkv, D, page))
+
+
+def _paged(kpages, vpages, table, lengths, cu, T: int | None, dev: int):
+    """The checked description of a paged cache and a call's sequences (``T`` None: the number of sequences)."""
+    (kc, ks), (vc, vs) = kpages, vpages
+    for t, name, nd in ((kc, "kpages codes", 4), (vc, "vpages codes", 4), (ks, "kpages scales", 2),
+                        (vs, "vpages scales", 2)):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.dim() != nd or not t.is_contiguous():
+            raise ValueError(f"{name} must be {nd}-D and contiguous")
+        if t.get_device() != dev:
+            raise ValueError(f"{name} must be on the device of the other arguments")
+    code = kc.dtype
+    if (code is not _INT8 and code is not _E4M3) or vc.dtype is not code:
+        raise TypeError("codes must be torch.int8 or torch.float8_e4m3fn, alike in kpages and vpages")
+    if ks.dtype is not torch.float32 or vs.dtype is not torch.float32:
+        raise TypeError("scales must be float32")
+    N, Hkv, page, D = kc.shape
+    if vc.shape != (N, Hkv, D, page) or ks.shape != (N, Hkv) or vs.shape != (N, Hkv):
+        raise ValueError("kpages must be [pages, Hkv, page, D], vpages [pages, Hkv, D, page] and scales [pages, Hkv]")
+    _need(table, "table", _INT32, 2)
+    _need(lengths, "lengths", _INT32, 1)
+    B, P = table.shape
+    if lengths.shape[0] != B:
+        raise ValueError("table must be [B, table_pages] and lengths [B]")
+    if cu is None:
+        if T is not None and T != B:
+            raise ValueError("without cu_seqlens every sequence has one token: T must be B")
+        T = B
+        at = None
+    else:
+        _need(cu, "cu_seqlens", _INT32, 1)
+        if cu.shape[0] != B + 1:
+            raise ValueError("cu_seqlens must be [B + 1]")
+        if cu.get_device() != dev:
+            raise ValueError("cu_seqlens must be on the device of the other arguments")
+        if T is None:
+            raise ValueError("T is needed where cu_seqlens is given")
+        at = cu.data_ptr()
+    if dev != table.get_device() or dev != lengths.get_device():
+        raise ValueError("table and lengths must be on the device of the other arguments")
+    return KvPaged(kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), table.data_ptr(), lengths.data_ptr(), at,
+                   N, page, P, B, T, Hkv, D, KV_INT8 if code is _INT8 else KV_E4M3)
+
+
+def kv_append_paged(k: torch.Tensor, v: torch.Tensor, kpages, vpages, table: torch.Tensor, lengths: torch.Tensor,
+                    cu_seqlens: torch.Tensor | None = None, freqs: torch.Tensor | None = None,
+                    positions: torch.Tensor | None = None, interleaved: bool = False, mscale: float = 1.0,
+                    q: torch.Tensor | None = None, q_out: torch.Tensor | None = None) -> torch.Tensor | None:
+    """Writes the last tokens of every sequence into the pages of :func:`kv_pages`, keys rotated on the way.
+
+    ``k`` and ``v [T, Hkv, D]`` (fp16 / bf16, adjacent heads, rows possibly strided) are the sequences' new
+    tokens: one each, or ``cu_seqlens[b + 1] - cu_seqlens[b]`` of sequence ``b`` from row ``cu_seqlens[b]`` on
+    (int32 ``[B + 1]``).  ``lengths`` (int32 ``[B]``) counts a sequence's tokens with the new ones, ``table``
+    (int32 ``[B, table_pages]``) names the pages of its tokens in turn; an entry that is no page of the pool takes
+    none.  A page that is written to must belong to one sequence.
+
+    A page's scale grows with the tokens written to it since its first slot was, earlier codes being rounded again; infinities
+    take the largest code, NaN 0.  ``freqs`` (:func:`rope_frequencies`; None: no rotation), ``interleaved`` and
+    ``mscale`` as in :func:`rope`, by ``positions`` (int32 ``[T]``) or the tokens' places in their sequences.
+    ``q [T, Hq, D]`` is rotated likewise into ``q_out`` (dense, apart from the inputs), which is returned."""
+    dt = _dtype_code(k)
+    dtype, dev = k.dtype, k.get_device()
+    ks, vs = _rows16(k, "k", dtype), _rows16(v, "v", dtype)
+    c = _paged(kpages, vpages, table, lengths, cu_seqlens, k.shape[0], dev)
+    T, Hkv, D = k.shape
+    if v.shape != k.shape or Hkv != c.Hkv or D != c.D:
+        raise ValueError("k and v must be [T, Hkv, D]")
+    R, f = 0, None
+    if freqs is not None:
+        _need(freqs, "freqs", torch.int64, 1)
+        R, f = 2 * freqs.shape[0], freqs.data_ptr()
+    if positions is not None:
+        _need(positions, "positions", _INT32, 1)
+        if positions.shape[0] != T:
+            raise ValueError("positions must be [T]")
+    Hq, qs, qp, qo = 0, 0, None, None
+    if q is not None:
+        qs = _rows16(q, "q", dtype)
+        if q.shape[0] != T or q.shape[2] != D:
+            raise ValueError("q must be [T, Hq, D]")
+        Hq = q.shape[1]
+        if q_out is None:
+            q_out = torch.empty((T, Hq, D), dtype=dtype, device=k.device)
+        else:
+            _need(q_out, "q_out", dtype, 3)
+            if q_out.shape != q.shape:
+                raise ValueError("q_out must be [T, Hq, D]")
+        qp, qo = q.data_ptr(), q_out.data_ptr()
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    _same_device(k, "k", v=v, freqs=freqs, positions=positions, q=q, q_out=q_out)
+    _call(lib().w4a16_kv_append_paged, "w4a16_kv_append_paged", k.device, c, k.data_ptr(), v.data_ptr(), dt, ks, vs,
+          None if positions is None else positions.data_ptr(), f, R, 1 if interleaved else 0, mscale, qp, Hq, qs, qo)
+    return q_out
+
+
+def kv_read_paged(kpages, vpages, table: torch.Tensor, lengths: torch.Tensor, cu_seqlens: torch.Tensor | None = None,
+                  T: int | None = None, dtype=torch.float16, out=None):
+    """The last tokens of every sequence as 16-bit rows ``(k, v)``, ``[T, Hkv, D]`` each: the tokens that
+    :func:`kv_append_paged` with the same arguments writes.  ``T`` is the number of packed rows where
+    ``cu_seqlens`` is given; ``out`` takes ``(k, v)`` to write into (their shape and type then count).  Tokens
+    without a page are zeros; rows of no sequence are not written."""
+    if out is not None:
+        ko, vo = out
+        _need(ko, "out k", ko.dtype, 3)
+        _need(vo, "out v", ko.dtype, 3)
+        if T is not None and T != ko.shape[0]:
+            raise ValueError("out and T disagree")
+        T, dtype = ko.shape[0], ko.dtype
+    dev = kpages[0].get_device()
+    c = _paged(kpages, vpages, table, lengths, cu_seqlens, T, dev)
+    shape = (c.T, c.Hkv, c.D)
+    if out is None:
+        ko, vo = (torch.empty(shape, dtype=dtype, device=kpages[0].device) for _ in range(2))
+    elif ko.shape != shape or vo.shape != shape:
+        raise ValueError("out must be two tensors [T, Hkv, D]")
+    if dev != ko.get_device() or dev != vo.get_device():
+        raise ValueError("out must be on the device of the pages")
+    _call(lib().w4a16_kv_read_paged, "w4a16_kv_read_paged", ko.device, c, _dtype_code(ko), ko.data_ptr(), vo.data_ptr())
+    return ko, vo
+
+
+def kv_attention_paged_workspace(Hq: int, Hkv: int, D: int, tokens: int) -> int:
+    """fp32 elements of a scratch buffer that holds every :func:`kv_attention_paged` call of these heads whose
+    table has room for at most ``tokens`` tokens (0: none)."""
+    need = lib().w4a16_kv_attention_paged_workspace(Hq, Hkv, D, tokens)
+    if need < 0:
+        raise W4A16Error(int(need), "w4a16_kv_attention_paged_workspace")
+    return int(need)
+
+
+def kv_attention_paged(q: torch.Tensor, kpages, vpages, table: torch.Tensor, lengths: torch.Tensor,
+                       cu_seqlens: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                       work: torch.Tensor | None = None) -> torch.Tensor:
+    """Causal attention of every sequence's last tokens over its pages, which hold their keys and values already
+    (:func:`kv_append_paged` with the same arguments): a decode step, or chunks of prompts where
+    ``cu_seqlens`` is given.
+
+    ``q [T, Hq, D]`` (fp16 / bf16, adjacent heads, rows possibly strided); a row sees the tokens up to its own,
+    heads ``h`` of q those of kv head ``h // (Hq / Hkv)``.  Rows that see nothing are zeros, rows of no sequence
+    are not written.  ``out`` must not overlap the inputs.  ``work`` is an optional fp32 buffer of at least
+    :func:`kv_attention_paged_workspace` elements (0 for short tables); calls that may overlap need one each.
+
+    Codes enter the products exactly; the softmax weights, with V's scales, are rounded once to fp16 (relative
+    2^-11); scores, statistics and sums are fp32."""
+    dt = _dtype_code(q)
+    qs = _rows16(q, "q", q.dtype)
+    T, Hq, D = q.shape
+    c = _paged(kpages, vpages, table, lengths, cu_seqlens, T, q.get_device())
+    if D != c.D:
+        raise ValueError("q must be [T, Hq, D]")
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
+    else:
+        _need(out, "out", q.dtype, 3)
+        if out.shape != q.shape or out.get_device() != q.get_device():
+            raise ValueError("out must be [T, Hq, D] on the device of q")
+    L = lib()
+    need = L.w4a16_kv_attention_paged_workspace(Hq, c.Hkv, D, c.table_pages * c.page)
+    if need or work is not None:
+        work = _work(work, need, "w4a16_kv_attention_paged_workspace", q)
+    _call(L.w4a16_kv_attention_paged, "w4a16_kv_attention_paged", q.device, c, q.data_ptr(), dt, Hq, qs,
+          None if work is None else work.data_ptr(), out.data_ptr())
+    return out

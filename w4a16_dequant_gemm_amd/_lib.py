@@ -17,6 +17,7 @@ ERR_NULL, ERR_SHAPE, ERR_GROUP, ERR_ALIGN, ERR_DTYPE, ERR_SCHEME, ERR_HIP, ERR_P
     ERR_OVERLAP = -1, -2, -3, -4, -5, -6, -7, -8, -9, -10
 F16, BF16 = 0, 1
 ASYM, SYM = 0, 1
+KV_INT8, KV_E4M3 = 0, 1
 PATH_AUTO, PATH_GEMV, PATH_SKINNY, PATH_PREFILL = 0, 1, 2, 3
 PATH_NAMES = {PATH_GEMV: "gemv", PATH_SKINNY: "skinny", PATH_PREFILL: "prefill"}
 
@@ -31,6 +32,15 @@ class KvCache(ctypes.Structure):
     """``w4a16_kv_cache`` / ``w4a16_kv_cache_out`` of the C ABI."""
     _fields_ = [("kcodes", ctypes.c_void_p), ("kscales", ctypes.c_void_p), ("kzeros", ctypes.c_void_p),
                 ("vcodes", ctypes.c_void_p), ("vscales", ctypes.c_void_p), ("vzeros", ctypes.c_void_p)]
+
+
+class KvPaged(ctypes.Structure):
+    """``w4a16_kv_paged`` of the C ABI."""
+    _fields_ = [("kcodes", ctypes.c_void_p), ("kscales", ctypes.c_void_p), ("vcodes", ctypes.c_void_p),
+                ("vscales", ctypes.c_void_p), ("table", ctypes.c_void_p), ("lengths", ctypes.c_void_p),
+                ("cu_seqlens", ctypes.c_void_p), ("pages", ctypes.c_int64), ("page", ctypes.c_int64),
+                ("table_pages", ctypes.c_int64), ("B", ctypes.c_int64), ("T", ctypes.c_int64), ("Hkv", ctypes.c_int64),
+                ("D", ctypes.c_int64), ("format", ctypes.c_int)]
 
 
 _lib = None
@@ -137,6 +147,17 @@ def lib() -> ctypes.CDLL:
     L.w4a16_kv_evict_workspace.argtypes = [i64, i64, i64]
     L.w4a16_gptq_quantize.restype = i32
     L.w4a16_gptq_quantize.argtypes = [vp, i64, i64, i64, i32, vp, vp, vp, vp, vp, vp]
+    f32, paged = ctypes.c_float, ctypes.POINTER(KvPaged)
+    L.w4a16_rope.restype = i32
+    L.w4a16_rope.argtypes = [vp, i32, i64, i64, i64, i64, vp, vp, i64, i32, f32, vp, i64, vp]
+    L.w4a16_kv_append_paged.restype = i32
+    L.w4a16_kv_append_paged.argtypes = [paged, vp, vp, i32, i64, i64, vp, vp, i64, i32, f32, vp, i64, i64, vp, vp]
+    L.w4a16_kv_read_paged.restype = i32
+    L.w4a16_kv_read_paged.argtypes = [paged, i32, vp, vp, vp]
+    L.w4a16_kv_attention_paged_workspace.restype = i64
+    L.w4a16_kv_attention_paged_workspace.argtypes = [i64, i64, i64, i64]
+    L.w4a16_kv_attention_paged.restype = i32
+    L.w4a16_kv_attention_paged.argtypes = [paged, vp, i32, i64, i64, vp, vp, vp]
     _lib = L
     return L
 

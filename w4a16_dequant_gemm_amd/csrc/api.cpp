@@ -635,6 +635,167 @@ int w4a16_kv_evict(const w4a16_kv_cache* in, const float* weights, const int32_t
     return hip_status(w4a16::launch_kv_evict(a, reinterpret_cast<uint32_t*>(work), static_cast<hipStream_t>(stream)));
 }
 
+// ----------------------------------------------------------------- paged 8-bit cache
+
+}  // extern "C"
+
+namespace {
+constexpr int64_t kMaxRows = int64_t(1) << 24;              // packed tokens of a call
+constexpr int64_t kMaxPagedBlocks = int64_t(1) << 23;       // of 256 threads, twice (K and V)
+
+int check_paged(const w4a16_kv_paged* c, w4a16::KvPages* p) {
+    if (!c || !c->kcodes || !c->kscales || !c->vcodes || !c->vscales || !c->table || !c->lengths) return W4A16_ERR_NULL;
+    if (c->format != W4A16_KV_INT8 && c->format != W4A16_KV_E4M3) return W4A16_ERR_SCHEME;
+    const int64_t page = c->page;
+    if ((page != 16 && page != 32 && page != 64 && page != 128) || (c->D != 64 && c->D != 128) || c->B < 1 ||
+        c->B > 65535 || c->T < 1 || c->T > kMaxRows || (!c->cu_seqlens && c->T != c->B) || c->Hkv < 1 ||
+        c->Hkv > 65535 || c->pages < 1 || c->pages > 0x7FFFFFFF || c->table_pages < 1 ||
+        c->table_pages > kMaxTokens / page || (c->T / page + 2 * c->B) * c->Hkv + c->T >= kMaxPagedBlocks)
+        return W4A16_ERR_SHAPE;
+    if (!aligned(c->kcodes, 16) || !aligned(c->vcodes, 16) || !aligned(c->kscales, 4) || !aligned(c->vscales, 4) ||
+        !aligned(c->table, 4) || !aligned(c->lengths, 4) || !aligned(c->cu_seqlens, 4))
+        return W4A16_ERR_ALIGN;
+    *p = {c->kcodes, c->vcodes, c->kscales, c->vscales, c->table, c->lengths, c->cu_seqlens, (int)c->pages, (int)c->Hkv,
+          (int)c->D, (int)page, c->format, (int)c->B, (int)c->table_pages, (int)c->T};
+    return W4A16_OK;
+}
+// The pool, and the description of the sequences.
+struct PoolSpans {
+    Span s[4];
+    explicit PoolSpans(const w4a16_kv_paged& c)
+        : s{{c.kcodes, c.pages * c.Hkv * c.page * c.D}, {c.vcodes, c.pages * c.Hkv * c.page * c.D},
+            {c.kscales, 4 * c.pages * c.Hkv}, {c.vscales, 4 * c.pages * c.Hkv}} {}
+};
+struct SequenceSpans {
+    Span s[3];
+    explicit SequenceSpans(const w4a16_kv_paged& c)
+        : s{{c.table, 4 * c.B * c.table_pages}, {c.lengths, 4 * c.B}, {c.cu_seqlens, 4 * (c.B + 1)}} {}
+};
+bool row_stride_ok(int64_t stride, int64_t row) { return stride >= row && stride <= kMaxRows; }
+Span rows_span(const void* p, int64_t T, int64_t stride, int64_t row) { return {p, 2 * ((T - 1) * stride + row)}; }
+}  // namespace
+
+extern "C" {
+
+int w4a16_rope(const void* x, int dtype, int64_t T, int64_t H, int64_t D, int64_t x_stride, const int32_t* positions,
+               const int64_t* freqs, int64_t R, int interleaved, float mscale, void* out, int64_t out_stride,
+               void* stream) {
+    if (!x || !positions || !freqs || !out) return W4A16_ERR_NULL;
+    if (dtype != W4A16_F16 && dtype != W4A16_BF16) return W4A16_ERR_DTYPE;
+    if (T < 1 || T > kMaxRows || H < 1 || H > 65535 || D < 2 || D > 512 || D % 2 || R < 2 || R > D || R % 2 ||
+        !row_stride_ok(x_stride, H * D) || !row_stride_ok(out_stride, H * D) || (x == out && x_stride != out_stride))
+        return W4A16_ERR_SHAPE;
+    if (!aligned(x, 2) || !aligned(out, 2) || !aligned(positions, 4) || !aligned(freqs, 8)) return W4A16_ERR_ALIGN;
+    const Span ins[] = {{x == out ? nullptr : x, rows_span(x, T, x_stride, H * D).n}, {positions, 4 * T}, {freqs, 4 * R}};
+    if (overlaps(rows_span(out, T, out_stride, H * D), ins)) return W4A16_ERR_OVERLAP;
+    w4a16::RopeArgs a = {};
+    a.x = x;
+    a.out = out;
+    a.positions = positions;
+    a.freqs = reinterpret_cast<const long long*>(freqs);
+    a.m = mscale;
+    a.dtype = dtype;
+    a.T = (int)T;
+    a.H = (int)H;
+    a.D = (int)D;
+    a.R = (int)R;
+    a.xs = (int)x_stride;
+    a.os = (int)out_stride;
+    a.inter = interleaved != 0;
+    return hip_status(w4a16::launch_rope(a, static_cast<hipStream_t>(stream)));
+}
+
+int w4a16_kv_append_paged(const w4a16_kv_paged* cache, const void* k, const void* v, int dtype, int64_t k_stride,
+                          int64_t v_stride, const int32_t* positions, const int64_t* freqs, int64_t R, int interleaved,
+                          float mscale, const void* q, int64_t Hq, int64_t q_stride, void* q_out, void* stream) {
+    if (!k || !v || (R != 0 && !freqs) || (!q != !q_out)) return W4A16_ERR_NULL;
+    if (dtype != W4A16_F16 && dtype != W4A16_BF16) return W4A16_ERR_DTYPE;
+    w4a16::KvAppendArgs a = {};
+    const int st = check_paged(cache, &a.c);
+    if (st != W4A16_OK) return st;
+    const int64_t T = cache->T, row = cache->Hkv * cache->D, qrow = q ? Hq * cache->D : 0;
+    if (R < 0 || R > cache->D || R % 2 || !row_stride_ok(k_stride, row) || !row_stride_ok(v_stride, row) ||
+        (q && (Hq < 1 || Hq > 65535 || !row_stride_ok(q_stride, qrow))))
+        return W4A16_ERR_SHAPE;
+    if (!aligned(k, 16) || !aligned(v, 16) || k_stride % 8 || v_stride % 8 || !aligned(positions, 4) ||
+        !aligned(freqs, 8) || (q && (!aligned(q, 16) || !aligned(q_out, 16) || q_stride % 8)))
+        return W4A16_ERR_ALIGN;
+    const Span ins[] = {rows_span(k, T, k_stride, row), rows_span(v, T, v_stride, row), {positions, 4 * T},
+                        {R ? freqs : nullptr, 4 * R}, rows_span(q, T, q_stride, qrow)};
+    const PoolSpans pool(*cache);
+    const SequenceSpans seqs(*cache);
+    const Span qo = {q_out, 2 * T * qrow};
+    if (overlaps(qo, ins) || overlaps(qo, pool.s) || overlaps(qo, seqs.s)) return W4A16_ERR_OVERLAP;
+    for (const Span& o : pool.s)
+        if (overlaps(o, ins) || overlaps(o, pool.s) || overlaps(o, seqs.s)) return W4A16_ERR_OVERLAP;
+    a.k = k;
+    a.v = v;
+    a.q = q;
+    a.q_out = q_out;
+    a.positions = positions;
+    a.freqs = reinterpret_cast<const long long*>(freqs);
+    a.m = mscale;
+    a.dtype = dtype;
+    a.ks = (int)k_stride;
+    a.vs = (int)v_stride;
+    a.qs = (int)q_stride;
+    a.Hq = (int)Hq;
+    a.R = (int)R;
+    a.inter = interleaved != 0;
+    return hip_status(w4a16::launch_kv_append(a, static_cast<hipStream_t>(stream)));
+}
+
+int w4a16_kv_read_paged(const w4a16_kv_paged* cache, int dtype, void* k_out, void* v_out, void* stream) {
+    if (!k_out || !v_out) return W4A16_ERR_NULL;
+    if (dtype != W4A16_F16 && dtype != W4A16_BF16) return W4A16_ERR_DTYPE;
+    w4a16::KvPages p;
+    const int st = check_paged(cache, &p);
+    if (st != W4A16_OK) return st;
+    if (!aligned(k_out, 16) || !aligned(v_out, 16)) return W4A16_ERR_ALIGN;
+    const int64_t n = 2 * cache->T * cache->Hkv * cache->D;
+    const Span outs[] = {{k_out, n}, {v_out, n}};
+    const PoolSpans pool(*cache);
+    const SequenceSpans seqs(*cache);
+    for (const Span& o : outs)
+        if (overlaps(o, outs) || overlaps(o, pool.s) || overlaps(o, seqs.s)) return W4A16_ERR_OVERLAP;
+    return hip_status(w4a16::launch_kv_read(p, dtype, k_out, v_out, static_cast<hipStream_t>(stream)));
+}
+
+int64_t w4a16_kv_attention_paged_workspace(int64_t Hq, int64_t Hkv, int64_t D, int64_t tokens) {
+    if (Hkv < 1 || Hkv > 65535 || Hq < 1 || Hq > 65535 || Hq % Hkv || (D != 64 && D != 128) || tokens < 1 ||
+        tokens > kMaxTokens)
+        return W4A16_ERR_SHAPE;
+    return w4a16::kv_paged_workspace_floats(Hq, Hkv, D, tokens);
+}
+
+int w4a16_kv_attention_paged(const w4a16_kv_paged* cache, const void* q, int dtype, int64_t Hq, int64_t q_stride,
+                             float* work, void* out, void* stream) {
+    if (!q || !out) return W4A16_ERR_NULL;
+    if (dtype != W4A16_F16 && dtype != W4A16_BF16) return W4A16_ERR_DTYPE;
+    w4a16::KvPagedArgs a = {};
+    const int st = check_paged(cache, &a.c);
+    if (st != W4A16_OK) return st;
+    const int64_t Hkv = cache->Hkv, T = cache->T, row = Hq * cache->D;
+    if (Hq < 1 || Hq > 65535 || Hq % Hkv || !row_stride_ok(q_stride, row) ||
+        (T * (Hq / Hkv) / 16 + cache->B + 1024) * Hkv >= kMaxPagedBlocks)
+        return W4A16_ERR_SHAPE;
+    const int64_t need = w4a16::kv_paged_workspace_floats(Hq, Hkv, cache->D, cache->table_pages * cache->page);
+    if (need > 0 && !work) return W4A16_ERR_NULL;
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(work, 16) || q_stride % 8) return W4A16_ERR_ALIGN;
+    const Span ins[] = {rows_span(q, T, q_stride, row)};
+    const Span outs[] = {{out, 2 * T * row}, {work, 4 * need}};
+    const PoolSpans pool(*cache);
+    const SequenceSpans seqs(*cache);
+    for (const Span& o : outs)
+        if (overlaps(o, ins) || overlaps(o, outs) || overlaps(o, pool.s) || overlaps(o, seqs.s)) return W4A16_ERR_OVERLAP;
+    a.q = q;
+    a.out = out;
+    a.dtype = dtype;
+    a.qs = (int)q_stride;
+    a.Hq = (int)Hq;
+    return hip_status(w4a16::launch_kv_paged(a, work, static_cast<hipStream_t>(stream)));
+}
+
 int w4a16_select_path(int64_t M, int64_t N, int64_t K, int64_t group_size, int dtype) {
     // Fake, aligned, non-null pointers: only shapes are examined.
     alignas(16) static const unsigned char dummy[16] = {0};

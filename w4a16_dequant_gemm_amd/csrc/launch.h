@@ -151,6 +151,48 @@ struct PromptArgs {
 };
 hipError_t launch_attention_prompt(const PromptArgs& a, hipStream_t st);
 
+// Paged 8-bit KV cache (pages.h has its layout): B sequences, whose last tokens a call is about, packed along T
+// by their bounds cu [B + 1] (clamped into [0, T]; NULL: one token each, T == B).
+struct KvPages {
+    void *kc, *vc;              // codes of N pages
+    float *ks, *vs;             // [N, Hkv]
+    const int* table;           // [B, P] page numbers; others than 0 .. N - 1 are no pages
+    const int *lens, *cu;       // lens [B]: tokens with the call's own
+    int N, Hkv, D, page, fmt, B, P, T;
+};
+// Rotations (kv_pages.hip): rows of x and out are xs and os elements apart, heads D; R values of a head turn
+// by positions times freqs (R / 2 fractions of a turn in units of 2^-64).
+struct RopeArgs {
+    const void* x;
+    void* out;
+    const int* positions;
+    const long long* freqs;
+    float m;
+    int dtype, T, H, D, R, xs, os, inter;
+};
+hipError_t launch_rope(const RopeArgs& a, hipStream_t st);
+struct KvAppendArgs {
+    KvPages c;
+    const void *k, *v, *q;      // q NULL: none
+    void* q_out;
+    const int* positions;       // NULL: places in the cache
+    const long long* freqs;
+    float m;
+    int dtype, ks, vs, qs, Hq, R, inter;
+};
+hipError_t launch_kv_append(const KvAppendArgs& a, hipStream_t st);
+hipError_t launch_kv_read(const KvPages& c, int dtype, void* kout, void* vout, hipStream_t st);
+// Attention over the pages (kv_paged.hip): q and out [T, Hq, D], rows of q qs elements apart.
+struct KvPagedArgs {
+    KvPages c;
+    const void* q;
+    void* out;
+    int dtype, qs, Hq;
+};
+// fp32 elements of workspace of every call of these heads (0: none where the table has few tokens).
+long long kv_paged_workspace_floats(long long Hq, long long Hkv, long long D, long long tokens);
+hipError_t launch_kv_paged(const KvPagedArgs& a, float* work, hipStream_t st);
+
 // AWQ (awq.hip)
 long long awq_workspace_doubles(long long N, long long K, long long n);
 hipError_t launch_awq_stats(const void* X, int dtype, int n, int K, float* xmean, hipStream_t s);
