@@ -531,7 +531,7 @@ int w4a16_kv_evict(const w4a16_kv_cache* in, const float* weights, const int32_t
  * A pool holds `pages` pages of `page` tokens (16, 32, 64 or 128).  Of page i and kv head h
  *   kcodes  [pages, Hkv, page, D]  8-bit codes, a token's row after the other;
  *   vcodes  [pages, Hkv, D, page]  across: a dimension's tokens after one another;
- *   kscales, vscales  [pages, Hkv] fp32; a code c stands for scale * c.
+ *   kscales, vscales  [pages, Hkv] fp32, not negative; a code c stands for scale * c.
  * format: W4A16_KV_INT8 (whole numbers -127 .. 127) or W4A16_KV_E4M3 (8-bit floats with 4 exponent and 3
  * mantissa bits, largest 448).  D is 64 or 128.  Codes 16-byte aligned, everything else 4-byte.
  *
@@ -619,7 +619,7 @@ int64_t w4a16_kv_attention_paged_workspace(int64_t Hq, int64_t Hkv, int64_t D, i
  *   work  w4a16_kv_attention_paged_workspace(...) fp32 elements, 16-byte aligned (scratch, contents undefined after
  *         the call; calls that overlap on one buffer race), or NULL when that is 0.
  * Codes enter the products exactly; the softmax weights times V's scales are rounded once to fp16 (relative
- * 2^-11 down to 2^-29 of the row's largest, below by 2^-40 of it); scores, softmax statistics and sums are fp32, the output is rounded once.
+ * 2^-11 down to 2^-25 of the row's largest, below by 2^-36 of it); scores, softmax statistics and sums are fp32, the output is rounded once.
  * The codes of a sequence's tokens have to be numbers (what w4a16_kv_append_paged writes is); behind them anything may lie.
  * out and work must be apart from the inputs and each other (W4A16_ERR_OVERLAP).
  * Limits besides the above: Hq <= 65535, (T * Hq / Hkv / 16 + B + 1024) * Hkv < 2^23.

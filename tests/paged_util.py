@@ -8,10 +8,10 @@ the two products and their sum by 2 * 2^-24 of |x0| + |x1| more; u is the roundi
 
 Attention: as for the contiguous caches (a weight has the fp32 error e of its score and the exponential and
 is rounded once to fp16 with V's scale, relative 2^-11; the sum of n / 16 products of 16 tokens runs in fp32), but
-weights times scales are held times 2^15 over the power of two above the largest scale, so that roundings below
-fp16's normal range cost 2^-25 2^-15 2 smax = 2^-39 smax per token, times the largest code:
+weights times scales are held times 2^11 (2^15 where there are few rows) over the power of two above the largest
+scale, so that roundings below fp16's normal range cost 2^-25 2^-11 2 smax = 2^-35 smax per token, times the largest code:
 
-    |out - ref| <= u |ref| + (1 + u) (2^-11 + e + (n / 16 + 40) 2^-24) sum p |v| + n 2^-39 smax cmax + 2^-25 [fp16].
+    |out - ref| <= u |ref| + (1 + u) (2^-11 + e + (n / 16 + 40) 2^-24) sum p |v| + n 2^-35 smax cmax + 2^-25 [fp16].
 """
 
 from __future__ import annotations
@@ -129,7 +129,7 @@ def check_attention(got, q, pool, b, n, Hq, dtype):
             ref, mag = p @ vv, p @ np.abs(vv)
             e = weight_error(D, float((np.abs(kk) @ np.abs(q[i, h])).max() / np.sqrt(D)))
             m = len(kk)
-            tol = u * np.abs(ref) + (1 + u) * (2.0 ** -11 + e + (m / 16 + 40) * 2.0 ** -24) * mag + m * 2.0 ** -39 * smax * cmax
+            tol = u * np.abs(ref) + (1 + u) * (2.0 ** -11 + e + (m / 16 + 40) * 2.0 ** -24) * mag + m * 2.0 ** -35 * smax * cmax
             if dtype == torch.float16:
                 tol = tol + 2.0 ** -25
             err = np.abs(got[i, h] - ref)

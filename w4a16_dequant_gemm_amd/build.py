@@ -25,7 +25,8 @@ PROBE_SOURCE = "probe.hip"
 OBJDIR = os.path.join(HERE, "_build")
 SOURCES = ["api.cpp", "quantize.hip", "gemv.hip", "skinny.hip", "decode.hip", "prefill.hip", "gptq.hip",
            "awq.hip", "w8a8.hip", "kv.hip", "w8a16.hip", "scratch.hip", "attention.hip", "kv_attend.hip",
-           "kv_evict.hip", "kv_pages.hip", "kv_paged.hip"]
+           "kv_evict.hip", "kv_pages.hip", "kv_paged.hip",
+           "kv_paged_chunk.hip"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",

@@ -1,0 +1,356 @@
+// Causal attention over a paged 8-bit KV cache for many query rows at a time: chunks of prompts behind what is
+// cached already (kv_paged.hip has the operator and takes few rows).
+//
+// One block = 128 rows (tokens times the heads of a kv head, token by token), 32 a wave; it walks the cached
+// tokens in tiles of 64.  Both products run transposed on 32 x 32 x 16 tiles (attn.h).  A tile's codes are read
+// two tiles ahead into registers, widened to 16 bits (exact) once for the block's rows and put into LDS while the
+// products of the tile before run.
+//
+// K's 32-row operands take the tokens with bits 2 and 3 of their index exchanged, so that a lane's scores of
+// registers 8 s .. 8 s + 7 are the consecutive tokens 16 s + 8 (l / 32) .. + 7, which V, whose tokens are
+// consecutive in memory, then has as 16 bytes.
+//
+// Scales: a tile is four groups of 16 tokens, each of one page.  K's scale and 1 / sqrt(D) ride on the multiply-add
+// before the exponential; V's does too, as its logarithm: the weights come out times scale / 2^unit, as they
+// enter the second product, and a group's sum is divided by that again.  Weights are held times 2^11 and
+// rounded once to fp16.  The running maximum may lag by 4 (base 2), so that O is rarely rescaled.
+#include <algorithm>
+
+#include "paged.h"
+
+namespace w4a16 {
+
+namespace {
+
+constexpr int kRows = 128;              // query rows of a block
+constexpr float kLag = 4.0f;            // the maximum may lag by so much (base 2)
+constexpr int kRaise = 11;              // weights are held times 2^kRaise; 2^(kLag + kRaise) < 65504
+constexpr int kDeepest = -60;           // scales below 2^kDeepest of the largest count as that (their share is nothing)
+constexpr float kLowest = -3.402823466e38f;
+
+// 64 pages of a sequence from page `base` on, one a lane.
+struct Window {
+    int base;
+    int id;                             // -1: no page
+    float kc;                           // K's scale times log2(e) / sqrt(D)
+    float lm, im;                       // logarithm (base 2) and reciprocal of V's scale's mantissa
+    int e;                              // its exponent; kNone: V's scale is 0, or there is no page
+};
+constexpr int kNone = -10000;
+
+__device__ __forceinline__ int lane_of(int v, int l) { return __builtin_amdgcn_readlane(v, l); }
+__device__ __forceinline__ float lane_of(float v, int l) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), l));
+}
+__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
+template <int DT, int FMT, int D>
+__global__ __launch_bounds__(256, 2) void kv_paged_chunk_kernel(PagedView a) {
+    constexpr int TILE = kTile * D, PR = D / 16, NL = kTile * PR / 256;   // 16-code pieces of a K row; loads of a thread
+    __shared__ __attribute__((aligned(16))) uint16_t lK[2][TILE], lV[2][TILE];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int n = lane & 31, hf = lane >> 5;
+    const int h = blockIdx.x % a.c.Hkv;
+    Piece p;
+    if (!find_piece<kRows, false>(a.s, blockIdx.x / a.c.Hkv, lane, p)) return;
+    const int shift = a.shift, page = 1 << shift, G = a.s.G;
+    const int rows = min(kRows, p.n * G - p.row0);
+    // tokens that rows see: row r those up to len - n + r / G
+    const int wrow = p.row0 + 32 * wave, row = p.row0 + min(32 * wave + n, rows - 1), past = p.len - p.n;
+    const int seen = past + row / G;
+    const int most = past + (p.row0 + rows - 1) / G;                            // of the block
+    const bool idle = 32 * wave >= rows;
+    const int tile1 = min(p.tile1, most >= 0 ? most / kTile + 1 : 0);           // the block's tiles: [tile0, tile1)
+    const int first = past + min(wrow, p.row0 + rows - 1) / G, last = past + min(wrow + 31, p.row0 + rows - 1) / G;
+    const int own1 = idle || last < 0 ? 0 : min(tile1, last / kTile + 1);       // the wave's tiles end there,
+    const int clear1 = first < 0 ? 0 : (first + 1) / kTile;                     // and those before need no mask
+
+    u32x4 qf[D / 16];
+    {
+        const uint16_t* qp = a.q + (long long)(p.first + row / G) * a.qs + (h * G + row % G) * D + 8 * hf;
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s) qf[s] = *reinterpret_cast<const u32x4*>(qp + 16 * s);
+    }
+    f32x16 o[D / 32];
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[i][e] = 0.0f;
+    float M = -__builtin_inff(), l = 0.0f;
+    int unit = -200;                            // o counts 2^(unit - kRaise)
+    const float c = 1.4426950408889634f / sqrtf((float)D);
+
+    const int* table = a.c.table + (long long)p.b * a.c.P;
+    const int last_page = max(p.len - 1, 0) >> shift;
+    Window w;
+    auto refresh = [&](int base) {
+        w.base = base;
+        const int id = table[min(base + lane, last_page)];
+        const bool live = (unsigned)id < (unsigned)a.c.N;
+        w.id = live ? id : -1;
+        const long long at = (long long)(live ? id : 0) * a.c.Hkv + h;
+        const float ks = a.c.ks[at], vs = live ? a.c.vs[at] : 0.0f;
+        w.kc = live ? fmaxf(ks * c, 1e-37f) : 1.0f;     // (not 0: hidden scores are -inf)
+        const bool any = vs > 0.0f;
+        const float m = any ? __builtin_amdgcn_frexp_mantf(vs) : 1.0f;
+        w.lm = __builtin_amdgcn_logf(m);
+        w.im = __builtin_amdgcn_rcpf(m);
+        w.e = any ? __builtin_amdgcn_frexp_expf(vs) : kNone;
+    };
+    auto group_page = [&](int t, int g) { return min((kTile * t + 16 * g) >> shift, last_page) - w.base; };
+
+    // a thread's pieces of a tile: of K token tid / PR + (256 / PR) i, codes 16 (tid % PR) and on; of V
+    // dimension tid / 4 + 64 i, tokens 16 (tid % 4) and on
+    u32x4 kw[NL], vw[NL];
+    const int kr = tid / PR, kj = tid % PR, vd = tid >> 2, vg = tid & 3;
+    auto load = [&](int t) {
+        if (t >= tile1) return;
+        int id[4];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) id[g] = max(lane_of(w.id, group_page(t, g)), 0);
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+            const int r = kr + (256 / PR) * i, g = r >> 4;          // (g is the same for a wave)
+            const int pg = __builtin_amdgcn_readfirstlane(g == 0 ? id[0] : g == 1 ? id[1] : g == 2 ? id[2] : id[3]);
+            const uint8_t* base = (const uint8_t*)a.c.kc + (((long long)pg * a.c.Hkv + h) << shift) * D;
+            kw[i] = *reinterpret_cast<const u32x4*>(base + ((kTile * t + r) & (page - 1)) * D + 16 * kj);
+        }
+        const int pv = vg == 0 ? id[0] : vg == 1 ? id[1] : vg == 2 ? id[2] : id[3];
+        const uint8_t* base = (const uint8_t*)a.c.vc + (((long long)pv * a.c.Hkv + h) << shift) * D +
+                              ((kTile * t + 16 * vg) & (page - 1));
+#pragma unroll
+        for (int i = 0; i < NL; ++i) vw[i] = *reinterpret_cast<const u32x4*>(base + ((vd + 64 * i) << shift));
+    };
+    // registers to LDS as 16-bit values: tile t
+    auto stage = [&](int t) {
+        if (t >= tile1) return;
+        uint16_t *K = lK[t & 1], *V = lV[t & 1];
+        bool none = false;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) none |= lane_of(w.e, group_page(t, g)) == kNone;
+        // V's codes where the weights do not hold its scale, and stale ones that may be no numbers
+        if (none || (FMT == FMT_E4M3 && kTile * (t + 1) > p.len)) {
+            bool mine = false;
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+                if (vg == g) mine = lane_of(w.e, group_page(t, g)) == kNone;
+            const int keep = mine ? 0 : p.len - kTile * t - 16 * vg;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int k = min(max(keep - 4 * j, 0), 4);
+                const uint32_t mask = k == 4 ? ~0u : (1u << (8 * k)) - 1u;
+#pragma unroll
+                for (int i = 0; i < NL; ++i) vw[i][j] &= mask;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+            const int r = kr + (256 / PR) * i;
+            *reinterpret_cast<u32x4*>(K + r * D + 8 * swz_k<D>(r, 2 * kj)) = widen<DT, FMT>(kw[i][0], kw[i][1]);
+            *reinterpret_cast<u32x4*>(K + r * D + 8 * swz_k<D>(r, 2 * kj + 1)) = widen<DT, FMT>(kw[i][2], kw[i][3]);
+            const int d = vd + 64 * i;
+            *reinterpret_cast<u32x4*>(V + d * kTile + 8 * ((2 * vg) ^ (d & 7))) = widen<DT_F16, FMT>(vw[i][0], vw[i][1]);
+            *reinterpret_cast<u32x4*>(V + d * kTile + 8 * ((2 * vg + 1) ^ (d & 7))) = widen<DT_F16, FMT>(vw[i][2], vw[i][3]);
+        }
+    };
+    const int kn = (n & ~12) | ((n & 4) << 1) | ((n & 8) >> 1);        // the token that row n of an operand holds
+    auto scores = [&](int t, f32x16 (&S)[2]) {
+        const uint16_t* K = lK[t & 1];
+        int at = kn * D + 8 * swz_k<D>(kn, hf);
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) S[kb][e] = 0.0f;
+#pragma unroll
+            for (int s = 0; s < D / 16; ++s)
+                S[kb] = mfma<DT>(*reinterpret_cast<const u32x4*>(K + 32 * kb * D + (at ^ (16 * s))), qf[s], S[kb]);
+        }
+    };
+    auto softmax = [&](int t, f32x16 (&S)[2], u32x4 (&P)[4]) {
+        float kc[4], lv[4], inv[4];
+        int ge[4], top = kNone, dead = 0;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const int i = group_page(t, g);
+            kc[g] = lane_of(w.kc, i);
+            lv[g] = lane_of(w.lm, i);
+            inv[g] = lane_of(w.im, i);
+            ge[g] = lane_of(w.e, i);
+            if (kTile * t + 16 * g > most) ge[g] = kNone;       // (no row sees it)
+            if (lane_of(w.id, i) < 0) dead |= 1 << g;
+            top = max(top, ge[g]);
+        }
+        float f = 1.0f;
+        if (top > unit) {
+            f = __builtin_amdgcn_ldexpf(1.0f, unit - top);
+            unit = top;
+        }
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const int e = ge[g] == kNone ? 0 : max(ge[g] - unit, kDeepest) + kRaise;
+            lv[g] = ge[g] == kNone ? 0.0f : lv[g] + (float)e;
+            inv[g] = ge[g] == kNone ? 1.0f : __builtin_amdgcn_ldexpf(inv[g], -e);
+        }
+        const bool masked = t >= clear1 || dead;
+        if (masked) {
+            const int upto = seen - kTile * t - 8 * hf;
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (16 * g + e > upto || (dead >> g & 1)) S[g >> 1][8 * (g & 1) + e] = -__builtin_inff();
+        }
+        float mt = -__builtin_inff();
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            float mg = S[g >> 1][8 * (g & 1)];
+#pragma unroll
+            for (int e = 1; e < 8; ++e) mg = fmaxf(mg, S[g >> 1][8 * (g & 1) + e]);
+            mt = fmaxf(mt, mg * kc[g]);
+        }
+        if (masked) {
+            // (a scale of 0 makes no number of a hidden score; what is seen at all counts as kLowest)
+            bool any = false;
+#pragma unroll
+            for (int g = 0; g < 4; ++g) any |= !(dead >> g & 1) && 16 * g <= seen - kTile * t - 8 * hf;
+            mt = any ? fmaxf(mt, kLowest) : -__builtin_inff();
+        } else mt = fmaxf(mt, kLowest);
+        mt = max_halves(mt);
+        if (any_lane(mt > M + kLag)) {
+            const float Mn = fmaxf(M, mt), r = M == Mn ? 1.0f : exp2_raw(M - Mn);
+            M = Mn;
+            l *= r;
+            f *= r;
+        }
+        if (any_lane(f != 1.0f)) {
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[i][e] *= f;
+        }
+        const float base = M == -__builtin_inff() ? 0.0f : M;
+        // the multiply-add below is exact but for the rounding of base - lv; rows of scores so large that this
+        // would count have the maximum taken off first
+        float sub[4];
+        const bool big = fabsf(base) > 1048576.0f;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) sub[g] = big ? -lv[g] : base - lv[g];
+        if (any_lane(big)) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const float back = 1.0f / kc[g];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float x = S[g >> 1][8 * (g & 1) + e];
+                    if (big) S[g >> 1][8 * (g & 1) + e] = (x * kc[g] - base) * back;
+                }
+            }
+        }
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float p0 = exp2_raw(fmaf(S[g >> 1][8 * (g & 1) + 2 * j], kc[g], -sub[g]));
+                float p1 = exp2_raw(fmaf(S[g >> 1][8 * (g & 1) + 2 * j + 1], kc[g], -sub[g]));
+                sum += p0 + p1;
+                P[g][j] = pack2<DT_F16>(p0, p1);
+            }
+            l = fmaf(sum, inv[g], l);
+        }
+    };
+    auto values = [&](int t, const u32x4 (&P)[4]) {
+        const uint16_t* V = lV[t & 1];
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                const int d = 32 * i + n;
+                o[i] = mfma<DT_F16>(*reinterpret_cast<const u32x4*>(V + d * kTile + 8 * ((2 * g + hf) ^ (d & 7))), P[g], o[i]);
+            }
+    };
+
+    // In iteration t LDS holds tile t, the registers tile t + 1.
+    const int tile0 = p.tile0;
+    if (tile0 < tile1) {
+        refresh(min((kTile * tile0) >> shift, last_page));
+        load(tile0);
+        stage(tile0);
+        load(tile0 + 1);
+        for (int t = tile0; t < tile1; ++t) {
+            // tiles t .. t + 2 have to be in the window
+            if (min((kTile * (t + 3) - 1) >> shift, last_page) - w.base > 63) refresh((kTile * t) >> shift);
+            wait_lds();
+            __syncthreads();
+            f32x16 S[2];
+            u32x4 P[4];
+            const bool mine = t < own1;
+            if (mine) scores(t, S);
+            stage(t + 1);
+            load(t + 2);
+            if (mine) {
+                softmax(t, S, P);
+                values(t, P);
+            }
+        }
+    }
+
+    l = sum_halves(l);
+    const float u = __builtin_amdgcn_ldexpf(1.0f, unit - kRaise);
+    if (32 * wave + n >= rows) return;
+    if (p.parts == 1) {
+        const float inv = M == -__builtin_inff() ? 0.0f : u / l;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+                store_out<DT, D>(a, p, h, row, 32 * i + 8 * g + 4 * hf,
+                                 f32x4{o[i][4 * g], o[i][4 * g + 1], o[i][4 * g + 2], o[i][4 * g + 3]}, inv);
+    } else {
+        float* part = a.work + ((long long)(p.slot + p.part) * a.c.Hkv + h) * kPartFloats<kRows, D>;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+                *reinterpret_cast<f32x4*>(part + (32 * wave + n) * D + 32 * i + 8 * g + 4 * hf) =
+                    f32x4{o[i][4 * g], o[i][4 * g + 1], o[i][4 * g + 2], o[i][4 * g + 3]} * u;
+        if (hf == 0) {
+            part[kRows * D + 2 * (32 * wave + n)] = M;
+            part[kRows * D + 2 * (32 * wave + n) + 1] = l;
+        }
+    }
+}
+
+constexpr int kTargetBlocks = 512;      // chunks x kv heads aimed at
+constexpr int kWhole = 16;              // up to so many tiles a sequence is never split
+constexpr int kLeast = 8;               // tiles of a chunk of a longer one
+int chunks(long long Hkv) { return (int)((kTargetBlocks + Hkv - 1) / Hkv); }
+
+template <int DT, int FMT, int D>
+hipError_t chunk(const PagedView& a, long long row_tiles, hipStream_t st) {
+    const unsigned blocks = (unsigned)((row_tiles + (a.s.most ? 0 : a.s.W)) * a.c.Hkv);
+    hipLaunchKernelGGL((kv_paged_chunk_kernel<DT, FMT, D>), dim3(blocks), dim3(256), 0, st, a);
+    if (!a.s.most)
+        hipLaunchKernelGGL((kv_paged_join_kernel<DT, D, kRows>), dim3((unsigned)(a.s.W * a.c.Hkv)), dim3(256), 0, st, a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+long long kv_paged_chunk_floats(long long Hkv, long long D, long long tokens) {
+    return tokens <= kWhole * kTile ? 0 : 2LL * chunks(Hkv) * Hkv * kRows * (D + 2);
+}
+
+hipError_t launch_kv_paged_chunk(const PagedView& v, int dtype, hipStream_t st) {
+    PagedView a = v;
+    a.s.W = chunks(a.c.Hkv);
+    a.s.least = kLeast;
+    a.s.most = a.s.tokens <= kWhole * kTile ? kWhole : 0;
+    const long long row_tiles = (long long)a.c.T * a.s.G / kRows + a.c.B;
+#define W4A16_CHUNK_D(DT, FMT) (a.c.D == 64 ? chunk<DT, FMT, 64>(a, row_tiles, st) : chunk<DT, FMT, 128>(a, row_tiles, st))
+    if (dtype == DT_F16) return a.c.fmt == FMT_INT8 ? W4A16_CHUNK_D(DT_F16, FMT_INT8) : W4A16_CHUNK_D(DT_F16, FMT_E4M3);
+    return a.c.fmt == FMT_INT8 ? W4A16_CHUNK_D(DT_BF16, FMT_INT8) : W4A16_CHUNK_D(DT_BF16, FMT_E4M3);
+#undef W4A16_CHUNK_D
+}
+
+}  // namespace w4a16

@@ -1,0 +1,190 @@
+// What the attention kernels over the paged cache share: codes as matrix operands, and how the work of
+// sequences of any lengths, known on the device only, is cut into blocks of about equal work.
+#pragma once
+
+#include "pages.h"
+
+namespace w4a16 {
+
+constexpr int kTile = 64;               // cached tokens of a step
+
+// Eight codes (two words) as 16-bit floats, exact.  int8 to fp16: the byte + 128 under the exponent of 1024 is
+// 1152 + c, less 1152; to bf16 by way of fp32, whose upper half holds them.
+template <int DT, int FMT>
+__device__ __forceinline__ u32x4 widen(uint32_t w0, uint32_t w1) {
+    u32x4 r;
+    if constexpr (FMT == FMT_E4M3) {
+        if constexpr (DT == DT_F16) {
+            r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w0, 1.0f, false));
+            r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w0, 1.0f, true));
+            r[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w1, 1.0f, false));
+            r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w1, 1.0f, true));
+        } else {
+            r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, 1.0f, false));
+            r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, 1.0f, true));
+            r[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, 1.0f, false));
+            r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, 1.0f, true));
+        }
+    } else if constexpr (DT == DT_F16) {
+        const uint32_t w[2] = {w0 ^ 0x80808080u, w1 ^ 0x80808080u};
+        const f16x2 bias = {(_Float16)1152.0f, (_Float16)1152.0f};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t x = perm(0x64646464u, w[i >> 1], i & 1 ? 0x04030402u : 0x04010400u);
+            r[i] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, x) - bias);
+        }
+    } else {
+        const uint32_t w[2] = {w0, w1};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float lo = code_value<FMT>(w[i >> 1], 2 * (i & 1)), hi = code_value<FMT>(w[i >> 1], 2 * (i & 1) + 1);
+            r[i] = perm(__builtin_bit_cast(uint32_t, hi), __builtin_bit_cast(uint32_t, lo), 0x07060302u);
+        }
+    }
+    return r;
+}
+
+__device__ __forceinline__ bool any_lane(bool p) { return __builtin_amdgcn_ballot_w64(p) != 0; }
+__device__ __forceinline__ int lanes_sum(int v) {
+    v += __builtin_amdgcn_mov_dpp(v, 0xB1, 0xF, 0xF, true);      // quad_perm [1,0,3,2]
+    v += __builtin_amdgcn_mov_dpp(v, 0x4E, 0xF, 0xF, true);      // quad_perm [2,3,0,1]
+    v += __builtin_amdgcn_mov_dpp(v, 0x141, 0xF, 0xF, true);     // row_half_mirror
+    v += __builtin_amdgcn_mov_dpp(v, 0x140, 0xF, 0xF, true);     // row_mirror
+    return (__builtin_amdgcn_readlane(v, 0) + __builtin_amdgcn_readlane(v, 16)) +
+           (__builtin_amdgcn_readlane(v, 32) + __builtin_amdgcn_readlane(v, 48));
+}
+__device__ __forceinline__ int wave_scan(int v, int lane) {     // inclusive
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int o = __builtin_amdgcn_ds_bpermute(4 * (lane - d), v);
+        if (lane >= d) v += o;
+    }
+    return v;
+}
+
+// What a block works on: ROWS rows from `row0` of sequence b, its tiles [tile0, tile1), and where the outcome
+// goes: chunk `part` of `parts` in the workspace from `slot`, or straight out if there is one.
+struct Piece {
+    int b, first, n, len, row0, tile0, tile1, part, parts, slot;
+};
+struct Sched {
+    const int *lens, *cu;
+    int B, T, G, tokens;        // tokens: of a table
+    int W, least, most;         // W: chunks aimed at; least: their tiles; most: a chunk's tiles, if no split is wanted
+};
+// A sequence's length, first new token, their count, row tiles and key tiles.
+template <int ROWS>
+__device__ __forceinline__ void sequence(const Sched& s, int b, int& len, int& first, int& n, int& rts, int& tiles) {
+    len = first = n = rts = tiles = 0;
+    if (b >= s.B) return;
+    len = min(max(s.lens[b], 0), s.tokens);
+    if (s.cu) {
+        first = min(max(s.cu[b], 0), s.T);
+        n = min(max(s.cu[b + 1], first), s.T) - first;
+    } else {
+        first = b;
+        n = 1;
+    }
+    rts = (int)(((long long)n * s.G + ROWS - 1) / ROWS);
+    tiles = max((len + kTile - 1) / kTile, 1);
+}
+// Chunks are cut by the lengths: at most q tiles each, q so that about W chunks arise from all sequences'
+// tiles.  Block `index` of a kv head is the index-th chunk; the walk is over 64 sequences at a time.
+// MERGE: index counts the row tiles that were split (their chunks' outcomes are to be joined).
+template <int ROWS, bool MERGE>
+__device__ __forceinline__ bool find_piece(const Sched& s, int index, int lane, Piece& p) {
+    int len, first, n, rts, tiles;
+    int q = s.most;
+    if (q == 0) {
+        long long all = 0;
+        for (int b0 = 0; b0 < s.B; b0 += 64) {
+            sequence<ROWS>(s, b0 + lane, len, first, n, rts, tiles);
+            const long long work = (long long)rts * tiles;
+            all += lanes_sum((int)(work & 0xFFFF)) + ((long long)lanes_sum((int)(work >> 16)) << 16);
+        }
+        q = max(s.least, (int)min((all + s.W - 1) / s.W, (long long)1 << 30));
+    }
+    int before = 0, slots = 0;
+    for (int b0 = 0; b0 < s.B; b0 += 64) {
+        sequence<ROWS>(s, b0 + lane, len, first, n, rts, tiles);
+        const int parts = (tiles + q - 1) / q;
+        const int mine = MERGE ? (parts > 1 ? rts : 0) : rts * parts, room = parts > 1 ? rts * parts : 0;
+        const int upto = wave_scan(mine, lane), total = __builtin_amdgcn_readlane(upto, 63);
+        const int sl = wave_scan(room, lane);
+        if (index < before + total) {
+            const unsigned long long m = __builtin_amdgcn_ballot_w64(before + upto > index);
+            const int l = __builtin_ctzll(m);
+            const auto at = [&](int v) { return __builtin_amdgcn_readlane(v, l); };
+            p.b = b0 + l;
+            p.first = at(first);
+            p.n = at(n);
+            p.len = at(len);
+            p.parts = at(parts);
+            const int k = index - before - (at(upto) - at(mine));
+            const int rt = MERGE ? k : k / p.parts;
+            p.part = MERGE ? 0 : k - rt * p.parts;
+            p.row0 = rt * ROWS;
+            const int t = at(tiles);
+            p.tile0 = (int)((long long)t * p.part / p.parts);
+            p.tile1 = (int)((long long)t * (p.part + 1) / p.parts);
+            p.slot = slots + at(sl) - at(room) + rt * p.parts;
+            return true;
+        }
+        before += total;
+        slots += __builtin_amdgcn_readlane(sl, 63);
+    }
+    return false;
+}
+
+struct PagedView {
+    KvPages c;
+    Sched s;
+    const uint16_t* q;
+    uint16_t* out;
+    float* work;
+    int qs, Hq, shift;
+};
+// A chunk's outcome in the workspace: ROWS rows of D sums, then (maximum, sum of weights) of each row.
+template <int ROWS, int D>
+constexpr int kPartFloats = ROWS * (D + 2);
+
+
+// Four values of row `row` of a piece, from dimension d on, times inv.
+template <int DT, int D>
+__device__ __forceinline__ void store_out(const PagedView& a, const Piece& p, int h, int row, int d, const f32x4& o,
+                                          float inv) {
+    const int token = row / a.s.G, head = h * a.s.G + row % a.s.G;
+    uint16_t* at = a.out + ((long long)(p.first + token) * a.Hq + head) * D + d;
+    *reinterpret_cast<u32x2*>(at) = u32x2{pack2<DT>(o[0] * inv, o[1] * inv), pack2<DT>(o[2] * inv, o[3] * inv)};
+}
+
+// Joins the chunks of row tiles that were split: a thread four values of a row.
+template <int DT, int D, int ROWS>
+__global__ __launch_bounds__(256) void kv_paged_join_kernel(PagedView a) {
+    const int tid = threadIdx.x, lane = tid & 63, h = blockIdx.x % a.c.Hkv;
+    Piece p;
+    if (!find_piece<ROWS, true>(a.s, blockIdx.x / a.c.Hkv, lane, p)) return;
+    const int rows = min(ROWS, p.n * a.s.G - p.row0);
+    const long long step = (long long)a.c.Hkv * kPartFloats<ROWS, D>;
+    const float* part = a.work + ((long long)p.slot * a.c.Hkv + h) * kPartFloats<ROWS, D>;
+    for (int u = tid; u < rows * (D / 4); u += 256) {
+        const int r = u / (D / 4), d = u % (D / 4);
+        const float* stat = part + ROWS * D + 2 * r;
+        float Mt = -__builtin_inff();
+        for (int i = 0; i < p.parts; ++i) Mt = fmaxf(Mt, stat[i * step]);
+        float lt = 0.0f;
+        f32x4 s = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int i = 0; i < p.parts; ++i) {
+            const float m = stat[i * step], f = m == -__builtin_inff() ? 0.0f : exp2_raw(m - Mt);
+            lt += stat[i * step + 1] * f;
+            s += *reinterpret_cast<const f32x4*>(part + i * step + r * D + 4 * d) * f;
+        }
+        store_out<DT, D>(a, p, h, p.row0 + r, 4 * d, s, Mt == -__builtin_inff() ? 0.0f : 1.0f / lt);
+    }
+}
+
+// Many rows a sequence (kv_paged_chunk.hip); the caller fills all of the view but how chunks are cut.
+hipError_t launch_kv_paged_chunk(const PagedView& v, int dtype, hipStream_t st);
+long long kv_paged_chunk_floats(long long Hkv, long long D, long long tokens);
+
+}  // namespace w4a16
