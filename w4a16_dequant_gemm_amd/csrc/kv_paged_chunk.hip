@@ -44,10 +44,17 @@ __device__ __forceinline__ float lane_of(float v, int l) {
 }
 __device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
-template <int DT, int FMT, int D>
+// In iteration t the scores of tile t are computed beside the widening of K(t + 1) and V(t + 1), whose codes were
+// asked for an iteration before, and its softmax beside the second product of tile t - 1; one barrier an
+// iteration.  (The scores of tile t + 1 beside the softmax of tile t, as in attention.hip, need 32 registers
+// more than there are with the codes on their way.)
+//
+// ONE: pages of at least a tile, so that its four groups are of one page.
+template <int DT, int FMT, int D, bool ONE>
 __global__ __launch_bounds__(256, 2) void kv_paged_chunk_kernel(PagedView a) {
     constexpr int TILE = kTile * D, PR = D / 16, NL = kTile * PR / 256;   // 16-code pieces of a K row; loads of a thread
-    __shared__ __attribute__((aligned(16))) uint16_t lK[2][TILE], lV[2][TILE];
+    constexpr int NG = ONE ? 1 : 4;
+    __shared__ __attribute__((aligned(16))) uint16_t lK[2 * TILE], lV[3 * TILE];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int n = lane & 31, hf = lane >> 5;
     const int h = blockIdx.x % a.c.Hkv;
@@ -60,6 +67,7 @@ __global__ __launch_bounds__(256, 2) void kv_paged_chunk_kernel(PagedView a) {
     const int seen = past + row / G;
     const int most = past + (p.row0 + rows - 1) / G;                            // of the block
     const bool idle = 32 * wave >= rows;
+    const int tile0 = p.tile0;
     const int tile1 = min(p.tile1, most >= 0 ? most / kTile + 1 : 0);           // the block's tiles: [tile0, tile1)
     const int first = past + min(wrow, p.row0 + rows - 1) / G, last = past + min(wrow + 31, p.row0 + rows - 1) / G;
     const int own1 = idle || last < 0 ? 0 : min(tile1, last / kTile + 1);       // the wave's tiles end there,
@@ -97,38 +105,41 @@ __global__ __launch_bounds__(256, 2) void kv_paged_chunk_kernel(PagedView a) {
         w.im = __builtin_amdgcn_rcpf(m);
         w.e = any ? __builtin_amdgcn_frexp_expf(vs) : kNone;
     };
+    // (tiles behind the last are taken for it: they are loaded, but nothing of them is used)
     auto group_page = [&](int t, int g) { return min((kTile * t + 16 * g) >> shift, last_page) - w.base; };
 
     // a thread's pieces of a tile: of K token tid / PR + (256 / PR) i, codes 16 (tid % PR) and on; of V
     // dimension tid / 4 + 64 i, tokens 16 (tid % 4) and on
     u32x4 kw[NL], vw[NL];
     const int kr = tid / PR, kj = tid % PR, vd = tid >> 2, vg = tid & 3;
-    auto load = [&](int t) {
-        if (t >= tile1) return;
-        int id[4];
+    // where tile t's pieces lie, and their loads
+    const uint8_t *kat[NL], *vat;
+    auto locate = [&](int t) {
+        t = min(t, tile1 - 1);
+        int id[NG];
 #pragma unroll
-        for (int g = 0; g < 4; ++g) id[g] = max(lane_of(w.id, group_page(t, g)), 0);
+        for (int g = 0; g < NG; ++g) id[g] = max(lane_of(w.id, group_page(t, g)), 0);
 #pragma unroll
         for (int i = 0; i < NL; ++i) {
             const int r = kr + (256 / PR) * i, g = r >> 4;          // (g is the same for a wave)
-            const int pg = __builtin_amdgcn_readfirstlane(g == 0 ? id[0] : g == 1 ? id[1] : g == 2 ? id[2] : id[3]);
+            int pg = id[0];
+            if constexpr (!ONE) pg = __builtin_amdgcn_readfirstlane(g == 0 ? id[0] : g == 1 ? id[1] : g == 2 ? id[2] : id[3]);
             const uint8_t* base = (const uint8_t*)a.c.kc + (((long long)pg * a.c.Hkv + h) << shift) * D;
-            kw[i] = *reinterpret_cast<const u32x4*>(base + ((kTile * t + r) & (page - 1)) * D + 16 * kj);
+            kat[i] = base + ((kTile * t + r) & (page - 1)) * D + 16 * kj;
         }
-        const int pv = vg == 0 ? id[0] : vg == 1 ? id[1] : vg == 2 ? id[2] : id[3];
-        const uint8_t* base = (const uint8_t*)a.c.vc + (((long long)pv * a.c.Hkv + h) << shift) * D +
-                              ((kTile * t + 16 * vg) & (page - 1));
-#pragma unroll
-        for (int i = 0; i < NL; ++i) vw[i] = *reinterpret_cast<const u32x4*>(base + ((vd + 64 * i) << shift));
+        int pv = id[0];
+        if constexpr (!ONE) pv = vg == 0 ? id[0] : vg == 1 ? id[1] : vg == 2 ? id[2] : id[3];
+        vat = (const uint8_t*)a.c.vc + (((long long)pv * a.c.Hkv + h) << shift) * D + ((kTile * t + 16 * vg) & (page - 1)) +
+              (vd << shift);
     };
-    // registers to LDS as 16-bit values: tile t
-    auto stage = [&](int t) {
-        if (t >= tile1) return;
-        uint16_t *K = lK[t & 1], *V = lV[t & 1];
+    auto load_k = [&](int i) { kw[i] = *reinterpret_cast<const u32x4*>(kat[i]); };
+    auto load_v = [&](int i) { vw[i] = *reinterpret_cast<const u32x4*>(vat + ((64 * i) << shift)); };
+    // V's codes where the weights do not hold its scale, and stale ones that may be no numbers, become 0
+    auto clean_v = [&](int t) {
+        t = min(t, tile1 - 1);
         bool none = false;
 #pragma unroll
-        for (int g = 0; g < 4; ++g) none |= lane_of(w.e, group_page(t, g)) == kNone;
-        // V's codes where the weights do not hold its scale, and stale ones that may be no numbers
+        for (int g = 0; g < NG; ++g) none |= lane_of(w.e, group_page(t, g)) == kNone;
         if (none || (FMT == FMT_E4M3 && kTile * (t + 1) > p.len)) {
             bool mine = false;
 #pragma unroll
@@ -143,40 +154,78 @@ __global__ __launch_bounds__(256, 2) void kv_paged_chunk_kernel(PagedView a) {
                 for (int i = 0; i < NL; ++i) vw[i][j] &= mask;
             }
         }
-#pragma unroll
-        for (int i = 0; i < NL; ++i) {
-            const int r = kr + (256 / PR) * i;
-            *reinterpret_cast<u32x4*>(K + r * D + 8 * swz_k<D>(r, 2 * kj)) = widen<DT, FMT>(kw[i][0], kw[i][1]);
-            *reinterpret_cast<u32x4*>(K + r * D + 8 * swz_k<D>(r, 2 * kj + 1)) = widen<DT, FMT>(kw[i][2], kw[i][3]);
-            const int d = vd + 64 * i;
-            *reinterpret_cast<u32x4*>(V + d * kTile + 8 * ((2 * vg) ^ (d & 7))) = widen<DT_F16, FMT>(vw[i][0], vw[i][1]);
-            *reinterpret_cast<u32x4*>(V + d * kTile + 8 * ((2 * vg + 1) ^ (d & 7))) = widen<DT_F16, FMT>(vw[i][2], vw[i][3]);
-        }
+    };
+    // half `part` of piece i: registers to LDS as 16-bit values
+    auto put_k = [&](uint16_t* K, int i, int part) {
+        const int r = kr + (256 / PR) * i;
+        // (not to be widened, and held, before it is needed)
+        asm volatile("" : "+v"(kw[i][2 * part]), "+v"(kw[i][2 * part + 1]));
+        *reinterpret_cast<u32x4*>(K + r * D + 8 * swz_k<D>(r, 2 * kj + part)) =
+            widen<DT, FMT>(kw[i][2 * part], kw[i][2 * part + 1]);
+    };
+    auto put_v = [&](uint16_t* V, int i, int part) {
+        const int d = vd + 64 * i;
+        asm volatile("" : "+v"(vw[i][2 * part]), "+v"(vw[i][2 * part + 1]));
+        *reinterpret_cast<u32x4*>(V + d * kTile + 8 * swz_k<64>(d, 2 * vg + part)) =
+            widen<DT_F16, FMT>(vw[i][2 * part], vw[i][2 * part + 1]);
     };
     const int kn = (n & ~12) | ((n & 4) << 1) | ((n & 8) >> 1);        // the token that row n of an operand holds
-    auto scores = [&](int t, f32x16 (&S)[2]) {
-        const uint16_t* K = lK[t & 1];
+    auto key_piece = [&](const uint16_t* K, int kb, int s) {
         int at = kn * D + 8 * swz_k<D>(kn, hf);
+        asm("" : "+v"(at));
+        return *reinterpret_cast<const u32x4*>(K + 32 * kb * D + (at ^ (16 * s)));
+    };
+    auto value_piece = [&](const uint16_t* V, int g, int i) {
+        int at = n * kTile + 8 * swz_k<64>(n, hf);
+        asm("" : "+v"(at));
+        return *reinterpret_cast<const u32x4*>(V + 32 * i * kTile + (at ^ (16 * g)));
+    };
+    // the scores of a tile, half a piece of the next codes to LDS beside the two products of a k-step
+    auto scores_and_stage = [&](const uint16_t* K, f32x16 (&S)[2], uint16_t* Kn, uint16_t* Vn) {
+        constexpr int KS = D / 16;
+        static_assert(KS == 4 * NL, "half a piece a k-step");
+        u32x4 a0 = key_piece(K, 0, 0), a1 = key_piece(K, 1, 0);
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
+        for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
             for (int e = 0; e < 16; ++e) S[kb][e] = 0.0f;
 #pragma unroll
-            for (int s = 0; s < D / 16; ++s)
-                S[kb] = mfma<DT>(*reinterpret_cast<const u32x4*>(K + 32 * kb * D + (at ^ (16 * s))), qf[s], S[kb]);
+        for (int s = 0; s < KS; ++s) {
+            u32x4 n0 = a0, n1 = a1;
+            if (s + 1 < KS) {
+                n0 = key_piece(K, 0, s + 1);
+                n1 = key_piece(K, 1, s + 1);
+            }
+            S[0] = mfma<DT>(a0, qf[s], S[0]);
+            S[1] = mfma<DT>(a1, qf[s], S[1]);
+            if (s & 2) put_v(Vn, s >> 2, s & 1);
+            else put_k(Kn, s >> 2, s & 1);
+            // the registers of a whole piece take the tile after the next
+            if ((s & 3) == 1) load_k(s >> 2);
+            if ((s & 3) == 3) load_v(s >> 2);
+            __builtin_amdgcn_sched_barrier(0);
+            a0 = n0;
+            a1 = n1;
         }
     };
-    auto softmax = [&](int t, f32x16 (&S)[2], u32x4 (&P)[4]) {
-        float kc[4], lv[4], inv[4];
-        int ge[4], top = kNone, dead = 0;
+    // the weights of the tile before, whose second product is still to come: none at first
+    u32x4 P[4];
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
+    for (int g = 0; g < 4; ++g) P[g] = u32x4{0, 0, 0, 0};
+    // masks, the running maximum and what the weights of tile t need; where the maximum or the unit rises, o, l and
+    // P are rescaled.  The maximum is held rounded up to a whole number, so that this is by powers of two and exact
+    float kc[NG], sub[NG], inv[NG];
+    auto prepare = [&](int t, f32x16 (&S)[2]) {
+        float lv[NG];
+        int ge[NG], top = kNone, dead = 0;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
             const int i = group_page(t, g);
             kc[g] = lane_of(w.kc, i);
             lv[g] = lane_of(w.lm, i);
             inv[g] = lane_of(w.im, i);
             ge[g] = lane_of(w.e, i);
-            if (kTile * t + 16 * g > most) ge[g] = kNone;       // (no row sees it)
+            if (!ONE && kTile * t + 16 * g > most) ge[g] = kNone;       // (no row sees it)
             if (lane_of(w.id, i) < 0) dead |= 1 << g;
             top = max(top, ge[g]);
         }
@@ -186,7 +235,7 @@ __global__ __launch_bounds__(256, 2) void kv_paged_chunk_kernel(PagedView a) {
             unit = top;
         }
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
+        for (int g = 0; g < NG; ++g) {
             const int e = ge[g] == kNone ? 0 : max(ge[g] - unit, kDeepest) + kRaise;
             lv[g] = ge[g] == kNone ? 0.0f : lv[g] + (float)e;
             inv[g] = ge[g] == kNone ? 1.0f : __builtin_amdgcn_ldexpf(inv[g], -e);
@@ -198,7 +247,7 @@ __global__ __launch_bounds__(256, 2) void kv_paged_chunk_kernel(PagedView a) {
             for (int g = 0; g < 4; ++g)
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    if (16 * g + e > upto || (dead >> g & 1)) S[g >> 1][8 * (g & 1) + e] = -__builtin_inff();
+                    if (16 * g + e > upto || (dead >> (ONE ? 0 : g) & 1)) S[g >> 1][8 * (g & 1) + e] = -__builtin_inff();
         }
         float mt = -__builtin_inff();
 #pragma unroll
@@ -206,18 +255,19 @@ __global__ __launch_bounds__(256, 2) void kv_paged_chunk_kernel(PagedView a) {
             float mg = S[g >> 1][8 * (g & 1)];
 #pragma unroll
             for (int e = 1; e < 8; ++e) mg = fmaxf(mg, S[g >> 1][8 * (g & 1) + e]);
-            mt = fmaxf(mt, mg * kc[g]);
+            mt = fmaxf(mt, ONE ? mg : mg * kc[ONE ? 0 : g]);
         }
+        if (ONE) mt *= kc[0];
+        // what is seen at all counts as kLowest
         if (masked) {
-            // (a scale of 0 makes no number of a hidden score; what is seen at all counts as kLowest)
             bool any = false;
 #pragma unroll
-            for (int g = 0; g < 4; ++g) any |= !(dead >> g & 1) && 16 * g <= seen - kTile * t - 8 * hf;
+            for (int g = 0; g < 4; ++g) any |= !(dead >> (ONE ? 0 : g) & 1) && 16 * g <= seen - kTile * t - 8 * hf;
             mt = any ? fmaxf(mt, kLowest) : -__builtin_inff();
         } else mt = fmaxf(mt, kLowest);
         mt = max_halves(mt);
         if (any_lane(mt > M + kLag)) {
-            const float Mn = fmaxf(M, mt), r = M == Mn ? 1.0f : exp2_raw(M - Mn);
+            const float Mn = __builtin_ceilf(fmaxf(M, mt)), r = M == Mn ? 1.0f : exp2_raw(M - Mn);
             M = Mn;
             l *= r;
             f *= r;
@@ -227,71 +277,127 @@ __global__ __launch_bounds__(256, 2) void kv_paged_chunk_kernel(PagedView a) {
             for (int i = 0; i < D / 32; ++i)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) o[i][e] *= f;
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    P[g][j] = pack2<DT_F16>(h2f((uint16_t)P[g][j]) * f, h2f((uint16_t)(P[g][j] >> 16)) * f);
         }
         const float base = M == -__builtin_inff() ? 0.0f : M;
-        // the multiply-add below is exact but for the rounding of base - lv; rows of scores so large that this
-        // would count have the maximum taken off first
-        float sub[4];
+        // the multiply-add of the weights is exact but for the rounding of base - lv; rows of scores so large that
+        // this would count have the maximum taken off first
         const bool big = fabsf(base) > 1048576.0f;
 #pragma unroll
-        for (int g = 0; g < 4; ++g) sub[g] = big ? -lv[g] : base - lv[g];
+        for (int g = 0; g < NG; ++g) sub[g] = big ? -lv[g] : base - lv[g];
         if (any_lane(big)) {
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-                const float back = 1.0f / kc[g];
+                const float k = kc[ONE ? 0 : g], back = 1.0f / k;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const float x = S[g >> 1][8 * (g & 1) + e];
-                    if (big) S[g >> 1][8 * (g & 1) + e] = (x * kc[g] - base) * back;
+                    if (big) S[g >> 1][8 * (g & 1) + e] = (x * k - base) * back;
                 }
             }
         }
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            float sum = 0.0f;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float p0 = exp2_raw(fmaf(S[g >> 1][8 * (g & 1) + 2 * j], kc[g], -sub[g]));
-                float p1 = exp2_raw(fmaf(S[g >> 1][8 * (g & 1) + 2 * j + 1], kc[g], -sub[g]));
-                sum += p0 + p1;
-                P[g][j] = pack2<DT_F16>(p0, p1);
-            }
-            l = fmaf(sum, inv[g], l);
+    };
+    float sum = 0.0f;                           // of the weights of a group (ONE: of a tile)
+    auto weight_pair = [&](const f32x16 (&S)[2], int pr) {
+        const int g = pr >> 2, j = pr & 3, gg = ONE ? 0 : g;
+        const float p0 = exp2_raw(fmaf(S[g >> 1][8 * (g & 1) + 2 * j], kc[gg], -sub[gg]));
+        const float p1 = exp2_raw(fmaf(S[g >> 1][8 * (g & 1) + 2 * j + 1], kc[gg], -sub[gg]));
+        sum += p0 + p1;
+        P[g][j] = pack2<DT_F16>(p0, p1);
+        if (ONE ? pr == 15 : j == 3) {
+            l = fmaf(sum, inv[gg], l);
+            sum = 0.0f;
         }
     };
-    auto values = [&](int t, const u32x4 (&P)[4]) {
-        const uint16_t* V = lV[t & 1];
+    // the second product of tile t - 1
+    auto values = [&](const uint16_t* V) {
 #pragma unroll
         for (int g = 0; g < 4; ++g)
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-                const int d = 32 * i + n;
-                o[i] = mfma<DT_F16>(*reinterpret_cast<const u32x4*>(V + d * kTile + 8 * ((2 * g + hf) ^ (d & 7))), P[g], o[i]);
-            }
+            for (int i = 0; i < D / 32; ++i) o[i] = mfma<DT_F16>(value_piece(V, g, i), P[g], o[i]);
     };
-
-    // In iteration t LDS holds tile t, the registers tile t + 1.
-    const int tile0 = p.tile0;
+    // ... with the weights of tile t beside it, a group's in place of those of the group that has gone in before
+    auto values_and_weights = [&](const uint16_t* V, const f32x16 (&S)[2]) {
+        constexpr int DB = D / 32, STEPS = 4 * DB, PW = 16 / STEPS;
+        u32x4 a0 = value_piece(V, 0, 0);
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) {
+            u32x4 n0 = a0;
+            if (s + 1 < STEPS) n0 = value_piece(V, (s + 1) / DB, (s + 1) % DB);
+            o[s % DB] = mfma<DT_F16>(a0, P[s / DB], o[s % DB]);
+            if (s >= DB)
+#pragma unroll
+                for (int i = 0; i < PW; ++i) weight_pair(S, PW * (s - DB) + i);
+            __builtin_amdgcn_sched_barrier(0);
+            a0 = n0;
+        }
+#pragma unroll
+        for (int pr = 12; pr < 16; ++pr) weight_pair(S, pr);
+    };
+    auto stage = [&](uint16_t* Kn, uint16_t* Vn) {
+#pragma unroll
+        for (int i = 0; i < NL; ++i)
+#pragma unroll
+            for (int part = 0; part < 2; ++part) {
+                put_k(Kn, i, part);
+                put_v(Vn, i, part);
+            }
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+            load_k(i);
+            load_v(i);
+        }
+    };
     if (tile0 < tile1) {
         refresh(min((kTile * tile0) >> shift, last_page));
-        load(tile0);
-        stage(tile0);
-        load(tile0 + 1);
-        for (int t = tile0; t < tile1; ++t) {
+        locate(tile0);
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+            load_k(i);
+            load_v(i);
+        }
+        // (what the weights of no tile are multiplied with has to be numbers)
+        for (int i = tid; i < TILE / 8; i += 256) *reinterpret_cast<u32x4*>(lV + 2 * TILE + 8 * i) = u32x4{0, 0, 0, 0};
+        clean_v(tile0);
+        locate(tile0 + 1);
+        stage(lK, lV);
+        int kc_at = 0, vp_at = 2 * TILE, vc_at = 0;     // where K(t), V(t - 1) and V(t) are
+        // the top of iteration t: K(t) and V(t) are in LDS, K(t - 1) and V(t - 2) have been read
+        auto top = [&](int t) {
             // tiles t .. t + 2 have to be in the window
             if (min((kTile * (t + 3) - 1) >> shift, last_page) - w.base > 63) refresh((kTile * t) >> shift);
             wait_lds();
             __syncthreads();
+            clean_v(t + 1);
+            locate(t + 2);
+        };
+        auto turn = [&] {
+            const int vn = 3 * TILE - vp_at - vc_at;
+            vp_at = vc_at;
+            vc_at = vn;
+            kc_at = TILE - kc_at;
+        };
+        int t = tile0;
+#pragma unroll 1
+        for (; t < own1; ++t) {
+            top(t);
             f32x16 S[2];
-            u32x4 P[4];
-            const bool mine = t < own1;
-            if (mine) scores(t, S);
-            stage(t + 1);
-            load(t + 2);
-            if (mine) {
-                softmax(t, S, P);
-                values(t, P);
-            }
+            scores_and_stage(lK + kc_at, S, lK + (TILE - kc_at), lV + (3 * TILE - vp_at - vc_at));
+            prepare(t, S);
+            values_and_weights(lV + vp_at, S);
+            turn();
+        }
+        if (t > tile0) values(lV + vp_at);
+        // tiles that only other waves' rows see
+#pragma unroll 1
+        for (; t < tile1; ++t) {
+            top(t);
+            stage(lK + (TILE - kc_at), lV + (3 * TILE - vp_at - vc_at));
+            turn();
         }
     }
 
@@ -326,10 +432,10 @@ constexpr int kWhole = 16;              // up to so many tiles a sequence is nev
 constexpr int kLeast = 8;               // tiles of a chunk of a longer one
 int chunks(long long Hkv) { return (int)((kTargetBlocks + Hkv - 1) / Hkv); }
 
-template <int DT, int FMT, int D>
+template <int DT, int FMT, int D, bool ONE>
 hipError_t chunk(const PagedView& a, long long row_tiles, hipStream_t st) {
     const unsigned blocks = (unsigned)((row_tiles + (a.s.most ? 0 : a.s.W)) * a.c.Hkv);
-    hipLaunchKernelGGL((kv_paged_chunk_kernel<DT, FMT, D>), dim3(blocks), dim3(256), 0, st, a);
+    hipLaunchKernelGGL((kv_paged_chunk_kernel<DT, FMT, D, ONE>), dim3(blocks), dim3(256), 0, st, a);
     if (!a.s.most)
         hipLaunchKernelGGL((kv_paged_join_kernel<DT, D, kRows>), dim3((unsigned)(a.s.W * a.c.Hkv)), dim3(256), 0, st, a);
     return hipGetLastError();
@@ -347,10 +453,13 @@ hipError_t launch_kv_paged_chunk(const PagedView& v, int dtype, hipStream_t st) 
     a.s.least = kLeast;
     a.s.most = a.s.tokens <= kWhole * kTile ? kWhole : 0;
     const long long row_tiles = (long long)a.c.T * a.s.G / kRows + a.c.B;
-#define W4A16_CHUNK_D(DT, FMT) (a.c.D == 64 ? chunk<DT, FMT, 64>(a, row_tiles, st) : chunk<DT, FMT, 128>(a, row_tiles, st))
+    const bool one = a.c.page >= kTile;
+#define W4A16_CHUNK(DT, FMT, D) (one ? chunk<DT, FMT, D, true>(a, row_tiles, st) : chunk<DT, FMT, D, false>(a, row_tiles, st))
+#define W4A16_CHUNK_D(DT, FMT) (a.c.D == 64 ? W4A16_CHUNK(DT, FMT, 64) : W4A16_CHUNK(DT, FMT, 128))
     if (dtype == DT_F16) return a.c.fmt == FMT_INT8 ? W4A16_CHUNK_D(DT_F16, FMT_INT8) : W4A16_CHUNK_D(DT_F16, FMT_E4M3);
     return a.c.fmt == FMT_INT8 ? W4A16_CHUNK_D(DT_BF16, FMT_INT8) : W4A16_CHUNK_D(DT_BF16, FMT_E4M3);
 #undef W4A16_CHUNK_D
+#undef W4A16_CHUNK
 }
 
 }  // namespace w4a16
