@@ -180,32 +180,36 @@ __global__ __launch_bounds__(256, 2) void kv_paged_chunk_kernel(PagedView a) {
         asm("" : "+v"(at));
         return *reinterpret_cast<const u32x4*>(V + 32 * i * kTile + (at ^ (16 * g)));
     };
-    // the scores of a tile, half a piece of the next codes to LDS beside the two products of a k-step
+    // the scores of a tile, half a piece of the next codes to LDS beside the two products of a k-step; K's operands are
+    // read kAhead steps early
     auto scores_and_stage = [&](const uint16_t* K, f32x16 (&S)[2], uint16_t* Kn, uint16_t* Vn) {
-        constexpr int KS = D / 16;
+        constexpr int KS = D / 16, kAhead = 2;
         static_assert(KS == 4 * NL, "half a piece a k-step");
-        u32x4 a0 = key_piece(K, 0, 0), a1 = key_piece(K, 1, 0);
+        u32x4 k[kAhead][2];
+#pragma unroll
+        for (int s = 0; s < kAhead; ++s) {
+            k[s][0] = key_piece(K, 0, s);
+            k[s][1] = key_piece(K, 1, s);
+        }
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
             for (int e = 0; e < 16; ++e) S[kb][e] = 0.0f;
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
-            u32x4 n0 = a0, n1 = a1;
-            if (s + 1 < KS) {
-                n0 = key_piece(K, 0, s + 1);
-                n1 = key_piece(K, 1, s + 1);
-            }
+            const u32x4 a0 = k[s % kAhead][0], a1 = k[s % kAhead][1];
             S[0] = mfma<DT>(a0, qf[s], S[0]);
             S[1] = mfma<DT>(a1, qf[s], S[1]);
+            if (s + kAhead < KS) {
+                k[s % kAhead][0] = key_piece(K, 0, s + kAhead);
+                k[s % kAhead][1] = key_piece(K, 1, s + kAhead);
+            }
             if (s & 2) put_v(Vn, s >> 2, s & 1);
             else put_k(Kn, s >> 2, s & 1);
             // the registers of a whole piece take the tile after the next
             if ((s & 3) == 1) load_k(s >> 2);
             if ((s & 3) == 3) load_v(s >> 2);
             __builtin_amdgcn_sched_barrier(0);
-            a0 = n0;
-            a1 = n1;
         }
     };
     // the weights of the tile before, whose second product is still to come: none at first
@@ -320,20 +324,24 @@ __global__ __launch_bounds__(256, 2) void kv_paged_chunk_kernel(PagedView a) {
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) o[i] = mfma<DT_F16>(value_piece(V, g, i), P[g], o[i]);
     };
-    // ... with the weights of tile t beside it, a group's in place of those of the group that has gone in before
+    // ... with the weights of tile t beside it, a group's in place of those of the group that has gone in before; the
+    // first kEarly operands are read by the caller, the others as many products early
+    constexpr int kEarly = 4;
+    u32x4 v[kEarly];
+    auto first_values = [&](const uint16_t* V) {
+#pragma unroll
+        for (int s = 0; s < kEarly; ++s) v[s] = value_piece(V, s / (D / 32), s % (D / 32));
+    };
     auto values_and_weights = [&](const uint16_t* V, const f32x16 (&S)[2]) {
         constexpr int DB = D / 32, STEPS = 4 * DB, PW = 16 / STEPS;
-        u32x4 a0 = value_piece(V, 0, 0);
 #pragma unroll
         for (int s = 0; s < STEPS; ++s) {
-            u32x4 n0 = a0;
-            if (s + 1 < STEPS) n0 = value_piece(V, (s + 1) / DB, (s + 1) % DB);
-            o[s % DB] = mfma<DT_F16>(a0, P[s / DB], o[s % DB]);
+            o[s % DB] = mfma<DT_F16>(v[s % kEarly], P[s / DB], o[s % DB]);
+            if (s + kEarly < STEPS) v[s % kEarly] = value_piece(V, (s + kEarly) / DB, (s + kEarly) % DB);
             if (s >= DB)
 #pragma unroll
                 for (int i = 0; i < PW; ++i) weight_pair(S, PW * (s - DB) + i);
             __builtin_amdgcn_sched_barrier(0);
-            a0 = n0;
         }
 #pragma unroll
         for (int pr = 12; pr < 16; ++pr) weight_pair(S, pr);
@@ -387,6 +395,7 @@ __global__ __launch_bounds__(256, 2) void kv_paged_chunk_kernel(PagedView a) {
             top(t);
             f32x16 S[2];
             scores_and_stage(lK + kc_at, S, lK + (TILE - kc_at), lV + (3 * TILE - vp_at - vc_at));
+            first_values(lV + vp_at);
             prepare(t, S);
             values_and_weights(lV + vp_at, S);
             turn();
