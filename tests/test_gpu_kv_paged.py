@@ -259,6 +259,20 @@ def test_chunks_long(codes):
     attend([2500, 40, 1200], [20, 40, 3], 4, 2, 128, 64, codes, torch.bfloat16, 11)
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("codes", CODES, ids=ids)
+@pytest.mark.parametrize("page", [16, 64, 128])
+def test_chunks_of_many_rows(page, codes, dtype):
+    """Hundreds of rows a sequence (256 to a block), split over blocks, beside a short, an empty and one with more
+    rows than tokens; pages that are none and of scale 0 in between."""
+    def change(pool):
+        pool.table[0, 2] = -1
+        pool.table[0, 600 // page] = 1 << 30
+        pool.vs[pool.table[1, 1]] = 0.0
+        pool.ks[pool.table[1, 3]] = 0.0
+    attend([2100, 1200, 30, 0], [301, 220, 33, 0], 4, 1, 128, page, codes, dtype, 13 + page, change=change)
+
+
 @pytest.mark.parametrize("codes", CODES, ids=ids)
 @pytest.mark.parametrize("decode", [True, False])
 def test_entries_that_are_no_pages(codes, decode):

@@ -215,8 +215,10 @@ template <int DT, int FMT, int D>
 hipError_t paged(const PagedView& a, long long row_tiles, hipStream_t st) {
     const unsigned blocks = (unsigned)((row_tiles + (a.s.most ? 0 : a.s.W)) * a.c.Hkv);
     hipLaunchKernelGGL((kv_paged_kernel<DT, FMT, D>), dim3(blocks), dim3(64 * kWaves), 0, st, a);
-    if (!a.s.most)
-        hipLaunchKernelGGL((kv_paged_join_kernel<DT, D, kRowTile>), dim3((unsigned)(a.s.W * a.c.Hkv)), dim3(256), 0, st, a);
+    if (!a.s.most) {
+        const dim3 joins = join_grid<D, kRowTile>(a, row_tiles);
+        hipLaunchKernelGGL((kv_paged_join_kernel<DT, D, kRowTile>), joins, dim3(256), 0, st, a);
+    }
     return hipGetLastError();
 }
 

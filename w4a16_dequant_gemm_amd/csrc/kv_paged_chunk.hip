@@ -1,7 +1,7 @@
 // Causal attention over a paged 8-bit KV cache for many query rows at a time: chunks of prompts behind what is
 // cached already (kv_paged.hip has the operator and takes few rows).
 //
-// One block = 128 rows (tokens times the heads of a kv head, token by token), 32 a wave; it walks the cached
+// One block = 128 or 256 rows (tokens times the heads of a kv head, token by token), 32 a wave; it walks the cached
 // tokens in tiles of 64.  Both products run transposed on 32 x 32 x 16 tiles (attn.h).  A tile's codes are read
 // two tiles ahead into registers, widened to 16 bits (exact) once for the block's rows and put into LDS while the
 // products of the tile before run.
@@ -22,7 +22,6 @@ namespace w4a16 {
 
 namespace {
 
-constexpr int kRows = 128;              // query rows of a block
 constexpr float kLag = 4.0f;            // the maximum may lag by so much (base 2)
 constexpr int kRaise = 11;              // weights are held times 2^kRaise; 2^(kLag + kRaise) < 65504
 constexpr int kDeepest = -60;           // scales below 2^kDeepest of the largest count as that (their share is nothing)
@@ -46,15 +45,19 @@ __device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)"
 
 // In iteration t the scores of tile t are computed beside the widening of K(t + 1) and V(t + 1), whose codes were
 // asked for an iteration before, and its softmax beside the second product of tile t - 1; one barrier an
-// iteration.  (The scores of tile t + 1 beside the softmax of tile t, as in attention.hip, need 32 registers
+// iteration (eight waves: K(t + 2) and V(t + 2), a barrier every other iteration: 1099 -> 1083 us).  (The scores of tile t + 1 beside the softmax of tile t, as in attention.hip, need 32 registers
 // more than there are with the codes on their way.)
 //
 // ONE: pages of at least a tile, so that its four groups are of one page.
-template <int DT, int FMT, int D, bool ONE>
-__global__ __launch_bounds__(256, 2) void kv_paged_chunk_kernel(PagedView a) {
-    constexpr int TILE = kTile * D, PR = D / 16, NL = kTile * PR / 256;   // 16-code pieces of a K row; loads of a thread
+template <int DT, int FMT, int D, bool ONE, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, 2) void kv_paged_chunk_kernel(PagedView a) {
+    constexpr int THREADS = 64 * WAVES, kRows = 32 * WAVES, TILE = kTile * D, PR = D / 16, NL = kTile * PR / THREADS;
+    static_assert(NL >= 1, "a piece a thread");
+      // 16-code pieces of a K row; loads of a thread
     constexpr int NG = ONE ? 1 : 4;
-    __shared__ __attribute__((aligned(16))) uint16_t lK[2 * TILE], lV[3 * TILE];
+    // tiles staged ahead, and how many of K and V there is room for
+    constexpr int AHEAD = WAVES == 8 ? 2 : 1, KR = 2 * AHEAD, VR = 2 * AHEAD + 1;
+    __shared__ __attribute__((aligned(16))) uint16_t lK[KR * TILE], lV[VR * TILE];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int n = lane & 31, hf = lane >> 5;
     const int h = blockIdx.x % a.c.Hkv;
@@ -108,7 +111,7 @@ __global__ __launch_bounds__(256, 2) void kv_paged_chunk_kernel(PagedView a) {
     // (tiles behind the last are taken for it: they are loaded, but nothing of them is used)
     auto group_page = [&](int t, int g) { return min((kTile * t + 16 * g) >> shift, last_page) - w.base; };
 
-    // a thread's pieces of a tile: of K token tid / PR + (256 / PR) i, codes 16 (tid % PR) and on; of V
+    // a thread's pieces of a tile: of K token tid / PR + (THREADS / PR) i, codes 16 (tid % PR) and on; of V
     // dimension tid / 4 + 64 i, tokens 16 (tid % 4) and on
     u32x4 kw[NL], vw[NL];
     const int kr = tid / PR, kj = tid % PR, vd = tid >> 2, vg = tid & 3;
@@ -121,7 +124,7 @@ __global__ __launch_bounds__(256, 2) void kv_paged_chunk_kernel(PagedView a) {
         for (int g = 0; g < NG; ++g) id[g] = max(lane_of(w.id, group_page(t, g)), 0);
 #pragma unroll
         for (int i = 0; i < NL; ++i) {
-            const int r = kr + (256 / PR) * i, g = r >> 4;          // (g is the same for a wave)
+            const int r = kr + (THREADS / PR) * i, g = r >> 4;          // (g is the same for a wave)
             int pg = id[0];
             if constexpr (!ONE) pg = __builtin_amdgcn_readfirstlane(g == 0 ? id[0] : g == 1 ? id[1] : g == 2 ? id[2] : id[3]);
             const uint8_t* base = (const uint8_t*)a.c.kc + (((long long)pg * a.c.Hkv + h) << shift) * D;
@@ -133,7 +136,7 @@ __global__ __launch_bounds__(256, 2) void kv_paged_chunk_kernel(PagedView a) {
               (vd << shift);
     };
     auto load_k = [&](int i) { kw[i] = *reinterpret_cast<const u32x4*>(kat[i]); };
-    auto load_v = [&](int i) { vw[i] = *reinterpret_cast<const u32x4*>(vat + ((64 * i) << shift)); };
+    auto load_v = [&](int i) { vw[i] = *reinterpret_cast<const u32x4*>(vat + ((THREADS / 4 * i) << shift)); };
     // V's codes where the weights do not hold its scale, and stale ones that may be no numbers, become 0
     auto clean_v = [&](int t) {
         t = min(t, tile1 - 1);
@@ -157,14 +160,14 @@ __global__ __launch_bounds__(256, 2) void kv_paged_chunk_kernel(PagedView a) {
     };
     // half `part` of piece i: registers to LDS as 16-bit values
     auto put_k = [&](uint16_t* K, int i, int part) {
-        const int r = kr + (256 / PR) * i;
+        const int r = kr + (THREADS / PR) * i;
         // (not to be widened, and held, before it is needed)
         asm volatile("" : "+v"(kw[i][2 * part]), "+v"(kw[i][2 * part + 1]));
         *reinterpret_cast<u32x4*>(K + r * D + 8 * swz_k<D>(r, 2 * kj + part)) =
             widen<DT, FMT>(kw[i][2 * part], kw[i][2 * part + 1]);
     };
     auto put_v = [&](uint16_t* V, int i, int part) {
-        const int d = vd + 64 * i;
+        const int d = vd + THREADS / 4 * i;
         asm volatile("" : "+v"(vw[i][2 * part]), "+v"(vw[i][2 * part + 1]));
         *reinterpret_cast<u32x4*>(V + d * kTile + 8 * swz_k<64>(d, 2 * vg + part)) =
             widen<DT_F16, FMT>(vw[i][2 * part], vw[i][2 * part + 1]);
@@ -184,7 +187,7 @@ __global__ __launch_bounds__(256, 2) void kv_paged_chunk_kernel(PagedView a) {
     // read kAhead steps early
     auto scores_and_stage = [&](const uint16_t* K, f32x16 (&S)[2], uint16_t* Kn, uint16_t* Vn) {
         constexpr int KS = D / 16, kAhead = 2;
-        static_assert(KS == 4 * NL, "half a piece a k-step");
+        constexpr int EVERY = KS / (4 * NL);        // half a piece every so many k-steps
         u32x4 k[kAhead][2];
 #pragma unroll
         for (int s = 0; s < kAhead; ++s) {
@@ -204,11 +207,14 @@ __global__ __launch_bounds__(256, 2) void kv_paged_chunk_kernel(PagedView a) {
                 k[s % kAhead][0] = key_piece(K, 0, s + kAhead);
                 k[s % kAhead][1] = key_piece(K, 1, s + kAhead);
             }
-            if (s & 2) put_v(Vn, s >> 2, s & 1);
-            else put_k(Kn, s >> 2, s & 1);
-            // the registers of a whole piece take the tile after the next
-            if ((s & 3) == 1) load_k(s >> 2);
-            if ((s & 3) == 3) load_v(s >> 2);
+            if (s % EVERY == 0) {
+                const int i = s / EVERY;
+                if (i & 2) put_v(Vn, i >> 2, i & 1);
+                else put_k(Kn, i >> 2, i & 1);
+                // the registers of a whole piece take the tile after the next
+                if ((i & 3) == 1) load_k(i >> 2);
+                if ((i & 3) == 3) load_v(i >> 2);
+            }
             __builtin_amdgcn_sched_barrier(0);
         }
     };
@@ -369,32 +375,40 @@ __global__ __launch_bounds__(256, 2) void kv_paged_chunk_kernel(PagedView a) {
             load_v(i);
         }
         // (what the weights of no tile are multiplied with has to be numbers)
-        for (int i = tid; i < TILE / 8; i += 256) *reinterpret_cast<u32x4*>(lV + 2 * TILE + 8 * i) = u32x4{0, 0, 0, 0};
-        clean_v(tile0);
-        locate(tile0 + 1);
-        stage(lK, lV);
-        int kc_at = 0, vp_at = 2 * TILE, vc_at = 0;     // where K(t), V(t - 1) and V(t) are
-        // the top of iteration t: K(t) and V(t) are in LDS, K(t - 1) and V(t - 2) have been read
+        for (int i = tid; i < TILE / 8; i += THREADS)
+            *reinterpret_cast<u32x4*>(lV + (VR - 1) * TILE + 8 * i) = u32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            clean_v(tile0 + i);
+            locate(tile0 + i + 1);
+            stage(lK + i * TILE, lV + i * TILE);
+        }
+        // where K(t), V(t - 1) and what is staged for t + AHEAD lie
+        int kc_at = 0, kn_at = AHEAD * TILE, vp_at = (VR - 1) * TILE, vn_at = AHEAD * TILE;
+        // the top of iteration t; where there is a barrier, K and V of the AHEAD tiles from t on are in LDS, and what the
+        // iterations up to the next one stage over has been read
         auto top = [&](int t) {
-            // tiles t .. t + 2 have to be in the window
-            if (min((kTile * (t + 3) - 1) >> shift, last_page) - w.base > 63) refresh((kTile * t) >> shift);
-            wait_lds();
-            __syncthreads();
-            clean_v(t + 1);
-            locate(t + 2);
+            // tiles t .. t + AHEAD + 1 have to be in the window
+            if (min((kTile * (t + AHEAD + 2) - 1) >> shift, last_page) - w.base > 63) refresh((kTile * t) >> shift);
+            if (AHEAD == 1 || ((t - tile0) & 1) == 0) {
+                wait_lds();
+                __syncthreads();
+            }
+            clean_v(t + AHEAD);
+            locate(t + AHEAD + 1);
         };
         auto turn = [&] {
-            const int vn = 3 * TILE - vp_at - vc_at;
-            vp_at = vc_at;
-            vc_at = vn;
-            kc_at = TILE - kc_at;
+            kc_at = kc_at == (KR - 1) * TILE ? 0 : kc_at + TILE;
+            kn_at = kn_at == (KR - 1) * TILE ? 0 : kn_at + TILE;
+            vp_at = vp_at == (VR - 1) * TILE ? 0 : vp_at + TILE;
+            vn_at = vn_at == (VR - 1) * TILE ? 0 : vn_at + TILE;
         };
         int t = tile0;
 #pragma unroll 1
         for (; t < own1; ++t) {
             top(t);
             f32x16 S[2];
-            scores_and_stage(lK + kc_at, S, lK + (TILE - kc_at), lV + (3 * TILE - vp_at - vc_at));
+            scores_and_stage(lK + kc_at, S, lK + kn_at, lV + vn_at);
             first_values(lV + vp_at);
             prepare(t, S);
             values_and_weights(lV + vp_at, S);
@@ -405,7 +419,7 @@ __global__ __launch_bounds__(256, 2) void kv_paged_chunk_kernel(PagedView a) {
 #pragma unroll 1
         for (; t < tile1; ++t) {
             top(t);
-            stage(lK + (TILE - kc_at), lV + (3 * TILE - vp_at - vc_at));
+            stage(lK + kn_at, lV + vn_at);
             turn();
         }
     }
@@ -436,39 +450,61 @@ __global__ __launch_bounds__(256, 2) void kv_paged_chunk_kernel(PagedView a) {
     }
 }
 
-constexpr int kTargetBlocks = 512;      // chunks x kv heads aimed at
 constexpr int kWhole = 16;              // up to so many tiles a sequence is never split
 constexpr int kLeast = 8;               // tiles of a chunk of a longer one
-int chunks(long long Hkv) { return (int)((kTargetBlocks + Hkv - 1) / Hkv); }
 
-template <int DT, int FMT, int D, bool ONE>
-hipError_t chunk(const PagedView& a, long long row_tiles, hipStream_t st) {
+// chunks aimed at for each kv head: a block of eight waves a CU, or two of four
+int chunks(long long Hkv, int waves) {
+    const int blocks = waves == 8 ? 256 : 512;
+    return (int)((blocks + Hkv - 1) / Hkv);
+}
+
+template <int DT, int FMT, int D, bool ONE, int WAVES>
+hipError_t chunk(PagedView a, hipStream_t st) {
+    constexpr int ROWS = 32 * WAVES;
+    a.s.W = chunks(a.c.Hkv, WAVES);
+    a.s.least = kLeast;
+    a.s.most = a.s.tokens <= kWhole * kTile ? kWhole : 0;
+    const long long row_tiles = (long long)a.c.T * a.s.G / ROWS + a.c.B;
     const unsigned blocks = (unsigned)((row_tiles + (a.s.most ? 0 : a.s.W)) * a.c.Hkv);
-    hipLaunchKernelGGL((kv_paged_chunk_kernel<DT, FMT, D, ONE>), dim3(blocks), dim3(256), 0, st, a);
-    if (!a.s.most)
-        hipLaunchKernelGGL((kv_paged_join_kernel<DT, D, kRows>), dim3((unsigned)(a.s.W * a.c.Hkv)), dim3(256), 0, st, a);
+    hipLaunchKernelGGL((kv_paged_chunk_kernel<DT, FMT, D, ONE, WAVES>), dim3(blocks), dim3(64 * WAVES), 0, st, a);
+    if (!a.s.most) {
+        const dim3 joins = join_grid<D, ROWS>(a, row_tiles);
+        hipLaunchKernelGGL((kv_paged_join_kernel<DT, D, ROWS>), joins, dim3(256), 0, st, a);
+    }
     return hipGetLastError();
+}
+
+// Eight waves of 256 rows where the sequences have them: a widened code serves twice the rows.  Four / eight
+// waves, us (32 / 8 heads, D = 128, int8, pages of 64): one chunk of 64 / 128 / 512 tokens behind 8000 28.5 / 32.9,
+// 38.9 / 38.8, 97.2 / 90.2, of 512 / 2048 behind 30000 294 / 264, 1144 / 1034; 8 of 64 / 128 behind 8000 97 / 90, 175 / 160.
+// Short tables are not split over blocks, and four waves leave fewer CUs idle: 512 tokens alone 19.0 / 23.9.
+bool wide(const PagedView& a) {
+    const long long rows = (long long)a.c.T * a.s.G;
+    return rows >= 512LL * a.c.B && (a.s.tokens > kWhole * kTile || rows * a.c.Hkv >= 256LL * 256);
+}
+
+template <int DT, int FMT, bool ONE>
+hipError_t chunk(const PagedView& a, hipStream_t st) {
+    if (a.c.D == 64) return chunk<DT, FMT, 64, ONE, 4>(a, st);
+    return wide(a) ? chunk<DT, FMT, 128, ONE, 8>(a, st) : chunk<DT, FMT, 128, ONE, 4>(a, st);
+}
+template <int DT, int FMT>
+hipError_t chunk(const PagedView& a, hipStream_t st) {
+    return a.c.page >= kTile ? chunk<DT, FMT, true>(a, st) : chunk<DT, FMT, false>(a, st);
 }
 
 }  // namespace
 
 long long kv_paged_chunk_floats(long long Hkv, long long D, long long tokens) {
-    return tokens <= kWhole * kTile ? 0 : 2LL * chunks(Hkv) * Hkv * kRows * (D + 2);
+    // (row tiles that are split have at most 2 W chunks; W times the rows is the same for both kernels up to rounding)
+    const long long rows = std::max(128LL * chunks(Hkv, 4), 256LL * chunks(Hkv, 8));
+    return tokens <= kWhole * kTile ? 0 : 2 * rows * Hkv * (D + 2);
 }
 
-hipError_t launch_kv_paged_chunk(const PagedView& v, int dtype, hipStream_t st) {
-    PagedView a = v;
-    a.s.W = chunks(a.c.Hkv);
-    a.s.least = kLeast;
-    a.s.most = a.s.tokens <= kWhole * kTile ? kWhole : 0;
-    const long long row_tiles = (long long)a.c.T * a.s.G / kRows + a.c.B;
-    const bool one = a.c.page >= kTile;
-#define W4A16_CHUNK(DT, FMT, D) (one ? chunk<DT, FMT, D, true>(a, row_tiles, st) : chunk<DT, FMT, D, false>(a, row_tiles, st))
-#define W4A16_CHUNK_D(DT, FMT) (a.c.D == 64 ? W4A16_CHUNK(DT, FMT, 64) : W4A16_CHUNK(DT, FMT, 128))
-    if (dtype == DT_F16) return a.c.fmt == FMT_INT8 ? W4A16_CHUNK_D(DT_F16, FMT_INT8) : W4A16_CHUNK_D(DT_F16, FMT_E4M3);
-    return a.c.fmt == FMT_INT8 ? W4A16_CHUNK_D(DT_BF16, FMT_INT8) : W4A16_CHUNK_D(DT_BF16, FMT_E4M3);
-#undef W4A16_CHUNK_D
-#undef W4A16_CHUNK
+hipError_t launch_kv_paged_chunk(const PagedView& a, int dtype, hipStream_t st) {
+    if (dtype == DT_F16) return a.c.fmt == FMT_INT8 ? chunk<DT_F16, FMT_INT8>(a, st) : chunk<DT_F16, FMT_E4M3>(a, st);
+    return a.c.fmt == FMT_INT8 ? chunk<DT_BF16, FMT_INT8>(a, st) : chunk<DT_BF16, FMT_E4M3>(a, st);
 }
 
 }  // namespace w4a16

@@ -158,29 +158,54 @@ __device__ __forceinline__ void store_out(const PagedView& a, const Piece& p, in
     *reinterpret_cast<u32x2*>(at) = u32x2{pack2<DT>(o[0] * inv, o[1] * inv), pack2<DT>(o[2] * inv, o[3] * inv)};
 }
 
-// Joins the chunks of row tiles that were split: a thread four values of a row.
+// Joins the chunks of row tiles that were split: a block 1024 / D rows (blockIdx.y), a thread four values of one,
+// eight chunks asked for at a time.
 template <int DT, int D, int ROWS>
 __global__ __launch_bounds__(256) void kv_paged_join_kernel(PagedView a) {
+    constexpr int AT = 8;
     const int tid = threadIdx.x, lane = tid & 63, h = blockIdx.x % a.c.Hkv;
     Piece p;
     if (!find_piece<ROWS, true>(a.s, blockIdx.x / a.c.Hkv, lane, p)) return;
-    const int rows = min(ROWS, p.n * a.s.G - p.row0);
+    const int r = blockIdx.y * (1024 / D) + tid / (D / 4), d = 4 * (tid % (D / 4));
+    if (r >= min(ROWS, p.n * a.s.G - p.row0)) return;
     const long long step = (long long)a.c.Hkv * kPartFloats<ROWS, D>;
     const float* part = a.work + ((long long)p.slot * a.c.Hkv + h) * kPartFloats<ROWS, D>;
-    for (int u = tid; u < rows * (D / 4); u += 256) {
-        const int r = u / (D / 4), d = u % (D / 4);
-        const float* stat = part + ROWS * D + 2 * r;
-        float Mt = -__builtin_inff();
-        for (int i = 0; i < p.parts; ++i) Mt = fmaxf(Mt, stat[i * step]);
-        float lt = 0.0f;
-        f32x4 s = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        for (int i = 0; i < p.parts; ++i) {
-            const float m = stat[i * step], f = m == -__builtin_inff() ? 0.0f : exp2_raw(m - Mt);
-            lt += stat[i * step + 1] * f;
-            s += *reinterpret_cast<const f32x4*>(part + i * step + r * D + 4 * d) * f;
+    float M = -__builtin_inff(), l = 0.0f;
+    f32x4 s = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int i = 0; i < p.parts; i += AT) {
+        float m[AT], w[AT];
+        f32x4 x[AT];
+#pragma unroll
+        for (int j = 0; j < AT; ++j) {
+            const float* at = part + min(i + j, p.parts - 1) * step;
+            m[j] = at[ROWS * D + 2 * r];
+            w[j] = at[ROWS * D + 2 * r + 1];
+            x[j] = *reinterpret_cast<const f32x4*>(at + r * D + d);
         }
-        store_out<DT, D>(a, p, h, p.row0 + r, 4 * d, s, Mt == -__builtin_inff() ? 0.0f : 1.0f / lt);
+        float Mn = M;
+#pragma unroll
+        for (int j = 0; j < AT; ++j) {
+            if (i + j >= p.parts) m[j] = -__builtin_inff();
+            Mn = fmaxf(Mn, m[j]);
+        }
+        if (Mn == -__builtin_inff()) continue;          // (rows that see nothing of these)
+        const float f = exp2_raw(M - Mn);
+        M = Mn;
+        l *= f;
+        s *= f;
+#pragma unroll
+        for (int j = 0; j < AT; ++j) {
+            const float e = exp2_raw(m[j] - M);
+            l += w[j] * e;
+            s += x[j] * e;
+        }
     }
+    store_out<DT, D>(a, p, h, p.row0 + r, d, s, M == -__builtin_inff() ? 0.0f : 1.0f / l);
+}
+// Its grid: at most W row tiles are split.
+template <int D, int ROWS>
+dim3 join_grid(const PagedView& a, long long row_tiles) {
+    return dim3((unsigned)((row_tiles < a.s.W ? row_tiles : a.s.W) * a.c.Hkv), ROWS * D / 1024);
 }
 
 // Many rows a sequence (kv_paged_chunk.hip); the caller fills all of the view but how chunks are cut.
