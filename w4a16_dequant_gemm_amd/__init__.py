@@ -39,6 +39,7 @@ the library's HIP kernels; there is no CPU or PyTorch fallback.
 
 from __future__ import annotations
 
+import functools
 import math
 
 import torch
@@ -939,14 +940,43 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "non
     return torch.tensor([w - 2 ** 64 if w >= 2 ** 63 else w for w in words], dtype=torch.int64, device=device), mscale
 
 
-def _rows16(t, name: str, dtype) -> int:
-    """``t [T, H, D]`` with adjacent heads, in the usual case in few steps; returns the rows' distance."""
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.dim() == 3 and t.is_cuda:
-        T, H, D = t.shape
-        st, sh, sd = t.stride()
-        if sd == 1 and sh == D and T > 1:
-            return st
-    return _need_heads(t, name, dtype)
+_CODES = {torch.float16: F16, torch.bfloat16: BF16}
+
+
+def _rows16(t, name: str, dtype, dev: int) -> int:
+    """``t [T, H, D]`` with adjacent heads on device ``dev``, in the usual case in few steps; returns the rows'
+    distance."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev >= 0:
+        st = t.stride()
+        if len(st) == 3 and st[2] == 1 and st[1] == t.size(2) and t.size(0) > 1:
+            return st[0]
+    st = _need_heads(t, name, dtype)
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the device of the other arguments")
+    return st
+
+
+def _vector(t, name: str, dtype, n: int, dev: int) -> int:
+    """``t [n]`` of a type on device ``dev``: its address."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and t.dim() == 1
+            and t.size(0) == n and t.is_contiguous()):
+        _need(t, name, dtype, 1)
+        if t.get_device() != dev:
+            raise ValueError(f"{name} must be on the device of the other arguments")
+        if t.shape[0] != n:
+            raise ValueError(f"{name} must have {n} elements")
+    return t.data_ptr()
+
+
+def _dense(t, name: str, dtype, shape, dev: int) -> int:
+    """A contiguous ``t`` of a type and shape on device ``dev``: its address."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev
+            and t.is_contiguous()):
+        _need(t, name, dtype, len(shape))
+        if t.get_device() != dev:
+            raise ValueError(f"{name} must be on the device of the other arguments")
+        raise ValueError(f"{name} must be {list(shape)}")
+    return t.data_ptr()
 
 
 def rope(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, interleaved: bool = False, mscale: float = 1.0,
@@ -958,23 +988,20 @@ def rope(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, interlea
     it must not overlap the inputs.  The gradient of ``x`` is ``rope(grad, -positions, ...)``."""
     dt = _dtype_code(x)
     dtype, dev = x.dtype, x.get_device()
-    xs = _rows16(x, "x", dtype)
-    T, H, D = x.shape
-    _need(positions, "positions", _INT32, 1)
-    _need(freqs, "freqs", torch.int64, 1)
-    if positions.shape[0] != T:
-        raise ValueError("positions must be [T]")
+    xs = _rows16(x, "x", dtype, dev)
+    shape = T, H, D = x.shape
+    at = _vector(positions, "positions", _INT32, T, dev)
+    pairs = freqs.shape[0] if isinstance(freqs, torch.Tensor) and freqs.dim() == 1 else 0
+    f = _vector(freqs, "freqs", torch.int64, pairs, dev)
     if out is None:
-        out = torch.empty((T, H, D), dtype=dtype, device=x.device)
+        out = torch.empty(shape, dtype=dtype, device=x.device)
         os = H * D
     else:
-        os = _rows16(out, "out", dtype)
-        if out.shape != x.shape:
+        os = _rows16(out, "out", dtype, dev)
+        if out.shape != shape:
             raise ValueError("out must be [T, H, D]")
-    if not dev == positions.get_device() == freqs.get_device() == out.get_device():
-        raise ValueError("positions, freqs and out must be on the device of x")
-    _call(lib().w4a16_rope, "w4a16_rope", x.device, x.data_ptr(), dt, T, H, D, xs, positions.data_ptr(), freqs.data_ptr(),
-          2 * freqs.shape[0], 1 if interleaved else 0, mscale, out.data_ptr(), os)
+    _call(lib().w4a16_rope, "w4a16_rope", x.device, x.data_ptr(), dt, T, H, D, xs, at, f, 2 * pairs,
+          1 if interleaved else 0, mscale, out.data_ptr(), os)
     return out
 
 
@@ -995,8 +1022,8 @@ def kv_pages(pages: int, Hkv: int, page: int, D: int, codes=torch.int8, device="
     return pool((pages, Hkv, page, D)), pool((pages, Hkv, D, page))
 
 
-def _paged(kpages, vpages, table, lengths, cu, T: int | None, dev: int):
-    """The checked description of a paged cache and a call's sequences (``T`` None: the number of sequences)."""
+def _paged_odd(kpages, vpages, table, lengths, cu, T, dev: int) -> None:
+    """Says what is wrong with the description of a paged cache."""
     (kc, ks), (vc, vs) = kpages, vpages
     for t, name, nd in ((kc, "kpages codes", 4), (vc, "vpages codes", 4), (ks, "kpages scales", 2),
                         (vs, "vpages scales", 2)):
@@ -1004,39 +1031,62 @@ def _paged(kpages, vpages, table, lengths, cu, T: int | None, dev: int):
             raise TypeError(f"{name} must be a torch.Tensor")
         if t.dim() != nd or not t.is_contiguous():
             raise ValueError(f"{name} must be {nd}-D and contiguous")
-        if t.get_device() != dev:
-            raise ValueError(f"{name} must be on the device of the other arguments")
-    code = kc.dtype
-    if (code is not _INT8 and code is not _E4M3) or vc.dtype is not code:
+        if not t.is_cuda or t.get_device() != dev:
+            raise ValueError(f"{name} must be on the GPU of the other arguments")
+    if kc.dtype not in (_INT8, _E4M3) or vc.dtype != kc.dtype:
         raise TypeError("codes must be torch.int8 or torch.float8_e4m3fn, alike in kpages and vpages")
-    if ks.dtype is not torch.float32 or vs.dtype is not torch.float32:
+    if ks.dtype != torch.float32 or vs.dtype != torch.float32:
         raise TypeError("scales must be float32")
     N, Hkv, page, D = kc.shape
     if vc.shape != (N, Hkv, D, page) or ks.shape != (N, Hkv) or vs.shape != (N, Hkv):
         raise ValueError("kpages must be [pages, Hkv, page, D], vpages [pages, Hkv, D, page] and scales [pages, Hkv]")
     _need(table, "table", _INT32, 2)
     _need(lengths, "lengths", _INT32, 1)
-    B, P = table.shape
+    B = table.shape[0]
     if lengths.shape[0] != B:
         raise ValueError("table must be [B, table_pages] and lengths [B]")
-    if cu is None:
-        if T is not None and T != B:
-            raise ValueError("without cu_seqlens every sequence has one token: T must be B")
-        T = B
-        at = None
-    else:
-        _need(cu, "cu_seqlens", _INT32, 1)
-        if cu.shape[0] != B + 1:
-            raise ValueError("cu_seqlens must be [B + 1]")
-        if cu.get_device() != dev:
-            raise ValueError("cu_seqlens must be on the device of the other arguments")
-        if T is None:
-            raise ValueError("T is needed where cu_seqlens is given")
-        at = cu.data_ptr()
-    if dev != table.get_device() or dev != lengths.get_device():
+    if table.get_device() != dev or lengths.get_device() != dev:
         raise ValueError("table and lengths must be on the device of the other arguments")
-    return KvPaged(kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), table.data_ptr(), lengths.data_ptr(), at,
-                   N, page, P, B, T, Hkv, D, KV_INT8 if code is _INT8 else KV_E4M3)
+    if cu is None:
+        raise ValueError("without cu_seqlens every sequence has one token: T must be B")
+    if T is None:
+        raise ValueError("T is needed where cu_seqlens is given")
+    _vector(cu, "cu_seqlens", _INT32, B + 1, dev)
+    raise ValueError("the description of the paged cache is wrong")
+
+
+_F32 = torch.float32
+
+
+def _paged(kpages, vpages, table, lengths, cu, T: int | None, dev: int):
+    """The checked description of a paged cache and a call's sequences (``T`` None: the number of sequences), and
+    its ``(T, Hkv, D)``."""
+    (kc, ks), (vc, vs) = kpages, vpages
+    if (isinstance(kc, torch.Tensor) and isinstance(ks, torch.Tensor) and isinstance(vc, torch.Tensor)
+            and isinstance(vs, torch.Tensor) and isinstance(table, torch.Tensor) and isinstance(lengths, torch.Tensor)
+            and kc.dim() == 4 and table.dim() == 2):
+        code = kc.dtype
+        N, Hkv, page, D = kc.shape
+        B, P = table.shape
+        per_head = (N, Hkv)
+        if cu is None:
+            at = None
+            if T is None:
+                T = B
+            fine = T == B
+        else:
+            fine = T is not None
+            at = _vector(cu, "cu_seqlens", _INT32, B + 1, dev)
+        if (fine and (code is _INT8 or code is _E4M3) and vc.dtype is code and ks.dtype is _F32 and vs.dtype is _F32
+                and vc.shape == (N, Hkv, D, page) and ks.shape == per_head and vs.shape == per_head
+                and table.dtype is _INT32 and lengths.dtype is _INT32 and lengths.dim() == 1 and lengths.size(0) == B
+                and 0 <= dev == kc.get_device() == ks.get_device() == vc.get_device() == vs.get_device()
+                == table.get_device() == lengths.get_device()
+                and kc.is_contiguous() and ks.is_contiguous() and vc.is_contiguous() and vs.is_contiguous()
+                and table.is_contiguous() and lengths.is_contiguous()):
+            return KvPaged(kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), table.data_ptr(),
+                           lengths.data_ptr(), at, N, page, P, B, T, Hkv, D, KV_INT8 if code is _INT8 else KV_E4M3), Hkv, D
+    _paged_odd(kpages, vpages, table, lengths, cu, T, dev)
 
 
 def kv_append_paged(k: torch.Tensor, v: torch.Tensor, kpages, vpages, table: torch.Tensor, lengths: torch.Tensor,
@@ -1057,37 +1107,31 @@ def kv_append_paged(k: torch.Tensor, v: torch.Tensor, kpages, vpages, table: tor
     ``q [T, Hq, D]`` is rotated likewise into ``q_out`` (dense, apart from the inputs), which is returned."""
     dt = _dtype_code(k)
     dtype, dev = k.dtype, k.get_device()
-    ks, vs = _rows16(k, "k", dtype), _rows16(v, "v", dtype)
-    c = _paged(kpages, vpages, table, lengths, cu_seqlens, k.shape[0], dev)
-    T, Hkv, D = k.shape
-    if v.shape != k.shape or Hkv != c.Hkv or D != c.D:
+    ks, vs = _rows16(k, "k", dtype, dev), _rows16(v, "v", dtype, dev)
+    shape = T, H, D = k.shape
+    c, Hkv, Dc = _paged(kpages, vpages, table, lengths, cu_seqlens, T, dev)
+    if v.shape != shape or H != Hkv or D != Dc:
         raise ValueError("k and v must be [T, Hkv, D]")
-    R, f = 0, None
+    R = f = 0
     if freqs is not None:
-        _need(freqs, "freqs", torch.int64, 1)
-        R, f = 2 * freqs.shape[0], freqs.data_ptr()
-    if positions is not None:
-        _need(positions, "positions", _INT32, 1)
-        if positions.shape[0] != T:
-            raise ValueError("positions must be [T]")
-    Hq, qs, qp, qo = 0, 0, None, None
+        R = freqs.shape[0] if isinstance(freqs, torch.Tensor) and freqs.dim() == 1 else 0
+        f = _vector(freqs, "freqs", torch.int64, R, dev)
+        R *= 2
+    Hq = qs = 0
+    qp = qo = None
     if q is not None:
-        qs = _rows16(q, "q", dtype)
-        if q.shape[0] != T or q.shape[2] != D:
+        qs = _rows16(q, "q", dtype, dev)
+        _, Hq, _ = qshape = q.shape
+        if qshape[0] != T or qshape[2] != D:
             raise ValueError("q must be [T, Hq, D]")
-        Hq = q.shape[1]
         if q_out is None:
-            q_out = torch.empty((T, Hq, D), dtype=dtype, device=k.device)
-        else:
-            _need(q_out, "q_out", dtype, 3)
-            if q_out.shape != q.shape:
-                raise ValueError("q_out must be [T, Hq, D]")
-        qp, qo = q.data_ptr(), q_out.data_ptr()
+            q_out = torch.empty(qshape, dtype=dtype, device=k.device)
+        qp, qo = q.data_ptr(), _dense(q_out, "q_out", dtype, qshape, dev)
     elif q_out is not None:
         raise ValueError("q_out needs q")
-    _same_device(k, "k", v=v, freqs=freqs, positions=positions, q=q, q_out=q_out)
     _call(lib().w4a16_kv_append_paged, "w4a16_kv_append_paged", k.device, c, k.data_ptr(), v.data_ptr(), dt, ks, vs,
-          None if positions is None else positions.data_ptr(), f, R, 1 if interleaved else 0, mscale, qp, Hq, qs, qo)
+          None if positions is None else _vector(positions, "positions", _INT32, T, dev), f or None, R,
+          1 if interleaved else 0, mscale, qp, Hq, qs, qo)
     return q_out
 
 
@@ -1097,26 +1141,30 @@ def kv_read_paged(kpages, vpages, table: torch.Tensor, lengths: torch.Tensor, cu
     :func:`kv_append_paged` with the same arguments writes.  ``T`` is the number of packed rows where
     ``cu_seqlens`` is given; ``out`` takes ``(k, v)`` to write into (their shape and type then count).  Tokens
     without a page are zeros; rows of no sequence are not written."""
+    pool = kpages[0]
+    if not isinstance(pool, torch.Tensor):
+        raise TypeError("kpages codes must be a torch.Tensor")
     if out is not None:
         ko, vo = out
-        _need(ko, "out k", ko.dtype, 3)
-        _need(vo, "out v", ko.dtype, 3)
+        if not isinstance(ko, torch.Tensor) or ko.dim() != 3:
+            raise ValueError("out must be two tensors [T, Hkv, D]")
         if T is not None and T != ko.shape[0]:
             raise ValueError("out and T disagree")
-        T, dtype = ko.shape[0], ko.dtype
-    dev = kpages[0].get_device()
-    c = _paged(kpages, vpages, table, lengths, cu_seqlens, T, dev)
-    shape = (c.T, c.Hkv, c.D)
+        T, dtype = ko.size(0), ko.dtype
+    dev = pool.get_device()
+    c, Hkv, D = _paged(kpages, vpages, table, lengths, cu_seqlens, T, dev)
+    shape = (c.T, Hkv, D)
     if out is None:
-        ko, vo = (torch.empty(shape, dtype=dtype, device=kpages[0].device) for _ in range(2))
-    elif ko.shape != shape or vo.shape != shape:
-        raise ValueError("out must be two tensors [T, Hkv, D]")
-    if dev != ko.get_device() or dev != vo.get_device():
-        raise ValueError("out must be on the device of the pages")
-    _call(lib().w4a16_kv_read_paged, "w4a16_kv_read_paged", ko.device, c, _dtype_code(ko), ko.data_ptr(), vo.data_ptr())
+        ko, vo = (torch.empty(shape, dtype=dtype, device=pool.device) for _ in range(2))
+    code = _CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"rows are float16 or bfloat16, got {dtype}")
+    _call(lib().w4a16_kv_read_paged, "w4a16_kv_read_paged", pool.device, c, code, _dense(ko, "out k", dtype, shape, dev),
+          _dense(vo, "out v", dtype, shape, dev))
     return ko, vo
 
 
+@functools.lru_cache(maxsize=256)
 def kv_attention_paged_workspace(Hq: int, Hkv: int, D: int, tokens: int) -> int:
     """fp32 elements of a scratch buffer that holds every :func:`kv_attention_paged` call of these heads whose
     table has room for at most ``tokens`` tokens (0: none)."""
@@ -1141,21 +1189,18 @@ def kv_attention_paged(q: torch.Tensor, kpages, vpages, table: torch.Tensor, len
     Codes enter the products exactly; the softmax weights, with V's scales, are rounded once to fp16 (relative
     2^-11); scores, statistics and sums are fp32."""
     dt = _dtype_code(q)
-    qs = _rows16(q, "q", q.dtype)
-    T, Hq, D = q.shape
-    c = _paged(kpages, vpages, table, lengths, cu_seqlens, T, q.get_device())
-    if D != c.D:
+    dtype, dev = q.dtype, q.get_device()
+    qs = _rows16(q, "q", dtype, dev)
+    shape = T, Hq, D = q.shape
+    c, Hkv, Dc = _paged(kpages, vpages, table, lengths, cu_seqlens, T, dev)
+    if D != Dc:
         raise ValueError("q must be [T, Hq, D]")
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
-    else:
-        _need(out, "out", q.dtype, 3)
-        if out.shape != q.shape or out.get_device() != q.get_device():
-            raise ValueError("out must be [T, Hq, D] on the device of q")
-    L = lib()
-    need = L.w4a16_kv_attention_paged_workspace(Hq, c.Hkv, D, c.table_pages * c.page)
+        out = torch.empty(shape, dtype=dtype, device=q.device)
+    o = _dense(out, "out", dtype, shape, dev)
+    need = kv_attention_paged_workspace(Hq, Hkv, D, table.size(1) * kpages[0].size(2))
     if need or work is not None:
         work = _work(work, need, "w4a16_kv_attention_paged_workspace", q)
-    _call(L.w4a16_kv_attention_paged, "w4a16_kv_attention_paged", q.device, c, q.data_ptr(), dt, Hq, qs,
-          None if work is None else work.data_ptr(), out.data_ptr())
+    _call(lib().w4a16_kv_attention_paged, "w4a16_kv_attention_paged", q.device, c, q.data_ptr(), dt, Hq, qs,
+          None if work is None else work.data_ptr(), o)
     return out
