@@ -49,6 +49,11 @@ struct RopeView {
 constexpr int kRopePairs = 1024;        // (token, pair) angles of a block
 constexpr int kRopeTokens = 4;          // tokens of a block at most
 
+template <int V>
+struct Piece { typedef u32x4 type; };
+template <>
+struct Piece<1> { typedef uint16_t type; };
+
 // Tokens t0 .. t0 + tb - 1 by one block: their angles' cos and sin once into LDS, then all heads, V pairs
 // a thread at a time.
 template <int DT, int V>
@@ -70,58 +75,67 @@ __device__ __forceinline__ void rope_block(const RopeView& r, int t0, int tb, fl
     const int turns = r.half / V, units = turns + (r.copy ? (r.D - 2 * r.half) / CP : 0);
     const int rows = 256 / units, unit = tid % units, row = tid / units;
     if (row >= rows) return;
-    int t = row / r.H, h = row - t * r.H;
+    const int heads = tb * r.H;
     const uint16_t* x = r.x + (long long)t0 * r.xs;
     uint16_t* out = r.out + (long long)t0 * r.os;
-    while (t < tb) {
-        const uint16_t* px = x + (long long)t * r.xs + h * r.D;
-        uint16_t* po = out + (long long)t * r.os + h * r.D;
-        if (!lp[t].y) {
-        } else if (unit < turns) {
-            const int p = unit * V, a = r.inter ? 2 * p : p, b = r.inter ? 2 * p + V : p + r.half;
-            const float *c = lc + t * r.half + p, *s = ls + t * r.half + p;
-            if constexpr (V == 8) {
-                const u32x4 lo = *reinterpret_cast<const u32x4*>(px + a), hi = *reinterpret_cast<const u32x4*>(px + b);
-                u32x4 ylo, yhi;
-                if (r.inter) {
+    const bool turning = unit < turns;
+    // the unit's values: two pieces (of V) of the rotation, or one to copy
+    const int p = unit * V, e = 2 * r.half + (unit - turns) * CP;
+    const int at0 = turning ? (r.inter ? 2 * p : p) : e, at1 = turning ? (r.inter ? 2 * p + V : p + r.half) : V == 1 ? e + 1 : e;
+    constexpr int AT = 4;                               // rows asked for at a time
+    int t = row / r.H, h = row - t * r.H;
+    for (int i = row; i < heads; i += AT * rows) {
+        int ts[AT], hs[AT];
+        typename Piece<V>::type lo[AT], hi[AT];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const uint32_t w = i < 4 ? lo[i] : hi[i - 4];
-                        const float x0 = in2f<DT>(w & 0xFFFFu), x1 = in2f<DT>(w >> 16);
-                        const uint32_t y = pack2<DT>(x0 * c[i] - x1 * s[i], x1 * c[i] + x0 * s[i]);
-                        if (i < 4) ylo[i] = y;
-                        else yhi[i - 4] = y;
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float c0 = c[2 * i], s0 = s[2 * i], c1 = c[2 * i + 1], s1 = s[2 * i + 1];
-                        const float a0 = in2f<DT>(lo[i] & 0xFFFFu), a1 = in2f<DT>(lo[i] >> 16);
-                        const float b0 = in2f<DT>(hi[i] & 0xFFFFu), b1 = in2f<DT>(hi[i] >> 16);
-                        ylo[i] = pack2<DT>(a0 * c0 - b0 * s0, a1 * c1 - b1 * s1);
-                        yhi[i] = pack2<DT>(b0 * c0 + a0 * s0, b1 * c1 + a1 * s1);
-                    }
-                }
-                *reinterpret_cast<u32x4*>(po + a) = ylo;
-                *reinterpret_cast<u32x4*>(po + b) = yhi;
-            } else {
-                const float x0 = in2f<DT>(px[a]), x1 = in2f<DT>(px[b]);
-                po[a] = f2out<DT>(x0 * c[0] - x1 * s[0]);
-                po[b] = f2out<DT>(x1 * c[0] + x0 * s[0]);
+        for (int j = 0; j < AT; ++j) {
+            ts[j] = t < tb && lp[t].y ? t : -1;
+            hs[j] = h;
+            if (ts[j] >= 0) {
+                const uint16_t* px = x + (long long)t * r.xs + h * r.D;
+                lo[j] = *reinterpret_cast<const typename Piece<V>::type*>(px + at0);
+                hi[j] = *reinterpret_cast<const typename Piece<V>::type*>(px + at1);
             }
-        } else {
-            const int e = 2 * r.half + (unit - turns) * CP;
-            if constexpr (V == 8) *reinterpret_cast<u32x4*>(po + e) = *reinterpret_cast<const u32x4*>(px + e);
-            else {
-                const uint16_t e0 = px[e], e1 = px[e + 1];
-                po[e] = e0;
-                po[e + 1] = e1;
+            h += rows;
+            while (h >= r.H) {
+                h -= r.H;
+                ++t;
             }
         }
-        h += rows;
-        while (h >= r.H) {
-            h -= r.H;
-            ++t;
+#pragma unroll
+        for (int j = 0; j < AT; ++j) {
+            if (ts[j] < 0) continue;
+            uint16_t* po = out + (long long)ts[j] * r.os + hs[j] * r.D;
+            if (turning) {
+                const float *c = lc + ts[j] * r.half + p, *s = ls + ts[j] * r.half + p;
+                if constexpr (V == 8) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if (r.inter) {
+                            float x0 = in2f<DT>(lo[j][k] & 0xFFFFu), x1 = in2f<DT>(lo[j][k] >> 16);
+                            float z0 = in2f<DT>(hi[j][k] & 0xFFFFu), z1 = in2f<DT>(hi[j][k] >> 16);
+                            turn_pair(x0, x1, c[k], s[k]);
+                            turn_pair(z0, z1, c[k + 4], s[k + 4]);
+                            lo[j][k] = pack2<DT>(x0, x1);
+                            hi[j][k] = pack2<DT>(z0, z1);
+                        } else {
+                            float x0 = in2f<DT>(lo[j][k] & 0xFFFFu), x1 = in2f<DT>(lo[j][k] >> 16);
+                            float z0 = in2f<DT>(hi[j][k] & 0xFFFFu), z1 = in2f<DT>(hi[j][k] >> 16);
+                            turn_pair(x0, z0, c[2 * k], s[2 * k]);
+                            turn_pair(x1, z1, c[2 * k + 1], s[2 * k + 1]);
+                            lo[j][k] = pack2<DT>(x0, x1);
+                            hi[j][k] = pack2<DT>(z0, z1);
+                        }
+                    }
+                } else {
+                    float x0 = in2f<DT>(lo[j]), x1 = in2f<DT>(hi[j]);
+                    turn_pair(x0, x1, c[0], s[0]);
+                    lo[j] = f2out<DT>(x0);
+                    hi[j] = f2out<DT>(x1);
+                }
+            }
+            *reinterpret_cast<typename Piece<V>::type*>(po + at0) = lo[j];
+            if (turning || V == 1) *reinterpret_cast<typename Piece<V>::type*>(po + at1) = hi[j];
         }
     }
 }
@@ -181,47 +195,65 @@ struct AppendView {
 };
 
 // One (page, head) of K (ACROSS false: rows, rotated) or V (columns).  Thread units of eight values: of K four
-// pairs (p .. p + 3 of the rotation, or eight adjacent ones behind it), of V eight adjacent ones.
-template <int DT, int FMT, int D, bool ACROSS>
-__device__ __forceinline__ void append_page(const AppendView& a, const PageTokens& p, int id, int h, int shift,
-                                            uint8_t* lds, float* red) {
-    constexpr int UR = D / 8, UNITS = 128 * UR / 256;       // units of a row; of a thread at most
+// pairs (p .. p + 3 of the rotation, or eight adjacent values behind it), of V eight adjacent ones.
+template <int DT, int FMT, int D, int PAGE, bool ACROSS>
+__device__ __forceinline__ void append_page(const AppendView& a, const PageTokens& p, int h, uint8_t* lds, float* red) {
+    constexpr int UR = D / 8, UNITS = PAGE * UR > 256 ? PAGE * UR / 256 : 1;       // units of a row; of a thread
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int page = 1 << shift, total = p.n * UR;
-    uint8_t* codes = (uint8_t*)(ACROSS ? a.c.vc : a.c.kc) + (((long long)id * a.c.Hkv + h) << shift) * D;
-    float* scale = (ACROSS ? a.c.vs : a.c.ks) + (long long)id * a.c.Hkv + h;
+    const int total = p.n * UR, j = tid % UR, t0 = tid / UR;       // unit i of a thread: token t0 + 256 / UR i, values of j
     const uint16_t* src = (ACROSS ? a.v : a.k) + h * D;
     const int stride = ACROSS ? a.vs : a.ks;
+
+    // a unit's values: of four pairs (first, second) in a word each, or eight in a row
+    u32x4 raw[UNITS];
+    const bool turns = !ACROSS && 4 * j < a.half;
+    const bool halves = turns && !a.inter && a.half % 4 == 0;      // two pieces of four values
+    const bool loose = turns && !a.inter && a.half % 4 != 0;       // value by value
+#pragma unroll
+    for (int i = 0; i < UNITS; ++i) {
+        if (256 * i >= total) break;
+        const uint16_t* row = src + (long long)(p.token + min(t0 + 256 / UR * i, p.n - 1)) * stride;
+        if (halves) {
+            const u32x2 lo = *reinterpret_cast<const u32x2*>(row + 4 * j), hi = *reinterpret_cast<const u32x2*>(row + a.half + 4 * j);
+            raw[i] = u32x4{perm(hi[0], lo[0], 0x05040100u), perm(hi[0], lo[0], 0x07060302u), perm(hi[1], lo[1], 0x05040100u),
+                           perm(hi[1], lo[1], 0x07060302u)};
+        } else if (loose) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int q = 4 * j + e;
+                const bool turn = q < a.half;
+                raw[i][e] = row[turn ? q : 2 * q] | (uint32_t)row[turn ? q + a.half : 2 * q + 1] << 16;
+            }
+        } else raw[i] = *reinterpret_cast<const u32x4*>(row + 8 * j);
+    }
+    long long f[4];
+    if (turns) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[e] = a.freqs[min(4 * j + e, a.half - 1)];
+    }
+    const int id = page_id(a.c.table, a.c.P, a.c.N, p.b, p.index);
+    if (id < 0) return;
+    uint8_t* codes = (uint8_t*)(ACROSS ? a.c.vc : a.c.kc) + ((long long)id * a.c.Hkv + h) * (PAGE * D);
+    float* scale = (ACROSS ? a.c.vs : a.c.ks) + (long long)id * a.c.Hkv + h;
+    if (tid == 0) red[4] = p.off > 0 ? *scale : 0.0f;      // (read by the thread that writes it)
 
     float x[UNITS][8];
     float top = 0.0f;
 #pragma unroll
     for (int i = 0; i < UNITS; ++i) {
-        const int u = tid + 256 * i;
+        const int t = t0 + 256 / UR * i;
         if (256 * i >= total) break;
-        if (u < total) {
-            const int t = u / UR, j = u % UR;
-            const uint16_t* row = src + (long long)(p.token + t) * stride;
-            if (ACROSS || 4 * j >= a.half) {
-                // (a rotation that ends inside the unit: pair by pair below)
-                const u32x4 w = *reinterpret_cast<const u32x4*>(row + 8 * j);
+        if (t < p.n) {
+            int position = 0;
+            if (turns) position = a.positions ? a.positions[p.token + t] : p.index * PAGE + p.off + t;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    x[i][2 * e] = in2f<DT>(w[e] & 0xFFFFu);
-                    x[i][2 * e + 1] = in2f<DT>(w[e] >> 16);
-                }
-            } else {
-                const int position = a.positions ? a.positions[p.token + t] : (p.index << shift) + p.off + t;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int q = 4 * j + e;
-                    const bool turn = q < a.half;
-                    const int e0 = a.inter || !turn ? 2 * q : q, e1 = a.inter || !turn ? 2 * q + 1 : q + a.half;
-                    const float x0 = in2f<DT>(row[e0]), x1 = in2f<DT>(row[e1]);
-                    float c = 1.0f, s = 0.0f;
-                    if (turn) position_cos_sin(position, a.freqs[q], a.m, c, s);
-                    x[i][2 * e] = x0 * c - x1 * s;
-                    x[i][2 * e + 1] = x1 * c + x0 * s;
+            for (int e = 0; e < 4; ++e) {
+                x[i][2 * e] = in2f<DT>(raw[i][e] & 0xFFFFu);
+                x[i][2 * e + 1] = in2f<DT>(raw[i][e] >> 16);
+                if (turns && 4 * j + e < a.half) {
+                    float c, s;
+                    position_cos_sin(position, f[e], a.m, c, s);
+                    turn_pair(x[i][2 * e], x[i][2 * e + 1], c, s);
                 }
             }
 #pragma unroll
@@ -230,7 +262,6 @@ __device__ __forceinline__ void append_page(const AppendView& a, const PageToken
     }
     top = wave_max(top);
     if (lane == 0) red[wave] = top;
-    if (tid == 0) red[4] = p.off > 0 ? *scale : 0.0f;      // (read by the thread that writes it)
     __syncthreads();
     const float old = red[4];
     top = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])) / kTop<FMT>;
@@ -250,23 +281,18 @@ __device__ __forceinline__ void append_page(const AppendView& a, const PageToken
             }
 #pragma unroll
         for (int i = 0; i < UNITS; ++i) {
-            const int u = tid + 256 * i;
-            if (u >= total) break;
-            const int t = u / UR, j = u % UR;
+            const int t = t0 + 256 / UR * i;
+            if (t >= p.n) break;
             uint8_t* row = codes + (p.off + t) * D;
             float y[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) y[e] = quotient(x[i][e]);
-            if (4 * j + 4 <= a.half && !a.inter) {
-                const uint32_t lo = pack_codes<FMT>(y[0], y[2], y[4], y[6]), hi = pack_codes<FMT>(y[1], y[3], y[5], y[7]);
-                *reinterpret_cast<uint32_t*>(row + 4 * j) = lo;
-                if (a.half % 4 == 0) *reinterpret_cast<uint32_t*>(row + a.half + 4 * j) = hi;
-                else
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) row[a.half + 4 * j + e] = (uint8_t)(hi >> (8 * e));
+            if (halves) {
+                *reinterpret_cast<uint32_t*>(row + 4 * j) = pack_codes<FMT>(y[0], y[2], y[4], y[6]);
+                *reinterpret_cast<uint32_t*>(row + a.half + 4 * j) = pack_codes<FMT>(y[1], y[3], y[5], y[7]);
             } else {
                 const uint32_t w[2] = {pack_codes<FMT>(y[0], y[1], y[2], y[3]), pack_codes<FMT>(y[4], y[5], y[6], y[7])};
-                if (a.inter || 4 * j >= a.half) *reinterpret_cast<u32x2*>(row + 8 * j) = u32x2{w[0], w[1]};
+                if (!loose) *reinterpret_cast<u32x2*>(row + 8 * j) = u32x2{w[0], w[1]};
                 else
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
@@ -279,12 +305,11 @@ __device__ __forceinline__ void append_page(const AppendView& a, const PageToken
         }
     } else {
         // through LDS, so that a dimension's tokens are stored together
-        const int pitch = page + 4;
+        constexpr int pitch = PAGE + 4;
 #pragma unroll
         for (int i = 0; i < UNITS; ++i) {
-            const int u = tid + 256 * i;
-            if (u >= total) break;
-            const int t = u / UR, j = u % UR;
+            const int t = t0 + 256 / UR * i;
+            if (t >= p.n) break;
             float y[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) y[e] = quotient(x[i][e]);
@@ -296,33 +321,38 @@ __device__ __forceinline__ void append_page(const AppendView& a, const PageToken
         // pieces of 16 tokens of a dimension: the earlier tokens' codes (rounded again), the new ones, and what
         // lies behind them as it was
         const int first = grown ? 0 : p.off >> 4, pieces = ((p.off + p.n + 15) >> 4) - first;
-        for (int i = tid; i < D * pieces; i += 256) {
-            const int d = i / pieces, piece = first + i % pieces, t0 = 16 * piece;
-            u32x4* at = reinterpret_cast<u32x4*>(codes + d * page + t0);
-            u32x4 w = {0, 0, 0, 0};
-            const bool whole = t0 >= p.off && t0 + 16 <= p.off + p.n;
-            if (!whole) w = *at;
+        for (int i = tid; i < D * (PAGE / 16); i += 256) {
+            const int d = i / (PAGE / 16), piece = i % (PAGE / 16), at = 16 * piece;
+            if (piece < first || piece >= first + pieces) continue;
+            u32x4* out = reinterpret_cast<u32x4*>(codes + d * PAGE + at);
+            u32x4 w = {0, 0, 0, 0}, y;
+            if (at >= p.off && at + 16 <= p.off + p.n) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t fresh = *reinterpret_cast<const uint32_t*>(lds + d * pitch + t0 + 4 * j);
-                const uint32_t again = grown && t0 + 4 * j < p.off ? requantize<FMT>(w[j], ratio) : w[j];
-                uint32_t y = 0;
+                for (int k = 0; k < 4; ++k) y[k] = *reinterpret_cast<const uint32_t*>(lds + d * pitch + at + 4 * k);
+            } else {
+                w = *out;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int slot = t0 + 4 * j + e;
-                    const uint32_t from = slot < p.off ? again : slot < p.off + p.n ? fresh : w[j];
-                    y |= from & (255u << (8 * e));
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t fresh = *reinterpret_cast<const uint32_t*>(lds + d * pitch + at + 4 * k);
+                    const uint32_t again = grown && at + 4 * k < p.off ? requantize<FMT>(w[k], ratio) : w[k];
+                    y[k] = 0;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int slot = at + 4 * k + e;
+                        const uint32_t from = slot < p.off ? again : slot < p.off + p.n ? fresh : w[k];
+                        y[k] |= from & (255u << (8 * e));
+                    }
                 }
-                w[j] = y;
             }
-            *at = w;
+            *out = y;
         }
     }
 }
 
-template <int DT, int FMT, int D>
-__global__ __launch_bounds__(256) void kv_append_kernel(AppendView a, int shift, int blocks, RopeView q, int tb) {
-    __shared__ __attribute__((aligned(16))) uint8_t lds[std::max(D * 132, 8 * kRopePairs)];
+template <int DT, int FMT, int D, int PAGE>
+__global__ __launch_bounds__(256) void kv_append_kernel(AppendView a, int blocks, RopeView q, int tb) {
+    constexpr int shift = PAGE == 16 ? 4 : PAGE == 32 ? 5 : PAGE == 64 ? 6 : 7;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[std::max(D * (PAGE + 4), 8 * kRopePairs)];
     __shared__ float red[5];
     __shared__ int2 lp[kRopeTokens];
     const int lane = threadIdx.x & 63;
@@ -333,11 +363,72 @@ __global__ __launch_bounds__(256) void kv_append_kernel(AppendView a, int shift,
     }
     const int which = blockIdx.x & 1, h = (blockIdx.x >> 1) % a.c.Hkv, slot = (blockIdx.x >> 1) / a.c.Hkv;
     PageTokens p;
-    if (!page_tokens(a.c.lens, a.c.cu, a.c.B, a.c.T, shift, slot, lane, p)) return;
-    const int id = page_id(a.c.table, a.c.P, a.c.N, p.b, p.index);
+    if (!page_tokens(a.c.lens, a.c.cu, a.c.B, a.c.T, shift, slot, lane, p) || p.index < 0) return;
+    if (which) append_page<DT, FMT, D, PAGE, true>(a, p, h, lds, red);
+    else append_page<DT, FMT, D, PAGE, false>(a, p, h, lds, red);
+}
+
+// A decode step: one token a sequence, a wave (sequence, head) of K or V, a lane a pair (or two adjacent values).
+template <int DT, int FMT, int D>
+__global__ __launch_bounds__(256) void kv_append_step_kernel(AppendView a, int shift, int blocks, RopeView q) {
+    __shared__ __attribute__((aligned(16))) float cs[2 * 256];
+    __shared__ int2 lp[kRopeTokens];
+    const int tid = threadIdx.x, lane = tid & 63;
+    if ((int)blockIdx.x >= blocks) {            // the queries
+        rope_block<DT, 8>(q, (int)blockIdx.x - blocks, 1, cs, cs + 256, lp);
+        return;
+    }
+    const int item = 4 * blockIdx.x + __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int which = item & 1, h = (item >> 1) % a.c.Hkv, b = (item >> 1) / a.c.Hkv;
+    if (b >= a.c.B) return;
+    const int page = 1 << shift;
+    const uint16_t* row = (which ? a.v + (long long)b * a.vs : a.k + (long long)b * a.ks) + h * D;
+    const bool mine = lane < D / 2, turn = !which && lane < a.half;
+    const int e0 = turn && !a.inter ? lane : 2 * lane, e1 = turn && !a.inter ? lane + a.half : 2 * lane + 1;
+    float x0 = 0.0f, x1 = 0.0f;
+    if (mine) {
+        x0 = in2f<DT>(row[e0]);
+        x1 = in2f<DT>(row[e1]);
+    }
+    const long long f = turn ? a.freqs[lane] : 0;
+    const int place = a.c.lens[b] - 1;
+    if (place < 0) return;
+    const int id = page_id(a.c.table, a.c.P, a.c.N, b, place >> shift), off = place & (page - 1);
     if (id < 0) return;
-    if (which) append_page<DT, FMT, D, true>(a, p, id, h, shift, lds, red);
-    else append_page<DT, FMT, D, false>(a, p, id, h, shift, lds, red);
+    uint8_t* codes = (uint8_t*)(which ? a.c.vc : a.c.kc) + (((long long)id * a.c.Hkv + h) << shift) * D;
+    float* scale = (which ? a.c.vs : a.c.ks) + (long long)id * a.c.Hkv + h;
+    const float old = off > 0 ? *scale : 0.0f;
+    if (turn) {
+        float c, s;
+        position_cos_sin(a.positions ? a.positions[b] : place, f, a.m, c, s);
+        turn_pair(x0, x1, c, s);
+    }
+    const float top = wave_max(fmaxf(size_of(x0), size_of(x1))) / kTop<FMT>;
+    const float s = fmaxf(old, top);
+    if (off > 0 && s > old) {
+        // earlier codes: of K the first off D bytes, of V the first off of every dimension's
+        const float ratio = old / s;
+        const int per = which ? (off + 15) >> 4 : D / 16, lines = which ? D : off;
+        for (int i = lane; i < lines * per; i += 64) {
+            u32x4* at = reinterpret_cast<u32x4*>(codes + (i / per) * (which ? page : D) + 16 * (i % per));
+            u32x4 w = *at;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                // (slots from the new one on are as they were: the new code is written below)
+                const int keep = which ? min(max(off - 16 * (i % per) - 4 * k, 0), 4) : 4;
+                const uint32_t mask = keep == 4 ? ~0u : (1u << (8 * keep)) - 1u;
+                w[k] = (requantize<FMT>(w[k], ratio) & mask) | (w[k] & ~mask);
+            }
+            *at = w;
+        }
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");       // (before other lanes' bytes of the same words)
+    }
+    if (lane == 0 && (off == 0 || s > old)) *scale = s;
+    if (mine) {
+        const uint32_t w = pack_codes<FMT>(s > 0.0f ? x0 / s : 0.0f, s > 0.0f ? x1 / s : 0.0f, 0.0f, 0.0f);
+        codes[which ? e0 * page + off : off * D + e0] = (uint8_t)w;
+        codes[which ? e1 * page + off : off * D + e1] = (uint8_t)(w >> 8);
+    }
 }
 
 // ---------------------------------------------------------------- read
@@ -347,59 +438,117 @@ __device__ __forceinline__ uint32_t two_values(uint32_t w, int byte, float s) {
     return pack2<DT>(code_value<FMT>(w, byte) * s, code_value<FMT>(w, byte + 1) * s);
 }
 
-// One (page, head) of K or V as 16-bit rows; tokens without a page are zeros.
-template <int DT, int FMT, int D>
-__global__ __launch_bounds__(256) void kv_read_kernel(KvPages c, int shift, uint16_t* __restrict__ kout,
-                                                      uint16_t* __restrict__ vout) {
-    __shared__ __attribute__((aligned(16))) uint8_t lds[D * 132];
+// One (page, head) of K and V as 16-bit rows; tokens without a page are zeros.  V's codes go through LDS, four
+// dimensions by four tokens turned round in registers.
+template <int DT, int FMT, int D, int PAGE>
+__global__ __launch_bounds__(256) void kv_read_kernel(KvPages c, uint16_t* __restrict__ kout, uint16_t* __restrict__ vout) {
+    constexpr int shift = PAGE == 16 ? 4 : PAGE == 32 ? 5 : PAGE == 64 ? 6 : 7, UR = D / 8;
+    constexpr int NK = PAGE * UR > 256 ? PAGE * UR / 256 : 1, NV = PAGE * D > 4096 ? PAGE * D / 4096 : 1;
+    constexpr int pitch = PAGE + 4;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[D * pitch];
     const int tid = threadIdx.x, lane = tid & 63;
-    const int across = blockIdx.x & 1, h = (blockIdx.x >> 1) % c.Hkv, slot = (blockIdx.x >> 1) / c.Hkv;
+    const int h = blockIdx.x % c.Hkv, slot = blockIdx.x / c.Hkv;
     PageTokens p;
     if (!page_tokens(c.lens, c.cu, c.B, c.T, shift, slot, lane, p)) return;
-    const int id = page_id(c.table, c.P, c.N, p.b, p.index), page = 1 << shift;
-    uint16_t* out = (across ? vout : kout) + ((long long)p.token * c.Hkv + h) * D;
+    const int id = page_id(c.table, c.P, c.N, p.b, p.index);
     const long long os = (long long)c.Hkv * D;
-    constexpr int UR = D / 8;
+    uint16_t *ko = kout + p.token * os + h * D, *vo = vout + p.token * os + h * D;
     if (id < 0) {
-        for (int u = tid; u < p.n * UR; u += 256)
-            *reinterpret_cast<u32x4*>(out + (u / UR) * os + 8 * (u % UR)) = u32x4{0, 0, 0, 0};
-        return;
-    }
-    const uint8_t* codes = (const uint8_t*)(across ? c.vc : c.kc) + (((long long)id * c.Hkv + h) << shift) * D;
-    const float s = (across ? c.vs : c.ks)[(long long)id * c.Hkv + h];
-    if (!across) {
         for (int u = tid; u < p.n * UR; u += 256) {
-            const int t = u / UR, j = u % UR;
-            const u32x2 w = *reinterpret_cast<const u32x2*>(codes + (p.off + t) * D + 8 * j);
-            *reinterpret_cast<u32x4*>(out + t * os + 8 * j) =
-                u32x4{two_values<FMT, DT>(w[0], 0, s), two_values<FMT, DT>(w[0], 2, s), two_values<FMT, DT>(w[1], 0, s),
-                      two_values<FMT, DT>(w[1], 2, s)};
+            *reinterpret_cast<u32x4*>(ko + (u / UR) * os + 8 * (u % UR)) = u32x4{0, 0, 0, 0};
+            *reinterpret_cast<u32x4*>(vo + (u / UR) * os + 8 * (u % UR)) = u32x4{0, 0, 0, 0};
         }
         return;
     }
-    const int pitch = page + 4, first = p.off >> 4, pieces = ((p.off + p.n + 15) >> 4) - first;
-    for (int i = tid; i < D * pieces; i += 256) {
-        const int d = i / pieces, t0 = 16 * (first + i % pieces);
-        const u32x4 w = *reinterpret_cast<const u32x4*>(codes + d * page + t0);
+    const long long at = (long long)id * c.Hkv + h;
+    const uint8_t *kc = (const uint8_t*)c.kc + at * (PAGE * D), *vc = (const uint8_t*)c.vc + at * (PAGE * D);
+    const float ks = c.ks[at], vs = c.vs[at];
+    u32x4 vw[NV];
+    u32x2 kw[NK];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) *reinterpret_cast<uint32_t*>(lds + d * pitch + t0 + 4 * j) = w[j];
+    for (int i = 0; i < NV; ++i) {
+        const int u = tid + 256 * i, t = 16 * (u % (PAGE / 16));
+        if (u < D * (PAGE / 16) && t + 16 > p.off && t < p.off + p.n) vw[i] = *reinterpret_cast<const u32x4*>(vc + 16 * u);
+    }
+#pragma unroll
+    for (int i = 0; i < NK; ++i) {
+        const int u = tid + 256 * i;
+        if (u < p.n * UR) kw[i] = *reinterpret_cast<const u32x2*>(kc + p.off * D + 8 * u);
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int u = tid + 256 * i, d = u / (PAGE / 16), t = 16 * (u % (PAGE / 16));
+        if (u < D * (PAGE / 16))
+#pragma unroll
+            for (int k = 0; k < 4; ++k) *reinterpret_cast<uint32_t*>(lds + d * pitch + t + 4 * k) = vw[i][k];
+    }
+#pragma unroll
+    for (int i = 0; i < NK; ++i) {
+        const int u = tid + 256 * i;
+        if (u < p.n * UR)
+            *reinterpret_cast<u32x4*>(ko + (u / UR) * os + 8 * (u % UR)) =
+                u32x4{two_values<FMT, DT>(kw[i][0], 0, ks), two_values<FMT, DT>(kw[i][0], 2, ks),
+                      two_values<FMT, DT>(kw[i][1], 0, ks), two_values<FMT, DT>(kw[i][1], 2, ks)};
     }
     __syncthreads();
-    for (int u = tid; u < p.n * UR; u += 256) {
-        const int t = u / UR, j = u % UR;
-        uint32_t w[2] = {0, 0};
+    // units of four tokens of eight dimensions
+    for (int u = tid; u < (PAGE / 4) * UR; u += 256) {
+        const int t4 = 4 * (u / UR), j = u % UR;
+        if (t4 + 4 <= p.off || t4 >= p.off + p.n) continue;
+        u32x4 lo, hi;                           // four tokens' codes of the first and of the last four dimensions
 #pragma unroll
-        for (int e = 0; e < 8; ++e) w[e >> 2] |= (uint32_t)lds[(8 * j + e) * pitch + p.off + t] << (8 * (e & 3));
-        *reinterpret_cast<u32x4*>(out + t * os + 8 * j) =
-            u32x4{two_values<FMT, DT>(w[0], 0, s), two_values<FMT, DT>(w[0], 2, s), two_values<FMT, DT>(w[1], 0, s),
-                  two_values<FMT, DT>(w[1], 2, s)};
+        for (int k = 0; k < 2; ++k) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] = *reinterpret_cast<const uint32_t*>(lds + (8 * j + 4 * k + e) * pitch + t4);
+            const uint32_t a0 = perm(w[1], w[0], 0x05010400u), a1 = perm(w[1], w[0], 0x07030602u);
+            const uint32_t b0 = perm(w[3], w[2], 0x05010400u), b1 = perm(w[3], w[2], 0x07030602u);
+            (k ? hi : lo) = u32x4{perm(b0, a0, 0x05040100u), perm(b0, a0, 0x07060302u), perm(b1, a1, 0x05040100u),
+                                  perm(b1, a1, 0x07060302u)};
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int t = t4 + e - p.off;
+            if (t >= 0 && t < p.n)
+                *reinterpret_cast<u32x4*>(vo + t * os + 8 * j) =
+                    u32x4{two_values<FMT, DT>(lo[e], 0, vs), two_values<FMT, DT>(lo[e], 2, vs),
+                          two_values<FMT, DT>(hi[e], 0, vs), two_values<FMT, DT>(hi[e], 2, vs)};
+        }
     }
 }
 
 int shift_of(int page) { return page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7; }
-// (page, head) blocks of K and of V
-unsigned page_blocks(const KvPages& c) {
-    return (unsigned)((c.cu ? (c.T >> shift_of(c.page)) + 2 * c.B : c.B) * c.Hkv) * 2u;
+// pages that a call may touch
+unsigned page_slots(const KvPages& c) { return (unsigned)(c.cu ? (c.T >> shift_of(c.page)) + 2 * c.B : c.B); }
+
+template <int DT, int FMT, int D>
+hipError_t append(const AppendView& a, const RopeView& q, int tb, unsigned more, hipStream_t st) {
+    const int page = a.c.page;
+    if (!a.c.cu) {
+        const unsigned blocks = ((unsigned)a.c.B * a.c.Hkv * 2 + 3) / 4;
+        hipLaunchKernelGGL((kv_append_step_kernel<DT, FMT, D>), dim3(blocks + more), dim3(256), 0, st, a, shift_of(page),
+                           (int)blocks, q);
+        return hipGetLastError();
+    }
+    const unsigned blocks = page_slots(a.c) * a.c.Hkv * 2;
+#define W4A16_APPEND(PAGE) \
+    hipLaunchKernelGGL((kv_append_kernel<DT, FMT, D, PAGE>), dim3(blocks + more), dim3(256), 0, st, a, (int)blocks, q, tb)
+    if (page == 16) W4A16_APPEND(16);
+    else if (page == 32) W4A16_APPEND(32);
+    else if (page == 64) W4A16_APPEND(64);
+    else W4A16_APPEND(128);
+#undef W4A16_APPEND
+    return hipGetLastError();
+}
+
+template <int DT, int FMT, int D>
+hipError_t read(const KvPages& c, uint16_t* ko, uint16_t* vo, hipStream_t st) {
+    const dim3 grid(page_slots(c) * c.Hkv), block(256);
+    if (c.page == 16) hipLaunchKernelGGL((kv_read_kernel<DT, FMT, D, 16>), grid, block, 0, st, c, ko, vo);
+    else if (c.page == 32) hipLaunchKernelGGL((kv_read_kernel<DT, FMT, D, 32>), grid, block, 0, st, c, ko, vo);
+    else if (c.page == 64) hipLaunchKernelGGL((kv_read_kernel<DT, FMT, D, 64>), grid, block, 0, st, c, ko, vo);
+    else hipLaunchKernelGGL((kv_read_kernel<DT, FMT, D, 128>), grid, block, 0, st, c, ko, vo);
+    return hipGetLastError();
 }
 
 }  // namespace
@@ -434,7 +583,6 @@ hipError_t launch_kv_append(const KvAppendArgs& a, hipStream_t st) {
     v.vs = a.vs;
     v.half = a.R / 2;
     v.inter = a.inter;
-    const int shift = shift_of(a.c.page);
     RopeView r = {};
     int tb = 1;
     unsigned more = 0;
@@ -452,50 +600,27 @@ hipError_t launch_kv_append(const KvAppendArgs& a, hipStream_t st) {
         r.half = v.half;
         r.inter = a.inter;
         r.copy = 1;
-        tb = rope_tokens(r);
-        more = (unsigned)((r.T + tb - 1) / tb);
-        if (!rope_wide(r)) {
+        if (rope_wide(r)) {
+            tb = a.c.cu ? rope_tokens(r) : 1;
+            more = (unsigned)((r.T + tb - 1) / tb);
+        } else {
             const hipError_t e = rope(r, a.dtype, st);
             if (e != hipSuccess) return e;
-            more = 0;
         }
     }
-    const unsigned blocks = page_blocks(a.c);
-#define W4A16_APPEND(DT, FMT, D)                                                                                       \
-    hipLaunchKernelGGL((kv_append_kernel<DT, FMT, D>), dim3(blocks + more), dim3(256), 0, st, v, shift, (int)blocks, r, tb)
-#define W4A16_APPEND_D(DT, FMT) \
-    if (a.c.D == 64) W4A16_APPEND(DT, FMT, 64); \
-    else W4A16_APPEND(DT, FMT, 128)
-    if (a.dtype == DT_F16) {
-        if (a.c.fmt == FMT_INT8) { W4A16_APPEND_D(DT_F16, FMT_INT8); }
-        else { W4A16_APPEND_D(DT_F16, FMT_E4M3); }
-    } else {
-        if (a.c.fmt == FMT_INT8) { W4A16_APPEND_D(DT_BF16, FMT_INT8); }
-        else { W4A16_APPEND_D(DT_BF16, FMT_E4M3); }
-    }
-#undef W4A16_APPEND_D
+#define W4A16_APPEND(DT, FMT) \
+    (a.c.D == 64 ? append<DT, FMT, 64>(v, r, tb, more, st) : append<DT, FMT, 128>(v, r, tb, more, st))
+    if (a.dtype == DT_F16) return a.c.fmt == FMT_INT8 ? W4A16_APPEND(DT_F16, FMT_INT8) : W4A16_APPEND(DT_F16, FMT_E4M3);
+    return a.c.fmt == FMT_INT8 ? W4A16_APPEND(DT_BF16, FMT_INT8) : W4A16_APPEND(DT_BF16, FMT_E4M3);
 #undef W4A16_APPEND
-    return hipGetLastError();
 }
 
 hipError_t launch_kv_read(const KvPages& c, int dtype, void* kout, void* vout, hipStream_t st) {
-    const int shift = shift_of(c.page);
     uint16_t *ko = static_cast<uint16_t*>(kout), *vo = static_cast<uint16_t*>(vout);
-#define W4A16_READ(DT, FMT, D) \
-    hipLaunchKernelGGL((kv_read_kernel<DT, FMT, D>), dim3(page_blocks(c)), dim3(256), 0, st, c, shift, ko, vo)
-#define W4A16_READ_D(DT, FMT) \
-    if (c.D == 64) W4A16_READ(DT, FMT, 64); \
-    else W4A16_READ(DT, FMT, 128)
-    if (dtype == DT_F16) {
-        if (c.fmt == FMT_INT8) { W4A16_READ_D(DT_F16, FMT_INT8); }
-        else { W4A16_READ_D(DT_F16, FMT_E4M3); }
-    } else {
-        if (c.fmt == FMT_INT8) { W4A16_READ_D(DT_BF16, FMT_INT8); }
-        else { W4A16_READ_D(DT_BF16, FMT_E4M3); }
-    }
-#undef W4A16_READ_D
+#define W4A16_READ(DT, FMT) (c.D == 64 ? read<DT, FMT, 64>(c, ko, vo, st) : read<DT, FMT, 128>(c, ko, vo, st))
+    if (dtype == DT_F16) return c.fmt == FMT_INT8 ? W4A16_READ(DT_F16, FMT_INT8) : W4A16_READ(DT_F16, FMT_E4M3);
+    return c.fmt == FMT_INT8 ? W4A16_READ(DT_BF16, FMT_INT8) : W4A16_READ(DT_BF16, FMT_E4M3);
 #undef W4A16_READ
-    return hipGetLastError();
 }
 
 }  // namespace w4a16

@@ -80,6 +80,15 @@ __device__ __forceinline__ void position_cos_sin(int position, long long freq, f
     s *= m;
 }
 
+// One pair turned; in these steps everywhere, so that all ways to a rotation give the same bits (nor is the rounding
+// to 16 bits that may follow taken into the last of them).
+__device__ __forceinline__ void turn_pair(float& x0, float& x1, float c, float s) {
+    const float y = fmaf(x0, c, -(x1 * s));
+    x1 = fmaf(x1, c, x0 * s);
+    x0 = y;
+    asm("" : "+v"(x0), "+v"(x1));
+}
+
 // ---- where tokens are
 
 // The last sequence whose first token is at or before `token` of the T packed ones (64-way search, one
@@ -108,8 +117,18 @@ struct PageTokens {
 };
 __device__ __forceinline__ bool page_tokens(const int* __restrict__ lens, const int* __restrict__ cu, int B, int T,
                                             int shift, int slot, int lane, PageTokens& p) {
-    int b, first, n;
-    if (cu) {
+    int b, first, n, len;
+    if (cu && B <= 64) {
+        // a lane a sequence: everything in one round of loads
+        const int c0 = min(max(cu[min(lane, B)], 0), T), c1 = cu[min(lane + 1, B)];
+        const int ln = lens[min(lane, B - 1)];
+        const unsigned long long m = __builtin_amdgcn_ballot_w64(lane < B && (c0 >> shift) + 2 * lane <= slot);
+        b = m ? 63 - __builtin_clzll(m) : 0;
+        first = __builtin_amdgcn_readlane(c0, b);
+        n = min(max(__builtin_amdgcn_readlane(c1, b), first), T) - first;
+        len = __builtin_amdgcn_readlane(ln, b);
+        slot -= (first >> shift) + 2 * b;
+    } else if (cu) {
         int lo = 0, hi = B;
         while (hi - lo > 1) {
             const int step = (hi - lo + 63) >> 6, at = lo + lane * step;
@@ -122,15 +141,18 @@ __device__ __forceinline__ bool page_tokens(const int* __restrict__ lens, const 
         b = lo;
         first = __builtin_amdgcn_readfirstlane(min(max(cu[b], 0), T));
         n = __builtin_amdgcn_readfirstlane(min(max(cu[b + 1], first), T)) - first;
+        len = __builtin_amdgcn_readfirstlane(lens[b]);
         slot -= (first >> shift) + 2 * b;
     } else {
         b = slot;
         first = slot;
         n = 1;
+        len = __builtin_amdgcn_readfirstlane(lens[b]);
         slot = 0;
     }
     // (a longer sequence than any table holds has no pages there: kept where sums stay in 32 bits)
-    const int len = __builtin_amdgcn_readfirstlane(min(max(lens[b], 0), 1 << 25)), before = len - n;
+    len = min(max(len, 0), 1 << 25);
+    const int before = len - n;
     p.b = b;
     p.index = (before >> shift) + slot;
     const int start = p.index << shift;
