@@ -573,7 +573,7 @@ typedef struct {
  *   out   likewise with out_stride; x itself (and its stride) for a rotation in place, else apart from the inputs.
  *   positions  int32 [T], any values; freqs int64 [R / 2]: the turns per position in units of 2^-64 (as unsigned
  *         numbers: turns modulo 1), so that angles are exact however far the position.
- * Rotated in fp32 and rounded once.  D and R even, 2 <= R <= D <= 512; 1 <= T <= 2^24, 1 <= H <= 65535.
+ * Rotated in fp32 and rounded once.  D and R even, 2 <= R <= D <= 512; 1 <= T < 2^24, 1 <= H <= 65535.
  * Pointers of 2-byte alignment do (4 and 8 for positions and freqs); rotations are widest with x, out and strides multiples of
  * 16 bytes, D of 8 and R of 16.
  */

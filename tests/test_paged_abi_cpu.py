@@ -172,7 +172,7 @@ def rope(lib, **kw):
 
 @pytest.mark.parametrize("kw,status", [
     (dict(x=None), L.ERR_NULL), (dict(pos=None), L.ERR_NULL), (dict(freqs=None), L.ERR_NULL), (dict(out=None), L.ERR_NULL),
-    (dict(dt=2), L.ERR_DTYPE), (dict(T=0), L.ERR_SHAPE), (dict(T=(1 << 24) + 1), L.ERR_SHAPE), (dict(H=0), L.ERR_SHAPE),
+    (dict(dt=2), L.ERR_DTYPE), (dict(T=0), L.ERR_SHAPE), (dict(T=1 << 24), L.ERR_SHAPE), (dict(H=0), L.ERR_SHAPE),
     (dict(H=65536, xs=1 << 24, os=1 << 24), L.ERR_SHAPE), (dict(D=63, R=62), L.ERR_SHAPE), (dict(D=514, xs=4096, os=4096), L.ERR_SHAPE),
     (dict(R=0), L.ERR_SHAPE), (dict(R=66), L.ERR_SHAPE), (dict(R=31), L.ERR_SHAPE), (dict(xs=255), L.ERR_SHAPE),
     (dict(os=255), L.ERR_SHAPE), (dict(out=0x20000000), L.ERR_SHAPE), (dict(x=0x20000001), L.ERR_ALIGN),

@@ -682,7 +682,7 @@ int w4a16_rope(const void* x, int dtype, int64_t T, int64_t H, int64_t D, int64_
                void* stream) {
     if (!x || !positions || !freqs || !out) return W4A16_ERR_NULL;
     if (dtype != W4A16_F16 && dtype != W4A16_BF16) return W4A16_ERR_DTYPE;
-    if (T < 1 || T > kMaxRows || H < 1 || H > 65535 || D < 2 || D > 512 || D % 2 || R < 2 || R > D || R % 2 ||
+    if (T < 1 || T >= kMaxRows || H < 1 || H > 65535 || D < 2 || D > 512 || D % 2 || R < 2 || R > D || R % 2 ||
         !row_stride_ok(x_stride, H * D) || !row_stride_ok(out_stride, H * D) || (x == out && x_stride != out_stride))
         return W4A16_ERR_SHAPE;
     if (!aligned(x, 2) || !aligned(out, 2) || !aligned(positions, 4) || !aligned(freqs, 8)) return W4A16_ERR_ALIGN;

@@ -46,86 +46,64 @@ struct RopeView {
     int inter, copy;        // copy: the values behind R too
 };
 
-constexpr int kRopePairs = 1024;        // (token, pair) angles of a block
-constexpr int kRopeTokens = 4;          // tokens of a block at most
+constexpr int kRopePairs = 256;         // pairs of a head at most
 
+// One token by one block: its angles' cos and sin once into LDS, then all heads, V pairs a thread at a time, two heads
+// asked for at once.  The inputs pass the caches by: most are not read again, and the outputs, which are, find more room
+// there (16384 tokens of 40 heads, D = 128: 70 -> 67 us, with the attention behind it 234 -> 230; outputs
+// past the caches too: 64, but with the attention 237).  More tokens a block were slower (two 63 us, four 67, one 59.6: 5.6 TB/s).
 template <int V>
 struct Piece { typedef u32x4 type; };
 template <>
 struct Piece<1> { typedef uint16_t type; };
 
-// Tokens t0 .. t0 + tb - 1 by one block: their angles' cos and sin once into LDS, then all heads, V pairs
-// a thread at a time.
 template <int DT, int V>
-__device__ __forceinline__ void rope_block(const RopeView& r, int t0, int tb, float* lc, float* ls, int2* lp) {
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    tb = min(tb, r.T - t0);
-    for (int i = wave; i < tb; i += 4) {
-        int p = 0;
-        const bool found = place_of(r.at, t0 + i, lane, p);
-        if (lane == 0) lp[i] = make_int2(p, found);
-    }
-    __syncthreads();
-    for (int i = tid; i < tb * r.half; i += 256) {
-        const int t = i / r.half;
-        position_cos_sin(lp[t].x, r.freqs[i - t * r.half], r.m, lc[i], ls[i]);
-    }
-    __syncthreads();
+__device__ __forceinline__ void rope_token(const RopeView& r, int token, float* lc, float* ls) {
+    typedef typename Piece<V>::type P;
     constexpr int CP = V == 8 ? 8 : 2;                  // values of a copying step
+    const int tid = threadIdx.x, lane = tid & 63;
+    int place = 0;
+    if (!place_of(r.at, token, lane, place)) return;
     const int turns = r.half / V, units = turns + (r.copy ? (r.D - 2 * r.half) / CP : 0);
     const int rows = 256 / units, unit = tid % units, row = tid / units;
-    if (row >= rows) return;
-    const int heads = tb * r.H;
-    const uint16_t* x = r.x + (long long)t0 * r.xs;
-    uint16_t* out = r.out + (long long)t0 * r.os;
     const bool turning = unit < turns;
     // the unit's values: two pieces (of V) of the rotation, or one to copy
     const int p = unit * V, e = 2 * r.half + (unit - turns) * CP;
     const int at0 = turning ? (r.inter ? 2 * p : p) : e, at1 = turning ? (r.inter ? 2 * p + V : p + r.half) : V == 1 ? e + 1 : e;
-    constexpr int AT = 4;                               // rows asked for at a time
-    int t = row / r.H, h = row - t * r.H;
-    for (int i = row; i < heads; i += AT * rows) {
-        int ts[AT], hs[AT];
-        typename Piece<V>::type lo[AT], hi[AT];
+    const uint16_t* x = r.x + (long long)token * r.xs;
+    uint16_t* out = r.out + (long long)token * r.os;
+    if (tid < r.half) position_cos_sin(place, r.freqs[tid], r.m, lc[tid], ls[tid]);
+    __syncthreads();
+    if (row >= rows) return;
+    constexpr int AT = 2;
+    for (int h0 = row; h0 < r.H; h0 += AT * rows) {
+        P lo[AT], hi[AT];
 #pragma unroll
         for (int j = 0; j < AT; ++j) {
-            ts[j] = t < tb && lp[t].y ? t : -1;
-            hs[j] = h;
-            if (ts[j] >= 0) {
-                const uint16_t* px = x + (long long)t * r.xs + h * r.D;
-                lo[j] = *reinterpret_cast<const typename Piece<V>::type*>(px + at0);
-                hi[j] = *reinterpret_cast<const typename Piece<V>::type*>(px + at1);
-            }
-            h += rows;
-            while (h >= r.H) {
-                h -= r.H;
-                ++t;
-            }
+            const int h = min(h0 + j * rows, r.H - 1);
+            lo[j] = __builtin_nontemporal_load(reinterpret_cast<const P*>(x + h * r.D + at0));
+            hi[j] = __builtin_nontemporal_load(reinterpret_cast<const P*>(x + h * r.D + at1));
         }
 #pragma unroll
         for (int j = 0; j < AT; ++j) {
-            if (ts[j] < 0) continue;
-            uint16_t* po = out + (long long)ts[j] * r.os + hs[j] * r.D;
+            const int h = h0 + j * rows;
+            if (h >= r.H) break;
             if (turning) {
-                const float *c = lc + ts[j] * r.half + p, *s = ls + ts[j] * r.half + p;
+                const float *c = lc + p, *s = ls + p;
                 if constexpr (V == 8) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
+                        float x0 = in2f<DT>(lo[j][k] & 0xFFFFu), x1 = in2f<DT>(lo[j][k] >> 16);
+                        float z0 = in2f<DT>(hi[j][k] & 0xFFFFu), z1 = in2f<DT>(hi[j][k] >> 16);
                         if (r.inter) {
-                            float x0 = in2f<DT>(lo[j][k] & 0xFFFFu), x1 = in2f<DT>(lo[j][k] >> 16);
-                            float z0 = in2f<DT>(hi[j][k] & 0xFFFFu), z1 = in2f<DT>(hi[j][k] >> 16);
                             turn_pair(x0, x1, c[k], s[k]);
                             turn_pair(z0, z1, c[k + 4], s[k + 4]);
-                            lo[j][k] = pack2<DT>(x0, x1);
-                            hi[j][k] = pack2<DT>(z0, z1);
                         } else {
-                            float x0 = in2f<DT>(lo[j][k] & 0xFFFFu), x1 = in2f<DT>(lo[j][k] >> 16);
-                            float z0 = in2f<DT>(hi[j][k] & 0xFFFFu), z1 = in2f<DT>(hi[j][k] >> 16);
                             turn_pair(x0, z0, c[2 * k], s[2 * k]);
                             turn_pair(x1, z1, c[2 * k + 1], s[2 * k + 1]);
-                            lo[j][k] = pack2<DT>(x0, x1);
-                            hi[j][k] = pack2<DT>(z0, z1);
                         }
+                        lo[j][k] = pack2<DT>(x0, x1);
+                        hi[j][k] = pack2<DT>(z0, z1);
                     }
                 } else {
                     float x0 = in2f<DT>(lo[j]), x1 = in2f<DT>(hi[j]);
@@ -134,35 +112,32 @@ __device__ __forceinline__ void rope_block(const RopeView& r, int t0, int tb, fl
                     hi[j] = f2out<DT>(x1);
                 }
             }
-            *reinterpret_cast<typename Piece<V>::type*>(po + at0) = lo[j];
-            if (turning || V == 1) *reinterpret_cast<typename Piece<V>::type*>(po + at1) = hi[j];
+            uint16_t* po = out + h * r.D;
+            *reinterpret_cast<P*>(po + at0) = lo[j];
+            if (turning || V == 1) *reinterpret_cast<P*>(po + at1) = hi[j];
         }
     }
 }
 
 template <int DT, int V>
-__global__ __launch_bounds__(256) void rope_kernel(RopeView r, int tb) {
+__global__ __launch_bounds__(256) void rope_kernel(RopeView r) {
     __shared__ __attribute__((aligned(16))) float lc[kRopePairs], ls[kRopePairs];
-    __shared__ int2 lp[kRopeTokens];
-    rope_block<DT, V>(r, blockIdx.x * tb, tb, lc, ls, lp);
+    rope_token<DT, V>(r, blockIdx.x, lc, ls);
 }
 
 bool rope_wide(const RopeView& r) {
     const auto at16 = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
     return r.half % 8 == 0 && r.D % 8 == 0 && r.xs % 8 == 0 && r.os % 8 == 0 && at16(r.x) && at16(r.out);
 }
-// Tokens of a block.
-int rope_tokens(const RopeView& r) { return std::max(1, std::min({kRopeTokens, kRopePairs / std::max(1, r.half), r.T / 1024})); }
 
 hipError_t rope(const RopeView& r, int dtype, hipStream_t st) {
-    const int tb = rope_tokens(r);
-    const dim3 grid((unsigned)((r.T + tb - 1) / tb)), block(256);
+    const dim3 grid((unsigned)r.T), block(256);
     if (rope_wide(r)) {
-        if (dtype == DT_F16) hipLaunchKernelGGL((rope_kernel<DT_F16, 8>), grid, block, 0, st, r, tb);
-        else hipLaunchKernelGGL((rope_kernel<DT_BF16, 8>), grid, block, 0, st, r, tb);
+        if (dtype == DT_F16) hipLaunchKernelGGL((rope_kernel<DT_F16, 8>), grid, block, 0, st, r);
+        else hipLaunchKernelGGL((rope_kernel<DT_BF16, 8>), grid, block, 0, st, r);
     } else {
-        if (dtype == DT_F16) hipLaunchKernelGGL((rope_kernel<DT_F16, 1>), grid, block, 0, st, r, tb);
-        else hipLaunchKernelGGL((rope_kernel<DT_BF16, 1>), grid, block, 0, st, r, tb);
+        if (dtype == DT_F16) hipLaunchKernelGGL((rope_kernel<DT_F16, 1>), grid, block, 0, st, r);
+        else hipLaunchKernelGGL((rope_kernel<DT_BF16, 1>), grid, block, 0, st, r);
     }
     return hipGetLastError();
 }
@@ -350,15 +325,14 @@ __device__ __forceinline__ void append_page(const AppendView& a, const PageToken
 }
 
 template <int DT, int FMT, int D, int PAGE>
-__global__ __launch_bounds__(256) void kv_append_kernel(AppendView a, int blocks, RopeView q, int tb) {
+__global__ __launch_bounds__(256) void kv_append_kernel(AppendView a, int blocks, RopeView q) {
     constexpr int shift = PAGE == 16 ? 4 : PAGE == 32 ? 5 : PAGE == 64 ? 6 : 7;
     __shared__ __attribute__((aligned(16))) uint8_t lds[std::max(D * (PAGE + 4), 8 * kRopePairs)];
     __shared__ float red[5];
-    __shared__ int2 lp[kRopeTokens];
     const int lane = threadIdx.x & 63;
     if ((int)blockIdx.x >= blocks) {            // the queries
         float* cs = reinterpret_cast<float*>(lds);
-        rope_block<DT, 8>(q, ((int)blockIdx.x - blocks) * tb, tb, cs, cs + kRopePairs, lp);
+        rope_token<DT, 8>(q, (int)blockIdx.x - blocks, cs, cs + kRopePairs);
         return;
     }
     const int which = blockIdx.x & 1, h = (blockIdx.x >> 1) % a.c.Hkv, slot = (blockIdx.x >> 1) / a.c.Hkv;
@@ -371,11 +345,10 @@ __global__ __launch_bounds__(256) void kv_append_kernel(AppendView a, int blocks
 // A decode step: one token a sequence, a wave (sequence, head) of K or V, a lane a pair (or two adjacent values).
 template <int DT, int FMT, int D>
 __global__ __launch_bounds__(256) void kv_append_step_kernel(AppendView a, int shift, int blocks, RopeView q) {
-    __shared__ __attribute__((aligned(16))) float cs[2 * 256];
-    __shared__ int2 lp[kRopeTokens];
+    __shared__ __attribute__((aligned(16))) float cs[2 * kRopePairs];
     const int tid = threadIdx.x, lane = tid & 63;
     if ((int)blockIdx.x >= blocks) {            // the queries
-        rope_block<DT, 8>(q, (int)blockIdx.x - blocks, 1, cs, cs + 256, lp);
+        rope_token<DT, 8>(q, (int)blockIdx.x - blocks, cs, cs + kRopePairs);
         return;
     }
     const int item = 4 * blockIdx.x + __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -522,7 +495,7 @@ int shift_of(int page) { return page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6
 unsigned page_slots(const KvPages& c) { return (unsigned)(c.cu ? (c.T >> shift_of(c.page)) + 2 * c.B : c.B); }
 
 template <int DT, int FMT, int D>
-hipError_t append(const AppendView& a, const RopeView& q, int tb, unsigned more, hipStream_t st) {
+hipError_t append(const AppendView& a, const RopeView& q, unsigned more, hipStream_t st) {
     const int page = a.c.page;
     if (!a.c.cu) {
         const unsigned blocks = ((unsigned)a.c.B * a.c.Hkv * 2 + 3) / 4;
@@ -532,7 +505,7 @@ hipError_t append(const AppendView& a, const RopeView& q, int tb, unsigned more,
     }
     const unsigned blocks = page_slots(a.c) * a.c.Hkv * 2;
 #define W4A16_APPEND(PAGE) \
-    hipLaunchKernelGGL((kv_append_kernel<DT, FMT, D, PAGE>), dim3(blocks + more), dim3(256), 0, st, a, (int)blocks, q, tb)
+    hipLaunchKernelGGL((kv_append_kernel<DT, FMT, D, PAGE>), dim3(blocks + more), dim3(256), 0, st, a, (int)blocks, q)
     if (page == 16) W4A16_APPEND(16);
     else if (page == 32) W4A16_APPEND(32);
     else if (page == 64) W4A16_APPEND(64);
@@ -584,7 +557,6 @@ hipError_t launch_kv_append(const KvAppendArgs& a, hipStream_t st) {
     v.half = a.R / 2;
     v.inter = a.inter;
     RopeView r = {};
-    int tb = 1;
     unsigned more = 0;
     if (a.q) {
         r.x = static_cast<const uint16_t*>(a.q);
@@ -601,15 +573,14 @@ hipError_t launch_kv_append(const KvAppendArgs& a, hipStream_t st) {
         r.inter = a.inter;
         r.copy = 1;
         if (rope_wide(r)) {
-            tb = a.c.cu ? rope_tokens(r) : 1;
-            more = (unsigned)((r.T + tb - 1) / tb);
+            more = (unsigned)r.T;
         } else {
             const hipError_t e = rope(r, a.dtype, st);
             if (e != hipSuccess) return e;
         }
     }
 #define W4A16_APPEND(DT, FMT) \
-    (a.c.D == 64 ? append<DT, FMT, 64>(v, r, tb, more, st) : append<DT, FMT, 128>(v, r, tb, more, st))
+    (a.c.D == 64 ? append<DT, FMT, 64>(v, r, more, st) : append<DT, FMT, 128>(v, r, more, st))
     if (a.dtype == DT_F16) return a.c.fmt == FMT_INT8 ? W4A16_APPEND(DT_F16, FMT_INT8) : W4A16_APPEND(DT_F16, FMT_E4M3);
     return a.c.fmt == FMT_INT8 ? W4A16_APPEND(DT_BF16, FMT_INT8) : W4A16_APPEND(DT_BF16, FMT_E4M3);
 #undef W4A16_APPEND
