@@ -57,11 +57,11 @@ struct Piece { typedef u32x4 type; };
 template <>
 struct Piece<1> { typedef uint16_t type; };
 
-template <int DT, int V>
+template <int DT, int V, int AT>
 __device__ __forceinline__ void rope_token(const RopeView& r, int token, float* lc, float* ls) {
     typedef typename Piece<V>::type P;
     constexpr int CP = V == 8 ? 8 : 2;                  // values of a copying step
-    const int tid = threadIdx.x, lane = tid & 63;
+    const int tid = threadIdx.x & 255, lane = tid & 63;
     int place = 0;
     if (!place_of(r.at, token, lane, place)) return;
     const int turns = r.half / V, units = turns + (r.copy ? (r.D - 2 * r.half) / CP : 0);
@@ -75,7 +75,6 @@ __device__ __forceinline__ void rope_token(const RopeView& r, int token, float* 
     if (tid < r.half) position_cos_sin(place, r.freqs[tid], r.m, lc[tid], ls[tid]);
     __syncthreads();
     if (row >= rows) return;
-    constexpr int AT = 2;
     for (int h0 = row; h0 < r.H; h0 += AT * rows) {
         P lo[AT], hi[AT];
 #pragma unroll
@@ -122,7 +121,7 @@ __device__ __forceinline__ void rope_token(const RopeView& r, int token, float* 
 template <int DT, int V>
 __global__ __launch_bounds__(256) void rope_kernel(RopeView r) {
     __shared__ __attribute__((aligned(16))) float lc[kRopePairs], ls[kRopePairs];
-    rope_token<DT, V>(r, blockIdx.x, lc, ls);
+    rope_token<DT, V, 2>(r, blockIdx.x, lc, ls);
 }
 
 bool rope_wide(const RopeView& r) {
@@ -169,14 +168,21 @@ struct AppendView {
     int half, inter;        // half: R / 2 (0: no rotation)
 };
 
-// One (page, head) of K (ACROSS false: rows, rotated) or V (columns).  Thread units of eight values: of K four
-// pairs (p .. p + 3 of the rotation, or eight adjacent values behind it), of V eight adjacent ones.
+// Heads h0 .. h1 - 1 of one page of K (ACROSS false: rows, rotated) or V (columns).  Thread units of eight values: of K
+// four pairs (p .. p + 3 of the rotation, or eight adjacent values behind it), of V eight adjacent ones.  A thread's
+// units are of the same tokens and pairs for every head: their angles are computed once.  (A head's rows asked for
+// while the one before is worked on: no faster, and half as fast with pages of 128, for its registers.)
+// Threads of a block: at most four units each.
+constexpr int append_threads(int D, int page) { return page * D >= 8192 ? 512 : 256; }
+
 template <int DT, int FMT, int D, int PAGE, bool ACROSS>
-__device__ __forceinline__ void append_page(const AppendView& a, const PageTokens& p, int h, uint8_t* lds, float* red) {
-    constexpr int UR = D / 8, UNITS = PAGE * UR > 256 ? PAGE * UR / 256 : 1;       // units of a row; of a thread
+__device__ __forceinline__ void append_page(const AppendView& a, const PageTokens& p, int h0, int h1, uint8_t* lds,
+                                            float (*red)[9]) {
+    constexpr int NT = append_threads(D, PAGE);
+    constexpr int UR = D / 8, UNITS = PAGE * UR > NT ? PAGE * UR / NT : 1;         // units of a row; of a thread
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int total = p.n * UR, j = tid % UR, t0 = tid / UR;       // unit i of a thread: token t0 + 256 / UR i, values of j
-    const uint16_t* src = (ACROSS ? a.v : a.k) + h * D;
+    const int total = p.n * UR, j = tid % UR, t0 = tid / UR;       // unit i of a thread: token t0 + NT / UR i, values of j
+    const uint16_t* src = ACROSS ? a.v : a.k;
     const int stride = ACROSS ? a.vs : a.ks;
 
     // a unit's values: of four pairs (first, second) in a word each, or eight in a row
@@ -184,171 +190,217 @@ __device__ __forceinline__ void append_page(const AppendView& a, const PageToken
     const bool turns = !ACROSS && 4 * j < a.half;
     const bool halves = turns && !a.inter && a.half % 4 == 0;      // two pieces of four values
     const bool loose = turns && !a.inter && a.half % 4 != 0;       // value by value
+    auto load = [&](int h) {
 #pragma unroll
-    for (int i = 0; i < UNITS; ++i) {
-        if (256 * i >= total) break;
-        const uint16_t* row = src + (long long)(p.token + min(t0 + 256 / UR * i, p.n - 1)) * stride;
-        if (halves) {
-            const u32x2 lo = *reinterpret_cast<const u32x2*>(row + 4 * j), hi = *reinterpret_cast<const u32x2*>(row + a.half + 4 * j);
-            raw[i] = u32x4{perm(hi[0], lo[0], 0x05040100u), perm(hi[0], lo[0], 0x07060302u), perm(hi[1], lo[1], 0x05040100u),
-                           perm(hi[1], lo[1], 0x07060302u)};
-        } else if (loose) {
+        for (int i = 0; i < UNITS; ++i) {
+            if (NT * i >= total) break;
+            const uint16_t* row = src + (long long)(p.token + min(t0 + NT / UR * i, p.n - 1)) * stride + h * D;
+            if (halves) {
+                const u32x2 lo = *reinterpret_cast<const u32x2*>(row + 4 * j);
+                const u32x2 hi = *reinterpret_cast<const u32x2*>(row + a.half + 4 * j);
+                raw[i] = u32x4{lo[0], lo[1], hi[0], hi[1]};
+            } else if (loose) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int q = 4 * j + e;
-                const bool turn = q < a.half;
-                raw[i][e] = row[turn ? q : 2 * q] | (uint32_t)row[turn ? q + a.half : 2 * q + 1] << 16;
-            }
-        } else raw[i] = *reinterpret_cast<const u32x4*>(row + 8 * j);
-    }
-    long long f[4];
-    if (turns) {
+                for (int e = 0; e < 4; ++e) {
+                    const int q = 4 * j + e;
+                    const bool turn = q < a.half;
+                    raw[i][e] = row[turn ? q : 2 * q] | (uint32_t)row[turn ? q + a.half : 2 * q + 1] << 16;
+                }
+            } else raw[i] = *reinterpret_cast<const u32x4*>(row + 8 * j);
+        }
+    };
+    load(h0);
+    float cs[ACROSS ? 1 : UNITS][8];            // cos and sin of a unit's pairs
+    if (!ACROSS && turns) {
+        long long f[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) f[e] = a.freqs[min(4 * j + e, a.half - 1)];
+#pragma unroll
+        for (int i = 0; i < UNITS; ++i) {
+            if (NT * i >= total) break;
+            const int t = min(t0 + NT / UR * i, p.n - 1);
+            const int position = a.positions ? a.positions[p.token + t] : p.index * PAGE + p.off + t;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                cs[ACROSS ? 0 : i][2 * e] = 1.0f;
+                cs[ACROSS ? 0 : i][2 * e + 1] = 0.0f;
+                if (4 * j + e < a.half) position_cos_sin(position, f[e], a.m, cs[ACROSS ? 0 : i][2 * e], cs[ACROSS ? 0 : i][2 * e + 1]);
+            }
+        }
     }
     const int id = page_id(a.c.table, a.c.P, a.c.N, p.b, p.index);
     if (id < 0) return;
-    uint8_t* codes = (uint8_t*)(ACROSS ? a.c.vc : a.c.kc) + ((long long)id * a.c.Hkv + h) * (PAGE * D);
-    float* scale = (ACROSS ? a.c.vs : a.c.ks) + (long long)id * a.c.Hkv + h;
-    if (tid == 0) red[4] = p.off > 0 ? *scale : 0.0f;      // (read by the thread that writes it)
+    float* scale = (ACROSS ? a.c.vs : a.c.ks) + (long long)id * a.c.Hkv + h0;
 
-    float x[UNITS][8];
-    float top = 0.0f;
-#pragma unroll
-    for (int i = 0; i < UNITS; ++i) {
-        const int t = t0 + 256 / UR * i;
-        if (256 * i >= total) break;
-        if (t < p.n) {
-            int position = 0;
-            if (turns) position = a.positions ? a.positions[p.token + t] : p.index * PAGE + p.off + t;
+#pragma unroll 1
+    for (int h = h0; h < h1; ++h, ++scale) {
+        uint8_t* codes = (uint8_t*)(ACROSS ? a.c.vc : a.c.kc) + ((long long)id * a.c.Hkv + h) * (PAGE * D);
+        float* r = red[h & 1];
+        if (h > h0) load(h);
+        if (tid == 0) r[8] = p.off > 0 ? *scale : 0.0f;         // (read by the thread that writes it)
+        // (turned here for the largest, and again for the codes: that is less than holding them in 32 bits)
+        auto values = [&](int i, float (&x)[8]) {
+            const u32x4 w = halves ? u32x4{perm(raw[i][2], raw[i][0], 0x05040100u), perm(raw[i][2], raw[i][0], 0x07060302u),
+                                           perm(raw[i][3], raw[i][1], 0x05040100u), perm(raw[i][3], raw[i][1], 0x07060302u)}
+                                   : raw[i];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                x[i][2 * e] = in2f<DT>(raw[i][e] & 0xFFFFu);
-                x[i][2 * e + 1] = in2f<DT>(raw[i][e] >> 16);
-                if (turns && 4 * j + e < a.half) {
-                    float c, s;
-                    position_cos_sin(position, f[e], a.m, c, s);
-                    turn_pair(x[i][2 * e], x[i][2 * e + 1], c, s);
-                }
+                x[2 * e] = in2f<DT>(w[e] & 0xFFFFu);
+                x[2 * e + 1] = in2f<DT>(w[e] >> 16);
+                if (!ACROSS && turns && 4 * j + e < a.half)
+                    turn_pair(x[2 * e], x[2 * e + 1], cs[ACROSS ? 0 : i][2 * e], cs[ACROSS ? 0 : i][2 * e + 1]);
             }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) top = fmaxf(top, size_of(x[i][e]));
-        }
-    }
-    top = wave_max(top);
-    if (lane == 0) red[wave] = top;
-    __syncthreads();
-    const float old = red[4];
-    top = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])) / kTop<FMT>;
-    const float s = fmaxf(old, top);
-    const bool grown = p.off > 0 && s > old;
-    const float ratio = old / s;
-    if (tid == 0 && (grown || p.off == 0)) *scale = s;
-    auto quotient = [&](float v) { return s > 0.0f ? v / s : 0.0f; };
-
-    if constexpr (!ACROSS) {
-        if (grown)
-            for (int i = tid; i < p.off * D / 16; i += 256) {
-                u32x4 w = reinterpret_cast<u32x4*>(codes)[i];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) w[e] = requantize<FMT>(w[e], ratio);
-                reinterpret_cast<u32x4*>(codes)[i] = w;
-            }
+        };
+        uint32_t bits = 0;                      // the largest |x|, as its bits: at least those of infinity if one is no number
 #pragma unroll
         for (int i = 0; i < UNITS; ++i) {
-            const int t = t0 + 256 / UR * i;
-            if (t >= p.n) break;
-            uint8_t* row = codes + (p.off + t) * D;
-            float y[8];
+            if (NT * i >= total) break;
+            float x[8];
+            values(i, x);
+            if (t0 + NT / UR * i < p.n)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = quotient(x[i][e]);
-            if (halves) {
-                *reinterpret_cast<uint32_t*>(row + 4 * j) = pack_codes<FMT>(y[0], y[2], y[4], y[6]);
-                *reinterpret_cast<uint32_t*>(row + a.half + 4 * j) = pack_codes<FMT>(y[1], y[3], y[5], y[7]);
-            } else {
-                const uint32_t w[2] = {pack_codes<FMT>(y[0], y[1], y[2], y[3]), pack_codes<FMT>(y[4], y[5], y[6], y[7])};
-                if (!loose) *reinterpret_cast<u32x2*>(row + 8 * j) = u32x2{w[0], w[1]};
-                else
+                for (int e = 0; e < 8; ++e) bits = max(bits, __builtin_bit_cast(uint32_t, x[e]) & 0x7FFFFFFFu);
+        }
+        float top = __builtin_bit_cast(float, bits);
+        const bool odd = bits >= 0x7F800000u;
+        if (odd) {
+            top = 0.0f;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int q = 4 * j + e;
-                        const bool turn = q < a.half;
-                        row[turn ? q : 2 * q] = (uint8_t)(w[e >> 1] >> (16 * (e & 1)));
-                        row[turn ? q + a.half : 2 * q + 1] = (uint8_t)(w[e >> 1] >> (16 * (e & 1) + 8));
-                    }
+            for (int i = 0; i < UNITS; ++i) {
+                if (t0 + NT / UR * i >= p.n) break;
+                float x[8];
+                values(i, x);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) top = fmaxf(top, size_of(x[e]));
             }
         }
-    } else {
-        // through LDS, so that a dimension's tokens are stored together
-        constexpr int pitch = PAGE + 4;
-#pragma unroll
-        for (int i = 0; i < UNITS; ++i) {
-            const int t = t0 + 256 / UR * i;
-            if (t >= p.n) break;
-            float y[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = quotient(x[i][e]);
-            const uint32_t w[2] = {pack_codes<FMT>(y[0], y[1], y[2], y[3]), pack_codes<FMT>(y[4], y[5], y[6], y[7])};
-#pragma unroll
-            for (int e = 0; e < 8; ++e) lds[(8 * j + e) * pitch + p.off + t] = (uint8_t)(w[e >> 2] >> (8 * (e & 3)));
-        }
+        top = wave_max(top);
+        if (lane == 0) r[wave] = top;
         __syncthreads();
-        // pieces of 16 tokens of a dimension: the earlier tokens' codes (rounded again), the new ones, and what
-        // lies behind them as it was
-        const int first = grown ? 0 : p.off >> 4, pieces = ((p.off + p.n + 15) >> 4) - first;
-        for (int i = tid; i < D * (PAGE / 16); i += 256) {
-            const int d = i / (PAGE / 16), piece = i % (PAGE / 16), at = 16 * piece;
-            if (piece < first || piece >= first + pieces) continue;
-            u32x4* out = reinterpret_cast<u32x4*>(codes + d * PAGE + at);
-            u32x4 w = {0, 0, 0, 0}, y;
-            if (at >= p.off && at + 16 <= p.off + p.n) {
+        const float old = r[8];
+        top = r[0];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) y[k] = *reinterpret_cast<const uint32_t*>(lds + d * pitch + at + 4 * k);
-            } else {
-                w = *out;
+        for (int i = 1; i < NT / 64; ++i) top = fmaxf(top, r[i]);
+        top /= kTop<FMT>;
+        const float s = fmaxf(old, top);
+        const bool grown = p.off > 0 && s > old;
+        const float ratio = old / s;
+        if (tid == 0 && (grown || p.off == 0)) *scale = s;
+        const Divisor by(s);
+        // eight values' codes, the first four and the last in the order a, b, c, d of `order`
+        auto pack = [&](const float (&v)[8], int i0, int i1, int i2, int i3) {
+            if (by.plain && !odd)
+                return pack_numbers<FMT>(by.quotient(v[i0]), by.quotient(v[i1]), by.quotient(v[i2]), by.quotient(v[i3]));
+            const auto q = [&](float y) { return s > 0.0f ? y / s : 0.0f; };
+            return pack_codes<FMT>(q(v[i0]), q(v[i1]), q(v[i2]), q(v[i3]));
+        };
+
+        if constexpr (!ACROSS) {
+            if (grown)
+                for (int i = tid; i < p.off * D / 16; i += NT) {
+                    u32x4 w = reinterpret_cast<u32x4*>(codes)[i];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint32_t fresh = *reinterpret_cast<const uint32_t*>(lds + d * pitch + at + 4 * k);
-                    const uint32_t again = grown && at + 4 * k < p.off ? requantize<FMT>(w[k], ratio) : w[k];
-                    y[k] = 0;
+                    for (int e = 0; e < 4; ++e) w[e] = requantize<FMT>(w[e], ratio);
+                    reinterpret_cast<u32x4*>(codes)[i] = w;
+                }
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int slot = at + 4 * k + e;
-                        const uint32_t from = slot < p.off ? again : slot < p.off + p.n ? fresh : w[k];
-                        y[k] |= from & (255u << (8 * e));
-                    }
+            for (int i = 0; i < UNITS; ++i) {
+                const int t = t0 + NT / UR * i;
+                if (t >= p.n) break;
+                uint8_t* row = codes + (p.off + t) * D;
+                float x[8];
+                values(i, x);
+                if (halves) {
+                    *reinterpret_cast<uint32_t*>(row + 4 * j) = pack(x, 0, 2, 4, 6);
+                    *reinterpret_cast<uint32_t*>(row + a.half + 4 * j) = pack(x, 1, 3, 5, 7);
+                } else {
+                    const uint32_t w[2] = {pack(x, 0, 1, 2, 3), pack(x, 4, 5, 6, 7)};
+                    if (!loose) *reinterpret_cast<u32x2*>(row + 8 * j) = u32x2{w[0], w[1]};
+                    else
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int q = 4 * j + e;
+                            const bool turn = q < a.half;
+                            row[turn ? q : 2 * q] = (uint8_t)(w[e >> 1] >> (16 * (e & 1)));
+                            row[turn ? q + a.half : 2 * q + 1] = (uint8_t)(w[e >> 1] >> (16 * (e & 1) + 8));
+                        }
                 }
             }
-            *out = y;
+        } else {
+            // through LDS, so that a dimension's tokens are stored together
+            constexpr int pitch = PAGE + 4;
+#pragma unroll
+            for (int i = 0; i < UNITS; ++i) {
+                const int t = t0 + NT / UR * i;
+                if (t >= p.n) break;
+                float x[8];
+                values(i, x);
+                const uint32_t w[2] = {pack(x, 0, 1, 2, 3), pack(x, 4, 5, 6, 7)};
+#pragma unroll
+                for (int e = 0; e < 8; ++e) lds[(8 * j + e) * pitch + p.off + t] = (uint8_t)(w[e >> 2] >> (8 * (e & 3)));
+            }
+            __syncthreads();
+            // pieces of 16 tokens of a dimension: the earlier tokens' codes (rounded again), the new ones, and what
+            // lies behind them as it was
+            const int first = grown ? 0 : p.off >> 4, pieces = ((p.off + p.n + 15) >> 4) - first;
+            for (int i = tid; i < D * (PAGE / 16); i += NT) {
+                const int d = i / (PAGE / 16), piece = i % (PAGE / 16), at = 16 * piece;
+                if (piece < first || piece >= first + pieces) continue;
+                u32x4* out = reinterpret_cast<u32x4*>(codes + d * PAGE + at);
+                u32x4 w = {0, 0, 0, 0}, y;
+                if (at >= p.off && at + 16 <= p.off + p.n) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) y[k] = *reinterpret_cast<const uint32_t*>(lds + d * pitch + at + 4 * k);
+                } else {
+                    w = *out;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t fresh = *reinterpret_cast<const uint32_t*>(lds + d * pitch + at + 4 * k);
+                        const uint32_t again = grown && at + 4 * k < p.off ? requantize<FMT>(w[k], ratio) : w[k];
+                        y[k] = 0;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int slot = at + 4 * k + e;
+                            const uint32_t from = slot < p.off ? again : slot < p.off + p.n ? fresh : w[k];
+                            y[k] |= from & (255u << (8 * e));
+                        }
+                    }
+                }
+                *out = y;
+            }
         }
     }
 }
 
 template <int DT, int FMT, int D, int PAGE>
-__global__ __launch_bounds__(256) void kv_append_kernel(AppendView a, int blocks, RopeView q) {
+__global__ __launch_bounds__(append_threads(D, PAGE)) void kv_append_kernel(AppendView a, int blocks, int groups, RopeView q) {
     constexpr int shift = PAGE == 16 ? 4 : PAGE == 32 ? 5 : PAGE == 64 ? 6 : 7;
-    __shared__ __attribute__((aligned(16))) uint8_t lds[std::max(D * (PAGE + 4), 8 * kRopePairs)];
-    __shared__ float red[5];
+    __shared__ __attribute__((aligned(16))) uint8_t lds[std::max(D * (PAGE + 4), 8 * kRopePairs * (append_threads(D, PAGE) / 256))];
+    __shared__ float red[2][9];
     const int lane = threadIdx.x & 63;
-    if ((int)blockIdx.x >= blocks) {            // the queries
-        float* cs = reinterpret_cast<float*>(lds);
-        rope_token<DT, 8>(q, (int)blockIdx.x - blocks, cs, cs + kRopePairs);
+    if ((int)blockIdx.x >= blocks) {            // the queries, a token 256 threads
+        constexpr int TOKENS = append_threads(D, PAGE) / 256;
+        const int mine = __builtin_amdgcn_readfirstlane(threadIdx.x >> 8);
+        float* cs = reinterpret_cast<float*>(lds) + 2 * kRopePairs * mine;
+        const int token = ((int)blockIdx.x - blocks) * TOKENS + mine;
+        if (token < q.T) rope_token<DT, 8, 1>(q, token, cs, cs + kRopePairs);
         return;
     }
-    const int which = blockIdx.x & 1, h = (blockIdx.x >> 1) % a.c.Hkv, slot = (blockIdx.x >> 1) / a.c.Hkv;
+    const int which = blockIdx.x & 1, group = (blockIdx.x >> 1) % groups, slot = (blockIdx.x >> 1) / groups;
+    const int h0 = group * a.c.Hkv / groups, h1 = (group + 1) * a.c.Hkv / groups;
     PageTokens p;
     if (!page_tokens(a.c.lens, a.c.cu, a.c.B, a.c.T, shift, slot, lane, p) || p.index < 0) return;
-    if (which) append_page<DT, FMT, D, PAGE, true>(a, p, h, lds, red);
-    else append_page<DT, FMT, D, PAGE, false>(a, p, h, lds, red);
+    if (which) append_page<DT, FMT, D, PAGE, true>(a, p, h0, h1, lds, red);
+    else append_page<DT, FMT, D, PAGE, false>(a, p, h0, h1, lds, red);
 }
 
 // A decode step: one token a sequence, a wave (sequence, head) of K or V, a lane a pair (or two adjacent values).
 template <int DT, int FMT, int D>
-__global__ __launch_bounds__(256) void kv_append_step_kernel(AppendView a, int shift, int blocks, RopeView q) {
+__global__ __launch_bounds__(256, 8) void kv_append_step_kernel(AppendView a, int shift, int blocks, RopeView q) {
     __shared__ __attribute__((aligned(16))) float cs[2 * kRopePairs];
     const int tid = threadIdx.x, lane = tid & 63;
     if ((int)blockIdx.x >= blocks) {            // the queries
-        rope_token<DT, 8>(q, (int)blockIdx.x - blocks, cs, cs + kRopePairs);
+        rope_token<DT, 8, 1>(q, (int)blockIdx.x - blocks, cs, cs + kRopePairs);
         return;
     }
     const int item = 4 * blockIdx.x + __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -491,6 +543,10 @@ __global__ __launch_bounds__(256) void kv_read_kernel(KvPages c, uint16_t* __res
 }
 
 int shift_of(int page) { return page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7; }
+// (page, group of heads, cache) blocks aimed at: 1024, and twice that of pages of 16, whose blocks have half the work.
+// 512 / 1024 / 2048 / 4096, us: 12 prompts of 200 tokens, 32 heads of K, V and queries, D = 128, pages of 32
+// 41 / 29 / 30 / 34, of 64 30 / 33 / 37 / 45, of 16 68 / 44 / 36 / 37; 8192 tokens, 32 / 8 heads, pages of 64 44 / 46 / 52 / 54.
+constexpr unsigned kAppendBlocks = 1024;
 // pages that a call may touch
 unsigned page_slots(const KvPages& c) { return (unsigned)(c.cu ? (c.T >> shift_of(c.page)) + 2 * c.B : c.B); }
 
@@ -503,9 +559,13 @@ hipError_t append(const AppendView& a, const RopeView& q, unsigned more, hipStre
                            (int)blocks, q);
         return hipGetLastError();
     }
-    const unsigned blocks = page_slots(a.c) * a.c.Hkv * 2;
+    // heads in groups, as many as fill the GPU
+    const unsigned slots = page_slots(a.c);
+    const int groups = (int)std::min<unsigned>(a.c.Hkv, std::max(1u, kAppendBlocks * (page == 16 ? 2 : 1) / (2 * slots)));
+    const unsigned blocks = slots * groups * 2;
 #define W4A16_APPEND(PAGE) \
-    hipLaunchKernelGGL((kv_append_kernel<DT, FMT, D, PAGE>), dim3(blocks + more), dim3(256), 0, st, a, (int)blocks, q)
+    hipLaunchKernelGGL((kv_append_kernel<DT, FMT, D, PAGE>), dim3(blocks + (append_threads(D, PAGE) == 512 ? (more + 1) / 2 : more)), \
+                       dim3(append_threads(D, PAGE)), 0, st, a, (int)blocks, groups, q)
     if (page == 16) W4A16_APPEND(16);
     else if (page == 32) W4A16_APPEND(32);
     else if (page == 64) W4A16_APPEND(64);

@@ -47,6 +47,29 @@ __device__ __forceinline__ uint32_t pack_codes(float a, float b, float c, float 
     }
     return __builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false), true);
 }
+// The same for quotients that are numbers of at most the largest code, up to their rounding: the sum with 1.5 * 2^23
+// holds the nearest whole number, ties to even, in its last byte.
+template <int FMT>
+__device__ __forceinline__ uint32_t pack_numbers(float a, float b, float c, float d) {
+    if constexpr (FMT == FMT_INT8) {
+        const auto bits = [](float x) { return __builtin_bit_cast(uint32_t, x + 12582912.0f); };
+        const uint32_t lo = perm(bits(b), bits(a), 0x0C0C0400u), hi = perm(bits(d), bits(c), 0x04000C0Cu);
+        return lo | hi;
+    }
+    return __builtin_amdgcn_cvt_pk_fp8_f32(c, d, __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false), true);
+}
+// x / s in three operations: with r the reciprocal of s rounded to nearest, the remainder of x r is exact and its
+// correction gives the quotient rounded to nearest (Markstein), away from the ends of the range.
+struct Divisor {
+    float s, r;
+    bool plain;
+    __device__ __forceinline__ explicit Divisor(float scale)
+        : s(scale), r(1.0f / scale), plain(scale > 7.9e-31f && scale < 1.2e30f) {}      // 2^-100 .. 2^100
+    __device__ __forceinline__ float quotient(float x) const {
+        const float q = x * r;
+        return fmaf(fmaf(-q, s, x), r, q);
+    }
+};
 // Four codes of a page whose scale has grown, times old / new scale, rounded again.
 template <int FMT>
 __device__ __forceinline__ uint32_t requantize(uint32_t w, float r) {
