@@ -605,9 +605,9 @@ int w4a16_kv_append_paged(const w4a16_kv_paged* cache, const void* k, const void
 int w4a16_kv_read_paged(const w4a16_kv_paged* cache, int dtype, void* k_out, void* v_out, void* stream);
 
 /* fp32 elements of workspace that hold every w4a16_kv_attention_paged call of these heads whose table has at most
- * table_pages * page == tokens of room (host only; 0: none, for short tables), or a negative status.  It does not
- * depend on the number of sequences or rows. */
-int64_t w4a16_kv_attention_paged_workspace(int64_t Hq, int64_t Hkv, int64_t D, int64_t tokens);
+ * table_pages * page == tokens of room (host only; 0: none, for short tables), or a negative status: of the
+ * calls without cu_seqlens (chunks == 0), or of all.  It does not depend on the number of sequences or rows. */
+int64_t w4a16_kv_attention_paged_workspace(int64_t Hq, int64_t Hkv, int64_t D, int64_t tokens, int chunks);
 
 /*
  * w4a16_kv_attention_paged -- causal attention of the call's tokens (whose own keys and values are in the
@@ -616,8 +616,8 @@ int64_t w4a16_kv_attention_paged_workspace(int64_t Hq, int64_t Hkv, int64_t D, i
  *   q     [T, Hq, D] fp16/bf16, 16-byte aligned, heads adjacent, rows q_stride elements apart (a multiple of 8).
  *   out   [T, Hq, D] dense, 16-byte aligned.  A row that sees no token (no place, no page) is zeros; one whose query is no
  *         number is NaN and leaves the others alone.
- *   work  w4a16_kv_attention_paged_workspace(...) fp32 elements, 16-byte aligned (scratch, contents undefined after
- *         the call; calls that overlap on one buffer race), or NULL when that is 0.
+ *   work  w4a16_kv_attention_paged_workspace(..., cu_seqlens != NULL) fp32 elements, 16-byte aligned (scratch,
+ *         contents undefined after the call; calls that overlap on one buffer race), or NULL when that is 0.
  * Codes enter the products exactly; the softmax weights times V's scales are rounded once to fp16 (relative
  * 2^-11 down to 2^-25 of the row's largest, below by 2^-36 of it); scores, softmax statistics and sums are fp32, the output is rounded once.
  * The codes of a sequence's tokens have to be numbers (what w4a16_kv_append_paged writes is); behind them anything may lie.

@@ -146,7 +146,7 @@ def test_attention_overlaps(lib):
     for lo, n in SEQUENCES + [(0x24000000, own)] + [(BASE[name], size) for name, size, _ in POOLS]:
         for at in touching(lo, n, own, 16):
             assert attend(lib, out=at) == L.ERR_OVERLAP
-    need = 4 * lib.w4a16_kv_attention_paged_workspace(8, 4, 64, 16000)
+    need = 4 * lib.w4a16_kv_attention_paged_workspace(8, 4, 64, 16000, 1)
     wide = dict(table_pages=1000)
     for lo, n in SEQUENCES[1:] + [(0x10000000, 8000), (0x24000000, own), (0x25000000, own)] + [
             (BASE[name], size) for name, size, _ in POOLS]:
@@ -156,10 +156,12 @@ def test_attention_overlaps(lib):
 
 def test_attention_workspace(lib):
     need = lib.w4a16_kv_attention_paged_workspace
-    assert need(8, 2, 64, 1024) == 0 and need(8, 2, 64, 1025) > 0
+    for chunks in (0, 1):
+        assert need(8, 2, 64, 1024, chunks) == 0 and need(8, 2, 64, 1025, chunks) > 0
+    assert need(8, 2, 64, 5000, 0) <= need(8, 2, 64, 5000, 1)
     for bad in ((8, 3, 64, 99), (0, 1, 64, 99), (8, 2, 96, 99), (8, 2, 64, 0), (8, 2, 64, (1 << 24) + 1), (65536, 1, 64, 9)):
-        assert need(*bad) == L.ERR_SHAPE
-    sizes = [need(8, 2, 64, t) for t in range(1, 20000, 37)]
+        assert need(*bad, 1) == L.ERR_SHAPE
+    sizes = [need(8, 2, 64, t, 1) for t in range(1, 20000, 37)]
     assert sizes == sorted(sizes)
 
 

@@ -1165,10 +1165,10 @@ def kv_read_paged(kpages, vpages, table: torch.Tensor, lengths: torch.Tensor, cu
 
 
 @functools.lru_cache(maxsize=256)
-def kv_attention_paged_workspace(Hq: int, Hkv: int, D: int, tokens: int) -> int:
+def kv_attention_paged_workspace(Hq: int, Hkv: int, D: int, tokens: int, chunks: bool = True) -> int:
     """fp32 elements of a scratch buffer that holds every :func:`kv_attention_paged` call of these heads whose
-    table has room for at most ``tokens`` tokens (0: none)."""
-    need = lib().w4a16_kv_attention_paged_workspace(Hq, Hkv, D, tokens)
+    table has room for at most ``tokens`` tokens (0: none); without ``chunks``, of those without ``cu_seqlens``."""
+    need = lib().w4a16_kv_attention_paged_workspace(Hq, Hkv, D, tokens, 1 if chunks else 0)
     if need < 0:
         raise W4A16Error(int(need), "w4a16_kv_attention_paged_workspace")
     return int(need)
@@ -1198,7 +1198,7 @@ def kv_attention_paged(q: torch.Tensor, kpages, vpages, table: torch.Tensor, len
     if out is None:
         out = torch.empty(shape, dtype=dtype, device=q.device)
     o = _dense(out, "out", dtype, shape, dev)
-    need = kv_attention_paged_workspace(Hq, Hkv, D, table.size(1) * kpages[0].size(2))
+    need = kv_attention_paged_workspace(Hq, Hkv, D, table.size(1) * kpages[0].size(2), cu_seqlens is not None)
     if need or work is not None:
         work = _work(work, need, "w4a16_kv_attention_paged_workspace", q)
     _call(lib().w4a16_kv_attention_paged, "w4a16_kv_attention_paged", q.device, c, q.data_ptr(), dt, Hq, qs,

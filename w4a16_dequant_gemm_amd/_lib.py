@@ -155,7 +155,7 @@ def lib() -> ctypes.CDLL:
     L.w4a16_kv_read_paged.restype = i32
     L.w4a16_kv_read_paged.argtypes = [paged, i32, vp, vp, vp]
     L.w4a16_kv_attention_paged_workspace.restype = i64
-    L.w4a16_kv_attention_paged_workspace.argtypes = [i64, i64, i64, i64]
+    L.w4a16_kv_attention_paged_workspace.argtypes = [i64, i64, i64, i64, i32]
     L.w4a16_kv_attention_paged.restype = i32
     L.w4a16_kv_attention_paged.argtypes = [paged, vp, i32, i64, i64, vp, vp, vp]
     _lib = L

@@ -761,11 +761,11 @@ int w4a16_kv_read_paged(const w4a16_kv_paged* cache, int dtype, void* k_out, voi
     return hip_status(w4a16::launch_kv_read(p, dtype, k_out, v_out, static_cast<hipStream_t>(stream)));
 }
 
-int64_t w4a16_kv_attention_paged_workspace(int64_t Hq, int64_t Hkv, int64_t D, int64_t tokens) {
+int64_t w4a16_kv_attention_paged_workspace(int64_t Hq, int64_t Hkv, int64_t D, int64_t tokens, int chunks) {
     if (Hkv < 1 || Hkv > 65535 || Hq < 1 || Hq > 65535 || Hq % Hkv || (D != 64 && D != 128) || tokens < 1 ||
         tokens > kMaxTokens)
         return W4A16_ERR_SHAPE;
-    return w4a16::kv_paged_workspace_floats(Hq, Hkv, D, tokens);
+    return w4a16::kv_paged_workspace_floats(Hkv, D, tokens, chunks != 0);
 }
 
 int w4a16_kv_attention_paged(const w4a16_kv_paged* cache, const void* q, int dtype, int64_t Hq, int64_t q_stride,
@@ -779,7 +779,8 @@ int w4a16_kv_attention_paged(const w4a16_kv_paged* cache, const void* q, int dty
     if (Hq < 1 || Hq > 65535 || Hq % Hkv || !row_stride_ok(q_stride, row) ||
         (T * (Hq / Hkv) / 16 + cache->B + 1024) * Hkv >= kMaxPagedBlocks)
         return W4A16_ERR_SHAPE;
-    const int64_t need = w4a16::kv_paged_workspace_floats(Hq, Hkv, cache->D, cache->table_pages * cache->page);
+    const int64_t need = w4a16::kv_paged_workspace_floats(Hkv, cache->D, cache->table_pages * cache->page,
+                                                           cache->cu_seqlens != nullptr);
     if (need > 0 && !work) return W4A16_ERR_NULL;
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(work, 16) || q_stride % 8) return W4A16_ERR_ALIGN;
     const Span ins[] = {rows_span(q, T, q_stride, row)};

@@ -27,7 +27,6 @@ constexpr int kRowTile = 16;            // query rows of a block
 constexpr int kWaves = 4;
 constexpr int kWhole = 16;              // up to so many tiles a sequence is never split
 constexpr int kLeast = 4;               // tiles of a chunk of a longer one
-constexpr int kTargetBlocks = 1024;     // chunks x kv heads aimed at
 
 template <int DT>
 __device__ __forceinline__ f32x4 mfma16(const u32x4& a, const u32x4& b, const f32x4& c) {
@@ -55,7 +54,14 @@ __device__ __forceinline__ float sum_groups(float x) {
     return __builtin_bit_cast(float, a) + __builtin_bit_cast(float, b);
 }
 
-template <int DT, int FMT, int D>
+template <bool ONCE>
+__device__ __forceinline__ u32x4 codes(const uint8_t* at) {
+    const u32x4* w = reinterpret_cast<const u32x4*>(at);
+    return ONCE ? __builtin_nontemporal_load(w) : *w;
+}
+
+// ONCE: codes to read past the caches, K's (1), V's too (2).
+template <int DT, int FMT, int D, int ONCE>
 __global__ __launch_bounds__(64 * kWaves, 2) void kv_paged_kernel(PagedView a) {
     constexpr int KB = D / 32, DB = D / 16, KL = D / 64;
     __shared__ __attribute__((aligned(16))) f32x4 lo[kWaves][DB][64];
@@ -64,7 +70,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_paged_kernel(PagedView a) {
     const int n16 = lane & 15, g4 = lane >> 4;
     const int h = blockIdx.x % a.c.Hkv;
     Piece p;
-    if (!find_piece<kRowTile, false>(a.s, blockIdx.x / a.c.Hkv, lane, p)) return;
+    const int q = cut<kRowTile>(a.s, lane);
+    if (blockIdx.x == 0 && tid == 0 && !a.s.most) *reinterpret_cast<int*>(a.work) = q;      // (for the joining)
+    if (!find_piece<kRowTile, false>(a.s, q, blockIdx.x / a.c.Hkv, lane, p)) return;
     const int shift = a.shift, page = 1 << shift;
     const int rows = min(kRowTile, p.n * a.s.G - p.row0), row = p.row0 + min(n16, rows - 1);
     // the last token that the lane's row sees, and the block's last row
@@ -89,9 +97,17 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_paged_kernel(PagedView a) {
     const int* table = a.c.table + (long long)p.b * a.c.P;
     const int last_page = max(p.len - 1, 0) >> shift;
     const int end = min(p.tile1, most >= 0 ? most / kTile + 1 : 0);
-    for (int t = p.tile0 + wave; t < end; t += kWaves) {
-        const int kt = kTile * t + 16 * (n16 >> 2), vt = kTile * t + 16 * g4;      // tokens of the lane's K rows, V columns
-        int kid = table[min(kt >> shift, last_page)], vid = table[min(vt >> shift, last_page)];
+    // tokens of the lane's K rows and V columns in a tile, and their pages, asked for a tile early
+    const auto k_token = [&](int t) { return kTile * t + 16 * (n16 >> 2); };
+    const auto v_token = [&](int t) { return kTile * t + 16 * g4; };
+    const auto page_of = [&](int token) { return table[min(token >> shift, last_page)]; };
+    const int t0 = p.tile0 + wave;
+    int kid_next = page_of(k_token(t0)), vid_next = page_of(v_token(t0));
+    for (int t = t0; t < end; t += kWaves) {
+        const int kt = k_token(t), vt = v_token(t);
+        int kid = kid_next, vid = vid_next;
+        kid_next = page_of(k_token(t + kWaves));
+        vid_next = page_of(v_token(t + kWaves));
         const bool live = (unsigned)vid < (unsigned)a.c.N;
         kid = (unsigned)kid < (unsigned)a.c.N ? kid : 0;
         vid = live ? vid : 0;
@@ -103,9 +119,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_paged_kernel(PagedView a) {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int i = 0; i < KL; ++i) kw[j][i] = *reinterpret_cast<const u32x4*>(kp + 4 * j * D + 64 * i);
+            for (int i = 0; i < KL; ++i) kw[j][i] = codes<ONCE >= 1>(kp + 4 * j * D + 64 * i);
 #pragma unroll
-        for (int i = 0; i < DB; ++i) vw[i] = *reinterpret_cast<const u32x4*>(vp + ((16 * i) << shift));
+        for (int i = 0; i < DB; ++i) vw[i] = codes<ONCE >= 2>(vp + ((16 * i) << shift));
         const float ks = a.c.ks[(long long)vid * a.c.Hkv + h];
         const float vs = live && vt <= most ? a.c.vs[(long long)vid * a.c.Hkv + h] : 0.0f;
 
@@ -192,7 +208,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_paged_kernel(PagedView a) {
         lt += ll[w][n16] * fw[w];
     }
     if (n16 >= rows) return;
-    float* part = a.work + ((long long)(p.slot + p.part) * a.c.Hkv + h) * kPartFloats<kRowTile, D>;
+    float* part = outcomes(a) + ((long long)(p.slot + p.part) * a.c.Hkv + h) * kPartFloats<kRowTile, D>;
     const float inv = Mt == -__builtin_inff() ? 0.0f : 1.0f / lt;
 #pragma unroll
     for (int i = wave * (DB / kWaves); i < (wave + 1) * (DB / kWaves); ++i) {
@@ -208,27 +224,40 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_paged_kernel(PagedView a) {
     }
 }
 
-// chunks aimed at for each kv head
-int chunks(long long Hkv) { return (int)((kTargetBlocks + Hkv - 1) / Hkv); }
+// Blocks that run at a time, for each kv head: three on a CU, four of D = 64.
+int resident(long long Hkv, long long D) { return (int)(((D == 128 ? 768 : 1024) + Hkv - 1) / Hkv); }
+// Chunks aimed at, at most (what is left over runs alone).
+int chunks(long long Hkv, long long D) { return (4 * resident(Hkv, D) + 2) / 3; }
 
 template <int DT, int FMT, int D>
 hipError_t paged(const PagedView& a, long long row_tiles, hipStream_t st) {
     const unsigned blocks = (unsigned)((row_tiles + (a.s.most ? 0 : a.s.W)) * a.c.Hkv);
-    hipLaunchKernelGGL((kv_paged_kernel<DT, FMT, D>), dim3(blocks), dim3(64 * kWaves), 0, st, a);
-    if (!a.s.most) {
-        const dim3 joins = join_grid<D, kRowTile>(a, row_tiles);
-        hipLaunchKernelGGL((kv_paged_join_kernel<DT, D, kRowTile>), joins, dim3(256), 0, st, a);
+    // Caches that one row tile reads pass the GPU's caches by (8 sequences of up to 65536 tokens, 8 kv heads, e4m3:
+    // 128 -> 119 us, 64 of up to 2048 51 -> 48), but not V in pages of 128, whose lines two waves share (162 -> 164).
+    if (a.s.cu || a.s.G > kRowTile)
+        hipLaunchKernelGGL((kv_paged_kernel<DT, FMT, D, 0>), dim3(blocks), dim3(64 * kWaves), 0, st, a);
+    else if (a.c.page == 128)
+        hipLaunchKernelGGL((kv_paged_kernel<DT, FMT, D, 1>), dim3(blocks), dim3(64 * kWaves), 0, st, a);
+    else
+        hipLaunchKernelGGL((kv_paged_kernel<DT, FMT, D, 2>), dim3(blocks), dim3(64 * kWaves), 0, st, a);
+    if (a.s.most) return hipGetLastError();
+    // few row tiles, of many chunks each: a row's chunks to four groups of threads (one sequence of 65536 tokens 56 -> 44 us)
+    if (8 * row_tiles <= a.s.W) {
+        const dim3 joins = join_grid<D, kRowTile, 4>(a, row_tiles);
+        hipLaunchKernelGGL((kv_paged_join_kernel<DT, D, kRowTile, 4>), joins, dim3(256), 0, st, a);
+    } else {
+        const dim3 joins = join_grid<D, kRowTile, 1>(a, row_tiles);
+        hipLaunchKernelGGL((kv_paged_join_kernel<DT, D, kRowTile, 1>), joins, dim3(256), 0, st, a);
     }
     return hipGetLastError();
 }
 
 }  // namespace
 
-long long kv_paged_workspace_floats(long long Hq, long long Hkv, long long D, long long tokens) {
-    (void)Hq;
+long long kv_paged_workspace_floats(long long Hkv, long long D, long long tokens, bool many) {
     // (row tiles that are split have at most 2 W chunks)
-    const long long few = tokens <= kWhole * kTile ? 0 : 2LL * chunks(Hkv) * Hkv * kRowTile * (D + 2);
-    return std::max(few, kv_paged_chunk_floats(Hkv, D, tokens));
+    const long long few = tokens <= kWhole * kTile ? 0 : 2LL * chunks(Hkv, D) * Hkv * kRowTile * (D + 2) + kWorkHead;
+    return many ? std::max(few, kv_paged_chunk_floats(Hkv, D, tokens)) : few;
 }
 
 hipError_t launch_kv_paged(const KvPagedArgs& x, float* work, hipStream_t st) {
@@ -241,7 +270,8 @@ hipError_t launch_kv_paged(const KvPagedArgs& x, float* work, hipStream_t st) {
     a.Hq = x.Hq;
     a.shift = x.c.page == 16 ? 4 : x.c.page == 32 ? 5 : x.c.page == 64 ? 6 : 7;
     const int G = x.Hq / x.c.Hkv, tokens = x.c.P << a.shift;
-    a.s = {x.c.lens, x.c.cu, x.c.B, x.c.T, G, tokens, chunks(x.c.Hkv), kLeast, tokens <= kWhole * kTile ? kWhole : 0};
+    a.s = {x.c.lens, x.c.cu, x.c.B, x.c.T, G, tokens, chunks(x.c.Hkv, x.c.D), kLeast, tokens <= kWhole * kTile ? kWhole : 0,
+           resident(x.c.Hkv, x.c.D)};
     // many rows a sequence: 128 at a time
     if (x.c.cu && (long long)x.c.T * G > 32LL * x.c.B) return launch_kv_paged_chunk(a, x.dtype, st);
     const long long row_tiles =

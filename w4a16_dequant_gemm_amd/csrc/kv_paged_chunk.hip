@@ -62,7 +62,9 @@ __global__ __launch_bounds__(64 * WAVES, 2) void kv_paged_chunk_kernel(PagedView
     const int n = lane & 31, hf = lane >> 5;
     const int h = blockIdx.x % a.c.Hkv;
     Piece p;
-    if (!find_piece<kRows, false>(a.s, blockIdx.x / a.c.Hkv, lane, p)) return;
+    const int q = cut<kRows>(a.s, lane);
+    if (blockIdx.x == 0 && tid == 0 && !a.s.most) *reinterpret_cast<int*>(a.work) = q;      // (for the joining)
+    if (!find_piece<kRows, false>(a.s, q, blockIdx.x / a.c.Hkv, lane, p)) return;
     const int shift = a.shift, page = 1 << shift, G = a.s.G;
     const int rows = min(kRows, p.n * G - p.row0);
     // tokens that rows see: row r those up to len - n + r / G
@@ -436,7 +438,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void kv_paged_chunk_kernel(PagedView
                 store_out<DT, D>(a, p, h, row, 32 * i + 8 * g + 4 * hf,
                                  f32x4{o[i][4 * g], o[i][4 * g + 1], o[i][4 * g + 2], o[i][4 * g + 3]}, inv);
     } else {
-        float* part = a.work + ((long long)(p.slot + p.part) * a.c.Hkv + h) * kPartFloats<kRows, D>;
+        float* part = outcomes(a) + ((long long)(p.slot + p.part) * a.c.Hkv + h) * kPartFloats<kRows, D>;
 #pragma unroll
         for (int i = 0; i < D / 32; ++i)
 #pragma unroll
@@ -463,14 +465,15 @@ template <int DT, int FMT, int D, bool ONE, int WAVES>
 hipError_t chunk(PagedView a, hipStream_t st) {
     constexpr int ROWS = 32 * WAVES;
     a.s.W = chunks(a.c.Hkv, WAVES);
+    a.s.R = 0;
     a.s.least = kLeast;
     a.s.most = a.s.tokens <= kWhole * kTile ? kWhole : 0;
     const long long row_tiles = (long long)a.c.T * a.s.G / ROWS + a.c.B;
     const unsigned blocks = (unsigned)((row_tiles + (a.s.most ? 0 : a.s.W)) * a.c.Hkv);
     hipLaunchKernelGGL((kv_paged_chunk_kernel<DT, FMT, D, ONE, WAVES>), dim3(blocks), dim3(64 * WAVES), 0, st, a);
     if (!a.s.most) {
-        const dim3 joins = join_grid<D, ROWS>(a, row_tiles);
-        hipLaunchKernelGGL((kv_paged_join_kernel<DT, D, ROWS>), joins, dim3(256), 0, st, a);
+        const dim3 joins = join_grid<D, ROWS, 1>(a, row_tiles);
+        hipLaunchKernelGGL((kv_paged_join_kernel<DT, D, ROWS, 1>), joins, dim3(256), 0, st, a);
     }
     return hipGetLastError();
 }
@@ -499,7 +502,7 @@ hipError_t chunk(const PagedView& a, hipStream_t st) {
 long long kv_paged_chunk_floats(long long Hkv, long long D, long long tokens) {
     // (row tiles that are split have at most 2 W chunks; W times the rows is the same for both kernels up to rounding)
     const long long rows = std::max(128LL * chunks(Hkv, 4), 256LL * chunks(Hkv, 8));
-    return tokens <= kWhole * kTile ? 0 : 2 * rows * Hkv * (D + 2);
+    return tokens <= kWhole * kTile ? 0 : 2 * rows * Hkv * (D + 2) + kWorkHead;
 }
 
 hipError_t launch_kv_paged_chunk(const PagedView& a, int dtype, hipStream_t st) {

@@ -189,8 +189,9 @@ struct KvPagedArgs {
     void* out;
     int dtype, qs, Hq;
 };
-// fp32 elements of workspace of every call of these heads (0: none where the table has few tokens).
-long long kv_paged_workspace_floats(long long Hq, long long Hkv, long long D, long long tokens);
+// fp32 elements of workspace of every call of these heads, without or with chunks (0: none where the table has
+// few tokens).
+long long kv_paged_workspace_floats(long long Hkv, long long D, long long tokens, bool chunks);
 hipError_t launch_kv_paged(const KvPagedArgs& a, float* work, hipStream_t st);
 
 // AWQ (awq.hip)

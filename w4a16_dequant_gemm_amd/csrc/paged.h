@@ -71,6 +71,7 @@ struct Sched {
     const int *lens, *cu;
     int B, T, G, tokens;        // tokens: of a table
     int W, least, most;         // W: chunks aimed at; least: their tiles; most: a chunk's tiles, if no split is wanted
+    int R;                      // 0, or the blocks of a kv head that run at a time, for up to 64 sequences
 };
 // A sequence's length, first new token, their count, row tiles and key tiles.
 template <int ROWS>
@@ -88,26 +89,62 @@ __device__ __forceinline__ void sequence(const Sched& s, int b, int& len, int& f
     rts = (int)(((long long)n * s.G + ROWS - 1) / ROWS);
     tiles = max((len + kTile - 1) / kTile, 1);
 }
-// Chunks are cut by the lengths: at most q tiles each, q so that about W chunks arise from all sequences'
-// tiles.  Block `index` of a kv head is the index-th chunk; the walk is over 64 sequences at a time.
+// ceil(tiles / q) by the reciprocal, made whole
+__device__ __forceinline__ int parts_of(int tiles, int q, float r) {
+    int n = (int)((float)tiles * r);
+    n += n * q < tiles;
+    n -= (n - 1) * q >= tiles;
+    return n;
+}
+// Chunks are cut by the lengths: at most q tiles each, so that about W chunks arise from all sequences' tiles.
+template <int ROWS>
+__device__ __forceinline__ int cut(const Sched& s, int lane) {
+    if (s.most) return s.most;
+    int len, first, n, rts = 0, tiles = 0;
+    long long all = 0;
+    for (int b0 = 0; b0 < s.B; b0 += 64) {
+        sequence<ROWS>(s, b0 + lane, len, first, n, rts, tiles);
+        const long long work = (long long)rts * tiles;
+        all += lanes_sum((int)(work & 0xFFFF)) + ((long long)lanes_sum((int)(work >> 16)) << 16);
+    }
+    int q = max(s.least, (int)min((all + s.W - 1) / s.W, (long long)1 << 30));
+    // Of a few cuts the one whose blocks should be done first: all at a time if there are no more than R, which then
+    // end with the largest; else one after another, the last of them a quarter of a chunk late on average.  A block
+    // costs two tiles besides.  (8 sequences of up to 65536 tokens, 8 kv heads: 120 -> 109 us.)
+    if (s.R && s.B <= 64 && all < 1 << 24) {
+        const float each = (float)all * __builtin_amdgcn_rcpf((float)s.R);
+        const int q1 = max(q, (int)each + 1), q2 = max(q, (int)(1.07f * each) + 1), q3 = max(q, (int)(1.5f * each) + 1);
+        const auto count = [&](int k) { return rts * parts_of(tiles, k, __builtin_amdgcn_rcpf((float)k)); };
+        // (two counts a sum: both are far below 2^16, as s.W chunks and the row tiles of 64 sequences are)
+        const int c01 = lanes_sum(min(count(q), 511) | min(count(q1), 511) << 16);
+        const int c23 = lanes_sum(min(count(q2), 511) | min(count(q3), 511) << 16);
+        const auto cost = [&](int k, int chunks) {
+            return chunks <= s.R ? k + 2.0f : fmaf(2.0f, (float)chunks, (float)all) * __builtin_amdgcn_rcpf((float)s.R) + 0.25f * k;
+        };
+        float best = cost(q, c01 & 0xFFFF);
+        const auto take = [&](int k, int chunks) {
+            const float c = cost(k, chunks);
+            if (c < best) {
+                best = c;
+                q = k;
+            }
+        };
+        take(q1, c01 >> 16);
+        take(q2, c23 & 0xFFFF);
+        take(q3, c23 >> 16);
+    }
+    return q;
+}
+// Block `index` of a kv head is the index-th chunk of a cut; the walk is over 64 sequences at a time.
 // MERGE: index counts the row tiles that were split (their chunks' outcomes are to be joined).
 template <int ROWS, bool MERGE>
-__device__ __forceinline__ bool find_piece(const Sched& s, int index, int lane, Piece& p) {
+__device__ __forceinline__ bool find_piece(const Sched& s, int q, int index, int lane, Piece& p) {
     int len, first, n, rts, tiles;
-    int q = s.most;
-    if (q == 0) {
-        long long all = 0;
-        for (int b0 = 0; b0 < s.B; b0 += 64) {
-            sequence<ROWS>(s, b0 + lane, len, first, n, rts, tiles);
-            const long long work = (long long)rts * tiles;
-            all += lanes_sum((int)(work & 0xFFFF)) + ((long long)lanes_sum((int)(work >> 16)) << 16);
-        }
-        q = max(s.least, (int)min((all + s.W - 1) / s.W, (long long)1 << 30));
-    }
+    const float rq = __builtin_amdgcn_rcpf((float)q);
     int before = 0, slots = 0;
     for (int b0 = 0; b0 < s.B; b0 += 64) {
         sequence<ROWS>(s, b0 + lane, len, first, n, rts, tiles);
-        const int parts = (tiles + q - 1) / q;
+        const int parts = parts_of(tiles, q, rq);
         const int mine = MERGE ? (parts > 1 ? rts : 0) : rts * parts, room = parts > 1 ? rts * parts : 0;
         const int upto = wave_scan(mine, lane), total = __builtin_amdgcn_readlane(upto, 63);
         const int sl = wave_scan(room, lane);
@@ -144,6 +181,9 @@ struct PagedView {
     float* work;
     int qs, Hq, shift;
 };
+// The workspace: the cut, then the chunks' outcomes.
+constexpr int kWorkHead = 4;
+__device__ __forceinline__ float* outcomes(const PagedView& a) { return a.work + kWorkHead; }
 // A chunk's outcome in the workspace: ROWS rows of D sums, then (maximum, sum of weights) of each row.
 template <int ROWS, int D>
 constexpr int kPartFloats = ROWS * (D + 2);
@@ -158,21 +198,26 @@ __device__ __forceinline__ void store_out(const PagedView& a, const Piece& p, in
     *reinterpret_cast<u32x2*>(at) = u32x2{pack2<DT>(o[0] * inv, o[1] * inv), pack2<DT>(o[2] * inv, o[3] * inv)};
 }
 
-// Joins the chunks of row tiles that were split: a block 1024 / D rows (blockIdx.y), a thread four values of one,
-// eight chunks asked for at a time.
-template <int DT, int D, int ROWS>
+// Joins the chunks of row tiles that were split: a block 1024 / (D GROUPS) rows (blockIdx.y), a thread four values of
+// one and every GROUPS-th eight chunks, which are asked for at a time.
+template <int DT, int D, int ROWS, int GROUPS>
 __global__ __launch_bounds__(256) void kv_paged_join_kernel(PagedView a) {
-    constexpr int AT = 8;
+    constexpr int AT = 8, RB = 1024 / (D * GROUPS);
+    __shared__ __attribute__((aligned(16))) f32x4 ls[GROUPS][256 / GROUPS];
+    __shared__ float lm[GROUPS][RB], ll[GROUPS][RB];
     const int tid = threadIdx.x, lane = tid & 63, h = blockIdx.x % a.c.Hkv;
     Piece p;
-    if (!find_piece<ROWS, true>(a.s, blockIdx.x / a.c.Hkv, lane, p)) return;
-    const int r = blockIdx.y * (1024 / D) + tid / (D / 4), d = 4 * (tid % (D / 4));
-    if (r >= min(ROWS, p.n * a.s.G - p.row0)) return;
+    const int q = __builtin_amdgcn_readfirstlane(*reinterpret_cast<const int*>(a.work));
+    if (!find_piece<ROWS, true>(a.s, q, blockIdx.x / a.c.Hkv, lane, p)) return;
+    const int rows = min(ROWS, p.n * a.s.G - p.row0), r0 = blockIdx.y * RB;
+    if (r0 >= rows) return;
+    const int group = tid / (256 / GROUPS), in = tid % (256 / GROUPS);
+    const int rb = in / (D / 4), r = min(r0 + rb, rows - 1), d = 4 * (in % (D / 4));
     const long long step = (long long)a.c.Hkv * kPartFloats<ROWS, D>;
-    const float* part = a.work + ((long long)p.slot * a.c.Hkv + h) * kPartFloats<ROWS, D>;
+    const float* part = outcomes(a) + ((long long)p.slot * a.c.Hkv + h) * kPartFloats<ROWS, D>;
     float M = -__builtin_inff(), l = 0.0f;
     f32x4 s = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int i = 0; i < p.parts; i += AT) {
+    for (int i = AT * group; i < p.parts; i += AT * GROUPS) {
         float m[AT], w[AT];
         f32x4 x[AT];
 #pragma unroll
@@ -200,12 +245,33 @@ __global__ __launch_bounds__(256) void kv_paged_join_kernel(PagedView a) {
             s += x[j] * e;
         }
     }
-    store_out<DT, D>(a, p, h, p.row0 + r, d, s, M == -__builtin_inff() ? 0.0f : 1.0f / l);
+    if constexpr (GROUPS > 1) {
+        ls[group][in] = s;
+        if (d == 0) {
+            lm[group][rb] = M;
+            ll[group][rb] = l;
+        }
+        __syncthreads();
+        if (group > 0) return;
+#pragma unroll
+        for (int g = 1; g < GROUPS; ++g) M = fmaxf(M, lm[g][rb]);
+        l = 0.0f;
+        s = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int g = 0; g < GROUPS; ++g) {
+            const float m = lm[g][rb], e = m == -__builtin_inff() ? 0.0f : exp2_raw(m - M);
+            l += ll[g][rb] * e;
+            s += ls[g][in] * e;
+        }
+    }
+    if (r0 + rb < rows) store_out<DT, D>(a, p, h, p.row0 + r, d, s, M == -__builtin_inff() ? 0.0f : 1.0f / l);
 }
-// Its grid: at most W row tiles are split.
-template <int D, int ROWS>
+// Its grid: at most W row tiles are split, of a decode step's G rows.
+template <int D, int ROWS, int GROUPS>
 dim3 join_grid(const PagedView& a, long long row_tiles) {
-    return dim3((unsigned)((row_tiles < a.s.W ? row_tiles : a.s.W) * a.c.Hkv), ROWS * D / 1024);
+    constexpr int RB = 1024 / (D * GROUPS);
+    const int rows = a.s.cu || a.s.G > ROWS ? ROWS : a.s.G;
+    return dim3((unsigned)((row_tiles < a.s.W ? row_tiles : a.s.W) * a.c.Hkv), (rows + RB - 1) / RB);
 }
 
 // Many rows a sequence (kv_paged_chunk.hip); the caller fills all of the view but how chunks are cut.
