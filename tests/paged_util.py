@@ -12,6 +12,9 @@ weights times scales are held times 2^11 (2^15 where there are few rows) over th
 scale, so that roundings below fp16's normal range cost 2^-25 2^-11 2 smax = 2^-35 smax per token, times the largest code:
 
     |out - ref| <= u |ref| + (1 + u) (2^-11 + e + (n / 16 + 40) 2^-24) sum p |v| + n 2^-35 smax cmax + 2^-25 [fp16].
+
+(Where the sum is of the rounded weights, sum_i p_i d_i (v_i - out), |d_i| <= 2^-11, may reach 2^-11 (sum p |v| + |out|);
+the bound stays the one of roundings that do not all have one sign.)
 """
 
 from __future__ import annotations

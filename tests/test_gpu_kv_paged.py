@@ -307,6 +307,28 @@ def test_one_page_outweighs_all():
     attend([5000, 5000], [1, 1], 4, 2, 64, 16, torch.int8, torch.float16, 41, decode=True, qscale=3.0, change=change)
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("n,page", [(1, 64), (1, 16), (40, 64), (40, 16), (300, 64)])
+def test_many_faint_tokens(n, page, dtype):
+    """One token of score 26 (base 2) whose V is 0 before 32768 of score 0 and V 1: all weights are powers of two, and
+    each output is L / (L + 2^26) for the L of them that its row sees, which 16 bits hold to half a step (the rest:
+    fp32 scores and sums)."""
+    L = 1 << 15
+    P = (L + 1 + n) // page + 1
+    (kc, ks), (vc, vs) = kp, vp = W4.kv_pages(P, 1, page, 128, torch.int8)
+    kc.zero_(), vc.fill_(127), ks.fill_(1.0), vs.fill_(1.0 / 127)
+    kc[0, 0, 0, 0], vc[0, 0, :, 0] = 127, 0
+    ks[0] = 26.0 * 128 ** 0.5 / (1.4426950408889634 * 127)
+    table = torch.arange(P, dtype=torch.int32, device="cuda")[None]
+    lengths = torch.tensor([L + 1], dtype=torch.int32, device="cuda")
+    q = torch.zeros((n, 1, 128), dtype=dtype, device="cuda")
+    q[:, :, 0] = 1.0
+    got = W4.kv_attention_paged(q, kp, vp, table, lengths, starts([n]) if n > 1 else None).double()
+    faint = (L - n + 1 + torch.arange(n, device="cuda").double())[:, None, None]
+    ref = faint / (faint + 2.0 ** 26)
+    assert ((got - ref).abs() <= (torch.finfo(dtype).eps / 2 + 2.0 ** -14) * ref).all()
+
+
 @pytest.mark.parametrize("decode", [True, False])
 def test_queries_that_are_no_numbers(decode):
     D, Hq, Hkv, page = 128, 8, 2, 32

@@ -13,7 +13,10 @@
 // Scales: a tile is four groups of 16 tokens, each of one page.  K's scale and 1 / sqrt(D) ride on the multiply-add
 // before the exponential; V's does too, as its logarithm: the weights come out times scale / 2^unit, as they
 // enter the second product, and a group's sum is divided by that again.  Weights are held times 2^11 and
-// rounded once to fp16.  The running maximum may lag by 4 (base 2), so that O is rarely rescaled.
+// rounded once to fp16 (half a step, relative 2^-11).  For fp16 outputs, where that counts beside their own rounding,
+// the sum is taken of the rounded weights, so that a row that few tokens make up is off by less (19 cases: 1.41 -> 1.14
+// times the error of the output's rounding alone; the roundings in a second fp16 operand 1.00, but 2048 tokens behind
+// 30000 1078 -> 1458 us).  The running maximum may lag by 4 (base 2), so that O is rarely rescaled.
 #include <algorithm>
 
 #include "paged.h"
@@ -25,6 +28,7 @@ namespace {
 constexpr float kLag = 4.0f;            // the maximum may lag by so much (base 2)
 constexpr int kRaise = 11;              // weights are held times 2^kRaise; 2^(kLag + kRaise) < 65504
 constexpr int kDeepest = -60;           // scales below 2^kDeepest of the largest count as that (their share is nothing)
+constexpr int kThin = -8;               // scales below 2^kThin of the largest have their weights summed in fp32
 constexpr float kLowest = -3.402823466e38f;
 
 // 64 pages of a sequence from page `base` on, one a lane.
@@ -55,6 +59,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void kv_paged_chunk_kernel(PagedView
     static_assert(NL >= 1, "a piece a thread");
       // 16-code pieces of a K row; loads of a thread
     constexpr int NG = ONE ? 1 : 4;
+    constexpr bool kRounded = DT == DT_F16;     // sums are of rounded weights
     // tiles staged ahead, and how many of K and V there is room for
     constexpr int AHEAD = WAVES == 8 ? 2 : 1, KR = 2 * AHEAD, VR = 2 * AHEAD + 1;
     __shared__ __attribute__((aligned(16))) uint16_t lK[KR * TILE], lV[VR * TILE];
@@ -230,6 +235,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void kv_paged_chunk_kernel(PagedView
     auto prepare = [&](int t, f32x16 (&S)[2]) {
         float lv[NG];
         int ge[NG], top = kNone, dead = 0;
+        bool thin = false;
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
             const int i = group_page(t, g);
@@ -251,6 +257,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void kv_paged_chunk_kernel(PagedView
             const int e = ge[g] == kNone ? 0 : max(ge[g] - unit, kDeepest) + kRaise;
             lv[g] = ge[g] == kNone ? 0.0f : lv[g] + (float)e;
             inv[g] = ge[g] == kNone ? 1.0f : __builtin_amdgcn_ldexpf(inv[g], -e);
+            thin |= kRounded && e < kThin + kRaise;
         }
         const bool masked = t >= clear1 || dead;
         if (masked) {
@@ -312,14 +319,34 @@ __global__ __launch_bounds__(64 * WAVES, 2) void kv_paged_chunk_kernel(PagedView
                 }
             }
         }
+        if (thin) {
+            // weights of so small a scale lose their last bits: they are summed before that
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const int gg = ONE ? 0 : g;
+                float s = 0.0f, off = sub[gg];
+                asm volatile("" : "+v"(off));           // (else these are taken for the weights below and all kept)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    s += exp2_raw(fmaf(S[g >> 1][8 * (g & 1) + e], kc[gg], -off));
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                l = fmaf(s, inv[gg], l);
+            }
+#pragma unroll
+            for (int g = 0; g < NG; ++g) inv[g] = 0.0f;
+        }
     };
     float sum = 0.0f;                           // of the weights of a group (ONE: of a tile)
     auto weight_pair = [&](const f32x16 (&S)[2], int pr) {
         const int g = pr >> 2, j = pr & 3, gg = ONE ? 0 : g;
         const float p0 = exp2_raw(fmaf(S[g >> 1][8 * (g & 1) + 2 * j], kc[gg], -sub[gg]));
         const float p1 = exp2_raw(fmaf(S[g >> 1][8 * (g & 1) + 2 * j + 1], kc[gg], -sub[gg]));
-        sum += p0 + p1;
         P[g][j] = pack2<DT_F16>(p0, p1);
+        if (kRounded) {
+            const f16x2 ones = {(_Float16)1.0f, (_Float16)1.0f};
+            sum = __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, (uint32_t)P[g][j]), ones, sum, false);
+        } else sum += p0 + p1;
         if (ONE ? pr == 15 : j == 3) {
             l = fmaf(sum, inv[gg], l);
             sum = 0.0f;
