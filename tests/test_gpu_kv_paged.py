@@ -498,3 +498,179 @@ def test_two_streams():
     for o, w in zip(outs, want):
         for x in o:
             assert torch.equal(x, w)
+
+
+# --------------------------------------------------------------------------- what calls may meet
+
+@pytest.mark.parametrize("codes", CODES, ids=ids)
+@pytest.mark.parametrize("counts", [[1, 1, 1], [70, 3, 200]])
+def test_pools_past_four_gib(counts, codes):
+    """The same sequences at the end of a pool of 4.5 GiB a cache and in a small one: the same bits."""
+    Hkv, D, page, dtype = 8, 128, 128, torch.bfloat16
+    lengths, T = [700, 130, 1500], sum(counts)
+    cu = None if counts == [1, 1, 1] else starts(counts)
+    outcome = []
+    for N in (32, 36864):                                  # pages of 128 KiB
+        kp, vp = W4.kv_pages(N, Hkv, page, D, codes)
+        pages = list(range(N - 1, N - 21, -1))
+        table = torch.full((3, 12), -1, dtype=torch.int32)
+        for b in range(3):
+            for j in range(-(-lengths[b] // page)):
+                table[b, j] = pages.pop()
+        table, lens = table.cuda(), torch.tensor(lengths, dtype=torch.int32).cuda()
+        k, v = fused(sum(lengths), [Hkv, Hkv], D, dtype, 1)
+        freqs, _ = W4.rope_frequencies(D)
+        W4.kv_append_paged(k, v, kp, vp, table, lens, starts(lengths), freqs=freqs)
+        q, k, v = fused(T, [4 * Hkv, Hkv, Hkv], D, dtype, 2, 3.0)
+        qo = W4.kv_append_paged(k, v, kp, vp, table, lens, cu, freqs=freqs, q=q)
+        outcome.append((W4.kv_attention_paged(qo, kp, vp, table, lens, cu),
+                        *W4.kv_read_paged(kp, vp, table, lens, starts(lengths), T=sum(lengths), dtype=dtype)))
+        del kp, vp
+    for a, b in zip(*outcome):
+        assert torch.equal(a, b)
+    assert outcome[0][0].float().abs().max() > 0
+
+
+def test_chunks_of_hundreds_of_sequences():
+    """Appending, reading and attending for 150 sequences of a call against a call for each."""
+    Hkv, Hq, D, page, B, dtype = 2, 4, 64, 16, 150, torch.float16
+    rng = np.random.default_rng(5)
+    counts = [int(c) for c in rng.integers(0, 40, B)]
+    lengths = [c + int(x) for c, x in zip(counts, rng.integers(0, 90, B))]
+    P = 9
+    table = torch.randperm(B * P, generator=torch.Generator().manual_seed(1)).view(B, P).to(torch.int32).cuda()
+    lens = torch.tensor(lengths, dtype=torch.int32).cuda()
+    T = sum(counts)
+    q, k, v = fused(T, [Hq, Hkv, Hkv], D, dtype, 6)
+    freqs, _ = W4.rope_frequencies(D)
+    kp, vp = W4.kv_pages(B * P, Hkv, page, D)
+    copy = tuple(tuple(t.clone() for t in c) for c in (kp, vp))
+    cu = starts(counts)
+    qo = W4.kv_append_paged(k, v, kp, vp, table, lens, cu, freqs=freqs, q=q)
+    got = (qo, W4.kv_attention_paged(qo, kp, vp, table, lens, cu), *W4.kv_read_paged(kp, vp, table, lens, cu, T=T))
+    at = 0
+    for b, n in enumerate(counts):
+        if n:
+            one = (table[b:b + 1], lens[b:b + 1], starts([n]))
+            rows = slice(at, at + n)
+            q1 = W4.kv_append_paged(k[rows], v[rows], *copy, *one, freqs=freqs, q=q[rows])
+            kv1 = W4.kv_read_paged(*copy, *one, T=n)
+            assert torch.equal(got[0][rows], q1)
+            assert torch.equal(got[2][rows], kv1[0]) and torch.equal(got[3][rows], kv1[1])
+            # (another kernel may serve the one sequence: the same up to roundings of weights and output)
+            o1 = W4.kv_attention_paged(q1, *copy, *one)
+            assert (got[1][rows].float() - o1.float()).abs().max() <= 4 * 2.0 ** -11 * max(1.0, float(kv1[1].abs().max()))
+        at += n
+    for a, c in zip((*kp, *vp), (*copy[0], *copy[1])):
+        assert torch.equal(a.view(torch.uint8), c.view(torch.uint8))
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_rows_that_are_no_numbers_in_long_chunks(dtype):
+    """Blocks of 256 rows: only the rows whose query is no number differ."""
+    D, Hq, Hkv, page = 128, 4, 1, 64
+    pool = Pool([2500], Hkv, D, page, torch.int8, 53)
+    n = 400
+    q, = fused(n, [Hq], D, dtype, 54)
+    kp, vp, table, lens = pool.cuda()
+    want = W4.kv_attention_paged(q, kp, vp, table, lens, starts([n]))
+    bad = q.clone()
+    bad[3, 1, 5], bad[200, 3, 0], bad[n - 1, 0] = float("nan"), float("inf"), float("-inf")
+    got = W4.kv_attention_paged(bad, kp, vp, table, lens, starts([n]))
+    odd = torch.zeros((n, Hq), dtype=torch.bool, device="cuda")
+    odd[3, 1] = odd[200, 3] = odd[n - 1, 0] = True
+    assert torch.isnan(got[odd]).any(-1).all()
+    assert torch.equal(got[~odd], want[~odd])
+
+
+@pytest.mark.parametrize("n", [1, 40, 400])
+@pytest.mark.parametrize("size", [1.0e5, 3.0e34])
+def test_scores_past_the_whole_numbers_of_fp32(n, size):
+    """Scores of 10^7 and of 10^36: one key takes all the weight and its V comes out exactly (V's codes and scale
+    are whole)."""
+    D, page, L = 128, 32, 1200
+    P = -(-L // page)
+    (kc, ks), (vc, vs) = kp, vp = W4.kv_pages(P, 1, page, D)
+    best = 500
+    kc[:, :, :, 0] = 3
+    kc[best // page, 0, best % page, 0] = 100
+    vc.copy_(torch.randint(-100, 101, vc.shape, dtype=torch.int8, generator=torch.Generator().manual_seed(3)))
+    ks.fill_(size)
+    vs.fill_(2.0)
+    q = torch.zeros((n, 1, D), dtype=torch.bfloat16, device="cuda")
+    q[:, :, 0] = 16.0
+    table = torch.arange(P, dtype=torch.int32, device="cuda")[None]
+    lens = torch.tensor([L], dtype=torch.int32, device="cuda")
+    got = W4.kv_attention_paged(q, kp, vp, table, lens, None if n == 1 else starts([n]))
+    want = 2.0 * vc[best // page, 0, :, best % page].to(torch.bfloat16)
+    assert torch.equal(got, want.expand(n, 1, D))
+
+
+def test_whatever_stands_in_the_tables():
+    """The largest and smallest whole numbers, and starts that decrease: outputs of sound sequences beside
+    them are as ever where starts are sound, and nothing outside is written where they are not."""
+    Hkv, Hq, D, page, dtype = 2, 8, 64, 16, torch.float16
+    lo, hi = -2 ** 31, 2 ** 31 - 1
+    pool = Pool([1500, 40, 900], Hkv, D, page, torch.int8, 61)
+    kp, vp, table, lens = pool.cuda()
+    q, = fused(3, [Hq], D, dtype, 62)
+    want = W4.kv_attention_paged(q, kp, vp, table, lens)
+    for place, value in ((0, lo), (0, hi), (1, lo)):
+        l2 = lens.clone()
+        l2[1] = value
+        t2 = table.clone()
+        t2[1, place] = value
+        got = W4.kv_attention_paged(q, kp, vp, t2, l2)
+        assert torch.equal(got[[0, 2]], want[[0, 2]])
+        W4.kv_read_paged(kp, vp, t2, l2)
+    before = [t.clone() for t in (*kp, *vp)]
+    k, v = fused(3, [Hkv, Hkv], D, dtype, 63)
+    none = torch.full_like(table, lo)
+    W4.kv_append_paged(k, v, kp, vp, none, torch.tensor([lo, hi, 0], dtype=torch.int32).cuda())
+    W4.kv_append_paged(k, v, kp, vp, none, torch.tensor([hi, lo, 5], dtype=torch.int32).cuda(), starts([1, 1, 1]))
+    for t, b in zip((*kp, *vp), before):
+        assert torch.equal(t.view(torch.uint8), b.view(torch.uint8))
+    for T in (3, 300):
+        big = torch.full((T + 2, Hq, D), 7.0, dtype=dtype, device="cuda")
+        q, = fused(T, [Hq], D, dtype, 64)
+        for cu in ([T, 0, T, 0], [lo, hi, lo, hi], [hi, hi, lo, lo], [2, 1, 0, hi]):
+            cu = torch.tensor(cu, dtype=torch.int32).cuda()
+            W4.kv_attention_paged(q, kp, vp, table, lens, cu, out=big[1:T + 1])
+            W4.kv_read_paged(kp, vp, table, lens, cu, T=T)
+        assert (big[0] == 7).all() and (big[T + 1] == 7).all()
+
+
+def test_two_graphs():
+    """A captured decode step and a captured chunk, scratch of their own captures, replayed in turn."""
+    D, Hq, Hkv, page = 128, 8, 2, 16
+    pools = [Pool(lengths, Hkv, D, page, torch.int8, 71 + i) for i, lengths in enumerate(([3000, 800], [2500]))]
+    data = [p.cuda() for p in pools]
+    qs = [fused(n, [Hq], D, torch.bfloat16, 73 + n)[0] for n in (2, 300)]
+    cus = [None, starts([300])]
+    outs = [torch.empty(q.shape, dtype=q.dtype, device="cuda") for q in qs]
+    graphs = [graph_of(lambda i=i: W4.kv_attention_paged(qs[i], *data[i], cus[i], out=outs[i])) for i in range(2)]
+    for rep in range(4):
+        for i in (0, 1, 0):
+            qs[i].copy_(torch.randn(qs[i].shape, generator=torch.Generator().manual_seed(10 * rep + i)))
+            data[i][3][0] -= 17
+            outs[i].zero_()
+            graphs[i].replay()
+            want = W4.kv_attention_paged(qs[i], *data[i], cus[i])
+            assert torch.equal(outs[i], want)
+
+
+def test_single_rows_of_wide_tensors():
+    """One token: rows of whatever distance, heads in the middle of a wider row."""
+    D, Hkv, page = 64, 2, 16
+    kp, vp = W4.kv_pages(4, Hkv, page, D)
+    wide = torch.randn((1, 5 * Hkv * D), generator=torch.Generator().manual_seed(1)).half().cuda()
+    part = lambda i: wide[:, i * Hkv * D:(i + 1) * Hkv * D].unflatten(1, (Hkv, D))
+    table = torch.tensor([[2, 1]], dtype=torch.int32).cuda()
+    one = torch.tensor([1], dtype=torch.int32).cuda()
+    freqs, _ = W4.rope_frequencies(D)
+    qo = W4.kv_append_paged(part(1), part(3), kp, vp, table, one, freqs=freqs, q=part(4))
+    got = W4.kv_attention_paged(qo, kp, vp, table, one)
+    assert torch.equal(qo, part(4))                        # (place 0)
+    # (half a step of the codes; fp16 roundings of the weight and of the output, of values below 8)
+    tol = part(3).float().abs().amax(2, keepdim=True) / 127 / 2 + 2 * 8 * 2.0 ** -11
+    assert ((got.float() - part(3).float()).abs() <= tol).all()

@@ -314,8 +314,10 @@ __global__ __launch_bounds__(64 * WAVES, 2) void kv_paged_chunk_kernel(PagedView
                 const float k = kc[ONE ? 0 : g], back = 1.0f / k;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const float x = S[g >> 1][8 * (g & 1) + e];
-                    if (big) S[g >> 1][8 * (g & 1) + e] = (x * k - base) * back;
+                    // (rounded as the maximum was: a difference from the exact product could be above 0 by far)
+                    float x = S[g >> 1][8 * (g & 1) + e] * k;
+                    asm("" : "+v"(x));
+                    if (big) S[g >> 1][8 * (g & 1) + e] = (x - base) * back;
                 }
             }
         }
