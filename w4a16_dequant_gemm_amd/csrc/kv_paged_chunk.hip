@@ -439,9 +439,14 @@ __global__ __launch_bounds__(64 * WAVES, 2) void kv_paged_chunk_kernel(PagedView
         for (; t < own1; ++t) {
             top(t);
             f32x16 S[2];
+            // a SIMD's other wave gives way up to the maxima, so that the two do not go in step: one's second product
+            // and exponentials beside the other's scores and masks (2048 tokens behind 30000 1040 -> 1016 us, 4 of 512
+            // behind 8000 in pages of 32 342 -> 323, 8 of 128 of D = 64 115 -> 106; the second half first: no gain)
+            __builtin_amdgcn_s_setprio(1);
             scores_and_stage(lK + kc_at, S, lK + kn_at, lV + vn_at);
             first_values(lV + vp_at);
             prepare(t, S);
+            __builtin_amdgcn_s_setprio(0);
             values_and_weights(lV + vp_at, S);
             turn();
         }
