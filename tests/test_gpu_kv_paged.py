@@ -674,3 +674,22 @@ def test_single_rows_of_wide_tensors():
     # (half a step of the codes; fp16 roundings of the weight and of the output, of values below 8)
     tol = part(3).float().abs().amax(2, keepdim=True) / 127 / 2 + 2 * 8 * 2.0 ** -11
     assert ((got.float() - part(3).float()).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("n,counts", [(5, 200), (3, 300), (6, 90), (2, 700)])
+def test_cuts_that_fit_the_gpu(n, counts):
+    """Chunks of several sequences whose even cut would not fit into one round of blocks, against a call for each
+    sequence (cut otherwise): the same up to the roundings of weights and outputs."""
+    D, Hkv, page, L = 128, 8, 64, 6000
+    pool = Pool([L] * n, Hkv, D, page, torch.int8, 121, outliers=False)
+    kp, vp, table, lens = pool.cuda()
+    q, = fused(n * counts, [Hkv], D, torch.float16, 122)
+    got = W4.kv_attention_paged(q, kp, vp, table, lens, starts([counts] * n)).float()
+    vmax = float(np.nanmax(f64(pool.vs))) * 127
+    for b in range(n):
+        rows = slice(b * counts, (b + 1) * counts)
+        want = W4.kv_attention_paged(q[rows], kp, vp, table[b:b + 1], lens[b:b + 1], starts([counts])).float()
+        # (each side: 2^-11 sum p (|v| + |out|) of the weights, 2^-11 |out| of the output, fp32 sums)
+        assert (got[rows] - want).abs().max() <= 2 * 3.1 * 2.0 ** -11 * vmax
+        # (over a row of uncorrelated values each of the two sides' two roundings has at most 2^-11 of the norm)
+        assert (got[rows] - want).norm() <= 4 * 2.0 ** -11 * want.norm()

@@ -281,7 +281,7 @@ hipError_t launch_kv_paged(const KvPagedArgs& x, float* work, hipStream_t st) {
     a.shift = x.c.page == 16 ? 4 : x.c.page == 32 ? 5 : x.c.page == 64 ? 6 : 7;
     const int G = x.Hq / x.c.Hkv, tokens = x.c.P << a.shift;
     a.s = {x.c.lens, x.c.cu, x.c.B, x.c.T, G, tokens, chunks(x.c.Hkv, x.c.D), kLeast, tokens <= kWhole * kTile ? kWhole : 0,
-           resident(x.c.Hkv, x.c.D)};
+           resident(x.c.Hkv, x.c.D), false};
     // many rows a sequence: 128 at a time
     if (x.c.cu && (long long)x.c.T * G > 32LL * x.c.B) return launch_kv_paged_chunk(a, x.dtype, st);
     const long long row_tiles =

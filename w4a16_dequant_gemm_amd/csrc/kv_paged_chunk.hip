@@ -499,7 +499,8 @@ template <int DT, int FMT, int D, bool ONE, int WAVES>
 hipError_t chunk(PagedView a, hipStream_t st) {
     constexpr int ROWS = 32 * WAVES;
     a.s.W = chunks(a.c.Hkv, WAVES);
-    a.s.R = 0;
+    a.s.R = a.s.W;
+    a.s.rounds = true;
     a.s.least = kLeast;
     a.s.most = a.s.tokens <= kWhole * kTile ? kWhole : 0;
     const long long row_tiles = (long long)a.c.T * a.s.G / ROWS + a.c.B;
@@ -512,13 +513,14 @@ hipError_t chunk(PagedView a, hipStream_t st) {
     return hipGetLastError();
 }
 
-// Eight waves of 256 rows where the sequences have them: a widened code serves twice the rows.  Four / eight
-// waves, us (32 / 8 heads, D = 128, int8, pages of 64): one chunk of 64 / 128 / 512 tokens behind 8000 28.5 / 32.9,
-// 38.9 / 38.8, 97.2 / 90.2, of 512 / 2048 behind 30000 294 / 264, 1144 / 1034; 8 of 64 / 128 behind 8000 97 / 90, 175 / 160.
-// Short tables are not split over blocks, and four waves leave fewer CUs idle: 512 tokens alone 19.0 / 23.9.
+// Eight waves of 256 rows where there are many: a widened code serves twice the rows.  Four / eight waves, us (32 / 8
+// heads, int8, pages of 64): a chunk of 64 / 128 / 512 tokens behind 8000 29.6 / 32.6, 39.1 / 39.2, 94 / 91, of 128 / 2048 behind
+// 30000 85 / 81, 1090 / 1012; 8 of 32 / 40 / 64 / 128 behind 8000 57.5 / 59.7, 81 / 73.6, 92.3 / 89.4, 165 / 158; 3 of 80
+// behind 20000 108 / 126.  Short tables are not split over blocks, and four waves leave fewer CUs idle: 512 tokens alone
+// 20 / 25, 64 times 1000 alone 838 / 873.
 bool wide(const PagedView& a) {
     const long long rows = (long long)a.c.T * a.s.G;
-    return rows >= 512LL * a.c.B && (a.s.tokens > kWhole * kTile || rows * a.c.Hkv >= 256LL * 256);
+    return a.s.tokens > kWhole * kTile && (rows >= 512LL * a.c.B || (rows >= 160LL * a.c.B && rows * a.c.Hkv >= 8192));
 }
 
 template <int DT, int FMT, bool ONE>

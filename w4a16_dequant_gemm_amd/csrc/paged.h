@@ -71,7 +71,8 @@ struct Sched {
     const int *lens, *cu;
     int B, T, G, tokens;        // tokens: of a table
     int W, least, most;         // W: chunks aimed at; least: their tiles; most: a chunk's tiles, if no split is wanted
-    int R;                      // 0, or the blocks of a kv head that run at a time, for up to 64 sequences
+    int R;                      // the blocks of a kv head that run at a time
+    bool rounds;                // they are as many as there are chunks, nearly: a chunk more is a round more
 };
 // A sequence's length, first new token, their count, row tiles and key tiles.
 template <int ROWS>
@@ -108,31 +109,48 @@ __device__ __forceinline__ int cut(const Sched& s, int lane) {
         all += lanes_sum((int)(work & 0xFFFF)) + ((long long)lanes_sum((int)(work >> 16)) << 16);
     }
     int q = max(s.least, (int)min((all + s.W - 1) / s.W, (long long)1 << 30));
-    // Of a few cuts the one whose blocks should be done first: all at a time if there are no more than R, which then
-    // end with the largest; else one after another, the last of them a quarter of a chunk late on average.  A block
-    // costs two tiles besides.  (8 sequences of up to 65536 tokens, 8 kv heads: 120 -> 109 us.)
-    if (s.R && s.B <= 64 && all < 1 << 24) {
-        const float each = (float)all * __builtin_amdgcn_rcpf((float)s.R);
-        const int q1 = max(q, (int)each + 1), q2 = max(q, (int)(1.07f * each) + 1), q3 = max(q, (int)(1.5f * each) + 1);
-        const auto count = [&](int k) { return rts * parts_of(tiles, k, __builtin_amdgcn_rcpf((float)k)); };
-        // (two counts a sum: both are far below 2^16, as s.W chunks and the row tiles of 64 sequences are)
-        const int c01 = lanes_sum(min(count(q), 511) | min(count(q1), 511) << 16);
-        const int c23 = lanes_sum(min(count(q2), 511) | min(count(q3), 511) << 16);
-        const auto cost = [&](int k, int chunks) {
-            return chunks <= s.R ? k + 2.0f : fmaf(2.0f, (float)chunks, (float)all) * __builtin_amdgcn_rcpf((float)s.R) + 0.25f * k;
-        };
-        float best = cost(q, c01 & 0xFFFF);
-        const auto take = [&](int k, int chunks) {
-            const float c = cost(k, chunks);
+    // Of a few cuts of up to 64 sequences the one whose blocks should be done first: all at a time if there are no
+    // more than R, which then end with the largest; else in rounds, or one after another with the last of them a quarter
+    // of a chunk late on average.  A block costs two tiles besides.  (8 sequences of up to 65536 tokens, 8 kv heads, a
+    // token each: 120 -> 109 us.)
+    if (s.B > 64 || all >= 1 << 24) return q;
+    const float each = (float)all * __builtin_amdgcn_rcpf((float)s.R);
+    const auto count = [&](int k) { return min(rts * parts_of(tiles, k, __builtin_amdgcn_rcpf((float)k)), 511); };
+    if (s.rounds) {
+        // (3 sequences' 80 tokens behind 20000, 32 / 8 heads: 155 -> 107 us)
+        int n = lanes_sum(count(q));
+        if (n <= s.R) return q;
+        const int q0 = q;
+        int best = (n + s.R - 1) / s.R * (q + 2);
+#pragma unroll
+        for (float f : {1.08f, 1.2f, 1.4f, 1.7f, 2.2f}) {
+            const int k = max(q0, (int)(f * each) + 1);
+            n = lanes_sum(count(k));
+            const int c = (n + s.R - 1) / s.R * (k + 2);
             if (c < best) {
                 best = c;
                 q = k;
             }
-        };
-        take(q1, c01 >> 16);
-        take(q2, c23 & 0xFFFF);
-        take(q3, c23 >> 16);
+        }
+        return q;
     }
+    const int q1 = max(q, (int)each + 1), q2 = max(q, (int)(1.07f * each) + 1), q3 = max(q, (int)(1.5f * each) + 1);
+    // (two counts a sum: 64 times 511 are below 2^15)
+    const int c01 = lanes_sum(count(q) | count(q1) << 16), c23 = lanes_sum(count(q2) | count(q3) << 16);
+    const auto cost = [&](int k, int chunks) {
+        return chunks <= s.R ? k + 2.0f : fmaf(2.0f, (float)chunks, (float)all) * __builtin_amdgcn_rcpf((float)s.R) + 0.25f * k;
+    };
+    float best = cost(q, c01 & 0xFFFF);
+    const auto take = [&](int k, int chunks) {
+        const float c = cost(k, chunks);
+        if (c < best) {
+            best = c;
+            q = k;
+        }
+    };
+    take(q1, c01 >> 16);
+    take(q2, c23 & 0xFFFF);
+    take(q3, c23 >> 16);
     return q;
 }
 // Block `index` of a kv head is the index-th chunk of a cut; the walk is over 64 sequences at a time.
