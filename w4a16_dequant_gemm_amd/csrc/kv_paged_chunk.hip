@@ -17,6 +17,9 @@
 // the sum is taken of the rounded weights, so that a row that few tokens make up is off by less (19 cases: 1.41 -> 1.14
 // times the error of the output's rounding alone; the roundings in a second fp16 operand 1.00, but 2048 tokens behind
 // 30000 1078 -> 1458 us).  The running maximum may lag by 4 (base 2), so that O is rarely rescaled.
+//
+// Bound by the vector units (57 % busy: softmax, widening) beside the matrix cores (44 %), at the power limit: 2048 tokens
+// behind 30000, 32 / 8 heads, D = 128, int8, take 1010 - 1050 us (1.0 PFLOP/s); 128 behind 8000 39 us.
 #include <algorithm>
 
 #include "paged.h"
@@ -49,15 +52,14 @@ __device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)"
 
 // In iteration t the scores of tile t are computed beside the widening of K(t + 1) and V(t + 1), whose codes were
 // asked for an iteration before, and its softmax beside the second product of tile t - 1; one barrier an
-// iteration (eight waves: K(t + 2) and V(t + 2), a barrier every other iteration: 1099 -> 1083 us).  (The scores of tile t + 1 beside the softmax of tile t, as in attention.hip, need 32 registers
-// more than there are with the codes on their way.)
+// iteration (eight waves: K(t + 2) and V(t + 2), a barrier every other iteration: 1026 -> 1008 us).  (The scores of tile
+// t + 1 beside the softmax of tile t, as in attention.hip, need 32 registers more than there are with the codes on their way.)
 //
 // ONE: pages of at least a tile, so that its four groups are of one page.
 template <int DT, int FMT, int D, bool ONE, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, 2) void kv_paged_chunk_kernel(PagedView a) {
     constexpr int THREADS = 64 * WAVES, kRows = 32 * WAVES, TILE = kTile * D, PR = D / 16, NL = kTile * PR / THREADS;
-    static_assert(NL >= 1, "a piece a thread");
-      // 16-code pieces of a K row; loads of a thread
+    static_assert(NL >= 1, "a piece a thread");         // PR: 16-code pieces of a K row; NL: loads of a thread
     constexpr int NG = ONE ? 1 : 4;
     constexpr bool kRounded = DT == DT_F16;     // sums are of rounded weights
     // tiles staged ahead, and how many of K and V there is room for
