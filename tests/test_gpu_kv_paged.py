@@ -693,3 +693,34 @@ def test_cuts_that_fit_the_gpu(n, counts):
         assert (got[rows] - want).abs().max() <= 2 * 3.1 * 2.0 ** -11 * vmax
         # (over a row of uncorrelated values each of the two sides' two roundings has at most 2^-11 of the norm)
         assert (got[rows] - want).norm() <= 4 * 2.0 ** -11 * want.norm()
+
+
+def test_descriptions_that_are_wrong():
+    """The binding names what is wrong with a cache's description, whichever way it is wrong."""
+    kp, vp = W4.kv_pages(4, 2, 16, 64)
+    table = torch.zeros((3, 2), dtype=torch.int32, device="cuda")
+    lens = torch.ones(3, dtype=torch.int32, device="cuda")
+    q = torch.zeros((3, 4, 64), dtype=torch.float16, device="cuda")
+    cu = starts([1, 1, 1])
+    good = dict(kpages=kp, vpages=vp, table=table, lengths=lens, cu_seqlens=None)
+    W4.kv_attention_paged(q, **good)
+    for error, change in ((TypeError, dict(kpages=(None, kp[1]))), (TypeError, dict(vpages=(vp[0], 3.0))),
+                          (TypeError, dict(kpages=(kp[0].cpu().numpy(), kp[1]))),
+                          (TypeError, dict(vpages=(vp[0].view(torch.uint8), vp[1]))),
+                          (TypeError, dict(kpages=(kp[0], kp[1].double()))), (TypeError, dict(table=None)),
+                          (TypeError, dict(table=table.long())), (TypeError, dict(lengths=[1, 1, 1])),
+                          (TypeError, dict(lengths=lens.float())), (TypeError, dict(cu_seqlens=cu.long())),
+                          (ValueError, dict(kpages=(kp[0][0], kp[1]))), (ValueError, dict(kpages=(kp[0][:, :1], kp[1]))),
+                          (ValueError, dict(kpages=vp)), (ValueError, dict(kpages=(kp[0], kp[1][:2]))),
+                          (ValueError, dict(table=table[0])), (ValueError, dict(table=table[:2])),
+                          (ValueError, dict(table=table.t().contiguous().t())), (ValueError, dict(lengths=lens[:, None])),
+                          (ValueError, dict(lengths=lens.cpu())), (ValueError, dict(cu_seqlens=cu[1:])),
+                          (ValueError, dict(kpages=(kp[0].cpu(), kp[1].cpu()))),
+                          (ValueError, dict(table=table[:2], lengths=lens[:2]))):
+        with pytest.raises(error):
+            W4.kv_attention_paged(q, **{**good, **change})
+        with pytest.raises(error):
+            W4.kv_append_paged(q[:, :2].contiguous(), q[:, :2].contiguous(), **{**good, **change})
+    for error, T in ((ValueError, None), (TypeError, 3.0), (ValueError, 2 ** 70), (W4.W4A16Error, 0)):
+        with pytest.raises(error):
+            W4.kv_read_paged(kp, vp, table, lens, cu, T=T)

@@ -41,6 +41,7 @@ from __future__ import annotations
 
 import functools
 import math
+import struct
 
 import torch
 
@@ -1051,6 +1052,8 @@ def _paged_odd(kpages, vpages, table, lengths, cu, T, dev: int) -> None:
         raise ValueError("without cu_seqlens every sequence has one token: T must be B")
     if T is None:
         raise ValueError("T is needed where cu_seqlens is given")
+    if not isinstance(T, int):
+        raise TypeError("T must be an int")
     _vector(cu, "cu_seqlens", _INT32, B + 1, dev)
     raise ValueError("the description of the paged cache is wrong")
 
@@ -1059,33 +1062,35 @@ _F32 = torch.float32
 
 
 def _paged(kpages, vpages, table, lengths, cu, T: int | None, dev: int):
-    """The checked description of a paged cache and a call's sequences (``T`` None: the number of sequences), and
-    its ``(T, Hkv, D)``."""
+    """The checked description of a paged cache and a call's sequences (``T`` None: the number of sequences), as
+    bytes, its ``T``, ``Hkv`` and ``D`` and the tokens that a row of the table has room for."""
     (kc, ks), (vc, vs) = kpages, vpages
-    if (isinstance(kc, torch.Tensor) and isinstance(ks, torch.Tensor) and isinstance(vc, torch.Tensor)
-            and isinstance(vs, torch.Tensor) and isinstance(table, torch.Tensor) and isinstance(lengths, torch.Tensor)
-            and kc.dim() == 4 and table.dim() == 2):
+    try:
         code = kc.dtype
         N, Hkv, page, D = kc.shape
         B, P = table.shape
         per_head = (N, Hkv)
         if cu is None:
-            at = None
+            at = 0
             if T is None:
                 T = B
             fine = T == B
         else:
             fine = T is not None
             at = _vector(cu, "cu_seqlens", _INT32, B + 1, dev)
+        # (what is no tensor fails one of the comparisons with a tensor's type, device or layout)
         if (fine and (code is _INT8 or code is _E4M3) and vc.dtype is code and ks.dtype is _F32 and vs.dtype is _F32
                 and vc.shape == (N, Hkv, D, page) and ks.shape == per_head and vs.shape == per_head
-                and table.dtype is _INT32 and lengths.dtype is _INT32 and lengths.dim() == 1 and lengths.size(0) == B
+                and table.dtype is _INT32 and lengths.dtype is _INT32 and lengths.shape == (B,)
                 and 0 <= dev == kc.get_device() == ks.get_device() == vc.get_device() == vs.get_device()
                 == table.get_device() == lengths.get_device()
                 and kc.is_contiguous() and ks.is_contiguous() and vc.is_contiguous() and vs.is_contiguous()
                 and table.is_contiguous() and lengths.is_contiguous()):
-            return KvPaged(kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), table.data_ptr(),
-                           lengths.data_ptr(), at, N, page, P, B, T, Hkv, D, KV_INT8 if code is _INT8 else KV_E4M3), Hkv, D
+            return KvPaged.pack(kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), table.data_ptr(),
+                                lengths.data_ptr(), at, N, page, P, B, T, Hkv, D,
+                                KV_INT8 if code is _INT8 else KV_E4M3), T, Hkv, D, P * page
+    except (AttributeError, TypeError, ValueError, struct.error):
+        pass
     _paged_odd(kpages, vpages, table, lengths, cu, T, dev)
 
 
@@ -1109,7 +1114,7 @@ def kv_append_paged(k: torch.Tensor, v: torch.Tensor, kpages, vpages, table: tor
     dtype, dev = k.dtype, k.get_device()
     ks, vs = _rows16(k, "k", dtype, dev), _rows16(v, "v", dtype, dev)
     shape = T, H, D = k.shape
-    c, Hkv, Dc = _paged(kpages, vpages, table, lengths, cu_seqlens, T, dev)
+    c, _, Hkv, Dc, _ = _paged(kpages, vpages, table, lengths, cu_seqlens, T, dev)
     if v.shape != shape or H != Hkv or D != Dc:
         raise ValueError("k and v must be [T, Hkv, D]")
     R = f = 0
@@ -1152,8 +1157,8 @@ def kv_read_paged(kpages, vpages, table: torch.Tensor, lengths: torch.Tensor, cu
             raise ValueError("out and T disagree")
         T, dtype = ko.size(0), ko.dtype
     dev = pool.get_device()
-    c, Hkv, D = _paged(kpages, vpages, table, lengths, cu_seqlens, T, dev)
-    shape = (c.T, Hkv, D)
+    c, T, Hkv, D, _ = _paged(kpages, vpages, table, lengths, cu_seqlens, T, dev)
+    shape = (T, Hkv, D)
     if out is None:
         ko, vo = (torch.empty(shape, dtype=dtype, device=pool.device) for _ in range(2))
     code = _CODES.get(dtype)
@@ -1192,13 +1197,13 @@ def kv_attention_paged(q: torch.Tensor, kpages, vpages, table: torch.Tensor, len
     dtype, dev = q.dtype, q.get_device()
     qs = _rows16(q, "q", dtype, dev)
     shape = T, Hq, D = q.shape
-    c, Hkv, Dc = _paged(kpages, vpages, table, lengths, cu_seqlens, T, dev)
+    c, _, Hkv, Dc, tokens = _paged(kpages, vpages, table, lengths, cu_seqlens, T, dev)
     if D != Dc:
         raise ValueError("q must be [T, Hq, D]")
     if out is None:
         out = torch.empty(shape, dtype=dtype, device=q.device)
     o = _dense(out, "out", dtype, shape, dev)
-    need = kv_attention_paged_workspace(Hq, Hkv, D, table.size(1) * kpages[0].size(2), cu_seqlens is not None)
+    need = kv_attention_paged_workspace(Hq, Hkv, D, tokens, cu_seqlens is not None)
     if need or work is not None:
         work = _work(work, need, "w4a16_kv_attention_paged_workspace", q)
     _call(lib().w4a16_kv_attention_paged, "w4a16_kv_attention_paged", q.device, c, q.data_ptr(), dt, Hq, qs,
