@@ -18,7 +18,7 @@
 // times the error of the output's rounding alone; the roundings in a second fp16 operand 1.00, but 2048 tokens behind
 // 30000 1078 -> 1458 us).  The running maximum may lag by 4 (base 2), so that O is rarely rescaled.
 //
-// Bound by the vector units (57 % busy: softmax, widening) beside the matrix cores (44 %), at the power limit: 2048 tokens
+// Bound by the vector units (61 % busy: softmax, widening) beside the matrix cores (47 %), at the power limit: 2048 tokens
 // behind 30000, 32 / 8 heads, D = 128, int8, take 1010 - 1050 us (1.0 PFLOP/s); 128 behind 8000 39 us.
 #include <algorithm>
 
