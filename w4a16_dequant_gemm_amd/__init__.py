@@ -948,8 +948,8 @@ def _rows16(t, name: str, dtype, dev: int) -> int:
     """``t [T, H, D]`` with adjacent heads on device ``dev``, in the usual case in few steps; returns the rows'
     distance."""
     if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev >= 0:
-        st = t.stride()
-        if len(st) == 3 and st[2] == 1 and st[1] == t.size(2) and t.size(0) > 1:
+        st, shape = t.stride(), t.shape
+        if len(st) == 3 and st[2] == 1 and st[1] == shape[2] and shape[0] > 1:
             return st[0]
     st = _need_heads(t, name, dtype)
     if t.get_device() != dev:
@@ -959,8 +959,8 @@ def _rows16(t, name: str, dtype, dev: int) -> int:
 
 def _vector(t, name: str, dtype, n: int, dev: int) -> int:
     """``t [n]`` of a type on device ``dev``: its address."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and t.dim() == 1
-            and t.size(0) == n and t.is_contiguous()):
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and t.shape == (n,)
+            and t.is_contiguous()):
         _need(t, name, dtype, 1)
         if t.get_device() != dev:
             raise ValueError(f"{name} must be on the device of the other arguments")
@@ -992,7 +992,7 @@ def rope(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, interlea
     xs = _rows16(x, "x", dtype, dev)
     shape = T, H, D = x.shape
     at = _vector(positions, "positions", _INT32, T, dev)
-    pairs = freqs.shape[0] if isinstance(freqs, torch.Tensor) and freqs.dim() == 1 else 0
+    pairs = freqs.numel() if isinstance(freqs, torch.Tensor) else 0
     f = _vector(freqs, "freqs", torch.int64, pairs, dev)
     if out is None:
         out = torch.empty(shape, dtype=dtype, device=x.device)
@@ -1119,7 +1119,7 @@ def kv_append_paged(k: torch.Tensor, v: torch.Tensor, kpages, vpages, table: tor
         raise ValueError("k and v must be [T, Hkv, D]")
     R = f = 0
     if freqs is not None:
-        R = freqs.shape[0] if isinstance(freqs, torch.Tensor) and freqs.dim() == 1 else 0
+        R = freqs.numel() if isinstance(freqs, torch.Tensor) else 0
         f = _vector(freqs, "freqs", torch.int64, R, dev)
         R *= 2
     Hq = qs = 0
