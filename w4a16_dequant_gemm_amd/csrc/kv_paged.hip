@@ -78,7 +78,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_paged_kernel(PagedView a) {
     const int h = blockIdx.x % a.c.Hkv;
     Piece p;
     const int q = cut<kRowTile>(a.s, lane);
-    if (blockIdx.x == 0 && tid == 0 && !a.s.most) *reinterpret_cast<int*>(a.work) = q;      // (for the joining)
+    if (blockIdx.x == 0 && wave == 0 && !a.s.most) keep_cut<kRowTile>(a, q, lane);
     if (!find_piece<kRowTile, false>(a.s, q, blockIdx.x / a.c.Hkv, lane, p)) return;
     const int shift = a.shift, page = 1 << shift;
     const int rows = min(kRowTile, p.n * a.s.G - p.row0), row = p.row0 + min(n16, rows - 1);

@@ -70,7 +70,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void kv_paged_chunk_kernel(PagedView
     const int h = blockIdx.x % a.c.Hkv;
     Piece p;
     const int q = cut<kRows>(a.s, lane);
-    if (blockIdx.x == 0 && tid == 0 && !a.s.most) *reinterpret_cast<int*>(a.work) = q;      // (for the joining)
+    if (blockIdx.x == 0 && wave == 0 && !a.s.most) keep_cut<kRows>(a, q, lane);
     if (!find_piece<kRows, false>(a.s, q, blockIdx.x / a.c.Hkv, lane, p)) return;
     const int shift = a.shift, page = 1 << shift, G = a.s.G;
     const int rows = min(kRows, p.n * G - p.row0);

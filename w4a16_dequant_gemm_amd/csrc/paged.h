@@ -216,6 +216,19 @@ __device__ __forceinline__ void store_out(const PagedView& a, const Piece& p, in
     *reinterpret_cast<u32x2*>(at) = u32x2{pack2<DT>(o[0] * inv, o[1] * inv), pack2<DT>(o[2] * inv, o[3] * inv)};
 }
 
+// The cut for the joining; 0: no row tile is split.  By one wave of the attention's first block.
+template <int ROWS>
+__device__ __forceinline__ void keep_cut(const PagedView& a, int q, int lane) {
+    bool any = false;
+    for (int b0 = 0; b0 < a.s.B; b0 += 64) {
+        int len, first, n, rts, tiles;
+        sequence<ROWS>(a.s, b0 + lane, len, first, n, rts, tiles);
+        any |= rts > 0 && tiles > q;
+    }
+    any = any_lane(any);
+    if (lane == 0) *reinterpret_cast<int*>(a.work) = any ? q : 0;
+}
+
 // Joins the chunks of row tiles that were split: a block 1024 / (D GROUPS) rows (blockIdx.y), a thread four values of
 // one and every GROUPS-th eight chunks, which are asked for at a time.
 template <int DT, int D, int ROWS, int GROUPS>
@@ -226,7 +239,7 @@ __global__ __launch_bounds__(256) void kv_paged_join_kernel(PagedView a) {
     const int tid = threadIdx.x, lane = tid & 63, h = blockIdx.x % a.c.Hkv;
     Piece p;
     const int q = __builtin_amdgcn_readfirstlane(*reinterpret_cast<const int*>(a.work));
-    if (!find_piece<ROWS, true>(a.s, q, blockIdx.x / a.c.Hkv, lane, p)) return;
+    if (q == 0 || !find_piece<ROWS, true>(a.s, q, blockIdx.x / a.c.Hkv, lane, p)) return;
     const int rows = min(ROWS, p.n * a.s.G - p.row0), r0 = blockIdx.y * RB;
     if (r0 >= rows) return;
     const int group = tid / (256 / GROUPS), in = tid % (256 / GROUPS);
