@@ -724,3 +724,24 @@ def test_descriptions_that_are_wrong():
     for error, T in ((ValueError, None), (TypeError, 3.0), (ValueError, 2 ** 70), (W4.W4A16Error, 0)):
         with pytest.raises(error):
             W4.kv_read_paged(kp, vp, table, lens, cu, T=T)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("step", [True, False])
+def test_queries_without_rotation_are_copied(D, step):
+    """Without frequencies q comes out as it went in, and K as without q."""
+    Hkv, Hq, page = 2, 6, 16
+    n = [1, 1, 1] if step else [5, 0, 33]
+    T = sum(n)
+    q, k, v = fused(T, [Hq, Hkv, Hkv], D, torch.bfloat16, 131)
+    table = torch.arange(9, dtype=torch.int32, device="cuda").view(3, 3)
+    lens = torch.tensor([max(c, 1) for c in n], dtype=torch.int32, device="cuda")
+    cu = None if step else starts(n)
+    pools = [W4.kv_pages(9, Hkv, page, D) for _ in range(2)]
+    qo = W4.kv_append_paged(k, v, *pools[0], table, lens, cu, q=q)
+    assert W4.kv_append_paged(k, v, *pools[1], table, lens, cu) is None
+    assert torch.equal(qo, q)
+    for a, b in zip(*pools):
+        for x, y in zip(a, b):
+            assert torch.equal(x, y)
+    assert pools[0][0][0].any()
