@@ -13,10 +13,11 @@
 // operand wants them.  Nothing passes through LDS until the waves are joined.
 //
 // Codes are exact in fp16 (values) and in the queries' type (keys); the scales stay out of the operands: K's
-// multiplies the scores, V's the weights, which are held times 2^15 over the largest scale's power of two
-// and rounded once to fp16 (relative 2^-11 down to 2^-29 of a row's largest); for fp16 outputs, beside whose own
-// rounding that would count (1.4 times their error), the rest goes into a second operand (16 sequences of 4096 tokens,
-// 32 heads: 78.5 -> 79 us).  Scores, maxima, sums and outputs are fp32.
+// multiplies the scores, V's the weights, which are held times 2^15 over the power of two above the largest scale of
+// V that their row has seen, and rounded once to fp16 (relative 2^-11 down to 2^-29 of that scale times the row's
+// largest softmax weight); for fp16 outputs, beside whose own rounding that would count (1.4 times their error), the
+// rest goes into a second operand (16 sequences of 4096 tokens, 32 heads: 78.5 -> 79 us).  Scores, maxima, sums and
+// outputs are fp32.
 //
 // Bound by memory: one token each of 8 sequences of up to 65536 tokens, 32 / 8 heads, D = 128, e4m3 (801 MB), take
 // 142 us with the joining (5.6 TB/s; vector units 25 % busy), of 16 of up to 4096, 32 heads, int8 (338 MB) 75 us; a few
@@ -130,7 +131,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_paged_kernel(PagedView a) {
 #pragma unroll
         for (int i = 0; i < DB; ++i) vw[i] = codes<ONCE >= 2>(vp + ((16 * i) << shift));
         const float ks = a.c.ks[(long long)vid * a.c.Hkv + h];
-        const float vs = live && vt <= most ? a.c.vs[(long long)vid * a.c.Hkv + h] : 0.0f;
+        // (0 where the row sees none of the 16 tokens: its unit below must not come from what it does not see)
+        const float vs = live && vt <= seen ? a.c.vs[(long long)vid * a.c.Hkv + h] : 0.0f;
 
         f32x4 S[4];
 #pragma unroll
@@ -156,7 +158,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_paged_kernel(PagedView a) {
         float f = M != Mn ? exp2_raw(M - Mn) : 1.0f;
         M = Mn;
         l *= f;
-        // V's largest scale so far gives the unit
+        // V's largest scale that the row has seen so far gives its unit
         const float vmax = max_groups(vs);
         const int e = vmax > 0.0f ? __builtin_amdgcn_frexp_expf(vmax) : -200;
         if (e > unit) {
