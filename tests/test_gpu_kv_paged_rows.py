@@ -43,3 +43,13 @@ def later_pages(dtype, codes, lengths, n, G, D, page, ratio):
 def test_later_pages_of_few_rows(D, page, codes, dtype, ratio):
     """(scales up to 2^100 times as large: weights in proportion to them would round to 0)"""
     later_pages(dtype, codes, [70, 200, 69 + page, 1300], [12, 8, 14, 10], 2, D, page, ratio)
+
+
+@pytest.mark.parametrize("ratio", [2.0 ** -20, 2.0 ** 12, 2.0 ** 30, 2.0 ** 100])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("codes", CODES, ids=ids)
+@pytest.mark.parametrize("D,page", [(64, 16), (128, 16), (128, 32), (128, 64), (64, 128)])
+def test_later_pages_of_chunks(D, page, codes, dtype, ratio):
+    """Blocks of 128 rows, and of 256 for long sequences."""
+    later_pages(dtype, codes, [150, 60, 69 + page, 350], [100, 40, 60, 200], 4, D, page, ratio)
+    later_pages(dtype, codes, [1700, 1200], [333, 250], 4, D, page, ratio)

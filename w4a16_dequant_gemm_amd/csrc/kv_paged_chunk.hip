@@ -12,11 +12,13 @@
 //
 // Scales: a tile is four groups of 16 tokens, each of one page.  K's scale and 1 / sqrt(D) ride on the multiply-add
 // before the exponential; V's does too, as its logarithm: the weights come out times scale / 2^unit, as they
-// enter the second product, and a group's sum is divided by that again.  Weights are held times 2^11 and
-// rounded once to fp16 (half a step, relative 2^-11).  For fp16 outputs, where that counts beside their own rounding,
-// the sum is taken of the rounded weights, so that a row that few tokens make up is off by less (19 cases: 1.41 -> 1.14
-// times the error of the output's rounding alone; the roundings in a second fp16 operand 1.00, but 2048 tokens behind
-// 30000 1078 -> 1458 us).  The running maximum may lag by 4 (base 2), so that O is rarely rescaled.
+// enter the second product, and a group's sum is divided by that again.  2^unit is the power of two above the largest
+// scale of V that the row has seen.  Weights are held times 2^11 and rounded once to fp16 (relative 2^-11 down to
+// 2^-25 of 2^unit, below that by 2^-36 of it, and by as much again where 2^unit or the maximum rises before they are
+// used).  For fp16 outputs, where that counts beside their own rounding, the sum is taken of the rounded weights, so that
+// a row that few tokens make up is off by less (19 cases: 1.41 -> 1.14 times the error of the output's rounding alone; the
+// roundings in a second fp16 operand 1.00, but 2048 tokens behind 30000 1078 -> 1458 us).  The running maximum may lag by
+// 4 (base 2), so that O is rarely rescaled.
 //
 // Bound by the vector units (61 % busy: softmax, widening) beside the matrix cores (47 %), at the power limit: 2048 tokens
 // behind 30000, 32 / 8 heads, D = 128, int8, take 1010 - 1050 us (1.0 PFLOP/s); 128 behind 8000 39 us.
@@ -97,7 +99,9 @@ __global__ __launch_bounds__(64 * WAVES, 2) void kv_paged_chunk_kernel(PagedView
 #pragma unroll
         for (int e = 0; e < 16; ++e) o[i][e] = 0.0f;
     float M = -__builtin_inff(), l = 0.0f;
-    int unit = -200;                            // o counts 2^(unit - kRaise)
+    // o counts 2^(unit - low - kRaise): unit is the exponent of V's largest scale that the wave has met, that of what
+    // the row itself has seen lies `low` below it
+    int unit = -200, low = 0;
     const float c = 1.4426950408889634f / sqrtf((float)D);
 
     const int* table = a.c.table + (long long)p.b * a.c.P;
@@ -250,6 +254,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void kv_paged_chunk_kernel(PagedView
             top = max(top, ge[g]);
         }
         float f = 1.0f;
+        const int before = unit - low;
         if (top > unit) {
             f = __builtin_amdgcn_ldexpf(1.0f, unit - top);
             unit = top;
@@ -260,6 +265,29 @@ __global__ __launch_bounds__(64 * WAVES, 2) void kv_paged_chunk_kernel(PagedView
             lv[g] = ge[g] == kNone ? 0.0f : lv[g] + (float)e;
             inv[g] = ge[g] == kNone ? 1.0f : __builtin_amdgcn_ldexpf(inv[g], -e);
             thin |= kRounded && e < kThin + kRaise;
+        }
+        unsigned long long thins = thin ? ~0ull : 0;        // rows whose weights lose bits
+        // In the last tiles a wave's rows see different groups: there each row's unit is of what it sees itself, so that no
+        // page behind it changes its outcome.  (The wave's largest scale for all its rows: 2 % faster on average, pages of
+        // 16 4 %, but with a page of 2^12 times the scale behind it a row's weights lost bits, with 2^40 all of them.)
+        if (t >= clear1) {
+            int mine = before;
+#pragma unroll
+            for (int g = 0; g < NG; ++g)
+                if (kTile * t + 16 * g <= seen) mine = max(mine, ge[g]);
+            low = unit - mine;
+            f = __builtin_amdgcn_ldexpf(1.0f, before - mine);
+            thin = false;
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                const int i = group_page(t, g);
+                const bool any = ge[g] != kNone && kTile * t + 16 * g <= seen;
+                const int e = any ? max(ge[g] - mine, kDeepest) + kRaise : 0;
+                lv[g] = any ? lane_of(w.lm, i) + (float)e : 0.0f;
+                inv[g] = any ? __builtin_amdgcn_ldexpf(lane_of(w.im, i), -e) : 1.0f;
+                thin |= e < kThin + kRaise;
+            }
+            thins = kRounded ? __builtin_amdgcn_ballot_w64(thin) : 0;
         }
         const bool masked = t >= clear1 || dead;
         if (masked) {
@@ -323,8 +351,9 @@ __global__ __launch_bounds__(64 * WAVES, 2) void kv_paged_chunk_kernel(PagedView
                 }
             }
         }
-        if (thin) {
+        if (thins) {
             // weights of so small a scale lose their last bits: they are summed before that
+            const bool mine = thins >> lane & 1;
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
                 const int gg = ONE ? 0 : g;
@@ -335,10 +364,10 @@ __global__ __launch_bounds__(64 * WAVES, 2) void kv_paged_chunk_kernel(PagedView
                     s += exp2_raw(fmaf(S[g >> 1][8 * (g & 1) + e], kc[gg], -off));
                     __builtin_amdgcn_sched_barrier(0);
                 }
-                l = fmaf(s, inv[gg], l);
+                if (mine) l = fmaf(s, inv[gg], l);
             }
 #pragma unroll
-            for (int g = 0; g < NG; ++g) inv[g] = 0.0f;
+            for (int g = 0; g < NG; ++g) inv[g] = mine ? 0.0f : inv[g];
         }
     };
     float sum = 0.0f;                           // of the weights of a group (ONE: of a tile)
@@ -463,7 +492,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void kv_paged_chunk_kernel(PagedView
     }
 
     l = sum_halves(l);
-    const float u = __builtin_amdgcn_ldexpf(1.0f, unit - kRaise);
+    const float u = __builtin_amdgcn_ldexpf(1.0f, unit - low - kRaise);
     if (32 * wave + n >= rows) return;
     if (p.parts == 1) {
         const float inv = M == -__builtin_inff() ? 0.0f : u / l;
