@@ -142,3 +142,33 @@ def test_steps_on_pages_of_small_scales(dtype, ratio, lean):
         for b, count in enumerate(n):
             check_rows(got[at:at + count], f64(q[at:at + count]), pool, b, count, Hq, dtype)
             at += count
+
+
+@pytest.mark.parametrize("dtype", [torch.float16])
+@pytest.mark.parametrize("codes", CODES, ids=ids)
+@pytest.mark.parametrize("D,page", [(64, 16), (128, 64)])
+def test_steps_round_once(D, page, codes, dtype):
+    """Small scores, so that fp32 counts for little: outputs are the nearest 16-bit numbers but for that, so weights are
+    held to more than 16 bits (their rests to 2^-22)."""
+    lengths, Hq = [5, 20, 64, 13, 7], 8
+    pool = Pool(lengths, 2, D, page, codes, 500, outliers=False)
+    kp, vp, table, lens = pool.cuda()
+    for n in ([1] * 5, [4, 3, 8, 2, 7]):
+        q = (torch.randn((sum(n), Hq, D), generator=torch.Generator().manual_seed(7)) * 0.05).to(dtype).cuda()
+        got = f64(W4.kv_attention_paged(q, kp, vp, table, lens, None if n[0] == 1 else starts(n)))
+        q, at = f64(q), 0
+        for b, count in enumerate(n):
+            k, v, _ = pool.rows(b)
+            for h in range(Hq):
+                for i in range(count):
+                    see = lengths[b] - count + i + 1
+                    s = k[:see, h // 4] @ q[at + i, h] / np.sqrt(D)
+                    p = np.exp(s - s.max())
+                    p /= p.sum()
+                    ref, mag = p @ v[:see, h // 4], p @ np.abs(v[:see, h // 4])
+                    e = weight_error(D, float((np.abs(k[:see, h // 4]) @ np.abs(q[at + i, h])).max() / np.sqrt(D)))
+                    out = got[at + i, h]
+                    # half a step where the larger of the two lies: U is half of 2^0's
+                    half = U[dtype] * np.exp2(np.floor(np.log2(np.maximum(np.maximum(np.abs(ref), np.abs(out)), 2.0 ** -14))))
+                    assert (np.abs(out - ref) <= half + (2.0 ** -22 + e + (see / 16 + 40) * 2.0 ** -24) * mag).all()
+            at += count

@@ -178,8 +178,12 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_paged_kernel(PagedView a) {
             for (int k = 0; k < 2; ++k) {
                 const float p0 = exp2_raw(S[j][2 * k] - base), p1 = exp2_raw(S[j][2 * k + 1] - base);
                 l += p0 + p1;
-                const f16x2 w = {(_Float16)(p0 * vf), (_Float16)(p1 * vf)};
-                P[j >> 1][2 * (j & 1) + k] = __builtin_bit_cast(uint32_t, w);
+                uint32_t word = pack2<DT_F16>(p0 * vf, p1 * vf);
+                // (the rest is of the very bits that go in: rounded anew, from the exact product, one weight in thousands
+                // came out a step of fp16 beside them)
+                asm("" : "+v"(word));
+                const f16x2 w = __builtin_bit_cast(f16x2, word);
+                P[j >> 1][2 * (j & 1) + k] = word;
                 if (kTwice)
                     rest[j >> 1][2 * (j & 1) + k] = pack2<DT_F16>(fmaf(p0, vf, -(float)w[0]), fmaf(p1, vf, -(float)w[1]));
             }
