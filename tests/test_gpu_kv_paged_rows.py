@@ -144,7 +144,7 @@ def test_steps_on_pages_of_small_scales(dtype, ratio, lean):
             at += count
 
 
-@pytest.mark.parametrize("dtype", [torch.float16])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
 @pytest.mark.parametrize("codes", CODES, ids=ids)
 @pytest.mark.parametrize("D,page", [(64, 16), (128, 64)])
 def test_steps_round_once(D, page, codes, dtype):

@@ -14,10 +14,11 @@
 //
 // Codes are exact in fp16 (values) and in the queries' type (keys); the scales stay out of the operands: K's
 // multiplies the scores, V's the weights, which are held times 2^15 over the power of two above the largest scale of
-// V that their row has seen, and rounded once to fp16 (relative 2^-11 down to 2^-29 of that scale times the row's
-// largest softmax weight); for fp16 outputs, beside whose own rounding that would count (1.4 times their error), the
-// rest goes into a second operand (16 sequences of 4096 tokens, 32 heads: 78.5 -> 79 us).  Scores, maxima, sums and
-// outputs are fp32.
+// V that their row has seen, and go in as two fp16 numbers, rounded and the rest (relative 2^-22 down to 2^-18 of that
+// scale times the row's largest softmax weight, below by 2^-39 of it).  The first alone would be off by as much as an fp16
+// output's own rounding (1.4 times its error) and turn bf16 outputs over (8 sequences of up to 65536 tokens: 1.05e-3 of the
+// norm off 32-bit weights' outputs, now 8e-5), in 0.4 to 3 % less time (bf16, 8 sequences of up to 40000 tokens, e4m3,
+// 113.6 against 116.1 us; 128 of up to 8000, int8, 364 against 376).  Scores, maxima, sums and outputs are fp32.
 //
 // Bound by memory: one token each of 8 sequences of up to 65536 tokens, 32 / 8 heads, D = 128, e4m3 (801 MB), take
 // 142 us with the joining (5.6 TB/s; vector units 25 % busy), of 16 of up to 4096, 32 heads, int8 (338 MB) 75 us; a few
@@ -71,7 +72,6 @@ __device__ __forceinline__ u32x4 codes(const uint8_t* at) {
 template <int DT, int FMT, int D, int ONCE>
 __global__ __launch_bounds__(64 * kWaves, 2) void kv_paged_kernel(PagedView a) {
     constexpr int KB = D / 32, DB = D / 16, KL = D / 64;
-    constexpr bool kTwice = DT == DT_F16;       // weights in two fp16 numbers
     __shared__ __attribute__((aligned(16))) f32x4 lo[kWaves][DB][64];
     __shared__ float lm[kWaves][kRowTile], ll[kWaves][kRowTile];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -184,8 +184,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_paged_kernel(PagedView a) {
                 asm("" : "+v"(word));
                 const f16x2 w = __builtin_bit_cast(f16x2, word);
                 P[j >> 1][2 * (j & 1) + k] = word;
-                if (kTwice)
-                    rest[j >> 1][2 * (j & 1) + k] = pack2<DT_F16>(fmaf(p0, vf, -(float)w[0]), fmaf(p1, vf, -(float)w[1]));
+                rest[j >> 1][2 * (j & 1) + k] = pack2<DT_F16>(fmaf(p0, vf, -(float)w[0]), fmaf(p1, vf, -(float)w[1]));
             }
         // stale codes may be no numbers, and weight 0 times them would not be 0
         if (FMT == FMT_E4M3 && (kTile * (t + 1) > p.len || any_lane(!live))) {
@@ -203,10 +202,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_paged_kernel(PagedView a) {
             const u32x4 v0 = widen<DT_F16, FMT>(vw[i][0], vw[i][1]), v1 = widen<DT_F16, FMT>(vw[i][2], vw[i][3]);
             o[i] = mfma16<DT_F16>(v0, P[0], o[i]);
             o[i] = mfma16<DT_F16>(v1, P[1], o[i]);
-            if (kTwice) {
-                o[i] = mfma16<DT_F16>(v0, rest[0], o[i]);
-                o[i] = mfma16<DT_F16>(v1, rest[1], o[i]);
-            }
+            o[i] = mfma16<DT_F16>(v0, rest[0], o[i]);
+            o[i] = mfma16<DT_F16>(v1, rest[1], o[i]);
         }
     }
     // the waves' outcomes joined
