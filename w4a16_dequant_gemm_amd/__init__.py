@@ -919,6 +919,8 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "non
         raise ValueError("scaling must be 'none', 'linear', 'base', 'bands' or 'ramp'")
     if scaling in ("bands", "ramp") and (original < 1 or not 0 < low < high):
         raise ValueError(f"scaling '{scaling}' needs original >= 1 and 0 < low < high")
+    if scaling == "ramp" and base == 1:
+        raise ValueError("scaling 'ramp' needs a base other than 1: the pairs' turns do not differ")
     mscale = 1.0
     if scaling == "base" and R > 2:
         base = base * factor ** (R / (R - 2))
