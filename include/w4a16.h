@@ -540,8 +540,8 @@ int w4a16_kv_evict(const w4a16_kv_cache* in, const float* weights, const int32_t
  *            An entry that is not one of 0 .. pages - 1 is no page: tokens there are not written, read as zeros
  *            and are not attended to.  Entries may repeat (a shared beginning), but a page that a call appends
  *            to belongs to one sequence, else its codes are unspecified.
- *   lengths  int32 [B]: each sequence's tokens, the call's own among them; clamped into
- *            [0, table_pages * page] (appending and reading: tokens behind the table have no page).
+ *   lengths  int32 [B]: each sequence's tokens, the call's own among them (negative: 0).  Tokens behind the table
+ *            have no page; rows keep their places there.
  *   cu_seqlens  int32 [B + 1], not decreasing: the call is about the last cu_seqlens[b + 1] - cu_seqlens[b]
  *            tokens of sequence b (possibly none), which are the rows cu_seqlens[b] and on of its T packed ones.
  *            Values are clamped into [0, T] on the device; decreasing ones leave outputs unspecified, never an

@@ -172,3 +172,33 @@ def test_steps_round_once(D, page, codes, dtype):
                     half = U[dtype] * np.exp2(np.floor(np.log2(np.maximum(np.maximum(np.abs(ref), np.abs(out)), 2.0 ** -14))))
                     assert (np.abs(out - ref) <= half + (2.0 ** -22 + e + (see / 16 + 40) * 2.0 ** -24) * mag).all()
             at += count
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("codes", CODES, ids=ids)
+@pytest.mark.parametrize("n,G", [([1, 1, 1], 2), ([9, 3, 6], 2), ([90, 40, 75], 4)])
+def test_lengths_past_the_table(n, G, codes, dtype):
+    """Tokens behind the table have no page: the same as with a wider table whose further entries are none.  Rows keep
+    their places (the first of a chunk that overruns the table see their own tokens)."""
+    D, page = 64, 16
+    pool = Pool([320, 300, 64], 2, D, page, codes, 600)
+    kp, vp, _, _ = pool.cuda()
+    narrow = pool.table[:, :10].contiguous()                # 160 tokens
+    narrow[2, 4:] = -1
+    wide = torch.full((3, 30), -1, dtype=torch.int32)
+    wide[:, :10] = narrow
+    lens = torch.tensor([165, 300, 64], dtype=torch.int32).cuda()
+    q = torch.randn((sum(n), 2 * G, D), generator=torch.Generator().manual_seed(8)).to(dtype).cuda()
+    cu = None if n[0] == 1 else starts(n)
+    got = W4.kv_attention_paged(q, kp, vp, narrow.cuda(), lens, cu)
+    want = W4.kv_attention_paged(q, kp, vp, wide.cuda(), lens, cu)
+    assert torch.equal(got, want) and torch.isfinite(got).all()
+    # (the last sequence may have more rows than tokens: its first rows have no place and see nothing)
+    places = np.concatenate([np.arange(length - c, length) for length, c in zip(lens.tolist(), n)])
+    assert np.array_equal((got != 0).any(-1).all(-1).cpu().numpy(), places >= 0)
+    # and what the rows of the first sequence see, by the formula
+    seen = Pool([160], 2, D, page, codes, 600)
+    seen.kc, seen.ks, seen.vc, seen.vs, seen.table = pool.kc, pool.ks, pool.vc, pool.vs, narrow[:1]
+    inside = n[0] - 5                                       # rows whose own tokens have a page
+    if inside > 0:
+        check_rows(f64(got[:inside]), f64(q[:inside]), seen, 0, inside, 2 * G, dtype)

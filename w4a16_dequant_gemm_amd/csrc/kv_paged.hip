@@ -84,7 +84,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_paged_kernel(PagedView a) {
     const int shift = a.shift, page = 1 << shift;
     const int rows = min(kRowTile, p.n * a.s.G - p.row0), row = p.row0 + min(n16, rows - 1);
     // the last token that the lane's row sees, and the block's last row
-    const int seen = p.len - p.n + row / a.s.G, most = p.len - p.n + (p.row0 + rows - 1) / a.s.G;
+    const int seen = min(p.past + row / a.s.G, p.len - 1), most = min(p.past + (p.row0 + rows - 1) / a.s.G, p.len - 1);
 
     u32x4 qf[KB];
     {

@@ -76,14 +76,14 @@ __global__ __launch_bounds__(64 * WAVES, 2) void kv_paged_chunk_kernel(PagedView
     if (!find_piece<kRows, false>(a.s, q, blockIdx.x / a.c.Hkv, lane, p)) return;
     const int shift = a.shift, page = 1 << shift, G = a.s.G;
     const int rows = min(kRows, p.n * G - p.row0);
-    // tokens that rows see: row r those up to len - n + r / G
-    const int wrow = p.row0 + 32 * wave, row = p.row0 + min(32 * wave + n, rows - 1), past = p.len - p.n;
-    const int seen = past + row / G;
-    const int most = past + (p.row0 + rows - 1) / G;                            // of the block
+    // the last token that a row sees
+    const auto upto = [&](int row) { return min(p.past + row / G, p.len - 1); };
+    const int wrow = p.row0 + 32 * wave, row = p.row0 + min(32 * wave + n, rows - 1);
+    const int seen = upto(row), most = upto(p.row0 + rows - 1);                 // of the lane's row, of the block
     const bool idle = 32 * wave >= rows;
     const int tile0 = p.tile0;
     const int tile1 = min(p.tile1, most >= 0 ? most / kTile + 1 : 0);           // the block's tiles: [tile0, tile1)
-    const int first = past + min(wrow, p.row0 + rows - 1) / G, last = past + min(wrow + 31, p.row0 + rows - 1) / G;
+    const int first = upto(min(wrow, p.row0 + rows - 1)), last = upto(min(wrow + 31, p.row0 + rows - 1));
     const int own1 = idle || last < 0 ? 0 : min(tile1, last / kTile + 1);       // the wave's tiles end there,
     const int clear1 = first < 0 ? 0 : (first + 1) / kTile;                     // and those before need no mask
 

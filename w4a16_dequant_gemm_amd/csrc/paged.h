@@ -64,8 +64,9 @@ __device__ __forceinline__ int wave_scan(int v, int lane) {     // inclusive
 
 // What a block works on: ROWS rows from `row0` of sequence b, its tiles [tile0, tile1), and where the outcome
 // goes: chunk `part` of `parts` in the workspace from `slot`, or straight out if there is one.
+// Row r (a token times its G heads) is at place past + r / G and sees the tokens up to that, of the table's `len`.
 struct Piece {
-    int b, first, n, len, row0, tile0, tile1, part, parts, slot;
+    int b, first, n, len, past, row0, tile0, tile1, part, parts, slot;
 };
 struct Sched {
     const int *lens, *cu;
@@ -74,12 +75,12 @@ struct Sched {
     int R;                      // the blocks of a kv head that run at a time
     bool rounds;                // they are as many as there are chunks, nearly: a chunk more is a round more
 };
-// A sequence's length, first new token, their count, row tiles and key tiles.
+// A sequence's length (its tokens behind the table among them), first new token, their count, row tiles and key tiles.
 template <int ROWS>
 __device__ __forceinline__ void sequence(const Sched& s, int b, int& len, int& first, int& n, int& rts, int& tiles) {
     len = first = n = rts = tiles = 0;
     if (b >= s.B) return;
-    len = min(max(s.lens[b], 0), s.tokens);
+    len = min(max(s.lens[b], 0), 1 << 25);      // (as in page_tokens: more than any table holds)
     if (s.cu) {
         first = min(max(s.cu[b], 0), s.T);
         n = min(max(s.cu[b + 1], first), s.T) - first;
@@ -88,7 +89,7 @@ __device__ __forceinline__ void sequence(const Sched& s, int b, int& len, int& f
         n = 1;
     }
     rts = (int)(((long long)n * s.G + ROWS - 1) / ROWS);
-    tiles = max((len + kTile - 1) / kTile, 1);
+    tiles = max((min(len, s.tokens) + kTile - 1) / kTile, 1);
 }
 // ceil(tiles / q) by the reciprocal, made whole
 __device__ __forceinline__ int parts_of(int tiles, int q, float r) {
@@ -173,7 +174,8 @@ __device__ __forceinline__ bool find_piece(const Sched& s, int q, int index, int
             p.b = b0 + l;
             p.first = at(first);
             p.n = at(n);
-            p.len = at(len);
+            p.len = min(at(len), s.tokens);
+            p.past = at(len) - p.n;
             p.parts = at(parts);
             const int k = index - before - (at(upto) - at(mine));
             const int rt = MERGE ? k : k / p.parts;
