@@ -1190,8 +1190,9 @@ def kv_attention_paged(q: torch.Tensor, kpages, vpages, table: torch.Tensor, len
 
     ``q [T, Hq, D]`` (fp16 / bf16, adjacent heads, rows possibly strided); a row sees the tokens up to its own,
     heads ``h`` of q those of kv head ``h // (Hq / Hkv)``; tokens without a page (an entry that is none, or behind the
-    table) are not attended to.  Rows that see nothing are zeros, rows of no sequence are not written.  ``out`` must not overlap the inputs.  ``work`` is an optional fp32 buffer of at least
-    :func:`kv_attention_paged_workspace` elements (0 for short tables); calls that may overlap need one each.
+    table) are not attended to.  Rows that see nothing are zeros, rows of no sequence are not written.  ``out`` must
+    not overlap the inputs.  ``work`` is an optional fp32 buffer of at least :func:`kv_attention_paged_workspace`
+    elements (0 for short tables); calls that may overlap need one each.
 
     Codes enter the products exactly; the softmax weights, with V's scales, are rounded once to fp16 (relative
     2^-11, down to 2^-23 of the row's largest weight times the largest scale of V that the row sees; in calls of few rows
