@@ -21,7 +21,7 @@
 // 113.6 against 116.1 us; 128 of up to 8000, int8, 364 against 376).  Scores, maxima, sums and outputs are fp32.
 //
 // Bound by memory: one token each of 8 sequences of up to 65536 tokens, 32 / 8 heads, D = 128, e4m3 (801 MB), take
-// 142 us with the joining (5.6 TB/s; vector units 25 % busy), of 16 of up to 4096, 32 heads, int8 (338 MB) 75 us; a few
+// 145 us with the joining (5.7 TB/s; vector units 28 % busy), of 16 of up to 4096, 32 heads, int8 (338 MB) 75 us; a few
 // hundred tokens 6.4 us, of dependent latencies.
 #include <algorithm>
 

@@ -20,8 +20,9 @@
 // roundings in a second fp16 operand 1.00, but 2048 tokens behind 30000 1078 -> 1458 us).  The running maximum may lag by
 // 4 (base 2), so that O is rarely rescaled.
 //
-// Bound by the vector units (61 % busy: softmax, widening) beside the matrix cores (47 %), at the power limit: 2048 tokens
-// behind 30000, 32 / 8 heads, D = 128, int8, take 1010 - 1050 us (1.0 PFLOP/s); 128 behind 8000 39 us.
+// Bound by the vector units (60 % busy: softmax, widening) beside the matrix cores (46 %), at the power limit: 2048 tokens
+// behind 30000, 32 / 8 heads, D = 128, int8, take 1050 - 1070 us in passes after one another (0.98 PFLOP/s); 128 behind
+// 8000 39 us.
 #include <algorithm>
 
 #include "paged.h"
@@ -268,8 +269,8 @@ __global__ __launch_bounds__(64 * WAVES, 2) void kv_paged_chunk_kernel(PagedView
         }
         unsigned long long thins = thin ? ~0ull : 0;        // rows whose weights lose bits
         // In the last tiles a wave's rows see different groups: there each row's unit is of what it sees itself, so that no
-        // page behind it changes its outcome.  (The wave's largest scale for all its rows: 2 % faster on average, pages of
-        // 16 4 %, but with a page of 2^12 times the scale behind it a row's weights lost bits, with 2^40 all of them.)
+        // page behind it changes its outcome.  (The wave's largest scale for all its rows: 0.4 % faster with pages of 64, up
+        // to 4 % with pages of 16, but a page of 2^12 times the scale behind a row cost its weights bits, 2^40 all of them.)
         if (t >= clear1) {
             int mine = before;
 #pragma unroll
