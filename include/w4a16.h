@@ -620,8 +620,8 @@ int64_t w4a16_kv_attention_paged_workspace(int64_t Hq, int64_t Hkv, int64_t D, i
  *         contents undefined after the call; calls that overlap on one buffer race), or NULL when that is 0.
  * Codes enter the products exactly; the softmax weights times V's scales are rounded once to fp16: relative 2^-11 down
  * to 2^-23 of the row's largest weight times the largest scale of V among the pages that the row sees (pages behind its
- * own token do not count), below that by 2^-33 of it.  Calls of few rows (T * Hq / Hkv <= 32 B) keep what that
- * leaves in a second number.  Scores, softmax statistics and sums are fp32, the output is rounded once.
+ * own token do not count), below that by 2^-33 of it.  Decode steps, and chunks of few rows (T * Hq / Hkv <= 32 B),
+ * keep what that leaves in a second number.  Scores, softmax statistics and sums are fp32, the output is rounded once.
  * The codes of a sequence's tokens have to be numbers (what w4a16_kv_append_paged writes is); behind them anything may lie.
  * out and work must be apart from the inputs and each other (W4A16_ERR_OVERLAP).
  * Limits besides the above: Hq <= 65535, (T * Hq / Hkv / 16 + B + 1024) * Hkv < 2^23.

@@ -1195,8 +1195,8 @@ def kv_attention_paged(q: torch.Tensor, kpages, vpages, table: torch.Tensor, len
     elements (0 for short tables); calls that may overlap need one each.
 
     Codes enter the products exactly; the softmax weights, with V's scales, are rounded once to fp16 (relative
-    2^-11, down to 2^-23 of the row's largest weight times the largest scale of V that the row sees; in calls of few rows
-    2^-22); scores, statistics and sums are fp32."""
+    2^-11, down to 2^-23 of the row's largest weight times the largest scale of V that the row sees; in steps and chunks of
+    few rows 2^-22); scores, statistics and sums are fp32."""
     dt = _dtype_code(q)
     dtype, dev = q.dtype, q.get_device()
     qs = _rows16(q, "q", dtype, dev)
