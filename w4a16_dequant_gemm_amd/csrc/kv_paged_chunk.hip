@@ -268,9 +268,9 @@ __global__ __launch_bounds__(64 * WAVES, 2) void kv_paged_chunk_kernel(PagedView
             thin |= kRounded && e < kThin + kRaise;
         }
         unsigned long long thins = thin ? ~0ull : 0;        // rows whose weights lose bits
-        // In the last tiles a wave's rows see different groups: there each row's unit is of what it sees itself, so that no
-        // page behind it changes its outcome.  (The wave's largest scale for all its rows: 0.4 % faster with pages of 64, up
-        // to 4 % with pages of 16, but a page of 2^12 times the scale behind a row cost its weights bits, 2^40 all of them.)
+        // In the last tiles a wave's rows see different groups: there each row's unit is of what it sees itself, so that V's
+        // scales behind it change no bit of its outcome.  (The wave's largest for all its rows: 0.4 % faster with pages of
+        // 64, up to 4 % with pages of 16, but a page of 2^12 times the scale behind a row cost its weights bits, 2^40 all.)
         if (t >= clear1) {
             int mine = before;
 #pragma unroll
